@@ -66,7 +66,8 @@ enum cca_status {
     CCA_ERR_UNSUPPORTED = -2, /* dtype/d combination not built, or the device is not sm_103 */
     CCA_ERR_CUDA = -3,        /* a CUDA runtime/driver call or the launch failed */
     CCA_ERR_TIMEOUT = -4,     /* written to dev_status by a kernel that gave up waiting */
-    CCA_ERR_SCRATCH_LIMIT = -5 /* cca_decode_fwd_noalloc: shapes exceed its fixed scratch */
+    CCA_ERR_SCRATCH_LIMIT = -5, /* cca_decode_fwd_noalloc: shapes exceed its fixed scratch */
+    CCA_ERR_NO_PAGES = -6     /* written to dev_status by cca_pages_reserve: too few free pages */
 };
 
 enum cca_dtype {
@@ -295,6 +296,186 @@ int cca_prefill_host(const void *hQ, const void *hK, const void *hV, void *hO, f
 
 /* Device bytes of workspace cca_prefill_host needs (0 on bad params). */
 uint64_t cca_prefill_host_workspace_size(const cca_params_t *params);
+
+/*
+ * Rotary positions.  CCA scores queries against keys that already carry their
+ * positions; these calls give them.  A pair (x_a, x_b) of a head at position p
+ * becomes
+ *   y_a = factor * (x_a cos t - x_b sin t),  y_b = factor * (x_b cos t + x_a sin t),
+ *   t = p * inv_freq[i],
+ * pair i = 0 .. rot/2 - 1 being columns (i, i + rot/2) with layout 0 and
+ * (2i, 2i + 1) with layout 1; columns rot .. d - 1 are copied.  The angle is
+ * reduced exactly: p times the frequency, held as a 64-bit fraction of a turn,
+ * modulo one turn in integer arithmetic, so far positions lose nothing.
+ * Frequencies scaled for long contexts come in through inv_freq and factor.
+ */
+typedef struct cca_rope_params {
+    int32_t B, N;             /* batch, rows per sequence                    >= 1 */
+    int32_t d;                /* head dimension: 64 or 128 */
+    int32_t rot;              /* columns rotated: even, 0 <= rot <= d (0: plain copy) */
+    int32_t layout;           /* 0: halves, 1: interleaved */
+    int32_t dtype;            /* enum cca_dtype */
+    int32_t inverse;          /* 1: rotate by -t (the gradient of the rotation) */
+    float factor;             /* scales the rotated columns (attention scaling of long contexts) */
+    const double *inv_freq;   /* device [rot/2], radians per position */
+    const int32_t *positions; /* device, or NULL: row n is at position start + n */
+    int64_t pos_stride;       /* elements between two sequences' positions (0: shared) */
+    int64_t start;
+} cca_rope_params_t;
+
+/* One tensor of a call: x and y are [B, H, N, d] by strides (elements, of b, h and n;
+ * columns contiguous, every row 16-byte aligned).  y may be x with the same strides;
+ * otherwise they must not overlap.  A y stride may not make two rows share memory. */
+typedef struct cca_rope_tensor {
+    const void *x;
+    void *y;
+    int32_t H;
+    int64_t x_stride[3], y_stride[3];
+} cca_rope_tensor_t;
+
+/* Rotates one or two tensors (queries and keys, with their own head counts) in one launch. */
+int cca_rope(const cca_rope_tensor_t *tensors, int n_tensors, const cca_rope_params_t *params, void *stream);
+
+/*
+ * Paged caches.  A pool holds pages of `rows` rows of every KV head,
+ *   K, V [layers, n_pages, Hkv, rows, d],
+ * and table[b * cols + c] names the page that holds rows c*rows .. (c+1)*rows - 1 of
+ * sequence b (any value outside [0, n_pages), by convention -1, where there is none).
+ * The raw tokens and the core tokens of a cache each have a pool and a table; the two
+ * may differ in page size.  Decoding reads the core tokens and the window, so the raw
+ * pages behind the window can be freed.  A contiguous cache [B, Hkv, Ncap, d] is a pool
+ * of B pages of Ncap rows with the table 0 .. B - 1.
+ * Lengths, tables, trees and paths are device data: the host never waits, and a
+ * captured call serves later lengths.  What they hold is checked on the device: an
+ * entry that names no page or a length outside the table is skipped (as described at
+ * each call) and reported as CCA_ERR_INVALID_ARG in *dev_status when that pointer is
+ * set; nothing out of range is read or written.
+ */
+typedef struct cca_pages {
+    void *K, *V;              /* device, 16-byte aligned, contiguous */
+    const int32_t *table;     /* device [B, cols] */
+    int32_t n_pages, rows, cols;
+    int32_t layers;           /* cca_pages_copy / cca_pages_compact move every layer; 1 elsewhere */
+} cca_pages_t;
+
+/*
+ * cca_rope_append - the new tokens of a step: rotates queries and keys and stores keys
+ * and values into the raw pages of their sequences, in one launch.  Token t of sequence
+ * b goes to row lens[b] + t.  With parents, the tokens are the nodes of a drafted tree
+ * (see cca_tree_fwd) and node t is at position lens[b] + depth(t); without, at lens[b] + t.
+ *   q       x [B, Hq, N, d] -> y, or NULL;  k, v  x [B, Hkv, N, d], y unused
+ *   params  B, N = tokens per sequence, d, rot, layout, dtype, factor, inv_freq as above
+ *           (positions, pos_stride, start and inverse must be 0)
+ *   lens    device [B];  parents  device [B, N] or NULL (then any N; with it N <= 256)
+ *   counts  device [B] or NULL: only the first counts[b] tokens are real
+ * Tokens that are not real (past counts, or a node whose chain of parents does not reach
+ * the root) are not stored, and their rows of q's output are zero.
+ */
+int cca_rope_append(const cca_rope_tensor_t *q, const cca_rope_tensor_t *k, const cca_rope_tensor_t *v,
+                    const cca_pages_t *raw, const int32_t *lens, const int32_t *parents, const int32_t *counts,
+                    int32_t *dev_status, const cca_rope_params_t *params, void *stream);
+
+/*
+ * cca_tree_fwd - CCA attention of a tree of drafted tokens over paged caches (the fusion
+ * equation, for several candidate continuations at once; one token with T = 1).
+ * Sequence b has lens[b] committed tokens.  Its T drafted nodes sit in raw rows
+ * lens[b] .. lens[b] + T - 1; parents[b*T + t] is the node before t (below t), -1 for a
+ * child of the last committed token.  Node t, at depth e below the root, is at position
+ * p = lens[b] + e and attends exactly as row p of cca_attn_fwd over the committed tokens
+ * followed by its chain: the cores j < lo(p)/g, the committed raw tokens from the window's
+ * start on, its ancestors and itself.
+ *   Q       [B, Hq, T, d];  O  [B, Hq, T, d];  LSE  [B, Hq, T] fp32
+ *   raw     table entries of rows [window start of lens[b], lens[b] + T) must be there
+ *   core    rows [0, lo(lens[b] + T - 1)/g) must be there
+ *   parents device [B, T], or NULL for one chain (node t's parent is t - 1)
+ *   params  B, Hq, Hkv, d, g, w, dtype, scale, dev_status, window_mode (N is not used)
+ * A parent that is neither -1 nor an earlier node ends the chain: such a node and its
+ * descendants are empty (O = 0, LSE = -inf), which is also how padding nodes are written
+ * (-2).  Keys whose table entry names no page count as not there.
+ * Keys that a row does not see never reach its output, whatever they hold.
+ * workspace: caller-owned, at least cca_tree_workspace_size(params, T) bytes, rewritten by
+ * every call; two calls that may run at the same time need one each.
+ * Supported: bf16 or f32, d in {64, 128}, 1 <= T <= min(256, w), B <= 1024.
+ */
+int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core, const int32_t *lens,
+                 const int32_t *parents, int T, void *O, float *LSE, const cca_params_t *params, void *workspace,
+                 uint64_t workspace_bytes, void *stream);
+/* Bytes of workspace cca_tree_fwd needs on the current device (0 on bad params). */
+uint64_t cca_tree_workspace_size(const cca_params_t *params, int T);
+
+/*
+ * cca_pool_pages - pools the groups that newly committed tokens complete (the pooling
+ * equation), from raw pages into core pages.  Sequence b had lens[b] tokens and gained
+ * accepted[b], whose K and V rows lie at lens[b] .. lens[b] + accepted[b] - 1; every group
+ * j with lens[b] < (j+1)*g <= lens[b] + accepted[b] is pooled.  The i-th new token's query
+ * is Q[b, :, path[b*A + i]] (path device [B, A]: the accepted nodes of the tree), or
+ * Q[b, :, i] with path NULL (then A = T).
+ *   Q [B, Hq, T, d];  params  B, Hq, Hkv, d, g, dtype, scale, dev_status, pool_mode
+ * accepted[b] > A is reported and pools nothing for b; a group with a row, a core page or
+ * a path entry that is not there is reported and skipped.
+ * Supported: bf16 or f32, d in {64, 128}.
+ */
+int cca_pool_pages(const void *Q, const cca_pages_t *raw, const cca_pages_t *core, const int32_t *lens,
+                   const int32_t *accepted, const int32_t *path, int A, int T, const cca_params_t *params,
+                   void *stream);
+
+/*
+ * The pages' book: refs[page] is the number of table entries that hold the page; a page
+ * with refs 0 is free.  All four calls order their work as if one table row came after
+ * the other, and results do not depend on timing.
+ *
+ * cca_pages_reserve - room for the rows [lens[b], lens[b] + extra[b]) of every sequence
+ * (extra <= 0: none): table entries of that range that name no page get one, and entries
+ * whose page is shared get one of their own, but for the page's last holder (copy on
+ * write).  Free pages are handed out lowest number first, in row order.  pairs[b] = (old,
+ * new) where the page of row lens[b] was replaced and holds committed rows, else (-1, -1):
+ * the pages for cca_pages_copy to copy.  If the pool has too few free pages, nothing
+ * changes, all pairs are -1 and *dev_status becomes CCA_ERR_NO_PAGES.  A row whose range
+ * leaves the table or has lens < 0 is reported (CCA_ERR_INVALID_ARG) and gets nothing.
+ *   workspace: 16-byte aligned, at least cca_pages_reserve_workspace_size(B, cols) bytes
+ */
+int cca_pages_reserve(int32_t *refs, int n_pages, int32_t *table, int B, int cols, int rows, const int32_t *lens,
+                      const int32_t *extra, int32_t *pairs, void *workspace, uint64_t workspace_bytes,
+                      int32_t *dev_status, void *stream);
+uint64_t cca_pages_reserve_workspace_size(int B, int cols);
+
+/*
+ * cca_pages_fork - table row dst[i] becomes a second holder of the pages of row src[i]:
+ * its first ceil(lens[src[i]] / rows) entries are copied (and counted in refs), the others
+ * become -1.  Every entry of a dst row must be free (-1) before.  A pair is reported and
+ * skipped when a row is out of range, src = dst, dst holds pages, dst is also a source of
+ * the call, or an earlier pair has the same dst.
+ */
+int cca_pages_fork(int32_t *refs, int n_pages, int32_t *table, int B, int cols, int rows, const int32_t *src,
+                   const int32_t *dst, int n, const int32_t *lens, int32_t *dev_status, void *stream);
+
+/*
+ * cca_pages_free - entries [first[b], last[b]) of every table row (clamped to the row)
+ * give up their pages: refs is counted down and the entry becomes -1.  Entries that name
+ * no page are left alone; a page whose refs is already 0 is reported and stays at 0.
+ */
+int cca_pages_free(int32_t *refs, int n_pages, int32_t *table, int B, int cols, const int32_t *first,
+                   const int32_t *last, int32_t *dev_status, void *stream);
+
+/*
+ * cca_pages_copy - copies page pairs[i][0] to page pairs[i][1] of the pool, K and V, every
+ * layer (the contents behind a page that cca_pages_reserve replaced).  Pairs with a
+ * negative entry are skipped.  A pair is reported and skipped when a page is out of range,
+ * an earlier pair has the same destination, or its destination is the source of any pair.
+ *   params  Hkv, d, dtype, dev_status;  pages  K, V, n_pages, rows, layers;  n <= 65535
+ */
+int cca_pages_copy(const cca_pages_t *pages, const int32_t *pairs, int n, const cca_params_t *params, void *stream);
+
+/*
+ * cca_pages_compact - keeps the accepted nodes of a drafted tree: raw row lens[b] + path[b*A
+ * + i] moves to row lens[b] + i for i < accepted[b], K and V, every layer.  The path names
+ * nodes from the root down, so it rises: path[i] >= i and path[i] < path[i+1].  A sequence
+ * whose path does not, whose accepted is outside [0, A] or whose rows are not all there is
+ * reported and left as it is.
+ *   params  B, Hkv, d, dtype, dev_status;  1 <= A <= 256
+ */
+int cca_pages_compact(const cca_pages_t *pages, const int32_t *lens, const int32_t *path, int A,
+                      const int32_t *accepted, const cca_params_t *params, void *stream);
 
 /* Static English text for a status code (never NULL). */
 const char *cca_status_string(int status);

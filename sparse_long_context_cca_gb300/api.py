@@ -21,6 +21,7 @@ CCA_ERR_UNSUPPORTED = -2
 CCA_ERR_CUDA = -3
 CCA_ERR_TIMEOUT = -4
 CCA_ERR_SCRATCH_LIMIT = -5
+CCA_ERR_NO_PAGES = -6
 CCA_BF16 = 0
 CCA_F32 = 1
 
@@ -42,6 +43,27 @@ class CcaParams(ctypes.Structure):
                 ("pool_mode", ctypes.c_int32)]
 
 
+class CcaRopeParams(ctypes.Structure):
+    """Mirror of cca_rope_params_t."""
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("pos_stride", ctypes.c_int64), ("start", ctypes.c_int64)]
+
+
+class CcaRopeTensor(ctypes.Structure):
+    """Mirror of cca_rope_tensor_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class CcaPages(ctypes.Structure):
+    """Mirror of cca_pages_t."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("layers", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -49,6 +71,9 @@ EXPORTED = ["cca_pool", "cca_attn_fwd", "cca_attn_fwd_rows", "cca_decode_fwd", "
             "cca_decode_kernels", "cca_pool_group",
             "cca_decode_fwd_noalloc", "cca_prefill_bwd", "cca_prefill_bwd_workspace_size",
             "cca_prefill_host", "cca_prefill_host_workspace_size",
+            "cca_rope", "cca_rope_append", "cca_tree_fwd", "cca_tree_workspace_size", "cca_pool_pages",
+            "cca_pages_reserve", "cca_pages_reserve_workspace_size", "cca_pages_fork", "cca_pages_free",
+            "cca_pages_copy", "cca_pages_compact",
             "cca_status_string", "cca_abi_version", "cca_test_set_wait_limit_ns", "cca_test_skip_q_load",
             "cca_test_decode_path"]
 
@@ -95,6 +120,22 @@ def load_library():
         lib.cca_decode_workspace_size.restype = ctypes.c_uint64
         lib.cca_pool_group.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int, pp, vp]
         lib.cca_pool_group.restype = ctypes.c_int
+        u64 = ctypes.c_uint64
+        rp, rt, pg = (ctypes.POINTER(x) for x in (CcaRopeParams, CcaRopeTensor, CcaPages))
+        for name, args, res in (
+                ("cca_rope", [rt, ci, rp, vp], ci),
+                ("cca_rope_append", [rt, rt, rt, pg, vp, vp, vp, vp, rp, vp], ci),
+                ("cca_tree_fwd", [vp, pg, pg, vp, vp, ci, vp, vp, pp, vp, u64, vp], ci),
+                ("cca_tree_workspace_size", [pp, ci], u64),
+                ("cca_pool_pages", [vp, pg, pg, vp, vp, vp, ci, ci, pp, vp], ci),
+                ("cca_pages_reserve", [vp, ci, vp, ci, ci, ci, vp, vp, vp, vp, u64, vp, vp], ci),
+                ("cca_pages_reserve_workspace_size", [ci, ci], u64),
+                ("cca_pages_fork", [vp, ci, vp, ci, ci, ci, vp, vp, ci, vp, vp, vp], ci),
+                ("cca_pages_free", [vp, ci, vp, ci, ci, vp, vp, vp, vp], ci),
+                ("cca_pages_copy", [pg, vp, ci, pp, vp], ci),
+                ("cca_pages_compact", [pg, vp, vp, ci, vp, pp, vp], ci)):
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = args, res
         lib.cca_status_string.argtypes = [ctypes.c_int]
         lib.cca_status_string.restype = ctypes.c_char_p
         lib.cca_abi_version.argtypes = []
@@ -457,6 +498,448 @@ class CcaAttentionFunction(torch.autograd.Function):
         return dQ.to(Q.dtype), dK.to(K.dtype), dV.to(V.dtype), None, None, None, None, None
 
 
-def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 0, window_mode: int = 0):
-    """CCA attention output O [B, Hq, N, d] with gradients for Q, K and V (prefill step)."""
+def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 0, window_mode: int = 0,
+                  inv_freq=None, **rotary):
+    """CCA attention output O [B, Hq, N, d] with gradients for Q, K and V (prefill step).
+    With inv_freq, Q and K are first given their positions by rope(Q, K, inv_freq, **rotary)."""
+    if inv_freq is not None:
+        Q, K = rope(Q, K, inv_freq, **rotary)
+    elif rotary:
+        raise ValueError(f"{sorted(rotary)} without inv_freq")
     return CcaAttentionFunction.apply(Q, K, V, g, w, scale, pool_mode, window_mode)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+_LAYOUT = {"half": 0, "interleaved": 1}
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original: int = 8192, low: float = 1.0, high: float = 4.0, device="cuda"):
+    """Frequencies of a rotary embedding, and the factor that goes with them: (inv_freq float64
+    [rot/2] on `device`, attention factor).  inv_freq[i] = base**(-2i/rot), stretched for contexts
+    `factor` times the `original` length by one of
+      "linear"  every frequency / factor (positions interpolated)
+      "ntk"     base * factor**(rot/(rot-2)): the slowest pair / factor, the fastest unchanged
+      "bands"   by the turns a pair makes over `original` positions: above `high` unchanged, below
+                `low` / factor, between them the mean weighted linearly in the turns
+      "yarn"    the same with the weight linear in the pair's index (low, high: 1, 32 by custom),
+                and the attention factor 0.1 ln(factor) + 1."""
+    import math
+    if rot < 2 or rot % 2 or factor < 1.0 or scaling not in (None, "linear", "ntk", "bands", "yarn"):
+        raise ValueError(f"rot {rot}, scaling {scaling!r}, factor {factor}")
+    if scaling == "ntk":
+        if rot == 2:
+            raise ValueError("ntk scaling needs more than one pair")
+        base = base * factor ** (rot / (rot - 2))
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    f = base ** (-2.0 * i / rot)
+    attention = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("bands", "yarn"):
+        if not 0.0 < low < high or original < 1:
+            raise ValueError("bands and yarn need 0 < low < high and original >= 1")
+        if scaling == "bands":
+            keep = (f * (original / (2.0 * math.pi)) - low) / (high - low)
+        else:
+            def pair(turns):    # the (fractional) pair that makes so many turns over `original`
+                return rot * math.log(original / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
+            a, z = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), rot - 1)
+            keep = 1.0 - (i - a) / max(z - a, 1e-3)
+            attention = 0.1 * math.log(factor) + 1.0
+        keep = keep.clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    return f.to(device), attention
+
+
+class _On:
+    """Runs a call on the tensors' device and on the caller's stream (the device's current one
+    without), so that what is allocated inside belongs to that stream too."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.there = torch.cuda.device(self.device)
+        self.there.__enter__()
+        self.over = None
+        if self.stream is None:
+            return int(torch.cuda.current_stream().cuda_stream)
+        s = self.stream
+        if not hasattr(s, "cuda_stream"):
+            s = torch.cuda.ExternalStream(int(s), device=self.device)
+        if s.device != self.device:
+            self.there.__exit__(None, None, None)
+            raise ValueError(f"stream is on {s.device}, the tensors on {self.device}")
+        self.over = torch.cuda.stream(s)
+        self.over.__enter__()
+        return int(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.over is not None:
+            self.over.__exit__(*exc)
+        self.there.__exit__(*exc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _words(t, name, shape, device):
+    """A contiguous int32 tensor of the call's device; its pointer (None for None)."""
+    if t is None:
+        return None
+    _check(t, name, torch.int32, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _rope_tensor(x, y, name) -> CcaRopeTensor:
+    if x.stride(3) != 1 or (y is not None and y.stride(3) != 1):
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    xs, ys = x.stride(), (0, 0, 0) if y is None else y.stride()
+    return CcaRopeTensor(x.data_ptr(), None if y is None else y.data_ptr(), x.shape[1],
+                         (ctypes.c_int64 * 3)(*xs[:3]), (ctypes.c_int64 * 3)(*ys[:3]))
+
+
+def _rows(t, name, dtype, shape):
+    """A CUDA tensor [B, H, N, d] whose rows may lie anywhere."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+
+
+def _freq_ptr(inv_freq, d, device):
+    if inv_freq is None:
+        return None, 0
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1 or 2 * inv_freq.numel() > d:
+        raise ValueError(f"inv_freq must be [rot/2] with rot <= {d}")
+    _check(inv_freq, "inv_freq", torch.float64, tuple(inv_freq.shape))
+    _same_device(device, inv_freq=inv_freq)
+    return inv_freq.data_ptr(), 2 * inv_freq.numel()
+
+
+def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", factor: float = 1.0,
+             inverse: bool = False, out=None, stream=None):
+    """Gives queries and keys their rotary positions, in one launch.  Q [B, Hq, N, d] and
+    K [B, Hkv, N, d] (or None) may have any strides with contiguous, 16-byte aligned rows, e.g.
+    the transposed view of a projection's output; the results are contiguous [B, H, N, d] (or
+    `out`, a pair of such tensors, which may be Q and K themselves).  The first 2 * len(inv_freq)
+    columns rotate.  Row n is at position start + n, or positions[n] / positions[b, n] (int32).
+    inverse: rotate back (the gradient).  Returns (Q', K')."""
+    lib = load_library()
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or Q.dtype not in _DTYPE:
+        raise ValueError("Q must be [B, H, N, d], bf16 or f32")
+    if layout not in _LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
+    B, _, N, d = Q.shape
+    dev = Q.device
+    ins = [("Q", Q)] if K is None else [("Q", Q), ("K", K)]
+    for name, t in ins:
+        _rows(t, name, Q.dtype, (B, t.shape[1] if t.dim() == 4 else -1, N, d))
+        _same_device(dev, **{name: t})
+    freq, rot = _freq_ptr(inv_freq, d, dev)
+    pos_stride = 0
+    if positions is not None:
+        if start:
+            raise ValueError("start and positions exclude each other")
+        _words(positions, "positions", (N,) if positions.dim() == 1 else (B, N), dev)
+        pos_stride = 0 if positions.dim() == 1 else N
+    with _On(dev, stream) as strm:
+        if out is None:
+            outs = [torch.empty((B, t.shape[1], N, d), dtype=t.dtype, device=dev) for _, t in ins]
+        else:
+            outs = [o for o in out if o is not None]
+            if len(outs) != len(ins):
+                raise ValueError("out must hold one tensor for each input")
+        for (name, t), o in zip(ins, outs):
+            _rows(o, "out " + name, t.dtype, t.shape)
+            _same_device(dev, **{"out " + name: o})
+        prm = CcaRopeParams(B, N, d, rot, _LAYOUT[layout], _DTYPE[Q.dtype], int(bool(inverse)), float(factor), freq,
+                            None if positions is None else positions.data_ptr(), pos_stride, int(start))
+        tensors = (CcaRopeTensor * 2)(*[_rope_tensor(t, o, name) for (name, t), o in zip(ins, outs)])
+        st = lib.cca_rope(tensors, len(ins), ctypes.byref(prm), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_rope")
+    return outs[0], (outs[1] if K is not None else None)
+
+
+def _rows_ready(t):
+    """t itself where its rows can be read in place, a contiguous copy otherwise."""
+    if t.data_ptr() % 16 == 0 and t.stride(3) == 1 and all(s * t.element_size() % 16 == 0 for s in t.stride()[:3]):
+        return t
+    return t.contiguous()
+
+
+class CcaRopeFunction(torch.autograd.Function):
+    """Autograd wrapper of cca_rope: the gradient is the rotation back, by the same kernel."""
+
+    @staticmethod
+    def forward(ctx, Q, K, inv_freq, positions, start, layout, factor):
+        ctx.save_for_backward(inv_freq, positions)
+        ctx.cfg = (start, layout, factor)
+        q, k = cca_rope(_rows_ready(Q), _rows_ready(K), inv_freq, positions, start, layout, factor)
+        return q, k
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        inv_freq, positions = ctx.saved_tensors
+        start, layout, factor = ctx.cfg
+        gq, gk = cca_rope(_rows_ready(dq), _rows_ready(dk), inv_freq, positions, start, layout, factor, inverse=True)
+        return gq, gk, None, None, None, None, None
+
+
+def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", factor: float = 1.0):
+    """cca_rope with gradients for Q and K (training): returns (Q', K')."""
+    return CcaRopeFunction.apply(Q, K, inv_freq, positions, start, layout, factor)
+
+
+# ---------------------------------------------------------------- paged caches
+
+def _pages(Kp, Vp, table, B, Hkv, d, dtype, what, layers: bool = False):
+    """(CcaPages, layers) of a pool [pages, Hkv, rows, d] ([layers, ...] where allowed) and its table."""
+    if not isinstance(Kp, torch.Tensor) or Kp.dim() not in ((4, 5) if layers else (4,)):
+        raise ValueError(f"{what} pool must be [{'layers, ' if layers else ''}pages, Hkv, rows, d]")
+    shape = tuple(Kp.shape)
+    if shape[-3] != Hkv or shape[-1] != d:
+        raise ValueError(f"{what} pool has shape {shape}, expected [pages, {Hkv}, rows, {d}]")
+    _check(Kp, what + " K pool", dtype, shape)
+    _check(Vp, what + " V pool", dtype, shape)
+    _same_device(Kp.device, **{what + " V pool": Vp})
+    cols, ptr = 0, None
+    if table is not None:
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError(f"{what} table must be [B, columns]")
+        ptr, cols = _words(table, what + " table", (B, table.shape[1]), Kp.device), table.shape[1]
+    return CcaPages(Kp.data_ptr(), Vp.data_ptr(), ptr, shape[-4], shape[-2], cols, shape[0] if len(shape) == 5 else 1)
+
+
+def _paged_params(B, Hq, Hkv, d, dtype, device, dev_status, g=1, w=1, scale=0.0, window_mode=0, pool_mode=0):
+    return make_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype], scale, _words(dev_status, "dev_status", (1,), device),
+                       window_mode, pool_mode)
+
+
+def cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq=None, parents=None, counts=None, layout: str = "half",
+                    factor: float = 1.0, out=None, dev_status=None, stream=None):
+    """The new tokens of a step: rotates Q [B, Hq, T, d] and K [B, Hkv, T, d], and stores K and V
+    into the raw pages at rows lens[b] + t.  Strides as in cca_rope.  parents [B, T] (int32): the
+    tokens are a drafted tree (see cca_tree_fwd), node t at position lens[b] + depth; without, at
+    lens[b] + t.  counts [B]: only the first counts[b] tokens are real.  Tokens that are not real are
+    not stored and their query rows are zero.  Without inv_freq nothing rotates (core tokens of a
+    prompt are stored that way, with Q None).  Returns the queries, contiguous [B, Hq, T, d]."""
+    lib = load_library()
+    if not isinstance(K, torch.Tensor) or K.dim() != 4 or K.dtype not in _DTYPE:
+        raise ValueError("K must be [B, Hkv, T, d], bf16 or f32")
+    if layout not in _LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
+    B, Hkv, T, d = K.shape
+    dev = K.device
+    _rows(K, "K", K.dtype, K.shape)
+    _rows(V, "V", K.dtype, K.shape)
+    if Q is not None:
+        _rows(Q, "Q", K.dtype, (B, Q.shape[1] if Q.dim() == 4 else -1, T, d))
+    _same_device(dev, Q=Q, V=V, pool=Kp)
+    pages = _pages(Kp, Vp, table, B, Hkv, d, K.dtype, "raw")
+    freq, rot = _freq_ptr(inv_freq, d, dev)
+    if parents is not None and T > 256:
+        raise ValueError("a tree has at most 256 nodes")
+    with _On(dev, stream) as strm:
+        if Q is not None and out is None:
+            out = torch.empty((B, Q.shape[1], T, d), dtype=K.dtype, device=dev)
+        qt = None
+        if Q is not None:
+            _rows(out, "out", K.dtype, Q.shape)
+            _same_device(dev, out=out)
+            qt = ctypes.byref(_rope_tensor(Q, out, "Q"))
+        prm = CcaRopeParams(B, T, d, rot, _LAYOUT[layout], _DTYPE[K.dtype], 0, float(factor), freq, None, 0, 0)
+        st = lib.cca_rope_append(qt, ctypes.byref(_rope_tensor(K, None, "K")), ctypes.byref(_rope_tensor(V, None, "V")),
+                                 ctypes.byref(pages), _words(lens, "lens", (B,), dev), _words(parents, "parents", (B, T), dev),
+                                 _words(counts, "counts", (B,), dev), _words(dev_status, "dev_status", (1,), dev),
+                                 ctypes.byref(prm), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_rope_append")
+    return out if Q is not None else None
+
+
+def tree_workspace_size(B, Hq, Hkv, T, d, g, w, dtype) -> int:
+    """Bytes of workspace cca_tree_fwd needs on the current device."""
+    prm = make_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype])
+    return int(load_library().cca_tree_workspace_size(ctypes.byref(prm), int(T)))
+
+
+def cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g: int, w: int, parents=None, O=None, LSE=None,
+                 workspace=None, scale: float = 0.0, dev_status=None, stream=None, window_mode: int = 0):
+    """CCA attention of drafted tokens over paged caches; T = 1 is plain decoding.
+    Q [B, Hq, T, d]; raw pool Kp, Vp [pages, Hkv, rows, d] with table [B, columns]; core pool Kcp, Vcp
+    with core_table; lens [B] committed tokens.  Node t's K and V lie in raw row lens[b] + t;
+    parents [B, T] is the node before it, -1 for a child of the last committed token, anything else
+    (-2) for padding; without parents the nodes are one chain.  Returns (O [B, Hq, T, d], LSE
+    [B, Hq, T] fp32); padding nodes have O = 0 and LSE = -inf."""
+    lib = load_library()
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or Q.dtype not in _DTYPE:
+        raise ValueError("Q must be [B, Hq, T, d], bf16 or f32")
+    B, Hq, T, d = Q.shape
+    dev = Q.device
+    _check(Q, "Q", Q.dtype, Q.shape)
+    Hkv = Kp.shape[1] if isinstance(Kp, torch.Tensor) and Kp.dim() == 4 else -1
+    raw = _pages(Kp, Vp, table, B, Hkv, d, Q.dtype, "raw")
+    core = _pages(Kcp, Vcp, core_table, B, Hkv, d, Q.dtype, "core")
+    _same_device(dev, raw_pool=Kp, core_pool=Kcp, O=O, LSE=LSE, workspace=workspace)
+    prm = _paged_params(B, Hq, Hkv, d, Q.dtype, dev, dev_status, g, w, scale, window_mode)
+    with _On(dev, stream) as strm:
+        need = int(lib.cca_tree_workspace_size(ctypes.byref(prm), T))
+        if O is None:
+            O = torch.empty_like(Q)
+        if LSE is None:
+            LSE = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        _check(O, "O", Q.dtype, (B, Hq, T, d))
+        _check(LSE, "LSE", torch.float32, (B, Hq, T))
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        nbytes = workspace.numel() * workspace.element_size()
+        if not workspace.is_cuda or nbytes < need:
+            raise ValueError(f"workspace must be a CUDA buffer of at least {need} bytes")
+        st = lib.cca_tree_fwd(Q.data_ptr(), ctypes.byref(raw), ctypes.byref(core), _words(lens, "lens", (B,), dev),
+                              _words(parents, "parents", (B, T), dev), T, O.data_ptr(), LSE.data_ptr(),
+                              ctypes.byref(prm), workspace.data_ptr(), nbytes, strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_tree_fwd")
+    return O, LSE
+
+
+def cca_pool_pages(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, accepted, g: int, path=None, scale: float = 0.0,
+                   dev_status=None, stream=None, pool_mode: int = 0):
+    """Pools the groups that the accepted[b] tokens after lens[b] complete, from raw pages into core
+    pages (in place).  Q [B, Hq, T, d] holds the step's queries; the i-th accepted token's is
+    Q[b, :, path[b, i]] (path [B, A] int32), or Q[b, :, i] without a path.  Returns (Kcp, Vcp)."""
+    lib = load_library()
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or Q.dtype not in _DTYPE:
+        raise ValueError("Q must be [B, Hq, T, d], bf16 or f32")
+    B, Hq, T, d = Q.shape
+    dev = Q.device
+    _check(Q, "Q", Q.dtype, Q.shape)
+    Hkv = Kp.shape[1] if isinstance(Kp, torch.Tensor) and Kp.dim() == 4 else -1
+    raw = _pages(Kp, Vp, table, B, Hkv, d, Q.dtype, "raw")
+    core = _pages(Kcp, Vcp, core_table, B, Hkv, d, Q.dtype, "core")
+    _same_device(dev, raw_pool=Kp, core_pool=Kcp)
+    A = T
+    if path is not None:
+        if path.dim() != 2:
+            raise ValueError("path must be [B, A]")
+        A = path.shape[1]
+    prm = _paged_params(B, Hq, Hkv, d, Q.dtype, dev, dev_status, g, 1, scale, pool_mode=pool_mode)
+    with _On(dev, stream) as strm:
+        st = lib.cca_pool_pages(Q.data_ptr(), ctypes.byref(raw), ctypes.byref(core), _words(lens, "lens", (B,), dev),
+                                _words(accepted, "accepted", (B,), dev), _words(path, "path", (B, A), dev), A, T,
+                                ctypes.byref(prm), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_pool_pages")
+    return Kcp, Vcp
+
+
+def _book(refs, table):
+    if not isinstance(refs, torch.Tensor) or not isinstance(table, torch.Tensor) or refs.dim() != 1 or table.dim() != 2:
+        raise ValueError("refs must be [pages] and table [B, columns]")
+    dev = refs.device
+    return dev, _words(refs, "refs", tuple(refs.shape), dev), _words(table, "table", tuple(table.shape), dev)
+
+
+def cca_pages_reserve(refs, table, lens, extra, rows: int, pairs=None, workspace=None, dev_status=None, stream=None):
+    """Room for rows [lens[b], lens[b] + extra[b]) of every sequence: table [B, columns] and refs
+    [pages] (int32, holders of each page) are updated in place.  Missing pages are the lowest free
+    ones; a shared page is replaced by one of the row's own.  Returns pairs [B, 2], (old, new) pages
+    for cca_pages_copy, (-1, -1) for none.  Too few free pages: nothing changes and dev_status
+    becomes CCA_ERR_NO_PAGES."""
+    lib = load_library()
+    dev, refs_p, table_p = _book(refs, table)
+    B, cols = table.shape
+    with _On(dev, stream) as strm:
+        if pairs is None:
+            pairs = torch.empty((B, 2), dtype=torch.int32, device=dev)
+        need = int(lib.cca_pages_reserve_workspace_size(B, cols))
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _same_device(dev, workspace=workspace)
+        nbytes = workspace.numel() * workspace.element_size()
+        if nbytes < need:
+            raise ValueError(f"workspace must be a CUDA buffer of at least {need} bytes")
+        st = lib.cca_pages_reserve(refs_p, refs.numel(), table_p, B, cols, int(rows), _words(lens, "lens", (B,), dev),
+                                   _words(extra, "extra", (B,), dev), _words(pairs, "pairs", (B, 2), dev),
+                                   workspace.data_ptr(), nbytes, _words(dev_status, "dev_status", (1,), dev), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_pages_reserve")
+    return pairs
+
+
+def cca_pages_fork(refs, table, src, dst, lens, rows: int, dev_status=None, stream=None):
+    """Table rows dst [n] become second holders of the pages of rows src [n] (the first
+    ceil(lens[src] / rows) entries), in place.  The dst rows must hold no pages."""
+    lib = load_library()
+    dev, refs_p, table_p = _book(refs, table)
+    B, cols = table.shape
+    n = src.numel()
+    with _On(dev, stream) as strm:
+        st = lib.cca_pages_fork(refs_p, refs.numel(), table_p, B, cols, int(rows), _words(src, "src", (n,), dev),
+                                _words(dst, "dst", (n,), dev), n, _words(lens, "lens", (B,), dev),
+                                _words(dev_status, "dev_status", (1,), dev), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_pages_fork")
+
+
+def cca_pages_free(refs, table, first, last, dev_status=None, stream=None):
+    """Entries [first[b], last[b]) of every table row give up their pages, in place."""
+    lib = load_library()
+    dev, refs_p, table_p = _book(refs, table)
+    B, cols = table.shape
+    with _On(dev, stream) as strm:
+        st = lib.cca_pages_free(refs_p, refs.numel(), table_p, B, cols, _words(first, "first", (B,), dev),
+                                _words(last, "last", (B,), dev), _words(dev_status, "dev_status", (1,), dev), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_pages_free")
+
+
+def _pool_dims(Kp):
+    if not isinstance(Kp, torch.Tensor) or Kp.dim() not in (4, 5) or Kp.dtype not in _DTYPE:
+        raise ValueError("pool must be [layers, pages, Hkv, rows, d] or [pages, Hkv, rows, d], bf16 or f32")
+    return Kp.shape[-3], Kp.shape[-1], Kp.device
+
+
+def cca_pages_copy(Kp, Vp, pairs, dev_status=None, stream=None):
+    """Copies page pairs[i, 0] to page pairs[i, 1] of the pools (every layer of a [layers, pages, ...]
+    pool), in place; pairs with a negative entry are skipped."""
+    lib = load_library()
+    Hkv, d, dev = _pool_dims(Kp)
+    pages = _pages(Kp, Vp, None, 1, Hkv, d, Kp.dtype, "the", layers=True)
+    if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2:
+        raise ValueError("pairs must be [n, 2]")
+    n = pairs.shape[0]
+    prm = _paged_params(1, Hkv, Hkv, d, Kp.dtype, dev, dev_status)
+    with _On(dev, stream) as strm:
+        st = lib.cca_pages_copy(ctypes.byref(pages), _words(pairs, "pairs", (n, 2), dev), n, ctypes.byref(prm), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_pages_copy")
+    return Kp, Vp
+
+
+def cca_pages_compact(Kp, Vp, table, lens, path, accepted, dev_status=None, stream=None):
+    """Keeps the accepted nodes of a drafted tree: raw row lens[b] + path[b, i] moves to row
+    lens[b] + i for i < accepted[b], K and V, every layer, in place.  path [B, A] rises."""
+    lib = load_library()
+    Hkv, d, dev = _pool_dims(Kp)
+    B = table.shape[0]
+    pages = _pages(Kp, Vp, table, B, Hkv, d, Kp.dtype, "raw", layers=True)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be [B, A]")
+    A = path.shape[1]
+    prm = _paged_params(B, Hkv, Hkv, d, Kp.dtype, dev, dev_status)
+    with _On(dev, stream) as strm:
+        st = lib.cca_pages_compact(ctypes.byref(pages), _words(lens, "lens", (B,), dev), _words(path, "path", (B, A), dev),
+                                   A, _words(accepted, "accepted", (B,), dev), ctypes.byref(prm), strm)
+    if st != CCA_OK:
+        raise CcaError(st, "cca_pages_compact")
+    return Kp, Vp

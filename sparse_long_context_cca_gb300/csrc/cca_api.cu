@@ -55,6 +55,10 @@ cca::Shape to_shape(const cca_params_t *p) {
     return s;
 }
 
+}  // namespace
+
+namespace cca {
+
 // The kernels are built for sm_103a only.
 int check_device() {
     int dev = 0;
@@ -73,7 +77,10 @@ int from_cuda(cudaError_t e) {
     return CCA_ERR_CUDA;
 }
 
-}  // namespace
+}  // namespace cca
+
+using cca::check_device;
+using cca::from_cuda;
 
 extern "C" {
 
@@ -265,6 +272,7 @@ const char *cca_status_string(int status) {
         case CCA_ERR_UNSUPPORTED: return "unsupported dtype/head-dim combination or device";
         case CCA_ERR_CUDA: return "CUDA error";
         case CCA_ERR_TIMEOUT: return "device pipeline wait timed out";
+        case CCA_ERR_NO_PAGES: return "too few free pages in the pool";
         case CCA_ERR_SCRATCH_LIMIT: return "shapes need more scratch than the no-allocation entry point holds";
         default: return "unknown status";
     }

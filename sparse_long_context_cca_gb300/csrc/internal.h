@@ -7,6 +7,11 @@
 
 namespace cca {
 
+// Status of the current device (the kernels are built for sm_103a only) and of a CUDA
+// call, as the C ABI reports them.
+int check_device();
+int from_cuda(cudaError_t e);
+
 struct Shape {
     int B, Hq, Hkv, N, d, g, w;
     float scale;  // resolved softmax scale (> 0)

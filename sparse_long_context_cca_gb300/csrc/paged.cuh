@@ -1,0 +1,66 @@
+// Shared by the kernels over paged caches: limits, host-side checks, and the list of keys
+// that the nodes of a drafted tree see.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/cca.h"
+#include "internal.h"
+#include "visibility.cuh"
+
+namespace cca {
+
+constexpr int TREE_MAX_NODES = 256;
+constexpr int TREE_MAX_BATCH = 1024;
+
+// A pool and its table as the ABI wants them (layers 0: any number).
+inline bool pages_ok(const cca_pages_t *p, int layers) {
+    if (p == nullptr || p->K == nullptr || p->V == nullptr || p->table == nullptr) return false;
+    if (((reinterpret_cast<uintptr_t>(p->K) | reinterpret_cast<uintptr_t>(p->V)) & 15u) != 0) return false;
+    if ((reinterpret_cast<uintptr_t>(p->table) & 3u) != 0) return false;
+    return p->n_pages >= 1 && p->rows >= 1 && p->cols >= 1 && p->layers >= 1 && (layers == 0 || p->layers == layers);
+}
+
+inline bool word_ptr(const void *p, bool needed) {
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 && (p != nullptr || !needed);
+}
+
+inline uint64_t pool_bytes(const cca_pages_t *p, const cca_params_t *q) {
+    return static_cast<uint64_t>(p->layers) * p->n_pages * p->rows * q->Hkv * q->d * (q->dtype == CCA_BF16 ? 2 : 4);
+}
+
+inline bool bytes_meet(const void *p, uint64_t n, const void *q, uint64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + m && b < a + n;
+}
+
+// Whether what is written (the core pool) lies in what is read, or its K in its V.  One pool
+// for both is fine: their tables name different pages.
+inline bool pools_meet(const cca_pages_t *raw, const cca_pages_t *core, const cca_params_t *q) {
+    const uint64_t r = pool_bytes(raw, q), c = pool_bytes(core, q);
+    if (raw->K == core->K && raw->V == core->V && raw->n_pages == core->n_pages && raw->rows == core->rows)
+        return bytes_meet(core->K, c, core->V, c);
+    return bytes_meet(core->K, c, core->V, c) || bytes_meet(core->K, c, raw->K, r) || bytes_meet(core->K, c, raw->V, r) ||
+           bytes_meet(core->V, c, raw->K, r) || bytes_meet(core->V, c, raw->V, r);
+}
+
+// cca_params_t for the paged calls: N is not used, w only where asked.
+inline int check_paged(const cca_params_t *p, bool need_w) {
+    if (p == nullptr) return CCA_ERR_INVALID_ARG;
+    if (p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->d < 1 || p->g < 1 || (need_w && p->w < 1)) return CCA_ERR_INVALID_ARG;
+    if (p->Hq % p->Hkv != 0) return CCA_ERR_INVALID_ARG;
+    if (p->dtype != CCA_BF16 && p->dtype != CCA_F32) return CCA_ERR_INVALID_ARG;
+    if (!(p->scale == p->scale) || isinf(p->scale)) return CCA_ERR_INVALID_ARG;
+    if (p->window_mode < 0 || p->window_mode > 1 || p->pool_mode < 0 || p->pool_mode > 3) return CCA_ERR_INVALID_ARG;
+    if (!word_ptr(p->dev_status, false)) return CCA_ERR_INVALID_ARG;
+    if (p->d != 64 && p->d != 128) return CCA_ERR_UNSUPPORTED;
+    return CCA_OK;
+}
+
+inline float resolve_scale(const cca_params_t *p) {
+    return p->scale > 0.f ? p->scale : 1.0f / sqrtf(static_cast<float>(p->d));
+}
+
+}  // namespace cca

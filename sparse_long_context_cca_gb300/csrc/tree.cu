@@ -1,0 +1,1092 @@
+// CCA attention of a tree of drafted tokens over paged caches (fusion equation of the
+// Method section, one row per node): node t at position p = len + depth(t) takes one
+// softmax over the cores j < lo(p)/g, the committed raw tokens of its window, its
+// ancestors and itself.  One node per sequence is plain decoding.
+//
+// What bounds it.  The r query heads of a KV head times T nodes are R = r*T rows that share
+// one list of keys: K and V rows are read once per (b, KV head) and meet R rows, so few rows
+// are bound by HBM and many by the matrix units.
+//
+// The key list of a sequence puts the keys that every node sees first (cores before the
+// shallowest node's window, raw tokens from the deepest one's window on), the few that only
+// some see last (at most T/g + 1 cores, T + g raw tokens, the T nodes).  Only tiles that
+// reach those, or that hold keys without a page, look at masks at all.
+//
+// Work split.  Lengths live on the device, so the split is made there: the tiles of all
+// (b, KV head) lists, one after the other, are dealt to the groups of the grid in equal
+// contiguous runs, whatever the lengths are.  A group finishes lists that lie wholly in its
+// run and writes a partial (max, sum, output) for its first and last list otherwise; a
+// second kernel joins the partials of a list in the order of the groups.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/cca.h"
+#include "internal.h"
+#include "paged.cuh"
+#include "sm100_ptx.cuh"
+
+namespace cca {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int TILE = 64;         // keys per tile
+constexpr int TREE_THREADS = 128;
+constexpr int MIN_TILES = 2;     // tiles a group takes at least
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct TreeArgs {
+    const void *Q, *K, *V, *Kc, *Vc;
+    const int32_t *table, *ctable, *lens, *parents;
+    int n_pages, rows, cols, n_cpages, crows, ccols;
+    int B, Hq, Hkv, T, g, w, window_mode;
+    int R;       // query rows of a KV head: Hq / Hkv * T
+    int n_mt;    // row tiles
+    int groups;  // groups of n_mt CTAs
+    float scale_log2;
+    void *O;
+    float *LSE;
+    float *ws;
+    int32_t *status;
+};
+
+// Keys of one sequence (see the top of the file).
+struct KeyList {
+    int len;
+    int cores_all, raw_all;  // cores [0, cores_all) and raw [raw_all, len) are seen by every node
+    int cores_some;          // cores [cores_all, cores_some) by some
+    int raw_some;            // raw [raw_some, raw_all) by some
+    int n_all, n;            // keys seen by every node; keys in all
+    int tiles;
+};
+
+__device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) {
+    KeyList k;
+    const int len = a.lens[b];
+    if (len < 0 || len > 0x7fffffff - 2 * TREE_MAX_NODES ||
+        static_cast<int64_t>(len) + a.T > static_cast<int64_t>(a.rows) * a.cols) {
+        // a length outside the table: an empty list, and one tile in which its rows are written
+        k = KeyList{0, 0, 0, 0, 0, 0, 0, 1};
+        return k;
+    }
+    const int last = len + a.T - 1;  // T <= w, so no window of a node begins after len
+    k.len = len;
+    k.cores_all = visible_cores(len, a.w, a.g);
+    k.cores_some = visible_cores(last, a.w, a.g);
+    k.raw_some = window_start(len, a.w, a.g, a.window_mode);
+    k.raw_all = window_start(last, a.w, a.g, a.window_mode);
+    k.n_all = k.cores_all + (len - k.raw_all);
+    k.n = k.n_all + (k.cores_some - k.cores_all) + (k.raw_all - k.raw_some) + a.T;
+    k.tiles = (k.n + TILE - 1) / TILE;
+    return k;
+}
+
+// What a key is: 0 seen by every node, 1 core `val`, 2 raw token `val`, 3 node `val`, 4 not there.
+struct Key {
+    int kind, val;
+    int64_t row;  // row of its pool: (page * Hkv + kv) * rows + row in the page
+    bool core;
+};
+
+__device__ __forceinline__ Key find_key(const TreeArgs &a, const KeyList &k, int b, int kv, int x) {
+    Key r;
+    r.kind = 0;
+    r.core = false;
+    r.row = -1;
+    int at;
+    if (x < k.cores_all) {
+        r.core = true;
+        at = x;
+    } else if (x < k.n_all) {
+        at = k.raw_all + (x - k.cores_all);
+    } else if (x >= k.n) {
+        r.kind = 4;
+        r.val = 0;
+        return r;
+    } else {
+        x -= k.n_all;
+        const int nc = k.cores_some - k.cores_all, nr = k.raw_all - k.raw_some;
+        if (x < nc) {
+            r.kind = 1;
+            r.core = true;
+            at = k.cores_all + x;
+        } else if (x < nc + nr) {
+            r.kind = 2;
+            at = k.raw_some + (x - nc);
+        } else {
+            r.kind = 3;
+            at = k.len + (x - nc - nr);
+        }
+    }
+    r.val = r.kind == 3 ? at - k.len : at;
+    const int per = r.core ? a.crows : a.rows;
+    const int c = at / per;
+    int page = -1;
+    if (c < (r.core ? a.ccols : a.cols))
+        page = (r.core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
+    if (page < 0 || page >= (r.core ? a.n_cpages : a.n_pages)) {
+        r.kind = 4;
+        if (a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        return r;
+    }
+    r.row = (static_cast<int64_t>(page) * a.Hkv + kv) * per + (at - c * per);
+    return r;
+}
+
+// ---------------------------------------------------------------- the split
+
+// Runs of tiles: group y takes tiles [begin(y), begin(y + 1)) of all W tiles.
+struct Split {
+    int64_t W;
+    int groups;
+    __device__ int64_t begin(int y) const { return W * y / groups; }
+    __device__ int owner(int64_t tile) const { return static_cast<int>(((tile + 1) * groups - 1) / W); }
+};
+
+__device__ __forceinline__ Split make_split(const TreeArgs &a, int64_t W) {
+    Split s;
+    s.W = W;
+    const int64_t most = W / MIN_TILES;
+    s.groups = most < a.groups ? static_cast<int>(most < 1 ? 1 : most) : a.groups;
+    return s;
+}
+
+// sm_first[b] = tiles of the sequences before b (times Hkv); returns all.  B <= 1024.
+__device__ int64_t scan_tiles(const TreeArgs &a, int64_t *sm_first, int64_t *sm_warp) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+    const int per = (a.B + nt - 1) / nt;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int64_t own = 0;
+    for (int b = b0; b < b1; ++b) own += static_cast<int64_t>(key_list(a, b).tiles) * a.Hkv;
+    int64_t x = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, x, off);
+        if (lane >= off) x += y;
+    }
+    if (lane == 31) sm_warp[warp] = x;
+    __syncthreads();
+    int64_t before = x - own, total = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i < warp) before += sm_warp[i];
+        total += sm_warp[i];
+    }
+    for (int b = b0; b < b1; ++b) {
+        sm_first[b] = before;
+        before += static_cast<int64_t>(key_list(a, b).tiles) * a.Hkv;
+    }
+    __syncthreads();
+    return total;
+}
+
+// The list that a tile belongs to.
+struct Item {
+    int b, kv;
+    int64_t first;  // its first tile
+    KeyList k;
+};
+
+__device__ __forceinline__ Item item_of(const TreeArgs &a, const int64_t *sm_first, int64_t tile) {
+    Item it;
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (sm_first[mid] <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    it.b = lo;
+    it.k = key_list(a, lo);
+    it.kv = static_cast<int>((tile - sm_first[lo]) / it.k.tiles);
+    it.first = sm_first[lo] + static_cast<int64_t>(it.kv) * it.k.tiles;
+    return it;
+}
+
+__device__ __forceinline__ void next_item(const TreeArgs &a, Item &it) {
+    it.first += it.k.tiles;
+    if (++it.kv == a.Hkv) {
+        it.kv = 0;
+        if (++it.b < a.B) it.k = key_list(a, it.b);
+    }
+}
+
+// ---------------------------------------------------------------- the nodes
+
+// Per node: its first raw token, its visible cores (-1 for an empty node), its ancestors and
+// itself as bits.  All threads call; `up` holds the parents meanwhile.
+struct Nodes {
+    int *start, *cores;
+    uint32_t *sees;  // [T][words]
+    int16_t *up;
+    int words;
+};
+
+__device__ void read_tree(const TreeArgs &a, const Nodes &n, const KeyList &k, int b) {
+    const int tid = threadIdx.x;
+    for (int t = tid; t < a.T; t += blockDim.x) {
+        int p = t - 1;
+        if (a.parents != nullptr) {
+            p = a.parents[static_cast<int64_t>(b) * a.T + t];
+            if (p != -1 && (p < 0 || p >= t)) p = -2;
+        }
+        n.up[t] = static_cast<int16_t>(p);
+    }
+    __syncthreads();
+    for (int t = tid; t < a.T; t += blockDim.x) {
+        for (int i = 0; i < n.words; ++i) n.sees[t * n.words + i] = 0;
+        int depth = -1, x = t;
+        while (x >= 0) {  // parents lie below their children, so this ends
+            n.sees[t * n.words + (x >> 5)] |= 1u << (x & 31);
+            ++depth;
+            x = n.up[x];
+        }
+        const int pos = k.len + depth;
+        const bool whole = x == -1 && k.n > 0;
+        n.cores[t] = whole ? visible_cores(pos, a.w, a.g) : -1;
+        n.start[t] = window_start(pos, a.w, a.g, a.window_mode);
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ bool row_sees(const Nodes &n, int t, int kind, int val) {
+    if (kind == 0) return true;
+    if (kind == 1) return val < n.cores[t];
+    if (kind == 2) return val >= n.start[t];
+    if (kind == 3) return (n.sees[t * n.words + (val >> 5)] >> (val & 31)) & 1u;
+    return false;
+}
+
+// Partials of a (group, row tile, slot): O [BM][D], max [BM], sum [BM] (log2 domain).
+__host__ __device__ __forceinline__ int64_t part_floats(int BM, int D) { return static_cast<int64_t>(BM) * (D + 2); }
+
+// Slot 0: the list that the group's run begins in; 1: the one it ends in.
+__device__ __forceinline__ float *part_at(const TreeArgs &a, int group, int mt, int slot, int BM, int D) {
+    return a.ws + ((static_cast<int64_t>(group) * a.n_mt + mt) * 2 + slot) * part_floats(BM, D);
+}
+
+// ---------------------------------------------------------------- bf16: matrix units
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+    const int n = there ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int STAGES = 3;
+constexpr int METAS = 4;  // addresses and kinds of the tiles from the one in work to the next to load
+
+struct Meta {
+    const char *k[TILE], *v[TILE];  // null: not there
+    int val[TILE];
+    uint32_t masked[2];  // bit per key: kind != 0
+    uint32_t odd[2];     // bit per key: V holds an infinity or NaN, and not every row sees it
+    uint8_t kind[TILE];
+};
+
+template <int D>
+struct TreeSmem {
+    static constexpr int ROW = D * 2;                  // bytes of a key row
+    static constexpr int TILE_BYTES = TILE * ROW;      // K or V
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int META_OFF = STAGES * STAGE_BYTES;
+    static constexpr int FIRST_OFF = META_OFF + METAS * static_cast<int>(sizeof(Meta));
+    // then: tiles before each sequence [B], 4 warp sums, node starts [T], cores [T], bits [T][words], parents [T]
+    static __host__ __device__ int bytes(int B, int T) {
+        return FIRST_OFF + 8 * (B + 4) + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16;
+    }
+};
+
+// Byte offset of 16-byte chunk c of row `row` in a tile: chunks are permuted inside each
+// 128 bytes by the row, so that the eight rows of an ldmatrix fall into different banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+    return static_cast<uint32_t>(row * (D * 2) + ((c ^ (row & 7)) << 4));
+}
+
+// WM warps side by side over 16-row blocks, 4 / WM over the keys of a tile.  One CTA walks
+// its group's run of tiles: cp.async keeps two tiles in flight behind the one in work, and
+// the page look-ups of the tile after those are done a step ahead, under the matrix work.
+template <int D, int WM>
+__global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs a) {
+    using S = TreeSmem<D>;
+    constexpr int BM = 16 * WM;
+    constexpr int WK = 4 / WM;
+    constexpr int KW = TILE / WK;  // keys of a warp
+    constexpr int NT = KW / 8;
+    constexpr int DT = D / 8;
+    constexpr int CPR = D / 8;     // 16-byte chunks per row
+    extern __shared__ __align__(128) unsigned char smem[];
+    Meta *meta = reinterpret_cast<Meta *>(smem + S::META_OFF);
+    int64_t *sm_first = reinterpret_cast<int64_t *>(smem + S::FIRST_OFF);
+    int64_t *sm_warp = sm_first + a.B;
+    Nodes nodes;
+    nodes.words = (a.T + 31) >> 5;
+    nodes.start = reinterpret_cast<int *>(sm_warp + 4);
+    nodes.cores = nodes.start + a.T;
+    nodes.sees = reinterpret_cast<uint32_t *>(nodes.cores + a.T);
+    nodes.up = reinterpret_cast<int16_t *>(nodes.sees + a.T * nodes.words);
+    const uint32_t stage0 = ptx::smem_addr(smem);
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wm = warp % WM, wk = warp / WM;
+    const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
+    const Split split = make_split(a, scan_tiles(a, sm_first, sm_warp));
+    if (group >= split.groups) return;
+    const int64_t x0 = split.begin(group), x1 = split.begin(group + 1);
+    if (x0 >= x1) return;
+
+    // ---- loading
+    Item ld = item_of(a, sm_first, x0);  // list of the tile whose addresses come next
+    auto look_up = [&](int64_t x, Key &key) {  // threads 0 .. 63, one key each
+        if (x >= x1) return;
+        if (x >= ld.first + ld.k.tiles) next_item(a, ld);
+        if (tid < TILE) key = find_key(a, ld.k, ld.b, ld.kv, static_cast<int>(x - ld.first) * TILE + tid);
+    };
+    auto put = [&](int64_t x, const Key &key) {
+        if (x >= x1 || tid >= TILE) return;
+        Meta &m = meta[(x - x0) & (METAS - 1)];
+        const int64_t off = key.row * S::ROW;
+        m.k[tid] = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Kc : a.K) + off;
+        m.v[tid] = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Vc : a.V) + off;
+        m.kind[tid] = static_cast<uint8_t>(key.kind);
+        m.val[tid] = key.val;
+        const unsigned some = __ballot_sync(kFull, key.kind != 0);
+        if (lane == 0) {
+            m.masked[warp] = some;
+            m.odd[warp] = 0;
+        }
+    };
+    auto issue = [&](int64_t x) {
+        if (x < x1) {
+            const Meta &m = meta[(x - x0) & (METAS - 1)];
+            const uint32_t base = stage0 + static_cast<uint32_t>((x - x0) % STAGES) * S::STAGE_BYTES;
+            constexpr int PER = TILE * CPR / TREE_THREADS;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = i * TREE_THREADS + tid, row = e / CPR, c = e % CPR;
+                const char *p = m.k[row];
+                cp16(base + chunk_at<D>(row, c), p == nullptr ? a.K : p + c * 16, p != nullptr);
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = i * TREE_THREADS + tid, row = e / CPR, c = e % CPR;
+                const char *p = m.v[row];
+                cp16(base + S::TILE_BYTES + chunk_at<D>(row, c), p == nullptr ? a.V : p + c * 16, p != nullptr);
+            }
+        }
+        cp_commit();
+    };
+    Key key = {};
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {  // the first STAGES tiles' addresses, all but one of them loaded
+        look_up(x0 + i, key);
+        put(x0 + i, key);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) issue(x0 + i);
+
+    // ---- the rows
+    Item it = item_of(a, sm_first, x0);
+    if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+    uint32_t qf[D / 16][4];
+    float o[DT][4], m[2], l[2];
+    int node[2];  // node of this thread's two rows, -1 past the last row
+    const int row0 = mt * BM + wm * 16 + (lane >> 2);
+    auto begin_item = [&]() {
+        read_tree(a, nodes, it.k, it.b);
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.Q) +
+                                 (static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T * D;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = row0 + 8 * i;
+            node[i] = row < a.R ? row % a.T : -1;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(q + static_cast<int64_t>(row) * D) + (lane & 3);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                qf[kk][i] = node[i] >= 0 ? src[kk * 8] : 0u;
+                qf[kk][2 + i] = node[i] >= 0 ? src[kk * 8 + 4] : 0u;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < DT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    };
+    begin_item();
+
+    for (int64_t x = x0; x < x1; ++x) {
+        cp_wait<STAGES - 2>();
+        __syncthreads();
+        issue(x + STAGES - 1);
+        look_up(x + STAGES, key);
+
+        const Meta &mt_ = meta[(x - x0) & (METAS - 1)];
+        const uint32_t kbase = stage0 + static_cast<uint32_t>((x - x0) % STAGES) * S::STAGE_BYTES;
+        const uint32_t vbase = kbase + S::TILE_BYTES;
+        const bool masked = (mt_.masked[0] | mt_.masked[1]) != 0;
+        // S = Q K^T over this warp's keys
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t f[4];
+                ldsm4(kbase + chunk_at<D>(wk * KW + n * 8 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), f);
+                mma16816(s[n], qf[kk], f[0], f[1]);
+                mma16816(s[n + 1], qf[kk], f[2], f[3]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] *= a.scale_log2;
+        }
+        if (masked) {
+            // An infinity or NaN in the V of a key that only some rows see would reach the
+            // others as 0 * NaN: such elements leave the tile and are added back by hand below.
+            Meta &mw = meta[(x - x0) & (METAS - 1)];
+            {
+                const int row = tid >> 1;
+                if (mw.kind[row] != 0 && mw.kind[row] != 4) {
+                    bool odd = false;
+                    for (int c = (tid & 1) * (CPR / 2); c < (tid & 1) * (CPR / 2) + CPR / 2; ++c) {
+                        uint4 *p = reinterpret_cast<uint4 *>(smem + (vbase - stage0) + chunk_at<D>(row, c));
+                        uint32_t v[4] = {p->x, p->y, p->z, p->w};
+                        bool hit = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if ((v[i] & 0x7f80u) == 0x7f80u) {
+                                v[i] &= 0xffff0000u;
+                                hit = true;
+                            }
+                            if ((v[i] & 0x7f800000u) == 0x7f800000u) {
+                                v[i] &= 0xffffu;
+                                hit = true;
+                            }
+                        }
+                        if (hit) *p = make_uint4(v[0], v[1], v[2], v[3]);
+                        odd |= hit;
+                    }
+                    if (odd) atomicOr(&mw.odd[row >> 5], 1u << (row & 31));
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = wk * KW + n * 8 + (lane & 3) * 2 + e;
+                    const int kind = mw.kind[c], val = mw.val[c];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (node[i] < 0 || !row_sees(nodes, node[i], kind, val)) s[n][2 * i + e] = -INFINITY;
+                }
+            }
+            __syncthreads();
+        }
+        // one step of the running softmax for this thread's two rows
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mx = s[0][2 * i];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+            mx = fmaxf(mx, m[i]);
+            const float base = mx == -INFINITY ? 0.f : mx;  // nothing visible yet: every p is 0
+            const float corr = ptx::ex2(m[i] - base);
+            m[i] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                s[n][2 * i] = ptx::ex2(s[n][2 * i] - base);
+                s[n][2 * i + 1] = ptx::ex2(s[n][2 * i + 1] - base);
+                sum += s[n][2 * i] + s[n][2 * i + 1];
+            }
+            l[i] = l[i] * corr + sum;  // this thread's columns; the quad adds up at the end
+#pragma unroll
+            for (int n = 0; n < DT; ++n) {
+                o[n][2 * i] *= corr;
+                o[n][2 * i + 1] *= corr;
+            }
+        }
+        // O += P V.  P is rounded to bf16 for the matrix units (the sum above is not).
+#pragma unroll
+        for (int kk = 0; kk < NT / 2; ++kk) {
+            const uint32_t p[4] = {ptx::pack_bf16x2(s[2 * kk][0], s[2 * kk][1]), ptx::pack_bf16x2(s[2 * kk][2], s[2 * kk][3]),
+                                   ptx::pack_bf16x2(s[2 * kk + 1][0], s[2 * kk + 1][1]),
+                                   ptx::pack_bf16x2(s[2 * kk + 1][2], s[2 * kk + 1][3])};
+#pragma unroll
+            for (int n = 0; n < DT; n += 2) {
+                uint32_t f[4];
+                ldsm4_t(vbase + chunk_at<D>(wk * KW + kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), n + (lane >> 4)), f);
+                mma16816(o[n], p, f[0], f[1]);
+                mma16816(o[n + 1], p, f[2], f[3]);
+            }
+        }
+        if (masked && (mt_.odd[0] | mt_.odd[1]) != 0) {
+            // p * v for the elements that were taken out, row by row
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                for (int c8 = 0; c8 < 8; ++c8) {
+                    const int c = wk * KW + n * 8 + c8;
+                    if (!((mt_.odd[c >> 5] >> (c & 31)) & 1u)) continue;
+                    const int owner = (lane & ~3) | (c8 >> 1);
+                    float p[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float even = __shfl_sync(kFull, s[n][2 * i], owner), odd = __shfl_sync(kFull, s[n][2 * i + 1], owner);
+                        p[i] = (c8 & 1) ? odd : even;
+                    }
+                    const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(mt_.v[c]);
+#pragma unroll
+                    for (int nn = 0; nn < DT; ++nn) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float f = __bfloat162float(v[nn * 8 + (lane & 3) * 2 + e]);
+                            if (f - f == 0.f) continue;  // finite
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (node[i] >= 0 && row_sees(nodes, node[i], mt_.kind[c], mt_.val[c])) o[nn][2 * i + e] += p[i] * f;
+                        }
+                    }
+                }
+            }
+        }
+        put(x + STAGES, key);
+
+        const int64_t end = it.first + it.k.tiles;
+        if (x + 1 != end && x + 1 != x1) continue;
+        // ---- the end of this list, or of this group's part of it
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(kFull, l[i], 1);
+            l[i] += __shfl_xor_sync(kFull, l[i], 2);
+        }
+        if constexpr (WK > 1) {
+            // the warps over the keys join: through the tile that was read last, which the
+            // next load reaches only after the barrier at the top
+            __syncthreads();
+            float *mine = reinterpret_cast<float *>(smem + (kbase - stage0)) + ((wk - 1) * WM + wm) * 16 * (D + 2);
+            if (wk > 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float *dst = mine + ((lane >> 2) + 8 * i) * (D + 2);
+#pragma unroll
+                    for (int n = 0; n < DT; ++n) {
+                        dst[n * 8 + (lane & 3) * 2] = o[n][2 * i];
+                        dst[n * 8 + (lane & 3) * 2 + 1] = o[n][2 * i + 1];
+                    }
+                    if ((lane & 3) == 0) {
+                        dst[D] = m[i];
+                        dst[D + 1] = l[i];
+                    }
+                }
+            }
+            __syncthreads();
+            if (wk == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float *src[WK];
+                    float mx = m[i];
+#pragma unroll
+                    for (int q = 1; q < WK; ++q) {
+                        src[q] = reinterpret_cast<float *>(smem + (kbase - stage0)) +
+                                 (((q - 1) * WM + wm) * 16 + (lane >> 2) + 8 * i) * (D + 2);
+                        mx = fmaxf(mx, src[q][D]);
+                    }
+                    const float base = mx == -INFINITY ? 0.f : mx;
+                    const float own = ptx::ex2(m[i] - base);
+                    l[i] *= own;
+#pragma unroll
+                    for (int n = 0; n < DT; ++n) {
+                        o[n][2 * i] *= own;
+                        o[n][2 * i + 1] *= own;
+                    }
+#pragma unroll
+                    for (int q = 1; q < WK; ++q) {
+                        const float f = ptx::ex2(src[q][D] - base);
+                        l[i] += src[q][D + 1] * f;
+#pragma unroll
+                        for (int n = 0; n < DT; ++n) {
+                            o[n][2 * i] += src[q][n * 8 + (lane & 3) * 2] * f;
+                            o[n][2 * i + 1] += src[q][n * 8 + (lane & 3) * 2 + 1] * f;
+                        }
+                    }
+                    m[i] = mx;
+                }
+            }
+        }
+        if (wk == 0) {
+            const bool whole = x0 <= it.first && end <= x1;
+            const int slot = x0 >= it.first ? 0 : 1;
+            float *part = part_at(a, group, mt, slot, BM, D);
+            const int64_t out0 = (static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = row0 + 8 * i, in = wm * 16 + (lane >> 2) + 8 * i;
+                if (node[i] < 0) continue;
+                if (nodes.cores[node[i]] < 0) {  // an empty node
+                    m[i] = -INFINITY;
+                    l[i] = 0.f;
+#pragma unroll
+                    for (int n = 0; n < DT; ++n) o[n][2 * i] = o[n][2 * i + 1] = 0.f;
+                }
+                if (whole) {
+                    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.O) + (out0 + row) * D) + (lane & 3);
+#pragma unroll
+                    for (int n = 0; n < DT; ++n) dst[n * 4] = ptx::pack_bf16x2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+                    if ((lane & 3) == 0) a.LSE[out0 + row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+                } else {
+                    float2 *dst = reinterpret_cast<float2 *>(part + static_cast<int64_t>(in) * D) + (lane & 3);
+#pragma unroll
+                    for (int n = 0; n < DT; ++n) dst[n * 4] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+                    if ((lane & 3) == 0) {
+                        part[BM * D + in] = m[i];
+                        part[BM * D + BM + in] = l[i];
+                    }
+                }
+            }
+        }
+        if (x + 1 < x1) {
+            next_item(a, it);
+            if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+            __syncthreads();  // the nodes of the old list have been used
+            begin_item();
+        }
+    }
+    cp_wait<0>();
+}
+
+// ---------------------------------------------------------------- fp32: CUDA cores
+
+constexpr int F32_BM = 16;
+
+template <int D>
+struct TreeF32Smem {
+    static constexpr int LD = D + 4;  // padded row: eight lanes' 16-byte reads of eight rows miss each other
+    static constexpr int V_OFF = TILE * LD;
+    static constexpr int Q_OFF = V_OFF + TILE * LD;
+    static constexpr int P_OFF = Q_OFF + F32_BM * D;
+    static constexpr int ML_OFF = P_OFF + F32_BM * TILE;  // max, sum, correction per row
+    static constexpr int KEY_OFF = ML_OFF + 3 * F32_BM;   // kind, value per key
+    static constexpr int FIRST_OFF = ((KEY_OFF + 2 * TILE) * 4 + 15) / 16 * 16;
+    static __host__ __device__ int bytes(int B, int T) {
+        return FIRST_OFF + 8 * (B + 4) + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16;
+    }
+};
+
+// The same walk with one tile in shared memory at a time; scores and sums in fp32.
+template <int D>
+__global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a) {
+    using S = TreeF32Smem<D>;
+    constexpr int BM = F32_BM;
+    constexpr int LD = S::LD;
+    constexpr int GROUPS = TREE_THREADS / D;  // row groups of the product with V
+    constexpr int RPT = BM / GROUPS;
+    extern __shared__ __align__(128) unsigned char smem[];
+    float *sk = reinterpret_cast<float *>(smem), *sv = sk + S::V_OFF, *sq = sk + S::Q_OFF, *sp = sk + S::P_OFF;
+    float *sm_m = sk + S::ML_OFF, *sm_l = sm_m + BM, *sm_c = sm_l + BM;
+    int *sm_kind = reinterpret_cast<int *>(sk + S::KEY_OFF), *sm_val = sm_kind + TILE;
+    int64_t *sm_first = reinterpret_cast<int64_t *>(smem + S::FIRST_OFF);
+    int64_t *sm_warp = sm_first + a.B;
+    Nodes nodes;
+    nodes.words = (a.T + 31) >> 5;
+    nodes.start = reinterpret_cast<int *>(sm_warp + 4);
+    nodes.cores = nodes.start + a.T;
+    nodes.sees = reinterpret_cast<uint32_t *>(nodes.cores + a.T);
+    nodes.up = reinterpret_cast<int16_t *>(nodes.sees + a.T * nodes.words);
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
+    const Split split = make_split(a, scan_tiles(a, sm_first, sm_warp));
+    if (group >= split.groups) return;
+    const int64_t x0 = split.begin(group), x1 = split.begin(group + 1);
+    if (x0 >= x1) return;
+    Item it = item_of(a, sm_first, x0);
+    const int col = tid % D, rg = tid / D;
+    float o[RPT];
+    int64_t out0 = 0;
+    bool fresh = true;
+    for (int64_t x = x0; x < x1; ++x) {
+        if (fresh) {
+            if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+            read_tree(a, nodes, it.k, it.b);
+            out0 = (static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T;
+            for (int e = tid; e < BM * D; e += TREE_THREADS) {
+                const int row = mt * BM + e / D;
+                sq[e] = row < a.R ? static_cast<const float *>(a.Q)[(out0 + row) * D + e % D] : 0.f;
+            }
+            if (tid < BM) {
+                sm_m[tid] = -INFINITY;
+                sm_l[tid] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) o[i] = 0.f;
+            fresh = false;
+        }
+        // two threads per key bring its K and V row
+        {
+            const int row = tid >> 1, half = tid & 1;
+            const Key key = find_key(a, it.k, it.b, it.kv, static_cast<int>(x - it.first) * TILE + row);
+            if (half == 0) {
+                sm_kind[row] = key.kind;
+                sm_val[row] = key.val;
+            }
+            const float4 *k = reinterpret_cast<const float4 *>(static_cast<const float *>(key.core ? a.Kc : a.K) + key.row * D);
+            const float4 *v = reinterpret_cast<const float4 *>(static_cast<const float *>(key.core ? a.Vc : a.V) + key.row * D);
+#pragma unroll 8
+            for (int c = half * (D / 8); c < (half + 1) * (D / 8); ++c) {
+                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(sk + row * LD + c * 4) = key.row < 0 ? zero : k[c];
+                *reinterpret_cast<float4 *>(sv + row * LD + c * 4) = key.row < 0 ? zero : v[c];
+            }
+        }
+        __syncthreads();
+        {
+            // thread: one key, eight rows
+            const int key = tid & (TILE - 1), r0 = (tid / TILE) * (BM / 2);
+            float s[BM / 2];
+#pragma unroll
+            for (int i = 0; i < BM / 2; ++i) s[i] = 0.f;
+            for (int c = 0; c < D; c += 4) {
+                const float4 k = *reinterpret_cast<const float4 *>(sk + key * LD + c);
+#pragma unroll
+                for (int i = 0; i < BM / 2; ++i) {
+                    const float4 q = *reinterpret_cast<const float4 *>(sq + (r0 + i) * D + c);
+                    s[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[i]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < BM / 2; ++i) {
+                const int row = mt * BM + r0 + i;
+                const bool sees = row < a.R && row_sees(nodes, row % a.T, sm_kind[key], sm_val[key]);
+                sp[(r0 + i) * TILE + key] = sees ? s[i] * a.scale_log2 : -INFINITY;
+            }
+        }
+        __syncthreads();
+        // a warp: four rows, two keys per lane
+#pragma unroll
+        for (int i = 0; i < BM / 4; ++i) {
+            const int row = warp * (BM / 4) + i;
+            const float s0 = sp[row * TILE + lane], s1 = sp[row * TILE + lane + 32];
+            float mx = fmaxf(s0, s1);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+            mx = fmaxf(mx, sm_m[row]);
+            const float base = mx == -INFINITY ? 0.f : mx;
+            const float p0 = exp2f(s0 - base), p1 = exp2f(s1 - base);
+            float sum = p0 + p1;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+            // -1 marks a key that the row does not see: its V is left out whatever it holds
+            sp[row * TILE + lane] = s0 == -INFINITY ? -1.f : p0;
+            sp[row * TILE + lane + 32] = s1 == -INFINITY ? -1.f : p1;
+            if (lane == 0) {
+                const float corr = exp2f(sm_m[row] - base);
+                sm_c[row] = corr;
+                sm_l[row] = sm_l[row] * corr + sum;
+                sm_m[row] = mx;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) o[i] *= sm_c[rg * RPT + i];
+        for (int key = 0; key < TILE; ++key) {
+            const float v = sv[key * LD + col];
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const float p = sp[(rg * RPT + i) * TILE + key];
+                if (!(p < 0.f)) o[i] = fmaf(p, v, o[i]);
+            }
+        }
+        const int64_t end = it.first + it.k.tiles;
+        if (x + 1 == end || x + 1 == x1) {
+            const bool whole = x0 <= it.first && end <= x1;
+            float *part = part_at(a, group, mt, x0 >= it.first ? 0 : 1, BM, D);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const int in = rg * RPT + i, row = mt * BM + in;
+                if (row >= a.R) continue;
+                const bool empty = nodes.cores[row % a.T] < 0;
+                const float l = empty ? 0.f : sm_l[in], mx = empty ? -INFINITY : sm_m[in], acc = empty ? 0.f : o[i];
+                if (whole) {
+                    static_cast<float *>(a.O)[(out0 + row) * D + col] = l == 0.f ? 0.f : acc / l;
+                    if (col == 0) a.LSE[out0 + row] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
+                } else {
+                    part[static_cast<int64_t>(in) * D + col] = acc;
+                    if (col == 0) {
+                        part[BM * D + in] = mx;
+                        part[BM * D + BM + in] = l;
+                    }
+                }
+            }
+            if (x + 1 < x1) {
+                next_item(a, it);
+                fresh = true;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- joining the partials
+
+constexpr int JOIN_WARPS = 4;
+
+// A warp joins one row of one list: the groups that wrote a part of it, in order.  Lists
+// that one group finished are already written.
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TreeArgs a, int BM) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    int64_t *sm_first = reinterpret_cast<int64_t *>(smem), *sm_warp = sm_first + a.B;
+    constexpr int C = D / 32;  // columns of a lane
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Split split = make_split(a, scan_tiles(a, sm_first, sm_warp));
+    const int64_t bk = blockIdx.x;
+    const int row = blockIdx.y * JOIN_WARPS + warp;
+    const int b = static_cast<int>(bk / a.Hkv), kv = static_cast<int>(bk - static_cast<int64_t>(b) * a.Hkv);
+    const int tiles = key_list(a, b).tiles;
+    const int64_t s = sm_first[b] + static_cast<int64_t>(kv) * tiles, e = s + tiles;
+    const int y0 = split.owner(s), y1 = split.owner(e - 1);
+    if (y0 == y1 || row >= a.R) return;
+    const int mt = row / BM, in = row - mt * BM;
+    auto part = [&](int y) -> const float * {
+        const int64_t x0 = split.begin(y);
+        if (split.begin(y + 1) <= x0) return nullptr;  // an empty run
+        return part_at(a, y, mt, x0 >= s ? 0 : 1, BM, D);
+    };
+    float mx = -INFINITY;
+    for (int y = y0 + lane; y <= y1; y += 32) {
+        const float *p = part(y);
+        if (p != nullptr) mx = fmaxf(mx, p[BM * D + in]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float acc[C], l = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+    for (int yb = y0; yb <= y1; yb += 32) {
+        const float *p = yb + lane <= y1 ? part(yb + lane) : nullptr;
+        const float f = p == nullptr ? 0.f : exp2f(p[BM * D + in] - base);
+        if (p != nullptr) l += p[BM * D + BM + in] * f;
+        const int n = min(32, y1 - yb + 1);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float w = __shfl_sync(kFull, f, k);
+            const float *q = reinterpret_cast<const float *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(p), k));
+            if (q == nullptr) continue;
+            q += static_cast<int64_t>(in) * D + lane * C;
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] = fmaf(q[c], w, acc[c]);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+    const int64_t at = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kv) * (a.Hq / a.Hkv)) * a.T + row;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const float v = l == 0.f ? 0.f : acc[c] / l;
+        if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16 *>(a.O)[at * D + lane * C + c] = __float2bfloat16_rn(v);
+        else static_cast<float *>(a.O)[at * D + lane * C + c] = v;
+    }
+    if (lane == 0) a.LSE[at] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- launch
+
+struct Plan {
+    int BM, n_mt, ctas;  // rows per CTA, row tiles, CTAs that are resident together
+    int smem;
+};
+
+template <typename K>
+cudaError_t prepare_kernel(K kernel, int smem, int &per_sm) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, TREE_THREADS, smem);
+}
+
+template <typename K>
+cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, const TreeArgs &a, bool join, int BM) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if constexpr (std::is_same<K, void (*)(TreeArgs)>::value) {
+        return cudaLaunchKernelEx(&cfg, kernel, a);
+    } else {
+        return cudaLaunchKernelEx(&cfg, kernel, a, BM);
+    }
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+constexpr int MAX_CTAS_PER_SM = 4;
+
+// Rows per CTA: 16 rows of a warp each, so that as few row tiles as possible read the keys.
+int rows_per_cta(int dtype, int R) { return dtype == CCA_F32 ? F32_BM : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+
+uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
+    // CTAs times two slots; a grid holds at most MAX_CTAS_PER_SM per SM, and one group of row tiles at least
+    const int BM = rows_per_cta(dtype, R);
+    const int64_t n_mt = (R + BM - 1) / BM;
+    int64_t ctas = static_cast<int64_t>(sms) * MAX_CTAS_PER_SM;
+    if (ctas < n_mt) ctas = n_mt;
+    return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
+}
+
+template <typename K, typename J>
+cudaError_t run_tree(K kernel, J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t stream) {
+    int per_sm = 0;
+    cudaError_t e = prepare_kernel(kernel, smem, per_sm);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    if (per_sm > MAX_CTAS_PER_SM) per_sm = MAX_CTAS_PER_SM;
+    a.n_mt = (a.R + BM - 1) / BM;
+    a.groups = per_sm * sms / a.n_mt;
+    if (a.groups < 1) a.groups = 1;
+    e = start(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a, false, BM);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_WARPS - 1) / JOIN_WARPS);
+    return start(join, grid, JOIN_WARPS * 32, 8 * (a.B + JOIN_WARPS), stream, a, true, BM);
+}
+
+template <int D>
+cudaError_t run_bf16(const TreeArgs &a, int sms, cudaStream_t stream) {
+    const int smem = TreeSmem<D>::bytes(a.B, a.T);
+    auto *join = tree_join_kernel<__nv_bfloat16, D>;
+    switch (rows_per_cta(CCA_BF16, a.R)) {
+        case 16: return run_tree(tree_bf16_kernel<D, 1>, join, a, 16, smem, sms, stream);
+        case 32: return run_tree(tree_bf16_kernel<D, 2>, join, a, 32, smem, sms, stream);
+        default: return run_tree(tree_bf16_kernel<D, 4>, join, a, 64, smem, sms, stream);
+    }
+}
+
+int check_tree(const cca_params_t *p, int T) {
+    const int st = check_paged(p, true);
+    if (st != CCA_OK) return st;
+    if (T < 1 || p->B > 0x7fffffff / p->Hkv) return CCA_ERR_INVALID_ARG;
+    if (T > TREE_MAX_NODES || T > p->w || p->B > TREE_MAX_BATCH) return CCA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(p->Hq / p->Hkv) * T > 4 * 65535) return CCA_ERR_UNSUPPORTED;
+    return CCA_OK;
+}
+
+}  // namespace
+}  // namespace cca
+
+extern "C" {
+
+uint64_t cca_tree_workspace_size(const cca_params_t *params, int T) {
+    using namespace cca;
+    if (check_tree(params, T) != CCA_OK) return 0;
+    int sms = sm_count();
+    if (sms < 1) sms = 152;  // no device here: the size a GB300 needs
+    return workspace_bytes_for(params->dtype, params->Hq / params->Hkv * T, params->d, sms);
+}
+
+int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core, const int32_t *lens,
+                 const int32_t *parents, int T, void *O, float *LSE, const cca_params_t *params, void *workspace,
+                 uint64_t workspace_bytes, void *stream) {
+    using namespace cca;
+    int st = check_tree(params, T);
+    if (st != CCA_OK) return st;
+    if (!pages_ok(raw, 1) || !pages_ok(core, 1)) return CCA_ERR_INVALID_ARG;
+    const void *ptrs[4] = {Q, O, LSE, workspace};
+    for (const void *p : ptrs)
+        if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) != 0) return CCA_ERR_INVALID_ARG;
+    if (!word_ptr(lens, true) || !word_ptr(parents, false)) return CCA_ERR_INVALID_ARG;
+    if (workspace_bytes < cca_tree_workspace_size(params, T)) return CCA_ERR_INVALID_ARG;
+    const uint64_t es = params->dtype == CCA_BF16 ? 2 : 4;
+    const uint64_t out = static_cast<uint64_t>(params->B) * params->Hq * T * params->d * es;
+    if (bytes_meet(O, out, Q, out)) return CCA_ERR_INVALID_ARG;  // row tiles of other CTAs may still read Q
+    if ((st = check_device()) != CCA_OK) return st;
+    const int sms = sm_count();
+    if (sms < 1) return CCA_ERR_CUDA;
+    TreeArgs a;
+    a.Q = Q;
+    a.K = raw->K;
+    a.V = raw->V;
+    a.Kc = core->K;
+    a.Vc = core->V;
+    a.table = raw->table;
+    a.ctable = core->table;
+    a.lens = lens;
+    a.parents = parents;
+    a.n_pages = raw->n_pages;
+    a.rows = raw->rows;
+    a.cols = raw->cols;
+    a.n_cpages = core->n_pages;
+    a.crows = core->rows;
+    a.ccols = core->cols;
+    a.B = params->B;
+    a.Hq = params->Hq;
+    a.Hkv = params->Hkv;
+    a.T = T;
+    a.g = params->g;
+    a.w = params->w;
+    a.window_mode = params->window_mode;
+    a.R = params->Hq / params->Hkv * T;
+    a.n_mt = 1;
+    a.groups = 1;
+    a.scale_log2 = resolve_scale(params) * 1.4426950408889634f;
+    a.O = O;
+    a.LSE = LSE;
+    a.ws = static_cast<float *>(workspace);
+    a.status = params->dev_status;
+    cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    if (params->dtype == CCA_BF16)
+        return from_cuda(params->d == 128 ? run_bf16<128>(a, sms, strm) : run_bf16<64>(a, sms, strm));
+    if (params->d == 128)
+        return from_cuda(run_tree(tree_f32_kernel<128>, tree_join_kernel<float, 128>, a, F32_BM,
+                                  TreeF32Smem<128>::bytes(a.B, T), sms, strm));
+    return from_cuda(run_tree(tree_f32_kernel<64>, tree_join_kernel<float, 64>, a, F32_BM, TreeF32Smem<64>::bytes(a.B, T),
+                              sms, strm));
+}
+
+}  // extern "C"
