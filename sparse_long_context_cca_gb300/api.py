@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -121,19 +122,20 @@ def load_library():
         lib.cca_pool_group.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int, pp, vp]
         lib.cca_pool_group.restype = ctypes.c_int
         u64 = ctypes.c_uint64
-        rp, rt, pg = (ctypes.POINTER(x) for x in (CcaRopeParams, CcaRopeTensor, CcaPages))
+        # structures of the newer calls arrive packed (_pack_*), so their pointers are plain
+        rp = rt = pg = pq = vp
         for name, args, res in (
                 ("cca_rope", [rt, ci, rp, vp], ci),
                 ("cca_rope_append", [rt, rt, rt, pg, vp, vp, vp, vp, rp, vp], ci),
-                ("cca_tree_fwd", [vp, pg, pg, vp, vp, ci, vp, vp, pp, vp, u64, vp], ci),
-                ("cca_tree_workspace_size", [pp, ci], u64),
-                ("cca_pool_pages", [vp, pg, pg, vp, vp, vp, ci, ci, pp, vp], ci),
+                ("cca_tree_fwd", [vp, pg, pg, vp, vp, ci, vp, vp, pq, vp, u64, vp], ci),
+                ("cca_tree_workspace_size", [pq, ci], u64),
+                ("cca_pool_pages", [vp, pg, pg, vp, vp, vp, ci, ci, pq, vp], ci),
                 ("cca_pages_reserve", [vp, ci, vp, ci, ci, ci, vp, vp, vp, vp, u64, vp, vp], ci),
                 ("cca_pages_reserve_workspace_size", [ci, ci], u64),
                 ("cca_pages_fork", [vp, ci, vp, ci, ci, ci, vp, vp, ci, vp, vp, vp], ci),
                 ("cca_pages_free", [vp, ci, vp, ci, ci, vp, vp, vp, vp], ci),
-                ("cca_pages_copy", [pg, vp, ci, pp, vp], ci),
-                ("cca_pages_compact", [pg, vp, vp, ci, vp, pp, vp], ci)):
+                ("cca_pages_copy", [pg, vp, ci, pq, vp], ci),
+                ("cca_pages_compact", [pg, vp, vp, ci, vp, pq, vp], ci)):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, res
         lib.cca_status_string.argtypes = [ctypes.c_int]
@@ -553,28 +555,41 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     return f.to(device), attention
 
 
-class _On:
-    """Runs a call on the tensors' device and on the caller's stream (the device's current one
-    without), so that what is allocated inside belongs to that stream too."""
+# A decoding step makes many small calls, so the ones below keep the host's share low: checks
+# that build nothing unless they fail, structures packed in one go (the layouts are those of
+# CcaParams, CcaRopeParams, CcaRopeTensor and CcaPages), and the raw stream of the device.
+_pack_params = struct.Struct("@8if4xP2i").pack
+_pack_rope = struct.Struct("@7ifPP2q").pack
+_pack_rope_tensor = struct.Struct("@PPi4x6q").pack
+_pack_pages = struct.Struct("@PPP4i").pack
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_F32, _F64, _I32 = torch.float32, torch.float64, torch.int32
 
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
+
+def _elsewhere(dev: int, stream) -> bool:
+    return stream is not None or torch.cuda.current_device() != dev
+
+
+class _On:
+    """The tensors' device and the caller's stream (the device's current one without) as current
+    ones, so that what a call allocates belongs to them too."""
+
+    def __init__(self, dev: int, stream):
+        self.dev, self.stream = dev, stream
 
     def __enter__(self):
-        self.there = torch.cuda.device(self.device)
+        s = self.stream
+        if s is not None:
+            if not hasattr(s, "cuda_stream"):
+                s = torch.cuda.ExternalStream(int(s), device=self.dev)
+            if s.device.index != self.dev:
+                raise ValueError(f"stream is on {s.device}, the tensors on cuda:{self.dev}")
+        self.there = torch.cuda.device(self.dev)
         self.there.__enter__()
         self.over = None
-        if self.stream is None:
-            return int(torch.cuda.current_stream().cuda_stream)
-        s = self.stream
-        if not hasattr(s, "cuda_stream"):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        if s.device != self.device:
-            self.there.__exit__(None, None, None)
-            raise ValueError(f"stream is on {s.device}, the tensors on {self.device}")
-        self.over = torch.cuda.stream(s)
-        self.over.__enter__()
-        return int(s.cuda_stream)
+        if s is not None:
+            self.over = torch.cuda.stream(s)
+            self.over.__enter__()
 
     def __exit__(self, *exc):
         if self.over is not None:
@@ -582,46 +597,54 @@ class _On:
         self.there.__exit__(*exc)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _words(t, name, shape, device):
-    """A contiguous int32 tensor of the call's device; its pointer (None for None)."""
-    if t is None:
-        return None
-    _check(t, name, torch.int32, shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t.data_ptr()
-
-
-def _rope_tensor(x, y, name) -> CcaRopeTensor:
-    if x.stride(3) != 1 or (y is not None and y.stride(3) != 1):
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    xs, ys = x.stride(), (0, 0, 0) if y is None else y.stride()
-    return CcaRopeTensor(x.data_ptr(), None if y is None else y.data_ptr(), x.shape[1],
-                         (ctypes.c_int64 * 3)(*xs[:3]), (ctypes.c_int64 * 3)(*ys[:3]))
-
-
-def _rows(t, name, dtype, shape):
-    """A CUDA tensor [B, H, N, d] whose rows may lie anywhere."""
+def _device_of(t, name: str, dims, dtypes=None) -> int:
+    """The device of the tensor that says where a call runs."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+    return t.get_device()
 
 
-def _freq_ptr(inv_freq, d, device):
+def _ptr(t, name: str, dtype, shape, dev: int):
+    """Pointer of a contiguous tensor of the call's device; None for None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _rows_of(t, name: str, dtype, shape, dev: int):
+    """Strides of a tensor [B, H, N, d] whose rows may lie anywhere."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{dev}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return s
+
+
+def _rope_tensor(x, y, xs, ys) -> bytes:
+    return _pack_rope_tensor(x.data_ptr(), 0 if y is None else y.data_ptr(), x.shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
+
+
+def _turns(inv_freq, d: int, dev: int):
+    """(pointer, rotated columns) of the frequencies."""
     if inv_freq is None:
-        return None, 0
+        return 0, 0
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1 or 2 * inv_freq.numel() > d:
         raise ValueError(f"inv_freq must be [rot/2] with rot <= {d}")
-    _check(inv_freq, "inv_freq", torch.float64, tuple(inv_freq.shape))
-    _same_device(device, inv_freq=inv_freq)
-    return inv_freq.data_ptr(), 2 * inv_freq.numel()
+    return _ptr(inv_freq, "inv_freq", _F64, inv_freq.shape, dev), 2 * inv_freq.numel()
+
+
+def _layout(name: str) -> int:
+    if name not in _LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
+    return _LAYOUT[name]
 
 
 def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", factor: float = 1.0,
@@ -632,41 +655,38 @@ def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half
     `out`, a pair of such tensors, which may be Q and K themselves).  The first 2 * len(inv_freq)
     columns rotate.  Row n is at position start + n, or positions[n] / positions[b, n] (int32).
     inverse: rotate back (the gradient).  Returns (Q', K')."""
-    lib = load_library()
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or Q.dtype not in _DTYPE:
-        raise ValueError("Q must be [B, H, N, d], bf16 or f32")
-    if layout not in _LAYOUT:
-        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
-    B, _, N, d = Q.shape
-    dev = Q.device
-    ins = [("Q", Q)] if K is None else [("Q", Q), ("K", K)]
-    for name, t in ins:
-        _rows(t, name, Q.dtype, (B, t.shape[1] if t.dim() == 4 else -1, N, d))
-        _same_device(dev, **{name: t})
-    freq, rot = _freq_ptr(inv_freq, d, dev)
-    pos_stride = 0
+    lib = _lib or load_library()
+    dev = _device_of(Q, "Q", (4,), _DTYPE)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_rope(Q, K, inv_freq, positions, start, layout, factor, inverse, out)
+    dtype = Q.dtype
+    B, Hq, N, d = Q.shape
+    freq, rot = _turns(inv_freq, d, dev)
+    pos = pos_stride = 0
     if positions is not None:
         if start:
             raise ValueError("start and positions exclude each other")
-        _words(positions, "positions", (N,) if positions.dim() == 1 else (B, N), dev)
-        pos_stride = 0 if positions.dim() == 1 else N
-    with _On(dev, stream) as strm:
-        if out is None:
-            outs = [torch.empty((B, t.shape[1], N, d), dtype=t.dtype, device=dev) for _, t in ins]
-        else:
-            outs = [o for o in out if o is not None]
-            if len(outs) != len(ins):
-                raise ValueError("out must hold one tensor for each input")
-        for (name, t), o in zip(ins, outs):
-            _rows(o, "out " + name, t.dtype, t.shape)
-            _same_device(dev, **{"out " + name: o})
-        prm = CcaRopeParams(B, N, d, rot, _LAYOUT[layout], _DTYPE[Q.dtype], int(bool(inverse)), float(factor), freq,
-                            None if positions is None else positions.data_ptr(), pos_stride, int(start))
-        tensors = (CcaRopeTensor * 2)(*[_rope_tensor(t, o, name) for (name, t), o in zip(ins, outs)])
-        st = lib.cca_rope(tensors, len(ins), ctypes.byref(prm), strm)
+        shared = isinstance(positions, torch.Tensor) and positions.dim() == 1
+        pos, pos_stride = _ptr(positions, "positions", _I32, (N,) if shared else (B, N), dev), 0 if shared else N
+    q, k = (None, None) if out is None else out
+    if (k is None) != (K is None) and out is not None:
+        raise ValueError("out must hold one tensor for each input")
+    if q is None:
+        q = torch.empty((B, Hq, N, d), dtype=dtype, device=Q.device)
+    tensors = _rope_tensor(Q, q, _rows_of(Q, "Q", dtype, (B, Hq, N, d), dev), _rows_of(q, "out Q", dtype, Q.shape, dev))
+    if K is not None:
+        Hkv = K.shape[1] if isinstance(K, torch.Tensor) and K.dim() == 4 else -1
+        ks = _rows_of(K, "K", dtype, (B, Hkv, N, d), dev)
+        if k is None:
+            k = torch.empty((B, Hkv, N, d), dtype=dtype, device=Q.device)
+        tensors += _rope_tensor(K, k, ks, _rows_of(k, "out K", dtype, K.shape, dev))
+    st = lib.cca_rope(tensors, 1 if K is None else 2,
+                      _pack_rope(B, N, d, rot, _layout(layout), _DTYPE[dtype], bool(inverse), factor, freq, pos, pos_stride, start),
+                      _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_rope")
-    return outs[0], (outs[1] if K is not None else None)
+    return q, k
 
 
 def _rows_ready(t):
@@ -701,27 +721,25 @@ def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", f
 
 # ---------------------------------------------------------------- paged caches
 
-def _pages(Kp, Vp, table, B, Hkv, d, dtype, what, layers: bool = False):
-    """(CcaPages, layers) of a pool [pages, Hkv, rows, d] ([layers, ...] where allowed) and its table."""
+def _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, what: str, layers: bool = False) -> bytes:
+    """A pool [pages, Hkv, rows, d] ([layers, pages, ...] where allowed) and its table, packed."""
     if not isinstance(Kp, torch.Tensor) or Kp.dim() not in ((4, 5) if layers else (4,)):
         raise ValueError(f"{what} pool must be [{'layers, ' if layers else ''}pages, Hkv, rows, d]")
-    shape = tuple(Kp.shape)
-    if shape[-3] != Hkv or shape[-1] != d:
-        raise ValueError(f"{what} pool has shape {shape}, expected [pages, {Hkv}, rows, {d}]")
-    _check(Kp, what + " K pool", dtype, shape)
-    _check(Vp, what + " V pool", dtype, shape)
-    _same_device(Kp.device, **{what + " V pool": Vp})
-    cols, ptr = 0, None
+    shape = Kp.shape
+    if Vp is None or shape[-3] != Hkv or shape[-1] != d:
+        raise ValueError(f"{what} pool has shape {tuple(shape)}, expected [pages, {Hkv}, rows, {d}]")
+    cols = ptr = 0
     if table is not None:
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError(f"{what} table must be [B, columns]")
-        ptr, cols = _words(table, what + " table", (B, table.shape[1]), Kp.device), table.shape[1]
-    return CcaPages(Kp.data_ptr(), Vp.data_ptr(), ptr, shape[-4], shape[-2], cols, shape[0] if len(shape) == 5 else 1)
+        cols = table.shape[1]
+        ptr = _ptr(table, what + " table", _I32, (B, cols), dev)
+    return _pack_pages(_ptr(Kp, what + " K pool", dtype, shape, dev), _ptr(Vp, what + " V pool", dtype, shape, dev), ptr,
+                       shape[-4], shape[-2], cols, shape[0] if len(shape) == 5 else 1)
 
 
-def _paged_params(B, Hq, Hkv, d, dtype, device, dev_status, g=1, w=1, scale=0.0, window_mode=0, pool_mode=0):
-    return make_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype], scale, _words(dev_status, "dev_status", (1,), device),
-                       window_mode, pool_mode)
+def _heads_of(Kp) -> int:
+    return Kp.shape[1] if isinstance(Kp, torch.Tensor) and Kp.dim() == 4 else -1
 
 
 def cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq=None, parents=None, counts=None, layout: str = "half",
@@ -732,44 +750,38 @@ def cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq=None, parents=None, c
     lens[b] + t.  counts [B]: only the first counts[b] tokens are real.  Tokens that are not real are
     not stored and their query rows are zero.  Without inv_freq nothing rotates (core tokens of a
     prompt are stored that way, with Q None).  Returns the queries, contiguous [B, Hq, T, d]."""
-    lib = load_library()
-    if not isinstance(K, torch.Tensor) or K.dim() != 4 or K.dtype not in _DTYPE:
-        raise ValueError("K must be [B, Hkv, T, d], bf16 or f32")
-    if layout not in _LAYOUT:
-        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
+    lib = _lib or load_library()
+    dev = _device_of(K, "K", (4,), _DTYPE)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out, dev_status)
+    dtype = K.dtype
     B, Hkv, T, d = K.shape
-    dev = K.device
-    _rows(K, "K", K.dtype, K.shape)
-    _rows(V, "V", K.dtype, K.shape)
+    none = (0, 0, 0)
+    k = _rope_tensor(K, None, _rows_of(K, "K", dtype, K.shape, dev), none)
+    v = _rope_tensor(V, None, _rows_of(V, "V", dtype, K.shape, dev), none)
+    pool = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw")
+    freq, rot = _turns(inv_freq, d, dev)
+    q = None
     if Q is not None:
-        _rows(Q, "Q", K.dtype, (B, Q.shape[1] if Q.dim() == 4 else -1, T, d))
-    _same_device(dev, Q=Q, V=V, pool=Kp)
-    pages = _pages(Kp, Vp, table, B, Hkv, d, K.dtype, "raw")
-    freq, rot = _freq_ptr(inv_freq, d, dev)
-    if parents is not None and T > 256:
-        raise ValueError("a tree has at most 256 nodes")
-    with _On(dev, stream) as strm:
-        if Q is not None and out is None:
-            out = torch.empty((B, Q.shape[1], T, d), dtype=K.dtype, device=dev)
-        qt = None
-        if Q is not None:
-            _rows(out, "out", K.dtype, Q.shape)
-            _same_device(dev, out=out)
-            qt = ctypes.byref(_rope_tensor(Q, out, "Q"))
-        prm = CcaRopeParams(B, T, d, rot, _LAYOUT[layout], _DTYPE[K.dtype], 0, float(factor), freq, None, 0, 0)
-        st = lib.cca_rope_append(qt, ctypes.byref(_rope_tensor(K, None, "K")), ctypes.byref(_rope_tensor(V, None, "V")),
-                                 ctypes.byref(pages), _words(lens, "lens", (B,), dev), _words(parents, "parents", (B, T), dev),
-                                 _words(counts, "counts", (B,), dev), _words(dev_status, "dev_status", (1,), dev),
-                                 ctypes.byref(prm), strm)
+        qs = _rows_of(Q, "Q", dtype, (B, Q.shape[1] if isinstance(Q, torch.Tensor) and Q.dim() == 4 else -1, T, d), dev)
+        if out is None:
+            out = torch.empty(Q.shape, dtype=dtype, device=Q.device)
+        q = _rope_tensor(Q, out, qs, _rows_of(out, "out", dtype, Q.shape, dev))
+    elif out is not None:
+        raise ValueError("out without Q")
+    st = lib.cca_rope_append(q, k, v, pool, _ptr(lens, "lens", _I32, (B,), dev), _ptr(parents, "parents", _I32, (B, T), dev),
+                             _ptr(counts, "counts", _I32, (B,), dev), _ptr(dev_status, "dev_status", _I32, (1,), dev),
+                             _pack_rope(B, T, d, rot, _layout(layout), _DTYPE[dtype], 0, factor, freq, 0, 0, 0), _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_rope_append")
-    return out if Q is not None else None
+    return out
 
 
 def tree_workspace_size(B, Hq, Hkv, T, d, g, w, dtype) -> int:
     """Bytes of workspace cca_tree_fwd needs on the current device."""
-    prm = make_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype])
-    return int(load_library().cca_tree_workspace_size(ctypes.byref(prm), int(T)))
+    prm = _pack_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype], 0.0, 0, 0, 0)
+    return int(load_library().cca_tree_workspace_size(prm, int(T)))
 
 
 def cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g: int, w: int, parents=None, O=None, LSE=None,
@@ -780,33 +792,33 @@ def cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g: int, w: int, p
     parents [B, T] is the node before it, -1 for a child of the last committed token, anything else
     (-2) for padding; without parents the nodes are one chain.  Returns (O [B, Hq, T, d], LSE
     [B, Hq, T] fp32); padding nodes have O = 0 and LSE = -inf."""
-    lib = load_library()
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or Q.dtype not in _DTYPE:
-        raise ValueError("Q must be [B, Hq, T, d], bf16 or f32")
-    B, Hq, T, d = Q.shape
-    dev = Q.device
-    _check(Q, "Q", Q.dtype, Q.shape)
-    Hkv = Kp.shape[1] if isinstance(Kp, torch.Tensor) and Kp.dim() == 4 else -1
-    raw = _pages(Kp, Vp, table, B, Hkv, d, Q.dtype, "raw")
-    core = _pages(Kcp, Vcp, core_table, B, Hkv, d, Q.dtype, "core")
-    _same_device(dev, raw_pool=Kp, core_pool=Kcp, O=O, LSE=LSE, workspace=workspace)
-    prm = _paged_params(B, Hq, Hkv, d, Q.dtype, dev, dev_status, g, w, scale, window_mode)
-    with _On(dev, stream) as strm:
-        need = int(lib.cca_tree_workspace_size(ctypes.byref(prm), T))
-        if O is None:
-            O = torch.empty_like(Q)
-        if LSE is None:
-            LSE = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-        _check(O, "O", Q.dtype, (B, Hq, T, d))
-        _check(LSE, "LSE", torch.float32, (B, Hq, T))
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        nbytes = workspace.numel() * workspace.element_size()
-        if not workspace.is_cuda or nbytes < need:
-            raise ValueError(f"workspace must be a CUDA buffer of at least {need} bytes")
-        st = lib.cca_tree_fwd(Q.data_ptr(), ctypes.byref(raw), ctypes.byref(core), _words(lens, "lens", (B,), dev),
-                              _words(parents, "parents", (B, T), dev), T, O.data_ptr(), LSE.data_ptr(),
-                              ctypes.byref(prm), workspace.data_ptr(), nbytes, strm)
+    lib = _lib or load_library()
+    dev = _device_of(Q, "Q", (4,), _DTYPE)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g, w, parents, O, LSE, workspace, scale,
+                                dev_status, None, window_mode)
+    dtype, shape = Q.dtype, Q.shape
+    B, Hq, T, d = shape
+    Hkv = _heads_of(Kp)
+    q = _ptr(Q, "Q", dtype, shape, dev)
+    raw = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw")
+    core = _pool(Kcp, Vcp, core_table, B, Hkv, d, dtype, dev, "core")
+    prm = _pack_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype], scale, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0,
+                       window_mode, 0)
+    if O is None:
+        O = torch.empty_like(Q)
+    if LSE is None:
+        LSE = torch.empty((B, Hq, T), dtype=_F32, device=Q.device)
+    need = lib.cca_tree_workspace_size(prm, T)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=Q.device)
+    nbytes = workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev or not workspace.is_contiguous() or nbytes < need:
+        raise ValueError(f"workspace must be a buffer of at least {need} bytes on cuda:{dev}")
+    st = lib.cca_tree_fwd(q, raw, core, _ptr(lens, "lens", _I32, (B,), dev), _ptr(parents, "parents", _I32, (B, T), dev), T,
+                          _ptr(O, "O", dtype, shape, dev), _ptr(LSE, "LSE", _F32, (B, Hq, T), dev), prm, workspace.data_ptr(),
+                          nbytes, _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_tree_fwd")
     return O, LSE
@@ -817,36 +829,39 @@ def cca_pool_pages(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, accepted, g: in
     """Pools the groups that the accepted[b] tokens after lens[b] complete, from raw pages into core
     pages (in place).  Q [B, Hq, T, d] holds the step's queries; the i-th accepted token's is
     Q[b, :, path[b, i]] (path [B, A] int32), or Q[b, :, i] without a path.  Returns (Kcp, Vcp)."""
-    lib = load_library()
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 4 or Q.dtype not in _DTYPE:
-        raise ValueError("Q must be [B, Hq, T, d], bf16 or f32")
+    lib = _lib or load_library()
+    dev = _device_of(Q, "Q", (4,), _DTYPE)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_pool_pages(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, accepted, g, path, scale, dev_status, None,
+                                  pool_mode)
+    dtype = Q.dtype
     B, Hq, T, d = Q.shape
-    dev = Q.device
-    _check(Q, "Q", Q.dtype, Q.shape)
-    Hkv = Kp.shape[1] if isinstance(Kp, torch.Tensor) and Kp.dim() == 4 else -1
-    raw = _pages(Kp, Vp, table, B, Hkv, d, Q.dtype, "raw")
-    core = _pages(Kcp, Vcp, core_table, B, Hkv, d, Q.dtype, "core")
-    _same_device(dev, raw_pool=Kp, core_pool=Kcp)
-    A = T
-    if path is not None:
-        if path.dim() != 2:
-            raise ValueError("path must be [B, A]")
-        A = path.shape[1]
-    prm = _paged_params(B, Hq, Hkv, d, Q.dtype, dev, dev_status, g, 1, scale, pool_mode=pool_mode)
-    with _On(dev, stream) as strm:
-        st = lib.cca_pool_pages(Q.data_ptr(), ctypes.byref(raw), ctypes.byref(core), _words(lens, "lens", (B,), dev),
-                                _words(accepted, "accepted", (B,), dev), _words(path, "path", (B, A), dev), A, T,
-                                ctypes.byref(prm), strm)
+    Hkv = _heads_of(Kp)
+    q = _ptr(Q, "Q", dtype, Q.shape, dev)
+    raw = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw")
+    core = _pool(Kcp, Vcp, core_table, B, Hkv, d, dtype, dev, "core")
+    A = T if path is None else _columns(path, "path")
+    prm = _pack_params(B, Hq, Hkv, 0, d, g, 1, _DTYPE[dtype], scale, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0, 0,
+                       pool_mode)
+    st = lib.cca_pool_pages(q, raw, core, _ptr(lens, "lens", _I32, (B,), dev), _ptr(accepted, "accepted", _I32, (B,), dev),
+                            _ptr(path, "path", _I32, (B, A), dev), A, T, prm, _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_pool_pages")
     return Kcp, Vcp
 
 
+def _columns(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape[1]
+
+
 def _book(refs, table):
-    if not isinstance(refs, torch.Tensor) or not isinstance(table, torch.Tensor) or refs.dim() != 1 or table.dim() != 2:
-        raise ValueError("refs must be [pages] and table [B, columns]")
-    dev = refs.device
-    return dev, _words(refs, "refs", tuple(refs.shape), dev), _words(table, "table", tuple(table.shape), dev)
+    """(device, refs pointer, pages, table pointer, rows, columns) of a pages' book."""
+    dev = _device_of(refs, "refs", (1,))
+    n, cols = refs.shape[0], _columns(table, "table")
+    return dev, _ptr(refs, "refs", _I32, (n,), dev), n, _ptr(table, "table", _I32, table.shape, dev), table.shape[0], cols
 
 
 def cca_pages_reserve(refs, table, lens, extra, rows: int, pairs=None, workspace=None, dev_status=None, stream=None):
@@ -855,22 +870,22 @@ def cca_pages_reserve(refs, table, lens, extra, rows: int, pairs=None, workspace
     ones; a shared page is replaced by one of the row's own.  Returns pairs [B, 2], (old, new) pages
     for cca_pages_copy, (-1, -1) for none.  Too few free pages: nothing changes and dev_status
     becomes CCA_ERR_NO_PAGES."""
-    lib = load_library()
-    dev, refs_p, table_p = _book(refs, table)
-    B, cols = table.shape
-    with _On(dev, stream) as strm:
-        if pairs is None:
-            pairs = torch.empty((B, 2), dtype=torch.int32, device=dev)
-        need = int(lib.cca_pages_reserve_workspace_size(B, cols))
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _same_device(dev, workspace=workspace)
-        nbytes = workspace.numel() * workspace.element_size()
-        if nbytes < need:
-            raise ValueError(f"workspace must be a CUDA buffer of at least {need} bytes")
-        st = lib.cca_pages_reserve(refs_p, refs.numel(), table_p, B, cols, int(rows), _words(lens, "lens", (B,), dev),
-                                   _words(extra, "extra", (B,), dev), _words(pairs, "pairs", (B, 2), dev),
-                                   workspace.data_ptr(), nbytes, _words(dev_status, "dev_status", (1,), dev), strm)
+    lib = _lib or load_library()
+    dev, refs_p, n, table_p, B, cols = _book(refs, table)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_pages_reserve(refs, table, lens, extra, rows, pairs, workspace, dev_status)
+    if pairs is None:
+        pairs = torch.empty((B, 2), dtype=_I32, device=refs.device)
+    need = lib.cca_pages_reserve_workspace_size(B, cols)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=refs.device)
+    nbytes = workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev or not workspace.is_contiguous() or nbytes < need:
+        raise ValueError(f"workspace must be a buffer of at least {need} bytes on cuda:{dev}")
+    st = lib.cca_pages_reserve(refs_p, n, table_p, B, cols, rows, _ptr(lens, "lens", _I32, (B,), dev),
+                               _ptr(extra, "extra", _I32, (B,), dev), _ptr(pairs, "pairs", _I32, (B, 2), dev),
+                               workspace.data_ptr(), nbytes, _ptr(dev_status, "dev_status", _I32, (1,), dev), _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_pages_reserve")
     return pairs
@@ -879,48 +894,45 @@ def cca_pages_reserve(refs, table, lens, extra, rows: int, pairs=None, workspace
 def cca_pages_fork(refs, table, src, dst, lens, rows: int, dev_status=None, stream=None):
     """Table rows dst [n] become second holders of the pages of rows src [n] (the first
     ceil(lens[src] / rows) entries), in place.  The dst rows must hold no pages."""
-    lib = load_library()
-    dev, refs_p, table_p = _book(refs, table)
-    B, cols = table.shape
-    n = src.numel()
-    with _On(dev, stream) as strm:
-        st = lib.cca_pages_fork(refs_p, refs.numel(), table_p, B, cols, int(rows), _words(src, "src", (n,), dev),
-                                _words(dst, "dst", (n,), dev), n, _words(lens, "lens", (B,), dev),
-                                _words(dev_status, "dev_status", (1,), dev), strm)
+    lib = _lib or load_library()
+    dev, refs_p, n, table_p, B, cols = _book(refs, table)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_pages_fork(refs, table, src, dst, lens, rows, dev_status)
+    count = src.numel() if isinstance(src, torch.Tensor) else -1
+    st = lib.cca_pages_fork(refs_p, n, table_p, B, cols, rows, _ptr(src, "src", _I32, (count,), dev),
+                            _ptr(dst, "dst", _I32, (count,), dev), count, _ptr(lens, "lens", _I32, (B,), dev),
+                            _ptr(dev_status, "dev_status", _I32, (1,), dev), _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_pages_fork")
 
 
 def cca_pages_free(refs, table, first, last, dev_status=None, stream=None):
     """Entries [first[b], last[b]) of every table row give up their pages, in place."""
-    lib = load_library()
-    dev, refs_p, table_p = _book(refs, table)
-    B, cols = table.shape
-    with _On(dev, stream) as strm:
-        st = lib.cca_pages_free(refs_p, refs.numel(), table_p, B, cols, _words(first, "first", (B,), dev),
-                                _words(last, "last", (B,), dev), _words(dev_status, "dev_status", (1,), dev), strm)
+    lib = _lib or load_library()
+    dev, refs_p, n, table_p, B, cols = _book(refs, table)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_pages_free(refs, table, first, last, dev_status)
+    st = lib.cca_pages_free(refs_p, n, table_p, B, cols, _ptr(first, "first", _I32, (B,), dev),
+                            _ptr(last, "last", _I32, (B,), dev), _ptr(dev_status, "dev_status", _I32, (1,), dev), _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_pages_free")
-
-
-def _pool_dims(Kp):
-    if not isinstance(Kp, torch.Tensor) or Kp.dim() not in (4, 5) or Kp.dtype not in _DTYPE:
-        raise ValueError("pool must be [layers, pages, Hkv, rows, d] or [pages, Hkv, rows, d], bf16 or f32")
-    return Kp.shape[-3], Kp.shape[-1], Kp.device
 
 
 def cca_pages_copy(Kp, Vp, pairs, dev_status=None, stream=None):
     """Copies page pairs[i, 0] to page pairs[i, 1] of the pools (every layer of a [layers, pages, ...]
     pool), in place; pairs with a negative entry are skipped."""
-    lib = load_library()
-    Hkv, d, dev = _pool_dims(Kp)
-    pages = _pages(Kp, Vp, None, 1, Hkv, d, Kp.dtype, "the", layers=True)
-    if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2:
-        raise ValueError("pairs must be [n, 2]")
-    n = pairs.shape[0]
-    prm = _paged_params(1, Hkv, Hkv, d, Kp.dtype, dev, dev_status)
-    with _On(dev, stream) as strm:
-        st = lib.cca_pages_copy(ctypes.byref(pages), _words(pairs, "pairs", (n, 2), dev), n, ctypes.byref(prm), strm)
+    lib = _lib or load_library()
+    dev = _device_of(Kp, "pool", (4, 5), _DTYPE)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_pages_copy(Kp, Vp, pairs, dev_status)
+    Hkv, d, dtype = Kp.shape[-3], Kp.shape[-1], Kp.dtype
+    pool = _pool(Kp, Vp, None, 1, Hkv, d, dtype, dev, "the", True)
+    n = pairs.shape[0] if _columns(pairs, "pairs") == 2 else -1
+    prm = _pack_params(1, Hkv, Hkv, 0, d, 1, 1, _DTYPE[dtype], 0.0, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0, 0, 0)
+    st = lib.cca_pages_copy(pool, _ptr(pairs, "pairs", _I32, (n, 2), dev), n, prm, _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_pages_copy")
     return Kp, Vp
@@ -929,17 +941,18 @@ def cca_pages_copy(Kp, Vp, pairs, dev_status=None, stream=None):
 def cca_pages_compact(Kp, Vp, table, lens, path, accepted, dev_status=None, stream=None):
     """Keeps the accepted nodes of a drafted tree: raw row lens[b] + path[b, i] moves to row
     lens[b] + i for i < accepted[b], K and V, every layer, in place.  path [B, A] rises."""
-    lib = load_library()
-    Hkv, d, dev = _pool_dims(Kp)
-    B = table.shape[0]
-    pages = _pages(Kp, Vp, table, B, Hkv, d, Kp.dtype, "raw", layers=True)
-    if not isinstance(path, torch.Tensor) or path.dim() != 2:
-        raise ValueError("path must be [B, A]")
-    A = path.shape[1]
-    prm = _paged_params(B, Hkv, Hkv, d, Kp.dtype, dev, dev_status)
-    with _On(dev, stream) as strm:
-        st = lib.cca_pages_compact(ctypes.byref(pages), _words(lens, "lens", (B,), dev), _words(path, "path", (B, A), dev),
-                                   A, _words(accepted, "accepted", (B,), dev), ctypes.byref(prm), strm)
+    lib = _lib or load_library()
+    dev = _device_of(Kp, "pool", (4, 5), _DTYPE)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return cca_pages_compact(Kp, Vp, table, lens, path, accepted, dev_status)
+    Hkv, d, dtype = Kp.shape[-3], Kp.shape[-1], Kp.dtype
+    A = _columns(path, "path")
+    B = path.shape[0]
+    pool = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw", True)
+    prm = _pack_params(B, Hkv, Hkv, 0, d, 1, 1, _DTYPE[dtype], 0.0, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0, 0, 0)
+    st = lib.cca_pages_compact(pool, _ptr(lens, "lens", _I32, (B,), dev), _ptr(path, "path", _I32, (B, A), dev), A,
+                               _ptr(accepted, "accepted", _I32, (B,), dev), prm, _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_pages_compact")
     return Kp, Vp

@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/cca.h"
 #include "internal.h"
 #include "visibility.cuh"
@@ -59,16 +61,40 @@ cca::Shape to_shape(const cca_params_t *p) {
 
 namespace cca {
 
-// The kernels are built for sm_103a only.
+// The kernels are built for sm_103a only.  A device's answer does not change, so it is asked
+// once (concurrent first calls store the same values).
+namespace {
+constexpr int MAX_DEVICES = 64;
+std::atomic<int> g_device_ok[MAX_DEVICES];   // 0 unknown, 1 sm_103, 2 another
+std::atomic<int> g_device_sms[MAX_DEVICES];  // 0 unknown
+}  // namespace
+
 int check_device() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CCA_ERR_CUDA;
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return CCA_ERR_CUDA;
-    if (major != 10 || minor != 3) return CCA_ERR_UNSUPPORTED;
-    return CCA_OK;
+    const bool kept = dev >= 0 && dev < MAX_DEVICES;
+    int ok = kept ? g_device_ok[dev].load(std::memory_order_relaxed) : 0;
+    if (ok == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+            return CCA_ERR_CUDA;
+        ok = major == 10 && minor == 3 ? 1 : 2;
+        if (kept) g_device_ok[dev].store(ok, std::memory_order_relaxed);
+    }
+    return ok == 1 ? CCA_OK : CCA_ERR_UNSUPPORTED;
+}
+
+int device_sms() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool kept = dev >= 0 && dev < MAX_DEVICES;
+    int sms = kept ? g_device_sms[dev].load(std::memory_order_relaxed) : 0;
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        if (kept) g_device_sms[dev].store(sms, std::memory_order_relaxed);
+    }
+    return sms;
 }
 
 int from_cuda(cudaError_t e) {

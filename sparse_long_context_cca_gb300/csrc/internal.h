@@ -8,8 +8,9 @@
 namespace cca {
 
 // Status of the current device (the kernels are built for sm_103a only) and of a CUDA
-// call, as the C ABI reports them.
+// call, as the C ABI reports them; SMs of the current device (0 without one).
 int check_device();
+int device_sms();
 int from_cuda(cudaError_t e);
 
 struct Shape {

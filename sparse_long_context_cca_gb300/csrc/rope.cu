@@ -275,10 +275,8 @@ cudaError_t launch_rope_any(int dtype, RopeArgs a, cudaStream_t stream) {
     const int64_t rows = PAGED ? a.N : static_cast<int64_t>(a.B) * a.N;
     const int64_t blocks = (rows * units + ROPE_THREADS - 1) / ROPE_THREADS;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    const int sms = device_sms();
+    if (sms < 1) return cudaErrorNoDevice;
     // Angles are shared by the heads of a group: as many heads per thread as still leave
     // eight blocks for every SM.
     const int64_t all = blocks * (PAGED ? a.B : 1);

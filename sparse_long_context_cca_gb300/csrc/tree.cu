@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/cca.h"
@@ -929,20 +930,31 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TreeAr
 
 // ---------------------------------------------------------------- launch
 
-struct Plan {
-    int BM, n_mt, ctas;  // rows per CTA, row tiles, CTAs that are resident together
-    int smem;
-};
+constexpr int MAX_SMEM = 227 * 1024;
 
-template <typename K>
-cudaError_t prepare_kernel(K kernel, int smem, int &per_sm) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Resident CTAs per SM of a kernel with `smem` bytes.  The answer depends on the kernel, the
+// device and the bytes alone; the last one of each kernel and device is kept.
+template <auto kernel>
+cudaError_t resident(int smem, int &per_sm) {
+    static std::atomic<uint64_t> kept[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, TREE_THREADS, smem);
+    const bool room = dev >= 0 && dev < 64;
+    const uint64_t k = room ? kept[dev].load(std::memory_order_relaxed) : 0;
+    if (k != 0 && static_cast<int>(k >> 32) == smem) {
+        per_sm = static_cast<int>(k & 0xffffffffu);
+        return cudaSuccess;
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, TREE_THREADS, smem);
+    if (e == cudaSuccess && room) kept[dev].store(static_cast<uint64_t>(smem) << 32 | static_cast<uint32_t>(per_sm));
+    return e;
 }
 
 template <typename K>
-cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, const TreeArgs &a, bool join, int BM) {
+cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, const TreeArgs &a, int BM) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -960,13 +972,6 @@ cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t strea
     }
 }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 constexpr int MAX_CTAS_PER_SM = 4;
 
 // Rows per CTA: 16 rows of a warp each, so that as few row tiles as possible read the keys.
@@ -981,20 +986,20 @@ uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
     return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
 }
 
-template <typename K, typename J>
-cudaError_t run_tree(K kernel, J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t stream) {
+template <auto kernel, typename J>
+cudaError_t run_tree(J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t stream) {
     int per_sm = 0;
-    cudaError_t e = prepare_kernel(kernel, smem, per_sm);
+    cudaError_t e = resident<kernel>(smem, per_sm);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     if (per_sm > MAX_CTAS_PER_SM) per_sm = MAX_CTAS_PER_SM;
     a.n_mt = (a.R + BM - 1) / BM;
     a.groups = per_sm * sms / a.n_mt;
     if (a.groups < 1) a.groups = 1;
-    e = start(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a, false, BM);
+    e = start(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a, BM);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_WARPS - 1) / JOIN_WARPS);
-    return start(join, grid, JOIN_WARPS * 32, 8 * (a.B + JOIN_WARPS), stream, a, true, BM);
+    return start(join, grid, JOIN_WARPS * 32, 8 * (a.B + JOIN_WARPS), stream, a, BM);
 }
 
 template <int D>
@@ -1002,9 +1007,9 @@ cudaError_t run_bf16(const TreeArgs &a, int sms, cudaStream_t stream) {
     const int smem = TreeSmem<D>::bytes(a.B, a.T);
     auto *join = tree_join_kernel<__nv_bfloat16, D>;
     switch (rows_per_cta(CCA_BF16, a.R)) {
-        case 16: return run_tree(tree_bf16_kernel<D, 1>, join, a, 16, smem, sms, stream);
-        case 32: return run_tree(tree_bf16_kernel<D, 2>, join, a, 32, smem, sms, stream);
-        default: return run_tree(tree_bf16_kernel<D, 4>, join, a, 64, smem, sms, stream);
+        case 16: return run_tree<tree_bf16_kernel<D, 1>>(join, a, 16, smem, sms, stream);
+        case 32: return run_tree<tree_bf16_kernel<D, 2>>(join, a, 32, smem, sms, stream);
+        default: return run_tree<tree_bf16_kernel<D, 4>>(join, a, 64, smem, sms, stream);
     }
 }
 
@@ -1025,7 +1030,7 @@ extern "C" {
 uint64_t cca_tree_workspace_size(const cca_params_t *params, int T) {
     using namespace cca;
     if (check_tree(params, T) != CCA_OK) return 0;
-    int sms = sm_count();
+    int sms = device_sms();
     if (sms < 1) sms = 152;  // no device here: the size a GB300 needs
     return workspace_bytes_for(params->dtype, params->Hq / params->Hkv * T, params->d, sms);
 }
@@ -1046,7 +1051,7 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     const uint64_t out = static_cast<uint64_t>(params->B) * params->Hq * T * params->d * es;
     if (bytes_meet(O, out, Q, out)) return CCA_ERR_INVALID_ARG;  // row tiles of other CTAs may still read Q
     if ((st = check_device()) != CCA_OK) return st;
-    const int sms = sm_count();
+    const int sms = device_sms();
     if (sms < 1) return CCA_ERR_CUDA;
     TreeArgs a;
     a.Q = Q;
@@ -1083,9 +1088,9 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     if (params->dtype == CCA_BF16)
         return from_cuda(params->d == 128 ? run_bf16<128>(a, sms, strm) : run_bf16<64>(a, sms, strm));
     if (params->d == 128)
-        return from_cuda(run_tree(tree_f32_kernel<128>, tree_join_kernel<float, 128>, a, F32_BM,
+        return from_cuda(run_tree<tree_f32_kernel<128>>(tree_join_kernel<float, 128>, a, F32_BM,
                                   TreeF32Smem<128>::bytes(a.B, T), sms, strm));
-    return from_cuda(run_tree(tree_f32_kernel<64>, tree_join_kernel<float, 64>, a, F32_BM, TreeF32Smem<64>::bytes(a.B, T),
+    return from_cuda(run_tree<tree_f32_kernel<64>>(tree_join_kernel<float, 64>, a, F32_BM, TreeF32Smem<64>::bytes(a.B, T),
                               sms, strm));
 }
 
