@@ -28,255 +28,21 @@
 #include "internal.h"
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
+#include "tree.cuh"
 
 namespace cca {
+extern unsigned long long g_wait_limit_ns;
+extern int g_skip_q_load;
+
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
-constexpr int TILE = 64;         // keys per tile
+using namespace tree;
+
+constexpr int TILE = 64;  // keys per tile of the kernels in this file
 constexpr int TREE_THREADS = 128;
-constexpr int MIN_TILES = 2;     // tiles a group takes at least
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct TreeArgs {
-    const void *Q, *K, *V, *Kc, *Vc;
-    const int32_t *table, *ctable, *lens, *parents;
-    int n_pages, rows, cols, n_cpages, crows, ccols;
-    int B, Hq, Hkv, T, g, w, window_mode;
-    int R;       // query rows of a KV head: Hq / Hkv * T
-    int n_mt;    // row tiles
-    int groups;  // groups of n_mt CTAs
-    float scale_log2;
-    void *O;
-    float *LSE;
-    float *ws;
-    int32_t *status;
-};
-
-// Keys of one sequence (see the top of the file).
-struct KeyList {
-    int len;
-    int cores_all, raw_all;  // cores [0, cores_all) and raw [raw_all, len) are seen by every node
-    int cores_some;          // cores [cores_all, cores_some) by some
-    int raw_some;            // raw [raw_some, raw_all) by some
-    int n_all, n;            // keys seen by every node; keys in all
-    int tiles;
-};
-
-__device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) {
-    KeyList k;
-    const int len = a.lens[b];
-    if (len < 0 || len > 0x7fffffff - 2 * TREE_MAX_NODES ||
-        static_cast<int64_t>(len) + a.T > static_cast<int64_t>(a.rows) * a.cols) {
-        // a length outside the table: an empty list, and one tile in which its rows are written
-        k = KeyList{0, 0, 0, 0, 0, 0, 0, 1};
-        return k;
-    }
-    const int last = len + a.T - 1;  // T <= w, so no window of a node begins after len
-    k.len = len;
-    k.cores_all = visible_cores(len, a.w, a.g);
-    k.cores_some = visible_cores(last, a.w, a.g);
-    k.raw_some = window_start(len, a.w, a.g, a.window_mode);
-    k.raw_all = window_start(last, a.w, a.g, a.window_mode);
-    k.n_all = k.cores_all + (len - k.raw_all);
-    k.n = k.n_all + (k.cores_some - k.cores_all) + (k.raw_all - k.raw_some) + a.T;
-    k.tiles = (k.n + TILE - 1) / TILE;
-    return k;
-}
-
-// What a key is: 0 seen by every node, 1 core `val`, 2 raw token `val`, 3 node `val`, 4 not there.
-struct Key {
-    int kind, val;
-    int64_t row;  // row of its pool: (page * Hkv + kv) * rows + row in the page
-    bool core;
-};
-
-__device__ __forceinline__ Key find_key(const TreeArgs &a, const KeyList &k, int b, int kv, int x) {
-    Key r;
-    r.kind = 0;
-    r.core = false;
-    r.row = -1;
-    int at;
-    if (x < k.cores_all) {
-        r.core = true;
-        at = x;
-    } else if (x < k.n_all) {
-        at = k.raw_all + (x - k.cores_all);
-    } else if (x >= k.n) {
-        r.kind = 4;
-        r.val = 0;
-        return r;
-    } else {
-        x -= k.n_all;
-        const int nc = k.cores_some - k.cores_all, nr = k.raw_all - k.raw_some;
-        if (x < nc) {
-            r.kind = 1;
-            r.core = true;
-            at = k.cores_all + x;
-        } else if (x < nc + nr) {
-            r.kind = 2;
-            at = k.raw_some + (x - nc);
-        } else {
-            r.kind = 3;
-            at = k.len + (x - nc - nr);
-        }
-    }
-    r.val = r.kind == 3 ? at - k.len : at;
-    const int per = r.core ? a.crows : a.rows;
-    const int c = at / per;
-    int page = -1;
-    if (c < (r.core ? a.ccols : a.cols))
-        page = (r.core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
-    if (page < 0 || page >= (r.core ? a.n_cpages : a.n_pages)) {
-        r.kind = 4;
-        if (a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
-        return r;
-    }
-    r.row = (static_cast<int64_t>(page) * a.Hkv + kv) * per + (at - c * per);
-    return r;
-}
-
-// ---------------------------------------------------------------- the split
-
-// Runs of tiles: group y takes tiles [begin(y), begin(y + 1)) of all W tiles.
-struct Split {
-    int64_t W;
-    int groups;
-    __device__ int64_t begin(int y) const { return W * y / groups; }
-    __device__ int owner(int64_t tile) const { return static_cast<int>(((tile + 1) * groups - 1) / W); }
-};
-
-__device__ __forceinline__ Split make_split(const TreeArgs &a, int64_t W) {
-    Split s;
-    s.W = W;
-    const int64_t most = W / MIN_TILES;
-    s.groups = most < a.groups ? static_cast<int>(most < 1 ? 1 : most) : a.groups;
-    return s;
-}
-
-// sm_first[b] = tiles of the sequences before b (times Hkv); returns all.  B <= 1024.
-__device__ int64_t scan_tiles(const TreeArgs &a, int64_t *sm_first, int64_t *sm_warp) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
-    const int per = (a.B + nt - 1) / nt;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    int64_t own = 0;
-    for (int b = b0; b < b1; ++b) own += static_cast<int64_t>(key_list(a, b).tiles) * a.Hkv;
-    int64_t x = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(kFull, x, off);
-        if (lane >= off) x += y;
-    }
-    if (lane == 31) sm_warp[warp] = x;
-    __syncthreads();
-    int64_t before = x - own, total = 0;
-    for (int i = 0; i < nw; ++i) {
-        if (i < warp) before += sm_warp[i];
-        total += sm_warp[i];
-    }
-    for (int b = b0; b < b1; ++b) {
-        sm_first[b] = before;
-        before += static_cast<int64_t>(key_list(a, b).tiles) * a.Hkv;
-    }
-    __syncthreads();
-    return total;
-}
-
-// The list that a tile belongs to.
-struct Item {
-    int b, kv;
-    int64_t first;  // its first tile
-    KeyList k;
-};
-
-__device__ __forceinline__ Item item_of(const TreeArgs &a, const int64_t *sm_first, int64_t tile) {
-    Item it;
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sm_first[mid] <= tile) lo = mid;
-        else hi = mid - 1;
-    }
-    it.b = lo;
-    it.k = key_list(a, lo);
-    it.kv = static_cast<int>((tile - sm_first[lo]) / it.k.tiles);
-    it.first = sm_first[lo] + static_cast<int64_t>(it.kv) * it.k.tiles;
-    return it;
-}
-
-__device__ __forceinline__ void next_item(const TreeArgs &a, Item &it) {
-    it.first += it.k.tiles;
-    if (++it.kv == a.Hkv) {
-        it.kv = 0;
-        if (++it.b < a.B) it.k = key_list(a, it.b);
-    }
-}
-
-// ---------------------------------------------------------------- the nodes
-
-// Per node: its first raw token, its visible cores (-1 for an empty node), its ancestors and
-// itself as bits.  All threads call; `up` holds the parents meanwhile.
-struct Nodes {
-    int *start, *cores;
-    uint32_t *sees;  // [T][words]
-    int16_t *up;
-    int words;
-};
-
-__device__ void read_tree(const TreeArgs &a, const Nodes &n, const KeyList &k, int b) {
-    const int tid = threadIdx.x;
-    for (int t = tid; t < a.T; t += blockDim.x) {
-        int p = t - 1;
-        if (a.parents != nullptr) {
-            p = a.parents[static_cast<int64_t>(b) * a.T + t];
-            if (p != -1 && (p < 0 || p >= t)) p = -2;
-        }
-        n.up[t] = static_cast<int16_t>(p);
-    }
-    __syncthreads();
-    for (int t = tid; t < a.T; t += blockDim.x) {
-        for (int i = 0; i < n.words; ++i) n.sees[t * n.words + i] = 0;
-        int depth = -1, x = t;
-        while (x >= 0) {  // parents lie below their children, so this ends
-            n.sees[t * n.words + (x >> 5)] |= 1u << (x & 31);
-            ++depth;
-            x = n.up[x];
-        }
-        const int pos = k.len + depth;
-        const bool whole = x == -1 && k.n > 0;
-        n.cores[t] = whole ? visible_cores(pos, a.w, a.g) : -1;
-        n.start[t] = window_start(pos, a.w, a.g, a.window_mode);
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ bool row_sees(const Nodes &n, int t, int kind, int val) {
-    if (kind == 0) return true;
-    if (kind == 1) return val < n.cores[t];
-    if (kind == 2) return val >= n.start[t];
-    if (kind == 3) return (n.sees[t * n.words + (val >> 5)] >> (val & 31)) & 1u;
-    return false;
-}
-
-// Partials of a (group, row tile, slot): O [BM][D], max [BM], sum [BM] (log2 domain).
-__host__ __device__ __forceinline__ int64_t part_floats(int BM, int D) { return static_cast<int64_t>(BM) * (D + 2); }
-
-// Slot 0: the list that the group's run begins in; 1: the one it ends in.
-__device__ __forceinline__ float *part_at(const TreeArgs &a, int group, int mt, int slot, int BM, int D) {
-    return a.ws + ((static_cast<int64_t>(group) * a.n_mt + mt) * 2 + slot) * part_floats(BM, D);
-}
 
 // ---------------------------------------------------------------- bf16: matrix units
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
-    const int n = there ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -930,7 +696,6 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TreeAr
 
 // ---------------------------------------------------------------- launch
 
-constexpr int MAX_SMEM = 227 * 1024;
 
 // Resident CTAs per SM of a kernel with `smem` bytes.  The answer depends on the kernel, the
 // device and the bytes alone; the last one of each kernel and device is kept.
@@ -974,16 +739,29 @@ cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t strea
 
 constexpr int MAX_CTAS_PER_SM = 4;
 
+// R > 16 query rows per KV head go to the tensor-core kernel.
+bool on_tensor_cores(int dtype, int R, int d) { return dtype == CCA_BF16 && d == 128 && R > 16; }
+
 // Rows per CTA: 16 rows of a warp each, so that as few row tiles as possible read the keys.
-int rows_per_cta(int dtype, int R) { return dtype == CCA_F32 ? F32_BM : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+int rows_per_cta(int dtype, int R, int d) {
+    if (dtype == CCA_F32) return F32_BM;
+    if (on_tensor_cores(dtype, R, d)) return tc_rows(R);
+    return R <= 16 ? 16 : R <= 32 ? 32 : 64;
+}
 
 uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
     // CTAs times two slots; a grid holds at most MAX_CTAS_PER_SM per SM, and one group of row tiles at least
-    const int BM = rows_per_cta(dtype, R);
+    const int BM = rows_per_cta(dtype, R, d);
     const int64_t n_mt = (R + BM - 1) / BM;
     int64_t ctas = static_cast<int64_t>(sms) * MAX_CTAS_PER_SM;
     if (ctas < n_mt) ctas = n_mt;
     return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
+}
+
+template <typename J>
+cudaError_t run_join(J join, const TreeArgs &a, int BM, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_WARPS - 1) / JOIN_WARPS);
+    return start(join, grid, JOIN_WARPS * 32, 8 * (a.B + JOIN_WARPS), stream, a, BM);
 }
 
 template <auto kernel, typename J>
@@ -998,15 +776,27 @@ cudaError_t run_tree(J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t
     if (a.groups < 1) a.groups = 1;
     e = start(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a, BM);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_WARPS - 1) / JOIN_WARPS);
-    return start(join, grid, JOIN_WARPS * 32, 8 * (a.B + JOIN_WARPS), stream, a, BM);
+    return run_join(join, a, BM, stream);
+}
+
+cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
+    const int BM = tc_rows(a.R);
+    a.n_mt = (a.R + BM - 1) / BM;
+    a.groups = sms / a.n_mt;
+    if (a.groups < 1) a.groups = 1;
+    a.tile_log2 = 7;
+    a.min_tiles = 1;
+    const cudaError_t e = launch_tc(a, sms, g_wait_limit_ns, g_skip_q_load, stream);
+    if (e != cudaSuccess) return e;
+    return run_join(tree_join_kernel<__nv_bfloat16, 128>, a, BM, stream);
 }
 
 template <int D>
 cudaError_t run_bf16(const TreeArgs &a, int sms, cudaStream_t stream) {
+    if (on_tensor_cores(CCA_BF16, a.R, D)) return run_tc(a, sms, stream);
     const int smem = TreeSmem<D>::bytes(a.B, a.T);
     auto *join = tree_join_kernel<__nv_bfloat16, D>;
-    switch (rows_per_cta(CCA_BF16, a.R)) {
+    switch (rows_per_cta(CCA_BF16, a.R, D)) {
         case 16: return run_tree<tree_bf16_kernel<D, 1>>(join, a, 16, smem, sms, stream);
         case 32: return run_tree<tree_bf16_kernel<D, 2>>(join, a, 32, smem, sms, stream);
         default: return run_tree<tree_bf16_kernel<D, 4>>(join, a, 64, smem, sms, stream);
@@ -1079,6 +869,8 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.R = params->Hq / params->Hkv * T;
     a.n_mt = 1;
     a.groups = 1;
+    a.tile_log2 = 6;
+    a.min_tiles = 2;
     a.scale_log2 = resolve_scale(params) * 1.4426950408889634f;
     a.O = O;
     a.LSE = LSE;

@@ -68,6 +68,10 @@ CASES = [  # B, T, Hq, Hkv, d, lens, g, w, rows, crows, mode
     (1, 3, 2, 1, 128, [40], 1, 10, 16, 16, 0),                    # every token its own core
     (1, 2, 2, 2, 64, [50], 64, 60, 1, 1, 0),                      # pages of one row; no core yet
     (5, 4, 4, 2, 128, [0, 3, 31, 32, 33], 16, 16, 16, 16, 1),
+    (3, 12, 4, 2, 128, [5000, 20, 2600], 16, 300, 64, 64, 0),     # tensor cores: lists of many tiles, several per CTA
+    (40, 10, 8, 4, 128, [17 * i + 3 for i in range(40)], 8, 33, 16, 10, 1),   # more lists than CTAs
+    (2, 64, 4, 1, 128, [9000, 4100], 2, 128, 64, 64, 0),          # two halves over runs of many tiles
+    (2, 96, 4, 1, 128, [333, 4100], 8, 128, 48, 16, 0),           # 384 rows: two row tiles of two halves, the last half empty
 ]
 
 
@@ -98,10 +102,12 @@ def test_padding_and_broken_chains():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("bad", [NAN, float("inf"), -float("inf")])
-def test_masked_rows_may_hold_anything(bad, dtype):
+@pytest.mark.parametrize("heads", [2, 4, 24, 40])    # rows for each of the kernels
+def test_masked_rows_may_hold_anything(bad, dtype, heads):
     """Infinities and NaN in keys and values that a node does not see leave it as it is, and reach the
     nodes that do see them."""
-    B, T, Hq, Hkv, d, g, w, rows = 1, 6, 4, 1, 128, 8, 40, 16
+    T = 6
+    B, Hq, Hkv, d, g, w, rows = 1, heads, 1, 128, 8, 40, 16
     x = make(B, T, Hq, Hkv, d, [200], g, w, rows, rows, dtype, seed=3)
     x["parents"] = torch.tensor([[-1, 0, 0, 1, 2, 2]], dtype=torch.int32)
     clean = call(x, g, w)
@@ -276,3 +282,25 @@ def test_refusals():
         run(parents=torch.zeros(1, 3, dtype=torch.int32, device="cuda"))
     with pytest.raises(api.CcaError):
         run(O=args[0])
+
+
+@pytest.mark.parametrize("T", [8, 40], ids=["one half", "two halves"])
+def test_wait_time_out_is_reported(T):
+    """Tensor-core kernel with no copies at all: its waits run out, it reports and returns, and the
+    next call is as before."""
+    x = make(2, T, 8, 2, 128, [300, 900], 16, 64, 32, 32, torch.bfloat16)
+    want = call(x, 16, 64)
+    torch.cuda.synchronize()
+    lib = api.load_library()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib.cca_test_set_wait_limit_ns(2_000_000)
+    lib.cca_test_skip_q_load(1)
+    try:
+        call(x, 16, 64, dev_status=status)
+        torch.cuda.synchronize()
+    finally:
+        lib.cca_test_skip_q_load(0)
+        lib.cca_test_set_wait_limit_ns(1_000_000_000)
+    assert status.item() == api.CCA_ERR_TIMEOUT
+    got = call(x, 16, 64)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
