@@ -80,7 +80,14 @@ __device__ __forceinline__ void tma_load_3d(const void *tmap, uint32_t bar, uint
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-
+// 2-D form of tma_load_3d.
+__device__ __forceinline__ void tma_load_2d(const void *tmap, uint32_t bar, uint32_t dst, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
 
 // Untiled bulk copy global -> shared (both addresses 16-byte aligned, size a
 // multiple of 16); completion is signalled on `bar` as transaction bytes.

@@ -21,6 +21,7 @@ struct TreeArgs {
     int R;       // query rows of a KV head: Hq / Hkv * T
     int n_mt;    // row tiles
     int tile_log2;  // keys per tile
+    int box_log2;   // rows of a box that one copy can bring (0: no runs)
     int groups;  // groups of n_mt CTAs
     int min_tiles;  // tiles a group takes at least
     float scale_log2;
@@ -30,55 +31,88 @@ struct TreeArgs {
     int32_t *status;
 };
 
-// Keys of one sequence (see the top of the file).
+// Keys of one sequence, in the order in which they are dealt to tiles:
+//   runs   with a.box > 0: whole boxes of a.box consecutive rows of one page that every node
+//          sees, cores first, then raw tokens; as many as fill whole tiles
+//   rest   the other keys that every node sees, then those that only some see: cores, raw
+//          tokens, the nodes themselves
 struct KeyList {
     int len;
-    int cores_all, raw_all;  // cores [0, cores_all) and raw [raw_all, len) are seen by every node
-    int cores_some;          // cores [cores_all, cores_some) by some
-    int raw_some;            // raw [raw_some, raw_all) by some
-    int n_all, n;            // keys seen by every node; keys in all
+    int cores_all, raw_all;   // cores [0, cores_all) and raw [raw_all, len) are seen by every node
+    int cores_some;           // cores [cores_all, cores_some) by some
+    int raw_some;             // raw [raw_some, raw_all) by some
+    int run_tiles, run_cores; // tiles made of runs; cores in them
+    int gap0, gap1;           // raw tokens [gap0, gap1) lie in runs
+    int n_all, n;             // of the rest: keys seen by every node; keys in all (0: no list)
     int tiles;
 };
 
 __device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) {
-    KeyList k;
+    KeyList k = {};
+    k.tiles = 1;
     const int len = a.lens[b];
+    // a length outside the table: an empty list, and one tile in which its rows are written
     if (len < 0 || len > 0x7fffffff - 2 * TREE_MAX_NODES ||
-        static_cast<int64_t>(len) + a.T > static_cast<int64_t>(a.rows) * a.cols) {
-        // a length outside the table: an empty list, and one tile in which its rows are written
-        k = KeyList{0, 0, 0, 0, 0, 0, 0, 1};
+        static_cast<int64_t>(len) + a.T > static_cast<int64_t>(a.rows) * a.cols)
         return k;
-    }
     const int last = len + a.T - 1;  // T <= w, so no window of a node begins after len
     k.len = len;
     k.cores_all = visible_cores(len, a.w, a.g);
     k.cores_some = visible_cores(last, a.w, a.g);
     k.raw_some = window_start(len, a.w, a.g, a.window_mode);
     k.raw_all = window_start(last, a.w, a.g, a.window_mode);
-    k.n_all = k.cores_all + (len - k.raw_all);
+    k.gap0 = k.gap1 = len;
+    if (a.box_log2 > 0) {
+        const int lg = a.box_log2;
+        const int cb = k.cores_all >> lg, r0 = (k.raw_all + (1 << lg) - 1) >> lg, r1 = len >> lg;
+        const int boxes = cb + (r1 > r0 ? r1 - r0 : 0);
+        k.run_tiles = boxes >> (a.tile_log2 - lg);
+        const int used = k.run_tiles << (a.tile_log2 - lg);
+        k.run_cores = (used < cb ? used : cb) << lg;
+        if (used > cb) {
+            k.gap0 = r0 << lg;
+            k.gap1 = (r0 + used - cb) << lg;
+        }
+    }
+    k.n_all = (k.cores_all - k.run_cores) + (k.gap0 - k.raw_all) + (len - k.gap1);
     k.n = k.n_all + (k.cores_some - k.cores_all) + (k.raw_all - k.raw_some) + a.T;
-    k.tiles = (k.n + (1 << a.tile_log2) - 1) >> a.tile_log2;
+    k.tiles = k.run_tiles + ((k.n + (1 << a.tile_log2) - 1) >> a.tile_log2);
     return k;
+}
+
+// The row of its pool that row `at` of a sequence lies in, -1 where no page is.
+__device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bool core, int at) {
+    const int per = core ? a.crows : a.rows;
+    const int c = at / per;
+    int page = -1;
+    if (c < (core ? a.ccols : a.cols))
+        page = (core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
+    if (page < 0 || page >= (core ? a.n_cpages : a.n_pages)) {
+        if (a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        return -1;
+    }
+    return (static_cast<int64_t>(page) * a.Hkv + kv) * per + (at - c * per);
 }
 
 // What a key is: 0 seen by every node, 1 core `val`, 2 raw token `val`, 3 node `val`, 4 not there.
 struct Key {
     int kind, val;
-    int64_t row;  // row of its pool: (page * Hkv + kv) * rows + row in the page
+    int64_t row;  // row of its pool
     bool core;
 };
 
+// Key x of the rest.
 __device__ __forceinline__ Key find_key(const TreeArgs &a, const KeyList &k, int b, int kv, int x) {
     Key r;
     r.kind = 0;
     r.core = false;
     r.row = -1;
     int at;
-    if (x < k.cores_all) {
-        r.core = true;
-        at = x;
-    } else if (x < k.n_all) {
-        at = k.raw_all + (x - k.cores_all);
+    if (x < k.n_all) {
+        const int nc = k.cores_all - k.run_cores;
+        r.core = x < nc;
+        at = r.core ? k.run_cores + x : k.raw_all + (x - nc);
+        if (!r.core && at >= k.gap0) at += k.gap1 - k.gap0;
     } else if (x >= k.n) {
         r.kind = 4;
         r.val = 0;
@@ -99,18 +133,16 @@ __device__ __forceinline__ Key find_key(const TreeArgs &a, const KeyList &k, int
         }
     }
     r.val = r.kind == 3 ? at - k.len : at;
-    const int per = r.core ? a.crows : a.rows;
-    const int c = at / per;
-    int page = -1;
-    if (c < (r.core ? a.ccols : a.cols))
-        page = (r.core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
-    if (page < 0 || page >= (r.core ? a.n_cpages : a.n_pages)) {
-        r.kind = 4;
-        if (a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
-        return r;
-    }
-    r.row = (static_cast<int64_t>(page) * a.Hkv + kv) * per + (at - c * per);
+    r.row = pool_row(a, b, kv, r.core, at);
+    if (r.row < 0) r.kind = 4;
     return r;
+}
+
+// Pool row at which box i of the runs begins, -1 where no page is.
+__device__ __forceinline__ int64_t find_box(const TreeArgs &a, const KeyList &k, int b, int kv, int i, bool &core) {
+    const int at = i << a.box_log2;
+    core = at < k.run_cores;
+    return pool_row(a, b, kv, core, core ? at : k.gap0 + (at - k.run_cores));
 }
 
 // ---------------------------------------------------------------- the split
@@ -261,7 +293,7 @@ constexpr int MAX_SMEM = 227 * 1024;
 
 // Tensor-core kernel (tree_tc.cu): bf16, d = 128.  Rows of a CTA for R rows per KV head.
 int tc_rows(int R);
-cudaError_t launch_tc(TreeArgs a, int sms, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream);
+cudaError_t launch_tc(TreeArgs a, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream);
 
 }  // namespace tree
 }  // namespace cca

@@ -10,10 +10,11 @@
 // Roles (warpgroups of four warps):
 //   0 .. HALVES-1   softmax and output of a half; thread t owns row t of it (TMEM lane t).
 //                   They also bring their half's queries, while the last tile's product runs.
-//   HALVES          producers: a lane looks up one key's page (a step ahead), the warp copies
-//                   its 32 keys' rows with cp.async, 16 lanes to a row, into 128-byte-swizzled
-//                   tiles.  Any page size and alignment goes; 16-byte copies keep the LSU at
-//                   a quarter of its rate.
+//   HALVES          producers, 32 keys of a tile per warp, page look-ups a tile ahead.  Tiles of
+//                   runs (whole boxes of consecutive rows of a page) come by TMA, a box per
+//                   lane; the rest, one to four tiles of a list, by cp.async, a key per lane to
+//                   look up and 16 lanes to a row to copy, so any page size and alignment goes.
+//                   Both fill 128-byte-swizzled tiles.
 //   HALVES+1        its first warp issues the MMAs.
 // K(t) and V(t) take two consecutive slots of a ring of NS 32 KB slots.
 //
@@ -35,6 +36,7 @@
 #include "internal.h"
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
+#include "tma_host.h"
 #include "tree.cuh"
 
 namespace cca {
@@ -91,7 +93,9 @@ struct Layout {
 
 template <int HALVES>
 __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
-    tree_tc_kernel(const TreeArgs a, const unsigned long long lim, const int skip_loads) {
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const __grid_constant__ CUtensorMap tmKc, const __grid_constant__ CUtensorMap tmVc, const TreeArgs a,
+                   const unsigned long long lim, const int skip_loads) {
     using L = Layout<HALVES>;
     constexpr int NS = L::NS;
     constexpr int BM = HALVES * 128;
@@ -152,8 +156,25 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         Item it = {};
         const char *kp = nullptr, *vp = nullptr;
         int kind = 4, val = 0;
+        int box_y = 0;         // of a tile of runs: this lane's box, as a row of its pool
+        bool runs = false, box_core = false;
+        const int per_warp = a.box_log2 > 0 ? 32 >> a.box_log2 : 0;  // boxes of a warp
         auto look_up = [&](int64_t x) {
-            const Key key = find_key(a, it.k, it.b, it.kv, static_cast<int>(x - it.first) * BN + pw * 32 + lane);
+            const int tile = static_cast<int>(x - it.first);
+            runs = tile < it.k.run_tiles;
+            if (runs) {
+                kind = 0;
+                if (lane < per_warp) {
+                    const int64_t row = find_box(a, it.k, it.b, it.kv, (tile * 4 + pw) * per_warp + lane, box_core);
+                    // no page: past the pool's end, where the copy fills in zeros
+                    box_y = static_cast<int>(row >= 0 ? row : static_cast<int64_t>(box_core ? a.n_cpages : a.n_pages) * a.Hkv * (box_core ? a.crows : a.rows));
+                    kind = row >= 0 ? 0 : 4;
+                }
+                // each lane: the kind of its key, which its box's lane knows
+                kind = __shfl_sync(kFull, kind, lane >> a.box_log2);
+                return;
+            }
+            const Key key = find_key(a, it.k, it.b, it.kv, (tile - it.k.run_tiles) * BN + pw * 32 + lane);
             const int64_t off = key.row * (HD * 2);
             kp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Kc : a.K) + off;
             vp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Vc : a.V) + off;
@@ -164,6 +185,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         int prev_slot = -1;
         uint32_t prev_mixed = 0;  // lanes' keys that only some rows see
         int prev_meta = 0;
+        int64_t last_run = -1;    // last tile of runs that was issued
         auto land = [&]() {       // that tile's copies (of this thread) have arrived
             if (prev_slot < 0) return;
             const int vslot = (prev_slot + 1) % NS;
@@ -226,6 +248,46 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             // A slot of METAS tiles ago: its softmax is over, as the scores of a later tile, which
             // freed this K slot, were issued after it.
             TileMeta &m = metas[(x - x0) & (METAS - 1)];
+            if (runs) {
+                const uint32_t gone = __ballot_sync(kFull, kind != 0);
+                if (gone != 0) {
+                    reinterpret_cast<uint8_t *>(m.kind)[pw * 32 + lane] = static_cast<uint8_t>(kind);
+                    m.val[pw * 32 + lane] = 0;
+                } else if (lane < 8) {
+                    m.kind[pw * 8 + lane] = 0;  // a neighbour's missing page may make the tile masked
+                }
+                if (lane == 0) {
+                    m.masked[pw] = gone;
+                    m.odd[pw] = 0;
+                }
+                if (prev_slot >= 0) {
+                    cp_wait<0>();
+                    land();
+                    prev_slot = -1;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(L::B_FULL + ks), 32 * HD * 2);
+                    ptx::mbar_arrive_expect_tx(bar(L::B_FULL + vs), 32 * HD * 2);
+                }
+                __syncwarp();
+                if (lane < per_warp) {
+                    const uint32_t at = base + L::OFF_RING + (pw * 32 + (lane << a.box_log2)) * 128;
+                    const void *mk = box_core ? static_cast<const void *>(&tmKc) : static_cast<const void *>(&tmK);
+                    const void *mv = box_core ? static_cast<const void *>(&tmVc) : static_cast<const void *>(&tmV);
+                    ptx::tma_load_2d(mk, bar(L::B_FULL + ks), at + ks * TILE_BYTES, 0, box_y);
+                    ptx::tma_load_2d(mk, bar(L::B_FULL + ks), at + ks * TILE_BYTES + HALF_BYTES, 64, box_y);
+                    ptx::tma_load_2d(mv, bar(L::B_FULL + vs), at + vs * TILE_BYTES, 0, box_y);
+                    ptx::tma_load_2d(mv, bar(L::B_FULL + vs), at + vs * TILE_BYTES + HALF_BYTES, 64, box_y);
+                }
+                last_run = x - x0;
+                __syncwarp();
+                if (x + 1 < x1) {
+                    if (x + 1 >= it.first + it.k.tiles) next_item(a, it);
+                    look_up(x + 1);
+                }
+                continue;
+            }
             const int at = pw * 32 + lane;
             m.v[at] = reinterpret_cast<const __nv_bfloat16 *>(vp);
             m.val[at] = val;
@@ -264,6 +326,16 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         }
         cp_wait<0>();
         if (ok) land();
+        if (*abort_flag && lane == 0) {
+            // bulk copies already issued land before the CTA's memory is given back
+            volatile int never = 0;
+            for (int64_t t = last_run > NS ? last_run - NS : 0; t <= last_run; ++t) {
+                const uint32_t u = static_cast<uint32_t>(t) * 2;
+                ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, &never, lim);
+                ptx::wait_bounded(bar(L::B_FULL + (u + 1) % NS), ((u + 1) / NS) & 1, &never, lim);
+            }
+        }
+        __syncwarp();
     } else if (wg == HALVES + 1) {
         // ------------------------------------------------------------ MMA issuer
         if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -676,7 +748,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
 }
 
 template <int HALVES>
-cudaError_t launch_halves(const TreeArgs &a, unsigned long long lim, int skip_loads, cudaStream_t stream) {
+cudaError_t launch_halves(const CUtensorMap (&map)[4], const TreeArgs &a, unsigned long long lim, int skip_loads, cudaStream_t stream) {
     static std::atomic<int> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -696,16 +768,31 @@ cudaError_t launch_halves(const TreeArgs &a, unsigned long long lim, int skip_lo
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<HALVES>, a, lim, skip_loads);
+    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<HALVES>, map[0], map[1], map[2], map[3], a, lim, skip_loads);
 }
 
 }  // namespace
 
 int tc_rows(int R) { return R <= 128 ? 128 : 256; }
 
-cudaError_t launch_tc(TreeArgs a, int, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream) {
-    return tc_rows(a.R) == 128 ? launch_halves<1>(a, wait_limit_ns, skip_loads, stream)
-                               : launch_halves<2>(a, wait_limit_ns, skip_loads, stream);
+cudaError_t launch_tc(TreeArgs a, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream) {
+    // Runs: boxes of 32, 16 or 8 rows, the most that both page sizes are made of; rows of a pool
+    // are 32-bit coordinates of its tensor map.  Otherwise every tile comes by cp.async.
+    CUtensorMap map[4];
+    const int64_t rows = static_cast<int64_t>(a.n_pages) * a.Hkv * a.rows, crows = static_cast<int64_t>(a.n_cpages) * a.Hkv * a.crows;
+    a.box_log2 = 0;
+    for (int lg = 5; lg >= 3 && a.box_log2 == 0; --lg)
+        if (((a.rows | a.crows) & ((1 << lg) - 1)) == 0) a.box_log2 = lg;
+    if (rows > 0x7fffffff - 32 || crows > 0x7fffffff - 32) a.box_log2 = 0;
+    EncodeTiledFn enc = get_encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const uint32_t box = a.box_log2 > 0 ? 1u << a.box_log2 : 8u;
+    const uint64_t n = a.box_log2 > 0 ? rows : 8, nc = a.box_log2 > 0 ? crows : 8;
+    if (!encode_rows_bf16_d128(enc, &map[0], a.K, n, box) || !encode_rows_bf16_d128(enc, &map[1], a.V, n, box) ||
+        !encode_rows_bf16_d128(enc, &map[2], a.Kc, nc, box) || !encode_rows_bf16_d128(enc, &map[3], a.Vc, nc, box))
+        return cudaErrorInvalidValue;
+    return tc_rows(a.R) == 128 ? launch_halves<1>(map, a, wait_limit_ns, skip_loads, stream)
+                               : launch_halves<2>(map, a, wait_limit_ns, skip_loads, stream);
 }
 
 }  // namespace tree

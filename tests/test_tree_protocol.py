@@ -21,11 +21,14 @@ class Bar:
 
 
 class Model:
-    """One CTA.  segs: tiles of each list in its run.  Roles are generators that yield a condition to
+    """One CTA.  segs: tiles of each list in its run, the first runs[i] of them copied by TMA (they
+    land by themselves), the others by the producers' own copies.  Roles are generators that yield a condition to
     wait for, or None for a step."""
 
-    def __init__(self, halves, segs, used=None):
+    def __init__(self, halves, segs, used=None, runs=0):
         self.H, self.segs = halves, segs
+        self.run_tiles = {x + i for _, x, end in self.tiles() for i in range(min(runs, end - x))}
+        self.flying, self.loaders = [], 4    # TMA copies in flight, producers at work
         self.NS = 4 if halves == 2 else 5
         self.used = [True] * halves if used is None else used
         n = self.NS
@@ -66,17 +69,31 @@ class Model:
                 land(pending)
                 pending = None
             yield ready
+            if x in self.run_tiles and pending is not None:
+                yield None
+                land(pending)
+                pending = None
             if w == 0:
                 for sl in (ks, vs):
                     self.slot[sl] = "loading"
                 self.meta[x & 3] = x
             yield None
+            if x in self.run_tiles:
+                self.flying.append(lambda p=(ks, vs, x): land(p))
+                continue
             if pending is not None:
                 land(pending)
             pending = (ks, vs, x)
         if pending is not None:
             yield None
             land(pending)
+        self.loaders -= 1
+
+    def tma(self, rng):
+        while self.loaders or self.flying:
+            yield lambda: bool(self.flying) or not self.loaders
+            if self.flying:
+                self.flying.pop(rng.randrange(len(self.flying)))()
 
     def issue(self, *op):
         self.pipe.append(op)
@@ -204,7 +221,7 @@ class Model:
             self.ofree[h].arrive()
 
     def run(self, rng):
-        roles = [self.producer(w) for w in range(4)] + [self.mma(), self.pipe_role()]
+        roles = [self.producer(w) for w in range(4)] + [self.mma(), self.pipe_role(), self.tma(rng)]
         roles += [self.softmax(h) for h in range(self.H) if self.used[h]]
         state = {i: (r, next(r, "end")) for i, r in enumerate(roles)}
         while True:
@@ -218,9 +235,10 @@ class Model:
         assert sorted(self.out) == sorted((h, s) for h in range(self.H) if self.used[h] for s in range(len(self.segs)))
 
 
+@pytest.mark.parametrize("runs", [0, 1, 4, 100])
 @pytest.mark.parametrize("halves,used", [(1, None), (2, None), (2, [True, False])])
 @pytest.mark.parametrize("segs", [[1], [2], [3, 1], [9], [1, 1, 1, 1], [2, 7, 1, 5], [30, 3], [1, 2, 3, 4, 5, 6]])
-def test_every_schedule_ends(halves, used, segs):
+def test_every_schedule_ends(halves, used, segs, runs):
     for seed in range(30):
         random.seed(seed)
-        Model(halves, segs, used).run(random.Random(seed))
+        Model(halves, segs, used, runs).run(random.Random(seed))
