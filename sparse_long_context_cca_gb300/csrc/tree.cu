@@ -79,11 +79,10 @@ struct TreeSmem {
     static constexpr int TILE_BYTES = TILE * ROW;      // K or V
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
     static constexpr int META_OFF = STAGES * STAGE_BYTES;
-    static constexpr int FIRST_OFF = META_OFF + METAS * static_cast<int>(sizeof(Meta));
-    // then: tiles before each sequence [B], 4 warp sums, node starts [T], cores [T], bits [T][words], parents [T]
-    static __host__ __device__ int bytes(int B, int T) {
-        return FIRST_OFF + 8 * (B + 4) + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16;
-    }
+    static constexpr int START_OFF = META_OFF + METAS * static_cast<int>(sizeof(Meta));
+    static constexpr int NODE_OFF = START_OFF + static_cast<int>(sizeof(Start));
+    // then: node starts [T], cores [T], bits [T][words], parents [T]
+    static __host__ __device__ int bytes(int T) { return NODE_OFF + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16; }
 };
 
 // Byte offset of 16-byte chunk c of row `row` in a tile: chunks are permuted inside each
@@ -107,11 +106,10 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     constexpr int CPR = D / 8;     // 16-byte chunks per row
     extern __shared__ __align__(128) unsigned char smem[];
     Meta *meta = reinterpret_cast<Meta *>(smem + S::META_OFF);
-    int64_t *sm_first = reinterpret_cast<int64_t *>(smem + S::FIRST_OFF);
-    int64_t *sm_warp = sm_first + a.B;
+    Start &st = *reinterpret_cast<Start *>(smem + S::START_OFF);
     Nodes nodes;
     nodes.words = (a.T + 31) >> 5;
-    nodes.start = reinterpret_cast<int *>(sm_warp + 4);
+    nodes.start = reinterpret_cast<int *>(smem + S::NODE_OFF);
     nodes.cores = nodes.start + a.T;
     nodes.sees = reinterpret_cast<uint32_t *>(nodes.cores + a.T);
     nodes.up = reinterpret_cast<int16_t *>(nodes.sees + a.T * nodes.words);
@@ -123,19 +121,18 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wm = warp % WM, wk = warp / WM;
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    const Split split = make_split(a, scan_tiles(a, sm_first, sm_warp));
-    if (group >= split.groups) return;
-    const int64_t x0 = split.begin(group), x1 = split.begin(group + 1);
+    find_run(a, group, st, blockIdx.x == 0);
+    const int x0 = st.x0, x1 = st.x1;
     if (x0 >= x1) return;
 
     // ---- loading
-    Item ld = item_of(a, sm_first, x0);  // list of the tile whose addresses come next
-    auto look_up = [&](int64_t x, Key &key) {  // threads 0 .. 63, one key each
+    Item ld = st.item;  // list of the tile whose addresses come next
+    auto look_up = [&](int x, Key &key) {  // threads 0 .. 63, one key each
         if (x >= x1) return;
         if (x >= ld.first + ld.k.tiles) next_item(a, ld);
-        if (tid < TILE) key = find_key(a, ld.k, ld.b, ld.kv, static_cast<int>(x - ld.first) * TILE + tid);
+        if (tid < TILE) key = find_key(a, ld.k, ld.b, ld.kv, (x - ld.first) * TILE + tid);
     };
-    auto put = [&](int64_t x, const Key &key) {
+    auto put = [&](int x, const Key &key) {
         if (x >= x1 || tid >= TILE) return;
         Meta &m = meta[(x - x0) & (METAS - 1)];
         const int64_t off = key.row * S::ROW;
@@ -149,10 +146,10 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
             m.odd[warp] = 0;
         }
     };
-    auto issue = [&](int64_t x) {
+    auto issue = [&](int x) {
         if (x < x1) {
             const Meta &m = meta[(x - x0) & (METAS - 1)];
-            const uint32_t base = stage0 + static_cast<uint32_t>((x - x0) % STAGES) * S::STAGE_BYTES;
+            const uint32_t base = stage0 + static_cast<uint32_t>(x - x0) % STAGES * S::STAGE_BYTES;
             constexpr int PER = TILE * CPR / TREE_THREADS;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -180,7 +177,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     for (int i = 0; i < STAGES - 1; ++i) issue(x0 + i);
 
     // ---- the rows
-    Item it = item_of(a, sm_first, x0);
+    Item it = st.item;
     if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
     uint32_t qf[D / 16][4];
     float o[DT][4], m[2], l[2];
@@ -208,14 +205,14 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     };
     begin_item();
 
-    for (int64_t x = x0; x < x1; ++x) {
+    for (int x = x0; x < x1; ++x) {
         cp_wait<STAGES - 2>();
         __syncthreads();
         issue(x + STAGES - 1);
         look_up(x + STAGES, key);
 
         const Meta &mt_ = meta[(x - x0) & (METAS - 1)];
-        const uint32_t kbase = stage0 + static_cast<uint32_t>((x - x0) % STAGES) * S::STAGE_BYTES;
+        const uint32_t kbase = stage0 + static_cast<uint32_t>(x - x0) % STAGES * S::STAGE_BYTES;
         const uint32_t vbase = kbase + S::TILE_BYTES;
         const bool masked = (mt_.masked[0] | mt_.masked[1]) != 0;
         // S = Q K^T over this warp's keys
@@ -350,7 +347,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
         }
         put(x + STAGES, key);
 
-        const int64_t end = it.first + it.k.tiles;
+        const int end = it.first + it.k.tiles;
         if (x + 1 != end && x + 1 != x1) continue;
         // ---- the end of this list, or of this group's part of it
 #pragma unroll
@@ -466,10 +463,9 @@ struct TreeF32Smem {
     static constexpr int P_OFF = Q_OFF + F32_BM * D;
     static constexpr int ML_OFF = P_OFF + F32_BM * TILE;  // max, sum, correction per row
     static constexpr int KEY_OFF = ML_OFF + 3 * F32_BM;   // kind, value per key
-    static constexpr int FIRST_OFF = ((KEY_OFF + 2 * TILE) * 4 + 15) / 16 * 16;
-    static __host__ __device__ int bytes(int B, int T) {
-        return FIRST_OFF + 8 * (B + 4) + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16;
-    }
+    static constexpr int START_OFF = ((KEY_OFF + 2 * TILE) * 4 + 15) / 16 * 16;
+    static constexpr int NODE_OFF = START_OFF + static_cast<int>(sizeof(Start));
+    static __host__ __device__ int bytes(int T) { return NODE_OFF + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16; }
 };
 
 // The same walk with one tile in shared memory at a time; scores and sums in fp32.
@@ -484,11 +480,10 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
     float *sk = reinterpret_cast<float *>(smem), *sv = sk + S::V_OFF, *sq = sk + S::Q_OFF, *sp = sk + S::P_OFF;
     float *sm_m = sk + S::ML_OFF, *sm_l = sm_m + BM, *sm_c = sm_l + BM;
     int *sm_kind = reinterpret_cast<int *>(sk + S::KEY_OFF), *sm_val = sm_kind + TILE;
-    int64_t *sm_first = reinterpret_cast<int64_t *>(smem + S::FIRST_OFF);
-    int64_t *sm_warp = sm_first + a.B;
+    Start &st = *reinterpret_cast<Start *>(smem + S::START_OFF);
     Nodes nodes;
     nodes.words = (a.T + 31) >> 5;
-    nodes.start = reinterpret_cast<int *>(sm_warp + 4);
+    nodes.start = reinterpret_cast<int *>(smem + S::NODE_OFF);
     nodes.cores = nodes.start + a.T;
     nodes.sees = reinterpret_cast<uint32_t *>(nodes.cores + a.T);
     nodes.up = reinterpret_cast<int16_t *>(nodes.sees + a.T * nodes.words);
@@ -498,16 +493,15 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    const Split split = make_split(a, scan_tiles(a, sm_first, sm_warp));
-    if (group >= split.groups) return;
-    const int64_t x0 = split.begin(group), x1 = split.begin(group + 1);
+    find_run(a, group, st, blockIdx.x == 0);
+    const int x0 = st.x0, x1 = st.x1;
     if (x0 >= x1) return;
-    Item it = item_of(a, sm_first, x0);
+    Item it = st.item;
     const int col = tid % D, rg = tid / D;
     float o[RPT];
     int64_t out0 = 0;
     bool fresh = true;
-    for (int64_t x = x0; x < x1; ++x) {
+    for (int x = x0; x < x1; ++x) {
         if (fresh) {
             if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
             read_tree(a, nodes, it.k, it.b);
@@ -527,7 +521,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
         // two threads per key bring its K and V row
         {
             const int row = tid >> 1, half = tid & 1;
-            const Key key = find_key(a, it.k, it.b, it.kv, static_cast<int>(x - it.first) * TILE + row);
+            const Key key = find_key(a, it.k, it.b, it.kv, (x - it.first) * TILE + row);
             if (half == 0) {
                 sm_kind[row] = key.kind;
                 sm_val[row] = key.val;
@@ -599,7 +593,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
                 if (!(p < 0.f)) o[i] = fmaf(p, v, o[i]);
             }
         }
-        const int64_t end = it.first + it.k.tiles;
+        const int end = it.first + it.k.tiles;
         if (x + 1 == end || x + 1 == x1) {
             const bool whole = x0 <= it.first && end <= x1;
             float *part = part_at(a, group, mt, x0 >= it.first ? 0 : 1, BM, D);
@@ -637,29 +631,22 @@ constexpr int JOIN_WARPS = 4;
 // that one group finished are already written.
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TreeArgs a, int BM) {
-    extern __shared__ __align__(128) unsigned char smem[];
-    int64_t *sm_first = reinterpret_cast<int64_t *>(smem), *sm_warp = sm_first + a.B;
     constexpr int C = D / 32;  // columns of a lane
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Split split = make_split(a, scan_tiles(a, sm_first, sm_warp));
-    const int64_t bk = blockIdx.x;
+    const int b = blockIdx.x / a.Hkv, kv = blockIdx.x - b * a.Hkv;
     const int row = blockIdx.y * JOIN_WARPS + warp;
-    const int b = static_cast<int>(bk / a.Hkv), kv = static_cast<int>(bk - static_cast<int64_t>(b) * a.Hkv);
-    const int tiles = key_list(a, b).tiles;
-    const int64_t s = sm_first[b] + static_cast<int64_t>(kv) * tiles, e = s + tiles;
+    const int f0 = a.firsts[b], f1 = a.firsts[b + 1], all = a.firsts[a.B];
+    const Split split = make_split(a, all);
+    const int tiles = (f1 - f0) / a.Hkv;
+    const int s = f0 + kv * tiles, e = s + tiles;
     const int y0 = split.owner(s), y1 = split.owner(e - 1);
     if (y0 == y1 || row >= a.R) return;
     const int mt = row / BM, in = row - mt * BM;
-    auto part = [&](int y) -> const float * {
-        const int64_t x0 = split.begin(y);
-        if (split.begin(y + 1) <= x0) return nullptr;  // an empty run
-        return part_at(a, y, mt, x0 >= s ? 0 : 1, BM, D);
-    };
+    auto part = [&](int y) { return static_cast<const float *>(part_at(a, y, mt, split.begin(y) >= s ? 0 : 1, BM, D)); };
     float mx = -INFINITY;
     for (int y = y0 + lane; y <= y1; y += 32) {
-        const float *p = part(y);
-        if (p != nullptr) mx = fmaxf(mx, p[BM * D + in]);
+        mx = fmaxf(mx, part(y)[BM * D + in]);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
@@ -749,19 +736,22 @@ int rows_per_cta(int dtype, int R, int d) {
     return R <= 16 ? 16 : R <= 32 ? 32 : 64;
 }
 
+constexpr uint64_t WS_HEAD = 8192;  // the lists' first tiles
+static_assert(WS_HEAD >= 4 * (TREE_MAX_BATCH + 1), "room for the first tiles");
+
 uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
     // CTAs times two slots; a grid holds at most MAX_CTAS_PER_SM per SM, and one group of row tiles at least
     const int BM = rows_per_cta(dtype, R, d);
     const int64_t n_mt = (R + BM - 1) / BM;
     int64_t ctas = static_cast<int64_t>(sms) * MAX_CTAS_PER_SM;
     if (ctas < n_mt) ctas = n_mt;
-    return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
+    return WS_HEAD + 32 + static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
 }
 
 template <typename J>
 cudaError_t run_join(J join, const TreeArgs &a, int BM, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_WARPS - 1) / JOIN_WARPS);
-    return start(join, grid, JOIN_WARPS * 32, 8 * (a.B + JOIN_WARPS), stream, a, BM);
+    return start(join, grid, JOIN_WARPS * 32, 0, stream, a, BM);
 }
 
 template <auto kernel, typename J>
@@ -794,7 +784,7 @@ cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
 template <int D>
 cudaError_t run_bf16(const TreeArgs &a, int sms, cudaStream_t stream) {
     if (on_tensor_cores(CCA_BF16, a.R, D)) return run_tc(a, sms, stream);
-    const int smem = TreeSmem<D>::bytes(a.B, a.T);
+    const int smem = TreeSmem<D>::bytes(a.T);
     auto *join = tree_join_kernel<__nv_bfloat16, D>;
     switch (rows_per_cta(CCA_BF16, a.R, D)) {
         case 16: return run_tree<tree_bf16_kernel<D, 1>>(join, a, 16, smem, sms, stream);
@@ -837,6 +827,11 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
         if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) != 0) return CCA_ERR_INVALID_ARG;
     if (!word_ptr(lens, true) || !word_ptr(parents, false)) return CCA_ERR_INVALID_ARG;
     if (workspace_bytes < cca_tree_workspace_size(params, T)) return CCA_ERR_INVALID_ARG;
+    // tiles of all lists are counted in 32 bits: the cores before a window and the window, or all
+    // rows of the table where that is less, and the nodes
+    const double rows = static_cast<double>(raw->rows) * raw->cols;
+    const double keys = fmin(rows / params->g + params->w + params->g, rows) + 3.0 * T + params->g;
+    if (keys / TILE * params->B * params->Hkv > 2.0e9) return CCA_ERR_UNSUPPORTED;
     const uint64_t es = params->dtype == CCA_BF16 ? 2 : 4;
     const uint64_t out = static_cast<uint64_t>(params->B) * params->Hq * T * params->d * es;
     if (bytes_meet(O, out, Q, out)) return CCA_ERR_INVALID_ARG;  // row tiles of other CTAs may still read Q
@@ -869,21 +864,26 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.R = params->Hq / params->Hkv * T;
     a.n_mt = 1;
     a.groups = 1;
+    a.by_g = fast_div(a.g);
+    a.by_rows = fast_div(a.rows);
+    a.by_crows = fast_div(a.crows);
     a.tile_log2 = 6;
     a.box_log2 = 0;
     a.min_tiles = 2;
     a.scale_log2 = resolve_scale(params) * 1.4426950408889634f;
     a.O = O;
     a.LSE = LSE;
-    a.ws = static_cast<float *>(workspace);
+    a.firsts = static_cast<int *>(workspace);
+    // partials are written 32 bytes at a time
+    a.ws = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(workspace) + WS_HEAD + 31) & ~uintptr_t{31});
     a.status = params->dev_status;
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
     if (params->dtype == CCA_BF16)
         return from_cuda(params->d == 128 ? run_bf16<128>(a, sms, strm) : run_bf16<64>(a, sms, strm));
     if (params->d == 128)
         return from_cuda(run_tree<tree_f32_kernel<128>>(tree_join_kernel<float, 128>, a, F32_BM,
-                                  TreeF32Smem<128>::bytes(a.B, T), sms, strm));
-    return from_cuda(run_tree<tree_f32_kernel<64>>(tree_join_kernel<float, 64>, a, F32_BM, TreeF32Smem<64>::bytes(a.B, T),
+                                  TreeF32Smem<128>::bytes(T), sms, strm));
+    return from_cuda(run_tree<tree_f32_kernel<64>>(tree_join_kernel<float, 64>, a, F32_BM, TreeF32Smem<64>::bytes(T),
                               sms, strm));
 }
 

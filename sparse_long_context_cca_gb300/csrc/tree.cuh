@@ -13,6 +13,14 @@ namespace tree {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Division by a number that the host knows: floor(n / d) for 0 <= n < 2^31 and d < 2^31 is the
+// high half of 4n * ceil(2^62 / d), as n * d < 2^62 keeps the rounding of the factor below 1/d.
+struct FastDiv {
+    uint64_t m;
+    __device__ __forceinline__ int div(int n) const { return static_cast<int>(__umul64hi(static_cast<uint64_t>(n) << 2, m)); }
+};
+inline FastDiv fast_div(int d) { return FastDiv{((uint64_t{1} << 62) + d - 1) / d}; }
+
 struct TreeArgs {
     const void *Q, *K, *V, *Kc, *Vc;
     const int32_t *table, *ctable, *lens, *parents;
@@ -24,10 +32,12 @@ struct TreeArgs {
     int box_log2;   // rows of a box that one copy can bring (0: no runs)
     int groups;  // groups of n_mt CTAs
     int min_tiles;  // tiles a group takes at least
+    FastDiv by_g, by_rows, by_crows;
     float scale_log2;
     void *O;
     float *LSE;
-    float *ws;
+    int *firsts;  // workspace: first tile of every sequence's lists and of none, [B + 1]
+    float *ws;    // workspace: partials
     int32_t *status;
 };
 
@@ -57,10 +67,10 @@ __device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) {
         return k;
     const int last = len + a.T - 1;  // T <= w, so no window of a node begins after len
     k.len = len;
-    k.cores_all = visible_cores(len, a.w, a.g);
-    k.cores_some = visible_cores(last, a.w, a.g);
-    k.raw_some = window_start(len, a.w, a.g, a.window_mode);
-    k.raw_all = window_start(last, a.w, a.g, a.window_mode);
+    k.cores_all = a.by_g.div(window_lo(len, a.w));
+    k.cores_some = a.by_g.div(window_lo(last, a.w));
+    k.raw_some = a.window_mode ? k.cores_all * a.g : window_lo(len, a.w);
+    k.raw_all = a.window_mode ? k.cores_some * a.g : window_lo(last, a.w);
     k.gap0 = k.gap1 = len;
     if (a.box_log2 > 0) {
         const int lg = a.box_log2;
@@ -83,7 +93,7 @@ __device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) {
 // The row of its pool that row `at` of a sequence lies in, -1 where no page is.
 __device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bool core, int at) {
     const int per = core ? a.crows : a.rows;
-    const int c = at / per;
+    const int c = core ? a.by_crows.div(at) : a.by_rows.div(at);
     int page = -1;
     if (c < (core ? a.ccols : a.cols))
         page = (core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
@@ -147,70 +157,86 @@ __device__ __forceinline__ int64_t find_box(const TreeArgs &a, const KeyList &k,
 
 // ---------------------------------------------------------------- the split
 
-// Runs of tiles: group y takes tiles [begin(y), begin(y + 1)) of all W tiles.
+// All W tiles in equal runs: the first W mod groups groups take one more.  W < 2^31.
 struct Split {
-    int64_t W;
-    int groups;
-    __device__ int64_t begin(int y) const { return W * y / groups; }
-    __device__ int owner(int64_t tile) const { return static_cast<int>(((tile + 1) * groups - 1) / W); }
+    int groups, each, more;
+    __device__ __forceinline__ int begin(int y) const { return y * each + min(y, more); }
+    __device__ __forceinline__ int owner(int tile) const {
+        const int big = more * (each + 1);
+        return tile < big ? tile / (each + 1) : more + (tile - big) / each;
+    }
 };
 
-__device__ __forceinline__ Split make_split(const TreeArgs &a, int64_t W) {
+__device__ __forceinline__ Split make_split(const TreeArgs &a, int W) {
     Split s;
-    s.W = W;
-    const int64_t most = W / a.min_tiles;
-    s.groups = most < a.groups ? static_cast<int>(most < 1 ? 1 : most) : a.groups;
+    const int most = W / a.min_tiles;
+    s.groups = most < a.groups ? max(most, 1) : a.groups;
+    s.each = W / s.groups;
+    s.more = W - s.each * s.groups;
     return s;
 }
 
-// sm_first[b] = tiles of the sequences before b (times Hkv); returns all.  B <= 1024.
-__device__ __forceinline__ int64_t scan_tiles(const TreeArgs &a, int64_t *sm_first, int64_t *sm_warp) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
-    const int per = (a.B + nt - 1) / nt;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    int64_t own = 0;
-    for (int b = b0; b < b1; ++b) own += static_cast<int64_t>(key_list(a, b).tiles) * a.Hkv;
-    int64_t x = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(kFull, x, off);
-        if (lane >= off) x += y;
-    }
-    if (lane == 31) sm_warp[warp] = x;
-    __syncthreads();
-    int64_t before = x - own, total = 0;
-    for (int i = 0; i < nw; ++i) {
-        if (i < warp) before += sm_warp[i];
-        total += sm_warp[i];
-    }
-    for (int b = b0; b < b1; ++b) {
-        sm_first[b] = before;
-        before += static_cast<int64_t>(key_list(a, b).tiles) * a.Hkv;
-    }
-    __syncthreads();
-    return total;
-}
-
-// The list that a tile belongs to.
+// One (b, KV head) list.
 struct Item {
     int b, kv;
-    int64_t first;  // its first tile
+    int first;  // its first tile
     KeyList k;
 };
 
-__device__ __forceinline__ Item item_of(const TreeArgs &a, const int64_t *sm_first, int64_t tile) {
-    Item it;
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sm_first[mid] <= tile) lo = mid;
-        else hi = mid - 1;
+// What a CTA finds out first, in shared memory.
+struct Start {
+    Item item;  // the list that its run begins in
+    int x0, x1; // its run of tiles
+    int warp_sum[16];
+};
+
+// Lengths to tiles to runs: every CTA adds up the tiles of all lists for itself (thread per
+// sequence), and the thread that owns the sequence its run begins in leaves that list behind.
+// The lists' first tiles go to the workspace for the joining kernel, from one CTA.
+__device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st, bool publish) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+    const int per = (a.B + nt - 1) / nt;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int own = 0;
+    KeyList k = {};
+    for (int b = b0; b < b1; ++b) {
+        k = key_list(a, b);
+        own += k.tiles * a.Hkv;
     }
-    it.b = lo;
-    it.k = key_list(a, lo);
-    it.kv = static_cast<int>((tile - sm_first[lo]) / it.k.tiles);
-    it.first = sm_first[lo] + static_cast<int64_t>(it.kv) * it.k.tiles;
-    return it;
+    int x = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, off);
+        if (lane >= off) x += y;
+    }
+    if (lane == 31) st.warp_sum[warp] = x;
+    if (tid == 0) st.x0 = st.x1 = 0;
+    __syncthreads();
+    int before = x - own, total = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i < warp) before += st.warp_sum[i];
+        total += st.warp_sum[i];
+    }
+    const Split s = make_split(a, total);
+    if (group < s.groups || publish) {
+        const int x0 = group < s.groups ? s.begin(group) : -1;
+        for (int b = b0; b < b1; ++b) {
+            if (per > 1) k = key_list(a, b);
+            const int tiles = k.tiles * a.Hkv;
+            if (x0 >= before && x0 < before + tiles) {
+                st.item.b = b;
+                st.item.kv = (x0 - before) / k.tiles;
+                st.item.first = before + st.item.kv * k.tiles;
+                st.item.k = k;
+                st.x0 = x0;
+                st.x1 = s.begin(group + 1);
+            }
+            if (publish) a.firsts[b] = before;
+            before += tiles;
+        }
+        if (publish && tid == 0) a.firsts[a.B] = total;
+    }
+    __syncthreads();
 }
 
 __device__ __forceinline__ void next_item(const TreeArgs &a, Item &it) {
@@ -232,29 +258,48 @@ struct Nodes {
     int words;
 };
 
+// A node's chain to the root: how deep it is, whether it gets there.  Its bits are added to
+// `bits`; parents lie below their children, so it ends and its words fall.
+struct Chain {
+    int depth;
+    bool whole;
+};
+__device__ __forceinline__ Chain walk_chain(const int16_t *up, uint32_t *bits, int n) {
+    int depth = -1, at = n >> 5;
+    uint32_t word = 0;
+    while (n >= 0) {
+        if ((n >> 5) != at) {
+            bits[at] = word;
+            word = 0;
+            at = n >> 5;
+        }
+        word |= 1u << (n & 31);
+        ++depth;
+        n = up[n];
+    }
+    bits[at] = word;
+    return Chain{depth, n == -1};
+}
+
+// A node's parent: an earlier node, -1 for the root, -2 for none.
+__device__ __forceinline__ int parent_of(const TreeArgs &a, int b, int t) {
+    if (a.parents == nullptr) return t - 1;
+    const int p = a.parents[static_cast<int64_t>(b) * a.T + t];
+    return p >= -1 && p < t ? p : -2;
+}
+
 __device__ __forceinline__ void read_tree(const TreeArgs &a, const Nodes &n, const KeyList &k, int b) {
     const int tid = threadIdx.x;
     for (int t = tid; t < a.T; t += blockDim.x) {
-        int p = t - 1;
-        if (a.parents != nullptr) {
-            p = a.parents[static_cast<int64_t>(b) * a.T + t];
-            if (p != -1 && (p < 0 || p >= t)) p = -2;
-        }
-        n.up[t] = static_cast<int16_t>(p);
+        n.up[t] = static_cast<int16_t>(parent_of(a, b, t));
     }
     __syncthreads();
     for (int t = tid; t < a.T; t += blockDim.x) {
         for (int i = 0; i < n.words; ++i) n.sees[t * n.words + i] = 0;
-        int depth = -1, x = t;
-        while (x >= 0) {  // parents lie below their children, so this ends
-            n.sees[t * n.words + (x >> 5)] |= 1u << (x & 31);
-            ++depth;
-            x = n.up[x];
-        }
-        const int pos = k.len + depth;
-        const bool whole = x == -1 && k.n > 0;
-        n.cores[t] = whole ? visible_cores(pos, a.w, a.g) : -1;
-        n.start[t] = window_start(pos, a.w, a.g, a.window_mode);
+        const Chain c = walk_chain(n.up, n.sees + t * n.words, t);
+        const int lo = window_lo(k.len + c.depth, a.w), cores = a.by_g.div(lo);
+        n.cores[t] = c.whole && k.n > 0 ? cores : -1;
+        n.start[t] = a.window_mode ? cores * a.g : lo;
     }
     __syncthreads();
 }

@@ -54,13 +54,10 @@ constexpr uint32_t IDESC_QK = ptx::idesc_bf16_f32(128, BN, 0, 0);  // Q, K both 
 constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(128, HD, 0, 1);  // P in tensor memory, V MN-major
 constexpr int METAS = 4;
 
-// What the softmax needs to know of a tile's keys.
+// What the softmax needs to know of a tile's keys, a bit for each.
 struct TileMeta {
-    const __nv_bfloat16 *v[BN];  // V rows, for the elements that `odd` takes out
-    int val[BN];
-    uint32_t kind[BN / 4];       // a byte per key
-    uint32_t masked[4];          // per producer warp: some key has kind != 0
-    uint32_t odd[4];             // bit per key: V holds an infinity or NaN that not every row sees
+    uint32_t gone[4];  // there is no such key: no page, or past the end of the list
+    uint32_t odd[4];   // its V holds an infinity or NaN, and not every row sees it
 };
 
 template <int HALVES>
@@ -72,24 +69,25 @@ struct Layout {
     static constexpr uint32_t OFF_RING = HALVES * TILE_BYTES;
     static constexpr uint32_t OFF_META = OFF_RING + NS * TILE_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_META + METAS * sizeof(TileMeta);
-    static constexpr int B_FULL = 0;                 // NS
-    static constexpr int B_EMPTY = B_FULL + NS;      // NS
-    static constexpr int B_QFULL = B_EMPTY + NS;     // HALVES
-    static constexpr int B_SFULL = B_QFULL + HALVES; // 2: per half, or per score buffer
-    static constexpr int B_PFULL = B_SFULL + 2;      // HALVES
-    static constexpr int B_PVDONE = B_PFULL + HALVES;// HALVES: two halves per list, one half per tile
-    static constexpr int B_OFREE = B_PVDONE + HALVES;// HALVES
+    static constexpr int B_FULL = 0;                  // NS
+    static constexpr int B_EMPTY = B_FULL + NS;       // NS
+    static constexpr int B_QFULL = B_EMPTY + NS;      // HALVES
+    static constexpr int B_SFULL = B_QFULL + HALVES;  // 2: per half, or per score buffer
+    static constexpr int B_PFULL = B_SFULL + 2;       // HALVES
+    static constexpr int B_PVDONE = B_PFULL + HALVES; // HALVES: two halves per list, one half per tile
+    static constexpr int B_OFREE = B_PVDONE + HALVES; // HALVES
     static constexpr int B_DRAIN = B_OFREE + HALVES;
     static constexpr int NUM_BARS = B_DRAIN + 1;
     static constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
     static constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-    static constexpr uint32_t OFF_FIRST = (OFF_ABORT + 4 + 15) / 16 * 16;
-    // then: tiles before each sequence [B], 16 warp sums, per half parents [T] and a bit row per
-    // query row [128][words]
-    static uint32_t bytes(int B, int T) {
-        return OFF_FIRST + 8 * (B + 16) + HALVES * (2 * ((T + 1) / 2 * 2) + 128 * 4 * ((T + 31) / 32)) + 1024;
-    }
+    static constexpr uint32_t OFF_START = (OFF_ABORT + 4 + 15) / 16 * 16;
+    static constexpr uint32_t OFF_NODES = (OFF_START + sizeof(Start) + 15) / 16 * 16;
+    // then, per half: bits of every row [128][words], parents [T]
+    static uint32_t bytes(int T) { return OFF_NODES + HALVES * (128 * 4 * ((T + 31) / 32) + 2 * ((T + 1) / 2 * 2)) + 1024; }
 };
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 template <int HALVES>
 __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
@@ -106,8 +104,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     auto bar = [&](int idx) -> uint32_t { return base + L::OFF_BAR + 8u * idx; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_ABORT);
     TileMeta *metas = reinterpret_cast<TileMeta *>(gbase + L::OFF_META);
-    int64_t *sm_first = reinterpret_cast<int64_t *>(gbase + L::OFF_FIRST);
-    int64_t *sm_warp = sm_first + a.B;
+    Start &st = *reinterpret_cast<Start *>(gbase + L::OFF_START);
     const int words = (a.T + 31) >> 5;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -123,8 +120,10 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             ptx::mbar_init(bar(L::B_PVDONE + h), 1);
             ptx::mbar_init(bar(L::B_OFREE + h), 4);
         }
-        ptx::mbar_init(bar(L::B_SFULL), 1);
-        ptx::mbar_init(bar(L::B_SFULL + 1), 1);
+        // the scores are done, and the issuer's own arrival: what the producers wrote about the
+        // tile before they handed it over is visible behind it
+        ptx::mbar_init(bar(L::B_SFULL), 2);
+        ptx::mbar_init(bar(L::B_SFULL + 1), 2);
         ptx::mbar_init(bar(L::B_DRAIN), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -133,70 +132,64 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         ptx::tmem_alloc(base + L::OFF_TMEMPTR, TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    if (warp == HALVES * 4 && lane < 4) ptx::prefetch_tmap(lane == 0 ? &tmK : lane == 1 ? &tmV : lane == 2 ? &tmKc : &tmVc);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     ptx::tc_fence_before();
-    __syncthreads();
+    const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
+    find_run(a, group, st, blockIdx.x == 0);  // holds barriers
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(gbase + L::OFF_TMEMPTR);
-
-    const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    const Split split = make_split(a, scan_tiles(a, sm_first, sm_warp));
-    const int64_t x0 = group < split.groups ? split.begin(group) : 0;
-    const int64_t x1 = group < split.groups ? split.begin(group + 1) : 0;
+    const int x0 = st.x0, x1 = st.x1;
     const bool half_used[2] = {true, HALVES == 2 && mt * BM + 128 < a.R};
 
     if (wg == HALVES) {
         // ------------------------------------------------------------ producers
-        if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         const int pw = warp & 3;
         const int sub = lane >> 4, chunk = lane & 15;
         bool ok = x0 < x1 && !skip_loads;
-        Item it = {};
+        Item it = st.item;
+        // the tile to load next: a lane's box of runs, or a lane's key of the rest
+        bool runs = false, core = false;
+        int box_y = 0;
         const char *kp = nullptr, *vp = nullptr;
-        int kind = 4, val = 0;
-        int box_y = 0;         // of a tile of runs: this lane's box, as a row of its pool
-        bool runs = false, box_core = false;
+        uint32_t gone = 0, mixed = 0;  // per key of this warp: not there; seen by some rows only
         const int per_warp = a.box_log2 > 0 ? 32 >> a.box_log2 : 0;  // boxes of a warp
-        auto look_up = [&](int64_t x) {
-            const int tile = static_cast<int>(x - it.first);
+        auto look_up = [&](int x) {
+            const int tile = x - it.first;
             runs = tile < it.k.run_tiles;
+            mixed = 0;
             if (runs) {
-                kind = 0;
+                int64_t row = 0;
                 if (lane < per_warp) {
-                    const int64_t row = find_box(a, it.k, it.b, it.kv, (tile * 4 + pw) * per_warp + lane, box_core);
+                    row = find_box(a, it.k, it.b, it.kv, (tile * 4 + pw) * per_warp + lane, core);
                     // no page: past the pool's end, where the copy fills in zeros
-                    box_y = static_cast<int>(row >= 0 ? row : static_cast<int64_t>(box_core ? a.n_cpages : a.n_pages) * a.Hkv * (box_core ? a.crows : a.rows));
-                    kind = row >= 0 ? 0 : 4;
+                    box_y = static_cast<int>(row >= 0 ? row : static_cast<int64_t>(core ? a.n_cpages : a.n_pages) * a.Hkv * (core ? a.crows : a.rows));
                 }
-                // each lane: the kind of its key, which its box's lane knows
-                kind = __shfl_sync(kFull, kind, lane >> a.box_log2);
+                gone = __ballot_sync(kFull, row < 0);  // a bit per box; usually none
+                if (gone != 0) gone = __ballot_sync(kFull, (gone >> (lane >> a.box_log2)) & 1u);
                 return;
             }
             const Key key = find_key(a, it.k, it.b, it.kv, (tile - it.k.run_tiles) * BN + pw * 32 + lane);
-            const int64_t off = key.row * (HD * 2);
-            kp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Kc : a.K) + off;
-            vp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Vc : a.V) + off;
-            kind = key.kind;
-            val = key.val;
+            kp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Kc : a.K) + key.row * (HD * 2);
+            vp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Vc : a.V) + key.row * (HD * 2);
+            gone = __ballot_sync(kFull, key.kind == 4);
+            mixed = __ballot_sync(kFull, key.kind != 0 && key.kind != 4);
         };
-        // The tile whose copies are in flight behind the one being issued.
-        int prev_slot = -1;
-        uint32_t prev_mixed = 0;  // lanes' keys that only some rows see
-        int prev_meta = 0;
-        int64_t last_run = -1;    // last tile of runs that was issued
-        auto land = [&]() {       // that tile's copies (of this thread) have arrived
-            if (prev_slot < 0) return;
-            const int vslot = (prev_slot + 1) % NS;
-            if (prev_mixed != 0) {
-                // infinities and NaN in the V of such keys would reach the other rows as 0 * NaN:
-                // they leave the tile, and the rows that see them add them back themselves
+        // a slot whose cp.async copies are in flight behind the one being filled
+        int held = -1, held_meta = 0;
+        uint32_t held_mixed = 0;
+        bool held_v = false;
+        auto land = [&]() {  // its copies (of this thread) have arrived
+            if (held < 0) return;
+            if (held_v && held_mixed != 0) {
+                // infinities and NaN in the V of a key that only some rows see would reach the others
+                // as 0 * NaN: they leave the tile, and the rows that see the key add them themselves
                 for (int j = 0; j < 16; ++j) {
                     const int r = 2 * j + sub;
-                    if (!((prev_mixed >> r) & 1u)) continue;
+                    if (!((held_mixed >> r) & 1u)) continue;
                     const int row = pw * 32 + r;
-                    uint4 *p = reinterpret_cast<uint4 *>(gbase + L::OFF_RING + vslot * TILE_BYTES + (chunk >> 3) * HALF_BYTES +
+                    uint4 *p = reinterpret_cast<uint4 *>(gbase + L::OFF_RING + held * TILE_BYTES + (chunk >> 3) * HALF_BYTES +
                                                          row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
                     uint32_t v[4] = {p->x, p->y, p->z, p->w};
                     bool hit = false;
@@ -213,176 +206,124 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                     }
                     if (hit) {
                         *p = make_uint4(v[0], v[1], v[2], v[3]);
-                        atomicOr(&metas[prev_meta].odd[row >> 5], 1u << (row & 31));
+                        atomicOr(&metas[held_meta].odd[row >> 5], 1u << (row & 31));
                     }
                 }
             }
             ptx::fence_proxy_async_smem();  // the MMAs read what this thread has written
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(bar(L::B_FULL + prev_slot));
-                ptx::mbar_arrive(bar(L::B_FULL + vslot));
-            }
+            if (lane == 0) ptx::mbar_arrive(bar(L::B_FULL + held));
+            held = -1;
         };
-        if (ok) {
-            it = item_of(a, sm_first, x0);
-            look_up(x0);
-        }
-        for (int64_t x = x0; ok && x < x1; ++x) {
-            const uint32_t u = static_cast<uint32_t>(x - x0) * 2;
-            const int ks = u % NS, vs = (u + 1) % NS;
-            // Before it waits for room, the tile in flight is handed over: with a ring of two tiles
-            // the room may depend on it (the first half's next scores come before the second
-            // half's product, which frees the slot).
-            if (prev_slot >= 0 && !__all_sync(kFull, ptx::mbar_try_wait(bar(L::B_EMPTY + ks), ((u / NS) & 1) ^ 1) &&
-                                                         ptx::mbar_try_wait(bar(L::B_EMPTY + vs), (((u + 1) / NS) & 1) ^ 1))) {
+        int last_bulk = -1;  // last slot fill that went by TMA
+        if (ok) look_up(x0);
+        for (int u = 0; ok && u < 2 * (x1 - x0); ++u) {
+            const int x = x0 + (u >> 1), slot = u % NS;
+            const bool is_v = u & 1;
+            // Before it waits for room, or fills a slot by TMA, what is in flight is handed over: the
+            // room may depend on it.
+            const uint32_t parity = ((u / NS) & 1) ^ 1;
+            if (held >= 0 && (runs || !__all_sync(kFull, ptx::mbar_try_wait(bar(L::B_EMPTY + slot), parity)))) {
                 cp_wait<0>();
                 land();
-                prev_slot = -1;
             }
-            if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_EMPTY + ks), ((u / NS) & 1) ^ 1, abort_flag, lim) &&
-                                       ptx::wait_bounded(bar(L::B_EMPTY + vs), (((u + 1) / NS) & 1) ^ 1, abort_flag, lim))) {
+            if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_EMPTY + slot), parity, abort_flag, lim))) {
                 ok = false;
                 break;
             }
-            // A slot of METAS tiles ago: its softmax is over, as the scores of a later tile, which
-            // freed this K slot, were issued after it.
-            TileMeta &m = metas[(x - x0) & (METAS - 1)];
-            if (runs) {
-                const uint32_t gone = __ballot_sync(kFull, kind != 0);
-                if (gone != 0) {
-                    reinterpret_cast<uint8_t *>(m.kind)[pw * 32 + lane] = static_cast<uint8_t>(kind);
-                    m.val[pw * 32 + lane] = 0;
-                } else if (lane < 8) {
-                    m.kind[pw * 8 + lane] = 0;  // a neighbour's missing page may make the tile masked
-                }
-                if (lane == 0) {
-                    m.masked[pw] = gone;
-                    m.odd[pw] = 0;
-                }
-                if (prev_slot >= 0) {
-                    cp_wait<0>();
-                    land();
-                    prev_slot = -1;
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(bar(L::B_FULL + ks), 32 * HD * 2);
-                    ptx::mbar_arrive_expect_tx(bar(L::B_FULL + vs), 32 * HD * 2);
-                }
-                __syncwarp();
-                if (lane < per_warp) {
-                    const uint32_t at = base + L::OFF_RING + (pw * 32 + (lane << a.box_log2)) * 128;
-                    const void *mk = box_core ? static_cast<const void *>(&tmKc) : static_cast<const void *>(&tmK);
-                    const void *mv = box_core ? static_cast<const void *>(&tmVc) : static_cast<const void *>(&tmV);
-                    ptx::tma_load_2d(mk, bar(L::B_FULL + ks), at + ks * TILE_BYTES, 0, box_y);
-                    ptx::tma_load_2d(mk, bar(L::B_FULL + ks), at + ks * TILE_BYTES + HALF_BYTES, 64, box_y);
-                    ptx::tma_load_2d(mv, bar(L::B_FULL + vs), at + vs * TILE_BYTES, 0, box_y);
-                    ptx::tma_load_2d(mv, bar(L::B_FULL + vs), at + vs * TILE_BYTES + HALF_BYTES, 64, box_y);
-                }
-                last_run = x - x0;
-                __syncwarp();
-                if (x + 1 < x1) {
-                    if (x + 1 >= it.first + it.k.tiles) next_item(a, it);
-                    look_up(x + 1);
-                }
-                continue;
-            }
-            const int at = pw * 32 + lane;
-            m.v[at] = reinterpret_cast<const __nv_bfloat16 *>(vp);
-            m.val[at] = val;
-            reinterpret_cast<uint8_t *>(m.kind)[at] = static_cast<uint8_t>(kind);
-            const uint32_t some = __ballot_sync(kFull, kind != 0);
-            const uint32_t mixed = __ballot_sync(kFull, kind != 0 && kind != 4);
-            if (lane == 0) {
-                m.masked[pw] = some;
-                m.odd[pw] = 0;
+            if (!is_v && lane == 0) {
+                // The tile of METAS before: its softmax is over, as the scores that freed this slot were
+                // issued behind it.
+                metas[(x - x0) & (METAS - 1)].gone[pw] = gone;
+                metas[(x - x0) & (METAS - 1)].odd[pw] = 0;
             }
             __syncwarp();
-            const uint32_t kdst = base + L::OFF_RING + ks * TILE_BYTES + (chunk >> 3) * HALF_BYTES;
-            const uint32_t vdst = base + L::OFF_RING + vs * TILE_BYTES + (chunk >> 3) * HALF_BYTES;
+            const uint32_t dst = base + L::OFF_RING + slot * TILE_BYTES;
+            if (runs) {
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::B_FULL + slot), 32 * HD * 2);
+                __syncwarp();
+                if (lane < per_warp) {
+                    const uint32_t at = dst + (pw * 32 + (lane << a.box_log2)) * 128;
+                    const void *map = is_v ? (core ? static_cast<const void *>(&tmVc) : static_cast<const void *>(&tmV))
+                                           : (core ? static_cast<const void *>(&tmKc) : static_cast<const void *>(&tmK));
+                    ptx::tma_load_2d(map, bar(L::B_FULL + slot), at, 0, box_y);
+                    ptx::tma_load_2d(map, bar(L::B_FULL + slot), at + HALF_BYTES, 64, box_y);
+                }
+                last_bulk = u;
+                __syncwarp();
+            } else {
+                const unsigned long long mine = reinterpret_cast<unsigned long long>(is_v ? vp : kp);
 #pragma unroll 4
-            for (int j = 0; j < 16; ++j) {
-                const int row = pw * 32 + 2 * j + sub;
-                const char *p = reinterpret_cast<const char *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(kp), 2 * j + sub));
-                cp16(kdst + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), p == nullptr ? static_cast<const char *>(a.K) : p + chunk * 16, p != nullptr);
+                for (int j = 0; j < 16; ++j) {
+                    const int row = pw * 32 + 2 * j + sub;
+                    const char *p = reinterpret_cast<const char *>(__shfl_sync(kFull, mine, 2 * j + sub));
+                    cp16(dst + (chunk >> 3) * HALF_BYTES + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
+                         p == nullptr ? static_cast<const char *>(a.K) : p + chunk * 16, p != nullptr);
+                }
+                cp_commit();
+                if (held >= 0) {
+                    cp_wait<1>();
+                    land();
+                }
+                held = slot;
+                held_v = is_v;
+                held_mixed = mixed;
+                held_meta = (x - x0) & (METAS - 1);
             }
-#pragma unroll 4
-            for (int j = 0; j < 16; ++j) {
-                const int row = pw * 32 + 2 * j + sub;
-                const char *p = reinterpret_cast<const char *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(vp), 2 * j + sub));
-                cp16(vdst + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), p == nullptr ? static_cast<const char *>(a.V) : p + chunk * 16, p != nullptr);
-            }
-            cp_commit();
-            if (x + 1 < x1) {
+            if (is_v && x + 1 < x1) {
                 if (x + 1 >= it.first + it.k.tiles) next_item(a, it);
                 look_up(x + 1);
             }
-            cp_wait<1>();
-            land();
-            prev_slot = ks;
-            prev_mixed = mixed;
-            prev_meta = static_cast<int>((x - x0) & (METAS - 1));
         }
         cp_wait<0>();
         if (ok) land();
         if (*abort_flag && lane == 0) {
             // bulk copies already issued land before the CTA's memory is given back
             volatile int never = 0;
-            for (int64_t t = last_run > NS ? last_run - NS : 0; t <= last_run; ++t) {
-                const uint32_t u = static_cast<uint32_t>(t) * 2;
+            for (int u = last_bulk >= NS ? last_bulk - NS + 1 : 0; u <= last_bulk; ++u)
                 ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, &never, lim);
-                ptx::wait_bounded(bar(L::B_FULL + (u + 1) % NS), ((u + 1) / NS) & 1, &never, lim);
-            }
         }
         __syncwarp();
     } else if (wg == HALVES + 1) {
         // ------------------------------------------------------------ MMA issuer
-        if constexpr (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         if ((warp & 3) == 0) {
             auto wwait = [&](int b, uint32_t parity) -> bool {
                 return __all_sync(kFull, ptx::wait_bounded(bar(b), parity, abort_flag, lim));
             };
+            auto slot_full = [&](int u) -> bool { return wwait(L::B_FULL + u % NS, (u / NS) & 1); };
             const uint64_t dq = ptx::smem_desc_sw128(base + L::OFF_Q, 16, 1024);
             const uint64_t dk = ptx::smem_desc_sw128(base + L::OFF_RING, 16, 1024);
             const uint64_t dv = ptx::smem_desc_sw128(base + L::OFF_RING, HALF_BYTES, 1024);
             constexpr uint64_t STEP = TILE_BYTES >> 4;
             bool ok = true;
-            uint32_t seg = 0;
-            uint32_t pcount = 0;  // tiles whose P was waited for (a used half each)
-            Item it = {};
-            if (x0 < x1) it = item_of(a, sm_first, x0);
-            int64_t x = x0;
+            uint32_t seg = 0, pcount = 0;  // lists; tiles whose P was waited for
+            Item it = st.item;
+            int x = x0;
+            // S = Q_h K(t)^T into score buffer `buf`; K(t) has been waited for
+            auto scores = [&](int h, int buf, int t) {
+                ptx::tc_fence_after();
+                ptx::mma_ss_k128_warp(tmem + buf * 128, dq + h * STEP, dk + (2 * (t - x0) % NS) * STEP, IDESC_QK, 0u);
+                ptx::tc_commit_warp(bar(L::B_SFULL + buf));
+                if (lane == 0) ptx::mbar_arrive(bar(L::B_SFULL + buf));
+                __syncwarp();
+            };
             while (ok && x < x1) {
-                const int64_t end = it.first + it.k.tiles < x1 ? it.first + it.k.tiles : x1;
+                const int end = min(it.first + it.k.tiles, x1);
                 if constexpr (HALVES == 2) {
-                    auto scores = [&](int h, int64_t t) {
-                        const uint32_t slot = (static_cast<uint32_t>(t - x0) * 2) % NS;
-                        ptx::tc_fence_after();
-                        ptx::mma_ss_k128_warp(tmem + h * 128, dq + h * STEP, dk + slot * STEP, IDESC_QK, 0u);
-                        ptx::tc_commit_warp(bar(L::B_SFULL + h));
-                    };
-                    {
-                        const uint32_t u = static_cast<uint32_t>(x - x0) * 2;
-                        for (int h = 0; ok && h < 2; ++h) {
-                            if (!half_used[h]) continue;
-                            if (!wwait(L::B_QFULL + h, seg & 1) || !wwait(L::B_FULL + u % NS, (u / NS) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            scores(h, x);
-                        }
-                        if (!ok) break;
-                        ptx::tc_commit_warp(bar(L::B_EMPTY + u % NS));
+                    for (int h = 0; ok && h < 2; ++h) {
+                        if (!half_used[h]) continue;
+                        ok = wwait(L::B_QFULL + h, seg & 1) && slot_full(2 * (x - x0));
+                        if (ok) scores(h, h, x);
                     }
-                    for (int64_t t = x; ok && t < end; ++t) {
-                        const uint32_t u = static_cast<uint32_t>(t - x0) * 2 + 1;
-                        if (!wwait(L::B_FULL + u % NS, (u / NS) & 1)) {
+                    if (!ok) break;
+                    ptx::tc_commit_warp(bar(L::B_EMPTY + 2 * (x - x0) % NS));
+                    for (int t = x; ok && t < end; ++t) {
+                        const int u = 2 * (t - x0) + 1;
+                        if (!slot_full(u)) {
                             ok = false;
                             break;
                         }
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
                             if (!half_used[h]) continue;
                             if (!wwait(L::B_PFULL + h, pcount & 1) || (t == x && !wwait(L::B_OFREE + h, (seg & 1) ^ 1))) {
@@ -392,11 +333,11 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             ptx::tc_fence_after();
                             ptx::mma_ts_k128_warp(tmem + TM_O + h * 128, tmem + h * 128, dv + (u % NS) * STEP, IDESC_PV, t == x ? 0u : 1u);
                             if (t + 1 < end) {
-                                if (!wwait(L::B_FULL + (u + 1) % NS, ((u + 1) / NS) & 1)) {
+                                if (!slot_full(u + 1)) {
                                     ok = false;
                                     break;
                                 }
-                                scores(h, t + 1);
+                                scores(h, h, t + 1);
                             } else {
                                 ptx::tc_commit_warp(bar(L::B_PVDONE + h));
                             }
@@ -407,34 +348,26 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                         ++pcount;
                     }
                 } else {
-                    auto scores = [&](int64_t t) -> bool {
-                        const uint32_t u = static_cast<uint32_t>(t - x0) * 2;
-                        if (!wwait(L::B_FULL + u % NS, (u / NS) & 1)) return false;
-                        const uint32_t buf = static_cast<uint32_t>(t - x0) & 1;
-                        ptx::tc_fence_after();
-                        ptx::mma_ss_k128_warp(tmem + buf * 128, dq, dk + (u % NS) * STEP, IDESC_QK, 0u);
-                        ptx::tc_commit_warp(bar(L::B_SFULL + buf));
-                        ptx::tc_commit_warp(bar(L::B_EMPTY + u % NS));
-                        return true;
-                    };
-                    if (!wwait(L::B_QFULL, seg & 1) || !scores(x)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int64_t t = x; ok && t < end; ++t) {
-                        if (t + 1 < end && !scores(t + 1)) {
-                            ok = false;
-                            break;
+                    ok = wwait(L::B_QFULL, seg & 1);
+                    for (int t = x; ok && t <= end; ++t) {
+                        // the scores of tile t, then the product of tile t - 1
+                        if (t < end) {
+                            const int u = 2 * (t - x0);
+                            if (!slot_full(u)) {
+                                ok = false;
+                                break;
+                            }
+                            scores(0, (t - x0) & 1, t);
+                            ptx::tc_commit_warp(bar(L::B_EMPTY + u % NS));
                         }
-                        const uint32_t u = static_cast<uint32_t>(t - x0) * 2 + 1;
-                        if (!wwait(L::B_FULL + u % NS, (u / NS) & 1) || !wwait(L::B_PFULL, pcount & 1) ||
-                            (t == x && !wwait(L::B_OFREE, (seg & 1) ^ 1))) {
+                        if (t == x) continue;
+                        const int u = 2 * (t - 1 - x0) + 1;
+                        if (!slot_full(u) || !wwait(L::B_PFULL, pcount & 1) || (t - 1 == x && !wwait(L::B_OFREE, (seg & 1) ^ 1))) {
                             ok = false;
                             break;
                         }
                         ptx::tc_fence_after();
-                        ptx::mma_ts_k128_warp(tmem + TM_O, tmem + (static_cast<uint32_t>(t - x0) & 1) * 128, dv + (u % NS) * STEP, IDESC_PV,
-                                              t == x ? 0u : 1u);
+                        ptx::mma_ts_k128_warp(tmem + TM_O, tmem + ((t - 1 - x0) & 1) * 128, dv + (u % NS) * STEP, IDESC_PV, t - 1 == x ? 0u : 1u);
                         ptx::tc_commit_warp(bar(L::B_PVDONE));
                         ptx::tc_commit_warp(bar(L::B_EMPTY + u % NS));
                         ++pcount;
@@ -452,8 +385,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         __syncwarp();
     } else if (wg == 0 || half_used[1]) {
         // ------------------------------------------------------------ softmax and output
-        if constexpr (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int h = HALVES == 2 ? wg : 0;
         const int quarter = warp & 3;
         const int in = h * 128 + quarter * 32 + lane;  // row of the CTA
@@ -462,115 +393,134 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         const bool idle = mt * BM + h * 128 + quarter * 32 >= a.R;  // no row of this warp
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tO = tmem + lane_addr + TM_O + h * 128;
-        int16_t *const up = reinterpret_cast<int16_t *>(sm_warp + 16) + h * ((a.T + 1) / 2 * 2);
-        uint32_t *const sees = reinterpret_cast<uint32_t *>(reinterpret_cast<int16_t *>(sm_warp + 16) + HALVES * ((a.T + 1) / 2 * 2)) +
-                               (h * 128 + quarter * 32 + lane) * words;
+        uint32_t *const sees = reinterpret_cast<uint32_t *>(gbase + L::OFF_NODES) + (h * 128 + quarter * 32 + lane) * words;
+        int16_t *const up = reinterpret_cast<int16_t *>(gbase + L::OFF_NODES + HALVES * 512 * words) + h * ((a.T + 1) / 2 * 2);
         const int node = live ? row % a.T : 0;
         bool ok = true;
         uint32_t seg = 0, n_s = 0;  // lists and tiles of this half so far
-        Item it = {};
-        int start = 0, cores = -1;  // this row's first raw token; its visible cores, -1: empty node
+        Item it = st.item;
         int tree_of = -1;
-        auto sees_key = [&](const TileMeta &tm, int col) {
-            const int kind = reinterpret_cast<const uint8_t *>(tm.kind)[col], val = tm.val[col];
-            if (kind == 3) return ((sees[val >> 5] >> (val & 31)) & 1u) != 0;
-            return kind == 0 || (kind == 1 && val < cores) || (kind == 2 && val >= start);
+        int start = 0, cores = -1;  // this row's first raw token; its visible cores, -1: empty node
+        auto list_row = [&]() { return (static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T; };
+        // The queries of this warp's rows, 16 lanes to a row, swizzled like the keys.  The scores of
+        // the last tile are done, so nothing reads the old ones.
+        auto load_q = [&]() {
+            const char *q = static_cast<const char *>(a.Q) + (list_row() + mt * BM + h * 128 + quarter * 32) * (HD * 2);
+            const int sub = lane >> 4, chunk = lane & 15;
+#pragma unroll 4
+            for (int j = 0; j < 16; ++j) {
+                const int r = 2 * j + sub;
+                const bool there = mt * BM + h * 128 + quarter * 32 + r < a.R;
+                cp16(base + L::OFF_Q + h * TILE_BYTES + (chunk >> 3) * HALF_BYTES + (quarter * 32 + r) * 128 + (((chunk & 7) ^ (r & 7)) << 4),
+                     there ? q + r * (HD * 2) + chunk * 16 : static_cast<const char *>(a.Q), there);
+            }
+            cp_commit();
         };
-        auto begin_list = [&]() {
-            // the queries, 16 chunks of a row, swizzled like the keys; S of the last tile is done,
-            // so nothing reads the old ones
-            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.Q) +
-                             ((static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T + row) * HD);
-            uint8_t *dst = gbase + L::OFF_Q + h * TILE_BYTES + (quarter * 32 + lane) * 128;
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-                *reinterpret_cast<uint4 *>(dst + (c >> 3) * HALF_BYTES + (((c & 7) ^ (lane & 7)) << 4)) = live ? q[c] : make_uint4(0, 0, 0, 0);
+        auto hand_q = [&]() {
+            cp_wait<0>();
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(L::B_QFULL + h));
         };
-        auto begin_tree = [&]() {
+        // The list's tree, when it is first needed: parents in shared memory, each row walks its own chain.
+        auto read_nodes = [&]() {
             if (it.b == tree_of) return;
             tree_of = it.b;
-            const int tid = quarter * 32 + lane;
             ptx::named_bar_sync(1 + h, 128);  // the old parents have been used
-            for (int t = tid; t < a.T; t += 128) {
-                int p = t - 1;
-                if (a.parents != nullptr) {
-                    p = a.parents[static_cast<int64_t>(it.b) * a.T + t];
-                    if (p != -1 && (p < 0 || p >= t)) p = -2;
-                }
-                up[t] = static_cast<int16_t>(p);
-            }
+            for (int t = quarter * 32 + lane; t < a.T; t += 128) up[t] = static_cast<int16_t>(parent_of(a, it.b, t));
             ptx::named_bar_sync(1 + h, 128);
             for (int i = 0; i < words; ++i) sees[i] = 0;
-            int depth = -1, n = node;
-            while (n >= 0) {  // parents lie below their children, so this ends
-                sees[n >> 5] |= 1u << (n & 31);
-                ++depth;
-                n = up[n];
+            const Chain c = walk_chain(up, sees, node);
+            const int lo = window_lo(it.k.len + c.depth, a.w), vis = a.by_g.div(lo);
+            cores = live && c.whole && it.k.n > 0 ? vis : -1;
+            start = a.window_mode ? vis * a.g : lo;
+        };
+        // Bits of the 32 keys from key `x` of the rest on that this row sees.
+        auto seen = [&](int x) {
+            const int A = it.k.n_all, nc = it.k.cores_some - it.k.cores_all, nr = it.k.raw_all - it.k.raw_some;
+            const int vc = min(max(cores - it.k.cores_all, 0), nc);      // of the cores that some see: the first vc
+            const int sr = min(max(start - it.k.raw_some, 0), nr);       // of the raw tokens: all but the first sr
+            uint32_t m = low_bits(A + vc - x) | (low_bits(A + nc + nr - x) & ~low_bits(A + nc + sr - x));
+            const int n0 = x - (A + nc + nr);                            // node of bit 0
+            if (n0 > -32 && n0 < a.T) {
+                const int w0 = n0 >> 5;
+                const uint32_t lo = w0 >= 0 ? sees[w0] : 0u, hi = w0 + 1 < words ? sees[w0 + 1] : 0u;
+                m |= __funnelshift_r(lo, hi, n0 & 31);
             }
-            const int pos = it.k.len + depth;
-            cores = live && n == -1 && it.k.n > 0 ? visible_cores(pos, a.w, a.g) : -1;
-            start = window_start(pos, a.w, a.g, a.window_mode);
+            return m;
         };
         if (x0 < x1) {
-            it = item_of(a, sm_first, x0);
-            begin_list();
-            begin_tree();
+            load_q();
+            hand_q();
         }
-        int64_t x = x0;
+        int x = x0;
         while (ok && x < x1) {
-            const int64_t end = it.first + it.k.tiles < x1 ? it.first + it.k.tiles : x1;
+            const int end = min(it.first + it.k.tiles, x1);
             float m = -INFINITY, l = 0.f;
             bool has_odd = false;
             float *const part = part_at(a, group, mt, x0 >= it.first ? 0 : 1, BM, HD);
             if (it.k.n == 0 && threadIdx.x == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
-            for (int64_t t = x; t < end; ++t, ++n_s) {
-                const uint32_t buf = HALVES == 2 ? h : static_cast<uint32_t>(t - x0) & 1;
-                const uint32_t s_parity = HALVES == 2 ? n_s & 1 : (n_s >> 1) & 1;
-                const uint32_t uv = static_cast<uint32_t>(t - x0) * 2 + 1;
-                // V(t)'s barrier: what the producers wrote about the tile is visible after it, and its
-                // slot is not filled again before this softmax is over
-                if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_SFULL + buf), s_parity, abort_flag, lim) &&
-                                           ptx::wait_bounded(bar(L::B_FULL + uv % NS), (uv / NS) & 1, abort_flag, lim))) {
+            for (int t = x; t < end; ++t, ++n_s) {
+                const int buf = HALVES == 2 ? h : (t - x0) & 1;
+                if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_SFULL + buf), HALVES == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag, lim))) {
                     ok = false;
                     break;
                 }
+                ptx::tc_fence_after();
+                if (t + 1 == end && end < x1) {  // the last tile of this list: its scores have read the queries
+                    const Item now = it;
+                    next_item(a, it);
+                    load_q();
+                    it = now;
+                }
                 const uint32_t tS = tmem + lane_addr + buf * 128;
                 const TileMeta &tm = metas[(t - x0) & (METAS - 1)];
+                const int rest = t - it.first - it.k.run_tiles;  // tile of the rest, < 0: runs
+                const uint4 gone = *reinterpret_cast<const uint4 *>(tm.gone);
+                const bool masked = rest >= 0 || (gone.x | gone.y | gone.z | gone.w) != 0;
+                if (rest >= 0) {
+                    read_nodes();
+                    // V(t)'s slot is not filled again before this softmax is over: what the producers
+                    // took out of it is known now
+                    const int u = 2 * (t - x0) + 1;
+                    if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, abort_flag, lim))) {
+                        ok = false;
+                        break;
+                    }
+                }
+                auto mask_of = [&](int c) {  // of columns 32c .. 32c + 31
+                    return (rest >= 0 ? seen(rest * BN + c * 32) : 0xffffffffu) & ~tm.gone[c];
+                };
                 if (!idle) {
-                    ptx::tc_fence_after();
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + c * 32, s[c]);
-                    ptx::tmem_wait_ld(s[0]);
-                    ptx::reg_touch(s[1]);
-                    ptx::reg_touch(s[2]);
-                    ptx::reg_touch(s[3]);
-                    if ((tm.masked[0] | tm.masked[1] | tm.masked[2] | tm.masked[3]) != 0) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t see = 0;
+                    // the row's maximum; 64 columns at a time, which keeps the code short (a launch
+                    // begins with cold instruction caches) and the registers few
+                    float mx = -INFINITY;
 #pragma unroll 1
-                            for (int kk = 0; kk < 32; ++kk) see |= static_cast<uint32_t>(sees_key(tm, c * 32 + kk)) << kk;
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t s[2][32];
+                        ptx::tmem_ld32(tS + c * 64, s[0]);
+                        ptx::tmem_ld32(tS + c * 64 + 32, s[1]);
+                        ptx::tmem_wait_ld(s[0]);
+                        ptx::reg_touch(s[1]);
+                        if (masked) {
 #pragma unroll
-                            for (int kk = 0; kk < 32; ++kk)
-                                if (!((see >> kk) & 1u)) s[c][kk] = __float_as_uint(-INFINITY);
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t see = mask_of(2 * c + i);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!((see >> k) & 1u)) s[i][k] = __float_as_uint(-INFINITY);
+                            }
                         }
+                        float mp[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            mp[q] = fmaxf(__uint_as_float(s[q >> 1][(q & 1) * 16]), __uint_as_float(s[q >> 1][(q & 1) * 16 + 1]));
+#pragma unroll
+                            for (int k = 2; k < 16; k += 2)
+                                mp[q] = ptx::max3(mp[q], __uint_as_float(s[q >> 1][(q & 1) * 16 + k]), __uint_as_float(s[q >> 1][(q & 1) * 16 + k + 1]));
+                        }
+                        mx = fmaxf(ptx::max3(mx, mp[0], mp[1]), fmaxf(mp[2], mp[3]));
                     }
-                    float mp[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        mp[q] = fmaxf(__uint_as_float(s[q >> 1][(q & 1) * 16]), __uint_as_float(s[q >> 1][(q & 1) * 16 + 1]));
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-#pragma unroll
-                        for (int kk = 2; kk < 16; kk += 2)
-                            mp[q] = ptx::max3(mp[q], __uint_as_float(s[q >> 1][(q & 1) * 16 + kk]),
-                                              __uint_as_float(s[q >> 1][(q & 1) * 16 + kk + 1]));
-                    }
-                    const float mx = ptx::max3(ptx::max3(mp[0], mp[1], mp[2]), ptx::max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
                     const float m_new = fmaxf(m, mx * a.scale_log2);
                     bool rescale = false;
                     if (m == -INFINITY) {
@@ -593,7 +543,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             ptx::tmem_ld16(tO + c * 16, o);
                             ptx::tmem_wait_ld16(o);
 #pragma unroll
-                            for (int kk = 0; kk < 16; ++kk) o[kk] = __float_as_uint(__uint_as_float(o[kk]) * f);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                             ptx::tmem_st16(tO + c * 16, o);
                         }
                         if (rescale) {
@@ -602,45 +552,65 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                         }
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
-                    if ((tm.odd[0] | tm.odd[1] | tm.odd[2] | tm.odd[3]) != 0) {
+                    if (rest >= 0 && (tm.odd[0] | tm.odd[1] | tm.odd[2] | tm.odd[3]) != 0) {
                         // what the producers took out of V, for the rows that see it: the sums of
-                        // infinities and NaN go to this row of the CTA's partial until the output
+                        // infinities and NaN wait in this row of the CTA's partial for the output
                         float *const sum = part + static_cast<int64_t>(in) * HD;
 #pragma unroll 1
                         for (int col = 0; col < BN; ++col) {
                             if (!((tm.odd[col >> 5] >> (col & 31)) & 1u)) continue;
                             __syncwarp();
-                            uint32_t sc;  // the raw score is still in tensor memory
+                            uint32_t sc;
                             asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(sc) : "r"(tS + col));
-                            if (!live || !sees_key(tm, col)) continue;
+                            if (!live || !((mask_of(col >> 5) >> (col & 31)) & 1u)) continue;
                             const float p = ptx::ex2(fmaf(__uint_as_float(sc), a.scale_log2, -mu));
+                            const Key key = find_key(a, it.k, it.b, it.kv, rest * BN + col);
+                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(key.core ? a.Vc : a.V) + key.row * HD;
                             for (int e = 0; e < HD; ++e) {
-                                const float f = __bfloat162float(tm.v[col][e]);
+                                const float f = __bfloat162float(v[e]);
                                 const float before = has_odd ? sum[e] : 0.f;
                                 sum[e] = f - f != 0.f ? before + p * f : before;
                             }
                             has_odd = true;
                         }
+                        __syncwarp();
                     }
                     // p = 2^(s*scale - mu), two columns per packed FMA; P rounds to bf16, the sum does not
                     const uint64_t sc2 = ptx::f2(a.scale_log2, a.scale_log2);
                     const uint64_t nm2 = ptx::f2(-mu, -mu);
                     uint64_t lp[2] = {0, 0};
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t s[2][32];
+                        ptx::tmem_ld32(tS + c * 64, s[0]);
+                        ptx::tmem_ld32(tS + c * 64 + 32, s[1]);
+                        ptx::tmem_wait_ld(s[0]);
+                        ptx::reg_touch(s[1]);
+                        if (masked) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t pk[8];
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t see = mask_of(2 * c + i);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const int col = (c & 1) * 16 + 2 * kk;
-                            const uint64_t x2 = ptx::fma2(ptx::f2(__uint_as_float(s[c >> 1][col]), __uint_as_float(s[c >> 1][col + 1])), sc2, nm2);
-                            float y0, y1;
-                            ptx::f2_split(x2, y0, y1);
-                            const float p0 = ptx::ex2(y0);
-                            const float p1 = ptx::ex2(y1);
-                            lp[kk & 1] = ptx::add2(lp[kk & 1], ptx::f2(p0, p1));
-                            pk[kk] = ptx::pack_bf16x2(p0, p1);
+                                for (int k = 0; k < 32; ++k)
+                                    if (!((see >> k) & 1u)) s[i][k] = __float_as_uint(-INFINITY);
+                            }
                         }
-                        ptx::tmem_st8(tS + c * 8, pk);  // P over the consumed scores
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t pk[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int col = (q & 1) * 16 + 2 * k;
+                                const uint64_t x2 = ptx::fma2(ptx::f2(__uint_as_float(s[q >> 1][col]), __uint_as_float(s[q >> 1][col + 1])), sc2, nm2);
+                                float y0, y1;
+                                ptx::f2_split(x2, y0, y1);
+                                const float p0 = ptx::ex2(y0);
+                                const float p1 = ptx::ex2(y1);
+                                lp[k & 1] = ptx::add2(lp[k & 1], ptx::f2(p0, p1));
+                                pk[k] = ptx::pack_bf16x2(p0, p1);
+                            }
+                            ptx::tmem_st8(tS + c * 32 + q * 8, pk);  // P over scores that have been read
+                        }
                     }
                     float a0, a1, b0, b1;
                     ptx::f2_split(lp[0], a0, a1);
@@ -660,15 +630,10 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 if (lane == 0) ptx::mbar_arrive(bar(L::B_PFULL + h));
             }
             if (!ok) break;
-            // the next list's queries, while the last product runs
-            const Item old = it;
+            if (end < x1) hand_q();  // the next list's
+            read_nodes();            // (a part of a list may end before its rest)
             const bool empty = cores < 0;
-            if (end < x1) {
-                next_item(a, it);
-                begin_list();
-            }
-            const uint32_t done_parity = HALVES == 2 ? seg & 1 : (n_s & 1) ^ 1;
-            if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_PVDONE + h), done_parity, abort_flag, lim))) {
+            if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_PVDONE + h), HALVES == 2 ? seg & 1 : (n_s & 1) ^ 1, abort_flag, lim))) {
                 ok = false;
                 break;
             }
@@ -681,7 +646,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                     ptx::tmem_ld16(tO + c * 16, v);
                     ptx::tmem_wait_ld16(v);
 #pragma unroll
-                    for (int kk = 0; kk < 16; ++kk) v[kk] = __float_as_uint(__uint_as_float(v[kk]) + (has_odd ? sum[c * 16 + kk] : 0.f));
+                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + (has_odd ? sum[c * 16 + k] : 0.f));
                     ptx::tmem_st16(tO + c * 16, v);
                 }
                 ptx::tmem_wait_st();
@@ -691,9 +656,9 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 l = 0.f;
             }
             const bool nothing = l == 0.f;  // no visible key in this part (or an empty node)
-            const bool whole = x0 <= old.first && old.first + old.k.tiles <= x1;
+            const bool whole = x0 <= it.first && it.first + it.k.tiles <= x1;
             const float scale = nothing ? 0.f : whole ? 1.f / l : 1.f;
-            const int64_t out = (static_cast<int64_t>(old.b) * a.Hq + static_cast<int64_t>(old.kv) * (a.Hq / a.Hkv)) * a.T + row;
+            const int64_t out = list_row() + row;
             if (!idle) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -715,9 +680,12 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             dst[q] = make_uint4(v[0], v[1], v[2], v[3]);
                         }
                     } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(part + static_cast<int64_t>(in) * HD + c * 32);
+                        float *dst = part + static_cast<int64_t>(in) * HD + c * 32;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t v[8] = {o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3], o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]};
+                            ptx::st_global_v8(dst + 8 * q, v);
+                        }
                     }
                 }
             }
@@ -734,8 +702,9 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             }
             ++seg;
             x = end;
-            if (x < x1) begin_tree();
+            if (x < x1) next_item(a, it);
         }
+        cp_wait<0>();
     }
 
     ptx::tc_fence_before();
@@ -761,7 +730,7 @@ cudaError_t launch_halves(const CUtensorMap (&map)[4], const TreeArgs &a, unsign
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.groups) * a.n_mt);
     cfg.blockDim = dim3(Layout<HALVES>::THREADS);
-    cfg.dynamicSmemBytes = Layout<HALVES>::bytes(a.B, a.T);
+    cfg.dynamicSmemBytes = Layout<HALVES>::bytes(a.T);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -34,7 +34,7 @@ class Model:
         n = self.NS
         self.full, self.empty = [Bar(4) for _ in range(n)], [Bar(1) for _ in range(n)]
         self.qfull, self.ofree = [Bar(1) for _ in range(halves)], [Bar(1) for _ in range(halves)]
-        self.sfull, self.pfull = [Bar(1), Bar(1)], [Bar(1) for _ in range(halves)]
+        self.sfull, self.pfull = [Bar(2), Bar(2)], [Bar(1) for _ in range(halves)]
         self.pvdone = [Bar(1) for _ in range(halves)]
         self.slot = [None] * n               # (what, tile) that has landed
         self.meta = [None] * 4
@@ -51,42 +51,37 @@ class Model:
             x += n
 
     def producer(self, w):
-        total, NS, pending = sum(self.segs), self.NS, None
+        total, NS, held = sum(self.segs), self.NS, None
 
         def land(p):
-            ks, vs, x = p
+            slot, what = p
             if w == 0:
-                self.slot[ks], self.slot[vs] = ("K", x), ("V", x)
-            self.full[ks].arrive()
-            self.full[vs].arrive()
+                self.slot[slot] = what
+            self.full[slot].arrive()
 
-        for x in range(total):
-            u = 2 * x
-            ks, vs = u % NS, (u + 1) % NS
-            ready = lambda: self.empty[ks].done((u // NS & 1) ^ 1) and self.empty[vs].done(((u + 1) // NS & 1) ^ 1)  # noqa: E731,B023
-            if pending is not None and not ready():
+        for u in range(2 * total):
+            x, slot = u >> 1, u % NS
+            what, runs = ("V" if u & 1 else "K", x), x in self.run_tiles
+            ready = lambda: self.empty[slot].done((u // NS & 1) ^ 1)  # noqa: E731,B023
+            if held is not None and (runs or not ready()):
                 yield None
-                land(pending)
-                pending = None
+                land(held)
+                held = None
             yield ready
-            if x in self.run_tiles and pending is not None:
-                yield None
-                land(pending)
-                pending = None
             if w == 0:
-                for sl in (ks, vs):
-                    self.slot[sl] = "loading"
-                self.meta[x & 3] = x
+                self.slot[slot] = "loading"
+                if not u & 1:
+                    self.meta[x & 3] = x
             yield None
-            if x in self.run_tiles:
-                self.flying.append(lambda p=(ks, vs, x): land(p))
+            if runs:
+                self.flying.append(lambda p=(slot, what): land(p))
                 continue
-            if pending is not None:
-                land(pending)
-            pending = (ks, vs, x)
-        if pending is not None:
+            if held is not None:
+                land(held)
+            held = (slot, what)
+        if held is not None:
             yield None
-            land(pending)
+            land(held)
         self.loaders -= 1
 
     def tma(self, rng):
@@ -134,6 +129,7 @@ class Model:
                     yield lambda: self.full[u % NS].done(u // NS)  # noqa: B023
                     self.issue("S", h, x0, h, u % NS, seg)
                     self.issue("commit", self.sfull[h])
+                    self.sfull[h].arrive()
                 self.issue("commit", self.empty[u % NS])
                 for t in range(x0, end):
                     v = 2 * t + 1
@@ -150,6 +146,7 @@ class Model:
                             yield lambda: self.full[(v + 1) % NS].done((v + 1) // NS)  # noqa: B023
                             self.issue("S", h, t + 1, h, (v + 1) % NS, seg)
                             self.issue("commit", self.sfull[h])
+                            self.sfull[h].arrive()
                         else:
                             self.issue("commit", self.pvdone[h])
                     self.issue("commit", self.empty[v % NS])
@@ -157,25 +154,24 @@ class Model:
                         self.issue("commit", self.empty[(v + 1) % NS])
                     pcount += 1
             else:
-                def scores(t):
-                    u = 2 * t
-                    yield lambda: self.full[u % NS].done(u // NS)
-                    self.issue("S", 0, t, t & 1, u % NS, seg)  # noqa: B023
-                    self.issue("commit", self.sfull[t & 1])
-                    self.issue("commit", self.empty[u % NS])
-
                 yield lambda: self.qfull[0].done(seg)  # noqa: B023
-                yield from scores(x0)
-                for t in range(x0, end):
-                    if t + 1 < end:
-                        yield from scores(t + 1)
-                    v = 2 * t + 1
+                for t in range(x0, end + 1):
+                    if t < end:
+                        u = 2 * t
+                        yield lambda: self.full[u % NS].done(u // NS)  # noqa: B023
+                        self.issue("S", 0, t, t & 1, u % NS, seg)
+                        self.issue("commit", self.sfull[t & 1])
+                        self.sfull[t & 1].arrive()
+                        self.issue("commit", self.empty[u % NS])
+                    if t == x0:
+                        continue
+                    v = 2 * (t - 1) + 1
                     yield lambda: self.full[v % NS].done(v // NS)  # noqa: B023
                     yield lambda: self.pfull[0].done(pcount)  # noqa: B023
-                    if t == x0:
+                    if t - 1 == x0:
                         yield lambda: self.ofree[0].done(seg + 1)  # noqa: B023
                         self.issue_first(0)
-                    self.issue("PV", 0, t, t & 1, v % NS, t == x0)
+                    self.issue("PV", 0, t - 1, (t - 1) & 1, v % NS, t - 1 == x0)
                     self.issue("commit", self.pvdone[0])
                     self.issue("commit", self.empty[v % NS])
                     pcount += 1
@@ -196,8 +192,12 @@ class Model:
                 buf = h if self.H == 2 else t & 1
                 v = 2 * t + 1
                 yield lambda: self.sfull[buf].done(n_s if self.H == 2 else n_s >> 1)  # noqa: B023
-                yield lambda: self.full[v % NS].done(v // NS)  # noqa: B023
+                if t not in self.run_tiles:
+                    yield lambda: self.full[v % NS].done(v // NS)  # noqa: B023
+                    assert self.slot[v % NS] == ("V", t)
                 assert self.s[buf] == ("S", h, t) and self.meta[t & 3] == t
+                if t + 1 == end and seg + 1 < len(segs):
+                    self.q[h] = seg + 1      # the next list's queries, handed over after this tile
                 yield None
                 if self.H == 1 and n_s > 0 and t > x0 and random.random() < 0.5:   # a rescale of O
                     yield lambda: self.pvdone[0].done(n_s + 1)  # noqa: B023
@@ -212,7 +212,6 @@ class Model:
                 n_s += 1
                 yield None
             if seg + 1 < len(segs):
-                self.q[h] = seg + 1
                 self.qfull[h].arrive()
             yield lambda: self.pvdone[h].done(seg if self.H == 2 else n_s + 1)  # noqa: B023
             assert self.o[h] == end - 1
