@@ -431,9 +431,9 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
                     for (int n = 0; n < DT; ++n) dst[n * 4] = ptx::pack_bf16x2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
                     if ((lane & 3) == 0) a.LSE[out0 + row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
                 } else {
-                    float2 *dst = reinterpret_cast<float2 *>(part + static_cast<int64_t>(in) * D) + (lane & 3);
 #pragma unroll
-                    for (int n = 0; n < DT; ++n) dst[n * 4] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+                    for (int n = 0; n < DT; ++n)
+                        *reinterpret_cast<float2 *>(part + part_col(BM, in, n * 8 + (lane & 3) * 2)) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
                     if ((lane & 3) == 0) {
                         part[BM * D + in] = m[i];
                         part[BM * D + BM + in] = l[i];
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
                     static_cast<float *>(a.O)[(out0 + row) * D + col] = l == 0.f ? 0.f : acc / l;
                     if (col == 0) a.LSE[out0 + row] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
                 } else {
-                    part[static_cast<int64_t>(in) * D + col] = acc;
+                    part[part_col(BM, in, col)] = acc;
                     if (col == 0) {
                         part[BM * D + in] = mx;
                         part[BM * D + BM + in] = l;
@@ -625,60 +625,83 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
 
 // ---------------------------------------------------------------- joining the partials
 
-constexpr int JOIN_WARPS = 4;
+constexpr int JOIN_ROWS = 32;
 
-// A warp joins one row of one list: the groups that wrote a part of it, in order.  Lists
-// that one group finished are already written.
+// A block joins up to 32 rows of one list, a quarter of the columns per warp.  A lane takes a
+// row; where there are fewer rows, the lanes left over take parts: lane group i the parts i,
+// i + groups, .. of the list, in the order of the groups that wrote them, and the lane groups
+// are added up in a fixed order.  Lists that one group finished are already written.
 template <typename T, int D>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const TreeArgs a, int BM) {
-    constexpr int C = D / 32;  // columns of a lane
+__global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM) {
+    constexpr int C = D / 16;  // float4 columns of a warp
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / a.Hkv, kv = blockIdx.x - b * a.Hkv;
-    const int row = blockIdx.y * JOIN_WARPS + warp;
+    int lanes = 32;  // a power of two that holds the rows
+    while (lanes / 2 >= a.R) lanes /= 2;
+    const int row = blockIdx.y * JOIN_ROWS + (lane & (lanes - 1)), step = 32 / lanes;
     const int f0 = a.firsts[b], f1 = a.firsts[b + 1], all = a.firsts[a.B];
     const Split split = make_split(a, all);
     const int tiles = (f1 - f0) / a.Hkv;
     const int s = f0 + kv * tiles, e = s + tiles;
     const int y0 = split.owner(s), y1 = split.owner(e - 1);
-    if (y0 == y1 || row >= a.R) return;
-    const int mt = row / BM, in = row - mt * BM;
+    if (y0 == y1) return;
+    const bool live = row < a.R;
+    const int mt = live ? row / BM : 0, in = live ? row - mt * BM : 0;
     auto part = [&](int y) { return static_cast<const float *>(part_at(a, y, mt, split.begin(y) >= s ? 0 : 1, BM, D)); };
     float mx = -INFINITY;
-    for (int y = y0 + lane; y <= y1; y += 32) {
-        mx = fmaxf(mx, part(y)[BM * D + in]);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float acc[C], l = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = 0.f;
-    for (int yb = y0; yb <= y1; yb += 32) {
-        const float *p = yb + lane <= y1 ? part(yb + lane) : nullptr;
-        const float f = p == nullptr ? 0.f : exp2f(p[BM * D + in] - base);
-        if (p != nullptr) l += p[BM * D + BM + in] * f;
-        const int n = min(32, y1 - yb + 1);
 #pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float w = __shfl_sync(kFull, f, k);
-            const float *q = reinterpret_cast<const float *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(p), k));
-            if (q == nullptr) continue;
-            q += static_cast<int64_t>(in) * D + lane * C;
+    for (int y = y0 + lane / lanes; y <= y1; y += step) mx = fmaxf(mx, part(y)[BM * D + in]);
+    for (int off = 16; off >= lanes; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float4 acc[C];
+    float l = 0.f;
 #pragma unroll
-            for (int c = 0; c < C; ++c) acc[c] = fmaf(q[c], w, acc[c]);
+    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int y = y0 + lane / lanes; y <= y1; y += step) {
+        const float *p = part(y);
+        const float4 *q = reinterpret_cast<const float4 *>(p) + warp * C * BM + in;
+        const float f = exp2f(p[BM * D + in] - base);
+        l += p[BM * D + BM + in] * f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float4 v = q[c * BM];
+            acc[c].x = fmaf(v.x, f, acc[c].x);
+            acc[c].y = fmaf(v.y, f, acc[c].y);
+            acc[c].z = fmaf(v.z, f, acc[c].z);
+            acc[c].w = fmaf(v.w, f, acc[c].w);
         }
     }
+    for (int off = 16; off >= lanes; off >>= 1) {
+        l += __shfl_xor_sync(kFull, l, off);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
-    const int64_t at = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kv) * (a.Hq / a.Hkv)) * a.T + row;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const float v = l == 0.f ? 0.f : acc[c] / l;
-        if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16 *>(a.O)[at * D + lane * C + c] = __float2bfloat16_rn(v);
-        else static_cast<float *>(a.O)[at * D + lane * C + c] = v;
+        for (int c = 0; c < C; ++c) {
+            acc[c].x += __shfl_xor_sync(kFull, acc[c].x, off);
+            acc[c].y += __shfl_xor_sync(kFull, acc[c].y, off);
+            acc[c].z += __shfl_xor_sync(kFull, acc[c].z, off);
+            acc[c].w += __shfl_xor_sync(kFull, acc[c].w, off);
+        }
     }
-    if (lane == 0) a.LSE[at] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
+    if (!live || lane >= lanes) return;
+    const int64_t at = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kv) * (a.Hq / a.Hkv)) * a.T + row;
+    const bool none = l == 0.f;
+#pragma unroll
+    for (int c = 0; c < C; c += 2) {
+        float v[8] = {acc[c].x, acc[c].y, acc[c].z, acc[c].w, acc[c + 1].x, acc[c + 1].y, acc[c + 1].z, acc[c + 1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = none ? 0.f : v[i] / l;
+        const int col = (warp * C + c) * 4;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.O) + at * D + col) =
+                make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]), ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.O) + at * D + col);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    if (warp == 0) a.LSE[at] = none ? -INFINITY : (mx + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- launch
@@ -745,13 +768,13 @@ uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
     const int64_t n_mt = (R + BM - 1) / BM;
     int64_t ctas = static_cast<int64_t>(sms) * MAX_CTAS_PER_SM;
     if (ctas < n_mt) ctas = n_mt;
-    return WS_HEAD + 32 + static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
+    return WS_HEAD + static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
 }
 
 template <typename J>
 cudaError_t run_join(J join, const TreeArgs &a, int BM, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_WARPS - 1) / JOIN_WARPS);
-    return start(join, grid, JOIN_WARPS * 32, 0, stream, a, BM);
+    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_ROWS - 1) / JOIN_ROWS);
+    return start(join, grid, 128, 0, stream, a, BM);
 }
 
 template <auto kernel, typename J>
@@ -798,7 +821,7 @@ int check_tree(const cca_params_t *p, int T) {
     if (st != CCA_OK) return st;
     if (T < 1 || p->B > 0x7fffffff / p->Hkv) return CCA_ERR_INVALID_ARG;
     if (T > TREE_MAX_NODES || T > p->w || p->B > TREE_MAX_BATCH) return CCA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(p->Hq / p->Hkv) * T > 4 * 65535) return CCA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(p->Hq / p->Hkv) * T > JOIN_ROWS * 65535) return CCA_ERR_UNSUPPORTED;
     return CCA_OK;
 }
 
@@ -874,8 +897,7 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.O = O;
     a.LSE = LSE;
     a.firsts = static_cast<int *>(workspace);
-    // partials are written 32 bytes at a time
-    a.ws = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(workspace) + WS_HEAD + 31) & ~uintptr_t{31});
+    a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + WS_HEAD);
     a.status = params->dev_status;
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
     if (params->dtype == CCA_BF16)

@@ -312,8 +312,11 @@ __device__ __forceinline__ bool row_sees(const Nodes &n, int t, int kind, int va
     return false;
 }
 
-// Partials of a (group, row tile, slot): O [BM][D], max [BM], sum [BM] (log2 domain).
+// Partials of a (group, row tile, slot): O as [D / 4][BM][4], so that the rows of a warp lie
+// side by side for those who write and read a row per lane; then max [BM] and sum [BM] (log2
+// domain).
 __host__ __device__ __forceinline__ int64_t part_floats(int BM, int D) { return static_cast<int64_t>(BM) * (D + 2); }
+__device__ __forceinline__ int part_col(int BM, int row, int col) { return (col >> 2) * BM * 4 + row * 4 + (col & 3); }
 
 // Slot 0: the list that the group's run begins in; 1: the one it ends in.
 __device__ __forceinline__ float *part_at(const TreeArgs &a, int group, int mt, int slot, int BM, int D) {

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(L::B_QFULL + h));
         };
-        // The list's tree, when it is first needed: parents in shared memory, each row walks its own chain.
+        // The list's tree: parents in shared memory, each row walks its own chain.
         auto read_nodes = [&]() {
             if (it.b == tree_of) return;
             tree_of = it.b;
@@ -452,6 +452,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         if (x0 < x1) {
             load_q();
             hand_q();
+            read_nodes();  // while the first scores are under way
         }
         int x = x0;
         while (ok && x < x1) {
@@ -479,7 +480,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 const uint4 gone = *reinterpret_cast<const uint4 *>(tm.gone);
                 const bool masked = rest >= 0 || (gone.x | gone.y | gone.z | gone.w) != 0;
                 if (rest >= 0) {
-                    read_nodes();
                     // V(t)'s slot is not filled again before this softmax is over: what the producers
                     // took out of it is known now
                     const int u = 2 * (t - x0) + 1;
@@ -555,7 +555,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                     if (rest >= 0 && (tm.odd[0] | tm.odd[1] | tm.odd[2] | tm.odd[3]) != 0) {
                         // what the producers took out of V, for the rows that see it: the sums of
                         // infinities and NaN wait in this row of the CTA's partial for the output
-                        float *const sum = part + static_cast<int64_t>(in) * HD;
 #pragma unroll 1
                         for (int col = 0; col < BN; ++col) {
                             if (!((tm.odd[col >> 5] >> (col & 31)) & 1u)) continue;
@@ -568,8 +567,9 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(key.core ? a.Vc : a.V) + key.row * HD;
                             for (int e = 0; e < HD; ++e) {
                                 const float f = __bfloat162float(v[e]);
-                                const float before = has_odd ? sum[e] : 0.f;
-                                sum[e] = f - f != 0.f ? before + p * f : before;
+                                float &sum = part[part_col(BM, in, e)];
+                                const float before = has_odd ? sum : 0.f;
+                                sum = f - f != 0.f ? before + p * f : before;
                             }
                             has_odd = true;
                         }
@@ -631,7 +631,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             }
             if (!ok) break;
             if (end < x1) hand_q();  // the next list's
-            read_nodes();            // (a part of a list may end before its rest)
             const bool empty = cores < 0;
             if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_PVDONE + h), HALVES == 2 ? seg & 1 : (n_s & 1) ^ 1, abort_flag, lim))) {
                 ok = false;
@@ -639,14 +638,13 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             }
             ptx::tc_fence_after();
             if (__any_sync(kFull, has_odd)) {
-                const float *const sum = part + static_cast<int64_t>(in) * HD;
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     uint32_t v[16];
                     ptx::tmem_ld16(tO + c * 16, v);
                     ptx::tmem_wait_ld16(v);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + (has_odd ? sum[c * 16 + k] : 0.f));
+                    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + (has_odd ? part[part_col(BM, in, c * 16 + k)] : 0.f));
                     ptx::tmem_st16(tO + c * 16, v);
                 }
                 ptx::tmem_wait_st();
@@ -680,12 +678,9 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             dst[q] = make_uint4(v[0], v[1], v[2], v[3]);
                         }
                     } else {
-                        float *dst = part + static_cast<int64_t>(in) * HD + c * 32;
+                        uint4 *dst = reinterpret_cast<uint4 *>(part + part_col(BM, in, c * 32));
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t v[8] = {o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3], o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]};
-                            ptx::st_global_v8(dst + 8 * q, v);
-                        }
+                        for (int q = 0; q < 8; ++q) dst[q * BM] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                     }
                 }
             }
@@ -702,7 +697,10 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             }
             ++seg;
             x = end;
-            if (x < x1) next_item(a, it);
+            if (x < x1) {
+                next_item(a, it);
+                read_nodes();
+            }
         }
         cp_wait<0>();
     }
