@@ -15,6 +15,14 @@ namespace cca {
 constexpr int TREE_MAX_NODES = 256;
 constexpr int TREE_MAX_BATCH = 1024;
 
+// Division by a number that the host knows: floor(n / d) for 0 <= n < 2^31 and d < 2^31 is the
+// high half of 4n * ceil(2^62 / d), as n * d < 2^62 keeps the rounding of the factor below 1/d.
+struct FastDiv {
+    uint64_t m;
+    __device__ __forceinline__ int div(int n) const { return static_cast<int>(__umul64hi(static_cast<uint64_t>(n) << 2, m)); }
+};
+inline FastDiv fast_div(int d) { return FastDiv{((uint64_t{1} << 62) + d - 1) / d}; }
+
 // A pool and its table as the ABI wants them (layers 0: any number).
 inline bool pages_ok(const cca_pages_t *p, int layers) {
     if (p == nullptr || p->K == nullptr || p->V == nullptr || p->table == nullptr) return false;

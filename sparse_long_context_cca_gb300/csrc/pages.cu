@@ -73,36 +73,41 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
         c0 = c1 = 0;
         if (ex <= 0) return true;
         const int64_t end = static_cast<int64_t>(len) + ex;
-        if (len < 0 || (end + a.rows - 1) / a.rows > a.cols) return false;
+        if (len < 0 || end > static_cast<int64_t>(a.cols) * a.rows) return false;
         c0 = len / a.rows;
         c1 = static_cast<int>((end + a.rows - 1) / a.rows);
         return true;
     };
+    // Whether row o's range takes in column c.
+    auto reaches = [&](int o, int c) {
+        const int len = a.lens[o], ex = a.extra[o];
+        const int64_t end = static_cast<int64_t>(len) + ex, at = static_cast<int64_t>(c) * a.rows;
+        return ex > 0 && len >= 0 && end <= static_cast<int64_t>(a.cols) * a.rows && at + a.rows > len && at < end;
+    };
     // 1. which entries need a page: empty ones, and shared ones but for the page's last
     // holder.  A page's holders stand in the same column (rows are positions), so the rows
-    // above that leave it are counted down one column.
+    // above that leave it are counted down one column, 32 rows at a time.
     for (int b = warp; b < a.B; b += RESERVE_WARPS) {
         int c0, c1, n = 0;
         if (!range(b, c0, c1) && lane == 0) report(a.status, CCA_ERR_INVALID_ARG);
         for (int base = c0; base < c1; base += 32) {
             const int c = base + lane;
-            bool need = false;
+            int32_t e = -1;
+            int held = 0;
             if (c < c1) {
-                const int32_t e = a.table[static_cast<int64_t>(b) * a.cols + c];
-                if (e < 0 || e >= a.n_pages) {
-                    need = true;
-                } else {
-                    const int held = a.refs[e];
-                    if (held > 1) {
-                        int left = 0;
-                        for (int o = 0; o < b; ++o) {
-                            int o0, o1;
-                            range(o, o0, o1);
-                            if (c >= o0 && c < o1 && a.table[static_cast<int64_t>(o) * a.cols + c] == e) ++left;
-                        }
-                        need = held - left > 1;
-                    }
-                }
+                e = a.table[static_cast<int64_t>(b) * a.cols + c];
+                if (e >= a.n_pages) e = -1;
+                if (e >= 0) held = a.refs[e];
+            }
+            bool need = c < c1 && e < 0;
+            for (unsigned shared = __ballot_sync(kFull, held > 1); shared != 0; shared &= shared - 1) {
+                const int src = __ffs(shared) - 1;
+                const int32_t es = __shfl_sync(kFull, e, src);
+                int left = 0;
+                for (int o = lane; o < b; o += 32)
+                    if (a.table[static_cast<int64_t>(o) * a.cols + base + src] == es && reaches(o, base + src)) ++left;
+                left = __reduce_add_sync(kFull, left);
+                if (lane == src) need = held - left > 1;
             }
             const unsigned m = __ballot_sync(kFull, need);
             if (need) a.want[static_cast<int64_t>(b) * a.cols + n + __popc(m & ((1u << lane) - 1u))] = c;

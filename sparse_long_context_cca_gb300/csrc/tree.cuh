@@ -13,14 +13,6 @@ namespace tree {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Division by a number that the host knows: floor(n / d) for 0 <= n < 2^31 and d < 2^31 is the
-// high half of 4n * ceil(2^62 / d), as n * d < 2^62 keeps the rounding of the factor below 1/d.
-struct FastDiv {
-    uint64_t m;
-    __device__ __forceinline__ int div(int n) const { return static_cast<int>(__umul64hi(static_cast<uint64_t>(n) << 2, m)); }
-};
-inline FastDiv fast_div(int d) { return FastDiv{((uint64_t{1} << 62) + d - 1) / d}; }
-
 struct TreeArgs {
     const void *Q, *K, *V, *Kc, *Vc;
     const int32_t *table, *ctable, *lens, *parents;
