@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wm = warp % WM, wk = warp / WM;
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    find_run(a, group, st, blockIdx.x == 0);
+    find_run(a, group, st);
     const int x0 = st.x0, x1 = st.x1;
     if (x0 >= x1) return;
 
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    find_run(a, group, st, blockIdx.x == 0);
+    find_run(a, group, st);
     const int x0 = st.x0, x1 = st.x1;
     if (x0 >= x1) return;
     Item it = st.item;
@@ -634,17 +634,34 @@ constexpr int JOIN_ROWS = 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM) {
     constexpr int C = D / 16;  // float4 columns of a warp
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ int sm_sum[2][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / a.Hkv, kv = blockIdx.x - b * a.Hkv;
     int lanes = 32;  // a power of two that holds the rows
     while (lanes / 2 >= a.R) lanes /= 2;
     const int row = blockIdx.y * JOIN_ROWS + (lane & (lanes - 1)), step = 32 / lanes;
-    const int f0 = a.firsts[b], f1 = a.firsts[b + 1], all = a.firsts[a.B];
+    // Where the list lies among all follows from the lengths, which the kernel before has waited
+    // for, so it is found while that one still runs.
+    int all = 0, f0 = 0;
+    for (int i = threadIdx.x; i < a.B; i += 128) {
+        const int n = key_list(a, i).tiles * a.Hkv;
+        all += n;
+        if (i < b) f0 += n;
+    }
+    all = __reduce_add_sync(kFull, all);
+    f0 = __reduce_add_sync(kFull, f0);
+    if (lane == 0) {
+        sm_sum[0][warp] = all;
+        sm_sum[1][warp] = f0;
+    }
+    __syncthreads();
+    all = sm_sum[0][0] + sm_sum[0][1] + sm_sum[0][2] + sm_sum[0][3];
+    f0 = sm_sum[1][0] + sm_sum[1][1] + sm_sum[1][2] + sm_sum[1][3];
     const Split split = make_split(a, all);
-    const int tiles = (f1 - f0) / a.Hkv;
+    const int tiles = key_list(a, b).tiles;
     const int s = f0 + kv * tiles, e = s + tiles;
     const int y0 = split.owner(s), y1 = split.owner(e - 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (y0 == y1) return;
     const bool live = row < a.R;
     const int mt = live ? row / BM : 0, in = live ? row - mt * BM : 0;
@@ -749,8 +766,9 @@ cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t strea
 
 constexpr int MAX_CTAS_PER_SM = 4;
 
-// R > 16 query rows per KV head go to the tensor-core kernel.
-bool on_tensor_cores(int dtype, int R, int d) { return dtype == CCA_BF16 && d == 128 && R > 16; }
+// bf16 with d = 128 runs on the tensor cores, whatever the rows (one row: 29.4 us against 31.6 us by
+// mma.sync for 32 heads at 32 K; 64 sequences of 8 K: 264 us against 274 us).
+bool on_tensor_cores(int dtype, int R, int d) { return dtype == CCA_BF16 && d == 128; }
 
 // Rows per CTA: 16 rows of a warp each, so that as few row tiles as possible read the keys.
 int rows_per_cta(int dtype, int R, int d) {
@@ -759,16 +777,13 @@ int rows_per_cta(int dtype, int R, int d) {
     return R <= 16 ? 16 : R <= 32 ? 32 : 64;
 }
 
-constexpr uint64_t WS_HEAD = 8192;  // the lists' first tiles
-static_assert(WS_HEAD >= 4 * (TREE_MAX_BATCH + 1), "room for the first tiles");
-
 uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
     // CTAs times two slots; a grid holds at most MAX_CTAS_PER_SM per SM, and one group of row tiles at least
     const int BM = rows_per_cta(dtype, R, d);
     const int64_t n_mt = (R + BM - 1) / BM;
     int64_t ctas = static_cast<int64_t>(sms) * MAX_CTAS_PER_SM;
     if (ctas < n_mt) ctas = n_mt;
-    return WS_HEAD + static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
+    return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
 }
 
 template <typename J>
@@ -896,8 +911,7 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.scale_log2 = resolve_scale(params) * 1.4426950408889634f;
     a.O = O;
     a.LSE = LSE;
-    a.firsts = static_cast<int *>(workspace);
-    a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + WS_HEAD);
+    a.ws = static_cast<float *>(workspace);
     a.status = params->dev_status;
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
     if (params->dtype == CCA_BF16)

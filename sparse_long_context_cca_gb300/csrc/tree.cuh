@@ -28,8 +28,7 @@ struct TreeArgs {
     float scale_log2;
     void *O;
     float *LSE;
-    int *firsts;  // workspace: first tile of every sequence's lists and of none, [B + 1]
-    float *ws;    // workspace: partials
+    float *ws;  // partials
     int32_t *status;
 };
 
@@ -184,8 +183,7 @@ struct Start {
 
 // Lengths to tiles to runs: every CTA adds up the tiles of all lists for itself (thread per
 // sequence), and the thread that owns the sequence its run begins in leaves that list behind.
-// The lists' first tiles go to the workspace for the joining kernel, from one CTA.
-__device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st, bool publish) {
+__device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
     const int per = (a.B + nt - 1) / nt;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -210,8 +208,8 @@ __device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st
         total += st.warp_sum[i];
     }
     const Split s = make_split(a, total);
-    if (group < s.groups || publish) {
-        const int x0 = group < s.groups ? s.begin(group) : -1;
+    if (group < s.groups) {
+        const int x0 = s.begin(group);
         for (int b = b0; b < b1; ++b) {
             if (per > 1) k = key_list(a, b);
             const int tiles = k.tiles * a.Hkv;
@@ -223,10 +221,8 @@ __device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st
                 st.x0 = x0;
                 st.x1 = s.begin(group + 1);
             }
-            if (publish) a.firsts[b] = before;
             before += tiles;
         }
-        if (publish && tid == 0) a.firsts[a.B] = total;
     }
     __syncthreads();
 }

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     ptx::tc_fence_before();
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    find_run(a, group, st, blockIdx.x == 0);  // holds barriers
+    find_run(a, group, st);  // holds barriers
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(gbase + L::OFF_TMEMPTR);
     const int x0 = st.x0, x1 = st.x1;
