@@ -627,13 +627,14 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
 
 constexpr int JOIN_ROWS = 32;
 
-// A block joins up to 32 rows of one list, a quarter of the columns per warp.  A lane takes a
+// A block joins up to 32 rows and a quarter of the columns of one list, a quarter of those per
+// warp (many blocks with few loads each: the time is that of the chain of reads).  A lane takes a
 // row; where there are fewer rows, the lanes left over take parts: lane group i the parts i,
 // i + groups, .. of the list, in the order of the groups that wrote them, and the lane groups
 // are added up in a fixed order.  Lists that one group finished are already written.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM) {
-    constexpr int C = D / 16;  // float4 columns of a warp
+    constexpr int C = D / 64;  // float4 columns of a warp
     __shared__ int sm_sum[2][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / a.Hkv, kv = blockIdx.x - b * a.Hkv;
@@ -666,6 +667,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM
     const bool live = row < a.R;
     const int mt = live ? row / BM : 0, in = live ? row - mt * BM : 0;
     auto part = [&](int y) { return static_cast<const float *>(part_at(a, y, mt, split.begin(y) >= s ? 0 : 1, BM, D)); };
+    const int col0 = (blockIdx.z * 4 + warp) * C;  // in float4
     float mx = -INFINITY;
 #pragma unroll 4
     for (int y = y0 + lane / lanes; y <= y1; y += step) mx = fmaxf(mx, part(y)[BM * D + in]);
@@ -675,10 +677,10 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM
     float l = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int y = y0 + lane / lanes; y <= y1; y += step) {
         const float *p = part(y);
-        const float4 *q = reinterpret_cast<const float4 *>(p) + warp * C * BM + in;
+        const float4 *q = reinterpret_cast<const float4 *>(p) + col0 * BM + in;
         const float f = exp2f(p[BM * D + in] - base);
         l += p[BM * D + BM + in] * f;
 #pragma unroll
@@ -704,21 +706,16 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM
     const int64_t at = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kv) * (a.Hq / a.Hkv)) * a.T + row;
     const bool none = l == 0.f;
 #pragma unroll
-    for (int c = 0; c < C; c += 2) {
-        float v[8] = {acc[c].x, acc[c].y, acc[c].z, acc[c].w, acc[c + 1].x, acc[c + 1].y, acc[c + 1].z, acc[c + 1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = none ? 0.f : v[i] / l;
-        const int col = (warp * C + c) * 4;
+    for (int c = 0; c < C; ++c) {
+        const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc[c].x / l, acc[c].y / l, acc[c].z / l, acc[c].w / l);
+        const int64_t to = at * D + (col0 + c) * 4;
         if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.O) + at * D + col) =
-                make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]), ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.O) + to) = make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
         } else {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.O) + at * D + col);
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.O) + to) = v;
         }
     }
-    if (warp == 0) a.LSE[at] = none ? -INFINITY : (mx + log2f(l)) * kLn2;
+    if (col0 == 0) a.LSE[at] = none ? -INFINITY : (mx + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- launch
@@ -788,7 +785,7 @@ uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
 
 template <typename J>
 cudaError_t run_join(J join, const TreeArgs &a, int BM, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_ROWS - 1) / JOIN_ROWS);
+    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_ROWS - 1) / JOIN_ROWS, 4);
     return start(join, grid, 128, 0, stream, a, BM);
 }
 

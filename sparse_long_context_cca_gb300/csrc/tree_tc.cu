@@ -398,14 +398,15 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         const int node = live ? row % a.T : 0;
         bool ok = true;
         uint32_t seg = 0, n_s = 0;  // lists and tiles of this half so far
-        Item it = st.item;
+        Item it = st.item, nxt = st.item;
         int tree_of = -1;
         int start = 0, cores = -1;  // this row's first raw token; its visible cores, -1: empty node
-        auto list_row = [&]() { return (static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T; };
+        const int heads = a.Hq / a.Hkv;
+        auto list_row = [&](const Item &i) { return (static_cast<int64_t>(i.b) * a.Hq + static_cast<int64_t>(i.kv) * heads) * a.T; };
         // The queries of this warp's rows, 16 lanes to a row, swizzled like the keys.  The scores of
         // the last tile are done, so nothing reads the old ones.
-        auto load_q = [&]() {
-            const char *q = static_cast<const char *>(a.Q) + (list_row() + mt * BM + h * 128 + quarter * 32) * (HD * 2);
+        auto load_q = [&](const Item &i) {
+            const char *q = static_cast<const char *>(a.Q) + (list_row(i) + mt * BM + h * 128 + quarter * 32) * (HD * 2);
             const int sub = lane >> 4, chunk = lane & 15;
 #pragma unroll 4
             for (int j = 0; j < 16; ++j) {
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             return m;
         };
         if (x0 < x1) {
-            load_q();
+            load_q(it);
             hand_q();
             read_nodes();  // while the first scores are under way
         }
@@ -469,10 +470,9 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 }
                 ptx::tc_fence_after();
                 if (t + 1 == end && end < x1) {  // the last tile of this list: its scores have read the queries
-                    const Item now = it;
-                    next_item(a, it);
-                    load_q();
-                    it = now;
+                    nxt = it;
+                    next_item(a, nxt);
+                    load_q(nxt);
                 }
                 const uint32_t tS = tmem + lane_addr + buf * 128;
                 const TileMeta &tm = metas[(t - x0) & (METAS - 1)];
@@ -492,6 +492,21 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                     return (rest >= 0 ? seen(rest * BN + c * 32) : 0xffffffffu) & ~tm.gone[c];
                 };
                 if (!idle) {
+                    // a masked tile: -inf into the scores that the row does not see, where they are
+                    if (masked) {
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t see = mask_of(c >> 1) >> (16 * (c & 1));
+                            uint32_t v[16];
+                            ptx::tmem_ld16(tS + c * 16, v);
+                            ptx::tmem_wait_ld16(v);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                if (!((see >> k) & 1u)) v[k] = __float_as_uint(-INFINITY);
+                            ptx::tmem_st16(tS + c * 16, v);
+                        }
+                        ptx::tmem_wait_st();
+                    }
                     // the row's maximum; 64 columns at a time, which keeps the code short (a launch
                     // begins with cold instruction caches) and the registers few
                     float mx = -INFINITY;
@@ -502,15 +517,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                         ptx::tmem_ld32(tS + c * 64 + 32, s[1]);
                         ptx::tmem_wait_ld(s[0]);
                         ptx::reg_touch(s[1]);
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t see = mask_of(2 * c + i);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!((see >> k) & 1u)) s[i][k] = __float_as_uint(-INFINITY);
-                            }
-                        }
                         float mp[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             __syncwarp();
                             uint32_t sc;
                             asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(sc) : "r"(tS + col));
-                            if (!live || !((mask_of(col >> 5) >> (col & 31)) & 1u)) continue;
+                            if (!live || __uint_as_float(sc) == -INFINITY) continue;
                             const float p = ptx::ex2(fmaf(__uint_as_float(sc), a.scale_log2, -mu));
                             const Key key = find_key(a, it.k, it.b, it.kv, rest * BN + col);
                             const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(key.core ? a.Vc : a.V) + key.row * HD;
@@ -586,15 +592,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                         ptx::tmem_ld32(tS + c * 64 + 32, s[1]);
                         ptx::tmem_wait_ld(s[0]);
                         ptx::reg_touch(s[1]);
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t see = mask_of(2 * c + i);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!((see >> k) & 1u)) s[i][k] = __float_as_uint(-INFINITY);
-                            }
-                        }
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t pk[8];
@@ -656,7 +653,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             const bool nothing = l == 0.f;  // no visible key in this part (or an empty node)
             const bool whole = x0 <= it.first && it.first + it.k.tiles <= x1;
             const float scale = nothing ? 0.f : whole ? 1.f / l : 1.f;
-            const int64_t out = list_row() + row;
+            const int64_t out = list_row(it) + row;
             if (!idle) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -698,7 +695,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             ++seg;
             x = end;
             if (x < x1) {
-                next_item(a, it);
+                it = nxt;
                 read_nodes();
             }
         }
