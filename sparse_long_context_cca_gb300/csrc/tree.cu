@@ -810,7 +810,6 @@ cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
     a.groups = sms / a.n_mt;
     if (a.groups < 1) a.groups = 1;
     a.tile_log2 = 7;
-    a.min_tiles = 1;
     const cudaError_t e = launch_tc(a, g_wait_limit_ns, g_skip_q_load, stream);
     if (e != cudaSuccess) return e;
     return run_join(tree_join_kernel<__nv_bfloat16, 128>, a, BM, stream);
@@ -904,7 +903,6 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.by_crows = fast_div(a.crows);
     a.tile_log2 = 6;
     a.box_log2 = 0;
-    a.min_tiles = 2;
     a.scale_log2 = resolve_scale(params) * 1.4426950408889634f;
     a.O = O;
     a.LSE = LSE;

@@ -23,7 +23,6 @@ struct TreeArgs {
     int tile_log2;  // keys per tile
     int box_log2;   // rows of a box that one copy can bring (0: no runs)
     int groups;  // groups of n_mt CTAs
-    int min_tiles;  // tiles a group takes at least
     FastDiv by_g, by_rows, by_crows;
     float scale_log2;
     void *O;
@@ -160,8 +159,7 @@ struct Split {
 
 __device__ __forceinline__ Split make_split(const TreeArgs &a, int W) {
     Split s;
-    const int most = W / a.min_tiles;
-    s.groups = most < a.groups ? max(most, 1) : a.groups;
+    s.groups = W < a.groups ? W : a.groups;
     s.each = W / s.groups;
     s.more = W - s.each * s.groups;
     return s;
