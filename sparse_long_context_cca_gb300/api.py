@@ -691,7 +691,8 @@ def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half
 
 def _rows_ready(t):
     """t itself where its rows can be read in place, a contiguous copy otherwise."""
-    if t.data_ptr() % 16 == 0 and t.stride(3) == 1 and all(s * t.element_size() % 16 == 0 for s in t.stride()[:3]):
+    s = t.stride()
+    if s[3] == 1 and (s[0] | s[1] | s[2]) * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0:
         return t
     return t.contiguous()
 

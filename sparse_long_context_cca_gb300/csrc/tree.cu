@@ -775,10 +775,11 @@ int rows_per_cta(int dtype, int R, int d) {
 }
 
 uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
-    // CTAs times two slots; a grid holds at most MAX_CTAS_PER_SM per SM, and one group of row tiles at least
+    // CTAs times two slots; a grid holds one CTA per SM on the tensor cores, MAX_CTAS_PER_SM at most
+    // elsewhere, and one group of row tiles at least
     const int BM = rows_per_cta(dtype, R, d);
     const int64_t n_mt = (R + BM - 1) / BM;
-    int64_t ctas = static_cast<int64_t>(sms) * MAX_CTAS_PER_SM;
+    int64_t ctas = static_cast<int64_t>(sms) * (on_tensor_cores(dtype, R, d) ? 1 : MAX_CTAS_PER_SM);
     if (ctas < n_mt) ctas = n_mt;
     return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
 }
