@@ -724,19 +724,33 @@ def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", f
 
 def _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, what: str, layers: bool = False) -> bytes:
     """A pool [pages, Hkv, rows, d] ([layers, pages, ...] where allowed) and its table, packed."""
-    if not isinstance(Kp, torch.Tensor) or Kp.dim() not in ((4, 5) if layers else (4,)):
-        raise ValueError(f"{what} pool must be [{'layers, ' if layers else ''}pages, Hkv, rows, d]")
+    if not isinstance(Kp, torch.Tensor) or not isinstance(Vp, torch.Tensor):
+        raise ValueError(f"{what} pool must be two tensors")
     shape = Kp.shape
-    if Vp is None or shape[-3] != Hkv or shape[-1] != d:
+    if len(shape) != 4 and not (layers and len(shape) == 5):
+        raise ValueError(f"{what} pool must be [{'layers, ' if layers else ''}pages, Hkv, rows, d]")
+    pages, heads, rows, width = shape[-4:]
+    if heads != Hkv or width != d:
         raise ValueError(f"{what} pool has shape {tuple(shape)}, expected [pages, {Hkv}, rows, {d}]")
     cols = ptr = 0
     if table is not None:
-        if not isinstance(table, torch.Tensor) or table.dim() != 2:
-            raise ValueError(f"{what} table must be [B, columns]")
-        cols = table.shape[1]
+        cols = _columns(table, what + " table")
         ptr = _ptr(table, what + " table", _I32, (B, cols), dev)
-    return _pack_pages(_ptr(Kp, what + " K pool", dtype, shape, dev), _ptr(Vp, what + " V pool", dtype, shape, dev), ptr,
-                       shape[-4], shape[-2], cols, shape[0] if len(shape) == 5 else 1)
+    if Kp.dtype is not dtype or Vp.dtype is not dtype or Vp.shape != shape or Kp.get_device() != dev or Vp.get_device() != dev \
+            or not Kp.is_contiguous() or not Vp.is_contiguous():
+        _ptr(Kp, what + " K pool", dtype, shape, dev)
+        _ptr(Vp, what + " V pool", dtype, shape, dev)
+    return _pack_pages(Kp.data_ptr(), Vp.data_ptr(), ptr, pages, rows, cols, shape[0] if len(shape) == 5 else 1)
+
+
+def _workspace(t, need: int, device):
+    """A caller's workspace, or one for this call alone, and its bytes."""
+    if t is None:
+        need = max(need, 16)
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError(f"workspace must be a buffer of at least {need} bytes on {device}")
+    return t, t.numel() * t.element_size()
 
 
 def _heads_of(Kp) -> int:
@@ -807,19 +821,19 @@ def cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g: int, w: int, p
     core = _pool(Kcp, Vcp, core_table, B, Hkv, d, dtype, dev, "core")
     prm = _pack_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype], scale, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0,
                        window_mode, 0)
+    lens, parents = _ptr(lens, "lens", _I32, (B,), dev), _ptr(parents, "parents", _I32, (B, T), dev)
     if O is None:
         O = torch.empty_like(Q)
+        o = O.data_ptr()
+    else:
+        o = _ptr(O, "O", dtype, shape, dev)
     if LSE is None:
         LSE = torch.empty((B, Hq, T), dtype=_F32, device=Q.device)
-    need = lib.cca_tree_workspace_size(prm, T)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=Q.device)
-    nbytes = workspace.numel() * workspace.element_size()
-    if workspace.get_device() != dev or not workspace.is_contiguous() or nbytes < need:
-        raise ValueError(f"workspace must be a buffer of at least {need} bytes on cuda:{dev}")
-    st = lib.cca_tree_fwd(q, raw, core, _ptr(lens, "lens", _I32, (B,), dev), _ptr(parents, "parents", _I32, (B, T), dev), T,
-                          _ptr(O, "O", dtype, shape, dev), _ptr(LSE, "LSE", _F32, (B, Hq, T), dev), prm, workspace.data_ptr(),
-                          nbytes, _raw_stream(dev))
+        lse = LSE.data_ptr()
+    else:
+        lse = _ptr(LSE, "LSE", _F32, (B, Hq, T), dev)
+    workspace, nbytes = _workspace(workspace, lib.cca_tree_workspace_size(prm, T), Q.device)
+    st = lib.cca_tree_fwd(q, raw, core, lens, parents, T, o, lse, prm, workspace.data_ptr(), nbytes, _raw_stream(dev))
     if st != CCA_OK:
         raise CcaError(st, "cca_tree_fwd")
     return O, LSE
@@ -878,12 +892,7 @@ def cca_pages_reserve(refs, table, lens, extra, rows: int, pairs=None, workspace
             return cca_pages_reserve(refs, table, lens, extra, rows, pairs, workspace, dev_status)
     if pairs is None:
         pairs = torch.empty((B, 2), dtype=_I32, device=refs.device)
-    need = lib.cca_pages_reserve_workspace_size(B, cols)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=refs.device)
-    nbytes = workspace.numel() * workspace.element_size()
-    if workspace.get_device() != dev or not workspace.is_contiguous() or nbytes < need:
-        raise ValueError(f"workspace must be a buffer of at least {need} bytes on cuda:{dev}")
+    workspace, nbytes = _workspace(workspace, lib.cca_pages_reserve_workspace_size(B, cols), refs.device)
     st = lib.cca_pages_reserve(refs_p, n, table_p, B, cols, rows, _ptr(lens, "lens", _I32, (B,), dev),
                                _ptr(extra, "extra", _I32, (B,), dev), _ptr(pairs, "pairs", _I32, (B, 2), dev),
                                workspace.data_ptr(), nbytes, _ptr(dev_status, "dev_status", _I32, (1,), dev), _raw_stream(dev))
