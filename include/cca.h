@@ -370,6 +370,8 @@ typedef struct cca_pages {
  *   counts  device [B] or NULL: only the first counts[b] tokens are real
  * Tokens that are not real (past counts, or a node whose chain of parents does not reach
  * the root) are not stored, and their rows of q's output are zero.
+ * The pages written must be the sequence's own: cca_pages_reserve gives a sequence that
+ * shares a page one of its own first.
  */
 int cca_rope_append(const cca_rope_tensor_t *q, const cca_rope_tensor_t *k, const cca_rope_tensor_t *v,
                     const cca_pages_t *raw, const int32_t *lens, const int32_t *parents, const int32_t *counts,
@@ -471,7 +473,7 @@ int cca_pages_copy(const cca_pages_t *pages, const int32_t *pairs, int n, const 
  * + i] moves to row lens[b] + i for i < accepted[b], K and V, every layer.  The path names
  * nodes from the root down, so it rises: path[i] >= i and path[i] < path[i+1].  A sequence
  * whose path does not, whose accepted is outside [0, A] or whose rows are not all there is
- * reported and left as it is.
+ * reported and left as it is.  The rows lens[b] .. of a sequence lie in pages of its own.
  *   params  B, Hkv, d, dtype, dev_status;  1 <= A <= 256
  */
 int cca_pages_compact(const cca_pages_t *pages, const int32_t *lens, const int32_t *path, int A,

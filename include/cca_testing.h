@@ -1,7 +1,8 @@
 /*
  * cca_testing.h - test hooks of libcca.so.  Not for production callers.
  *
- * The first two exercise the bounded-wait path of the bf16 attention kernel without
+ * The first two exercise the bounded-wait path of the bf16 attention kernel (and of
+ * the tensor-core backward and tree kernels, which have the same one) without
  * faulting or hanging the GPU: every mbarrier wait in that kernel gives up
  * after a time limit, raises a CTA-wide abort flag, drains the copies and
  * tensor-core operations it already issued, frees its tensor memory and
@@ -23,8 +24,8 @@ void cca_test_set_wait_limit_ns(unsigned long long ns);
 
 /* on != 0: later bf16 attention launches never load the query tile, so the
  * tensor-core issuer's first wait runs out and the kernel reports a time-out;
- * the tensor-core backward kernels issue no copies at all, so their first wait
- * runs out the same way.  on == 0 restores normal operation. */
+ * the tensor-core backward and tree kernels issue no copies at all, so their
+ * first wait runs out the same way.  on == 0 restores normal operation. */
 void cca_test_skip_q_load(int on);
 
 /* Which decode path later cca_decode_fwd / cca_decode_fwd_noalloc calls take:

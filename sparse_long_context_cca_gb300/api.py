@@ -698,26 +698,29 @@ def _rows_ready(t):
 
 
 class CcaRopeFunction(torch.autograd.Function):
-    """Autograd wrapper of cca_rope: the gradient is the rotation back, by the same kernel."""
+    """Autograd wrapper of cca_rope.  The rotation is linear, so its gradient is the rotation back, by
+    the same kernel, and that can be differentiated again."""
 
     @staticmethod
-    def forward(ctx, Q, K, inv_freq, positions, start, layout, factor):
+    def forward(ctx, Q, K, inv_freq, positions, start, layout, factor, inverse):
         ctx.save_for_backward(inv_freq, positions)
-        ctx.cfg = (start, layout, factor)
-        q, k = cca_rope(_rows_ready(Q), _rows_ready(K), inv_freq, positions, start, layout, factor)
-        return q, k
+        ctx.cfg = (start, layout, factor, inverse)
+        return cca_rope(_rows_ready(Q), _rows_ready(K), inv_freq, positions, start, layout, factor, inverse)
 
     @staticmethod
     def backward(ctx, dq, dk):
         inv_freq, positions = ctx.saved_tensors
-        start, layout, factor = ctx.cfg
-        gq, gk = cca_rope(_rows_ready(dq), _rows_ready(dk), inv_freq, positions, start, layout, factor, inverse=True)
-        return gq, gk, None, None, None, None, None
+        start, layout, factor, inverse = ctx.cfg
+        turn = CcaRopeFunction.apply if torch.is_grad_enabled() else cca_rope
+        gq, gk = turn(_rows_ready(dq), _rows_ready(dk), inv_freq, positions, start, layout, factor, not inverse)
+        return gq, gk, None, None, None, None, None, None
 
 
 def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", factor: float = 1.0):
-    """cca_rope with gradients for Q and K (training): returns (Q', K')."""
-    return CcaRopeFunction.apply(Q, K, inv_freq, positions, start, layout, factor)
+    """cca_rope with gradients for Q and K (training): returns (Q', K').  As with any autograd
+    function, a backward pass is captured into a CUDA graph together with its forward pass, from
+    leaves that no eager graph still holds."""
+    return CcaRopeFunction.apply(Q, K, inv_freq, positions, start, layout, factor, False)
 
 
 # ---------------------------------------------------------------- paged caches

@@ -483,7 +483,7 @@ cudaError_t launch_ring(const PoolPagesArgs &a, cudaStream_t stream) {
     if (lists * parts < static_cast<int64_t>(sms) * warps_per_block)  // few lists: spread over the SMs
         warps_per_block = static_cast<int>((lists * parts + sms - 1) / sms);
     const int64_t blocks = (lists * parts + warps_per_block - 1) / warps_per_block;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (blocks > 0x7fffffff) return cudaErrorNotSupported;
     pool_pages_ring_kernel<T, D><<<static_cast<unsigned>(blocks), warps_per_block * 32, smem, stream>>>(a, static_cast<int>(per_warp),
                                                                                                  static_cast<int>(parts), stage);
     return cudaGetLastError();

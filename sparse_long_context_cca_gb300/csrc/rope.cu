@@ -268,7 +268,7 @@ cudaError_t launch_rope_any(int dtype, RopeArgs a, cudaStream_t stream) {
     const int units = (a.layout == 0 ? a.rot / 2 : a.rot) / vv + (a.d - a.rot) / vv;
     const int64_t rows = PAGED ? a.N : static_cast<int64_t>(a.B) * a.N;
     const int64_t blocks = (rows * units + ROPE_THREADS - 1) / ROPE_THREADS;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (blocks > 0x7fffffff) return cudaErrorNotSupported;
     const int sms = device_sms();
     if (sms < 1) return cudaErrorNoDevice;
     // Angles are shared by the heads of a group: as many heads per thread as still leave
@@ -279,7 +279,7 @@ cudaError_t launch_rope_any(int dtype, RopeArgs a, cudaStream_t stream) {
     if (groups > most) groups = most;
     a.heads_per_block = (a.heads + groups - 1) / groups;
     groups = (a.heads + a.heads_per_block - 1) / a.heads_per_block;
-    if (groups > 65535) return cudaErrorInvalidValue;
+    if (groups > 65535) return cudaErrorNotSupported;
     const dim3 grid(static_cast<unsigned>(blocks), groups, PAGED ? a.B : 1);
     if (dtype == CCA_BF16) {
         switch (v) {

@@ -73,9 +73,10 @@ struct Meta {
     uint8_t kind[TILE];
 };
 
-template <int D>
+constexpr int MMA_D = 64;  // head dimension of the mma.sync kernel
+
 struct TreeSmem {
-    static constexpr int ROW = D * 2;                  // bytes of a key row
+    static constexpr int ROW = MMA_D * 2;                  // bytes of a key row
     static constexpr int TILE_BYTES = TILE * ROW;      // K or V
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
     static constexpr int META_OFF = STAGES * STAGE_BYTES;
@@ -85,19 +86,19 @@ struct TreeSmem {
     static __host__ __device__ int bytes(int T) { return NODE_OFF + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16; }
 };
 
-// Byte offset of 16-byte chunk c of row `row` in a tile: chunks are permuted inside each
-// 128 bytes by the row, so that the eight rows of an ldmatrix fall into different banks.
-template <int D>
+// Byte offset of 16-byte chunk c of row `row` in a tile: chunks are permuted inside a row, so
+// that the eight rows of an ldmatrix fall into different banks.
 __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
-    return static_cast<uint32_t>(row * (D * 2) + ((c ^ (row & 7)) << 4));
+    return static_cast<uint32_t>(row * TreeSmem::ROW + ((c ^ (row & 7)) << 4));
 }
 
-// WM warps side by side over 16-row blocks, 4 / WM over the keys of a tile.  One CTA walks
+// bf16 with d = 64.  WM warps side by side over 16-row blocks, 4 / WM over the keys of a tile.  One CTA walks
 // its group's run of tiles: cp.async keeps two tiles in flight behind the one in work, and
 // the page look-ups of the tile after those are done a step ahead, under the matrix work.
-template <int D, int WM>
+template <int WM>
 __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs a) {
-    using S = TreeSmem<D>;
+    using S = TreeSmem;
+    constexpr int D = MMA_D;
     constexpr int BM = 16 * WM;
     constexpr int WK = 4 / WM;
     constexpr int KW = TILE / WK;  // keys of a warp
@@ -155,13 +156,13 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
             for (int i = 0; i < PER; ++i) {
                 const int e = i * TREE_THREADS + tid, row = e / CPR, c = e % CPR;
                 const char *p = m.k[row];
-                cp16(base + chunk_at<D>(row, c), p == nullptr ? a.K : p + c * 16, p != nullptr);
+                cp16(base + chunk_at(row, c), p == nullptr ? a.K : p + c * 16, p != nullptr);
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int e = i * TREE_THREADS + tid, row = e / CPR, c = e % CPR;
                 const char *p = m.v[row];
-                cp16(base + S::TILE_BYTES + chunk_at<D>(row, c), p == nullptr ? a.V : p + c * 16, p != nullptr);
+                cp16(base + S::TILE_BYTES + chunk_at(row, c), p == nullptr ? a.V : p + c * 16, p != nullptr);
             }
         }
         cp_commit();
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
 #pragma unroll
             for (int n = 0; n < NT; n += 2) {
                 uint32_t f[4];
-                ldsm4(kbase + chunk_at<D>(wk * KW + n * 8 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), f);
+                ldsm4(kbase + chunk_at(wk * KW + n * 8 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), f);
                 mma16816(s[n], qf[kk], f[0], f[1]);
                 mma16816(s[n + 1], qf[kk], f[2], f[3]);
             }
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
                 if (mw.kind[row] != 0 && mw.kind[row] != 4) {
                     bool odd = false;
                     for (int c = (tid & 1) * (CPR / 2); c < (tid & 1) * (CPR / 2) + CPR / 2; ++c) {
-                        uint4 *p = reinterpret_cast<uint4 *>(smem + (vbase - stage0) + chunk_at<D>(row, c));
+                        uint4 *p = reinterpret_cast<uint4 *>(smem + (vbase - stage0) + chunk_at(row, c));
                         uint32_t v[4] = {p->x, p->y, p->z, p->w};
                         bool hit = false;
 #pragma unroll
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
 #pragma unroll
             for (int n = 0; n < DT; n += 2) {
                 uint32_t f[4];
-                ldsm4_t(vbase + chunk_at<D>(wk * KW + kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), n + (lane >> 4)), f);
+                ldsm4_t(vbase + chunk_at(wk * KW + kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), n + (lane >> 4)), f);
                 mma16816(o[n], p, f[0], f[1]);
                 mma16816(o[n + 1], p, f[2], f[3]);
             }
@@ -763,14 +764,15 @@ cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t strea
 
 constexpr int MAX_CTAS_PER_SM = 4;
 
-// bf16 with d = 128 runs on the tensor cores, whatever the rows (one row: 29.4 us against 31.6 us by
-// mma.sync for 32 heads at 32 K; 64 sequences of 8 K: 264 us against 274 us).
-bool on_tensor_cores(int dtype, int R, int d) { return dtype == CCA_BF16 && d == 128; }
+// bf16 with d = 128 runs on tcgen05, whatever the rows: one row of 32 heads at 32 K took 29.4 us
+// there and 31.6 us by mma.sync, 64 such sequences of 8 K 264 and 274 us (16 rows of 32
+// sequences 79 and 83 us).
+bool on_tensor_cores(int dtype, int d) { return dtype == CCA_BF16 && d == 128; }
 
 // Rows per CTA: 16 rows of a warp each, so that as few row tiles as possible read the keys.
 int rows_per_cta(int dtype, int R, int d) {
     if (dtype == CCA_F32) return F32_BM;
-    if (on_tensor_cores(dtype, R, d)) return tc_rows(R);
+    if (on_tensor_cores(dtype, d)) return tc_rows(R);
     return R <= 16 ? 16 : R <= 32 ? 32 : 64;
 }
 
@@ -779,7 +781,7 @@ uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
     // elsewhere, and one group of row tiles at least
     const int BM = rows_per_cta(dtype, R, d);
     const int64_t n_mt = (R + BM - 1) / BM;
-    int64_t ctas = static_cast<int64_t>(sms) * (on_tensor_cores(dtype, R, d) ? 1 : MAX_CTAS_PER_SM);
+    int64_t ctas = static_cast<int64_t>(sms) * (on_tensor_cores(dtype, d) ? 1 : MAX_CTAS_PER_SM);
     if (ctas < n_mt) ctas = n_mt;
     return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
 }
@@ -816,16 +818,12 @@ cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
     return run_join(tree_join_kernel<__nv_bfloat16, 128>, a, BM, stream);
 }
 
-template <int D>
-cudaError_t run_bf16(const TreeArgs &a, int sms, cudaStream_t stream) {
-    if (on_tensor_cores(CCA_BF16, a.R, D)) return run_tc(a, sms, stream);
-    const int smem = TreeSmem<D>::bytes(a.T);
-    auto *join = tree_join_kernel<__nv_bfloat16, D>;
-    switch (rows_per_cta(CCA_BF16, a.R, D)) {
-        case 16: return run_tree<tree_bf16_kernel<D, 1>>(join, a, 16, smem, sms, stream);
-        case 32: return run_tree<tree_bf16_kernel<D, 2>>(join, a, 32, smem, sms, stream);
-        default: return run_tree<tree_bf16_kernel<D, 4>>(join, a, 64, smem, sms, stream);
-    }
+cudaError_t run_mma(const TreeArgs &a, int sms, cudaStream_t stream) {
+    const int smem = TreeSmem::bytes(a.T), BM = rows_per_cta(CCA_BF16, a.R, MMA_D);
+    auto *join = tree_join_kernel<__nv_bfloat16, MMA_D>;
+    if (BM == 16) return run_tree<tree_bf16_kernel<1>>(join, a, BM, smem, sms, stream);
+    if (BM == 32) return run_tree<tree_bf16_kernel<2>>(join, a, BM, smem, sms, stream);
+    return run_tree<tree_bf16_kernel<4>>(join, a, BM, smem, sms, stream);
 }
 
 int check_tree(const cca_params_t *p, int T) {
@@ -910,8 +908,7 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.ws = static_cast<float *>(workspace);
     a.status = params->dev_status;
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
-    if (params->dtype == CCA_BF16)
-        return from_cuda(params->d == 128 ? run_bf16<128>(a, sms, strm) : run_bf16<64>(a, sms, strm));
+    if (params->dtype == CCA_BF16) return from_cuda(params->d == 128 ? run_tc(a, sms, strm) : run_mma(a, sms, strm));
     if (params->d == 128)
         return from_cuda(run_tree<tree_f32_kernel<128>>(tree_join_kernel<float, 128>, a, F32_BM,
                                   TreeF32Smem<128>::bytes(T), sms, strm));

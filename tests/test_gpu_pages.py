@@ -303,7 +303,8 @@ def test_append_out_of_the_table_is_reported():
 @pytest.mark.parametrize("mode", [0, 1, 2, 3])
 @pytest.mark.parametrize("B,T,Hq,Hkv,d,g,rows,crows,lens", [
     (3, 20, 4, 2, 128, 8, 16, 5, [0, 37, 100]), (2, 33, 3, 1, 64, 3, 7, 64, [5, 64]), (1, 1, 2, 2, 128, 1, 16, 16, [9]),
-    (2, 64, 8, 1, 128, 64, 24, 4, [63, 200]), (1, 40, 2, 2, 64, 16, 40, 8, [0])])
+    (2, 64, 8, 1, 128, 64, 24, 4, [63, 200]), (1, 40, 2, 2, 64, 16, 40, 8, [0]),
+    (1, 1100, 8, 8, 64, 2, 48, 33, [5])])   # several groups per warp
 def test_pool_pages(B, T, Hq, Hkv, d, g, rows, crows, lens, mode, dtype):
     rng = np.random.default_rng(T + mode)
     gen = torch.Generator().manual_seed(T)

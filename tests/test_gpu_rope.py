@@ -208,3 +208,45 @@ def test_frequencies(rot, scaling):
         np.testing.assert_allclose([f[0], f[-1]], [plain[0], plain[-1] / 8], rtol=1e-12)
         assert (f <= plain * (1 + 1e-12)).all() and (f >= plain / 8 * (1 - 1e-12)).all() and (np.diff(f) < 0).all()
     assert factor == pytest.approx(0.1 * np.log(8) + 1 if scaling == "yarn" else 1.0, rel=1e-15)
+
+
+def test_gradient_of_the_gradient():
+    """The rotation is linear: differentiating its gradient rotates forth again."""
+    Q, K = rand(1, 2, 7, 64).requires_grad_(), rand(1, 1, 7, 64, seed=1).requires_grad_()
+    f = freqs(64)
+    q, k = api.rope(Q, K, f, start=9, factor=1.5)
+    dq, dk = rand(1, 2, 7, 64, seed=2).requires_grad_(), rand(1, 1, 7, 64, seed=3).requires_grad_()
+    gq, gk = torch.autograd.grad([q, k], [Q, K], [dq, dk], create_graph=True)
+    e, z = rand(1, 2, 7, 64, seed=4), rand(1, 1, 7, 64, seed=5)
+    hq, hk = torch.autograd.grad([gq, gk], [dq, dk], [e, z])
+    pos = 9 + np.arange(7)[None]
+    close(hq, *rotate(e, pos, f.cpu(), "half", 1.5), "ddQ")
+    close(hk, *rotate(z, pos, f.cpu(), "half", 1.5), "ddK")
+
+
+def test_forward_and_backward_in_one_graph():
+    f = freqs(128)
+    mk = lambda s, h: rand(1, h, 21, 128, dtype=torch.bfloat16, seed=s)  # noqa: E731
+    Q, K, dq, dk = mk(0, 3).requires_grad_(), mk(1, 1).requires_grad_(), mk(2, 3), mk(3, 1)
+
+    def step():
+        q, k = api.rope(Q, K, f, layout="interleaved")
+        return (q, k, *torch.autograd.grad([q, k], [Q, K], [dq, dk]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    with torch.no_grad():
+        Q.copy_(mk(4, 3))
+        dk.copy_(mk(5, 1))
+    graph.replay()
+    torch.cuda.synchronize()
+    pos = np.arange(21)[None]
+    close(out[0], *rotate(Q, pos, f.cpu(), "interleaved"), "Q")
+    close(out[3], *rotate(dk, pos, f.cpu(), "interleaved", 1.0, -1.0), "dK")

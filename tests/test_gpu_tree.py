@@ -71,6 +71,7 @@ CASES = [  # B, T, Hq, Hkv, d, lens, g, w, rows, crows, mode
     (3, 12, 4, 2, 128, [5000, 20, 2600], 16, 300, 64, 64, 0),     # tensor cores: lists of many tiles, several per CTA
     (40, 10, 8, 4, 128, [17 * i + 3 for i in range(40)], 8, 33, 16, 10, 1),   # more lists than CTAs
     (2, 64, 4, 1, 128, [9000, 4100], 2, 128, 64, 64, 0),          # two halves over runs of many tiles
+    (2, 24, 4, 2, 64, [2600, 700], 8, 100, 48, 24, 0),            # d = 64: 48 rows, several lists per CTA
     (2, 96, 4, 1, 128, [333, 4100], 8, 128, 48, 16, 0),           # 384 rows: two row tiles of two halves, the last half empty
 ]
 
@@ -102,12 +103,13 @@ def test_padding_and_broken_chains():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("bad", [NAN, float("inf"), -float("inf")])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("heads", [2, 4, 24, 40])    # rows for each of the kernels
-def test_masked_rows_may_hold_anything(bad, dtype, heads):
+def test_masked_rows_may_hold_anything(bad, dtype, heads, d):
     """Infinities and NaN in keys and values that a node does not see leave it as it is, and reach the
     nodes that do see them."""
     T = 6
-    B, Hq, Hkv, d, g, w, rows = 1, heads, 1, 128, 8, 40, 16
+    B, Hq, Hkv, g, w, rows = 1, heads, 1, 8, 40, 16
     x = make(B, T, Hq, Hkv, d, [200], g, w, rows, rows, dtype, seed=3)
     x["parents"] = torch.tensor([[-1, 0, 0, 1, 2, 2]], dtype=torch.int32)
     clean = call(x, g, w)
