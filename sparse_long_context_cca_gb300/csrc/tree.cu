@@ -122,12 +122,12 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wm = warp % WM, wk = warp / WM;
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    find_run(a, group, st);
-    const int x0 = st.x0, x1 = st.x1;
+    const Run run = find_run(a, group, st);
+    const int x0 = run.x0, x1 = run.x1;
     if (x0 >= x1) return;
 
     // ---- loading
-    Item ld = st.item;  // list of the tile whose addresses come next
+    Item ld = run.item;  // list of the tile whose addresses come next
     auto look_up = [&](int x, Key &key) {  // threads 0 .. 63, one key each
         if (x >= x1) return;
         if (x >= ld.first + ld.k.tiles) next_item(a, ld);
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     for (int i = 0; i < STAGES - 1; ++i) issue(x0 + i);
 
     // ---- the rows
-    Item it = st.item;
+    Item it = run.item;
     if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
     uint32_t qf[D / 16][4];
     float o[DT][4], m[2], l[2];
@@ -494,10 +494,10 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    find_run(a, group, st);
-    const int x0 = st.x0, x1 = st.x1;
+    const Run run = find_run(a, group, st);
+    const int x0 = run.x0, x1 = run.x1;
     if (x0 >= x1) return;
-    Item it = st.item;
+    Item it = run.item;
     const int col = tid % D, rg = tid / D;
     float o[RPT];
     int64_t out0 = 0;

@@ -172,17 +172,49 @@ struct Item {
     KeyList k;
 };
 
-// What a CTA finds out first, in shared memory.
+// A CTA's run of tiles and the list that it begins in.
+struct Run {
+    Item item;
+    int x0, x1;
+};
+
+// What a larger batch needs of shared memory to find it.
 struct Start {
-    Item item;  // the list that its run begins in
-    int x0, x1; // its run of tiles
+    Run run;
     int warp_sum[16];
 };
 
-// Lengths to tiles to runs: every CTA adds up the tiles of all lists for itself (thread per
-// sequence), and the thread that owns the sequence its run begins in leaves that list behind.
-__device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st) {
+// Lengths to tiles to runs: every CTA adds up the tiles of all lists for itself, a thread per
+// sequence.  Up to 32 sequences each warp does it alone, in registers; more go through shared
+// memory and two barriers.
+__device__ __forceinline__ Run find_run(const TreeArgs &a, int group, Start &st) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+    if (a.B <= 32) {
+        KeyList k = {};
+        if (lane < a.B) k = key_list(a, lane);
+        const int own = k.tiles * a.Hkv;
+        int x = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(kFull, x, off);
+            if (lane >= off) x += y;
+        }
+        const Split s = make_split(a, __shfl_sync(kFull, x, 31));
+        Run r = {};
+        if (group >= s.groups) return r;
+        r.x0 = s.begin(group);
+        r.x1 = s.begin(group + 1);
+        const int src = __ffs(__ballot_sync(kFull, x > r.x0)) - 1;  // the sequence that holds tile x0
+        r.item.b = src;
+        int *out = reinterpret_cast<int *>(&r.item.k);
+        const int *in = reinterpret_cast<const int *>(&k);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(KeyList) / 4); ++i) out[i] = __shfl_sync(kFull, in[i], src);
+        const int before = __shfl_sync(kFull, x - own, src);
+        r.item.kv = (r.x0 - before) / r.item.k.tiles;
+        r.item.first = before + r.item.kv * r.item.k.tiles;
+        return r;
+    }
     const int per = (a.B + nt - 1) / nt;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     int own = 0;
@@ -198,7 +230,7 @@ __device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st
         if (lane >= off) x += y;
     }
     if (lane == 31) st.warp_sum[warp] = x;
-    if (tid == 0) st.x0 = st.x1 = 0;
+    if (tid == 0) st.run.x0 = st.run.x1 = 0;
     __syncthreads();
     int before = x - own, total = 0;
     for (int i = 0; i < nw; ++i) {
@@ -212,17 +244,18 @@ __device__ __forceinline__ void find_run(const TreeArgs &a, int group, Start &st
             if (per > 1) k = key_list(a, b);
             const int tiles = k.tiles * a.Hkv;
             if (x0 >= before && x0 < before + tiles) {
-                st.item.b = b;
-                st.item.kv = (x0 - before) / k.tiles;
-                st.item.first = before + st.item.kv * k.tiles;
-                st.item.k = k;
-                st.x0 = x0;
-                st.x1 = s.begin(group + 1);
+                st.run.item.b = b;
+                st.run.item.kv = (x0 - before) / k.tiles;
+                st.run.item.first = before + st.run.item.kv * k.tiles;
+                st.run.item.k = k;
+                st.run.x0 = x0;
+                st.run.x1 = s.begin(group + 1);
             }
             before += tiles;
         }
     }
     __syncthreads();
+    return st.run;
 }
 
 __device__ __forceinline__ void next_item(const TreeArgs &a, Item &it) {

@@ -133,14 +133,15 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         ptx::tmem_relinquish();
     }
     if (warp == HALVES * 4 && lane < 4) ptx::prefetch_tmap(lane == 0 ? &tmK : lane == 1 ? &tmV : lane == 2 ? &tmKc : &tmVc);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
     ptx::tc_fence_before();
-    const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
-    find_run(a, group, st);  // holds barriers
+    __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(gbase + L::OFF_TMEMPTR);
-    const int x0 = st.x0, x1 = st.x1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
+    const Run run = find_run(a, group, st);
+    const int x0 = run.x0, x1 = run.x1;
     const bool half_used[2] = {true, HALVES == 2 && mt * BM + 128 < a.R};
 
     if (wg == HALVES) {
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         const int pw = warp & 3;
         const int sub = lane >> 4, chunk = lane & 15;
         bool ok = x0 < x1 && !skip_loads;
-        Item it = st.item;
+        Item it = run.item;
         // the tile to load next: a lane's box of runs, or a lane's key of the rest
         bool runs = false, core = false;
         int box_y = 0;
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             constexpr uint64_t STEP = TILE_BYTES >> 4;
             bool ok = true;
             uint32_t seg = 0, pcount = 0;  // lists; tiles whose P was waited for
-            Item it = st.item;
+            Item it = run.item;
             int x = x0;
             // S = Q_h K(t)^T into score buffer `buf`; K(t) has been waited for
             auto scores = [&](int h, int buf, int t) {
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         const int node = live ? row % a.T : 0;
         bool ok = true;
         uint32_t seg = 0, n_s = 0;  // lists and tiles of this half so far
-        Item it = st.item, nxt = st.item;
+        Item it = run.item, nxt = run.item;
         int tree_of = -1;
         int start = 0, cores = -1;  // this row's first raw token; its visible cores, -1: empty node
         const int heads = a.Hq / a.Hkv;
