@@ -628,8 +628,9 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
 
 constexpr int JOIN_ROWS = 32;
 
-// A block joins up to 32 rows and a quarter of the columns of one list, a quarter of those per
-// warp (many blocks with few loads each: the time is that of the chain of reads).  A lane takes a
+// A block joins up to 32 rows of one list: all columns, a half or a quarter of them (gridDim.z),
+// a quarter of those per warp.  The time is that of the chain of reads, so few lists take many
+// blocks of few loads, and many lists as many blocks as are resident at once.  A lane takes a
 // row; where there are fewer rows, the lanes left over take parts: lane group i the parts i,
 // i + groups, .. of the list, in the order of the groups that wrote them, and the lane groups
 // are added up in a fixed order.  Lists that one group finished are already written.
@@ -668,55 +669,58 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM
     const bool live = row < a.R;
     const int mt = live ? row / BM : 0, in = live ? row - mt * BM : 0;
     auto part = [&](int y) { return static_cast<const float *>(part_at(a, y, mt, split.begin(y) >= s ? 0 : 1, BM, D)); };
-    const int col0 = (blockIdx.z * 4 + warp) * C;  // in float4
     float mx = -INFINITY;
 #pragma unroll 4
     for (int y = y0 + lane / lanes; y <= y1; y += step) mx = fmaxf(mx, part(y)[BM * D + in]);
     for (int off = 16; off >= lanes; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
     const float base = mx == -INFINITY ? 0.f : mx;
-    float4 acc[C];
-    float l = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int y = y0 + lane / lanes; y <= y1; y += step) {
-        const float *p = part(y);
-        const float4 *q = reinterpret_cast<const float4 *>(p) + col0 * BM + in;
-        const float f = exp2f(p[BM * D + in] - base);
-        l += p[BM * D + BM + in] * f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const float4 v = q[c * BM];
-            acc[c].x = fmaf(v.x, f, acc[c].x);
-            acc[c].y = fmaf(v.y, f, acc[c].y);
-            acc[c].z = fmaf(v.z, f, acc[c].z);
-            acc[c].w = fmaf(v.w, f, acc[c].w);
-        }
-    }
-    for (int off = 16; off >= lanes; off >>= 1) {
-        l += __shfl_xor_sync(kFull, l, off);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            acc[c].x += __shfl_xor_sync(kFull, acc[c].x, off);
-            acc[c].y += __shfl_xor_sync(kFull, acc[c].y, off);
-            acc[c].z += __shfl_xor_sync(kFull, acc[c].z, off);
-            acc[c].w += __shfl_xor_sync(kFull, acc[c].w, off);
-        }
-    }
-    if (!live || lane >= lanes) return;
     const int64_t at = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kv) * (a.Hq / a.Hkv)) * a.T + row;
-    const bool none = l == 0.f;
+    const int rounds = 4 / gridDim.z;
+    for (int i = 0; i < rounds; ++i) {
+        const int col0 = ((blockIdx.z * 4 + warp) * rounds + i) * C;  // in float4
+        float4 acc[C];
+        float l = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc[c].x / l, acc[c].y / l, acc[c].z / l, acc[c].w / l);
-        const int64_t to = at * D + (col0 + c) * 4;
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.O) + to) = make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
-        } else {
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.O) + to) = v;
+        for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int y = y0 + lane / lanes; y <= y1; y += step) {
+            const float *p = part(y);
+            const float4 *q = reinterpret_cast<const float4 *>(p) + col0 * BM + in;
+            const float f = exp2f(p[BM * D + in] - base);
+            l += p[BM * D + BM + in] * f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float4 v = q[c * BM];
+                acc[c].x = fmaf(v.x, f, acc[c].x);
+                acc[c].y = fmaf(v.y, f, acc[c].y);
+                acc[c].z = fmaf(v.z, f, acc[c].z);
+                acc[c].w = fmaf(v.w, f, acc[c].w);
+            }
         }
+        for (int off = 16; off >= lanes; off >>= 1) {
+            l += __shfl_xor_sync(kFull, l, off);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                acc[c].x += __shfl_xor_sync(kFull, acc[c].x, off);
+                acc[c].y += __shfl_xor_sync(kFull, acc[c].y, off);
+                acc[c].z += __shfl_xor_sync(kFull, acc[c].z, off);
+                acc[c].w += __shfl_xor_sync(kFull, acc[c].w, off);
+            }
+        }
+        if (!live || lane >= lanes) continue;
+        const bool none = l == 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc[c].x / l, acc[c].y / l, acc[c].z / l, acc[c].w / l);
+            const int64_t to = at * D + (col0 + c) * 4;
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.O) + to) = make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.O) + to) = v;
+            }
+        }
+        if (col0 == 0) a.LSE[at] = none ? -INFINITY : (mx + log2f(l)) * kLn2;
     }
-    if (col0 == 0) a.LSE[at] = none ? -INFINITY : (mx + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- launch
@@ -787,8 +791,10 @@ uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
 }
 
 template <typename J>
-cudaError_t run_join(J join, const TreeArgs &a, int BM, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_ROWS - 1) / JOIN_ROWS, 4);
+cudaError_t run_join(J join, const TreeArgs &a, int BM, int sms, cudaStream_t stream) {
+    dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_ROWS - 1) / JOIN_ROWS, 4);
+    // eight blocks are resident per SM
+    while (grid.z > 1 && static_cast<int64_t>(grid.x) * grid.y * grid.z > 8ll * sms) grid.z /= 2;
     return start(join, grid, 128, 0, stream, a, BM);
 }
 
@@ -804,7 +810,7 @@ cudaError_t run_tree(J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t
     if (a.groups < 1) a.groups = 1;
     e = start(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a, BM);
     if (e != cudaSuccess) return e;
-    return run_join(join, a, BM, stream);
+    return run_join(join, a, BM, sms, stream);
 }
 
 cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
@@ -815,7 +821,7 @@ cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
     a.tile_log2 = 7;
     const cudaError_t e = launch_tc(a, g_wait_limit_ns, g_skip_q_load, stream);
     if (e != cudaSuccess) return e;
-    return run_join(tree_join_kernel<__nv_bfloat16, 128>, a, BM, stream);
+    return run_join(tree_join_kernel<__nv_bfloat16, 128>, a, BM, sms, stream);
 }
 
 cudaError_t run_mma(const TreeArgs &a, int sms, cudaStream_t stream) {
