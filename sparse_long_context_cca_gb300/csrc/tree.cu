@@ -3,6 +3,9 @@
 // softmax over the cores j < lo(p)/g, the committed raw tokens of its window, its
 // ancestors and itself.  One node per sequence is plain decoding.
 //
+// Three kernels walk the lists: tree_tc.cu (bf16, d = 128, tcgen05), tree_bf16_kernel (bf16,
+// d = 64, mma.sync) and tree_f32_kernel (fp32 on CUDA cores).
+//
 // What bounds it.  The r query heads of a KV head times T nodes are R = r*T rows that share
 // one list of keys: K and V rows are read once per (b, KV head) and meet R rows, so few rows
 // are bound by HBM and many by the matrix units.
@@ -469,7 +472,9 @@ struct TreeF32Smem {
     static __host__ __device__ int bytes(int T) { return NODE_OFF + 8 * T + 4 * T * ((T + 31) / 32) + 2 * T + 16; }
 };
 
-// The same walk with one tile in shared memory at a time; scores and sums in fp32.
+// The same walk with one tile in shared memory at a time; scores and sums in fp32.  Three sequences
+// of 1.5 K, seven nodes, four heads over two (0.8 MB): 16.5 us, a chain of one tile per CTA and the
+// join; with two tiles per CTA at least it was 23 us.
 template <int D>
 __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a) {
     using S = TreeF32Smem<D>;

@@ -1,11 +1,19 @@
-// Tree attention on the tcgen05 tensor cores: bf16, d = 128, more than 16 query rows per KV
-// head (T nodes times the query heads that share it).  What it computes, the key list and
-// the split over the grid are those of tree.cuh; this file is the walk of one CTA over its
+// Tree attention on the tcgen05 tensor cores: bf16, d = 128.  What it computes, the key list
+// and the split over the grid are those of tree.cuh; this file is the walk of one CTA over its
 // run of 128-key tiles.
 //
-// One CTA holds HALVES * 128 rows, so up to 256 rows read K and V once.  Per tile of 128
-// keys an SM's share of HBM needs 64 KB / 44 GB/s = 1.5 us, the MMAs of 256 rows 0.7 us for
-// each product: with one half the loads bound it, with two the MMAs and loads are level.
+// One CTA holds HALVES * 128 rows (T nodes times the query heads that share a KV head), so up
+// to 256 rows read K and V once; the rows that a small tree leaves empty cost nothing, as the
+// loads bound it.  Per tile an SM's share of HBM needs 64 KB / 44 GB/s = 1.5 us (2800 cycles).
+// Measured: one half 2300 cycles a tile from L2, so HBM is the bound (64 sequences of one token,
+// 32 heads, 8 K: 262 us, 0.80 of the copy bandwidth); two halves 3500 cycles, the four products
+// at 820 cycles each against 512 of tensor work, as both read their operands from shared memory
+// (192 KB a tile at 128 B a cycle, next to 64 KB of copies): 16 sequences x 64 nodes, 32 heads
+// over 8, 128 K: 145 us, 4.1 TB/s and 1.0 PFLOP/s.  64-key tiles with two score buffers per half
+// free the softmax from waiting for its product, but their N = 64 products took 740 cycles each:
+// 201 us.  A call on little work is a chain: the CTA's run 1.8 us, page look-up and first copy
+// 2.5 us, first softmax 1.4 us, output 1.5 us, then the join (one token of 32 heads at 32 K,
+// 49 MB: 19.5 us warm, 23.8 us from HBM).
 //
 // Roles (warpgroups of four warps):
 //   0 .. HALVES-1   softmax and output of a half; thread t owns row t of it (TMEM lane t).
@@ -16,7 +24,9 @@
 //                   look up and 16 lanes to a row to copy, so any page size and alignment goes.
 //                   Both fill 128-byte-swizzled tiles.
 //   HALVES+1        its first warp issues the MMAs.
-// K(t) and V(t) take two consecutive slots of a ring of NS 32 KB slots.
+// K(t) and V(t) take two consecutive slots of a ring of NS 32 KB slots and are freed apart: K
+// when its scores are done, V when its product is (both at once cost a load's latency per tile:
+// 230 us in place of 158 at the time).
 //
 // Two halves: S_A | S_B | O_A | O_B fill the tensor memory; the halves' softmaxes and MMAs
 // alternate.  P_h overwrites S_h, and S_h of the next tile is issued after the product that
