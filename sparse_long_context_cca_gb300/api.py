@@ -691,6 +691,8 @@ def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half
 
 def _rows_ready(t):
     """t itself where its rows can be read in place, a contiguous copy otherwise."""
+    if t is None:
+        return None
     s = t.stride()
     if s[3] == 1 and (s[0] | s[1] | s[2]) * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0:
         return t
@@ -717,7 +719,7 @@ class CcaRopeFunction(torch.autograd.Function):
 
 
 def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", factor: float = 1.0):
-    """cca_rope with gradients for Q and K (training): returns (Q', K').  As with any autograd
+    """cca_rope with gradients for Q and K (or Q alone, with K None): returns (Q', K').  As with any autograd
     function, a backward pass is captured into a CUDA graph together with its forward pass, from
     leaves that no eager graph still holds."""
     return CcaRopeFunction.apply(Q, K, inv_freq, positions, start, layout, factor, False)

@@ -506,15 +506,17 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                     // a masked tile: -inf into the scores that the row does not see, where they are
                     if (masked) {
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            const uint32_t see = mask_of(c >> 1) >> (16 * (c & 1));
-                            uint32_t v[16];
-                            ptx::tmem_ld16(tS + c * 16, v);
-                            ptx::tmem_wait_ld16(v);
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t see = mask_of(c);
+                            if (__all_sync(kFull, see == 0xffffffffu)) continue;
+                            uint32_t v[32];
+                            ptx::tmem_ld32(tS + c * 32, v);
+                            ptx::tmem_wait_ld(v);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
+                            for (int k = 0; k < 32; ++k)
                                 if (!((see >> k) & 1u)) v[k] = __float_as_uint(-INFINITY);
-                            ptx::tmem_st16(tS + c * 16, v);
+                            ptx::tmem_st16(tS + c * 32, reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                            ptx::tmem_st16(tS + c * 32 + 16, reinterpret_cast<const uint32_t(&)[16]>(v[16]));
                         }
                         ptx::tmem_wait_st();
                     }

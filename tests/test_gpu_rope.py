@@ -133,6 +133,9 @@ def test_gradient_of_a_sum_and_of_one_output():
     Q, K = rand(1, 2, 5, 64).requires_grad_(), rand(1, 1, 5, 64, seed=1).requires_grad_()
     f = freqs(64)
     q, _ = api.rope(Q, K, f, start=3)
+    alone, none = api.rope(Q, None, f, start=3)
+    assert none is None and torch.equal(alone, q)
+    assert torch.equal(torch.autograd.grad(alone.sum(), Q)[0], torch.autograd.grad(q.sum(), Q, retain_graph=True)[0])
     gq, gk = torch.autograd.grad(q.sum(), [Q, K])
     close(gq, *rotate(torch.ones(1, 2, 5, 64), 3 + np.arange(5)[None], f.cpu(), "half", 1.0, -1.0), "dQ")
     assert not gk.any()
