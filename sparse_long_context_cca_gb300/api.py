@@ -4,12 +4,15 @@ Every step of the computation runs in the library's CUDA kernels; this module
 allocates outputs with torch (device memory is plumbing), checks that tensors
 match the C ABI's layout, and forwards raw device pointers.  There is no
 fallback: if the library is missing or a call fails, an exception is raised.
+
+The rotary and paged calls, of which a decoding step makes many, are checked and
+marshalled by the extension module _binding (csrc/binding.cpp), bound to the same
+library.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 import torch
@@ -66,6 +69,7 @@ class CcaPages(ctypes.Structure):
 
 
 _lib = None
+_fast = None    # the _binding module, bound to the library
 _lock = threading.Lock()
 
 EXPORTED = ["cca_pool", "cca_attn_fwd", "cca_attn_fwd_rows", "cca_decode_fwd", "cca_decode_workspace_size",
@@ -85,7 +89,7 @@ def library_path() -> str:
 
 def load_library():
     """Load libcca.so; raises if it has not been built."""
-    global _lib
+    global _lib, _fast
     with _lock:
         if _lib is not None:
             return _lib
@@ -122,20 +126,19 @@ def load_library():
         lib.cca_pool_group.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int, pp, vp]
         lib.cca_pool_group.restype = ctypes.c_int
         u64 = ctypes.c_uint64
-        # structures of the newer calls arrive packed (_pack_*), so their pointers are plain
-        rp = rt = pg = pq = vp
+        rp, rt, pg = (ctypes.POINTER(x) for x in (CcaRopeParams, CcaRopeTensor, CcaPages))
         for name, args, res in (
                 ("cca_rope", [rt, ci, rp, vp], ci),
                 ("cca_rope_append", [rt, rt, rt, pg, vp, vp, vp, vp, rp, vp], ci),
-                ("cca_tree_fwd", [vp, pg, pg, vp, vp, ci, vp, vp, pq, vp, u64, vp], ci),
-                ("cca_tree_workspace_size", [pq, ci], u64),
-                ("cca_pool_pages", [vp, pg, pg, vp, vp, vp, ci, ci, pq, vp], ci),
+                ("cca_tree_fwd", [vp, pg, pg, vp, vp, ci, vp, vp, pp, vp, u64, vp], ci),
+                ("cca_tree_workspace_size", [pp, ci], u64),
+                ("cca_pool_pages", [vp, pg, pg, vp, vp, vp, ci, ci, pp, vp], ci),
                 ("cca_pages_reserve", [vp, ci, vp, ci, ci, ci, vp, vp, vp, vp, u64, vp, vp], ci),
                 ("cca_pages_reserve_workspace_size", [ci, ci], u64),
                 ("cca_pages_fork", [vp, ci, vp, ci, ci, ci, vp, vp, ci, vp, vp, vp], ci),
                 ("cca_pages_free", [vp, ci, vp, ci, ci, vp, vp, vp, vp], ci),
-                ("cca_pages_copy", [pg, vp, ci, pq, vp], ci),
-                ("cca_pages_compact", [pg, vp, vp, ci, vp, pq, vp], ci)):
+                ("cca_pages_copy", [pg, vp, ci, pp, vp], ci),
+                ("cca_pages_compact", [pg, vp, vp, ci, vp, pp, vp], ci)):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, res
         lib.cca_status_string.argtypes = [ctypes.c_int]
@@ -148,8 +151,19 @@ def load_library():
         lib.cca_test_skip_q_load.restype = None
         lib.cca_test_decode_path.argtypes = [ctypes.c_int]
         lib.cca_test_decode_path.restype = None
-        _lib = lib
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"_binding.so not found at {_build.BINDING}: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        from . import _binding
+        _binding.bind(CcaError, {n: ctypes.cast(getattr(lib, n), vp).value for n in EXPORTED if not n.startswith("cca_test")})
+        _lib, _fast = lib, _binding
         return lib
+
+
+def _bound():
+    """The binding of the rotary and paged calls; loads the library first."""
+    load_library()
+    return _fast
 
 
 def status_string(status: int) -> str:
@@ -513,9 +527,6 @@ def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 
 
 # ---------------------------------------------------------------- rotary positions
 
-_LAYOUT = {"half": 0, "interleaved": 1}
-
-
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
                      original: int = 8192, low: float = 1.0, high: float = 4.0, device="cuda"):
     """Frequencies of a rotary embedding, and the factor that goes with them: (inv_freq float64
@@ -555,96 +566,23 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     return f.to(device), attention
 
 
-# A decoding step makes many small calls, so the ones below keep the host's share low: checks
-# that build nothing unless they fail, structures packed in one go (the layouts are those of
-# CcaParams, CcaRopeParams, CcaRopeTensor and CcaPages), and the raw stream of the device.
-_pack_params = struct.Struct("@8if4xP2i").pack
-_pack_rope = struct.Struct("@7ifPP2q").pack
-_pack_rope_tensor = struct.Struct("@PPi4x6q").pack
-_pack_pages = struct.Struct("@PPP4i").pack
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_F32, _F64, _I32 = torch.float32, torch.float64, torch.int32
-
-
-def _elsewhere(dev: int, stream) -> bool:
-    return stream is not None or torch.cuda.current_device() != dev
-
-
 class _On:
-    """The tensors' device and the caller's stream (the device's current one without) as current
-    ones, so that what a call allocates belongs to them too."""
+    """The caller's stream as the current one, so that what a call allocates belongs to it too."""
 
-    def __init__(self, dev: int, stream):
-        self.dev, self.stream = dev, stream
+    def __init__(self, t, stream):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("the first tensor must be a CUDA tensor")
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        self.over = torch.cuda.stream(stream)
 
     def __enter__(self):
-        s = self.stream
-        if s is not None:
-            if not hasattr(s, "cuda_stream"):
-                s = torch.cuda.ExternalStream(int(s), device=self.dev)
-            if s.device.index != self.dev:
-                raise ValueError(f"stream is on {s.device}, the tensors on cuda:{self.dev}")
-        self.there = torch.cuda.device(self.dev)
-        self.there.__enter__()
-        self.over = None
-        if s is not None:
-            self.over = torch.cuda.stream(s)
-            self.over.__enter__()
+        self.over.__enter__()
 
     def __exit__(self, *exc):
-        if self.over is not None:
-            self.over.__exit__(*exc)
-        self.there.__exit__(*exc)
-
-
-def _device_of(t, name: str, dims, dtypes=None) -> int:
-    """The device of the tensor that says where a call runs."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() not in dims:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
-    return t.get_device()
-
-
-def _ptr(t, name: str, dtype, shape, dev: int):
-    """Pointer of a contiguous tensor of the call's device; None for None."""
-    if t is None:
-        return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _check(t, name, dtype, shape)
-    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-
-
-def _rows_of(t, name: str, dtype, shape, dev: int):
-    """Strides of a tensor [B, H, N, d] whose rows may lie anywhere."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{dev}")
-    s = t.stride()
-    if s[3] != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return s
-
-
-def _rope_tensor(x, y, xs, ys) -> bytes:
-    return _pack_rope_tensor(x.data_ptr(), 0 if y is None else y.data_ptr(), x.shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
-
-
-def _turns(inv_freq, d: int, dev: int):
-    """(pointer, rotated columns) of the frequencies."""
-    if inv_freq is None:
-        return 0, 0
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1 or 2 * inv_freq.numel() > d:
-        raise ValueError(f"inv_freq must be [rot/2] with rot <= {d}")
-    return _ptr(inv_freq, "inv_freq", _F64, inv_freq.shape, dev), 2 * inv_freq.numel()
-
-
-def _layout(name: str) -> int:
-    if name not in _LAYOUT:
-        raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
-    return _LAYOUT[name]
+        self.over.__exit__(*exc)
 
 
 def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", factor: float = 1.0,
@@ -655,38 +593,11 @@ def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half
     `out`, a pair of such tensors, which may be Q and K themselves).  The first 2 * len(inv_freq)
     columns rotate.  Row n is at position start + n, or positions[n] / positions[b, n] (int32).
     inverse: rotate back (the gradient).  Returns (Q', K')."""
-    lib = _lib or load_library()
-    dev = _device_of(Q, "Q", (4,), _DTYPE)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(Q, stream):
             return cca_rope(Q, K, inv_freq, positions, start, layout, factor, inverse, out)
-    dtype = Q.dtype
-    B, Hq, N, d = Q.shape
-    freq, rot = _turns(inv_freq, d, dev)
-    pos = pos_stride = 0
-    if positions is not None:
-        if start:
-            raise ValueError("start and positions exclude each other")
-        shared = isinstance(positions, torch.Tensor) and positions.dim() == 1
-        pos, pos_stride = _ptr(positions, "positions", _I32, (N,) if shared else (B, N), dev), 0 if shared else N
     q, k = (None, None) if out is None else out
-    if (k is None) != (K is None) and out is not None:
-        raise ValueError("out must hold one tensor for each input")
-    if q is None:
-        q = torch.empty((B, Hq, N, d), dtype=dtype, device=Q.device)
-    tensors = _rope_tensor(Q, q, _rows_of(Q, "Q", dtype, (B, Hq, N, d), dev), _rows_of(q, "out Q", dtype, Q.shape, dev))
-    if K is not None:
-        Hkv = K.shape[1] if isinstance(K, torch.Tensor) and K.dim() == 4 else -1
-        ks = _rows_of(K, "K", dtype, (B, Hkv, N, d), dev)
-        if k is None:
-            k = torch.empty((B, Hkv, N, d), dtype=dtype, device=Q.device)
-        tensors += _rope_tensor(K, k, ks, _rows_of(k, "out K", dtype, K.shape, dev))
-    st = lib.cca_rope(tensors, 1 if K is None else 2,
-                      _pack_rope(B, N, d, rot, _layout(layout), _DTYPE[dtype], bool(inverse), factor, freq, pos, pos_stride, start),
-                      _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_rope")
-    return q, k
+    return (_fast or _bound()).rope(Q, K, inv_freq, positions, start, layout, factor, inverse, q, k)
 
 
 def _rows_ready(t):
@@ -727,41 +638,6 @@ def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", f
 
 # ---------------------------------------------------------------- paged caches
 
-def _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, what: str, layers: bool = False) -> bytes:
-    """A pool [pages, Hkv, rows, d] ([layers, pages, ...] where allowed) and its table, packed."""
-    if not isinstance(Kp, torch.Tensor) or not isinstance(Vp, torch.Tensor):
-        raise ValueError(f"{what} pool must be two tensors")
-    shape = Kp.shape
-    if len(shape) != 4 and not (layers and len(shape) == 5):
-        raise ValueError(f"{what} pool must be [{'layers, ' if layers else ''}pages, Hkv, rows, d]")
-    pages, heads, rows, width = shape[-4:]
-    if heads != Hkv or width != d:
-        raise ValueError(f"{what} pool has shape {tuple(shape)}, expected [pages, {Hkv}, rows, {d}]")
-    cols = ptr = 0
-    if table is not None:
-        cols = _columns(table, what + " table")
-        ptr = _ptr(table, what + " table", _I32, (B, cols), dev)
-    if Kp.dtype is not dtype or Vp.dtype is not dtype or Vp.shape != shape or Kp.get_device() != dev or Vp.get_device() != dev \
-            or not Kp.is_contiguous() or not Vp.is_contiguous():
-        _ptr(Kp, what + " K pool", dtype, shape, dev)
-        _ptr(Vp, what + " V pool", dtype, shape, dev)
-    return _pack_pages(Kp.data_ptr(), Vp.data_ptr(), ptr, pages, rows, cols, shape[0] if len(shape) == 5 else 1)
-
-
-def _workspace(t, need: int, device):
-    """A caller's workspace, or one for this call alone, and its bytes."""
-    if t is None:
-        need = max(need, 16)
-        return torch.empty(need, dtype=torch.uint8, device=device), need
-    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous() or t.numel() * t.element_size() < need:
-        raise ValueError(f"workspace must be a buffer of at least {need} bytes on {device}")
-    return t, t.numel() * t.element_size()
-
-
-def _heads_of(Kp) -> int:
-    return Kp.shape[1] if isinstance(Kp, torch.Tensor) and Kp.dim() == 4 else -1
-
-
 def cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq=None, parents=None, counts=None, layout: str = "half",
                     factor: float = 1.0, out=None, dev_status=None, stream=None):
     """The new tokens of a step: rotates Q [B, Hq, T, d] and K [B, Hkv, T, d], and stores K and V
@@ -770,38 +646,16 @@ def cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq=None, parents=None, c
     lens[b] + t.  counts [B]: only the first counts[b] tokens are real.  Tokens that are not real are
     not stored and their query rows are zero.  Without inv_freq nothing rotates (core tokens of a
     prompt are stored that way, with Q None).  Returns the queries, contiguous [B, Hq, T, d]."""
-    lib = _lib or load_library()
-    dev = _device_of(K, "K", (4,), _DTYPE)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(K, stream):
             return cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out, dev_status)
-    dtype = K.dtype
-    B, Hkv, T, d = K.shape
-    none = (0, 0, 0)
-    k = _rope_tensor(K, None, _rows_of(K, "K", dtype, K.shape, dev), none)
-    v = _rope_tensor(V, None, _rows_of(V, "V", dtype, K.shape, dev), none)
-    pool = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw")
-    freq, rot = _turns(inv_freq, d, dev)
-    q = None
-    if Q is not None:
-        qs = _rows_of(Q, "Q", dtype, (B, Q.shape[1] if isinstance(Q, torch.Tensor) and Q.dim() == 4 else -1, T, d), dev)
-        if out is None:
-            out = torch.empty(Q.shape, dtype=dtype, device=Q.device)
-        q = _rope_tensor(Q, out, qs, _rows_of(out, "out", dtype, Q.shape, dev))
-    elif out is not None:
-        raise ValueError("out without Q")
-    st = lib.cca_rope_append(q, k, v, pool, _ptr(lens, "lens", _I32, (B,), dev), _ptr(parents, "parents", _I32, (B, T), dev),
-                             _ptr(counts, "counts", _I32, (B,), dev), _ptr(dev_status, "dev_status", _I32, (1,), dev),
-                             _pack_rope(B, T, d, rot, _layout(layout), _DTYPE[dtype], 0, factor, freq, 0, 0, 0), _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_rope_append")
-    return out
+    return (_fast or _bound()).rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out, dev_status)
 
 
 def tree_workspace_size(B, Hq, Hkv, T, d, g, w, dtype) -> int:
     """Bytes of workspace cca_tree_fwd needs on the current device."""
-    prm = _pack_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype], 0.0, 0, 0, 0)
-    return int(load_library().cca_tree_workspace_size(prm, int(T)))
+    prm = make_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype])
+    return int(load_library().cca_tree_workspace_size(ctypes.byref(prm), int(T)))
 
 
 def cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g: int, w: int, parents=None, O=None, LSE=None,
@@ -812,36 +666,12 @@ def cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g: int, w: int, p
     parents [B, T] is the node before it, -1 for a child of the last committed token, anything else
     (-2) for padding; without parents the nodes are one chain.  Returns (O [B, Hq, T, d], LSE
     [B, Hq, T] fp32); padding nodes have O = 0 and LSE = -inf."""
-    lib = _lib or load_library()
-    dev = _device_of(Q, "Q", (4,), _DTYPE)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(Q, stream):
             return cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g, w, parents, O, LSE, workspace, scale,
                                 dev_status, None, window_mode)
-    dtype, shape = Q.dtype, Q.shape
-    B, Hq, T, d = shape
-    Hkv = _heads_of(Kp)
-    q = _ptr(Q, "Q", dtype, shape, dev)
-    raw = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw")
-    core = _pool(Kcp, Vcp, core_table, B, Hkv, d, dtype, dev, "core")
-    prm = _pack_params(B, Hq, Hkv, 0, d, g, w, _DTYPE[dtype], scale, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0,
-                       window_mode, 0)
-    lens, parents = _ptr(lens, "lens", _I32, (B,), dev), _ptr(parents, "parents", _I32, (B, T), dev)
-    if O is None:
-        O = torch.empty_like(Q)
-        o = O.data_ptr()
-    else:
-        o = _ptr(O, "O", dtype, shape, dev)
-    if LSE is None:
-        LSE = torch.empty((B, Hq, T), dtype=_F32, device=Q.device)
-        lse = LSE.data_ptr()
-    else:
-        lse = _ptr(LSE, "LSE", _F32, (B, Hq, T), dev)
-    workspace, nbytes = _workspace(workspace, lib.cca_tree_workspace_size(prm, T), Q.device)
-    st = lib.cca_tree_fwd(q, raw, core, lens, parents, T, o, lse, prm, workspace.data_ptr(), nbytes, _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_tree_fwd")
-    return O, LSE
+    return (_fast or _bound()).tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g, w, parents, O, LSE, workspace, scale,
+                                        dev_status, window_mode)
 
 
 def cca_pool_pages(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, accepted, g: int, path=None, scale: float = 0.0,
@@ -849,39 +679,12 @@ def cca_pool_pages(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, accepted, g: in
     """Pools the groups that the accepted[b] tokens after lens[b] complete, from raw pages into core
     pages (in place).  Q [B, Hq, T, d] holds the step's queries; the i-th accepted token's is
     Q[b, :, path[b, i]] (path [B, A] int32), or Q[b, :, i] without a path.  Returns (Kcp, Vcp)."""
-    lib = _lib or load_library()
-    dev = _device_of(Q, "Q", (4,), _DTYPE)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(Q, stream):
             return cca_pool_pages(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, accepted, g, path, scale, dev_status, None,
                                   pool_mode)
-    dtype = Q.dtype
-    B, Hq, T, d = Q.shape
-    Hkv = _heads_of(Kp)
-    q = _ptr(Q, "Q", dtype, Q.shape, dev)
-    raw = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw")
-    core = _pool(Kcp, Vcp, core_table, B, Hkv, d, dtype, dev, "core")
-    A = T if path is None else _columns(path, "path")
-    prm = _pack_params(B, Hq, Hkv, 0, d, g, 1, _DTYPE[dtype], scale, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0, 0,
-                       pool_mode)
-    st = lib.cca_pool_pages(q, raw, core, _ptr(lens, "lens", _I32, (B,), dev), _ptr(accepted, "accepted", _I32, (B,), dev),
-                            _ptr(path, "path", _I32, (B, A), dev), A, T, prm, _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_pool_pages")
+    (_fast or _bound()).pool_pages(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, accepted, g, path, scale, dev_status, pool_mode)
     return Kcp, Vcp
-
-
-def _columns(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
-    return t.shape[1]
-
-
-def _book(refs, table):
-    """(device, refs pointer, pages, table pointer, rows, columns) of a pages' book."""
-    dev = _device_of(refs, "refs", (1,))
-    n, cols = refs.shape[0], _columns(table, "table")
-    return dev, _ptr(refs, "refs", _I32, (n,), dev), n, _ptr(table, "table", _I32, table.shape, dev), table.shape[0], cols
 
 
 def cca_pages_reserve(refs, table, lens, extra, rows: int, pairs=None, workspace=None, dev_status=None, stream=None):
@@ -890,84 +693,44 @@ def cca_pages_reserve(refs, table, lens, extra, rows: int, pairs=None, workspace
     ones; a shared page is replaced by one of the row's own.  Returns pairs [B, 2], (old, new) pages
     for cca_pages_copy, (-1, -1) for none.  Too few free pages: nothing changes and dev_status
     becomes CCA_ERR_NO_PAGES."""
-    lib = _lib or load_library()
-    dev, refs_p, n, table_p, B, cols = _book(refs, table)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(refs, stream):
             return cca_pages_reserve(refs, table, lens, extra, rows, pairs, workspace, dev_status)
-    if pairs is None:
-        pairs = torch.empty((B, 2), dtype=_I32, device=refs.device)
-    workspace, nbytes = _workspace(workspace, lib.cca_pages_reserve_workspace_size(B, cols), refs.device)
-    st = lib.cca_pages_reserve(refs_p, n, table_p, B, cols, rows, _ptr(lens, "lens", _I32, (B,), dev),
-                               _ptr(extra, "extra", _I32, (B,), dev), _ptr(pairs, "pairs", _I32, (B, 2), dev),
-                               workspace.data_ptr(), nbytes, _ptr(dev_status, "dev_status", _I32, (1,), dev), _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_pages_reserve")
-    return pairs
+    return (_fast or _bound()).pages_reserve(refs, table, lens, extra, rows, pairs, workspace, dev_status)
 
 
 def cca_pages_fork(refs, table, src, dst, lens, rows: int, dev_status=None, stream=None):
     """Table rows dst [n] become second holders of the pages of rows src [n] (the first
     ceil(lens[src] / rows) entries), in place.  The dst rows must hold no pages."""
-    lib = _lib or load_library()
-    dev, refs_p, n, table_p, B, cols = _book(refs, table)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(refs, stream):
             return cca_pages_fork(refs, table, src, dst, lens, rows, dev_status)
-    count = src.numel() if isinstance(src, torch.Tensor) else -1
-    st = lib.cca_pages_fork(refs_p, n, table_p, B, cols, rows, _ptr(src, "src", _I32, (count,), dev),
-                            _ptr(dst, "dst", _I32, (count,), dev), count, _ptr(lens, "lens", _I32, (B,), dev),
-                            _ptr(dev_status, "dev_status", _I32, (1,), dev), _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_pages_fork")
+    (_fast or _bound()).pages_fork(refs, table, src, dst, lens, rows, dev_status)
 
 
 def cca_pages_free(refs, table, first, last, dev_status=None, stream=None):
     """Entries [first[b], last[b]) of every table row give up their pages, in place."""
-    lib = _lib or load_library()
-    dev, refs_p, n, table_p, B, cols = _book(refs, table)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(refs, stream):
             return cca_pages_free(refs, table, first, last, dev_status)
-    st = lib.cca_pages_free(refs_p, n, table_p, B, cols, _ptr(first, "first", _I32, (B,), dev),
-                            _ptr(last, "last", _I32, (B,), dev), _ptr(dev_status, "dev_status", _I32, (1,), dev), _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_pages_free")
+    (_fast or _bound()).pages_free(refs, table, first, last, dev_status)
 
 
 def cca_pages_copy(Kp, Vp, pairs, dev_status=None, stream=None):
     """Copies page pairs[i, 0] to page pairs[i, 1] of the pools (every layer of a [layers, pages, ...]
     pool), in place; pairs with a negative entry are skipped."""
-    lib = _lib or load_library()
-    dev = _device_of(Kp, "pool", (4, 5), _DTYPE)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(Kp, stream):
             return cca_pages_copy(Kp, Vp, pairs, dev_status)
-    Hkv, d, dtype = Kp.shape[-3], Kp.shape[-1], Kp.dtype
-    pool = _pool(Kp, Vp, None, 1, Hkv, d, dtype, dev, "the", True)
-    n = pairs.shape[0] if _columns(pairs, "pairs") == 2 else -1
-    prm = _pack_params(1, Hkv, Hkv, 0, d, 1, 1, _DTYPE[dtype], 0.0, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0, 0, 0)
-    st = lib.cca_pages_copy(pool, _ptr(pairs, "pairs", _I32, (n, 2), dev), n, prm, _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_pages_copy")
+    (_fast or _bound()).pages_copy(Kp, Vp, pairs, dev_status)
     return Kp, Vp
 
 
 def cca_pages_compact(Kp, Vp, table, lens, path, accepted, dev_status=None, stream=None):
     """Keeps the accepted nodes of a drafted tree: raw row lens[b] + path[b, i] moves to row
     lens[b] + i for i < accepted[b], K and V, every layer, in place.  path [B, A] rises."""
-    lib = _lib or load_library()
-    dev = _device_of(Kp, "pool", (4, 5), _DTYPE)
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
+    if stream is not None:
+        with _On(Kp, stream):
             return cca_pages_compact(Kp, Vp, table, lens, path, accepted, dev_status)
-    Hkv, d, dtype = Kp.shape[-3], Kp.shape[-1], Kp.dtype
-    A = _columns(path, "path")
-    B = path.shape[0]
-    pool = _pool(Kp, Vp, table, B, Hkv, d, dtype, dev, "raw", True)
-    prm = _pack_params(B, Hkv, Hkv, 0, d, 1, 1, _DTYPE[dtype], 0.0, _ptr(dev_status, "dev_status", _I32, (1,), dev) or 0, 0, 0)
-    st = lib.cca_pages_compact(pool, _ptr(lens, "lens", _I32, (B,), dev), _ptr(path, "path", _I32, (B, A), dev), A,
-                               _ptr(accepted, "accepted", _I32, (B,), dev), prm, _raw_stream(dev))
-    if st != CCA_OK:
-        raise CcaError(st, "cca_pages_compact")
+    (_fast or _bound()).pages_compact(Kp, Vp, table, lens, path, accepted, dev_status)
     return Kp, Vp

@@ -1,16 +1,19 @@
-"""Build libcca.so in-tree with nvcc for sm_103a (one -gencode, translation units in parallel)."""
+"""Build libcca.so in-tree with nvcc for sm_103a (one -gencode, translation units in parallel), and
+the CPython binding of its rotary and paged calls with the host compiler."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcca.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["cca_api.cu", "pool.cu", "attn_f32.cu", "attn_tc.cu", "decode.cu", "bwd.cu", "bwd_tc.cu", "host_pipeline.cu",
            "rope.cu", "pages.cu", "pool_pages.cu", "tree.cu", "tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -24,6 +27,24 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def cxx() -> str:
+    for cand in (os.environ.get("CXX"), shutil.which("g++"), shutil.which("c++")):
+        if cand and os.path.exists(cand):
+            return cand
+    raise RuntimeError("no C++ compiler found")
+
+
+def _binding_command(out: str) -> list[str]:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    return [cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[x for i in inc for x in ("-I", i)], os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
 def _deps_mtime() -> float:
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", f)
                                                                   for f in os.listdir(os.path.join(ROOT, "include"))]
@@ -31,7 +52,7 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime() for p in (LIB, BINDING)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -47,8 +68,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        tmp = BINDING + ".tmp%d" % os.getpid()
+        r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

@@ -1,7 +1,6 @@
-"""Host-only checks of the rotary and paged calls: packed structures, workspace sizes, and every
-refusal that needs no GPU (the pointers are never dereferenced)."""
+"""Host-only checks of the rotary and paged calls: workspace sizes, and every refusal that needs no
+GPU (the pointers are never dereferenced), of the C ABI and of the binding."""
 import ctypes
-import struct
 
 import pytest
 import torch
@@ -19,29 +18,23 @@ def lib():
     return api.load_library()
 
 
-@pytest.mark.parametrize("pack,mirror", [(api._pack_params, api.CcaParams), (api._pack_rope, api.CcaRopeParams),
-                                         (api._pack_rope_tensor, api.CcaRopeTensor), (api._pack_pages, api.CcaPages)])
-def test_packed_structures_are_the_mirrors(pack, mirror):
-    """Every field lands where the ctypes mirror has it."""
-    fields = []
-    for name, kind in mirror._fields_:
-        fields += [(name, i) for i in range(kind._length_)] if hasattr(kind, "_length_") else [(name, None)]
-    values = [float(i + 2) if dict(mirror._fields_)[n] is ctypes.c_float else i + 2 for i, (n, _) in enumerate(fields)]
-    m = mirror.from_buffer_copy(pack(*values).ljust(ctypes.sizeof(mirror), b"\0"))
-    for v, (n, i) in zip(values, fields):
-        got = getattr(m, n)
-        assert (got if i is None else got[i]) == v, n
-    assert len(pack(*values)) == ctypes.sizeof(mirror)
+def rope_params(*v):
+    return ctypes.byref(api.CcaRopeParams(*v))
+
+
+def rope_tensors(*each):
+    """x, y, H, three strides of x, three of y; one or more tensors."""
+    return (api.CcaRopeTensor * len(each))(*[api.CcaRopeTensor(*e[:3], (ctypes.c_int64 * 3)(*e[3:6]), (ctypes.c_int64 * 3)(*e[6:9]))
+                                             for e in each])
 
 
 def rope_call(lib, x=None, y=None, n=1, xs=(8192, 4096, 64), ys=None, H=2, second=None, **kw):
     prm = dict(B=1, N=64, d=64, rot=64, layout=0, dtype=api.CCA_F32, inverse=0, factor=1.0, inv_freq=P[8], positions=0,
                pos_stride=0, start=0)
     prm.update(kw)
-    t = api._pack_rope_tensor(P[0] if x is None else x, P[1] if y is None else y, H, *xs, *(ys or xs))
-    if second is not None:
-        t += api._pack_rope_tensor(*second)
-    return lib.cca_rope(t, n, api._pack_rope(*prm.values()), None)
+    first = (P[0] if x is None else x, P[1] if y is None else y, H, *xs, *(ys or xs))
+    t = rope_tensors(first, *([second] if second is not None else []))
+    return lib.cca_rope(t, n, rope_params(*prm.values()), None)
 
 
 @pytest.mark.parametrize("kw", [
@@ -62,8 +55,8 @@ def test_rope_refuses_two_tensors_that_meet(lib):
     assert rope_call(lib, n=2, second=(P[1], P[2], 2, *s, *s)) == BAD            # the second reads the first's output
     assert rope_call(lib, y=P[0], n=2, second=(P[0], P[0], 2, *s, *s)) == BAD    # the same tensor twice in place
     assert rope_call(lib, d=96, rot=64) == UNSUP
-    assert lib.cca_rope(None, 1, api._pack_rope(1, 64, 64, 64, 0, 1, 0, 1.0, P[8], 0, 0, 0), None) == BAD
-    assert lib.cca_rope(api._pack_rope_tensor(P[0], P[1], 2, *s, *s), 1, None, None) == BAD
+    assert lib.cca_rope(None, 1, rope_params(1, 64, 64, 64, 0, 1, 0, 1.0, P[8], 0, 0, 0), None) == BAD
+    assert lib.cca_rope(rope_tensors((P[0], P[1], 2, *s, *s)), 1, None, None) == BAD
 
 
 def append_call(lib, q=True, kv=None, pages=None, lens=P[4], parents=0, counts=0, status=0, **kw):
@@ -71,12 +64,12 @@ def append_call(lib, q=True, kv=None, pages=None, lens=P[4], parents=0, counts=0
                pos_stride=0, start=0)
     prm.update(kw)
     s = (4 * 64 * 2, 4 * 64, 64)
-    t = lambda x, y: api._pack_rope_tensor(x, y, 2, *s, *s)  # noqa: E731
+    t = lambda x, y: rope_tensors((x, y, 2, *s, *s))  # noqa: E731
     k, v = kv or (P[2], P[3])
     pg = dict(K=P[5], V=P[6], table=P[7], n_pages=4, rows=16, cols=2, layers=1)
     pg.update(pages or {})
-    return lib.cca_rope_append(t(P[0], P[1]) if q else None, t(k, 0), t(v, 0), api._pack_pages(*pg.values()), lens or None,
-                               parents or None, counts or None, status or None, api._pack_rope(*prm.values()), None)
+    return lib.cca_rope_append(t(P[0], P[1]) if q else None, t(k, 0), t(v, 0), ctypes.byref(api.CcaPages(*pg.values())),
+                               lens or None, parents or None, counts or None, status or None, rope_params(*prm.values()), None)
 
 
 @pytest.mark.parametrize("kw", [
@@ -97,13 +90,13 @@ def test_append_tree_limit(lib):
 def params(**kw):
     p = dict(B=2, Hq=4, Hkv=2, N=0, d=128, g=16, w=64, dtype=api.CCA_BF16, scale=0.0, status=0, window_mode=0, pool_mode=0)
     p.update(kw)
-    return api._pack_params(*p.values())
+    return ctypes.pointer(api.CcaParams(*p.values()))
 
 
 def pages(**kw):
     p = dict(K=P[0], V=P[1], table=P[2], n_pages=4, rows=16, cols=8, layers=1)
     p.update(kw)
-    return api._pack_pages(*p.values())
+    return ctypes.pointer(api.CcaPages(*p.values()))
 
 
 CORE = dict(K=P[3], V=P[4], table=P[5], rows=4)
@@ -230,4 +223,16 @@ def test_frequencies_on_the_cpu():
     f, _ = api.rope_frequencies(8, 10000.0, "bands", 4.0, device="cpu")
     keep = (0.001 * 8192 / (2 * 3.141592653589793) - 1) / 3
     assert f[0] == 1.0 and f[3].item() == pytest.approx(0.001 * (keep + (1 - keep) / 4), rel=1e-12)
-    assert struct.calcsize("d") == f.element_size()
+
+
+def test_binding_refuses_arguments_before_tensors_are_used(lib):
+    from sparse_long_context_cca_gb300 import _binding
+    with pytest.raises(TypeError):
+        _binding.rope(1)
+    for args in ((None,) * 10, (3,) * 10, ("Q",) * 10):
+        with pytest.raises(ValueError):
+            _binding.rope(*args)
+    with pytest.raises(ValueError):
+        _binding.bind(api.CcaError, {"cca_rope": 0})
+    with pytest.raises(TypeError):
+        _binding.bind(api.CcaError)
