@@ -600,40 +600,12 @@ def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half
     return (_fast or _bound()).rope(Q, K, inv_freq, positions, start, layout, factor, inverse, q, k)
 
 
-def _rows_ready(t):
-    """t itself where its rows can be read in place, a contiguous copy otherwise."""
-    if t is None:
-        return None
-    s = t.stride()
-    if s[3] == 1 and (s[0] | s[1] | s[2]) * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0:
-        return t
-    return t.contiguous()
-
-
-class CcaRopeFunction(torch.autograd.Function):
-    """Autograd wrapper of cca_rope.  The rotation is linear, so its gradient is the rotation back, by
-    the same kernel, and that can be differentiated again."""
-
-    @staticmethod
-    def forward(ctx, Q, K, inv_freq, positions, start, layout, factor, inverse):
-        ctx.save_for_backward(inv_freq, positions)
-        ctx.cfg = (start, layout, factor, inverse)
-        return cca_rope(_rows_ready(Q), _rows_ready(K), inv_freq, positions, start, layout, factor, inverse)
-
-    @staticmethod
-    def backward(ctx, dq, dk):
-        inv_freq, positions = ctx.saved_tensors
-        start, layout, factor, inverse = ctx.cfg
-        turn = CcaRopeFunction.apply if torch.is_grad_enabled() else cca_rope
-        gq, gk = turn(_rows_ready(dq), _rows_ready(dk), inv_freq, positions, start, layout, factor, not inverse)
-        return gq, gk, None, None, None, None, None, None
-
-
 def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", factor: float = 1.0):
-    """cca_rope with gradients for Q and K (or Q alone, with K None): returns (Q', K').  As with any autograd
-    function, a backward pass is captured into a CUDA graph together with its forward pass, from
-    leaves that no eager graph still holds."""
-    return CcaRopeFunction.apply(Q, K, inv_freq, positions, start, layout, factor, False)
+    """cca_rope with gradients for Q and K (or Q alone, with K None): returns (Q', K').  The gradient is
+    the rotation back, by the same kernel, and can be differentiated again.  Rows that cannot be read
+    in place are copied first.  As with any autograd function, a backward pass is captured into a CUDA
+    graph together with its forward pass, from leaves that no eager graph still holds."""
+    return (_fast or _bound()).rope_grad(Q, K, inv_freq, positions, start, layout, factor)
 
 
 # ---------------------------------------------------------------- paged caches

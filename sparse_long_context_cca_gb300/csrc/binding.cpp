@@ -5,6 +5,7 @@
 // linked: api.py hands over their addresses with bind().
 #include <Python.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -227,42 +228,173 @@ int layout(PyObject *o) {
     refuse("layout must be 'half' or 'interleaved'");
 }
 
+// What a rotation needs besides the tensors it turns.
+struct Turn {
+    at::Tensor inv_freq, positions;  // positions: undefined without
+    int64_t start = 0;
+    int layout = 0;
+    float factor = 1.f;
+    bool inverse = false;
+    // Q, K, inv_freq, positions, start, layout, factor
+    Turn(PyObject *const *a, const at::Tensor &q, int dev) {
+        cca_rope_params_t p = {};
+        frequencies(a[2], q.size(3), dev, p);
+        if (!none(a[2])) inv_freq = THPVariable_Unpack(a[2]);
+        start = integer(a[4], "start");
+        if (!none(a[3])) {
+            if (start != 0) refuse("start and positions exclude each other");
+            positions = tensor(a[3], "positions");
+            if (positions.dim() == 1) words(a[3], "positions", {q.size(2)}, dev);
+            else words(a[3], "positions", {q.size(0), q.size(2)}, dev);
+        }
+        layout = ::layout(a[5]);
+        factor = real(a[6], "factor");
+    }
+    Turn() = default;
+    cca_rope_params_t params(const at::Tensor &q, int dtype) const {
+        cca_rope_params_t p = {};
+        p.B = static_cast<int32_t>(q.size(0));
+        p.N = static_cast<int32_t>(q.size(2));
+        p.d = static_cast<int32_t>(q.size(3));
+        p.dtype = dtype;
+        if (inv_freq.defined()) {
+            p.inv_freq = static_cast<const double *>(inv_freq.data_ptr());
+            p.rot = static_cast<int32_t>(2 * inv_freq.numel());
+        }
+        if (positions.defined()) {
+            p.positions = static_cast<const int32_t *>(positions.data_ptr());
+            p.pos_stride = positions.dim() == 1 ? 0 : p.N;
+        }
+        p.start = start;
+        p.layout = layout;
+        p.factor = factor;
+        p.inverse = inverse;
+        return p;
+    }
+};
+
+// Queries and (where there are any) keys that belong together.
+int check_pair(PyObject *const *a, const at::Tensor &q, int dev) {
+    size32(q.size(0), "batch"), size32(q.size(2), "rows"), size32(q.size(3), "head dimension");
+    if (!none(a[1])) same(a[1], "K", q.scalar_type(), {q.size(0), leader(a[1], "K").size(1), q.size(2), q.size(3)}, dev);
+    return dtype_of(q, "Q");
+}
+
 // Q, K, inv_freq, positions, start, layout, factor, inverse, out Q, out K
 PyObject *rope(PyObject *const *a) {
     const at::Tensor &q = leader(a[0], "Q");
     const Place at(q);
-    const int64_t B = q.size(0), N = q.size(2), d = q.size(3);
-    cca_rope_params_t p = {};
-    p.B = size32(B, "batch");
-    p.N = size32(N, "rows");
-    p.d = size32(d, "head dimension");
-    p.dtype = dtype_of(q, "Q");
-    frequencies(a[2], d, at.dev, p);
-    p.start = integer(a[4], "start");
-    if (!none(a[3])) {
-        if (p.start != 0) refuse("start and positions exclude each other");
-        const bool shared = tensor(a[3], "positions").dim() == 1;
-        p.positions = shared ? words(a[3], "positions", {N}, at.dev) : words(a[3], "positions", {B, N}, at.dev);
-        p.pos_stride = shared ? 0 : N;
-    }
-    p.layout = layout(a[5]);
-    p.factor = real(a[6], "factor");
-    p.inverse = PyObject_IsTrue(a[7]) == 1;
+    const int dtype = check_pair(a, q, at.dev);
+    Turn turn(a, q, at.dev);
+    turn.inverse = PyObject_IsTrue(a[7]) == 1;
     const bool two = !none(a[1]);
-    if (!two && !none(a[9])) refuse("out must hold one tensor for each input");
-    if (two && none(a[8]) != none(a[9])) refuse("out must hold one tensor for each input");
+    if ((!two && !none(a[9])) || (two && none(a[8]) != none(a[9]))) refuse("out must hold one tensor for each input");
     at::Tensor outs[2];
     cca_rope_tensor_t t[2];
     for (int i = 0; i < (two ? 2 : 1); ++i) {
-        const char *name = i == 0 ? "Q" : "K";
-        const at::Tensor &x = i == 0 ? q : leader(a[1], "K");
-        if (i == 1) same(a[1], "K", q.scalar_type(), {B, x.size(1), N, d}, at.dev);
+        const at::Tensor &x = THPVariable_Unpack(a[i]);
         outs[i] = none(a[8 + i]) ? at::empty(x.sizes(), q.options()) : same(a[8 + i], "out", q.scalar_type(), x.sizes(), at.dev);
-        t[i] = rows(x, &outs[i], name);
+        t[i] = rows(x, &outs[i], i == 0 ? "Q" : "K");
     }
+    const cca_rope_params_t p = turn.params(q, dtype);
     check(lib.rope(t, two ? 2 : 1, &p, at.stream), "cca_rope");
     PyObject *first = THPVariable_Wrap(outs[0]);
     if (two) return Py_BuildValue("(NN)", first, THPVariable_Wrap(outs[1]));
+    return Py_BuildValue("(NO)", first, Py_None);
+}
+
+// Autograd of the rotation.  It is linear: the gradient is the rotation back, by the same kernel,
+// and can be differentiated again.  The backward pass runs on the engine's thread, without Python.
+struct RopeFunction : torch::autograd::Function<RopeFunction> {
+    using List = torch::autograd::variable_list;
+
+    // x itself where its rows can be read in place, a contiguous copy otherwise
+    static at::Tensor ready(const at::Tensor &x) {
+        const int64_t es = x.element_size();
+        const bool in_place = x.stride(3) == 1 && (x.stride(0) | x.stride(1) | x.stride(2)) * es % 16 == 0 &&
+                              reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
+        return in_place ? x : x.contiguous();
+    }
+
+    static List turned(const Turn &turn, const List &in) {
+        const c10::cuda::CUDAGuard guard(in[0].device());
+        List out;
+        cca_rope_tensor_t t[2];
+        List held;
+        for (size_t i = 0; i < in.size(); ++i) {
+            held.push_back(ready(in[i]));
+            out.push_back(at::empty(in[i].sizes(), in[i].options()));
+            cca_rope_tensor_t &r = t[i];
+            r = {};
+            r.x = held[i].data_ptr();
+            r.y = out[i].data_ptr();
+            r.H = static_cast<int32_t>(in[i].size(1));
+            for (int k = 0; k < 3; ++k) {
+                r.x_stride[k] = held[i].stride(k);
+                r.y_stride[k] = out[i].stride(k);
+            }
+        }
+        const cca_rope_params_t p = turn.params(in[0], in[0].scalar_type() == at::kBFloat16 ? CCA_BF16 : CCA_F32);
+        const int status = lib.rope(t, static_cast<int>(in.size()), &p, c10::cuda::getCurrentCUDAStream(in[0].get_device()).stream());
+        TORCH_CHECK(status == CCA_OK, "cca_rope: status ", status);
+        return out;
+    }
+
+    static List forward(torch::autograd::AutogradContext *ctx, const at::Tensor &q, const c10::optional<at::Tensor> &k,
+                        const at::Tensor &inv_freq, const c10::optional<at::Tensor> &positions, int64_t start, int64_t layout,
+                        double factor, bool inverse) {
+        ctx->save_for_backward({inv_freq, positions.has_value() ? *positions : at::Tensor()});
+        ctx->saved_data["start"] = start;
+        ctx->saved_data["layout"] = layout;
+        ctx->saved_data["factor"] = factor;
+        ctx->saved_data["inverse"] = inverse;
+        ctx->saved_data["two"] = k.has_value();
+        Turn turn;
+        turn.inv_freq = inv_freq;
+        if (positions.has_value()) turn.positions = *positions;
+        turn.start = start;
+        turn.layout = static_cast<int>(layout);
+        turn.factor = static_cast<float>(factor);
+        turn.inverse = inverse;
+        return turned(turn, k.has_value() ? List{q, *k} : List{q});
+    }
+
+    static List backward(torch::autograd::AutogradContext *ctx, const List &grads) {
+        const List saved = ctx->get_saved_variables();
+        const bool two = ctx->saved_data["two"].toBool();
+        Turn turn;
+        turn.inv_freq = saved[0];
+        turn.positions = saved[1];
+        turn.start = ctx->saved_data["start"].toInt();
+        turn.layout = static_cast<int>(ctx->saved_data["layout"].toInt());
+        turn.factor = static_cast<float>(ctx->saved_data["factor"].toDouble());
+        turn.inverse = !ctx->saved_data["inverse"].toBool();
+        List g;
+        if (c10::GradMode::is_enabled()) {
+            g = apply(grads[0], two ? c10::optional<at::Tensor>(grads[1]) : c10::nullopt, turn.inv_freq,
+                      turn.positions.defined() ? c10::optional<at::Tensor>(turn.positions) : c10::nullopt, turn.start,
+                      static_cast<int64_t>(turn.layout), static_cast<double>(turn.factor), turn.inverse);
+        } else {
+            g = turned(turn, two ? List{grads[0], grads[1]} : List{grads[0]});
+        }
+        return {g[0], two ? g[1] : at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
+    }
+};
+
+// Q, K, inv_freq, positions, start, layout, factor
+PyObject *rope_grad(PyObject *const *a) {
+    const at::Tensor &q = leader(a[0], "Q");
+    const Place at(q);
+    check_pair(a, q, at.dev);
+    const Turn turn(a, q, at.dev);
+    if (!turn.inv_freq.defined()) refuse("inv_freq must be a CUDA tensor");
+    const bool two = !none(a[1]);
+    const auto out = RopeFunction::apply(
+        q, two ? c10::optional<at::Tensor>(THPVariable_Unpack(a[1])) : c10::nullopt, turn.inv_freq,
+        turn.positions.defined() ? c10::optional<at::Tensor>(turn.positions) : c10::nullopt, turn.start,
+        static_cast<int64_t>(turn.layout), static_cast<double>(turn.factor), false);
+    PyObject *first = THPVariable_Wrap(out[0]);
+    if (two) return Py_BuildValue("(NN)", first, THPVariable_Wrap(out[1]));
     return Py_BuildValue("(NO)", first, Py_None);
 }
 
@@ -480,6 +612,7 @@ PyObject *bind(PyObject *, PyObject *args) {
 
 #define CCA_ENTRY(name, count) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(entry<name, count>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CCA_ENTRY(rope, 10),
+                         CCA_ENTRY(rope_grad, 7),
                          CCA_ENTRY(rope_append, 14),
                          CCA_ENTRY(tree_fwd, 17),
                          CCA_ENTRY(pool_pages, 14),
