@@ -17,6 +17,14 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// The page kernels of a step follow one another, so each is launched as a programmatic dependent
+// of the kernel before it: its blocks may be scheduled while that one drains, wait for its
+// completion before they read anything, and let their own dependents be scheduled.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
 __device__ __forceinline__ void report(int32_t *status, int code) {
     if (status != nullptr) *status = code;
 }
@@ -68,7 +76,10 @@ __device__ int block_scan(int v, int *sm_warp, int &total) {
 // its own one at a time).
 __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const ReserveArgs a) {
     __shared__ int sm_warp[RESERVE_WARPS];
+    __shared__ int32_t sm_count[RESERVE_THREADS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t *const count = a.B <= RESERVE_THREADS ? sm_count : a.count;
+    after_previous();
     // The columns [c0, c1) of row b that its new rows lie in; an empty range for a bad row.
     auto range = [&](int b, int &c0, int &c1) {
         const int len = a.lens[b], ex = a.extra[b];
@@ -115,65 +126,68 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
             if (need) a.want[static_cast<int64_t>(b) * a.cols + n + __popc(m & ((1u << lane) - 1u))] = c;
             n += __popc(m);
         }
-        if (lane == 0) a.count[b] = n;
+        if (lane == 0) count[b] = n;
     }
     __syncthreads();
     // 2. where each row's pages stand among all
     int total = 0;
     for (int base = 0; base < a.B; base += RESERVE_THREADS) {
         const int b = base + tid;
-        const int v = b < a.B ? a.count[b] : 0;
+        const int v = b < a.B ? count[b] : 0;
         int sum;
         const int at = block_scan(v, sm_warp, sum) + total;
-        if (b < a.B) a.count[b] = at;
+        if (b < a.B) count[b] = at;
         total += sum;
     }
-    // 3. are there enough free pages?  Stops as soon as there are.
-    auto free4 = [&](int64_t p0, bool (&f)[4]) {
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = p0 + i < a.n_pages && a.refs[p0 + i] == 0;
-            n += f[i];
-        }
-        return n;
-    };
-    int found = 0;
-    int64_t stop = 0;  // pages below `stop` hold the first `found` free ones
-    while (found < total && stop < a.n_pages) {
-        bool f[4];
-        int sum;
-        block_scan(free4(stop + 4 * tid, f), sm_warp, sum);
-        found += sum;
-        stop += 4 * RESERVE_THREADS;
-    }
-    const bool fits = found >= total;
-    if (!fits && tid == 0) report(a.status, CCA_ERR_NO_PAGES);
     for (int b = tid; b < a.B; b += RESERVE_THREADS) {
         a.pairs[2 * b] = -1;
         a.pairs[2 * b + 1] = -1;
     }
-    __syncthreads();
-    if (!fits || total == 0) return;
+    if (total == 0) return;
+    // 3. are there enough free pages?  Stops as soon as there are; usually the first 4096 pages do,
+    // and what was found in them is used below.
+    constexpr int STEP = 4 * RESERVE_THREADS;
+    bool free_page[4];
+    auto look = [&](int64_t p0, int &sum) {  // this thread's four pages from p0 on: free pages before them
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t p = p0 + 4 * tid + i;
+            free_page[i] = p < a.n_pages && a.refs[p] == 0;
+            n += free_page[i];
+        }
+        return block_scan(n, sm_warp, sum);  // ends with a barrier: refs are read before they change
+    };
+    int found = 0, k = 0;
+    int64_t stop = 0;  // the pages below hold the first `found` free ones
+    while (found < total && stop < a.n_pages) {
+        int sum;
+        k = look(stop, sum);
+        found += sum;
+        stop += STEP;
+    }
+    if (found < total) {
+        if (tid == 0) report(a.status, CCA_ERR_NO_PAGES);
+        return;
+    }
     // 4. the k-th place gets the k-th free page.  A place is found by its number: the row by
     // bisection of the rows' first places.
     int k0 = 0;
-    for (int64_t p0 = 0; k0 < total; p0 += 4 * RESERVE_THREADS) {
-        bool f[4];
-        int sum;
-        int k = block_scan(free4(p0 + 4 * tid, f), sm_warp, sum) + k0;  // ends with a barrier: refs are read before they change
+    for (int64_t p0 = 0; k0 < total; p0 += STEP) {
+        int sum = found;
+        if (stop > STEP) k = look(p0, sum) + k0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (!f[i]) continue;
+            if (!free_page[i]) continue;
             if (k < total) {
                 int lo = 0, hi = a.B - 1;  // the last row whose first place is <= k
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
-                    if (a.count[mid] <= k) lo = mid;
+                    if (count[mid] <= k) lo = mid;
                     else hi = mid - 1;
                 }
                 const int b = lo;
-                const int c = a.want[static_cast<int64_t>(b) * a.cols + (k - a.count[b])];
+                const int c = a.want[static_cast<int64_t>(b) * a.cols + (k - count[b])];
                 int32_t *entry = a.table + static_cast<int64_t>(b) * a.cols + c;
                 const int32_t old = *entry;
                 const int page = static_cast<int>(p0 + 4 * tid + i);
@@ -202,6 +216,7 @@ __global__ void __launch_bounds__(128) pages_fork_kernel(int32_t *refs, int n_pa
                                                          int rows, const int32_t *src, const int32_t *dst, int n,
                                                          const int32_t *lens, int32_t *status) {
     const int i = blockIdx.x, tid = threadIdx.x;
+    after_previous();
     const int s = src[i], d = dst[i];
     bool ok = s >= 0 && s < B && d >= 0 && d < B && s != d;
     int bad = !ok;
@@ -235,6 +250,7 @@ __global__ void __launch_bounds__(128) pages_fork_kernel(int32_t *refs, int n_pa
 __global__ void __launch_bounds__(128) pages_free_kernel(int32_t *refs, int n_pages, int32_t *table, int cols,
                                                          const int32_t *first, const int32_t *last, int32_t *status) {
     const int b = blockIdx.x;
+    after_previous();
     const int c0 = max(first[b], 0), c1 = min(last[b], cols);
     for (int c = c0 + static_cast<int>(threadIdx.x); c < c1; c += blockDim.x) {
         int32_t *entry = table + static_cast<int64_t>(b) * cols + c;
@@ -259,6 +275,7 @@ constexpr int COPY_UNROLL = 8;  // 16-byte loads in flight per thread
 __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(uint4 *K, uint4 *V, int64_t page_vecs, int n_pages,
                                                                   const int2 *pairs, int n, int32_t *status) {
     const int i = blockIdx.y, tid = threadIdx.x;
+    after_previous();
     const int2 p = pairs[i];
     if (p.x < 0 || p.y < 0) return;
     int bad = p.x >= n_pages || p.y >= n_pages;
@@ -303,6 +320,7 @@ struct CompactArgs {
 __global__ void __launch_bounds__(COPY_THREADS) pages_compact_kernel(const CompactArgs a) {
     __shared__ int64_t sm_from[TREE_MAX_NODES], sm_to[TREE_MAX_NODES];  // page << 32 | row inside it
     const int b = blockIdx.y, tid = threadIdx.x;
+    after_previous();
     const int n = a.accepted[b], len = a.lens[b];
     int bad = n < 0 || n > a.A || (len < 0 && n > 0);
     if (!bad) {
@@ -403,8 +421,7 @@ int cca_pages_reserve(int32_t *refs, int n_pages, int32_t *table, int B, int col
     a.count = static_cast<int32_t *>(workspace);
     a.want = a.count + B;
     a.status = dev_status;
-    pages_reserve_kernel<<<1, RESERVE_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return from_cuda(cudaGetLastError());
+    return from_cuda(start_dependent(pages_reserve_kernel, dim3(1), RESERVE_THREADS, 0, static_cast<cudaStream_t>(stream), a));
 }
 
 int cca_pages_fork(int32_t *refs, int n_pages, int32_t *table, int B, int cols, int rows, const int32_t *src,
@@ -417,9 +434,8 @@ int cca_pages_fork(int32_t *refs, int n_pages, int32_t *table, int B, int cols, 
     int st;
     if ((st = check_device()) != CCA_OK) return st;
     if (n == 0) return CCA_OK;
-    pages_fork_kernel<<<n, 128, 0, static_cast<cudaStream_t>(stream)>>>(refs, n_pages, table, B, cols, rows, src, dst, n,
-                                                                        lens, dev_status);
-    return from_cuda(cudaGetLastError());
+    return from_cuda(start_dependent(pages_fork_kernel, dim3(n), 128, 0, static_cast<cudaStream_t>(stream), refs, n_pages, table, B,
+                                     cols, rows, src, dst, n, lens, dev_status));
 }
 
 int cca_pages_free(int32_t *refs, int n_pages, int32_t *table, int B, int cols, const int32_t *first,
@@ -429,9 +445,8 @@ int cca_pages_free(int32_t *refs, int n_pages, int32_t *table, int B, int cols, 
     if (!good4(refs) || !good4(table) || !good4(first) || !good4(last) || !aligned4(dev_status)) return CCA_ERR_INVALID_ARG;
     int st;
     if ((st = check_device()) != CCA_OK) return st;
-    pages_free_kernel<<<B, 128, 0, static_cast<cudaStream_t>(stream)>>>(refs, n_pages, table, cols, first, last,
-                                                                        dev_status);
-    return from_cuda(cudaGetLastError());
+    return from_cuda(start_dependent(pages_free_kernel, dim3(B), 128, 0, static_cast<cudaStream_t>(stream), refs, n_pages, table, cols,
+                                     first, last, dev_status));
 }
 
 int cca_pages_copy(const cca_pages_t *pages, const int32_t *pairs, int n, const cca_params_t *params, void *stream) {
@@ -453,10 +468,9 @@ int cca_pages_copy(const cca_pages_t *pages, const int32_t *pairs, int n, const 
     if ((st = check_device()) != CCA_OK) return st;
     if (n == 0) return CCA_OK;
     const dim3 grid(static_cast<unsigned>(chunks), n, 2 * pages->layers);
-    pages_copy_kernel<<<grid, COPY_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<uint4 *>(pages->K), static_cast<uint4 *>(pages->V), vecs, pages->n_pages,
-        reinterpret_cast<const int2 *>(pairs), n, params->dev_status);
-    return from_cuda(cudaGetLastError());
+    return from_cuda(start_dependent(pages_copy_kernel, grid, COPY_THREADS, 0, static_cast<cudaStream_t>(stream),
+                                     static_cast<uint4 *>(pages->K), static_cast<uint4 *>(pages->V), vecs, pages->n_pages,
+                                     reinterpret_cast<const int2 *>(pairs), n, params->dev_status));
 }
 
 int cca_pages_compact(const cca_pages_t *pages, const int32_t *lens, const int32_t *path, int A,
@@ -485,9 +499,8 @@ int cca_pages_compact(const cca_pages_t *pages, const int32_t *lens, const int32
     const int64_t blocks = (static_cast<int64_t>(a.Hkv) * a.row_vecs * a.layers * 2 + COPY_THREADS - 1) / COPY_THREADS;
     if (blocks > 0x7fffffff) return CCA_ERR_UNSUPPORTED;
     if ((st = check_device()) != CCA_OK) return st;
-    pages_compact_kernel<<<dim3(static_cast<unsigned>(blocks), params->B), COPY_THREADS, 0,
-                           static_cast<cudaStream_t>(stream)>>>(a);
-    return from_cuda(cudaGetLastError());
+    return from_cuda(start_dependent(pages_compact_kernel, dim3(static_cast<unsigned>(blocks), params->B), COPY_THREADS, 0,
+                                     static_cast<cudaStream_t>(stream), a));
 }
 
 }  // extern "C"

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(PP_WARPS * 32) pool_pages_kernel(const PoolPag
     if (bk >= static_cast<int64_t>(a.B) * a.Hkv) return;
     const int b = static_cast<int>(bk / a.Hkv), kv = static_cast<int>(bk - static_cast<int64_t>(b) * a.Hkv);
     const int r = a.Hq / a.Hkv;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = a.lens[b], got = a.accepted[b];
     if (len < 0 || got < 0 || got > a.A || got > 0x7fffffff - len) {
         if (lane == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(RING_MAX_WARPS * 32) pool_pages_ring_kernel(co
     if (bk >= static_cast<int64_t>(a.B) * a.Hkv) return;
     const int b = static_cast<int>(bk / a.Hkv), kv = static_cast<int>(bk - static_cast<int64_t>(b) * a.Hkv);
     const int r = a.Hq / a.Hkv;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = a.lens[b], got = a.accepted[b];
     if (len < 0 || got < 0 || got > a.A || got > 0x7fffffff - len) {
         if (lane == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
@@ -484,9 +486,8 @@ cudaError_t launch_ring(const PoolPagesArgs &a, cudaStream_t stream) {
         warps_per_block = static_cast<int>((lists * parts + sms - 1) / sms);
     const int64_t blocks = (lists * parts + warps_per_block - 1) / warps_per_block;
     if (blocks > 0x7fffffff) return cudaErrorNotSupported;
-    pool_pages_ring_kernel<T, D><<<static_cast<unsigned>(blocks), warps_per_block * 32, smem, stream>>>(a, static_cast<int>(per_warp),
-                                                                                                 static_cast<int>(parts), stage);
-    return cudaGetLastError();
+    return start_dependent(pool_pages_ring_kernel<T, D>, dim3(static_cast<unsigned>(blocks)), warps_per_block * 32, smem, stream, a,
+                           static_cast<int>(per_warp), static_cast<int>(parts), stage);
 }
 
 }  // namespace
@@ -546,13 +547,11 @@ extern "C" int cca_pool_pages(const void *Q, const cca_pages_t *raw, const cca_p
             return from_cuda(params->d == 128 ? launch_ring<__nv_bfloat16, 128>(a, strm) : launch_ring<__nv_bfloat16, 64>(a, strm));
         return from_cuda(params->d == 128 ? launch_ring<float, 128>(a, strm) : launch_ring<float, 64>(a, strm));
     }
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (params->dtype == CCA_BF16) {
-        if (params->d == 128) pool_pages_kernel<__nv_bfloat16, 128><<<grid, PP_WARPS * 32, 0, strm>>>(a);
-        else pool_pages_kernel<__nv_bfloat16, 64><<<grid, PP_WARPS * 32, 0, strm>>>(a);
-    } else {
-        if (params->d == 128) pool_pages_kernel<float, 128><<<grid, PP_WARPS * 32, 0, strm>>>(a);
-        else pool_pages_kernel<float, 64><<<grid, PP_WARPS * 32, 0, strm>>>(a);
-    }
-    return from_cuda(cudaGetLastError());
+    const dim3 grid(static_cast<unsigned>(blocks));
+    constexpr int threads = PP_WARPS * 32;
+    if (params->dtype == CCA_BF16)
+        return from_cuda(params->d == 128 ? start_dependent(pool_pages_kernel<__nv_bfloat16, 128>, grid, threads, 0, strm, a)
+                                          : start_dependent(pool_pages_kernel<__nv_bfloat16, 64>, grid, threads, 0, strm, a));
+    return from_cuda(params->d == 128 ? start_dependent(pool_pages_kernel<float, 128>, grid, threads, 0, strm, a)
+                                      : start_dependent(pool_pages_kernel<float, 64>, grid, threads, 0, strm, a));
 }

@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a)
                 if (HALF && turn) hi[k].raw = *reinterpret_cast<const R *>(x + k * t.xs[1] + other);
             }
     };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     if (work) load(h0, batch_heads(h0));
 
     for (int i = threadIdx.x; i < half; i += ROPE_THREADS) {
@@ -241,14 +243,11 @@ __global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a)
 }
 
 template <typename T, int V, bool PAGED>
-void launch_one(const RopeArgs &a, dim3 grid, cudaStream_t stream) {
-    if (a.layout == 0) {
-        rope_kernel<T, V, true, PAGED><<<grid, ROPE_THREADS, 0, stream>>>(a);
-    } else {
-        // an interleaved chunk holds whole pairs
-        constexpr int VI = V < 2 ? 2 : V;
-        rope_kernel<T, VI, false, PAGED><<<grid, ROPE_THREADS, 0, stream>>>(a);
-    }
+cudaError_t launch_one(const RopeArgs &a, dim3 grid, cudaStream_t stream) {
+    if (a.layout == 0) return start_dependent(rope_kernel<T, V, true, PAGED>, grid, ROPE_THREADS, 0, stream, a);
+    // an interleaved chunk holds whole pairs
+    constexpr int VI = V < 2 ? 2 : V;
+    return start_dependent(rope_kernel<T, VI, false, PAGED>, grid, ROPE_THREADS, 0, stream, a);
 }
 
 // The widest access that every chunk boundary allows: rows are 16-byte aligned, so it is
@@ -283,19 +282,17 @@ cudaError_t launch_rope_any(int dtype, RopeArgs a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(blocks), groups, PAGED ? a.B : 1);
     if (dtype == CCA_BF16) {
         switch (v) {
-            case 8: launch_one<__nv_bfloat16, 8, PAGED>(a, grid, stream); break;
-            case 4: launch_one<__nv_bfloat16, 4, PAGED>(a, grid, stream); break;
-            case 2: launch_one<__nv_bfloat16, 2, PAGED>(a, grid, stream); break;
-            default: launch_one<__nv_bfloat16, 1, PAGED>(a, grid, stream); break;
-        }
-    } else {
-        switch (v) {
-            case 4: launch_one<float, 4, PAGED>(a, grid, stream); break;
-            case 2: launch_one<float, 2, PAGED>(a, grid, stream); break;
-            default: launch_one<float, 1, PAGED>(a, grid, stream); break;
+            case 8: return launch_one<__nv_bfloat16, 8, PAGED>(a, grid, stream);
+            case 4: return launch_one<__nv_bfloat16, 4, PAGED>(a, grid, stream);
+            case 2: return launch_one<__nv_bfloat16, 2, PAGED>(a, grid, stream);
+            default: return launch_one<__nv_bfloat16, 1, PAGED>(a, grid, stream);
         }
     }
-    return cudaGetLastError();
+    switch (v) {
+        case 4: return launch_one<float, 4, PAGED>(a, grid, stream);
+        case 2: return launch_one<float, 2, PAGED>(a, grid, stream);
+        default: return launch_one<float, 1, PAGED>(a, grid, stream);
+    }
 }
 
 // ---------------------------------------------------------------- argument checks

@@ -25,7 +25,6 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "../../include/cca.h"
 #include "internal.h"
@@ -649,10 +648,10 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM
     while (lanes / 2 >= a.R) lanes /= 2;
     const int row = blockIdx.y * JOIN_ROWS + (lane & (lanes - 1)), step = 32 / lanes;
     // Where the list lies among all follows from the lengths, which the kernel before has waited
-    // for, so it is found while that one still runs.
+    // for, so it is found while that one still runs (from L2, where its wait has seen them).
     int all = 0, f0 = 0;
     for (int i = threadIdx.x; i < a.B; i += 128) {
-        const int n = key_list(a, i).tiles * a.Hkv;
+        const int n = key_list_of(a, __ldcg(a.lens + i)).tiles * a.Hkv;
         all += n;
         if (i < b) f0 += n;
     }
@@ -666,7 +665,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM
     all = sm_sum[0][0] + sm_sum[0][1] + sm_sum[0][2] + sm_sum[0][3];
     f0 = sm_sum[1][0] + sm_sum[1][1] + sm_sum[1][2] + sm_sum[1][3];
     const Split split = make_split(a, all);
-    const int tiles = key_list(a, b).tiles;
+    const int tiles = key_list_of(a, __ldcg(a.lens + b)).tiles;
     const int s = f0 + kv * tiles, e = s + tiles;
     const int y0 = split.owner(s), y1 = split.owner(e - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -752,25 +751,6 @@ cudaError_t resident(int smem, int &per_sm) {
     return e;
 }
 
-template <typename K>
-cudaError_t start(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, const TreeArgs &a, int BM) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if constexpr (std::is_same<K, void (*)(TreeArgs)>::value) {
-        return cudaLaunchKernelEx(&cfg, kernel, a);
-    } else {
-        return cudaLaunchKernelEx(&cfg, kernel, a, BM);
-    }
-}
-
 constexpr int MAX_CTAS_PER_SM = 4;
 
 // bf16 with d = 128 runs on tcgen05, whatever the rows: one row of 32 heads at 32 K took 29.4 us
@@ -800,7 +780,7 @@ cudaError_t run_join(J join, const TreeArgs &a, int BM, int sms, cudaStream_t st
     dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_ROWS - 1) / JOIN_ROWS, 4);
     // eight blocks are resident per SM
     while (grid.z > 1 && static_cast<int64_t>(grid.x) * grid.y * grid.z > 8ll * sms) grid.z /= 2;
-    return start(join, grid, 128, 0, stream, a, BM);
+    return start_dependent(join, grid, 128, 0, stream, a, BM);
 }
 
 template <auto kernel, typename J>
@@ -813,7 +793,7 @@ cudaError_t run_tree(J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t
     a.n_mt = (a.R + BM - 1) / BM;
     a.groups = per_sm * sms / a.n_mt;
     if (a.groups < 1) a.groups = 1;
-    e = start(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a, BM);
+    e = start_dependent(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a);
     if (e != cudaSuccess) return e;
     return run_join(join, a, BM, sms, stream);
 }

@@ -47,10 +47,9 @@ struct KeyList {
     int tiles;
 };
 
-__device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) {
+__device__ __forceinline__ KeyList key_list_of(const TreeArgs &a, int len) {
     KeyList k = {};
     k.tiles = 1;
-    const int len = a.lens[b];
     // a length outside the table: an empty list, and one tile in which its rows are written
     if (len < 0 || len > 0x7fffffff - 2 * TREE_MAX_NODES ||
         static_cast<int64_t>(len) + a.T > static_cast<int64_t>(a.rows) * a.cols)
@@ -79,6 +78,8 @@ __device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) {
     k.tiles = k.run_tiles + ((k.n + (1 << a.tile_log2) - 1) >> a.tile_log2);
     return k;
 }
+
+__device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) { return key_list_of(a, a.lens[b]); }
 
 // The row of its pool that row `at` of a sequence lies in, -1 where no page is.
 __device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bool core, int at) {

@@ -735,17 +735,8 @@ cudaError_t launch_halves(const CUtensorMap (&map)[4], const TreeArgs &a, unsign
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(1, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.groups) * a.n_mt);
-    cfg.blockDim = dim3(Layout<HALVES>::THREADS);
-    cfg.dynamicSmemBytes = Layout<HALVES>::bytes(a.T);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_tc_kernel<HALVES>, map[0], map[1], map[2], map[3], a, lim, skip_loads);
+    return start_dependent(tree_tc_kernel<HALVES>, dim3(static_cast<unsigned>(a.groups) * a.n_mt), Layout<HALVES>::THREADS,
+                           static_cast<int>(Layout<HALVES>::bytes(a.T)), stream, map[0], map[1], map[2], map[3], a, lim, skip_loads);
 }
 
 }  // namespace

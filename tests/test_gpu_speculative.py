@@ -216,3 +216,61 @@ def test_step_in_one_graph():
         results.append(got)
     for a, b in zip(*results):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def branch(refs, table, K, V, lens, extra, src, dst, last, gate):
+    """Forked rows get room, their shared pages are copied, the old rows end; `gate` makes the lengths."""
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    side.wait_stream(here)
+    with torch.cuda.stream(side):
+        late = lens + gate.sum(dtype=torch.int32)      # a kernel on another stream, still running
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    here.wait_stream(side)
+    api.cca_pages_fork(refs, table, src, dst, late, K.shape[-2], dev_status=status)
+    pairs = api.cca_pages_reserve(refs, table, late, extra, K.shape[-2], dev_status=status)
+    api.cca_pages_copy(K, V, pairs, dev_status=status)
+    kept = pairs.clone()                               # a copy between two of the calls
+    api.cca_pages_free(refs, table, torch.zeros_like(lens), last, dev_status=status)
+    return kept, status
+
+
+def test_calls_behind_copies_and_other_streams():
+    """The page calls may be scheduled while the work before them drains; they wait for it, also
+    where it is a copy or another stream's, eager and captured."""
+    B, cols, rows, n = 6, 9, 16, 40
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    K0, V0 = (torch.randn(n, 2, rows, 64, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    lens, grown = i32([70, 33, 70, 33, 9, 0]), [75, 38]  # the forked rows are as long as their sources
+    held, extra = i32([75, 38, 0, 0, 14, 0]), i32([0, 0, 20, 20, 0, 0])
+    src, dst, last = i32([0, 1]), i32([2, 3]), i32([cols, cols, 0, 0, 0, 0])
+    gate = torch.zeros(64 << 20, dtype=torch.int8, device="cuda")
+    gate[:5] = 1                                       # lengths grow by 5
+    results = []
+    for captured in (False, True):
+        refs, table = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.full((B, cols), -1, dtype=torch.int32, device="cuda")
+        api.cca_pages_reserve(refs, table, torch.zeros_like(lens), held, rows)
+        K, V = K0.clone(), V0.clone()
+        start = refs.clone(), table.clone()
+        args = refs, table, K, V, lens, extra, src, dst, last, gate
+        branch(*args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        if captured:
+            with torch.cuda.graph(graph):
+                kept, status = branch(*args)
+        refs.copy_(start[0]), table.copy_(start[1]), K.copy_(K0), V.copy_(V0)
+        if captured:
+            graph.replay()
+        else:
+            kept, status = branch(*args)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        results.append([t.clone() for t in (refs, table, K, V, kept)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    refs, table, K, V, kept = results[0]
+    for b, s in ((2, 0), (3, 1)):
+        old, new = kept[b].tolist()
+        assert old >= 0 and new == table[b][grown[s] // rows].item() and refs[new].item() == 1
+        assert torch.equal(K[new], K0[old]) and torch.equal(V[new], V0[old])
+    assert (table[:2] == -1).all() and kept[4].tolist() == [-1, -1]
