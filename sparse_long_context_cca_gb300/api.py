@@ -507,6 +507,7 @@ class CcaAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dO):
+        (_fast or _bound()).check_leaves()
         Q, K, V, Kc, Vc, O, LSE = ctx.saved_tensors
         g, w, scale, pool_mode, window_mode = ctx.cfg
         dQ, dK, dV = cca_prefill_bwd(Q, K, V, Kc, Vc, O, LSE, dO.contiguous().to(Q.dtype), g, w, scale,
@@ -604,7 +605,8 @@ def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", f
     """cca_rope with gradients for Q and K (or Q alone, with K None): returns (Q', K').  The gradient is
     the rotation back, by the same kernel, and can be differentiated again.  Rows that cannot be read
     in place are copied first.  As with any autograd function, a backward pass is captured into a CUDA
-    graph together with its forward pass, from leaves that no eager graph still holds."""
+    graph together with its forward pass, from leaves that no eager graph still holds on the default
+    stream (RuntimeError where one does)."""
     return (_fast or _bound()).rope_grad(Q, K, inv_freq, positions, start, layout, factor)
 
 

@@ -6,14 +6,18 @@
 #include <Python.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cstdint>
 #include <cstring>
+#include <unordered_set>
+#include <vector>
 
 #include "../../include/cca.h"
 
@@ -305,6 +309,28 @@ PyObject *rope(PyObject *const *a) {
 
 // Autograd of the rotation.  It is linear: the gradient is the rotation back, by the same kernel,
 // and can be differentiated again.  The backward pass runs on the engine's thread, without Python.
+// A leaf's gradient is accumulated on the stream where an earlier graph that still lives first used
+// the leaf.  Inside a capture the default stream cannot be waited for, and autograd ends the process
+// when it tries, so a captured backward pass that would come there is refused before it does.
+void refuse_uncapturable_leaves() {
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
+    const auto here = torch::autograd::get_current_node();
+    std::vector<torch::autograd::Node *> todo{here.get()};
+    std::unordered_set<torch::autograd::Node *> seen;
+    while (!todo.empty()) {
+        torch::autograd::Node *node = todo.back();
+        todo.pop_back();
+        if (node == nullptr || !seen.insert(node).second) continue;
+        if (dynamic_cast<torch::autograd::AccumulateGrad *>(node) != nullptr) {
+            const auto stream = node->stream();
+            TORCH_CHECK(!stream || !stream->device().is_cuda() || c10::cuda::CUDAStream(*stream).stream() != nullptr,
+                        "a backward pass is being captured, but a graph made outside the capture still holds one of its "
+                        "leaves on the default stream: let go of that graph's outputs first");
+        }
+        for (const auto &edge : node->next_edges()) todo.push_back(edge.function.get());
+    }
+}
+
 struct RopeFunction : torch::autograd::Function<RopeFunction> {
     using List = torch::autograd::variable_list;
 
@@ -360,6 +386,7 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
     }
 
     static List backward(torch::autograd::AutogradContext *ctx, const List &grads) {
+        refuse_uncapturable_leaves();
         const List saved = ctx->get_saved_variables();
         const bool two = ctx->saved_data["two"].toBool();
         Turn turn;
@@ -396,6 +423,11 @@ PyObject *rope_grad(PyObject *const *a) {
     PyObject *first = THPVariable_Wrap(out[0]);
     if (two) return Py_BuildValue("(NN)", first, THPVariable_Wrap(out[1]));
     return Py_BuildValue("(NO)", first, Py_None);
+}
+
+PyObject *check_leaves(PyObject *const *) {
+    refuse_uncapturable_leaves();
+    Py_RETURN_NONE;
 }
 
 // Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out, dev_status
@@ -613,6 +645,7 @@ PyObject *bind(PyObject *, PyObject *args) {
 #define CCA_ENTRY(name, count) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(entry<name, count>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CCA_ENTRY(rope, 10),
                          CCA_ENTRY(rope_grad, 7),
+                         CCA_ENTRY(check_leaves, 0),
                          CCA_ENTRY(rope_append, 14),
                          CCA_ENTRY(tree_fwd, 17),
                          CCA_ENTRY(pool_pages, 14),

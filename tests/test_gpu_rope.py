@@ -253,3 +253,33 @@ def test_forward_and_backward_in_one_graph():
     pos = np.arange(21)[None]
     close(out[0], *rotate(Q, pos, f.cpu(), "interleaved"), "Q")
     close(out[3], *rotate(dk, pos, f.cpu(), "interleaved", 1.0, -1.0), "dK")
+
+
+@pytest.mark.parametrize("attention", [False, True], ids=["rope", "attention"])
+def test_backward_in_a_graph(attention):
+    """A captured step gives the eager step's gradients; while an eager graph still holds the leaves on the
+    default stream it is refused (autograd would end the process), and the next capture works."""
+    leaves = [rand(1, h, 96, 128, dtype=torch.bfloat16, seed=h).requires_grad_() for h in (4, 2, 2)][:3 if attention else 2]
+    f = freqs(128)
+
+    def step():
+        if attention:
+            loss = api.cca_attention(*leaves, 16, 32, inv_freq=f).float().square().sum()
+        else:
+            q, k = api.rope(*leaves, f)
+            loss = q[0, 0, 3].float().square().sum() + k.float().sin().sum()
+        return loss, torch.autograd.grad(loss, leaves)
+
+    eager, want = step()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="being captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            step()
+    del eager
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, got = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
