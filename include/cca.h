@@ -397,6 +397,7 @@ int cca_rope_append(const cca_rope_tensor_t *q, const cca_rope_tensor_t *k, cons
  * Keys that a row does not see never reach its output, whatever they hold.
  * workspace: caller-owned, at least cca_tree_workspace_size(params, T) bytes, rewritten by
  * every call; two calls that may run at the same time need one each.
+ * O, LSE and the workspace must overlap neither an input nor one another.
  * Supported: bf16 or f32, d in {64, 128}, 1 <= T <= min(256, w), B <= 1024.
  */
 int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core, const int32_t *lens,

@@ -110,6 +110,14 @@ int size32(int64_t v, const char *name) {
     if (v > INT32_MAX) refuse("%s is too large", name);
     return static_cast<int>(v);
 }
+bool flag(PyObject *o, const char *name) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        refuse("%s must be true or false", name);
+    }
+    return v == 1;
+}
 float real(PyObject *o, const char *name) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) {
@@ -290,7 +298,7 @@ PyObject *rope(PyObject *const *a) {
     const Place at(q);
     const int dtype = check_pair(a, q, at.dev);
     Turn turn(a, q, at.dev);
-    turn.inverse = PyObject_IsTrue(a[7]) == 1;
+    turn.inverse = flag(a[7], "inverse");
     const bool two = !none(a[1]);
     if ((!two && !none(a[9])) || (two && none(a[8]) != none(a[9]))) refuse("out must hold one tensor for each input");
     at::Tensor outs[2];
@@ -307,8 +315,6 @@ PyObject *rope(PyObject *const *a) {
     return Py_BuildValue("(NO)", first, Py_None);
 }
 
-// Autograd of the rotation.  It is linear: the gradient is the rotation back, by the same kernel,
-// and can be differentiated again.  The backward pass runs on the engine's thread, without Python.
 // A leaf's gradient is accumulated on the stream where an earlier graph that still lives first used
 // the leaf.  Inside a capture the default stream cannot be waited for, and autograd ends the process
 // when it tries, so a captured backward pass that would come there is refused before it does.
@@ -331,6 +337,8 @@ void refuse_uncapturable_leaves() {
     }
 }
 
+// Autograd of the rotation.  It is linear: the gradient is the rotation back, by the same kernel,
+// and can be differentiated again.  The backward pass runs on the engine's thread, without Python.
 struct RopeFunction : torch::autograd::Function<RopeFunction> {
     using List = torch::autograd::variable_list;
 

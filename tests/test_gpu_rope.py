@@ -283,3 +283,10 @@ def test_backward_in_a_graph(attention):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_refuses_a_flag_without_a_truth_value():
+    x = rand(1, 2, 8, 64)
+    with pytest.raises(ValueError, match="inverse"):
+        api.cca_rope(x, None, freqs(64), inverse=torch.zeros(2))
+    api.cca_rope(x, None, freqs(64), inverse=torch.ones((), dtype=torch.bool))
