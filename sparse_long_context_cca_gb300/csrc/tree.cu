@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
                 }
             }
         }
+        if (tid == 0 && mt == 0) note_span(a, it, group, x0, x1);
         if (x + 1 < x1) {
             next_item(a, it);
             if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
@@ -619,6 +620,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
                     }
                 }
             }
+            if (threadIdx.x == 0 && mt == 0) note_span(a, it, group, x0, x1);
             if (x + 1 < x1) {
                 next_item(a, it);
                 fresh = true;
@@ -631,76 +633,61 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
 // ---------------------------------------------------------------- joining the partials
 
 constexpr int JOIN_ROWS = 32;
+constexpr int JOIN_RESIDENT = 8;  // blocks per SM
 
-// A block joins up to 32 rows of one list: all columns, a half or a quarter of them (gridDim.z),
-// a quarter of those per warp.  The time is that of the chain of reads, so few lists take many
-// blocks of few loads, and many lists as many blocks as are resident at once.  A lane takes a
+// A warp joins 4C columns of up to 32 rows of one list.  The time is that of three dependent steps
+// (the list's span, its parts, the stores), so blocks are small.  Where the lists are few, C is
+// least, for the most blocks; many lists take twice that, which makes a row's store a whole sector
+// of the output (16 sequences of 64 nodes, 128 lists of 256 rows: 15.3 -> 10 us).  A lane takes a
 // row; where there are fewer rows, the lanes left over take parts: lane group i the parts i,
 // i + groups, .. of the list, in the order of the groups that wrote them, and the lane groups
 // are added up in a fixed order.  Lists that one group finished are already written.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM) {
-    constexpr int C = D / 64;  // float4 columns of a warp
-    __shared__ int sm_sum[2][4];
+template <typename T, int D, int C>
+__global__ void __launch_bounds__(128, JOIN_RESIDENT) tree_join_kernel(const TreeArgs a, int BM) {
+    constexpr int AHEAD = 8 / C;  // parts whose loads are in flight together
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / a.Hkv, kv = blockIdx.x - b * a.Hkv;
     int lanes = 32;  // a power of two that holds the rows
     while (lanes / 2 >= a.R) lanes /= 2;
     const int row = blockIdx.y * JOIN_ROWS + (lane & (lanes - 1)), step = 32 / lanes;
-    // Where the list lies among all follows from the lengths, which the kernel before has waited
-    // for, so it is found while that one still runs (from L2, where its wait has seen them).
-    int all = 0, f0 = 0;
-    for (int i = threadIdx.x; i < a.B; i += 128) {
-        const int n = key_list_of(a, __ldcg(a.lens + i)).tiles * a.Hkv;
-        all += n;
-        if (i < b) f0 += n;
-    }
-    all = __reduce_add_sync(kFull, all);
-    f0 = __reduce_add_sync(kFull, f0);
-    if (lane == 0) {
-        sm_sum[0][warp] = all;
-        sm_sum[1][warp] = f0;
-    }
-    __syncthreads();
-    all = sm_sum[0][0] + sm_sum[0][1] + sm_sum[0][2] + sm_sum[0][3];
-    f0 = sm_sum[1][0] + sm_sum[1][1] + sm_sum[1][2] + sm_sum[1][3];
-    const Split split = make_split(a, all);
-    const int tiles = key_list_of(a, __ldcg(a.lens + b)).tiles;
-    const int s = f0 + kv * tiles, e = s + tiles;
-    const int y0 = split.owner(s), y1 = split.owner(e - 1);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (y0 == y1) return;
     const bool live = row < a.R;
     const int mt = live ? row / BM : 0, in = live ? row - mt * BM : 0;
-    auto part = [&](int y) { return static_cast<const float *>(part_at(a, y, mt, split.begin(y) >= s ? 0 : 1, BM, D)); };
-    float mx = -INFINITY;
-#pragma unroll 4
-    for (int y = y0 + lane / lanes; y <= y1; y += step) mx = fmaxf(mx, part(y)[BM * D + in]);
-    for (int off = 16; off >= lanes; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-    const float base = mx == -INFINITY ? 0.f : mx;
-    const int64_t at = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kv) * (a.Hq / a.Hkv)) * a.T + row;
-    const int rounds = 4 / gridDim.z;
-    for (int i = 0; i < rounds; ++i) {
-        const int col0 = ((blockIdx.z * 4 + warp) * rounds + i) * C;  // in float4
-        float4 acc[C];
-        float l = 0.f;
+    const int col0 = (blockIdx.z * 4 + warp) * C;  // in float4
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 span = a.spans[blockIdx.x];
+    const int y0 = span.x >> 1, y1 = span.y;
+    if (y0 < 0 || y0 >= y1 || y1 >= a.groups) return;  // no parts (or a call that gave up)
+    float mx = -INFINITY, l = 0.f;
+    float4 acc[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int y = y0 + lane / lanes; y <= y1; y += step) {
-            const float *p = part(y);
-            const float4 *q = reinterpret_cast<const float4 *>(p) + col0 * BM + in;
-            const float f = exp2f(p[BM * D + in] - base);
-            l += p[BM * D + BM + in] * f;
+    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll AHEAD
+    for (int y = y0 + lane / lanes; y <= y1; y += step) {
+        const float *p = part_at(a, y, mt, y == y0 ? span.x & 1 : 0, BM, D);
+        const float4 *q = reinterpret_cast<const float4 *>(p) + col0 * BM + in;
+        const float m = p[BM * D + in], s = p[BM * D + BM + in];
+        float4 v[C];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const float4 v = q[c * BM];
-                acc[c].x = fmaf(v.x, f, acc[c].x);
-                acc[c].y = fmaf(v.y, f, acc[c].y);
-                acc[c].z = fmaf(v.z, f, acc[c].z);
-                acc[c].w = fmaf(v.w, f, acc[c].w);
-            }
+        for (int c = 0; c < C; ++c) v[c] = q[c * BM];
+        const float top = fmaxf(mx, m), base = top == -INFINITY ? 0.f : top;
+        const float f0 = exp2f(mx - base), f = exp2f(m - base);
+        mx = top;
+        l = fmaf(s, f, l * f0);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            acc[c].x = fmaf(v[c].x, f, acc[c].x * f0);
+            acc[c].y = fmaf(v[c].y, f, acc[c].y * f0);
+            acc[c].z = fmaf(v[c].z, f, acc[c].z * f0);
+            acc[c].w = fmaf(v[c].w, f, acc[c].w * f0);
         }
+    }
+    if (step > 1) {
+        float top = mx;
+        for (int off = 16; off >= lanes; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        const float f = exp2f(mx - (top == -INFINITY ? 0.f : top));
+        mx = top;
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = make_float4(acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f);
         for (int off = 16; off >= lanes; off >>= 1) {
             l += __shfl_xor_sync(kFull, l, off);
 #pragma unroll
@@ -711,20 +698,32 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a, int BM
                 acc[c].w += __shfl_xor_sync(kFull, acc[c].w, off);
             }
         }
-        if (!live || lane >= lanes) continue;
-        const bool none = l == 0.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc[c].x / l, acc[c].y / l, acc[c].z / l, acc[c].w / l);
-            const int64_t to = at * D + (col0 + c) * 4;
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.O) + to) = make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
-            } else {
-                *reinterpret_cast<float4 *>(static_cast<float *>(a.O) + to) = v;
-            }
-        }
-        if (col0 == 0) a.LSE[at] = none ? -INFINITY : (mx + log2f(l)) * kLn2;
     }
+    if (!live || lane >= lanes) return;
+    const int b = blockIdx.x / a.Hkv, kv = blockIdx.x - b * a.Hkv;
+    const int64_t at = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kv) * (a.Hq / a.Hkv)) * a.T + row;
+    const bool none = l == 0.f;
+    const float by = none ? 0.f : 1.f / l;
+    const int64_t to = at * D + col0 * 4;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc[c].x * by, acc[c].y * by, acc[c].z * by, acc[c].w * by);
+    if constexpr (sizeof(T) == 2) {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.O) + to;
+        uint2 r[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) r[c] = make_uint2(ptx::pack_bf16x2(acc[c].x, acc[c].y), ptx::pack_bf16x2(acc[c].z, acc[c].w));
+        if constexpr (C == 1) {
+            *reinterpret_cast<uint2 *>(o) = r[0];
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; c += 2) reinterpret_cast<uint4 *>(o)[c / 2] = make_uint4(r[c].x, r[c].y, r[c + 1].x, r[c + 1].y);
+        }
+    } else {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.O) + to);
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = acc[c];
+    }
+    if (col0 == 0) a.LSE[at] = none ? -INFINITY : (mx + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- launch
@@ -765,26 +764,30 @@ int rows_per_cta(int dtype, int R, int d) {
     return R <= 16 ? 16 : R <= 32 ? 32 : 64;
 }
 
-uint64_t workspace_bytes_for(int dtype, int R, int d, int sms) {
+// The spans of the lists come first, then the partials.
+int64_t span_bytes(int Hkv) { return static_cast<int64_t>(TREE_MAX_BATCH) * Hkv * sizeof(int2); }
+
+uint64_t workspace_bytes_for(int dtype, int R, int Hkv, int d, int sms) {
     // CTAs times two slots; a grid holds one CTA per SM on the tensor cores, MAX_CTAS_PER_SM at most
     // elsewhere, and one group of row tiles at least
     const int BM = rows_per_cta(dtype, R, d);
     const int64_t n_mt = (R + BM - 1) / BM;
     int64_t ctas = static_cast<int64_t>(sms) * (on_tensor_cores(dtype, d) ? 1 : MAX_CTAS_PER_SM);
     if (ctas < n_mt) ctas = n_mt;
-    return static_cast<uint64_t>(ctas) * 2 * part_floats(BM, d) * 4;
+    return static_cast<uint64_t>(span_bytes(Hkv) + ctas * 2 * part_floats(BM, d) * 4);
 }
 
-template <typename J>
-cudaError_t run_join(J join, const TreeArgs &a, int BM, int sms, cudaStream_t stream) {
+template <typename T, int D>
+cudaError_t run_join(const TreeArgs &a, int BM, int sms, cudaStream_t stream) {
     dim3 grid(static_cast<unsigned>(a.B) * a.Hkv, (a.R + JOIN_ROWS - 1) / JOIN_ROWS, 4);
-    // eight blocks are resident per SM
-    while (grid.z > 1 && static_cast<int64_t>(grid.x) * grid.y * grid.z > 8ll * sms) grid.z /= 2;
-    return start_dependent(join, grid, 128, 0, stream, a, BM);
+    if (static_cast<int64_t>(grid.x) * grid.y * grid.z <= static_cast<int64_t>(JOIN_RESIDENT) * sms)
+        return start_dependent(tree_join_kernel<T, D, D / 64>, grid, 128, 0, stream, a, BM);
+    grid.z = 2;
+    return start_dependent(tree_join_kernel<T, D, D / 32>, grid, 128, 0, stream, a, BM);
 }
 
-template <auto kernel, typename J>
-cudaError_t run_tree(J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t stream) {
+template <auto kernel, typename T, int D>
+cudaError_t run_tree(TreeArgs a, int BM, int smem, int sms, cudaStream_t stream) {
     int per_sm = 0;
     cudaError_t e = resident<kernel>(smem, per_sm);
     if (e != cudaSuccess) return e;
@@ -795,7 +798,7 @@ cudaError_t run_tree(J join, TreeArgs a, int BM, int smem, int sms, cudaStream_t
     if (a.groups < 1) a.groups = 1;
     e = start_dependent(kernel, dim3(static_cast<unsigned>(a.groups) * a.n_mt), TREE_THREADS, smem, stream, a);
     if (e != cudaSuccess) return e;
-    return run_join(join, a, BM, sms, stream);
+    return run_join<T, D>(a, BM, sms, stream);
 }
 
 cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
@@ -806,15 +809,14 @@ cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
     a.tile_log2 = 7;
     const cudaError_t e = launch_tc(a, g_wait_limit_ns, g_skip_q_load, stream);
     if (e != cudaSuccess) return e;
-    return run_join(tree_join_kernel<__nv_bfloat16, 128>, a, BM, sms, stream);
+    return run_join<__nv_bfloat16, 128>(a, BM, sms, stream);
 }
 
 cudaError_t run_mma(const TreeArgs &a, int sms, cudaStream_t stream) {
     const int smem = TreeSmem::bytes(a.T), BM = rows_per_cta(CCA_BF16, a.R, MMA_D);
-    auto *join = tree_join_kernel<__nv_bfloat16, MMA_D>;
-    if (BM == 16) return run_tree<tree_bf16_kernel<1>>(join, a, BM, smem, sms, stream);
-    if (BM == 32) return run_tree<tree_bf16_kernel<2>>(join, a, BM, smem, sms, stream);
-    return run_tree<tree_bf16_kernel<4>>(join, a, BM, smem, sms, stream);
+    if (BM == 16) return run_tree<tree_bf16_kernel<1>, __nv_bfloat16, MMA_D>(a, BM, smem, sms, stream);
+    if (BM == 32) return run_tree<tree_bf16_kernel<2>, __nv_bfloat16, MMA_D>(a, BM, smem, sms, stream);
+    return run_tree<tree_bf16_kernel<4>, __nv_bfloat16, MMA_D>(a, BM, smem, sms, stream);
 }
 
 int check_tree(const cca_params_t *p, int T) {
@@ -836,7 +838,7 @@ uint64_t cca_tree_workspace_size(const cca_params_t *params, int T) {
     if (check_tree(params, T) != CCA_OK) return 0;
     int sms = device_sms();
     if (sms < 1) sms = 152;  // no device here: the size a GB300 needs
-    return workspace_bytes_for(params->dtype, params->Hq / params->Hkv * T, params->d, sms);
+    return workspace_bytes_for(params->dtype, params->Hq / params->Hkv * T, params->Hkv, params->d, sms);
 }
 
 int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core, const int32_t *lens,
@@ -896,15 +898,14 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.scale_log2 = resolve_scale(params) * 1.4426950408889634f;
     a.O = O;
     a.LSE = LSE;
-    a.ws = static_cast<float *>(workspace);
+    a.spans = static_cast<int2 *>(workspace);
+    a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + span_bytes(a.Hkv));
     a.status = params->dev_status;
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
     if (params->dtype == CCA_BF16) return from_cuda(params->d == 128 ? run_tc(a, sms, strm) : run_mma(a, sms, strm));
     if (params->d == 128)
-        return from_cuda(run_tree<tree_f32_kernel<128>>(tree_join_kernel<float, 128>, a, F32_BM,
-                                  TreeF32Smem<128>::bytes(T), sms, strm));
-    return from_cuda(run_tree<tree_f32_kernel<64>>(tree_join_kernel<float, 64>, a, F32_BM, TreeF32Smem<64>::bytes(T),
-                              sms, strm));
+        return from_cuda(run_tree<tree_f32_kernel<128>, float, 128>(a, F32_BM, TreeF32Smem<128>::bytes(T), sms, strm));
+    return from_cuda(run_tree<tree_f32_kernel<64>, float, 64>(a, F32_BM, TreeF32Smem<64>::bytes(T), sms, strm));
 }
 
 }  // extern "C"

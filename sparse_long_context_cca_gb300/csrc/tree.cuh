@@ -27,6 +27,7 @@ struct TreeArgs {
     float scale_log2;
     void *O;
     float *LSE;
+    int2 *spans;  // per list: the group it begins in, times two, plus its slot there; the group it ends in
     float *ws;  // partials
     int32_t *status;
 };
@@ -341,6 +342,13 @@ __device__ __forceinline__ int part_col(int BM, int row, int col) { return (col 
 // Slot 0: the list that the group's run begins in; 1: the one it ends in.
 __device__ __forceinline__ float *part_at(const TreeArgs &a, int group, int mt, int slot, int BM, int D) {
     return a.ws + ((static_cast<int64_t>(group) * a.n_mt + mt) * 2 + slot) * part_floats(BM, D);
+}
+
+// The groups of a run's first and last lists say so for the join, which need not find them again.
+__device__ __forceinline__ void note_span(const TreeArgs &a, const Item &it, int group, int x0, int x1) {
+    int2 *span = a.spans + it.b * a.Hkv + it.kv;
+    if (it.first >= x0) span->x = 2 * group + (it.first == x0 ? 0 : 1);
+    if (it.first + it.k.tiles <= x1) span->y = group;
 }
 
 // ---------------------------------------------------------------- copies

@@ -705,6 +705,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                     part[BM * HD + BM + in] = l;
                 }
             }
+            if (threadIdx.x == 0 && mt == 0) note_span(a, it, group, x0, x1);
             ++seg;
             x = end;
             if (x < x1) {
