@@ -473,7 +473,7 @@ struct TreeF32Smem {
 };
 
 // The same walk with one tile in shared memory at a time; scores and sums in fp32.  Three sequences
-// of 1.5 K, seven nodes, four heads over two (0.8 MB): 16.5 us, a chain of one tile per CTA and the
+// of 1.5 K, seven nodes, four heads over two (0.8 MB): 15 us, a chain of one tile per CTA and the
 // join; with two tiles per CTA at least it was 23 us.
 template <int D>
 __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a) {
@@ -857,7 +857,7 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     // rows of the table where that is less, and the nodes
     const double rows = static_cast<double>(raw->rows) * raw->cols;
     const double keys = fmin(rows / params->g + params->w + params->g, rows) + 3.0 * T + params->g;
-    if (keys / TILE * params->B * params->Hkv > 2.0e9) return CCA_ERR_UNSUPPORTED;
+    if ((keys / TILE + LIST_COST) * params->B * params->Hkv > 2.0e9) return CCA_ERR_UNSUPPORTED;
     const uint64_t es = params->dtype == CCA_BF16 ? 2 : 4;
     const uint64_t out = static_cast<uint64_t>(params->B) * params->Hq * T * params->d * es;
     if (bytes_meet(O, out, Q, out)) return CCA_ERR_INVALID_ARG;  // row tiles of other CTAs may still read Q

@@ -6,14 +6,14 @@
 // to 256 rows read K and V once; the rows that a small tree leaves empty cost nothing, as the
 // loads bound it.  Per tile an SM's share of HBM needs 64 KB / 44 GB/s = 1.5 us (2800 cycles).
 // Measured: one half 2300 cycles a tile from L2, so HBM is the bound (64 sequences of one token,
-// 32 heads, 8 K: 262 us, 0.80 of the copy bandwidth); two halves 3500 cycles, the four products
+// 32 heads, 8 K: 244 us, 0.86 of the copy bandwidth); two halves 3500 cycles, the four products
 // at 820 cycles each against 512 of tensor work, as both read their operands from shared memory
 // (192 KB a tile at 128 B a cycle, next to 64 KB of copies): 16 sequences x 64 nodes, 32 heads
-// over 8, 128 K: 145 us, 4.1 TB/s and 1.0 PFLOP/s.  64-key tiles with two score buffers per half
+// over 8, 128 K: 135 us, 4.4 TB/s and 1.1 PFLOP/s.  64-key tiles with two score buffers per half
 // free the softmax from waiting for its product, but their N = 64 products took 740 cycles each:
 // 201 us.  A call on little work is a chain: the CTA's run 1.8 us, page look-up and first copy
 // 2.5 us, first softmax 1.4 us, output 1.5 us, then the join (one token of 32 heads at 32 K,
-// 49 MB: 19.5 us warm, 23.8 us from HBM).
+// 49 MB: 17.8 us warm, 22.5 us from HBM).
 //
 // Roles (warpgroups of four warps):
 //   0 .. HALVES-1   softmax and output of a half; thread t owns row t of it (TMEM lane t).
@@ -41,6 +41,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/cca.h"
 #include "internal.h"
@@ -196,12 +197,22 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             if (held_v && held_mixed != 0) {
                 // infinities and NaN in the V of a key that only some rows see would reach the others
                 // as 0 * NaN: they leave the tile, and the rows that see the key add them themselves
+                auto at = [&](int r) {
+                    return reinterpret_cast<uint4 *>(gbase + L::OFF_RING + held * TILE_BYTES + (chunk >> 3) * HALF_BYTES +
+                                                     (pw * 32 + r) * 128 + (((chunk & 7) ^ (r & 7)) << 4));
+                };
+                // an exponent of all ones carries into the sign's place
+                auto carry = [](uint32_t v) { return (v & 0x7f807f80u) + 0x00800080u; };
+                uint32_t any = 0;
+#pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int r = 2 * j + sub;
+                    const uint4 v = *at(2 * j + sub);
+                    any |= carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w);
+                }
+                for (int j = 0; (any & 0x80008000u) != 0 && j < 16; ++j) {
+                    const int r = 2 * j + sub, row = pw * 32 + r;
                     if (!((held_mixed >> r) & 1u)) continue;
-                    const int row = pw * 32 + r;
-                    uint4 *p = reinterpret_cast<uint4 *>(gbase + L::OFF_RING + held * TILE_BYTES + (chunk >> 3) * HALF_BYTES +
-                                                         row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+                    uint4 *p = at(r);
                     uint32_t v[4] = {p->x, p->y, p->z, p->w};
                     bool hit = false;
 #pragma unroll
@@ -490,55 +501,55 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 const int rest = t - it.first - it.k.run_tiles;  // tile of the rest, < 0: runs
                 const uint4 gone = *reinterpret_cast<const uint4 *>(tm.gone);
                 const bool masked = rest >= 0 || (gone.x | gone.y | gone.z | gone.w) != 0;
-                if (rest >= 0) {
-                    // V(t)'s slot is not filled again before this softmax is over: what the producers
-                    // took out of it is known now
-                    const int u = 2 * (t - x0) + 1;
-                    if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, abort_flag, lim))) {
-                        ok = false;
-                        break;
-                    }
-                }
                 auto mask_of = [&](int c) {  // of columns 32c .. 32c + 31
                     return (rest >= 0 ? seen(rest * BN + c * 32) : 0xffffffffu) & ~tm.gone[c];
                 };
                 if (!idle) {
-                    // a masked tile: -inf into the scores that the row does not see, where they are
-                    if (masked) {
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t see = mask_of(c);
-                            if (__all_sync(kFull, see == 0xffffffffu)) continue;
-                            uint32_t v[32];
-                            ptx::tmem_ld32(tS + c * 32, v);
-                            ptx::tmem_wait_ld(v);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!((see >> k) & 1u)) v[k] = __float_as_uint(-INFINITY);
-                            ptx::tmem_st16(tS + c * 32, reinterpret_cast<const uint32_t(&)[16]>(v[0]));
-                            ptx::tmem_st16(tS + c * 32 + 16, reinterpret_cast<const uint32_t(&)[16]>(v[16]));
-                        }
-                        ptx::tmem_wait_st();
-                    }
                     // the row's maximum; 64 columns at a time, which keeps the code short (a launch
-                    // begins with cold instruction caches) and the registers few
+                    // begins with cold instruction caches) and the registers few.  A masked tile has
+                    // a pass of its own: -inf into the scores that the row does not see, here and
+                    // where they are.
                     float mx = -INFINITY;
+                    auto maximum = [&](auto with_masks) {
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t s[2][32];
-                        ptx::tmem_ld32(tS + c * 64, s[0]);
-                        ptx::tmem_ld32(tS + c * 64 + 32, s[1]);
-                        ptx::tmem_wait_ld(s[0]);
-                        ptx::reg_touch(s[1]);
-                        float mp[4];
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t s[2][32];
+                            ptx::tmem_ld32(tS + c * 64, s[0]);
+                            ptx::tmem_ld32(tS + c * 64 + 32, s[1]);
+                            uint32_t see[2] = {};
+                            if constexpr (with_masks.value) {
+                                see[0] = mask_of(2 * c);
+                                see[1] = mask_of(2 * c + 1);
+                            }
+                            ptx::tmem_wait_ld(s[0]);
+                            ptx::reg_touch(s[1]);
+                            if constexpr (with_masks.value) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            mp[q] = fmaxf(__uint_as_float(s[q >> 1][(q & 1) * 16]), __uint_as_float(s[q >> 1][(q & 1) * 16 + 1]));
+                                for (int j = 0; j < 2; ++j) {
+                                    if (__all_sync(kFull, see[j] == 0xffffffffu)) continue;
 #pragma unroll
-                            for (int k = 2; k < 16; k += 2)
-                                mp[q] = ptx::max3(mp[q], __uint_as_float(s[q >> 1][(q & 1) * 16 + k]), __uint_as_float(s[q >> 1][(q & 1) * 16 + k + 1]));
+                                    for (int k = 0; k < 32; ++k)
+                                        if (!((see[j] >> k) & 1u)) s[j][k] = __float_as_uint(-INFINITY);
+                                    ptx::tmem_st16(tS + c * 64 + j * 32, reinterpret_cast<const uint32_t(&)[16]>(s[j][0]));
+                                    ptx::tmem_st16(tS + c * 64 + j * 32 + 16, reinterpret_cast<const uint32_t(&)[16]>(s[j][16]));
+                                }
+                            }
+                            float mp[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                mp[q] = fmaxf(__uint_as_float(s[q >> 1][(q & 1) * 16]), __uint_as_float(s[q >> 1][(q & 1) * 16 + 1]));
+#pragma unroll
+                                for (int k = 2; k < 16; k += 2)
+                                    mp[q] = ptx::max3(mp[q], __uint_as_float(s[q >> 1][(q & 1) * 16 + k]), __uint_as_float(s[q >> 1][(q & 1) * 16 + k + 1]));
+                            }
+                            mx = fmaxf(ptx::max3(mx, mp[0], mp[1]), fmaxf(mp[2], mp[3]));
                         }
-                        mx = fmaxf(ptx::max3(mx, mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+                    };
+                    if (masked) {
+                        maximum(std::true_type());
+                        ptx::tmem_wait_st();
+                    } else {
+                        maximum(std::false_type());
                     }
                     const float m_new = fmaxf(m, mx * a.scale_log2);
                     bool rescale = false;
@@ -571,6 +582,15 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                         }
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
+                    if (rest >= 0) {
+                        // V(t)'s slot is not filled again before this softmax is over: what the producers
+                        // took out of it is known now
+                        const int u = 2 * (t - x0) + 1;
+                        if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, abort_flag, lim))) {
+                            ok = false;
+                            break;
+                        }
+                    }
                     if (rest >= 0 && (tm.odd[0] | tm.odd[1] | tm.odd[2] | tm.odd[3]) != 0) {
                         // what the producers took out of V, for the rows that see it: the sums of
                         // infinities and NaN wait in this row of the CTA's partial for the output
