@@ -42,11 +42,11 @@ inline bool encode_3d_bf16_d128(EncodeTiledFn enc, CUtensorMap *map, const void 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 rows of 128 columns viewed as 2-D (128, rows); box = 64 columns x `box` rows with
+// bf16 rows of d columns (64 or 128) viewed as 2-D (d, rows); box = 64 columns x `box` rows with
 // 128-byte swizzle.  Rows past `rows` read as zeros.
-inline bool encode_rows_bf16_d128(EncodeTiledFn enc, CUtensorMap *map, const void *ptr, uint64_t rows, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {128, rows};
-    const cuuint64_t strides[1] = {128 * 2};
+inline bool encode_rows_bf16(EncodeTiledFn enc, CUtensorMap *map, const void *ptr, int d, uint64_t rows, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), rows};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
     const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,

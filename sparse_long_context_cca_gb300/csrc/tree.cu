@@ -3,8 +3,8 @@
 // softmax over the cores j < lo(p)/g, the committed raw tokens of its window, its
 // ancestors and itself.  One node per sequence is plain decoding.
 //
-// Three kernels walk the lists: tree_tc.cu (bf16, d = 128, tcgen05), tree_bf16_kernel (bf16,
-// d = 64, mma.sync) and tree_f32_kernel (fp32 on CUDA cores).
+// Three kernels walk the lists: tree_tc.cu (bf16 on tcgen05), tree_bf16_kernel (bf16, d = 64, up
+// to 16 rows per KV head, mma.sync) and tree_f32_kernel (fp32 on CUDA cores).
 //
 // What bounds it.  The r query heads of a KV head times T nodes are R = r*T rows that share
 // one list of keys: K and V rows are read once per (b, KV head) and meet R rows, so few rows
@@ -75,7 +75,7 @@ struct Meta {
     uint8_t kind[TILE];
 };
 
-constexpr int MMA_D = 64;  // head dimension of the mma.sync kernel
+constexpr int MMA_D = 64, MMA_ROWS = 16;  // head dimension and rows of the mma.sync kernel
 
 struct TreeSmem {
     static constexpr int ROW = MMA_D * 2;                  // bytes of a key row
@@ -94,15 +94,15 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
     return static_cast<uint32_t>(row * TreeSmem::ROW + ((c ^ (row & 7)) << 4));
 }
 
-// bf16 with d = 64.  WM warps side by side over 16-row blocks, 4 / WM over the keys of a tile.  One CTA walks
-// its group's run of tiles: cp.async keeps two tiles in flight behind the one in work, and
-// the page look-ups of the tile after those are done a step ahead, under the matrix work.
-template <int WM>
+// bf16 with d = 64 and up to 16 rows: the four warps share them and take a quarter of a tile's
+// keys each.  One CTA walks its group's run of tiles: cp.async keeps two tiles in flight behind
+// the one in work, and the page look-ups of the tile after those are done a step ahead, under the
+// matrix work.
 __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs a) {
     using S = TreeSmem;
     constexpr int D = MMA_D;
-    constexpr int BM = 16 * WM;
-    constexpr int WK = 4 / WM;
+    constexpr int BM = MMA_ROWS;
+    constexpr int WK = 4;          // warps over the keys
     constexpr int KW = TILE / WK;  // keys of a warp
     constexpr int NT = KW / 8;
     constexpr int DT = D / 8;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     asm volatile("griddepcontrol.launch_dependents;");
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wm = warp % WM, wk = warp / WM;
+    const int wk = warp;
     const int mt = blockIdx.x % a.n_mt, group = blockIdx.x / a.n_mt;
     const Run run = find_run(a, group, st);
     const int x0 = run.x0, x1 = run.x1;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     uint32_t qf[D / 16][4];
     float o[DT][4], m[2], l[2];
     int node[2];  // node of this thread's two rows, -1 past the last row
-    const int row0 = mt * BM + wm * 16 + (lane >> 2);
+    const int row0 = mt * BM + (lane >> 2);
     auto begin_item = [&]() {
         read_tree(a, nodes, it.k, it.b);
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.Q) +
@@ -358,11 +358,11 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
             l[i] += __shfl_xor_sync(kFull, l[i], 1);
             l[i] += __shfl_xor_sync(kFull, l[i], 2);
         }
-        if constexpr (WK > 1) {
+        {
             // the warps over the keys join: through the tile that was read last, which the
             // next load reaches only after the barrier at the top
             __syncthreads();
-            float *mine = reinterpret_cast<float *>(smem + (kbase - stage0)) + ((wk - 1) * WM + wm) * 16 * (D + 2);
+            float *mine = reinterpret_cast<float *>(smem + (kbase - stage0)) + (wk - 1) * 16 * (D + 2);
             if (wk > 0) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
 #pragma unroll
                     for (int q = 1; q < WK; ++q) {
                         src[q] = reinterpret_cast<float *>(smem + (kbase - stage0)) +
-                                 (((q - 1) * WM + wm) * 16 + (lane >> 2) + 8 * i) * (D + 2);
+                                 ((q - 1) * 16 + (lane >> 2) + 8 * i) * (D + 2);
                         mx = fmaxf(mx, src[q][D]);
                     }
                     const float base = mx == -INFINITY ? 0.f : mx;
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
             const int64_t out0 = (static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int row = row0 + 8 * i, in = wm * 16 + (lane >> 2) + 8 * i;
+                const int row = row0 + 8 * i, in = (lane >> 2) + 8 * i;
                 if (node[i] < 0) continue;
                 if (nodes.cores[node[i]] < 0) {  // an empty node
                     m[i] = -INFINITY;
@@ -752,16 +752,17 @@ cudaError_t resident(int smem, int &per_sm) {
 
 constexpr int MAX_CTAS_PER_SM = 4;
 
-// bf16 with d = 128 runs on tcgen05, whatever the rows: one row of 32 heads at 32 K took 29.4 us
-// there and 31.6 us by mma.sync, 64 such sequences of 8 K 264 and 274 us (16 rows of 32
-// sequences 79 and 83 us).
-bool on_tensor_cores(int dtype, int d) { return dtype == CCA_BF16 && d == 128; }
+// bf16 runs on tcgen05, but for up to 16 rows at d = 64, where a tile's softmax takes longer than
+// its copy and mma.sync spreads it over four warps.  tcgen05 and mma.sync, us from HBM: d = 128, one
+// row of 32 heads at 32 K 29.4 and 31.6, 64 such sequences of 8 K 264 and 274; d = 64, one row of 32
+// heads at 32 K 18.2 and 16.3, 32 sequences of 16 rows 50.6 and 46.8, of 24 rows 41.2 and 40.8, eight
+// of 24 rows 23.4 and 25.1, of 96 rows 23.7 and 38.4, one of 20 rows at 2 K 14.9 and 19.6.
+bool on_tensor_cores(int dtype, int R, int d) { return dtype == CCA_BF16 && (d == 128 || R > MMA_ROWS); }
 
-// Rows per CTA: 16 rows of a warp each, so that as few row tiles as possible read the keys.
 int rows_per_cta(int dtype, int R, int d) {
     if (dtype == CCA_F32) return F32_BM;
-    if (on_tensor_cores(dtype, d)) return tc_rows(R);
-    return R <= 16 ? 16 : R <= 32 ? 32 : 64;
+    if (on_tensor_cores(dtype, R, d)) return tc_rows(R);
+    return MMA_ROWS;
 }
 
 // The spans of the lists come first, then the partials.
@@ -772,7 +773,7 @@ uint64_t workspace_bytes_for(int dtype, int R, int Hkv, int d, int sms) {
     // elsewhere, and one group of row tiles at least
     const int BM = rows_per_cta(dtype, R, d);
     const int64_t n_mt = (R + BM - 1) / BM;
-    int64_t ctas = static_cast<int64_t>(sms) * (on_tensor_cores(dtype, d) ? 1 : MAX_CTAS_PER_SM);
+    int64_t ctas = static_cast<int64_t>(sms) * (on_tensor_cores(dtype, R, d) ? 1 : MAX_CTAS_PER_SM);
     if (ctas < n_mt) ctas = n_mt;
     return static_cast<uint64_t>(span_bytes(Hkv) + ctas * 2 * part_floats(BM, d) * 4);
 }
@@ -801,22 +802,15 @@ cudaError_t run_tree(TreeArgs a, int BM, int smem, int sms, cudaStream_t stream)
     return run_join<T, D>(a, BM, sms, stream);
 }
 
-cudaError_t run_tc(TreeArgs a, int sms, cudaStream_t stream) {
+cudaError_t run_tc(TreeArgs a, int d, int sms, cudaStream_t stream) {
     const int BM = tc_rows(a.R);
     a.n_mt = (a.R + BM - 1) / BM;
     a.groups = sms / a.n_mt;
     if (a.groups < 1) a.groups = 1;
     a.tile_log2 = 7;
-    const cudaError_t e = launch_tc(a, g_wait_limit_ns, g_skip_q_load, stream);
+    const cudaError_t e = launch_tc(a, d, g_wait_limit_ns, g_skip_q_load, stream);
     if (e != cudaSuccess) return e;
-    return run_join<__nv_bfloat16, 128>(a, BM, sms, stream);
-}
-
-cudaError_t run_mma(const TreeArgs &a, int sms, cudaStream_t stream) {
-    const int smem = TreeSmem::bytes(a.T), BM = rows_per_cta(CCA_BF16, a.R, MMA_D);
-    if (BM == 16) return run_tree<tree_bf16_kernel<1>, __nv_bfloat16, MMA_D>(a, BM, smem, sms, stream);
-    if (BM == 32) return run_tree<tree_bf16_kernel<2>, __nv_bfloat16, MMA_D>(a, BM, smem, sms, stream);
-    return run_tree<tree_bf16_kernel<4>, __nv_bfloat16, MMA_D>(a, BM, smem, sms, stream);
+    return d == 64 ? run_join<__nv_bfloat16, 64>(a, BM, sms, stream) : run_join<__nv_bfloat16, 128>(a, BM, sms, stream);
 }
 
 int check_tree(const cca_params_t *p, int T) {
@@ -902,7 +896,9 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + span_bytes(a.Hkv));
     a.status = params->dev_status;
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
-    if (params->dtype == CCA_BF16) return from_cuda(params->d == 128 ? run_tc(a, sms, strm) : run_mma(a, sms, strm));
+    if (on_tensor_cores(params->dtype, a.R, params->d)) return from_cuda(run_tc(a, params->d, sms, strm));
+    if (params->dtype == CCA_BF16)
+        return from_cuda(run_tree<tree_bf16_kernel, __nv_bfloat16, MMA_D>(a, MMA_ROWS, TreeSmem::bytes(T), sms, strm));
     if (params->d == 128)
         return from_cuda(run_tree<tree_f32_kernel<128>, float, 128>(a, F32_BM, TreeF32Smem<128>::bytes(T), sms, strm));
     return from_cuda(run_tree<tree_f32_kernel<64>, float, 64>(a, F32_BM, TreeF32Smem<64>::bytes(T), sms, strm));

@@ -415,7 +415,7 @@ constexpr int MAX_SMEM = 227 * 1024;
 
 // Tensor-core kernel (tree_tc.cu): bf16, d = 128.  Rows of a CTA for R rows per KV head.
 int tc_rows(int R);
-cudaError_t launch_tc(TreeArgs a, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream);
+cudaError_t launch_tc(TreeArgs a, int d, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream);
 
 }  // namespace tree
 }  // namespace cca

@@ -1,4 +1,4 @@
-// Tree attention on the tcgen05 tensor cores: bf16, d = 128.  What it computes, the key list
+// Tree attention on the tcgen05 tensor cores: bf16, d = 128 or 64.  What it computes, the key list
 // and the split over the grid are those of tree.cuh; this file is the walk of one CTA over its
 // run of 128-key tiles.
 //
@@ -14,6 +14,8 @@
 // 201 us.  A call on little work is a chain: the CTA's run 1.8 us, page look-up and first copy
 // 2.5 us, first softmax 1.4 us, output 1.5 us, then the join (one token of 32 heads at 32 K,
 // 49 MB: 17.8 us warm, 22.5 us from HBM).
+// At d = 64 a tile is half as long to copy (1400 cycles) and its softmax (2100) is the bound: 8
+// sequences of 24 nodes, 32 heads over 8, up to 32 K: 23.6 us (38.4 by mma.sync).
 //
 // Roles (warpgroups of four warps):
 //   0 .. HALVES-1   softmax and output of a half; thread t owns row t of it (TMEM lane t).
@@ -24,7 +26,7 @@
 //                   look up and 16 lanes to a row to copy, so any page size and alignment goes.
 //                   Both fill 128-byte-swizzled tiles.
 //   HALVES+1        its first warp issues the MMAs.
-// K(t) and V(t) take two consecutive slots of a ring of NS 32 KB slots and are freed apart: K
+// K(t) and V(t) take two consecutive slots of a ring of NS tiles and are freed apart: K
 // when its scores are done, V when its product is (both at once cost a load's latency per tile:
 // 230 us in place of 158 at the time).
 //
@@ -54,16 +56,13 @@ namespace cca {
 namespace tree {
 namespace {
 
-constexpr int HD = 128;
 constexpr int BN = 128;                       // keys per tile
-constexpr uint32_t TILE_BYTES = BN * HD * 2;  // 32 KB
-constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;
+constexpr uint32_t HALF_BYTES = BN * 128;     // 64 columns of a tile
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_O = 256;
 constexpr float LAZY_RESCALE_LOG2 = 16.0f;  // keep a stale max while it is within 2^16
 constexpr uint32_t IDESC_QK = ptx::idesc_bf16_f32(128, BN, 0, 0);  // Q, K both K-major
-constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(128, HD, 0, 1);  // P in tensor memory, V MN-major
-constexpr int METAS = 4;
+constexpr int METAS = 8;
 
 // What the softmax needs to know of a tile's keys, a bit for each.
 struct TileMeta {
@@ -71,10 +70,12 @@ struct TileMeta {
     uint32_t odd[4];   // its V holds an infinity or NaN, and not every row sees it
 };
 
-template <int HALVES>
+template <int HALVES, int D>
 struct Layout {
-    // ring slots: what 227 KB leave next to the queries and the bookkeeping
-    static constexpr int NS = HALVES == 2 ? 4 : 5;
+    static constexpr uint32_t TILE_BYTES = BN * D * 2;
+    // ring slots: what 227 KB leave next to the queries and the bookkeeping; four tiles are enough
+    static constexpr int NS = D == 64 ? 8 : HALVES == 2 ? 4 : 5;
+    static_assert(METAS >= NS / 2 + 2, "a tile's bits stay until its softmax is over");
     static constexpr int THREADS = (HALVES + 2) * 128;
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_RING = HALVES * TILE_BYTES;
@@ -100,13 +101,17 @@ struct Layout {
 // The lowest n bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-template <int HALVES>
+template <int HALVES, int D>
 __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ CUtensorMap tmKc, const __grid_constant__ CUtensorMap tmVc, const TreeArgs a,
                    const unsigned long long lim, const int skip_loads) {
-    using L = Layout<HALVES>;
+    using L = Layout<HALVES, D>;
     constexpr int NS = L::NS;
+    constexpr uint32_t TILE_BYTES = L::TILE_BYTES;
+    constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(128, D, 0, 1);  // P in tensor memory, V MN-major
+    constexpr int CHUNKS = D / 8;              // 16-byte chunks of a row
+    constexpr int ROWS_AT_ONCE = 32 / CHUNKS;  // rows that a warp copies at once
     constexpr int BM = HALVES * 128;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     if (wg == HALVES) {
         // ------------------------------------------------------------ producers
         const int pw = warp & 3;
-        const int sub = lane >> 4, chunk = lane & 15;
+        const int sub = lane / CHUNKS, chunk = lane % CHUNKS;
         bool ok = x0 < x1 && !skip_loads;
         Item it = run.item;
         // the tile to load next: a lane's box of runs, or a lane's key of the rest
@@ -183,8 +188,8 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 return;
             }
             const Key key = find_key(a, it.k, it.b, it.kv, (tile - it.k.run_tiles) * BN + pw * 32 + lane);
-            kp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Kc : a.K) + key.row * (HD * 2);
-            vp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Vc : a.V) + key.row * (HD * 2);
+            kp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Kc : a.K) + key.row * (D * 2);
+            vp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Vc : a.V) + key.row * (D * 2);
             gone = __ballot_sync(kFull, key.kind == 4);
             mixed = __ballot_sync(kFull, key.kind != 0 && key.kind != 4);
         };
@@ -205,12 +210,12 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 auto carry = [](uint32_t v) { return (v & 0x7f807f80u) + 0x00800080u; };
                 uint32_t any = 0;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint4 v = *at(2 * j + sub);
+                for (int j = 0; j < CHUNKS; ++j) {
+                    const uint4 v = *at(ROWS_AT_ONCE * j + sub);
                     any |= carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w);
                 }
-                for (int j = 0; (any & 0x80008000u) != 0 && j < 16; ++j) {
-                    const int r = 2 * j + sub, row = pw * 32 + r;
+                for (int j = 0; (any & 0x80008000u) != 0 && j < CHUNKS; ++j) {
+                    const int r = ROWS_AT_ONCE * j + sub, row = pw * 32 + r;
                     if (!((held_mixed >> r) & 1u)) continue;
                     uint4 *p = at(r);
                     uint32_t v[4] = {p->x, p->y, p->z, p->w};
@@ -262,23 +267,23 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             __syncwarp();
             const uint32_t dst = base + L::OFF_RING + slot * TILE_BYTES;
             if (runs) {
-                if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::B_FULL + slot), 32 * HD * 2);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::B_FULL + slot), 32 * D * 2);
                 __syncwarp();
                 if (lane < per_warp) {
                     const uint32_t at = dst + (pw * 32 + (lane << a.box_log2)) * 128;
                     const void *map = is_v ? (core ? static_cast<const void *>(&tmVc) : static_cast<const void *>(&tmV))
                                            : (core ? static_cast<const void *>(&tmKc) : static_cast<const void *>(&tmK));
                     ptx::tma_load_2d(map, bar(L::B_FULL + slot), at, 0, box_y);
-                    ptx::tma_load_2d(map, bar(L::B_FULL + slot), at + HALF_BYTES, 64, box_y);
+                    if constexpr (D == 128) ptx::tma_load_2d(map, bar(L::B_FULL + slot), at + HALF_BYTES, 64, box_y);
                 }
                 last_bulk = u;
                 __syncwarp();
             } else {
                 const unsigned long long mine = reinterpret_cast<unsigned long long>(is_v ? vp : kp);
 #pragma unroll 4
-                for (int j = 0; j < 16; ++j) {
-                    const int row = pw * 32 + 2 * j + sub;
-                    const char *p = reinterpret_cast<const char *>(__shfl_sync(kFull, mine, 2 * j + sub));
+                for (int j = 0; j < CHUNKS; ++j) {
+                    const int row = pw * 32 + ROWS_AT_ONCE * j + sub;
+                    const char *p = reinterpret_cast<const char *>(__shfl_sync(kFull, mine, ROWS_AT_ONCE * j + sub));
                     cp16(dst + (chunk >> 3) * HALF_BYTES + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
                          p == nullptr ? static_cast<const char *>(a.K) : p + chunk * 16, p != nullptr);
                 }
@@ -324,7 +329,9 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             // S = Q_h K(t)^T into score buffer `buf`; K(t) has been waited for
             auto scores = [&](int h, int buf, int t) {
                 ptx::tc_fence_after();
-                ptx::mma_ss_k128_warp(tmem + buf * 128, dq + h * STEP, dk + (2 * (t - x0) % NS) * STEP, IDESC_QK, 0u);
+                const uint64_t k = dk + (2 * (t - x0) % NS) * STEP;
+                if constexpr (D == 128) ptx::mma_ss_k128_warp(tmem + buf * 128, dq + h * STEP, k, IDESC_QK, 0u);
+                else ptx::mma_ss_k64_warp(tmem + buf * 128, dq + h * STEP, k, IDESC_QK, 0u);
                 ptx::tc_commit_warp(bar(L::B_SFULL + buf));
                 if (lane == 0) ptx::mbar_arrive(bar(L::B_SFULL + buf));
                 __syncwarp();
@@ -428,14 +435,14 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         // The queries of this warp's rows, 16 lanes to a row, swizzled like the keys.  The scores of
         // the last tile are done, so nothing reads the old ones.
         auto load_q = [&](const Item &i) {
-            const char *q = static_cast<const char *>(a.Q) + (list_row(i) + mt * BM + h * 128 + quarter * 32) * (HD * 2);
-            const int sub = lane >> 4, chunk = lane & 15;
+            const char *q = static_cast<const char *>(a.Q) + (list_row(i) + mt * BM + h * 128 + quarter * 32) * (D * 2);
+            const int sub = lane / CHUNKS, chunk = lane % CHUNKS;
 #pragma unroll 4
-            for (int j = 0; j < 16; ++j) {
-                const int r = 2 * j + sub;
+            for (int j = 0; j < CHUNKS; ++j) {
+                const int r = ROWS_AT_ONCE * j + sub;
                 const bool there = mt * BM + h * 128 + quarter * 32 + r < a.R;
                 cp16(base + L::OFF_Q + h * TILE_BYTES + (chunk >> 3) * HALF_BYTES + (quarter * 32 + r) * 128 + (((chunk & 7) ^ (r & 7)) << 4),
-                     there ? q + r * (HD * 2) + chunk * 16 : static_cast<const char *>(a.Q), there);
+                     there ? q + r * (D * 2) + chunk * 16 : static_cast<const char *>(a.Q), there);
             }
             cp_commit();
         };
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             const int end = min(it.first + it.k.tiles, x1);
             float m = -INFINITY, l = 0.f;
             bool has_odd = false;
-            float *const part = part_at(a, group, mt, x0 >= it.first ? 0 : 1, BM, HD);
+            float *const part = part_at(a, group, mt, x0 >= it.first ? 0 : 1, BM, D);
             if (it.k.n == 0 && threadIdx.x == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
             for (int t = x; t < end; ++t, ++n_s) {
                 const int buf = HALVES == 2 ? h : (t - x0) & 1;
@@ -568,7 +575,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                         }
                         const float f = rescale ? ptx::ex2(m - m_new) : 1.f;
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
+                        for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
                             ptx::tmem_ld16(tO + c * 16, o);
                             ptx::tmem_wait_ld16(o);
@@ -603,8 +610,8 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             if (!live || __uint_as_float(sc) == -INFINITY) continue;
                             const float p = ptx::ex2(fmaf(__uint_as_float(sc), a.scale_log2, -mu));
                             const Key key = find_key(a, it.k, it.b, it.kv, rest * BN + col);
-                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(key.core ? a.Vc : a.V) + key.row * HD;
-                            for (int e = 0; e < HD; ++e) {
+                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(key.core ? a.Vc : a.V) + key.row * D;
+                            for (int e = 0; e < D; ++e) {
                                 const float f = __bfloat162float(v[e]);
                                 float &sum = part[part_col(BM, in, e)];
                                 const float before = has_odd ? sum : 0.f;
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             ptx::tc_fence_after();
             if (__any_sync(kFull, has_odd)) {
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < D / 16; ++c) {
                     uint32_t v[16];
                     ptx::tmem_ld16(tO + c * 16, v);
                     ptx::tmem_wait_ld16(v);
@@ -689,7 +696,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             const int64_t out = list_row(it) + row;
             if (!idle) {
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < D / 32; ++c) {
                     __syncwarp();
                     uint32_t o[32];
                     ptx::tmem_ld32(tO + c * 32, o);
@@ -698,7 +705,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = nothing ? 0u : __float_as_uint(__uint_as_float(o[k]) * scale);
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.O) + out * HD + c * 32);
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.O) + out * D + c * 32);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t v[4];
@@ -721,8 +728,8 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 if (whole) {
                     a.LSE[out] = nothing ? -INFINITY : (m + log2f(l)) * kLn2;
                 } else {
-                    part[BM * HD + in] = m;
-                    part[BM * HD + BM + in] = l;
+                    part[BM * D + in] = m;
+                    part[BM * D + BM + in] = l;
                 }
             }
             if (threadIdx.x == 0 && mt == 0) note_span(a, it, group, x0, x1);
@@ -745,26 +752,26 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     }
 }
 
-template <int HALVES>
+template <int HALVES, int D>
 cudaError_t launch_halves(const CUtensorMap (&map)[4], const TreeArgs &a, unsigned long long lim, int skip_loads, cudaStream_t stream) {
     static std::atomic<int> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || ready[dev].load(std::memory_order_relaxed) == 0) {
-        e = cudaFuncSetAttribute(tree_tc_kernel<HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+        e = cudaFuncSetAttribute(tree_tc_kernel<HALVES, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(1, std::memory_order_relaxed);
     }
-    return start_dependent(tree_tc_kernel<HALVES>, dim3(static_cast<unsigned>(a.groups) * a.n_mt), Layout<HALVES>::THREADS,
-                           static_cast<int>(Layout<HALVES>::bytes(a.T)), stream, map[0], map[1], map[2], map[3], a, lim, skip_loads);
+    return start_dependent(tree_tc_kernel<HALVES, D>, dim3(static_cast<unsigned>(a.groups) * a.n_mt), Layout<HALVES, D>::THREADS,
+                           static_cast<int>(Layout<HALVES, D>::bytes(a.T)), stream, map[0], map[1], map[2], map[3], a, lim, skip_loads);
 }
 
 }  // namespace
 
 int tc_rows(int R) { return R <= 128 ? 128 : 256; }
 
-cudaError_t launch_tc(TreeArgs a, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream) {
+cudaError_t launch_tc(TreeArgs a, int d, unsigned long long wait_limit_ns, int skip_loads, cudaStream_t stream) {
     // Runs: boxes of 32, 16 or 8 rows, the most that both page sizes are made of; rows of a pool
     // are 32-bit coordinates of its tensor map.  Otherwise every tile comes by cp.async.
     CUtensorMap map[4];
@@ -777,11 +784,13 @@ cudaError_t launch_tc(TreeArgs a, unsigned long long wait_limit_ns, int skip_loa
     if (enc == nullptr) return cudaErrorNotSupported;
     const uint32_t box = a.box_log2 > 0 ? 1u << a.box_log2 : 8u;
     const uint64_t n = a.box_log2 > 0 ? rows : 8, nc = a.box_log2 > 0 ? crows : 8;
-    if (!encode_rows_bf16_d128(enc, &map[0], a.K, n, box) || !encode_rows_bf16_d128(enc, &map[1], a.V, n, box) ||
-        !encode_rows_bf16_d128(enc, &map[2], a.Kc, nc, box) || !encode_rows_bf16_d128(enc, &map[3], a.Vc, nc, box))
+    if (!encode_rows_bf16(enc, &map[0], a.K, d, n, box) || !encode_rows_bf16(enc, &map[1], a.V, d, n, box) ||
+        !encode_rows_bf16(enc, &map[2], a.Kc, d, nc, box) || !encode_rows_bf16(enc, &map[3], a.Vc, d, nc, box))
         return cudaErrorInvalidValue;
-    return tc_rows(a.R) == 128 ? launch_halves<1>(map, a, wait_limit_ns, skip_loads, stream)
-                               : launch_halves<2>(map, a, wait_limit_ns, skip_loads, stream);
+    const bool one = tc_rows(a.R) == 128;
+    if (d == 64)
+        return one ? launch_halves<1, 64>(map, a, wait_limit_ns, skip_loads, stream) : launch_halves<2, 64>(map, a, wait_limit_ns, skip_loads, stream);
+    return one ? launch_halves<1, 128>(map, a, wait_limit_ns, skip_loads, stream) : launch_halves<2, 128>(map, a, wait_limit_ns, skip_loads, stream);
 }
 
 }  // namespace tree

@@ -306,3 +306,20 @@ def test_wait_time_out_is_reported(T):
     assert status.item() == api.CCA_ERR_TIMEOUT
     got = call(x, 16, 64)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("d,heads,T", [(128, 1, 3), (128, 4, 40), (64, 2, 5), (64, 1, 20), (64, 4, 40)])
+@pytest.mark.parametrize("seed", range(3))
+def test_runs_that_begin_and_end_anywhere(d, heads, T, seed):
+    """Lists of one tile to many, more of them than groups or fewer: a run may begin inside a list, at its
+    end, or hold several; with d = 64 on both kernels."""
+    rng = np.random.default_rng([seed, d, T])
+    B, Hkv = [(3, 8), (37, 3), (7, 2)][seed]
+    lens = [int(rng.choice([0, 5, 100, 900, 2500, 6000])) + int(rng.integers(0, 90)) for _ in range(B)]
+    if B > 30:
+        lens = [n % 1500 for n in lens]
+    g, w, rows, crows = 2, 64, [16, 64, 48][seed], [64, 8, 40][seed]
+    x = make(B, T, heads * Hkv, Hkv, d, lens, g, w, rows, crows, torch.bfloat16, seed=seed)
+    O, LSE = check(x, g, w, rows, crows, what=f"lens {lens}")
+    again = call(x, g, w)
+    assert torch.equal(O, again[0]) and torch.equal(LSE, again[1])

@@ -25,11 +25,11 @@ class Model:
     land by themselves), the others by the producers' own copies.  Roles are generators that yield a condition to
     wait for, or None for a step."""
 
-    def __init__(self, halves, segs, used=None, runs=0):
+    def __init__(self, halves, segs, used=None, runs=0, slots=None, metas=4):
         self.H, self.segs = halves, segs
         self.run_tiles = {x + i for _, x, end in self.tiles() for i in range(min(runs, end - x))}
         self.flying, self.loaders = [], 4    # TMA copies in flight, producers at work
-        self.NS = 4 if halves == 2 else 5
+        self.NS = slots or (4 if halves == 2 else 5)
         self.used = [True] * halves if used is None else used
         n = self.NS
         self.full, self.empty = [Bar(4) for _ in range(n)], [Bar(1) for _ in range(n)]
@@ -37,7 +37,7 @@ class Model:
         self.sfull, self.pfull = [Bar(2), Bar(2)], [Bar(1) for _ in range(halves)]
         self.pvdone = [Bar(1) for _ in range(halves)]
         self.slot = [None] * n               # (what, tile) that has landed
-        self.meta = [None] * 4
+        self.meta = [None] * metas
         self.q = [None] * halves             # list whose queries are in shared memory
         self.s = [None, None]                # score buffers: ("S" | "P", half, tile)
         self.o = [None] * halves             # last tile added to O, and its list
@@ -71,7 +71,7 @@ class Model:
             if w == 0:
                 self.slot[slot] = "loading"
                 if not u & 1:
-                    self.meta[x & 3] = x
+                    self.meta[x % len(self.meta)] = x
             yield None
             if runs:
                 self.flying.append(lambda p=(slot, what): land(p))
@@ -195,7 +195,7 @@ class Model:
                 if t not in self.run_tiles:
                     yield lambda: self.full[v % NS].done(v // NS)  # noqa: B023
                     assert self.slot[v % NS] == ("V", t)
-                assert self.s[buf] == ("S", h, t) and self.meta[t & 3] == t
+                assert self.s[buf] == ("S", h, t) and self.meta[t % len(self.meta)] == t
                 if t + 1 == end and seg + 1 < len(segs):
                     self.q[h] = seg + 1      # the next list's queries, handed over after this tile
                 yield None
@@ -204,7 +204,7 @@ class Model:
                     assert self.o[0] == t - 1
                 elif self.H == 2 and t > x0:
                     assert self.o[h] == t - 1
-                assert self.s[buf] == ("S", h, t) and self.meta[t & 3] == t
+                assert self.s[buf] == ("S", h, t) and self.meta[t % len(self.meta)] == t
                 self.s[buf] = ("P", h, t)
                 if self.H == 1 and n_s > 0:
                     yield lambda: self.pvdone[0].done(n_s + 1)  # noqa: B023
@@ -241,3 +241,14 @@ def test_every_schedule_ends(halves, used, segs, runs):
     for seed in range(30):
         random.seed(seed)
         Model(halves, segs, used, runs).run(random.Random(seed))
+
+
+@pytest.mark.parametrize("halves", [1, 2])
+@pytest.mark.parametrize("slots", [4, 5, 8])
+@pytest.mark.parametrize("segs", [[1], [9], [3, 1], [2, 7, 1, 5], [30, 3], [1, 2, 3, 4, 5, 6]])
+def test_every_ring_depth_ends(halves, segs, slots):
+    """Eight sets of a tile's bits are enough for a ring of four tiles, as d = 64 has it."""
+    for runs in (0, 2, 100):
+        for seed in range(15):
+            random.seed(seed)
+            Model(halves, segs, None, runs, slots, 8).run(random.Random(seed))
