@@ -638,7 +638,7 @@ constexpr int JOIN_RESIDENT = 8;  // blocks per SM
 // A warp joins 4C columns of up to 32 rows of one list.  The time is that of three dependent steps
 // (the list's span, its parts, the stores), so blocks are small.  Where the lists are few, C is
 // least, for the most blocks; many lists take twice that, which makes a row's store a whole sector
-// of the output (16 sequences of 64 nodes, 128 lists of 256 rows: 15.3 -> 10 us).  A lane takes a
+// of the output (16 sequences of 64 nodes, 128 lists of 256 rows: 15.3 -> 9.6 us).  A lane takes a
 // row; where there are fewer rows, the lanes left over take parts: lane group i the parts i,
 // i + groups, .. of the list, in the order of the groups that wrote them, and the lane groups
 // are added up in a fixed order.  Lists that one group finished are already written.
