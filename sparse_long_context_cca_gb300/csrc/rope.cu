@@ -41,6 +41,7 @@ struct RopeArgs {
     RopeSrc t[3];
     int n_t, heads;       // tensors, and their heads added up
     int heads_per_block;  // heads one thread walks through
+    uint64_t by_units;    // 2^64 over the units of a row, rounded up
     int B, N, d, rot, layout, inverse;
     float factor;
     const double *inv_freq;
@@ -95,23 +96,38 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t turn, float factor, float 
 }
 
 constexpr int ROPE_BATCH = 2;  // heads whose loads are in flight together
+template <int V, bool HALF>
+__host__ __device__ constexpr int angles() { return HALF ? V : V / 2 > 0 ? V / 2 : 1; }  // of a thread
+__host__ __device__ constexpr int share(int n) { return n < 4 ? n : 4; }                 // threads that make them
+// Heads per thread up to which they are shared.  Each thread its own against shared, us: 32 + 8 heads
+// of 128, bf16, 16 tokens 3.2 and 2.5, 512 (2 heads) 5.0 and 3.6, 2048 (3) 10.4 and 9.0, 4096 (4)
+// 16.6 and 17.7; fp32, 1024 (3) 7.5 and 7.6, 2048 (4) 13.0 and 15.7; storing 16 x 32 tokens of 48
+// heads (2) 8.0 and 4.8.
+constexpr int SHARE_MAX = 3;
 
 // V: columns per access.  HALF: pairs (i, i + rot/2), a thread owns V pairs in two chunks;
 // otherwise pairs (2i, 2i + 1), a thread owns the V/2 pairs of one chunk.
 // PAGED: the serving form, one block row per sequence.
-template <typename T, int V, bool HALF, bool PAGED>
-__global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a) {
+// SHARED: few heads per thread, so that the angles would be most of the work: a block takes fewer
+// rows and `share` times the heads, and its threads make the angles together.
+template <typename T, int V, bool HALF, bool PAGED, bool SHARED>
+__global__ void __launch_bounds__(ROPE_THREADS, SHARED ? 3 : 5) rope_kernel(const RopeArgs a) {
     using R = typename Raw<sizeof(T) * V>::type;
     __shared__ uint64_t sm_freq[64];
     __shared__ int16_t sm_parent[PAGED ? TREE_MAX_NODES : 1];
+    constexpr int NA = angles<V, HALF>();
+    constexpr int S = SHARED ? share(NA) : 1;
+    constexpr int PER = ROPE_THREADS / S;  // row units of a block
+    __shared__ float2 sm_angle[SHARED ? NA * PER : 1];
     const int half = a.rot / 2;
     // units of a row: the rotated chunks (or chunk pairs), then the copied ones
     const int turned = (HALF ? half : a.rot) / V;
     const int units = turned + (a.d - a.rot) / V;
-    const int64_t idx = static_cast<int64_t>(blockIdx.x) * ROPE_THREADS + threadIdx.x;
-    const int64_t row = idx / units;
+    const int local = SHARED ? threadIdx.x % PER : threadIdx.x, sub = SHARED ? threadIdx.x / PER : 0;
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * PER + local;
+    const int64_t row = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(idx), a.by_units));
     const int u = static_cast<int>(idx - row * units);
-    const bool work = row < (PAGED ? a.N : static_cast<int64_t>(a.B) * a.N);
+    const bool inside = row < (PAGED ? a.N : static_cast<int64_t>(a.B) * a.N);
     const int b = PAGED ? static_cast<int>(blockIdx.z) : static_cast<int>(row / a.N);
     const int64_t n = PAGED ? row : row - static_cast<int64_t>(b) * a.N;
     const bool turn = u < turned;
@@ -119,9 +135,10 @@ __global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a)
     const int64_t other = HALF ? half * static_cast<int64_t>(sizeof(T)) : 0;
 
     // The head walk: tensors one after the other, ROPE_BATCH heads at a time.
-    const int h0 = blockIdx.y * a.heads_per_block, h1 = min(h0 + a.heads_per_block, a.heads);
+    const int h0 = (blockIdx.y * S + sub) * a.heads_per_block, h1 = min(h0 + a.heads_per_block, a.heads);
+    const bool work = inside && (!SHARED || h0 < h1);
     int which = 0, first = 0;  // tensor of the batch, heads before it
-    while (h0 - first >= a.t[which].H) first += a.t[which++].H;
+    while ((!SHARED || work) && h0 - first >= a.t[which].H) first += a.t[which++].H;
     Chunk<T, V> lo[ROPE_BATCH], hi[ROPE_BATCH];
     auto batch_heads = [&](int h) { return min(min(ROPE_BATCH, h1 - h), first + a.t[which].H - h); };
     auto load = [&](int h, int count) {
@@ -137,6 +154,11 @@ __global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if (work) load(h0, batch_heads(h0));
+    int len = 0, count_b = 0;
+    if constexpr (PAGED) {  // asked for with the rest: what follows is a chain
+        len = a.lens[b];
+        count_b = a.counts != nullptr ? a.counts[b] : a.N;
+    }
 
     for (int i = threadIdx.x; i < half; i += ROPE_THREADS) {
         double f = a.inv_freq[i] * 0.15915494309189535;  // turns per position
@@ -151,28 +173,27 @@ __global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a)
             }
     }
     __syncthreads();
-    if (!work) return;
-    int64_t pos;
+    if (!SHARED && !work) return;
+    int64_t pos = 0;
     bool real = true;
     int64_t page = -1;  // of the row's slot, and the row inside it
     int page_off = 0;
     if constexpr (PAGED) {
-        int len = a.lens[b];
         if (len < 0) {
             if (a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
             real = false;
             len = 0;
         }
         pos = static_cast<int64_t>(len) + n;
-        if (a.counts != nullptr && n >= a.counts[b]) real = false;
-        if (real) {
-            const int64_t slot = static_cast<int64_t>(len) + n;
-            const int64_t c = slot / a.rows;
-            page = c < a.cols ? a.table[static_cast<int64_t>(b) * a.cols + c] : -1;
+        if (n >= count_b) real = false;
+        if (real && inside) {
+            const uint32_t slot = static_cast<uint32_t>(len) + static_cast<uint32_t>(n);  // below 2^32
+            const uint32_t c = slot / static_cast<uint32_t>(a.rows);
+            page = c < static_cast<uint32_t>(a.cols) ? a.table[static_cast<int64_t>(b) * a.cols + c] : -1;
             page_off = static_cast<int>(slot - c * a.rows);
         }
         if (a.parents != nullptr) {
-            int depth = 0, k = sm_parent[n];
+            int depth = 0, k = inside ? sm_parent[n] : -1;
             while (k >= 0) {  // parents are below their children, so this ends
                 ++depth;
                 k = sm_parent[k];
@@ -180,20 +201,30 @@ __global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a)
             if (k != -1) real = false;
             pos = static_cast<int64_t>(len) + depth;
         }
-        if (real && (page < 0 || page >= a.n_pages) && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        if (real && inside && (page < 0 || page >= a.n_pages) && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
         if (!real || page >= a.n_pages) page = -1;
-    } else {
+    } else if (inside) {
         pos = a.positions != nullptr ? a.positions[b * a.pos_stride + n] : a.start + n;
     }
     // this thread's cosines and sines
-    constexpr int NA = HALF ? V : V / 2 > 0 ? V / 2 : 1;
     float c[NA], s[NA];
     if (turn) {
 #pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            const int pair = HALF ? col + i : col / 2 + i;
+        for (int i = 0; i < NA / S; ++i) {
+            const int k = sub * (NA / S) + i, pair = HALF ? col + k : col / 2 + k;
             turn_cos_sin(static_cast<uint64_t>(pos) * sm_freq[pair], a.factor, c[i], s[i]);
             if (a.inverse) s[i] = -s[i];
+            if (SHARED) sm_angle[k * PER + local] = make_float2(c[i], s[i]);
+        }
+    }
+    if constexpr (SHARED) {
+        __syncthreads();
+        if (!work) return;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const float2 cs = sm_angle[i * PER + local];
+            c[i] = cs.x;
+            s[i] = cs.y;
         }
     }
     for (int h = h0; h < h1;) {
@@ -242,12 +273,12 @@ __global__ void __launch_bounds__(ROPE_THREADS, 5) rope_kernel(const RopeArgs a)
     }
 }
 
-template <typename T, int V, bool PAGED>
+template <typename T, int V, bool PAGED, bool SHARED>
 cudaError_t launch_one(const RopeArgs &a, dim3 grid, cudaStream_t stream) {
-    if (a.layout == 0) return start_dependent(rope_kernel<T, V, true, PAGED>, grid, ROPE_THREADS, 0, stream, a);
+    if (a.layout == 0) return start_dependent(rope_kernel<T, V, true, PAGED, SHARED>, grid, ROPE_THREADS, 0, stream, a);
     // an interleaved chunk holds whole pairs
     constexpr int VI = V < 2 ? 2 : V;
-    return start_dependent(rope_kernel<T, VI, false, PAGED>, grid, ROPE_THREADS, 0, stream, a);
+    return start_dependent(rope_kernel<T, VI, false, PAGED, SHARED>, grid, ROPE_THREADS, 0, stream, a);
 }
 
 // The widest access that every chunk boundary allows: rows are 16-byte aligned, so it is
@@ -265,6 +296,7 @@ cudaError_t launch_rope_any(int dtype, RopeArgs a, cudaStream_t stream) {
     const int v = access_width(a, dtype == CCA_BF16 ? 8 : 4);
     const int vv = a.layout == 1 && v < 2 ? 2 : v;
     const int units = (a.layout == 0 ? a.rot / 2 : a.rot) / vv + (a.d - a.rot) / vv;
+    a.by_units = ~uint64_t{0} / units + 1;  // units >= 4; exact below 2^57
     const int64_t rows = PAGED ? a.N : static_cast<int64_t>(a.B) * a.N;
     const int64_t blocks = (rows * units + ROPE_THREADS - 1) / ROPE_THREADS;
     if (blocks > 0x7fffffff) return cudaErrorNotSupported;
@@ -279,19 +311,26 @@ cudaError_t launch_rope_any(int dtype, RopeArgs a, cudaStream_t stream) {
     a.heads_per_block = (a.heads + groups - 1) / groups;
     groups = (a.heads + a.heads_per_block - 1) / a.heads_per_block;
     if (groups > 65535) return cudaErrorNotSupported;
-    const dim3 grid(static_cast<unsigned>(blocks), groups, PAGED ? a.B : 1);
+    dim3 grid(static_cast<unsigned>(blocks), groups, PAGED ? a.B : 1);
+    if (a.heads_per_block <= SHARE_MAX && v == (dtype == CCA_BF16 ? 8 : 4)) {
+        const int s = share(a.layout == 0 ? v : v / 2), per = ROPE_THREADS / s;
+        grid.x = static_cast<unsigned>((rows * units + per - 1) / per);
+        grid.y = (a.heads + s * a.heads_per_block - 1) / (s * a.heads_per_block);
+        return dtype == CCA_BF16 ? launch_one<__nv_bfloat16, 8, PAGED, true>(a, grid, stream)
+                                 : launch_one<float, 4, PAGED, true>(a, grid, stream);
+    }
     if (dtype == CCA_BF16) {
         switch (v) {
-            case 8: return launch_one<__nv_bfloat16, 8, PAGED>(a, grid, stream);
-            case 4: return launch_one<__nv_bfloat16, 4, PAGED>(a, grid, stream);
-            case 2: return launch_one<__nv_bfloat16, 2, PAGED>(a, grid, stream);
-            default: return launch_one<__nv_bfloat16, 1, PAGED>(a, grid, stream);
+            case 8: return launch_one<__nv_bfloat16, 8, PAGED, false>(a, grid, stream);
+            case 4: return launch_one<__nv_bfloat16, 4, PAGED, false>(a, grid, stream);
+            case 2: return launch_one<__nv_bfloat16, 2, PAGED, false>(a, grid, stream);
+            default: return launch_one<__nv_bfloat16, 1, PAGED, false>(a, grid, stream);
         }
     }
     switch (v) {
-        case 4: return launch_one<float, 4, PAGED>(a, grid, stream);
-        case 2: return launch_one<float, 2, PAGED>(a, grid, stream);
-        default: return launch_one<float, 1, PAGED>(a, grid, stream);
+        case 4: return launch_one<float, 4, PAGED, false>(a, grid, stream);
+        case 2: return launch_one<float, 2, PAGED, false>(a, grid, stream);
+        default: return launch_one<float, 1, PAGED, false>(a, grid, stream);
     }
 }
 

@@ -290,3 +290,22 @@ def test_refuses_a_flag_without_a_truth_value():
     with pytest.raises(ValueError, match="inverse"):
         api.cca_rope(x, None, freqs(64), inverse=torch.zeros(2))
     api.cca_rope(x, None, freqs(64), inverse=torch.ones((), dtype=torch.bool))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,rot", [(1, 1, 1, 0, 64, 64), (1, 1, 3, 1, 128, 128), (3, 5, 7, 2, 64, 32), (2, 33, 9, 8, 128, 64),
+                                              (1, 700, 5, 5, 128, 128), (1, 1500, 32, 8, 128, 128), (1, 3000, 32, 8, 64, 64)])
+def test_few_and_many_heads_per_thread(B, N, Hq, Hkv, d, rot, dtype, layout):
+    """Angles made by a block together or by each thread, heads that do not fill the last block."""
+    Q, K = rand(B, Hq, N, d, dtype=dtype), rand(B, Hkv, N, d, dtype=dtype, seed=1) if Hkv else None
+    f = freqs(rot)
+    q, k = api.cca_rope(Q, K, f, start=70000, layout=layout, factor=1.25)
+    pos = 70000 + np.arange(N)[None].repeat(B, 0)
+    close(q, *rotate(Q, pos, f.cpu(), layout, 1.25), "Q")
+    if Hkv:
+        close(k, *rotate(K, pos, f.cpu(), layout, 1.25), "K")
+    back = api.cca_rope(q, k, f, start=70000, layout=layout, factor=1.25, inverse=True)
+    for i, (y, x) in enumerate(zip(back, (q, k))):
+        if x is not None:
+            close(y, *rotate(x, pos, f.cpu(), layout, 1.25, -1.0), f"back {i}")
