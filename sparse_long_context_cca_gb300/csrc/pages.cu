@@ -78,11 +78,21 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
     __shared__ int sm_warp[RESERVE_WARPS];
     __shared__ int32_t sm_count[RESERVE_THREADS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int32_t *const count = a.B <= RESERVE_THREADS ? sm_count : a.count;
+    __shared__ int32_t sm_len[RESERVE_THREADS], sm_extra[RESERVE_THREADS];
+    const bool few = a.B <= RESERVE_THREADS;  // then what is known of a row is kept here
+    int32_t *const count = few ? sm_count : a.count;
     after_previous();
+    if (few) {
+        if (tid < a.B) {
+            sm_len[tid] = a.lens[tid];
+            sm_extra[tid] = a.extra[tid];
+        }
+        __syncthreads();
+    }
+    const int32_t *const lens = few ? sm_len : a.lens, *const extra = few ? sm_extra : a.extra;
     // The columns [c0, c1) of row b that its new rows lie in; an empty range for a bad row.
     auto range = [&](int b, int &c0, int &c1) {
-        const int len = a.lens[b], ex = a.extra[b];
+        const int len = lens[b], ex = extra[b];
         c0 = c1 = 0;
         if (ex <= 0) return true;
         const int64_t end = static_cast<int64_t>(len) + ex;
@@ -93,7 +103,7 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
     };
     // Whether row o's range takes in column c.
     auto reaches = [&](int o, int c) {
-        const int len = a.lens[o], ex = a.extra[o];
+        const int len = lens[o], ex = extra[o];
         const int64_t end = static_cast<int64_t>(len) + ex, at = static_cast<int64_t>(c) * a.rows;
         return ex > 0 && len >= 0 && end <= static_cast<int64_t>(a.cols) * a.rows && at + a.rows > len && at < end;
     };
@@ -195,7 +205,7 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
                 a.refs[page] = 1;
                 if (old >= 0 && old < a.n_pages) {
                     atomicSub(&a.refs[old], 1);  // stays above 0: its last holder keeps it
-                    const int len = a.lens[b];
+                    const int len = lens[b];
                     if (c == len / a.rows && len % a.rows != 0) {
                         a.pairs[2 * b] = old;
                         a.pairs[2 * b + 1] = page;
