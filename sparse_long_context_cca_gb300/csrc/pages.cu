@@ -72,7 +72,7 @@ __device__ int block_scan(int v, int *sm_warp, int &total) {
 
 // One block: the calls of a step touch a few entries per row, so what bounds this is the
 // chain of dependent reads (lengths, table, refs, the scan), not bandwidth: 6.5 us for 8 rows,
-// 9.3 us for 64 rows of which 32 share a page (42 us when a lane looked through the rows before
+// 9.1 us for 64 rows of which 32 share a page (42 us when a lane looked through the rows before
 // its own one at a time; 12 us with the counts in memory and a second look for the free pages).
 __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const ReserveArgs a) {
     __shared__ int sm_warp[RESERVE_WARPS];
