@@ -16,8 +16,8 @@
 // reach those, or that hold keys without a page, look at masks at all.
 //
 // Work split.  Lengths live on the device, so the split is made there: the tiles of all
-// (b, KV head) lists, one after the other, are dealt to the groups of the grid in equal
-// contiguous runs, whatever the lengths are.  A group finishes lists that lie wholly in its
+// (b, KV head) lists, one after the other, are dealt to the groups of the grid in contiguous
+// runs of equal cost, whatever the lengths are.  A group finishes lists that lie wholly in its
 // run and writes a partial (max, sum, output) for its first and last list otherwise; a
 // second kernel joins the partials of a list in the order of the groups.
 #include <cuda_bf16.h>
