@@ -333,7 +333,8 @@ void refuse_uncapturable_leaves() {
                         "a backward pass is being captured, but a graph made outside the capture still holds one of its "
                         "leaves on the default stream: let go of that graph's outputs first");
         }
-        for (const auto &edge : node->next_edges()) todo.push_back(edge.function.get());
+        for (size_t i = 0; i < node->num_outputs(); ++i)  // where this pass goes on
+            if (node->task_should_compute_output(i)) todo.push_back(node->next_edge(i).function.get());
     }
 }
 
@@ -404,15 +405,24 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
         turn.layout = static_cast<int>(ctx->saved_data["layout"].toInt());
         turn.factor = static_cast<float>(ctx->saved_data["factor"].toDouble());
         turn.inverse = !ctx->saved_data["inverse"].toBool();
+        // the gradients that this pass asks for: of Q, K or both
+        const auto here = torch::autograd::get_current_node();
+        List in;
+        for (int k = 0; k < (two ? 2 : 1); ++k)
+            if (here == nullptr || here->task_should_compute_output(k)) in.push_back(grads[k]);
         List g;
-        if (c10::GradMode::is_enabled()) {
-            g = apply(grads[0], two ? c10::optional<at::Tensor>(grads[1]) : c10::nullopt, turn.inv_freq,
+        if (in.empty()) {
+        } else if (c10::GradMode::is_enabled()) {
+            g = apply(in[0], in.size() == 2 ? c10::optional<at::Tensor>(in[1]) : c10::nullopt, turn.inv_freq,
                       turn.positions.defined() ? c10::optional<at::Tensor>(turn.positions) : c10::nullopt, turn.start,
                       static_cast<int64_t>(turn.layout), static_cast<double>(turn.factor), turn.inverse);
         } else {
-            g = turned(turn, two ? List{grads[0], grads[1]} : List{grads[0]});
+            g = turned(turn, in);
         }
-        return {g[0], two ? g[1] : at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
+        List out(8);
+        for (size_t k = 0, n = 0; n < g.size(); ++k)
+            if (here == nullptr || here->task_should_compute_output(k)) out[k] = g[n++];
+        return out;
     }
 };
 

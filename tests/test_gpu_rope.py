@@ -309,3 +309,53 @@ def test_few_and_many_heads_per_thread(B, N, Hq, Hkv, d, rot, dtype, layout):
     for i, (y, x) in enumerate(zip(back, (q, k))):
         if x is not None:
             close(y, *rotate(x, pos, f.cpu(), layout, 1.25, -1.0), f"back {i}")
+
+
+def test_backward_in_a_graph_past_held_leaves():
+    """A captured pass that does not come to a held leaf, or to one held on another stream, is not refused."""
+    Q, K = (rand(1, 2, 40, 64, seed=s).requires_grad_() for s in (1, 2))
+    f = freqs(64)
+
+    def step(leaves):
+        q, k = api.rope(Q, K, f)
+        loss = (q * k).square().sum()
+        return loss, torch.autograd.grad(loss, leaves)
+
+    want = step([Q, K])[1]
+    held = K.exp()                          # keeps K on the default stream
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step([Q])[1]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0])
+    del held
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        held = step([Q, K])[0]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step([Q, K])[1]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and held.isfinite()
+
+
+def test_one_gradient_of_two():
+    Q, K = rand(2, 4, 21, 64).requires_grad_(), rand(2, 2, 21, 64, seed=1).requires_grad_()
+    f = freqs(48)
+    dq, dk = rand(2, 4, 21, 64, seed=2), rand(2, 2, 21, 64, seed=3)
+    run = lambda leaves, q, k, **kw: torch.autograd.grad(api.rope(q, k, f, start=9), leaves, [dq, dk], **kw)  # noqa: E731
+    want = run([Q, K], Q, K)
+    for i, leaf in enumerate((Q, K)):
+        assert torch.equal(run([leaf], Q, K)[0], want[i])
+        assert torch.equal(run([leaf], *[x if x is leaf else x.detach() for x in (Q, K)])[0], want[i])
+        # differentiated again: the rotation of the second gradient
+        d = rand(*leaf.shape, seed=7)
+        dy = [g.clone().requires_grad_() for g in (dq, dk)]
+        g, = torch.autograd.grad(api.rope(Q, K, f, start=9), [leaf], dy, create_graph=True)
+        again, = torch.autograd.grad(g, [dy[i]], d)
+        assert torch.equal(again, api.cca_rope(d, None, f, start=9)[0])
