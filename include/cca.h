@@ -398,6 +398,10 @@ int cca_rope_append(const cca_rope_tensor_t *q, const cca_rope_tensor_t *k, cons
  * workspace: caller-owned, at least cca_tree_workspace_size(params, T) bytes, rewritten by
  * every call; two calls that may run at the same time need one each.
  * O, LSE and the workspace must overlap neither an input nor one another.
+ * Precision: scores, sums and outputs are fp32.  In bf16 the softmax weights meet V rounded to
+ * bf16, as in cca_attn_fwd; up to 16 rows per KV head (T * Hq / Hkv: plain decoding) they meet it
+ * in two bf16 parts, so that an output is off by little more than its own rounding, as it is in
+ * cca_decode_fwd.
  * Supported: bf16 or f32, d in {64, 128}, 1 <= T <= min(256, w), B <= 1024.
  */
 int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core, const int32_t *lens,

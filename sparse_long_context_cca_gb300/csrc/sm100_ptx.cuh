@@ -408,5 +408,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return r;
 }
 
+// The same, both cut off towards zero.
+__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
 }  // namespace ptx
 }  // namespace cca

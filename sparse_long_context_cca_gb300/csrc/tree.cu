@@ -305,18 +305,25 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
                 o[n][2 * i + 1] *= corr;
             }
         }
-        // O += P V.  P is rounded to bf16 for the matrix units (the sum above is not).
+        // O += P V, each weight as two bf16 parts (the sum above has it whole)
 #pragma unroll
         for (int kk = 0; kk < NT / 2; ++kk) {
-            const uint32_t p[4] = {ptx::pack_bf16x2(s[2 * kk][0], s[2 * kk][1]), ptx::pack_bf16x2(s[2 * kk][2], s[2 * kk][3]),
-                                   ptx::pack_bf16x2(s[2 * kk + 1][0], s[2 * kk + 1][1]),
-                                   ptx::pack_bf16x2(s[2 * kk + 1][2], s[2 * kk + 1][3])};
+            uint32_t high[4], low[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float p0 = s[2 * kk + (i >> 1)][(i & 1) * 2], p1 = s[2 * kk + (i >> 1)][(i & 1) * 2 + 1];
+                high[i] = ptx::cut_bf16x2(p0, p1);
+                low_parts(p0, p1, 0xffff0000u, LOW_MORE);
+                low[i] = ptx::cut_bf16x2(p0, p1);
+            }
 #pragma unroll
             for (int n = 0; n < DT; n += 2) {
                 uint32_t f[4];
                 ldsm4_t(vbase + chunk_at(wk * KW + kk * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), n + (lane >> 4)), f);
-                mma16816(o[n], p, f[0], f[1]);
-                mma16816(o[n + 1], p, f[2], f[3]);
+                mma16816(o[n], high, f[0], f[1]);
+                mma16816(o[n + 1], high, f[2], f[3]);
+                mma16816(o[n], low, f[0], f[1]);
+                mma16816(o[n + 1], low, f[2], f[3]);
             }
         }
         if (masked && (mt_.odd[0] | mt_.odd[1]) != 0) {

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "paged.cuh"
+#include "sm100_ptx.cuh"
 
 namespace cca {
 namespace tree {
@@ -395,6 +396,26 @@ __device__ __forceinline__ void note_span(const TreeArgs &a, const Item &it, int
     int2 *span = a.spans + it.b * a.Hkv + it.kv;
     if (it.first >= x0) span->x = 2 * group + (it.first == x0 ? 0 : 1);
     if (it.first + it.k.tiles <= x1) span->y = group;
+}
+
+// ---------------------------------------------------------------- the weights
+
+// Rows per KV head up to which the softmax weights meet V in two bf16 parts, 2^-14 of a weight in
+// all: one token of up to 16 heads is plain decoding, which keeps its weights in fp32 over a
+// contiguous cache.  One part, 2^-8, makes an output's error 1.4 times what its own rounding to bf16
+// makes; more rows, which are there for the matrix units, have that (a second product each and the
+// parts' arithmetic took 8 sequences of 24 nodes from 26.5 to 28.7 us).
+constexpr int TWO_PART_ROWS = 16;
+
+// The high part is a weight cut off to bf16, so the low part is not negative; it takes 2^-23 of the
+// weight along (factor `more`) and is 0 for the weight 0 alone: an infinity in V times either part is
+// what it is times the weight.
+constexpr float LOW_MORE = 1.00000011920928955f;
+// p - cut(p) for two weights; mask 0 (and more = 1) leaves them as they are.
+__device__ __forceinline__ void low_parts(float &p0, float &p1, uint32_t mask, float more) {
+    const uint64_t cut = ptx::f2(__uint_as_float((__float_as_uint(p0) & mask) ^ 0x80000000u),
+                                 __uint_as_float((__float_as_uint(p1) & mask) ^ 0x80000000u));
+    ptx::f2_split(ptx::fma2(ptx::f2(p0, p1), ptx::f2(more, more), cut), p0, p1);
 }
 
 // ---------------------------------------------------------------- copies

@@ -6,14 +6,15 @@
 // to 256 rows read K and V once; the rows that a small tree leaves empty cost nothing, as the
 // loads bound it.  Per tile an SM's share of HBM needs 64 KB / 44 GB/s = 1.5 us (2800 cycles).
 // Measured: one half 2300 cycles a tile from L2, so HBM is the bound (64 sequences of one token,
-// 32 heads, 8 K: 244 us, 0.86 of the copy bandwidth); two halves 3500 cycles, the four products
+// 32 heads, 8 K: 246 us with weights of one part, 0.94 of the copy bandwidth, 271 us with the two
+// that so few rows have); two halves 3500 cycles, the four products
 // at 820 cycles each against 512 of tensor work, as both read their operands from shared memory
 // (192 KB a tile at 128 B a cycle, next to 64 KB of copies): 16 sequences x 64 nodes, 32 heads
 // over 8, 128 K: 135 us, 4.4 TB/s and 1.1 PFLOP/s.  64-key tiles with two score buffers per half
 // free the softmax from waiting for its product, but their N = 64 products took 740 cycles each:
 // 201 us.  A call on little work is a chain: the CTA's run 1.8 us, page look-up and first copy
 // 2.5 us, first softmax 1.4 us, output 1.5 us, then the join (one token of 32 heads at 32 K,
-// 49 MB: 17.8 us warm, 22.5 us from HBM).
+// 49 MB: 19.4 us warm, 24.0 us from HBM).
 // At d = 64 a tile is half as long to copy (1400 cycles) and its softmax (2100) is the bound: 8
 // sequences of 24 nodes, 32 heads over 8, up to 32 K: 23.6 us (38.4 by mma.sync).
 //
@@ -29,6 +30,12 @@
 // K(t) and V(t) take two consecutive slots of a ring of NS tiles and are freed apart: K
 // when its scores are done, V when its product is (both at once cost a load's latency per tile:
 // 230 us in place of 158 at the time).
+//
+// Up to TWO_PART_ROWS rows the weights keep two parts: lanes 16 .. 31 of the first warp hold the
+// same rows again (their queries too, so their scores and weights are the same to the bit) and put
+// the weights' low parts into P, and the two outputs of a row are added at the list's end.  That
+// costs three instructions for two weights and no matrix work: one token of 32 heads at 32 K 18.0 -> 19.4
+// us, 64 sequences of one token at 8 K 246 -> 271, with 32 heads over 8 69 -> 76.
 //
 // Two halves: S_A | S_B | O_A | O_B fill the tensor memory; the halves' softmaxes and MMAs
 // alternate.  P_h overwrites S_h, and S_h of the next tile is issued after the product that
@@ -101,7 +108,8 @@ struct Layout {
 // The lowest n bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-template <int HALVES, int D>
+// TWO_PARTS: up to TWO_PART_ROWS rows (with one half).
+template <int HALVES, int D, bool TWO_PARTS>
 __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ CUtensorMap tmKc, const __grid_constant__ CUtensorMap tmVc, const TreeArgs a,
@@ -416,9 +424,14 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         // ------------------------------------------------------------ softmax and output
         const int h = HALVES == 2 ? wg : 0;
         const int quarter = warp & 3;
-        const int in = h * 128 + quarter * 32 + lane;  // row of the CTA
-        const int row = mt * BM + in;                  // row of the KV head
+        // A lane's row among its warp's 32; with two parts lane 16 + r has row r again, for the low ones.
+        auto row_of = [](int r) { return TWO_PARTS ? r & (TWO_PART_ROWS - 1) : r; };
+        const int in = h * 128 + quarter * 32 + row_of(lane);  // row of the CTA
+        const int row = mt * BM + in;                          // row of the KV head
         const bool live = row < a.R;
+        const bool mine = live && row_of(lane) == lane;        // it writes the row
+        const uint32_t cut = row_of(lane) == lane ? 0u : 0xffff0000u;
+        const float more = row_of(lane) == lane ? 1.f : LOW_MORE;
         const bool idle = mt * BM + h * 128 + quarter * 32 >= a.R;  // no row of this warp
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tO = tmem + lane_addr + TM_O + h * 128;
@@ -440,9 +453,9 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
 #pragma unroll 4
             for (int j = 0; j < CHUNKS; ++j) {
                 const int r = ROWS_AT_ONCE * j + sub;
-                const bool there = mt * BM + h * 128 + quarter * 32 + r < a.R;
+                const bool there = mt * BM + h * 128 + quarter * 32 + row_of(r) < a.R;
                 cp16(base + L::OFF_Q + h * TILE_BYTES + (chunk >> 3) * HALF_BYTES + (quarter * 32 + r) * 128 + (((chunk & 7) ^ (r & 7)) << 4),
-                     there ? q + r * (D * 2) + chunk * 16 : static_cast<const char *>(a.Q), there);
+                     there ? q + row_of(r) * (D * 2) + chunk * 16 : static_cast<const char *>(a.Q), there);
             }
             cp_commit();
         };
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                             __syncwarp();
                             uint32_t sc;
                             asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(sc) : "r"(tS + col));
-                            if (!live || __uint_as_float(sc) == -INFINITY) continue;
+                            if (!mine || __uint_as_float(sc) == -INFINITY) continue;
                             const float p = ptx::ex2(fmaf(__uint_as_float(sc), a.scale_log2, -mu));
                             const Key key = find_key(a, it.k, it.b, it.kv, rest * BN + col);
                             const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(key.core ? a.Vc : a.V) + key.row * D;
@@ -621,7 +634,8 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                         }
                         __syncwarp();
                     }
-                    // p = 2^(s*scale - mu), two columns per packed FMA; P rounds to bf16, the sum does not
+                    // p = 2^(s*scale - mu), two columns per packed FMA; P rounds to bf16 (see
+                    // TWO_PART_ROWS), the sum does not
                     const uint64_t sc2 = ptx::f2(a.scale_log2, a.scale_log2);
                     const uint64_t nm2 = ptx::f2(-mu, -mu);
                     uint64_t lp[2] = {0, 0};
@@ -641,10 +655,15 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                                 const uint64_t x2 = ptx::fma2(ptx::f2(__uint_as_float(s[q >> 1][col]), __uint_as_float(s[q >> 1][col + 1])), sc2, nm2);
                                 float y0, y1;
                                 ptx::f2_split(x2, y0, y1);
-                                const float p0 = ptx::ex2(y0);
-                                const float p1 = ptx::ex2(y1);
+                                float p0 = ptx::ex2(y0);
+                                float p1 = ptx::ex2(y1);
                                 lp[k & 1] = ptx::add2(lp[k & 1], ptx::f2(p0, p1));
-                                pk[k] = ptx::pack_bf16x2(p0, p1);
+                                if constexpr (TWO_PARTS) {
+                                    low_parts(p0, p1, cut, more);
+                                    pk[k] = ptx::cut_bf16x2(p0, p1);
+                                } else {
+                                    pk[k] = ptx::pack_bf16x2(p0, p1);
+                                }
                             }
                             ptx::tmem_st8(tS + c * 32 + q * 8, pk);  // P over scores that have been read
                         }
@@ -701,7 +720,12 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                     uint32_t o[32];
                     ptx::tmem_ld32(tO + c * 32, o);
                     ptx::tmem_wait_ld(o);
-                    if (!live) continue;
+                    if constexpr (TWO_PARTS) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) + __shfl_down_sync(kFull, __uint_as_float(o[k]), TWO_PART_ROWS));
+                    }
+                    if (!mine) continue;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = nothing ? 0u : __float_as_uint(__uint_as_float(o[k]) * scale);
                     if (whole) {
@@ -724,7 +748,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(L::B_OFREE + h));
-            if (live) {
+            if (mine) {
                 if (whole) {
                     a.LSE[out] = nothing ? -INFINITY : (m + log2f(l)) * kLn2;
                 } else {
@@ -752,18 +776,18 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     }
 }
 
-template <int HALVES, int D>
+template <int HALVES, int D, bool TWO_PARTS = false>
 cudaError_t launch_halves(const CUtensorMap (&map)[4], const TreeArgs &a, unsigned long long lim, int skip_loads, cudaStream_t stream) {
     static std::atomic<int> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || ready[dev].load(std::memory_order_relaxed) == 0) {
-        e = cudaFuncSetAttribute(tree_tc_kernel<HALVES, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+        e = cudaFuncSetAttribute(tree_tc_kernel<HALVES, D, TWO_PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev].store(1, std::memory_order_relaxed);
     }
-    return start_dependent(tree_tc_kernel<HALVES, D>, dim3(static_cast<unsigned>(a.groups) * a.n_mt), Layout<HALVES, D>::THREADS,
+    return start_dependent(tree_tc_kernel<HALVES, D, TWO_PARTS>, dim3(static_cast<unsigned>(a.groups) * a.n_mt), Layout<HALVES, D>::THREADS,
                            static_cast<int>(Layout<HALVES, D>::bytes(a.T)), stream, map[0], map[1], map[2], map[3], a, lim, skip_loads);
 }
 
@@ -790,6 +814,7 @@ cudaError_t launch_tc(TreeArgs a, int d, unsigned long long wait_limit_ns, int s
     const bool one = tc_rows(a.R) == 128;
     if (d == 64)
         return one ? launch_halves<1, 64>(map, a, wait_limit_ns, skip_loads, stream) : launch_halves<2, 64>(map, a, wait_limit_ns, skip_loads, stream);
+    if (a.R <= TWO_PART_ROWS) return launch_halves<1, 128, true>(map, a, wait_limit_ns, skip_loads, stream);
     return one ? launch_halves<1, 128>(map, a, wait_limit_ns, skip_loads, stream) : launch_halves<2, 128>(map, a, wait_limit_ns, skip_loads, stream);
 }
 

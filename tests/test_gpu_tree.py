@@ -323,3 +323,53 @@ def test_runs_that_begin_and_end_anywhere(d, heads, T, seed):
     O, LSE = check(x, g, w, rows, crows, what=f"lens {lens}")
     again = call(x, g, w)
     assert torch.equal(O, again[0]) and torch.equal(LSE, again[1])
+
+
+WEIGHTS = [  # B, T, Hq, Hkv, d, lens, g, w, mode: up to 16 rows per KV head, few keys or a few that carry the weight
+    (1, 1, 1, 1, 128, [9], 4, 16, 0),
+    (2, 1, 32, 32, 128, [12, 2600], 16, 24, 0),
+    (2, 1, 16, 1, 128, [7, 250], 16, 24, 0),
+    (3, 4, 8, 2, 128, [6, 30, 700], 8, 20, 1),
+    (2, 5, 6, 2, 128, [1, 5000], 4, 40, 0),
+    (2, 1, 4, 1, 64, [10, 900], 8, 12, 0),
+    (2, 4, 8, 2, 64, [5, 400], 16, 16, 1),
+]
+
+
+@pytest.mark.parametrize("case", range(len(WEIGHTS)))
+def test_few_rows_keep_their_weights(case):
+    """Up to 16 rows per KV head the softmax weights meet V as two bf16 parts, so that the output's own
+    rounding is nearly all of its error.
+
+    Bound: that of the fp32 call on the same values, the weights' two parts (the first cut off, which
+    leaves less than 2^-7 of the weight; the second, cut off as well, leaves 2^-7 of that: 2^-14 of
+    sum p |v| / sum p, which max |v| bounds) and the output's rounding.  One part, rounded, is off by up to
+    2^-8 of each weight: with ten keys that is some 2^-9 / sqrt(10) of |v|, ten times the bound of an
+    output near 0."""
+    B, T, Hq, Hkv, d, lens, g, w, mode = WEIGHTS[case]
+    x = make(B, T, Hq, Hkv, d, lens, g, w, 16, 16, torch.bfloat16, mode, seed=50 + case)
+    O, LSE = call(x, g, w, window_mode=mode)
+    wide = {k: v.float() if v is not None and v.is_floating_point() else v for k, v in x.items()}
+    ref, lse, dO, dL = tree(wide["Q"], wide["Kp"], wide["Vp"], x["table"], wide["Kcp"], wide["Vcp"], x["core_table"], x["lens"],
+                            x["parents"], g, w, 16, 16, mode)
+    big = max(float(v[~v.isnan()].abs().max()) for v in (wide["Vp"], wide["Vcp"]) if bool((~v.isnan()).any()))
+    near = dO + 2.0 ** -14 * big
+    close(O, ref, near + 2.0 ** -8 * (np.abs(ref) + near), f"case {case} O")
+    close(LSE, lse, dL, f"case {case} LSE")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), NAN])
+@pytest.mark.parametrize("d,heads", [(128, 1), (128, 40), (64, 1), (64, 16), (64, 40)])
+def test_infinities_that_every_row_sees(d, heads, bad):
+    """An infinity in the V of a key that every node sees is what each of them puts out, a NaN likewise;
+    among runs of whole pages and among the keys around them."""
+    g, w, rows = 8, 200, 16
+    for at in (150, 299):                  # inside whole pages; next to the nodes
+        x = make(1, 3, heads, 1, d, [300], g, w, rows, rows, torch.bfloat16, seed=4)
+        clean = call(x, g, w)
+        x["Vp"][int(x["table"][0, at // rows]), 0, at % rows, 5] = bad
+        O, LSE = call(x, g, w)
+        want = clean[0].float()
+        want[..., 5] = bad
+        torch.testing.assert_close(O.float(), want, rtol=0, atol=0, equal_nan=True)
+        assert torch.equal(LSE, clean[1])
