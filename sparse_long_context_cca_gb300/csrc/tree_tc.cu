@@ -44,7 +44,9 @@
 // softmax; the softmax then waits for the earlier product itself before it touches O.
 //
 // Every wait is bounded: on a time-out the CTA stops, drains, frees its tensor memory and
-// reports CCA_ERR_TIMEOUT.
+// reports CCA_ERR_TIMEOUT.  The warps of a role may disagree on whether a wait ran out (one looks
+// before the barrier completes and sees another role's time-out, the next looks after), so nothing
+// but such waits joins them between the CTA's two __syncthreads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -101,8 +103,8 @@ struct Layout {
     static constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
     static constexpr uint32_t OFF_START = (OFF_ABORT + 4 + 15) / 16 * 16;
     static constexpr uint32_t OFF_NODES = (OFF_START + sizeof(Start) + 15) / 16 * 16;
-    // then, per half: bits of every row [128][words], parents [T]
-    static uint32_t bytes(int T) { return OFF_NODES + HALVES * (128 * 4 * ((T + 31) / 32) + 2 * ((T + 1) / 2 * 2)) + 1024; }
+    // then, per half: bits of every row [128][words]; per softmax warp: parents [T]
+    static uint32_t bytes(int T) { return OFF_NODES + HALVES * (128 * 4 * ((T + 31) / 32) + 4 * 2 * ((T + 1) / 2 * 2)) + 1024; }
 };
 
 // The lowest n bits.
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tO = tmem + lane_addr + TM_O + h * 128;
         uint32_t *const sees = reinterpret_cast<uint32_t *>(gbase + L::OFF_NODES) + (h * 128 + quarter * 32 + lane) * words;
-        int16_t *const up = reinterpret_cast<int16_t *>(gbase + L::OFF_NODES + HALVES * 512 * words) + h * ((a.T + 1) / 2 * 2);
+        int16_t *const up = reinterpret_cast<int16_t *>(gbase + L::OFF_NODES + HALVES * 512 * words) + (h * 4 + quarter) * ((a.T + 1) / 2 * 2);
         const int node = live ? row % a.T : 0;
         bool ok = true;
         uint32_t seg = 0, n_s = 0;  // lists and tiles of this half so far
@@ -465,13 +467,13 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(L::B_QFULL + h));
         };
-        // The list's tree: parents in shared memory, each row walks its own chain.
+        // The list's tree: parents in this warp's own shared memory, each row walks its own chain.
         auto read_nodes = [&]() {
             if (it.b == tree_of) return;
             tree_of = it.b;
-            ptx::named_bar_sync(1 + h, 128);  // the old parents have been used
-            for (int t = quarter * 32 + lane; t < a.T; t += 128) up[t] = static_cast<int16_t>(parent_of(a, it.b, t));
-            ptx::named_bar_sync(1 + h, 128);
+            __syncwarp();  // the old parents have been used
+            for (int t = lane; t < a.T; t += 32) up[t] = static_cast<int16_t>(parent_of(a, it.b, t));
+            __syncwarp();
             for (int i = 0; i < words; ++i) sees[i] = 0;
             const Chain c = walk_chain(up, sees, node);
             const int lo = window_lo(it.k.len + c.depth, a.w), vis = a.by_g.div(lo);
