@@ -169,6 +169,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
     const Run run = find_run(a, group, st);
     const int x0 = run.x0, x1 = run.x1;
     const bool half_used[2] = {true, HALVES == 2 && mt * BM + 128 < a.R};
+    int last_bulk = -1;  // of a producer warp: the last slot fill that went by TMA
 
     if (wg == HALVES) {
         // ------------------------------------------------------------ producers
@@ -252,7 +253,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             if (lane == 0) ptx::mbar_arrive(bar(L::B_FULL + held));
             held = -1;
         };
-        int last_bulk = -1;  // last slot fill that went by TMA
         if (ok) look_up(x0);
         for (int u = 0; ok && u < 2 * (x1 - x0); ++u) {
             const int x = x0 + (u >> 1), slot = u % NS;
@@ -314,12 +314,6 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         }
         cp_wait<0>();
         if (ok) land();
-        if (*abort_flag && lane == 0) {
-            // bulk copies already issued land before the CTA's memory is given back
-            volatile int never = 0;
-            for (int u = last_bulk >= NS ? last_bulk - NS + 1 : 0; u <= last_bulk; ++u)
-                ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, &never, lim);
-        }
         __syncwarp();
     } else if (wg == HALVES + 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -771,6 +765,14 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
 
     ptx::tc_fence_before();
     __syncthreads();
+    if (*abort_flag && wg == HALVES && lane == 0) {
+        // Bulk copies already issued land before the CTA's memory is given back.  A producer may have
+        // been through before another role gave up, so this is asked behind the barrier.  A fill that
+        // other warps left unfinished never completes: one such wait is long enough for all.
+        volatile int never = 0;
+        for (int u = last_bulk >= NS ? last_bulk - NS + 1 : 0; u <= last_bulk; ++u)
+            if (!ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, &never, lim)) break;
+    }
     if (*abort_flag && threadIdx.x == 0 && a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(CCA_ERR_TIMEOUT));
     if (warp == 0) {
         ptx::tc_fence_after();

@@ -27,10 +27,12 @@ class Cta:
     """Roles are generators, one per warp.  `yield cond` is a bounded wait: True once the condition holds;
     False when it does not and a wait has run out somewhere, or this one runs out.  `yield None` is a step.
     A wait looks at its condition first, then at the flag, as the kernel's does.
-    joint: the warps of a half meet at an unbounded barrier before a list's parents are read."""
+    joint: the warps of a half meet at an unbounded barrier before a list's parents are read.
+    drain: after a time-out the producers wait for their copies behind the CTA's last barrier ("last"), or
+    where they end, if they see it there ("own")."""
 
-    def __init__(self, halves, segs, runs, joint):
-        self.H, self.segs, self.runs, self.joint = halves, segs, runs, joint
+    def __init__(self, halves, segs, runs, joint, drain="last"):
+        self.H, self.segs, self.runs, self.joint, self.drain = halves, segs, runs, joint, drain
         self.NS = n = 4 if halves == 2 else 5
         self.total = sum(segs)
         self.full, self.empty = [Bar(4) for _ in range(n)], [Bar(1) for _ in range(n)]
@@ -58,7 +60,8 @@ class Cta:
                 self.full[held].arrive()
                 held = None
             if not (yield room):
-                return
+                held = None
+                break
             if bulk:
                 self.flying.append(self.full[slot])
                 continue
@@ -68,6 +71,8 @@ class Cta:
             yield None
         if held is not None:
             self.full[held].arrive()
+        while self.drain == "own" and self.abort and self.flying:
+            yield None
 
     def mma(self):
         H, NS, pcount = self.H, self.NS, 0
@@ -165,6 +170,8 @@ class Cta:
                 self.flying.pop(rng.randrange(len(self.flying))).arrive()
             live = [i for i, s in state.items() if s[1] != "end"]
             if not live:
+                # the CTA's last barrier; behind it the producers that gave up wait for what still flies
+                self.left = 0 if self.abort and self.drain == "last" else len(self.flying)
                 return True
             # unbounded barriers that nothing can complete any more: the CTA hangs
             if all(state[i][1] == "unbounded" for i in live) and not self.pipe and not self.flying:
@@ -207,6 +214,22 @@ def test_a_barrier_among_warps_that_may_disagree_hangs():
     """What the kernel must not have: some schedule leaves one warp at the barrier for good."""
     assert all(Cta(1, [1, 1, 1, 1], 0, joint=True).run(random.Random(s), 0.0) for s in range(20))
     assert not all(Cta(1, [1, 1, 1, 1], 0, joint=True).run(random.Random(s), 10.0 ** -(1 + s % 3)) for s in range(400))
+
+
+def test_no_copy_outlives_the_cta():
+    def left(drain, patience):
+        out = []
+        for seed in range(300):
+            cta = Cta(1 + seed % 2, SEGS[seed % len(SEGS)], 100, False, drain)
+            assert cta.run(random.Random(seed), patience)
+            out.append(cta.left)
+        return out
+
+    assert not any(left("last", 0.03)) and not any(left("last", 0.0)) and any(left("own", 0.03))
+    source = open(os.path.join(cbuild.CSRC, "tree_tc.cu")).read()
+    code = re.sub(r"//[^\n]*", "", source)
+    # the wait for the copies stands behind the last barrier
+    assert code.rindex("__syncthreads()") < code.index("last_bulk >= NS")
 
 
 def test_the_kernel_has_no_such_barrier():
