@@ -350,6 +350,10 @@ int cca_rope(const cca_rope_tensor_t *tensors, int n_tensors, const cca_rope_par
  * entry that names no page or a length outside the table is skipped (as described at
  * each call) and reported as CCA_ERR_INVALID_ARG in *dev_status when that pointer is
  * set; nothing out of range is read or written.
+ * One status word may serve all the calls of a step, from here on to cca_pages_compact:
+ * the first error in it stays, but CCA_ERR_INVALID_ARG gives way to CCA_ERR_NO_PAGES and
+ * CCA_ERR_TIMEOUT.  (After a reserve that found too few pages, the calls behind it find
+ * none for the new tokens; the word keeps saying why.)  The caller sets it back to 0.
  */
 typedef struct cca_pages {
     void *K, *V;              /* device, 16-byte aligned, contiguous */

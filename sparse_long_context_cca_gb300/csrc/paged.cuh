@@ -28,6 +28,16 @@ cudaError_t start_dependent(void (*kernel)(P...), dim3 grid, int threads, int sm
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// An error for the caller's status word.  One word may serve all calls of a step: the first error in
+// it stays, but a bad argument gives way to what matters more (too few pages, of which a bad argument
+// in a later call may be the consequence; a time-out, after which an output is not complete).
+__device__ __forceinline__ void report(int32_t *status, int code) {
+    if (status == nullptr) return;
+    int held = *static_cast<volatile int32_t *>(status);  // many threads may report the same
+    if (held == 0) held = atomicCAS(status, 0, code);
+    if (held == CCA_ERR_INVALID_ARG && code != held) atomicCAS(status, held, code);
+}
+
 constexpr int TREE_MAX_NODES = 256;
 constexpr int TREE_MAX_BATCH = 1024;
 

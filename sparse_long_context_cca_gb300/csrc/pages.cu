@@ -25,10 +25,6 @@ __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.launch_dependents;");
 }
 
-__device__ __forceinline__ void report(int32_t *status, int code) {
-    if (status != nullptr) *status = code;
-}
-
 // ---------------------------------------------------------------- reserve
 
 constexpr int RESERVE_THREADS = 1024;

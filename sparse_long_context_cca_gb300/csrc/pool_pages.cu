@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(PP_WARPS * 32) pool_pages_kernel(const PoolPag
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = a.lens[b], got = a.accepted[b];
     if (len < 0 || got < 0 || got > a.A || got > 0x7fffffff - len) {
-        if (lane == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        if (lane == 0) report(a.status, CCA_ERR_INVALID_ARG);
         return;
     }
     const int64_t j = len / a.g + (item - bk * a.slots);
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(PP_WARPS * 32) pool_pages_kernel(const PoolPag
         if (p < 0 || p >= a.n_pages) ok = false;
     }
     if (!__all_sync(kFull, ok)) {
-        if (lane == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        if (lane == 0) report(a.status, CCA_ERR_INVALID_ARG);
         return;
     }
     const T *Kp = static_cast<const T *>(a.K) + cl * E, *Vp = static_cast<const T *>(a.V) + cl * E;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(RING_MAX_WARPS * 32) pool_pages_ring_kernel(co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = a.lens[b], got = a.accepted[b];
     if (len < 0 || got < 0 || got > a.A || got > 0x7fffffff - len) {
-        if (lane == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        if (lane == 0) report(a.status, CCA_ERR_INVALID_ARG);
         return;
     }
     const int64_t begin = a.by_g.div(len) + (w - bk * parts) * static_cast<int64_t>(per_warp);
@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(RING_MAX_WARPS * 32) pool_pages_ring_kernel(co
                     ring_copy(vd + t * ROW, static_cast<const T *>(a.V) + row);
                 }
                 core = p.cpage;
-            } else if (lane == 0 && a.status != nullptr) {
-                *a.status = CCA_ERR_INVALID_ARG;
+            } else if (lane == 0) {
+                report(a.status, CCA_ERR_INVALID_ARG);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");

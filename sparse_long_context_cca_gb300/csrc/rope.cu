@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, SHARED ? 3 : 5) rope_kernel(cons
     int page_off = 0;
     if constexpr (PAGED) {
         if (len < 0) {
-            if (a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+            report(a.status, CCA_ERR_INVALID_ARG);
             real = false;
             len = 0;
         }
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, SHARED ? 3 : 5) rope_kernel(cons
             if (k != -1) real = false;
             pos = static_cast<int64_t>(len) + depth;
         }
-        if (real && inside && (page < 0 || page >= a.n_pages) && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        if (real && inside && (page < 0 || page >= a.n_pages)) report(a.status, CCA_ERR_INVALID_ARG);
         if (!real || page >= a.n_pages) page = -1;
     } else if (inside) {
         pos = a.positions != nullptr ? a.positions[b * a.pos_stride + n] : a.start + n;

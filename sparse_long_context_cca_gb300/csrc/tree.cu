@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
 
     // ---- the rows
     Item it = run.item;
-    if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+    if (it.k.n == 0 && tid == 0) report(a.status, CCA_ERR_INVALID_ARG);
     uint32_t qf[D / 16][4];
     float o[DT][4], m[2], l[2];
     int node[2];  // node of this thread's two rows, -1 past the last row
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
         if (tid == 0 && mt == 0) note_span(a, it, group, x0, x1);
         if (x + 1 < x1) {
             next_item(a, it);
-            if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+            if (it.k.n == 0 && tid == 0) report(a.status, CCA_ERR_INVALID_ARG);
             __syncthreads();  // the nodes of the old list have been used
             begin_item();
         }
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
     bool fresh = true;
     for (int x = x0; x < x1; ++x) {
         if (fresh) {
-            if (it.k.n == 0 && tid == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+            if (it.k.n == 0 && tid == 0) report(a.status, CCA_ERR_INVALID_ARG);
             read_tree(a, nodes, it.k, it.b);
             out0 = (static_cast<int64_t>(it.b) * a.Hq + static_cast<int64_t>(it.kv) * (a.Hq / a.Hkv)) * a.T;
             for (int e = tid; e < BM * D; e += TREE_THREADS) {

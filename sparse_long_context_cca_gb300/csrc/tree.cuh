@@ -91,7 +91,7 @@ __device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bo
     if (c < (core ? a.ccols : a.cols))
         page = (core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
     if (page < 0 || page >= (core ? a.n_cpages : a.n_pages)) {
-        if (a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+        report(a.status, CCA_ERR_INVALID_ARG);
         return -1;
     }
     return (static_cast<int64_t>(page) * a.Hkv + kv) * per + (at - c * per);

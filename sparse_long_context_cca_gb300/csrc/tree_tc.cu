@@ -499,7 +499,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
             float m = -INFINITY, l = 0.f;
             bool has_odd = false;
             float *const part = part_at(a, group, mt, x0 >= it.first ? 0 : 1, BM, D);
-            if (it.k.n == 0 && threadIdx.x == 0 && a.status != nullptr) *a.status = CCA_ERR_INVALID_ARG;
+            if (it.k.n == 0 && threadIdx.x == 0) report(a.status, CCA_ERR_INVALID_ARG);
             for (int t = x; t < end; ++t, ++n_s) {
                 const int buf = HALVES == 2 ? h : (t - x0) & 1;
                 if (!__all_sync(kFull, ptx::wait_bounded(bar(L::B_SFULL + buf), HALVES == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag, lim))) {
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
         for (int u = last_bulk >= NS ? last_bulk - NS + 1 : 0; u <= last_bulk; ++u)
             if (!ptx::wait_bounded(bar(L::B_FULL + u % NS), (u / NS) & 1, &never, lim)) break;
     }
-    if (*abort_flag && threadIdx.x == 0 && a.status != nullptr) atomicCAS(a.status, 0, static_cast<int32_t>(CCA_ERR_TIMEOUT));
+    if (*abort_flag && threadIdx.x == 0) report(a.status, CCA_ERR_TIMEOUT);
     if (warp == 0) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, TMEM_COLS);
