@@ -593,7 +593,9 @@ def cca_rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half
     the transposed view of a projection's output; the results are contiguous [B, H, N, d] (or
     `out`, a pair of such tensors, which may be Q and K themselves).  The first 2 * len(inv_freq)
     columns rotate.  Row n is at position start + n, or positions[n] / positions[b, n] (int32).
-    inverse: rotate back (the gradient).  Returns (Q', K')."""
+    inverse: rotate back (the gradient).  Returns (Q', K').  Autograd does not follow this call (rope()
+    is the one with gradients): an `out` that requires a gradient is refused outside torch.no_grad(), and
+    counts as modified in place, as whatever a call of this module is given to write."""
     if stream is not None:
         with _On(Q, stream):
             return cca_rope(Q, K, inv_freq, positions, start, layout, factor, inverse, out)

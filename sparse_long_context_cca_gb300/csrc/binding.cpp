@@ -93,6 +93,20 @@ int32_t *words(PyObject *o, const char *name, at::IntArrayRef shape, int dev) {
     return ptr<int32_t>(o, name, at::kInt, shape, dev);
 }
 
+// A tensor that the call is given to write.  Autograd learns of it as of any write in place: what it
+// has saved of the tensor is out of date.  Where the write would have to be differentiated it is refused.
+void to_write(PyObject *o, const char *name) {
+    if (none(o)) return;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        refuse("%s requires a gradient: it cannot be written in place outside torch.no_grad()", name);
+}
+void wrote(PyObject *o) {
+    if (none(o)) return;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 int64_t integer(PyObject *o, const char *name) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) {
@@ -307,9 +321,11 @@ PyObject *rope(PyObject *const *a) {
         const at::Tensor &x = THPVariable_Unpack(a[i]);
         outs[i] = none(a[8 + i]) ? at::empty(x.sizes(), q.options()) : same(a[8 + i], "out", q.scalar_type(), x.sizes(), at.dev);
         t[i] = rows(x, &outs[i], i == 0 ? "Q" : "K");
+        to_write(a[8 + i], "out");
     }
     const cca_rope_params_t p = turn.params(q, dtype);
     check(lib.rope(t, two ? 2 : 1, &p, at.stream), "cca_rope");
+    wrote(a[8]), wrote(a[9]);
     PyObject *first = THPVariable_Wrap(outs[0]);
     if (two) return Py_BuildValue("(NN)", first, THPVariable_Wrap(outs[1]));
     return Py_BuildValue("(NO)", first, Py_None);
@@ -477,7 +493,9 @@ PyObject *rope_append(PyObject *const *a) {
     } else if (!none(a[12])) {
         refuse("out without Q");
     }
+    to_write(a[3], "raw pool"), to_write(a[4], "raw pool"), to_write(a[12], "out");
     check(lib.rope_append(has_q ? &qt : nullptr, &kt, &vt, &raw, lens, parents, counts, status, &p, at.stream), "cca_rope_append");
+    wrote(a[3]), wrote(a[4]), wrote(a[12]);
     if (has_q) return THPVariable_Wrap(out);
     Py_RETURN_NONE;
 }
@@ -504,11 +522,13 @@ PyObject *tree_fwd(PyObject *const *a) {
     else ptr(a[11], "O", q.scalar_type(), q.sizes(), at.dev), O = THPVariable_Unpack(a[11]);
     if (none(a[12])) LSE = at::empty({B, H, T}, q.options().dtype(at::kFloat));
     else ptr(a[12], "LSE", at::kFloat, {B, H, T}, at.dev), LSE = THPVariable_Unpack(a[12]);
+    to_write(a[11], "O"), to_write(a[12], "LSE");
     const int nodes = size32(T, "nodes");
     const Workspace ws(a[13], lib.tree_workspace_size(&p, nodes), q);
     check(lib.tree_fwd(qp, &raw, &core, lens, parents, nodes, O.data_ptr(), static_cast<float *>(LSE.data_ptr()), &p, ws.p, ws.bytes,
                        at.stream),
           "cca_tree_fwd");
+    wrote(a[11]), wrote(a[12]);
     PyObject *first = THPVariable_Wrap(O);
     return Py_BuildValue("(NN)", first, THPVariable_Wrap(LSE));
 }
@@ -527,9 +547,11 @@ PyObject *pool_pages(PyObject *const *a) {
     const cca_pages_t raw = pool(a[1], a[2], a[3], B, Hkv, d, q.scalar_type(), at.dev, "raw pool", false);
     const cca_pages_t core = pool(a[4], a[5], a[6], B, Hkv, d, q.scalar_type(), at.dev, "core pool", false);
     const int64_t A = none(a[10]) ? T : columns(a[10], "path");
+    to_write(a[4], "core pool"), to_write(a[5], "core pool");
     check(lib.pool_pages(qp, &raw, &core, words(a[7], "lens", {B}, at.dev), words(a[8], "accepted", {B}, at.dev),
                          words(a[10], "path", {B, A}, at.dev), size32(A, "path"), size32(T, "tokens"), &p, at.stream),
           "cca_pool_pages");
+    wrote(a[4]), wrote(a[5]);
     Py_RETURN_NONE;
 }
 
@@ -560,6 +582,7 @@ PyObject *pages_reserve(PyObject *const *a) {
                             words(a[3], "extra", {k.B}, dev), static_cast<int32_t *>(pairs.data_ptr()), ws.p, ws.bytes,
                             words(a[7], "dev_status", {1}, dev), k.at.stream),
           "cca_pages_reserve");
+    wrote(a[0]), wrote(a[1]), wrote(a[5]);
     return THPVariable_Wrap(pairs);
 }
 
@@ -571,6 +594,7 @@ PyObject *pages_fork(PyObject *const *a) {
     check(lib.pages_fork(k.r, k.n, k.t, k.B, k.cols, int32(a[5], "rows"), words(a[2], "src", {n}, dev), words(a[3], "dst", {n}, dev),
                          size32(n, "src"), words(a[4], "lens", {k.B}, dev), words(a[6], "dev_status", {1}, dev), k.at.stream),
           "cca_pages_fork");
+    wrote(a[0]), wrote(a[1]);
     Py_RETURN_NONE;
 }
 
@@ -581,6 +605,7 @@ PyObject *pages_free(PyObject *const *a) {
     check(lib.pages_free(k.r, k.n, k.t, k.B, k.cols, words(a[2], "first", {k.B}, dev), words(a[3], "last", {k.B}, dev),
                          words(a[4], "dev_status", {1}, dev), k.at.stream),
           "cca_pages_free");
+    wrote(a[0]), wrote(a[1]);
     Py_RETURN_NONE;
 }
 
@@ -598,7 +623,9 @@ PyObject *pages_copy(PyObject *const *a) {
     const cca_pages_t pages = pool(a[0], a[1], nullptr, 1, k.size(-3), k.size(-1), k.scalar_type(), at.dev, "pool", true);
     if (columns(a[2], "pairs") != 2) refuse("pairs must be [n, 2]");
     const int64_t n = THPVariable_Unpack(a[2]).size(0);
+    to_write(a[0], "pool"), to_write(a[1], "pool");
     check(lib.pages_copy(&pages, words(a[2], "pairs", {n, 2}, at.dev), size32(n, "pairs"), &p, at.stream), "cca_pages_copy");
+    wrote(a[0]), wrote(a[1]);
     Py_RETURN_NONE;
 }
 
@@ -609,9 +636,11 @@ PyObject *pages_compact(PyObject *const *a) {
     const int64_t A = columns(a[4], "path"), B = THPVariable_Unpack(a[4]).size(0);
     const cca_params_t p = params(B, k.size(-3), k.size(-3), k.size(-1), dtype_of(k, "pool"), words(a[6], "dev_status", {1}, at.dev));
     const cca_pages_t pages = pool(a[0], a[1], a[2], B, k.size(-3), k.size(-1), k.scalar_type(), at.dev, "pool", true);
+    to_write(a[0], "pool"), to_write(a[1], "pool");
     check(lib.pages_compact(&pages, words(a[3], "lens", {B}, at.dev), words(a[4], "path", {B, A}, at.dev), size32(A, "path"),
                             words(a[5], "accepted", {B}, at.dev), &p, at.stream),
           "cca_pages_compact");
+    wrote(a[0]), wrote(a[1]);
     Py_RETURN_NONE;
 }
 

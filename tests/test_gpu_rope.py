@@ -359,3 +359,74 @@ def test_one_gradient_of_two():
         g, = torch.autograd.grad(api.rope(Q, K, f, start=9), [leaf], dy, create_graph=True)
         again, = torch.autograd.grad(g, [dy[i]], d)
         assert torch.equal(again, api.cca_rope(d, None, f, start=9)[0])
+
+
+def test_in_place_rotation_counts_as_a_write():
+    """What autograd saved of a tensor that is rotated in place is out of date, and its backward pass says so."""
+    f = freqs(64)
+    for append in (False, True):
+        x = rand(1, 2, 8, 64).requires_grad_()
+        q = (x * 2.0).detach()
+        y = (x * q).sum()                        # saves q
+        with torch.no_grad():
+            if append:
+                k = rand(1, 1, 8, 64, seed=1)
+                Kp, Vp = (torch.zeros(1, 1, 16, 64, device="cuda") for _ in range(2))
+                zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+                api.cca_rope_append(q, k, k, Kp, Vp, zero[:, None].contiguous(), zero, f, out=q)
+            else:
+                api.cca_rope(q, None, f, out=(q, None))
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+
+def written_by_calls():
+    """(name, tensors that the call writes, the call) for every call that writes what it is given."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = freqs(64)
+    q, k = rand(1, 2, 4, 64), rand(1, 1, 4, 64, seed=1)
+    Kp, Vp, Kc, Vc = (torch.zeros(4, 1, 16, 64, device="cuda") for _ in range(4))
+    table, ctable, lens, one, zero = i32(0, 1).view(1, 2), i32(0).view(1, 1), i32(8), i32(1), i32(0)
+    O, L, out, out_k = torch.empty_like(q), torch.empty(1, 2, 4, device="cuda"), torch.empty_like(q), torch.empty_like(k)
+    refs, book, pairs = i32(0, 0, 0, 0), i32(-1, -1, -1, -1).view(2, 2), i32(-1, -1, -1, -1).view(2, 2)
+    return [
+        ("rope", (out, out_k), lambda: api.cca_rope(q, k, f, out=(out, out_k))),
+        ("append", (out, Kp, Vp), lambda: api.cca_rope_append(q, k, k, Kp, Vp, table, lens, f, out=out)),
+        ("tree", (O, L), lambda: api.cca_tree_fwd(q, Kp, Vp, table, Kc, Vc, ctable, lens, 8, 16, O=O, LSE=L)),
+        ("pool", (Kc, Vc), lambda: api.cca_pool_pages(q, Kp, Vp, table, Kc, Vc, ctable, i32(4), i32(4), 8)),
+        ("compact", (Kp, Vp), lambda: api.cca_pages_compact(Kp, Vp, table, lens, i32(1).view(1, 1), one)),
+        ("copy", (Kp, Vp), lambda: api.cca_pages_copy(Kp, Vp, i32(0, 3).view(1, 2))),
+        ("reserve", (refs, book, pairs), lambda: api.cca_pages_reserve(refs, book, i32(0, 0), i32(4, 0), 16, pairs=pairs)),
+        ("fork", (refs, book), lambda: api.cca_pages_fork(refs, book, zero, one, i32(4, 0), 16)),
+        ("free", (refs, book), lambda: api.cca_pages_free(refs, book, i32(0, 0), i32(2, 2))),
+    ]
+
+
+def test_every_call_counts_what_it_writes():
+    for name, written, run in written_by_calls():
+        before = [t._version for t in written]
+        run()
+        assert all(t._version > n for t, n in zip(written, before)), name
+        with torch.inference_mode():
+            run()
+    torch.cuda.synchronize()
+
+
+def test_refuses_to_write_what_requires_a_gradient():
+    """As for any out= of torch: the write would be missing from the tensor's history."""
+    f = freqs(64)
+    for leaf in (True, False):
+        q = rand(1, 2, 8, 64).requires_grad_()
+        q = q if leaf else q * 1.0
+        with pytest.raises(ValueError, match="requires a gradient"):
+            api.cca_rope(q, None, f, out=(q, None))
+        with torch.no_grad():
+            api.cca_rope(q, None, f, out=(q, None))
+    api.cca_rope(rand(1, 2, 8, 64).requires_grad_(), None, f)        # only read
+    for name, written, run in written_by_calls():
+        for t in written:
+            if t.is_floating_point():
+                t.requires_grad_()
+                with pytest.raises(ValueError, match="requires a gradient"):
+                    run()
+                t.requires_grad_(False)
