@@ -391,13 +391,14 @@ int cca_rope_append(const cca_rope_tensor_t *q, const cca_rope_tensor_t *k, cons
  * followed by its chain: the cores j < lo(p)/g, the committed raw tokens from the window's
  * start on, its ancestors and itself.
  *   Q       [B, Hq, T, d];  O  [B, Hq, T, d];  LSE  [B, Hq, T] fp32
- *   raw     table entries of rows [window start of lens[b], lens[b] + T) must be there
+ *   raw     table entries of rows [window start of lens[b], lens[b] + T) must be there, but for
+ *           those of padding nodes, which may also lie past the table's end
  *   core    rows [0, lo(lens[b] + T - 1)/g) must be there
  *   parents device [B, T], or NULL for one chain (node t's parent is t - 1)
  *   params  B, Hq, Hkv, d, g, w, dtype, scale, dev_status, window_mode (N is not used)
  * A parent that is neither -1 nor an earlier node ends the chain: such a node and its
  * descendants are empty (O = 0, LSE = -inf), which is also how padding nodes are written
- * (-2).  Keys whose table entry names no page count as not there.
+ * (-2).  Keys whose table entry names no page count as not there, and are reported.
  * Keys that a row does not see never reach its output, whatever they hold.
  * workspace: caller-owned, at least cca_tree_workspace_size(params, T) bytes, rewritten by
  * every call; two calls that may run at the same time need one each.

@@ -640,7 +640,7 @@ def cca_tree_fwd(Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g: int, w: int, p
     Q [B, Hq, T, d]; raw pool Kp, Vp [pages, Hkv, rows, d] with table [B, columns]; core pool Kcp, Vcp
     with core_table; lens [B] committed tokens.  Node t's K and V lie in raw row lens[b] + t;
     parents [B, T] is the node before it, -1 for a child of the last committed token, anything else
-    (-2) for padding; without parents the nodes are one chain.  Returns (O [B, Hq, T, d], LSE
+    (-2) for padding, which needs no page; without parents the nodes are one chain.  Returns (O [B, Hq, T, d], LSE
     [B, Hq, T] fp32); padding nodes have O = 0 and LSE = -inf."""
     if stream is not None:
         with _On(Q, stream):

@@ -52,10 +52,9 @@ struct KeyList {
 __device__ __forceinline__ KeyList key_list_of(const TreeArgs &a, int len) {
     KeyList k = {};
     k.tiles = 1;
-    // a length outside the table: an empty list, and one tile in which its rows are written
-    if (len < 0 || len > 0x7fffffff - 2 * TREE_MAX_NODES ||
-        static_cast<int64_t>(len) + a.T > static_cast<int64_t>(a.rows) * a.cols)
-        return k;
+    // A length outside the table: an empty list, and one tile in which its rows are written.  Nodes
+    // past the table's end are keys that are not there (padding may lie there).
+    if (len < 0 || len > 0x7fffffff - 2 * TREE_MAX_NODES || len > static_cast<int64_t>(a.rows) * a.cols) return k;
     const int last = len + a.T - 1;  // T <= w, so no window of a node begins after len
     k.len = len;
     k.cores_all = a.by_g.div(window_lo(len, a.w));
@@ -83,15 +82,29 @@ __device__ __forceinline__ KeyList key_list_of(const TreeArgs &a, int len) {
 
 __device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) { return key_list_of(a, a.lens[b]); }
 
-// The row of its pool that row `at` of a sequence lies in, -1 where no page is.
-__device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bool core, int at) {
+// A node's parent: an earlier node, -1 for the root, -2 for none.
+__device__ __forceinline__ int parent_of(const TreeArgs &a, int b, int t) {
+    if (a.parents == nullptr) return t - 1;
+    const int p = a.parents[static_cast<int64_t>(b) * a.T + t];
+    return p >= -1 && p < t ? p : -2;
+}
+
+// Whether a node's chain reaches the root; the others are padding.
+__device__ __forceinline__ bool real_node(const TreeArgs &a, int b, int t) {
+    while (t >= 0) t = parent_of(a, b, t);
+    return t == -1;
+}
+
+// The row of its pool that row `at` of a sequence lies in, -1 where no page is.  That is reported but
+// for the row of a padding node (`node`, -1 for other rows), which needs no page.
+__device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bool core, int at, int node = -1) {
     const int per = core ? a.crows : a.rows;
     const int c = core ? a.by_crows.div(at) : a.by_rows.div(at);
     int page = -1;
     if (c < (core ? a.ccols : a.cols))
         page = (core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
     if (page < 0 || page >= (core ? a.n_cpages : a.n_pages)) {
-        report(a.status, CCA_ERR_INVALID_ARG);
+        if (a.status != nullptr && (node < 0 || real_node(a, b, node))) report(a.status, CCA_ERR_INVALID_ARG);
         return -1;
     }
     return (static_cast<int64_t>(page) * a.Hkv + kv) * per + (at - c * per);
@@ -136,7 +149,7 @@ __device__ __forceinline__ Key find_key(const TreeArgs &a, const KeyList &k, int
         }
     }
     r.val = r.kind == 3 ? at - k.len : at;
-    r.row = pool_row(a, b, kv, r.core, at);
+    r.row = pool_row(a, b, kv, r.core, at, r.kind == 3 ? r.val : -1);
     if (r.row < 0) r.kind = 4;
     return r;
 }
@@ -347,13 +360,6 @@ __device__ __forceinline__ Chain walk_chain(const int16_t *up, uint32_t *bits, i
     }
     bits[at] = word;
     return Chain{depth, n == -1};
-}
-
-// A node's parent: an earlier node, -1 for the root, -2 for none.
-__device__ __forceinline__ int parent_of(const TreeArgs &a, int b, int t) {
-    if (a.parents == nullptr) return t - 1;
-    const int p = a.parents[static_cast<int64_t>(b) * a.T + t];
-    return p >= -1 && p < t ? p : -2;
 }
 
 __device__ __forceinline__ void read_tree(const TreeArgs &a, const Nodes &n, const KeyList &k, int b) {

@@ -373,3 +373,50 @@ def test_infinities_that_every_row_sees(d, heads, bad):
         want[..., 5] = bad
         torch.testing.assert_close(O.float(), want, rtol=0, atol=0, equal_nan=True)
         assert torch.equal(LSE, clean[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads,d", [(1, 128), (24, 128), (40, 128), (1, 64), (8, 64)])     # rows for each of the kernels
+def test_padding_nodes_need_no_page(heads, d, dtype):
+    """Trees of different sizes, padded to one T: pages for the real nodes alone, up to the table's last
+    row.  Nothing is reported, and the real nodes are as they are with pages for all."""
+    T, g, w, rows = 6, 8, 40, 16
+    lens = [13, 60, 94, 96, 95]                      # real nodes: 3, 4, 2, none, 1; the table has 96 rows
+    real = [3, 4, 2, 0, 1]
+    x = make(5, T, heads, 1, d, lens, g, w, rows, rows, dtype, seed=6, cols=7)
+    x["parents"] = torch.tensor([[-1, 0, 0, -2, -2, 3], [-1, 0, 1, 2, -2, -2], [-1, 0, -2, -2, -2, -2], [-2] * 6,
+                                 [-1, -2, -2, -2, -2, -2]], dtype=torch.int32)
+    want = check(x, g, w, rows, rows, what="pages for all")
+    y = dict(x, table=x["table"][:, :6].clone())
+    for b in range(5):
+        y["table"][b, -(-(lens[b] + real[b]) // rows):] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    O, LSE = call(y, g, w, dev_status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    # lists may be cut at other keys, so the last bits may differ
+    ref = tree(x["Q"], x["Kp"], x["Vp"], x["table"], x["Kcp"], x["Vcp"], x["core_table"], x["lens"], x["parents"], g, w, rows, rows)
+    close(O, ref[0], ref[2], "O")
+    close(LSE, ref[1], ref[3], "LSE")
+    assert torch.isinf(LSE).any() and torch.equal(torch.isinf(LSE), torch.isinf(want[1]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("chain", [True, False])
+def test_real_nodes_past_the_pages_are_reported(dtype, chain):
+    """A real node without a page, or past the table's end, is reported and counts as not there for the
+    nodes below it; the others are as they were."""
+    T, g, w, rows = 5, 8, 32, 16
+    x = make(2, T, 4, 2, 64, [60, 30], g, w, rows, rows, dtype, seed=7, cols=5)
+    x["parents"] = None if chain else torch.tensor([[-1, 0, 1, 2, 3], [-1, -1, -1, -1, -2]], dtype=torch.int32)
+    clean = call(x, g, w)
+    for cols in (5, 4):                              # no page for rows 64 .., or no such rows in the table
+        y = dict(x, table=x["table"][:, :cols].contiguous())
+        if cols == 5:
+            y["table"][0, 4] = -1
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        O, LSE = call(y, g, w, dev_status=status)
+        assert status.item() == api.CCA_ERR_INVALID_ARG
+        assert torch.equal(O[1], clean[0][1]) and torch.equal(LSE[1], clean[1][1])
+        assert torch.equal(O[0, :, :4], clean[0][0, :, :4]) and torch.equal(LSE[0, :, :4], clean[1][0, :, :4])
+        assert not torch.equal(LSE[0, :, 4], clean[1][0, :, 4]) and torch.isfinite(LSE).equal(torch.isfinite(clean[1]))
