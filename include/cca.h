@@ -435,6 +435,10 @@ int cca_pool_pages(const void *Q, const cca_pages_t *raw, const cca_pages_t *cor
  * The pages' book: refs[page] is the number of table entries that hold the page; a page
  * with refs 0 is free.  All four calls order their work as if one table row came after
  * the other, and results do not depend on timing.
+ * A page that several rows hold stands in the same column of each of them (rows of a page
+ * are positions), and at most once in a row: the calls below keep it so.  From a table that
+ * breaks this, cca_pages_reserve may take a page away from all its holders; it is free
+ * after the call.
  *
  * cca_pages_reserve - room for the rows [lens[b], lens[b] + extra[b]) of every sequence
  * (extra <= 0: none): table entries of that range that name no page get one, and entries

@@ -34,7 +34,7 @@ struct ReserveArgs {
     int32_t *refs, *table, *pairs;
     int n_pages, B, cols, rows;
     const int32_t *lens, *extra;
-    int32_t *want;   // workspace [B * cols]: the places that get a page, in row order
+    int32_t *want;   // workspace [B * cols]: the places that get a page, in row order; then what they held
     int32_t *count;  // workspace [B]: how many each row gets, then where its first one stands
     int32_t *status;
 };
@@ -177,11 +177,14 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
         return;
     }
     // 4. the k-th place gets the k-th free page.  A place is found by its number: the row by
-    // bisection of the rows' first places.
+    // bisection of the rows' first places.  Where refs are looked at again meanwhile, a page that loses
+    // a holder is counted down behind that: should it lose its last one (its holders stand in several
+    // columns, against the rule), it is free after the call and not given out by it.
+    const bool later = stop > STEP;
     int k0 = 0;
     for (int64_t p0 = 0; k0 < total; p0 += STEP) {
         int sum = found;
-        if (stop > STEP) k = look(p0, sum) + k0;
+        if (later) k = look(p0, sum) + k0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (!free_page[i]) continue;
@@ -193,14 +196,16 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
                     else hi = mid - 1;
                 }
                 const int b = lo;
-                const int c = a.want[static_cast<int64_t>(b) * a.cols + (k - count[b])];
+                int32_t *place = a.want + static_cast<int64_t>(b) * a.cols + (k - count[b]);
+                const int c = *place;
                 int32_t *entry = a.table + static_cast<int64_t>(b) * a.cols + c;
                 const int32_t old = *entry;
                 const int page = static_cast<int>(p0 + 4 * tid + i);
                 *entry = page;
                 a.refs[page] = 1;
+                if (later) *place = old;
                 if (old >= 0 && old < a.n_pages) {
-                    atomicSub(&a.refs[old], 1);  // stays above 0: its last holder keeps it
+                    if (!later) atomicSub(&a.refs[old], 1);
                     const int len = lens[b];
                     if (c == len / a.rows && len % a.rows != 0) {
                         a.pairs[2 * b] = old;
@@ -211,6 +216,15 @@ __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_kernel(const Re
             ++k;
         }
         k0 += sum;
+    }
+    if (!later) return;
+    __syncthreads();
+    for (int b = warp; b < a.B; b += RESERVE_WARPS) {
+        const int n = (b + 1 < a.B ? count[b + 1] : total) - count[b];
+        for (int i = lane; i < n; i += 32) {
+            const int old = a.want[static_cast<int64_t>(b) * a.cols + i];
+            if (old >= 0 && old < a.n_pages) atomicSub(&a.refs[old], 1);
+        }
     }
 }
 

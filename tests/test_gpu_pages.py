@@ -373,3 +373,52 @@ def test_offsets_pass_32_bits(dtype):
     assert torch.equal(Kp[last, :, 1000:1002], x[0, :, 1:]) and torch.equal(Vp[last, :, 1002], x[0, :, 2])
     api.cca_pages_copy(Kp, Vp, i32([[last, last - 1]]))
     assert torch.equal(Kp[last - 1], Kp[last]) and torch.equal(Vp[last - 1], Vp[last]) and not Kp[:last - 1].any()
+
+
+def test_a_page_shared_across_columns_is_not_handed_out():
+    """A page stands in the same column of every row that holds it.  In a table that breaks the rule a
+    page may lose all its holders within one reserve; it is free after the call, and not given out by it:
+    the copies behind it read it."""
+    n = 12288
+    refs = torch.ones(n, dtype=torch.int32, device="cuda")
+    free = [7, 8, 9000]                          # the free pages lie in different steps of the scan
+    refs[free] = 0
+    shared = 4100
+    refs[shared] = 2
+    table = i32([[shared, -1], [-1, shared], [-1, -1]])
+    status = i32([0])
+    pairs = api.cca_pages_reserve(refs, table, i32([3, 19, 0]), i32([1, 1, 1]), 16, dev_status=status)
+    t = table.cpu()
+    held = [int(t[0, 0]), int(t[1, 1]), int(t[2, 0])]
+    assert held == free
+    assert pairs.cpu().tolist() == [[shared, 7], [shared, 8], [-1, -1]]
+    assert refs[shared].item() == 0 and refs.sum().item() == n - 1 and status.item() == 0
+    K, V = torch.zeros(n, 1, 16, 64, device="cuda"), torch.zeros(n, 1, 16, 64, device="cuda")
+    K[shared] = 3.0
+    api.cca_pages_copy(K, V, pairs, dev_status=status)
+    assert status.item() == 0 and (K[7] == 3.0).all() and (K[8] == 3.0).all()
+
+
+def test_the_book_keeps_shared_pages_in_their_column():
+    """Forks and copies on write leave every page in one column, whatever is dropped between them."""
+    rng = np.random.default_rng(5)
+    refs, table = i32([0] * 64), i32(np.full((6, 5), -1))
+    lens, status, rows = np.zeros(6, dtype=np.int64), i32([0]), 4
+    for step in range(60):
+        b, o = rng.permutation(6)[:2]
+        if rng.random() < 0.4:
+            first, last = np.zeros(6), np.zeros(6)
+            last[o] = 5
+            api.cca_pages_free(refs, table, i32(first), i32(last), dev_status=status)
+            api.cca_pages_fork(refs, table, i32([b]), i32([o]), i32(lens), rows, dev_status=status)
+            lens[o] = lens[b]
+        extra = np.minimum(rng.integers(0, 4, 6), 5 * rows - lens)
+        api.cca_pages_reserve(refs, table, i32(lens), i32(extra), rows, dev_status=status)
+        lens = np.where(lens + extra >= 5 * rows, lens, lens + extra)
+        t = table.cpu().numpy()
+        where = {}
+        for c in range(5):
+            for page in t[:, c][t[:, c] >= 0]:
+                assert where.setdefault(int(page), c) == c, step
+        count = np.bincount(t[t >= 0], minlength=64)
+        assert status.item() == 0 and (refs.cpu().numpy() == count).all(), step
