@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_bf16_kernel(const TreeArgs 
     auto look_up = [&](int x, Key &key) {  // threads 0 .. 63, one key each
         if (x >= x1) return;
         if (x >= ld.first + ld.k.tiles) next_item(a, ld);
-        if (tid < TILE) key = find_key(a, ld.k, ld.b, ld.kv, (x - ld.first) * TILE + tid);
+        if (tid < TILE) key = settled(a, ld.b, find_key(a, ld.k, ld.b, ld.kv, (x - ld.first) * TILE + tid));
     };
     auto put = [&](int x, const Key &key) {
         if (x >= x1 || tid >= TILE) return;
@@ -541,14 +541,26 @@ __global__ void __launch_bounds__(TREE_THREADS) tree_f32_kernel(const TreeArgs a
             }
             const float4 *k = reinterpret_cast<const float4 *>(static_cast<const float *>(key.core ? a.Kc : a.K) + key.row * D);
             const float4 *v = reinterpret_cast<const float4 *>(static_cast<const float *>(key.core ? a.Vc : a.V) + key.row * D);
-#pragma unroll 8
-            for (int c = half * (D / 8); c < (half + 1) * (D / 8); ++c) {
-                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-                *reinterpret_cast<float4 *>(sk + row * LD + c * 4) = key.row < 0 ? zero : k[c];
-                *reinterpret_cast<float4 *>(sv + row * LD + c * 4) = key.row < 0 ? zero : v[c];
+            constexpr int STEP = 8;  // 16-byte loads of K, and of V, in flight together
+            for (int c0 = half * (D / 8); c0 < (half + 1) * (D / 8); c0 += STEP) {
+                float4 kx[STEP], vx[STEP];
+#pragma unroll
+                for (int i = 0; i < STEP; ++i) {
+                    kx[i] = vx[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (key.row >= 0) {
+                        kx[i] = k[c0 + i];
+                        vx[i] = v[c0 + i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < STEP; ++i) {
+                    *reinterpret_cast<float4 *>(sk + row * LD + (c0 + i) * 4) = kx[i];
+                    *reinterpret_cast<float4 *>(sv + row * LD + (c0 + i) * 4) = vx[i];
+                }
             }
         }
         __syncthreads();
+        if (tid < TILE && sm_kind[tid] == 5 && nodes.cores[sm_val[tid]] >= 0) report(a.status, CCA_ERR_INVALID_ARG);
         {
             // thread: one key, eight rows
             const int key = tid & (TILE - 1), r0 = (tid / TILE) * (BM / 2);
@@ -885,6 +897,7 @@ int cca_tree_fwd(const void *Q, const cca_pages_t *raw, const cca_pages_t *core,
     a.Hq = params->Hq;
     a.Hkv = params->Hkv;
     a.T = T;
+    a.most = static_cast<int>(fmin(rows, 0x7fffffff - 2 * TREE_MAX_NODES));
     a.g = params->g;
     a.w = params->w;
     a.window_mode = params->window_mode;

@@ -19,6 +19,7 @@ struct TreeArgs {
     const int32_t *table, *ctable, *lens, *parents;
     int n_pages, rows, cols, n_cpages, crows, ccols;
     int B, Hq, Hkv, T, g, w, window_mode;
+    int most;  // the longest length that lies in the table
     int R;       // query rows of a KV head: Hq / Hkv * T
     int n_mt;    // row tiles
     int tile_log2;  // keys per tile
@@ -54,7 +55,7 @@ __device__ __forceinline__ KeyList key_list_of(const TreeArgs &a, int len) {
     k.tiles = 1;
     // A length outside the table: an empty list, and one tile in which its rows are written.  Nodes
     // past the table's end are keys that are not there (padding may lie there).
-    if (len < 0 || len > 0x7fffffff - 2 * TREE_MAX_NODES || len > static_cast<int64_t>(a.rows) * a.cols) return k;
+    if (len < 0 || len > a.most) return k;
     const int last = len + a.T - 1;  // T <= w, so no window of a node begins after len
     k.len = len;
     k.cores_all = a.by_g.div(window_lo(len, a.w));
@@ -83,34 +84,31 @@ __device__ __forceinline__ KeyList key_list_of(const TreeArgs &a, int len) {
 __device__ __forceinline__ KeyList key_list(const TreeArgs &a, int b) { return key_list_of(a, a.lens[b]); }
 
 // A node's parent: an earlier node, -1 for the root, -2 for none.
-__device__ __forceinline__ int parent_of(const TreeArgs &a, int b, int t) {
-    if (a.parents == nullptr) return t - 1;
-    const int p = a.parents[static_cast<int64_t>(b) * a.T + t];
+__device__ __forceinline__ int parent_in(const int32_t *parents, int t) {
+    const int p = parents[t];
     return p >= -1 && p < t ? p : -2;
 }
-
-// Whether a node's chain reaches the root; the others are padding.
-__device__ __forceinline__ bool real_node(const TreeArgs &a, int b, int t) {
-    while (t >= 0) t = parent_of(a, b, t);
-    return t == -1;
+__device__ __forceinline__ int parent_of(const TreeArgs &a, int b, int t) {
+    return a.parents == nullptr ? t - 1 : parent_in(a.parents + static_cast<int64_t>(b) * a.T, t);
 }
 
 // The row of its pool that row `at` of a sequence lies in, -1 where no page is.  That is reported but
-// for the row of a padding node (`node`, -1 for other rows), which needs no page.
-__device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bool core, int at, int node = -1) {
+// for the row of a node, which may be padding.
+__device__ __forceinline__ int64_t pool_row(const TreeArgs &a, int b, int kv, bool core, int at, bool node = false) {
     const int per = core ? a.crows : a.rows;
     const int c = core ? a.by_crows.div(at) : a.by_rows.div(at);
     int page = -1;
     if (c < (core ? a.ccols : a.cols))
         page = (core ? a.ctable + static_cast<int64_t>(b) * a.ccols : a.table + static_cast<int64_t>(b) * a.cols)[c];
     if (page < 0 || page >= (core ? a.n_cpages : a.n_pages)) {
-        if (a.status != nullptr && (node < 0 || real_node(a, b, node))) report(a.status, CCA_ERR_INVALID_ARG);
+        if (!node) report(a.status, CCA_ERR_INVALID_ARG);
         return -1;
     }
     return (static_cast<int64_t>(page) * a.Hkv + kv) * per + (at - c * per);
 }
 
-// What a key is: 0 seen by every node, 1 core `val`, 2 raw token `val`, 3 node `val`, 4 not there.
+// What a key is: 0 seen by every node, 1 core `val`, 2 raw token `val`, 3 node `val`, 4 not there,
+// 5 node `val`, which has no page.
 struct Key {
     int kind, val;
     int64_t row;  // row of its pool
@@ -149,9 +147,25 @@ __device__ __forceinline__ Key find_key(const TreeArgs &a, const KeyList &k, int
         }
     }
     r.val = r.kind == 3 ? at - k.len : at;
-    r.row = pool_row(a, b, kv, r.core, at, r.kind == 3 ? r.val : -1);
-    if (r.row < 0) r.kind = 4;
+    r.row = pool_row(a, b, kv, r.core, at, r.kind == 3);
+    if (r.row < 0) r.kind = r.kind == 3 ? 5 : 4;
     return r;
+}
+
+// For kernels that look keys up before they know the tree: a node without a page is reported if its
+// chain reaches the root (others are padding) and becomes a key that is not there.  Not inlined, as it
+// is rare.
+static __device__ __noinline__ void report_node(int32_t *status, const int32_t *parents, int t) {
+    if (parents == nullptr) t = -1;
+    while (t >= 0) t = parent_in(parents, t);
+    if (t == -1) report(status, CCA_ERR_INVALID_ARG);
+}
+__device__ __forceinline__ Key settled(const TreeArgs &a, int b, Key key) {
+    if (key.kind == 5) {
+        if (a.status != nullptr) report_node(a.status, a.parents == nullptr ? nullptr : a.parents + static_cast<int64_t>(b) * a.T, key.val);
+        key.kind = 4;
+    }
+    return key;
 }
 
 // Pool row at which box i of the runs begins, -1 where no page is.

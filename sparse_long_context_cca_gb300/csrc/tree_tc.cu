@@ -198,7 +198,7 @@ __global__ void __launch_bounds__((HALVES + 2) * 128, 1)
                 if (gone != 0) gone = __ballot_sync(kFull, (gone >> (lane >> a.box_log2)) & 1u);
                 return;
             }
-            const Key key = find_key(a, it.k, it.b, it.kv, (tile - it.k.run_tiles) * BN + pw * 32 + lane);
+            const Key key = settled(a, it.b, find_key(a, it.k, it.b, it.kv, (tile - it.k.run_tiles) * BN + pw * 32 + lane));
             kp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Kc : a.K) + key.row * (D * 2);
             vp = key.row < 0 ? nullptr : static_cast<const char *>(key.core ? a.Vc : a.V) + key.row * (D * 2);
             gone = __ballot_sync(kFull, key.kind == 4);
