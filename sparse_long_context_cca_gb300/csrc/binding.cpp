@@ -47,14 +47,29 @@ template <typename... Args>
     throw Refused();
 }
 
-void check(int status, const char *what) {
-    if (status == CCA_OK) return;
+void set_error(int status, const char *what) {
     PyObject *e = PyObject_CallFunction(error_class, "is", status, what);
     if (e != nullptr) {
         PyErr_SetObject(error_class, e);
         Py_DECREF(e);
     }
+}
+
+void check(int status, const char *what) {
+    if (status == CCA_OK) return;
+    set_error(status, what);
     throw Refused();
+}
+
+// The same where autograd's threads may be the callers: the error travels with the exception.
+void check_anywhere(int status, const char *what) {
+    if (status == CCA_OK) return;
+    python_error e;
+    const PyGILState_STATE gil = PyGILState_Ensure();
+    set_error(status, what);
+    e.persist();
+    PyGILState_Release(gil);
+    throw e;
 }
 
 bool none(PyObject *o) { return o == nullptr || o == Py_None; }
@@ -387,7 +402,7 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
         }
         const cca_rope_params_t p = turn.params(in[0], in[0].scalar_type() == at::kBFloat16 ? CCA_BF16 : CCA_F32);
         const int status = lib.rope(t, static_cast<int>(in.size()), &p, c10::cuda::getCurrentCUDAStream(in[0].get_device()).stream());
-        TORCH_CHECK(status == CCA_OK, "cca_rope: status ", status);
+        check_anywhere(status, "cca_rope");
         return out;
     }
 

@@ -430,3 +430,18 @@ def test_refuses_to_write_what_requires_a_gradient():
                 with pytest.raises(ValueError, match="requires a gradient"):
                     run()
                 t.requires_grad_(False)
+
+
+def test_a_refused_rotation_raises_the_librarys_error():
+    """rope() raises what cca_rope() raises, with the status and its text."""
+    x = rand(1, 2, 8, 96)
+    f = freqs(64)
+    seen = []
+    for call in (lambda: api.cca_rope(x, None, f), lambda: api.rope(x, None, f), lambda: api.rope(x, x[:, :1].contiguous(), f),
+                 lambda: api.rope(x.requires_grad_(), None, f)):
+        with pytest.raises(api.CcaError) as e:
+            call()
+        seen.append((e.value.status, str(e.value)))
+    assert len(set(seen)) == 1 and seen[0][0] == api.CCA_ERR_UNSUPPORTED
+    with pytest.raises(api.CcaError):
+        api.rope(rand(1, 2, 8, 64), None, f, factor=float("nan"))
