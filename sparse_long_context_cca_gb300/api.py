@@ -89,7 +89,7 @@ def library_path() -> str:
 
 def load_library():
     """Load libcca.so; raises if it has not been built."""
-    global _lib, _fast
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -151,19 +151,25 @@ def load_library():
         lib.cca_test_skip_q_load.restype = None
         lib.cca_test_decode_path.argtypes = [ctypes.c_int]
         lib.cca_test_decode_path.restype = None
-        if not os.path.exists(_build.BINDING):
-            raise RuntimeError(f"_binding.so not found at {_build.BINDING}: build it first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')")
-        from . import _binding
-        _binding.bind(CcaError, {n: ctypes.cast(getattr(lib, n), vp).value for n in EXPORTED if not n.startswith("cca_test")})
-        _lib, _fast = lib, _binding
+        _lib = lib
         return lib
 
 
 def _bound():
-    """The binding of the rotary and paged calls; loads the library first."""
-    load_library()
-    return _fast
+    """The binding of the rotary and paged calls (the others do without it); raises if it has not been
+    built, or for another torch."""
+    global _fast
+    lib = load_library()
+    with _lock:
+        if _fast is None:
+            if not _build.binding_is_for_this_torch():
+                raise RuntimeError(f"{_build.BINDING} is not there or was built for another torch or Python: build it first "
+                                   "(python -c 'import __graft_entry__ as g; g.build()')")
+            from . import _binding
+            _binding.bind(CcaError, {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                                     for n in EXPORTED if not n.startswith("cca_test")})
+            _fast = _binding
+        return _fast
 
 
 def status_string(status: int) -> str:
@@ -507,7 +513,8 @@ class CcaAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dO):
-        (_fast or _bound()).check_leaves()
+        if torch.cuda.is_current_stream_capturing() and _build.binding_is_for_this_torch():
+            (_fast or _bound()).check_leaves()
         Q, K, V, Kc, Vc, O, LSE = ctx.saved_tensors
         g, w, scale, pool_mode, window_mode = ctx.cfg
         dQ, dK, dV = cca_prefill_bwd(Q, K, V, Kc, Vc, O, LSE, dO.contiguous().to(Q.dtype), g, w, scale,

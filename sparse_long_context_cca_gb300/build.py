@@ -6,6 +6,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -14,6 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcca.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding_for")  # what it was built for
 SOURCES = ["cca_api.cu", "pool.cu", "attn_f32.cu", "attn_tc.cu", "decode.cu", "bwd.cu", "bwd_tc.cu", "host_pipeline.cu",
            "rope.cu", "pages.cu", "pool_pages.cu", "tree.cu", "tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,6 +47,20 @@ def _binding_command(out: str) -> list[str]:
             "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
 
 
+def _this_torch() -> str:
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version.split()[0]}"
+
+
+def binding_is_for_this_torch() -> bool:
+    """Whether the binding is there and was built against the torch and Python that run now."""
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read() == _this_torch() and os.path.exists(BINDING)
+    except OSError:
+        return False
+
+
 def _deps_mtime() -> float:
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", f)
                                                                   for f in os.listdir(os.path.join(ROOT, "include"))]
@@ -52,7 +68,13 @@ def _deps_mtime() -> float:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime() for p in (LIB, BINDING)):
+    """Builds what is not up to date.  Where the binding's compiler or torch's headers are missing, the
+    library is built all the same (all calls but the rotary and paged ones), and then this raises."""
+    def current(path):
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime()
+
+    lib_current, binding_current = current(LIB), current(BINDING) and binding_is_for_this_torch()
+    if lib_current and binding_current:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -74,19 +96,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if r.returncode != 0:
             raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, BINDING)
+        with open(BINDING_FOR, "w") as f:
+            f.write(_this_torch())
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
-    tmp = LIB + ".tmp%d" % os.getpid()
-    r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        binding = None if binding_current else ex.submit(compile_binding)
+        if not lib_current:
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = LIB + ".tmp%d" % os.getpid()
+            r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB)
+        if binding is not None:
+            binding.result()
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force=True, verbose=True, extra_flags=sys.argv[1:]))
