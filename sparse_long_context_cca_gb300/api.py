@@ -536,19 +536,21 @@ def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 
 # ---------------------------------------------------------------- rotary positions
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
-                     original: int = 8192, low: float = 1.0, high: float = 4.0, device="cuda"):
+                     original: int = 8192, low: float = 1.0, high: float | None = None, device="cuda"):
     """Frequencies of a rotary embedding, and the factor that goes with them: (inv_freq float64
     [rot/2] on `device`, attention factor).  inv_freq[i] = base**(-2i/rot), stretched for contexts
     `factor` times the `original` length by one of
       "linear"  every frequency / factor (positions interpolated)
       "ntk"     base * factor**(rot/(rot-2)): the slowest pair / factor, the fastest unchanged
-      "bands"   by the turns a pair makes over `original` positions: above `high` unchanged, below
-                `low` / factor, between them the mean weighted linearly in the turns
-      "yarn"    the same with the weight linear in the pair's index (low, high: 1, 32 by custom),
-                and the attention factor 0.1 ln(factor) + 1."""
+      "bands"   by the turns a pair makes over `original` positions: above `high` (4 unless given)
+                unchanged, below `low` / factor, between them the mean weighted linearly in the turns
+      "yarn"    the same with the weight linear in the pair's index (`high` 32 unless given), and the
+                attention factor 0.1 ln(factor) + 1."""
     import math
     if rot < 2 or rot % 2 or factor < 1.0 or scaling not in (None, "linear", "ntk", "bands", "yarn"):
         raise ValueError(f"rot {rot}, scaling {scaling!r}, factor {factor}")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
     if scaling == "ntk":
         if rot == 2:
             raise ValueError("ntk scaling needs more than one pair")

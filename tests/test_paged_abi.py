@@ -236,3 +236,20 @@ def test_binding_refuses_arguments_before_tensors_are_used(lib):
         _binding.bind(api.CcaError, {"cca_rope": 0})
     with pytest.raises(TypeError):
         _binding.bind(api.CcaError)
+
+
+def test_yarn_without_its_limits_takes_the_usual_ones():
+    """Unchanged above 32 turns over the original length, stretched below one; "bands" above 4."""
+    import math
+    plain, _ = api.rope_frequencies(128, 10000.0, device="cpu")
+    turns = plain * (8192 / (2 * math.pi))
+    for scaling, high in (("yarn", 32.0), ("bands", 4.0)):
+        f, _ = api.rope_frequencies(128, 10000.0, scaling, 8.0, 8192, device="cpu")
+        given, _ = api.rope_frequencies(128, 10000.0, scaling, 8.0, 8192, 1.0, high, device="cpu")
+        assert torch.equal(f, given)
+        assert torch.equal(f[turns > high], plain[turns > high])
+        assert torch.allclose(f[turns < 1.0][1:], plain[turns < 1.0][1:] / 8, rtol=1e-14, atol=0)
+        between = (turns < high / 1.2) & (turns > 1.2)
+        assert (f[between] < plain[between]).all() and (f[between] > plain[between] / 8).all()
+    with pytest.raises(ValueError):
+        api.rope_frequencies(128, 10000.0, "yarn", 8.0, 8192, 40.0, device="cpu")
