@@ -420,3 +420,32 @@ def test_real_nodes_past_the_pages_are_reported(dtype, chain):
         assert torch.equal(O[1], clean[0][1]) and torch.equal(LSE[1], clean[1][1])
         assert torch.equal(O[0, :, :4], clean[0][0, :, :4]) and torch.equal(LSE[0, :, :4], clean[1][0, :, :4])
         assert not torch.equal(LSE[0, :, 4], clean[1][0, :, 4]) and torch.isfinite(LSE).equal(torch.isfinite(clean[1]))
+
+
+MORE_ROWS = [  # as CASES: bf16 with d = 64 and more rows than a CTA has, one KV head each and several
+    (1, 100, 3, 1, 64, [700], 8, 128, 16, 24, 0),                 # 300 rows: two row tiles, the second with a half alone
+    (2, 72, 16, 2, 64, [90, 3000], 16, 80, 64, 64, 1),            # 576 rows: three row tiles, runs of whole pages
+    (3, 256, 2, 1, 64, [1500, 0, 300], 4, 256, 128, 32, 0),       # 512 rows of the largest trees
+]
+
+
+@pytest.mark.parametrize("case", range(len(MORE_ROWS)))
+def test_more_rows_than_a_cta_has_at_d_64(case):
+    B, T, Hq, Hkv, d, lens, g, w, rows, crows, mode = MORE_ROWS[case]
+    x = make(B, T, Hq, Hkv, d, lens, g, w, rows, crows, torch.bfloat16, mode, seed=80 + case)
+    check(x, g, w, rows, crows, mode, f"case {case}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,Hq,T", [(128, 8, 16), (128, 2, 1), (64, 2, 2), (64, 8, 16), (128, 32, 24)])
+def test_a_sequence_alone_and_in_a_batch(d, Hq, T, dtype):
+    """What else is in the batch decides where a list is cut, and so the last bits alone: each sequence,
+    alone and among others, is within the bound of the definition, and so within twice it of itself."""
+    g, w, rows, lens = 16, 256, 64, [900, 10, 2500, 1300]
+    x = make(4, T, Hq, 2, d, lens, g, w, rows, rows, dtype, seed=90)
+    O, LSE = check(x, g, w, rows, rows, what="batch")
+    for b in range(4):
+        y = {k: v if "cp" in k or k in ("Kp", "Vp") else v[b:b + 1].contiguous() for k, v in x.items()}
+        o, lse = check(y, g, w, rows, rows, what=f"sequence {b} alone")
+        ref = tree(y["Q"], x["Kp"], x["Vp"], y["table"], x["Kcp"], x["Vcp"], y["core_table"], y["lens"], y["parents"], g, w, rows, rows)
+        assert (np.abs(t64(o) - t64(O[b:b + 1])) <= 2 * ref[2]).all() and (np.abs(t64(lse) - t64(LSE[b:b + 1])) <= 2 * ref[3]).all()
