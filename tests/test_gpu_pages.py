@@ -422,3 +422,27 @@ def test_the_book_keeps_shared_pages_in_their_column():
                 assert where.setdefault(int(page), c) == c, step
         count = np.bincount(t[t >= 0], minlength=64)
         assert status.item() == 0 and (refs.cpu().numpy() == count).all(), step
+
+
+def test_reserve_from_a_large_pool_mostly_held():
+    """Free pages few and far apart: several steps of the scan, shared pages among those replaced."""
+    n, B, cols, rows = 30000, 40, 6, 16
+    rng = np.random.default_rng(8)
+    free = np.sort(rng.choice(np.arange(100, n), 500, replace=False))
+    book = Book(n, B, cols, rows)
+    held = [p for p in range(n) if p not in set(free.tolist())]
+    for p in held:
+        book.refs[p] = 1                                     # by other tables
+    lens = rng.integers(0, 60, B)
+    for b in range(0, B, 2):                                 # rows in pairs share their pages
+        for c in range(-(-int(max(lens[b], lens[b + 1])) // rows)):
+            page = held.pop(int(rng.integers(len(held))))
+            book.table[b][c] = book.table[b + 1][c] = page
+            book.refs[page] = 2
+    extra = rng.integers(0, 36, B)
+    refs, table = book.gpu()
+    s = status()
+    pairs = api.cca_pages_reserve(refs, table, i32(lens), i32(extra), rows, dev_status=s)
+    want = book.reserve(lens.tolist(), extra.tolist())
+    book.same(refs, table)
+    assert s.item() == 0 and pairs.tolist() == want
