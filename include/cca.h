@@ -325,7 +325,11 @@ typedef struct cca_rope_params {
 
 /* One tensor of a call: x and y are [B, H, N, d] by strides (elements, of b, h and n;
  * columns contiguous, every row 16-byte aligned).  y may be x with the same strides;
- * otherwise they must not overlap.  A y stride may not make two rows share memory. */
+ * otherwise they must not overlap.  A y stride may not make two rows share memory.
+ * What is refused as overlapping is told by the spans that the strides cover, with one
+ * exception: cca_rope takes two tensors of one packed projection in place, where every
+ * token has the one's heads before the other's and the sequences come one after the
+ * other. */
 typedef struct cca_rope_tensor {
     const void *x;
     void *y;

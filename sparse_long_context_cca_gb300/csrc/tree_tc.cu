@@ -6,15 +6,17 @@
 // to 256 rows read K and V once; the rows that a small tree leaves empty cost nothing, as the
 // loads bound it.  Per tile an SM's share of HBM needs 64 KB / 44 GB/s = 1.5 us (2800 cycles).
 // Measured: one half 2300 cycles a tile from L2, so HBM is the bound (64 sequences of one token,
-// 32 heads, 8 K: 246 us with weights of one part, 0.94 of the copy bandwidth, 271 us with the two
-// that so few rows have); two halves 3500 cycles, the four products
-// at 820 cycles each against 512 of tensor work, as both read their operands from shared memory
-// (192 KB a tile at 128 B a cycle, next to 64 KB of copies): 16 sequences x 64 nodes, 32 heads
-// over 8, 128 K: 135 us, 4.4 TB/s and 1.1 PFLOP/s.  64-key tiles with two score buffers per half
+// 32 heads, 8 K: 246 us with weights of one part, 0.94 of the copy bandwidth, 270 us with the two
+// that so few rows have); two halves 3500 cycles: 16 sequences x 64 nodes, 32 heads
+// over 8, 128 K, 135 us, 4.4 TB/s and 1.1 PFLOP/s.  That is the chain of a half: its softmax (2100
+// cycles, two passes over the scores, as 512 threads leave a thread no room for a row), then its
+// product, its next scores and the hand-offs (about 1370 in the prefill kernel).  Tensor work is
+// 2048, and the operands that the products read from shared memory (192 KB at 128 B a cycle, next to
+// 64 KB of copies) take no longer.  64-key tiles with two score buffers per half
 // free the softmax from waiting for its product, but their N = 64 products took 740 cycles each:
 // 201 us.  A call on little work is a chain: the CTA's run 1.8 us, page look-up and first copy
 // 2.5 us, first softmax 1.4 us, output 1.5 us, then the join (one token of 32 heads at 32 K,
-// 49 MB: 19.4 us warm, 24.0 us from HBM).
+// 49 MB: 19.2 us warm, 24.0 us from HBM).
 // At d = 64 a tile is half as long to copy (1400 cycles) and its softmax (2100) is the bound: 8
 // sequences of 24 nodes, 32 heads over 8, up to 32 K: 23.6 us (38.4 by mma.sync).
 //
@@ -34,8 +36,8 @@
 // Up to TWO_PART_ROWS rows the weights keep two parts: lanes 16 .. 31 of the first warp hold the
 // same rows again (their queries too, so their scores and weights are the same to the bit) and put
 // the weights' low parts into P, and the two outputs of a row are added at the list's end.  That
-// costs three instructions for two weights and no matrix work: one token of 32 heads at 32 K 18.0 -> 19.4
-// us, 64 sequences of one token at 8 K 246 -> 271, with 32 heads over 8 69 -> 76.
+// costs three instructions for two weights and no matrix work: one token of 32 heads at 32 K 18.0 -> 19.2
+// us, 64 sequences of one token at 8 K 246 -> 270, with 32 heads over 8 69 -> 75.
 //
 // Two halves: S_A | S_B | O_A | O_B fill the tensor memory; the halves' softmaxes and MMAs
 // alternate.  P_h overwrites S_h, and S_h of the next tile is issued after the product that
