@@ -341,6 +341,48 @@ typedef struct cca_rope_tensor {
 int cca_rope(const cca_rope_tensor_t *tensors, int n_tensors, const cca_rope_params_t *params, void *stream);
 
 /*
+ * Norms of queries and keys for each head, with the rotation in the same pass.  A row x of a head becomes
+ *   n = x * r * (offset + weight),  r = (mean of x^2 + eps)^(-1/2),  y = n rotated as by cca_rope
+ * (rot 0: not rotated).  The mean goes over all d columns; the weights are [d], one for each column, or
+ * [H, d] with weight_heads = H; without weights n = x * r.  Everything between the input and the result
+ * is fp32.
+ */
+typedef struct cca_norm_tensor {
+    const void *x;            /* [B, H, N, d] by strides, as in cca_rope_tensor_t */
+    void *y;                  /* the result; backward: the gradient of x */
+    const void *dy;           /* backward: the gradient of the result (NULL forward) */
+    const void *weight;       /* device [weight_heads, d], contiguous, or NULL */
+    void *dweight;            /* backward: its gradient, overwritten, or NULL */
+    int32_t H;
+    int32_t weight_heads;     /* 1 or H */
+    int64_t x_stride[3], y_stride[3], dy_stride[3];
+} cca_norm_tensor_t;
+
+typedef struct cca_norm_params {
+    cca_rope_params_t rope;   /* sizes, type, rotation; inverse must be 0 */
+    float eps;                /* >= 0 */
+    float offset;             /* added to the weights (1 for weights kept around zero) */
+    int32_t weight_dtype;     /* enum cca_dtype, of weight and dweight */
+} cca_norm_params_t;
+
+/* One or two tensors (queries and keys) in one launch.  y may be x with the same strides; what may not
+ * overlap is as in cca_rope. */
+int cca_norm_rope(const cca_norm_tensor_t *tensors, int n_tensors, const cca_norm_params_t *params, void *stream);
+
+/*
+ * Its gradient: with dn the rotation back of dy and t = dn * (offset + weight),
+ *   dx = r * (t - x * r^2 * mean(t x)),   dweight = sum over rows (and heads that share it) of dn * x * r.
+ * The rows' statistics are formed again from x.  The sums behind dweight have a fixed order, so that
+ * results repeat to the bit.  y (= dx) may not overlap x or dy.
+ *   workspace: 16-byte aligned, at least cca_norm_rope_bwd_workspace_size() bytes; not needed (NULL)
+ *   where no dweight is asked for.  Calls that may run at the same time need one each.
+ */
+int cca_norm_rope_bwd(const cca_norm_tensor_t *tensors, int n_tensors, const cca_norm_params_t *params, void *workspace,
+                      uint64_t workspace_bytes, void *stream);
+/* Bytes of workspace on the current device (0 where none is needed, and on bad arguments). */
+uint64_t cca_norm_rope_bwd_workspace_size(const cca_norm_tensor_t *tensors, int n_tensors, const cca_norm_params_t *params);
+
+/*
  * Paged caches.  A pool holds pages of `rows` rows of every KV head,
  *   K, V [layers, n_pages, Hkv, rows, d],
  * and table[b * cols + c] names the page that holds rows c*rows .. (c+1)*rows - 1 of
@@ -384,6 +426,15 @@ typedef struct cca_pages {
 int cca_rope_append(const cca_rope_tensor_t *q, const cca_rope_tensor_t *k, const cca_rope_tensor_t *v,
                     const cca_pages_t *raw, const int32_t *lens, const int32_t *parents, const int32_t *counts,
                     int32_t *dev_status, const cca_rope_params_t *params, void *stream);
+
+/*
+ * cca_norm_rope_append - cca_rope_append with queries and keys normed for each head before they are
+ * rotated (see cca_norm_rope); values are stored as they are.  rope.positions, pos_stride, start and
+ * inverse must be 0, and rot may be 0.  Everything else as cca_rope_append.
+ */
+int cca_norm_rope_append(const cca_norm_tensor_t *q, const cca_norm_tensor_t *k, const cca_rope_tensor_t *v,
+                         const cca_pages_t *raw, const int32_t *lens, const int32_t *parents, const int32_t *counts,
+                         int32_t *dev_status, const cca_norm_params_t *params, void *stream);
 
 /*
  * cca_tree_fwd - CCA attention of a tree of drafted tokens over paged caches (the fusion
@@ -496,6 +547,90 @@ int cca_pages_copy(const cca_pages_t *pages, const int32_t *pairs, int n, const 
  */
 int cca_pages_compact(const cca_pages_t *pages, const int32_t *lens, const int32_t *path, int A,
                       const int32_t *accepted, const cca_params_t *params, void *stream);
+
+/*
+ * Packed sequences: sequences of different lengths one behind the other, [H, T, d] by strides.  Sequence
+ * s holds the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 and knows none of the others: position,
+ * groups, windows and cores are counted from its own first row, with the definitions above (its last
+ * n % g tokens are in no group).  Rows before cu_seqlens[0] and from cu_seqlens[S] on belong to no
+ * sequence; what is written leaves them as they were.
+ * The core tokens of sequence s are the rows cu_seqlens[s] / g + j of Kc, Vc [Hkv, T / g, d]
+ * (contiguous), j < n / g.
+ *
+ * cca_pack - reads the lengths once for all the calls of a batch (every layer, forward and backward)
+ * and lays out their work in `plan`: the tiles of all sequences by falling cost, every token's position,
+ * every group's first token.  The lengths stay on the device: the host never waits, and a captured call
+ * serves later lengths.  The calls below read the plan alone; a plan that cca_pack did not finish, or
+ * made for another T, g, w or window_mode than the call's, is reported in *dev_status
+ * (CCA_ERR_INVALID_ARG) and nothing is written.
+ * cu_seqlens that fall, start below 0 or end above T are reported and make such a plan.
+ */
+typedef struct cca_packed {
+    void *plan;               /* device, 16-byte aligned, cca_pack_size(S, T, g) bytes */
+    uint64_t plan_bytes;
+    int32_t S;                /* sequences, 1 .. 65535; any of them may be empty */
+    int32_t T;                /* rows of the packed tensors             >= 1 */
+    int32_t g;                /* group size                             >= 1 */
+    int32_t w;                /* local window                           >= 1; w >= the longest sequence:
+                                 full causal attention, no core is visible */
+    int32_t window_mode;
+} cca_packed_t;
+
+/* Bytes of a plan (0 on bad sizes). */
+uint64_t cca_pack_size(int S, int T, int g);
+/* Where a plan keeps the tokens' positions: int32 [T], from this byte on (0 for tokens of no sequence). */
+uint64_t cca_pack_positions_offset(int S, int T, int g);
+int cca_pack(const int32_t *cu_seqlens, const cca_packed_t *packed, int32_t *dev_status, void *stream);
+
+/* A packed tensor [H, T, d]: columns contiguous, every row 16-byte aligned, strides (elements) of head
+ * and row.  Those of a result may not make two rows share memory. */
+typedef struct cca_packed_rows {
+    void *p;
+    int64_t head_stride, row_stride;
+} cca_packed_rows_t;
+
+/* params of the calls below: Hq, Hkv, d, dtype, scale, dev_status, pool_mode; the others are not used. */
+
+/*
+ * cca_pool_packed - the pooling equation for every whole group of every sequence.  Core rows that
+ * belong to no group are set to zero.  Supported: bf16 or f32, d in {64, 128}, pool_mode 0 or 1.
+ */
+int cca_pool_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const cca_packed_rows_t *V, void *Kc, void *Vc,
+                    const cca_packed_t *packed, const cca_params_t *params, void *stream);
+
+/*
+ * cca_attn_packed - the fusion equation for every row of every sequence.  O by strides, LSE [Hq, T] fp32.
+ * Kc, Vc may be NULL where w >= T.  What a row does not see (later tokens, other sequences, other
+ * cores) never reaches its output, whatever it holds.
+ * Supported: bf16 or f32, d in {64, 128}; bf16 with d = 128 on the tensor cores.
+ */
+int cca_attn_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const cca_packed_rows_t *V, const void *Kc,
+                    const void *Vc, const cca_packed_rows_t *O, float *LSE, const cca_packed_t *packed,
+                    const cca_params_t *params, void *stream);
+
+/*
+ * cca_packed_clear - sets the rows of no sequence of n <= 4 packed tensors (heads[i] heads each) to zero; all
+ * their rows for a plan that cca_pack did not finish or made for other sizes.  params: d, dtype.
+ */
+int cca_packed_clear(const cca_packed_rows_t *tensors, const int32_t *heads, int n, const cca_packed_t *packed,
+                     const cca_params_t *params, void *stream);
+
+/*
+ * cca_packed_bwd - gradients of the loss sum(dO * O) through cca_attn_packed and, where w < T,
+ * cca_pool_packed, in the inputs' type (rounded once).  Kc, Vc, O, LSE are the forward's.  Sums have a
+ * fixed order: results repeat to the bit.  The gradients of a sequence that holds infinities or NaN
+ * (in any tensor) are not defined; those of the others are not touched by it.
+ *   workspace: 16-byte aligned, at least cca_packed_bwd_workspace_size() bytes, rewritten by every call;
+ *   calls that may run at the same time need one each.
+ * Support as cca_attn_packed and cca_pool_packed.
+ */
+int cca_packed_bwd(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const cca_packed_rows_t *V, const void *Kc,
+                   const void *Vc, const cca_packed_rows_t *O, const float *LSE, const cca_packed_rows_t *dO,
+                   const cca_packed_rows_t *dQ, const cca_packed_rows_t *dK, const cca_packed_rows_t *dV,
+                   const cca_packed_t *packed, const cca_params_t *params, void *workspace, uint64_t workspace_bytes,
+                   void *stream);
+/* Bytes of workspace cca_packed_bwd needs on the current device (0 on bad arguments). */
+uint64_t cca_packed_bwd_workspace_size(const cca_packed_t *packed, const cca_params_t *params);
 
 /* Static English text for a status code (never NULL). */
 const char *cca_status_string(int status);

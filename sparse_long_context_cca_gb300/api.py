@@ -5,7 +5,7 @@ allocates outputs with torch (device memory is plumbing), checks that tensors
 match the C ABI's layout, and forwards raw device pointers.  There is no
 fallback: if the library is missing or a call fails, an exception is raised.
 
-The rotary and paged calls, of which a decoding step makes many, are checked and
+The rotary, paged and packed calls, of which a step makes many, are checked and
 marshalled by the extension module _binding (csrc/binding.cpp), bound to the same
 library.
 """
@@ -61,6 +61,30 @@ class CcaRopeTensor(ctypes.Structure):
                 ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
 
 
+class CcaNormTensor(ctypes.Structure):
+    """Mirror of cca_norm_tensor_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("H", ctypes.c_int32), ("weight_heads", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3), ("dy_stride", ctypes.c_int64 * 3)]
+
+
+class CcaNormParams(ctypes.Structure):
+    """Mirror of cca_norm_params_t."""
+    _fields_ = [("rope", CcaRopeParams), ("eps", ctypes.c_float), ("offset", ctypes.c_float),
+                ("weight_dtype", ctypes.c_int32)]
+
+
+class CcaPacked(ctypes.Structure):
+    """Mirror of cca_packed_t."""
+    _fields_ = [("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_uint64), ("S", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("g", ctypes.c_int32), ("w", ctypes.c_int32), ("window_mode", ctypes.c_int32)]
+
+
+class CcaPackedRows(ctypes.Structure):
+    """Mirror of cca_packed_rows_t."""
+    _fields_ = [("p", ctypes.c_void_p), ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
 class CcaPages(ctypes.Structure):
     """Mirror of cca_pages_t."""
     _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("table", ctypes.c_void_p),
@@ -79,6 +103,10 @@ EXPORTED = ["cca_pool", "cca_attn_fwd", "cca_attn_fwd_rows", "cca_decode_fwd", "
             "cca_rope", "cca_rope_append", "cca_tree_fwd", "cca_tree_workspace_size", "cca_pool_pages",
             "cca_pages_reserve", "cca_pages_reserve_workspace_size", "cca_pages_fork", "cca_pages_free",
             "cca_pages_copy", "cca_pages_compact",
+            "cca_norm_rope", "cca_norm_rope_bwd", "cca_norm_rope_bwd_workspace_size", "cca_norm_rope_append",
+            "cca_pack", "cca_pack_size", "cca_pack_positions_offset", "cca_pool_packed", "cca_attn_packed",
+            "cca_packed_clear",
+            "cca_packed_bwd", "cca_packed_bwd_workspace_size",
             "cca_status_string", "cca_abi_version", "cca_test_set_wait_limit_ns", "cca_test_skip_q_load",
             "cca_test_decode_path"]
 
@@ -126,7 +154,8 @@ def load_library():
         lib.cca_pool_group.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int, pp, vp]
         lib.cca_pool_group.restype = ctypes.c_int
         u64 = ctypes.c_uint64
-        rp, rt, pg = (ctypes.POINTER(x) for x in (CcaRopeParams, CcaRopeTensor, CcaPages))
+        rp, rt, pg, nt, np_, pk, pr = (ctypes.POINTER(x) for x in (CcaRopeParams, CcaRopeTensor, CcaPages, CcaNormTensor,
+                                                                  CcaNormParams, CcaPacked, CcaPackedRows))
         for name, args, res in (
                 ("cca_rope", [rt, ci, rp, vp], ci),
                 ("cca_rope_append", [rt, rt, rt, pg, vp, vp, vp, vp, rp, vp], ci),
@@ -138,7 +167,19 @@ def load_library():
                 ("cca_pages_fork", [vp, ci, vp, ci, ci, ci, vp, vp, ci, vp, vp, vp], ci),
                 ("cca_pages_free", [vp, ci, vp, ci, ci, vp, vp, vp, vp], ci),
                 ("cca_pages_copy", [pg, vp, ci, pp, vp], ci),
-                ("cca_pages_compact", [pg, vp, vp, ci, vp, pp, vp], ci)):
+                ("cca_pages_compact", [pg, vp, vp, ci, vp, pp, vp], ci),
+                ("cca_norm_rope", [nt, ci, np_, vp], ci),
+                ("cca_norm_rope_bwd", [nt, ci, np_, vp, u64, vp], ci),
+                ("cca_norm_rope_bwd_workspace_size", [nt, ci, np_], u64),
+                ("cca_norm_rope_append", [nt, nt, rt, pg, vp, vp, vp, vp, np_, vp], ci),
+                ("cca_pack_size", [ci, ci, ci], u64),
+                ("cca_pack_positions_offset", [ci, ci, ci], u64),
+                ("cca_pack", [vp, pk, vp, vp], ci),
+                ("cca_pool_packed", [pr, pr, pr, vp, vp, pk, pp, vp], ci),
+                ("cca_attn_packed", [pr, pr, pr, vp, vp, pr, vp, pk, pp, vp], ci),
+                ("cca_packed_clear", [pr, ctypes.POINTER(ctypes.c_int32), ci, pk, pp, vp], ci),
+                ("cca_packed_bwd", [pr, pr, pr, vp, vp, pr, vp, pr, pr, pr, pr, pk, pp, vp, u64, vp], ci),
+                ("cca_packed_bwd_workspace_size", [pk, pp], u64)):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, res
         lib.cca_status_string.argtypes = [ctypes.c_int]
@@ -156,7 +197,7 @@ def load_library():
 
 
 def _bound():
-    """The binding of the rotary and paged calls (the others do without it); raises if it has not been
+    """The binding of the rotary, paged and packed calls (the others do without it); raises if it has not been
     built, or for another torch."""
     global _fast
     lib = load_library()
@@ -522,14 +563,23 @@ class CcaAttentionFunction(torch.autograd.Function):
         return dQ.to(Q.dtype), dK.to(K.dtype), dV.to(V.dtype), None, None, None, None, None
 
 
-def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 0, window_mode: int = 0,
-                  inv_freq=None, **rotary):
-    """CCA attention output O [B, Hq, N, d] with gradients for Q, K and V (prefill step).
-    With inv_freq, Q and K are first given their positions by rope(Q, K, inv_freq, **rotary)."""
+def _positioned(Q, K, q_weight, k_weight, norm, inv_freq, rotary):
+    """Q and K normed and given their positions, as far as they are asked for."""
+    if norm or q_weight is not None or k_weight is not None:
+        return norm_rope(Q, K, q_weight, k_weight, inv_freq, **rotary)
     if inv_freq is not None:
-        Q, K = rope(Q, K, inv_freq, **rotary)
-    elif rotary:
+        return rope(Q, K, inv_freq, **rotary)
+    if rotary:
         raise ValueError(f"{sorted(rotary)} without inv_freq")
+    return Q, K
+
+
+def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 0, window_mode: int = 0,
+                  inv_freq=None, q_weight=None, k_weight=None, norm: bool = False, **rotary):
+    """CCA attention output O [B, Hq, N, d] with gradients for Q, K and V (prefill step).
+    With inv_freq, Q and K are first given their positions by rope(Q, K, inv_freq, **rotary); with
+    weights of their norms (or norm=True), by norm_rope(Q, K, q_weight, k_weight, inv_freq, **rotary)."""
+    Q, K = _positioned(Q, K, q_weight, k_weight, norm, inv_freq, rotary)
     return CcaAttentionFunction.apply(Q, K, V, g, w, scale, pool_mode, window_mode)
 
 
@@ -621,6 +671,164 @@ def rope(Q, K, inv_freq, positions=None, start: int = 0, layout: str = "half", f
     return (_fast or _bound()).rope_grad(Q, K, inv_freq, positions, start, layout, factor)
 
 
+def cca_norm_rope(Q, K, q_weight=None, k_weight=None, inv_freq=None, positions=None, start: int = 0, layout: str = "half",
+                  factor: float = 1.0, eps: float = 1e-6, offset: float = 0.0, out=None, stream=None):
+    """cca_rope of queries and keys that are first normed for each head, in one launch: every row is divided
+    by its root mean square (sqrt(mean + eps)) and multiplied by offset + weight, weights [d] or
+    [heads, d] in the inputs' type or fp32 (None: by nothing).  Without inv_freq nothing rotates.
+    Everything else as cca_rope.  Returns (Q', K')."""
+    if stream is not None:
+        with _On(Q, stream):
+            return cca_norm_rope(Q, K, q_weight, k_weight, inv_freq, positions, start, layout, factor, eps, offset, out)
+    q, k = (None, None) if out is None else out
+    return (_fast or _bound()).norm_rope(Q, K, inv_freq, positions, start, layout, factor, q_weight, k_weight, eps, offset, q, k)
+
+
+def norm_rope(Q, K, q_weight=None, k_weight=None, inv_freq=None, positions=None, start: int = 0, layout: str = "half",
+              factor: float = 1.0, eps: float = 1e-6, offset: float = 0.0):
+    """cca_norm_rope with gradients for Q, K (or Q alone, with K None) and the weights: returns (Q', K').
+    The gradient cannot be differentiated again (RuntimeError); captured backward passes as in rope()."""
+    return (_fast or _bound()).norm_rope_grad(Q, K, inv_freq, positions, start, layout, factor, q_weight, k_weight, eps, offset)
+
+
+# ---------------------------------------------------------------- packed sequences
+
+class Packed:
+    """A batch of packed sequences as cca_pack lays it out: `plan` (the device buffer that the packed
+    calls read), `positions` (int32 [tokens], every token's position in its sequence, for rope),
+    and the sizes that it was made for."""
+    __slots__ = ("plan", "positions", "sequences", "tokens", "g", "w", "window_mode")
+
+    def __init__(self, plan, positions, sequences, tokens, g, w, window_mode):
+        self.plan, self.positions = plan, positions
+        self.sequences, self.tokens, self.g, self.w, self.window_mode = sequences, tokens, g, w, window_mode
+
+    def _args(self):
+        return self.plan, self.sequences, self.tokens, self.g, self.w, self.window_mode
+
+    @property
+    def cores(self) -> bool:
+        """Whether a sequence may be long enough to see core tokens."""
+        return self.w < self.tokens and self.g <= self.tokens
+
+
+def cca_pack(cu_seqlens, tokens: int, g: int = 16, w: int | None = None, window_mode: int = 0, plan=None, dev_status=None,
+             stream=None) -> Packed:
+    """Lays out a batch of sequences that lie one behind the other in [heads, tokens, d] tensors: sequence s
+    holds rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 [S + 1] on the device, never read by the host;
+    any sequence may be empty).  Made once for a batch and given to every packed call of every layer.
+    w None: every earlier token of the sequence is seen (full causal attention, no core tokens).
+    A captured call serves later lengths of the same cu_seqlens; `plan` may hold a buffer to use again."""
+    if stream is not None:
+        with _On(cu_seqlens, stream):
+            return cca_pack(cu_seqlens, tokens, g, w, window_mode, plan, dev_status)
+    w = tokens if w is None else w
+    plan, positions = (_fast or _bound()).pack(cu_seqlens, tokens, g, w, window_mode, plan, dev_status)
+    return Packed(plan, positions, cu_seqlens.shape[0] - 1, tokens, g, w, window_mode)
+
+
+def cca_pool_packed(Q, K, V, packed: Packed, Kc=None, Vc=None, scale: float = 0.0, pool_mode: int = 0, dev_status=None,
+                    stream=None):
+    """Global-aware pooling of every whole group of every packed sequence: Q [Hq, tokens, d], K, V [Hkv, tokens, d]
+    with any strides (contiguous, 16-byte aligned rows).  Returns (Kc, Vc), each [Hkv, tokens // g, d]:
+    group j of the sequence that starts at row a is row a // g + j; rows of no group are zero.
+    pool_mode 0 or 1 (see cca_pool)."""
+    if stream is not None:
+        with _On(Q, stream):
+            return cca_pool_packed(Q, K, V, packed, Kc, Vc, scale, pool_mode, dev_status)
+    return (_fast or _bound()).pool_packed(Q, K, V, *packed._args(), Kc, Vc, scale, pool_mode, dev_status)
+
+
+def cca_attn_packed(Q, K, V, Kc, Vc, packed: Packed, O=None, LSE=None, scale: float = 0.0, dev_status=None, stream=None):
+    """CCA attention of every row of every packed sequence over its own tokens and cores (Kc, Vc None where
+    packed.w covers all tokens).  Strides as in cca_pool_packed, of O too.  Returns (O [Hq, tokens, d],
+    LSE [Hq, tokens] fp32); rows of no sequence are left as they were."""
+    if stream is not None:
+        with _On(Q, stream):
+            return cca_attn_packed(Q, K, V, Kc, Vc, packed, O, LSE, scale, dev_status)
+    return (_fast or _bound()).attn_packed(Q, K, V, Kc, Vc, *packed._args(), O, LSE, scale, dev_status)
+
+
+def cca_prefill_packed(Q, K, V, packed: Packed, scale: float = 0.0, pool_mode: int = 0, out=None, dev_status=None, stream=None):
+    """Both steps of CCA prefill over packed sequences: pooling (where a core can be seen), then attention.
+    Returns (O, LSE, Kc, Vc), Kc and Vc None without cores.  `out` may hold preallocated (O, LSE, Kc, Vc)."""
+    if stream is not None:
+        with _On(Q, stream):
+            return cca_prefill_packed(Q, K, V, packed, scale, pool_mode, out, dev_status)
+    O, LSE, Kc, Vc = (None,) * 4 if out is None else out
+    if packed.cores:
+        Kc, Vc = cca_pool_packed(Q, K, V, packed, Kc, Vc, scale, pool_mode, dev_status)
+    else:
+        Kc = Vc = None
+    O, LSE = cca_attn_packed(Q, K, V, Kc, Vc, packed, O, LSE, scale, dev_status)
+    return O, LSE, Kc, Vc
+
+
+def cca_packed_bwd(Q, K, V, Kc, Vc, O, LSE, dO, packed: Packed, scale: float = 0.0, pool_mode: int = 0, dQ=None, dK=None,
+                   dV=None, workspace=None, dev_status=None, stream=None):
+    """Gradients (dQ, dK, dV) of sum(dO * O) for cca_prefill_packed, in the inputs' type.  Rows of no sequence
+    are left as they were."""
+    if stream is not None:
+        with _On(Q, stream):
+            return cca_packed_bwd(Q, K, V, Kc, Vc, O, LSE, dO, packed, scale, pool_mode, dQ, dK, dV, workspace, dev_status)
+    return (_fast or _bound()).packed_bwd(Q, K, V, Kc, Vc, O, LSE, dO, *packed._args(), dQ, dK, dV, workspace, scale, pool_mode,
+                                          dev_status)
+
+
+def cca_packed_clear(packed: Packed, *tensors, stream=None):
+    """Sets the rows of no sequence (before the first one, behind the last one) of up to four packed tensors
+    [heads, tokens, d] to zero, in place; all rows where the lengths were refused."""
+    if stream is not None:
+        with _On(tensors[0], stream):
+            return cca_packed_clear(packed, *tensors)
+    (_fast or _bound()).packed_clear(*packed._args(), *(tensors + (None,) * (4 - len(tensors))))
+
+
+def _packed_rows(t):
+    """t itself where its rows can be read in place, a contiguous copy otherwise."""
+    es = t.element_size()
+    ok = t.stride(2) == 1 and all(s >= 0 and s * es % 16 == 0 for s in t.stride()[:2]) and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+class CcaPackedAttentionFunction(torch.autograd.Function):
+    """Autograd wrapper of cca_prefill_packed: backward = cca_packed_bwd.  Tokens of no sequence have output
+    and gradients zero."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, packed, scale, pool_mode):
+        Q, K, V = (_packed_rows(t) for t in (Q, K, V))
+        O, LSE, Kc, Vc = cca_prefill_packed(Q, K, V, packed, scale, pool_mode)
+        cca_packed_clear(packed, O)
+        ctx.save_for_backward(Q, K, V, Kc, Vc, O, LSE)
+        ctx.cfg = (packed, scale, pool_mode)
+        return O
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dO):
+        if torch.cuda.is_current_stream_capturing():
+            (_fast or _bound()).check_leaves()
+        Q, K, V, Kc, Vc, O, LSE = ctx.saved_tensors
+        packed, scale, pool_mode = ctx.cfg
+        grads = cca_packed_bwd(Q, K, V, Kc, Vc, O, LSE, _packed_rows(dO.to(Q.dtype)), packed, scale, pool_mode)
+        cca_packed_clear(packed, *grads)
+        return (*grads, None, None, None)
+
+
+def cca_attention_packed(Q, K, V, packed: Packed, scale: float = 0.0, pool_mode: int = 0, inv_freq=None, q_weight=None,
+                         k_weight=None, norm: bool = False, **rotary):
+    """CCA attention output O [Hq, tokens, d] of packed sequences with gradients for Q, K and V.  With inv_freq
+    and weights of the norms (see cca_attention), Q and K are first normed and given their positions
+    within their sequences."""
+    if inv_freq is not None or norm or q_weight is not None or k_weight is not None:
+        Q, K = _positioned(Q[None], K[None], q_weight, k_weight, norm, inv_freq, {"positions": packed.positions, **rotary})
+        Q, K = Q[0], K[0]
+    elif rotary:
+        raise ValueError(f"{sorted(rotary)} without inv_freq")
+    return CcaPackedAttentionFunction.apply(Q, K, V, packed, scale, pool_mode)
+
+
 # ---------------------------------------------------------------- paged caches
 
 def cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq=None, parents=None, counts=None, layout: str = "half",
@@ -635,6 +843,19 @@ def cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq=None, parents=None, c
         with _On(K, stream):
             return cca_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out, dev_status)
     return (_fast or _bound()).rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out, dev_status)
+
+
+def cca_norm_rope_append(Q, K, V, Kp, Vp, table, lens, q_weight=None, k_weight=None, inv_freq=None, parents=None, counts=None,
+                         layout: str = "half", factor: float = 1.0, eps: float = 1e-6, offset: float = 0.0, out=None,
+                         dev_status=None, stream=None):
+    """cca_rope_append of queries and keys that are first normed for each head (see cca_norm_rope), in one
+    launch; values are stored as they are.  Returns the queries, contiguous [B, Hq, T, d]."""
+    if stream is not None:
+        with _On(K, stream):
+            return cca_norm_rope_append(Q, K, V, Kp, Vp, table, lens, q_weight, k_weight, inv_freq, parents, counts, layout,
+                                        factor, eps, offset, out, dev_status)
+    return (_fast or _bound()).norm_rope_append(Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out,
+                                                dev_status, q_weight, k_weight, eps, offset)
 
 
 def tree_workspace_size(B, Hq, Hkv, T, d, g, w, dtype) -> int:

@@ -1,4 +1,4 @@
-// CPython binding of the rotary and paged calls of include/cca.h: argument checks and
+// CPython binding of the rotary, paged and packed calls of include/cca.h: argument checks and
 // marshalling only, as api.py does for the others through ctypes.  A decoding step makes many
 // small calls, and looking at a tensor costs about 0.1 us per attribute from Python, a call
 // 20-60 us in all; here it is 2-4 us besides the launches.  The library's functions are not
@@ -35,6 +35,18 @@ struct Library {
     decltype(&cca_pages_free) pages_free;
     decltype(&cca_pages_copy) pages_copy;
     decltype(&cca_pages_compact) pages_compact;
+    decltype(&cca_norm_rope) norm_rope;
+    decltype(&cca_norm_rope_bwd) norm_rope_bwd;
+    decltype(&cca_norm_rope_bwd_workspace_size) norm_rope_bwd_workspace_size;
+    decltype(&cca_norm_rope_append) norm_rope_append;
+    decltype(&cca_pack) pack;
+    decltype(&cca_pack_size) pack_size;
+    decltype(&cca_pack_positions_offset) pack_positions_offset;
+    decltype(&cca_pool_packed) pool_packed;
+    decltype(&cca_attn_packed) attn_packed;
+    decltype(&cca_packed_clear) packed_clear;
+    decltype(&cca_packed_bwd) packed_bwd;
+    decltype(&cca_packed_bwd_workspace_size) packed_bwd_workspace_size;
 } lib;
 PyObject *error_class = nullptr;  // api.CcaError(status, what)
 
@@ -515,6 +527,383 @@ PyObject *rope_append(PyObject *const *a) {
     Py_RETURN_NONE;
 }
 
+// ---------------------------------------------------------------- norms with the rotation
+
+// Weights [d] or [H, d] of a tensor of H heads, contiguous, in the tensor's type or fp32 (nothing for None).
+void norm_weight(PyObject *o, const char *name, const at::Tensor &x, int dev, at::Tensor &w) {
+    if (none(o)) return;
+    w = tensor(o, name);
+    const int64_t d = x.size(3), H = x.size(1);
+    if (w.dim() == 1) same(o, name, w.scalar_type(), {d}, dev);
+    else same(o, name, w.scalar_type(), {H, d}, dev);
+    if (w.scalar_type() != x.scalar_type() && w.scalar_type() != at::kFloat)
+        refuse("%s has dtype %s, expected %s or Float", name, at::toString(w.scalar_type()), at::toString(x.scalar_type()));
+    if (!w.is_contiguous()) refuse("%s must be contiguous", name);
+}
+
+// What a norm needs besides the tensors: the rotation, and eps and offset.
+struct Norm {
+    Turn turn;
+    at::Tensor w[2];
+    float eps = 0.f, offset = 0.f;
+    int weight_type() const {
+        const at::Tensor &x = w[0].defined() ? w[0] : w[1];
+        return x.defined() && x.scalar_type() == at::kBFloat16 ? CCA_BF16 : CCA_F32;
+    }
+    cca_norm_params_t params(const at::Tensor &q, int dtype) const {
+        cca_norm_params_t p = {};
+        p.rope = turn.params(q, dtype);
+        p.eps = eps;
+        p.offset = offset;
+        p.weight_dtype = weight_type();
+        return p;
+    }
+    // q_weight, k_weight, eps, offset
+    void read(PyObject *const *a, const at::Tensor *q, const at::Tensor *k, int dev) {
+        if (q != nullptr) norm_weight(a[0], "q_weight", *q, dev, w[0]);
+        else if (!none(a[0])) refuse("q_weight without Q");
+        if (k != nullptr) norm_weight(a[1], "k_weight", *k, dev, w[1]);
+        else if (!none(a[1])) refuse("k_weight without K");
+        if (w[0].defined() && w[1].defined() && w[0].scalar_type() != w[1].scalar_type())
+            refuse("q_weight and k_weight must have the same dtype");
+        eps = real(a[2], "eps");
+        offset = real(a[3], "offset");
+    }
+};
+
+cca_norm_tensor_t norm_tensor(const at::Tensor &x, const at::Tensor &y, const at::Tensor &w, const char *name) {
+    const cca_rope_tensor_t r = rows(x, y.defined() ? &y : nullptr, name);
+    cca_norm_tensor_t t = {};
+    t.x = r.x;
+    t.y = r.y;
+    t.H = r.H;
+    for (int i = 0; i < 3; ++i) t.x_stride[i] = r.x_stride[i], t.y_stride[i] = r.y_stride[i];
+    t.weight = w.defined() ? w.data_ptr() : nullptr;
+    t.weight_heads = w.defined() && w.dim() == 2 ? r.H : 1;
+    return t;
+}
+
+// Q, K, inv_freq, positions, start, layout, factor, q_weight, k_weight, eps, offset, out Q, out K
+PyObject *norm_rope(PyObject *const *a) {
+    const at::Tensor &q = leader(a[0], "Q");
+    const Place at(q);
+    const int dtype = check_pair(a, q, at.dev);
+    const bool two = !none(a[1]);
+    Norm norm;
+    norm.turn = Turn(a, q, at.dev);
+    norm.read(a + 7, &q, two ? &THPVariable_Unpack(a[1]) : nullptr, at.dev);
+    if ((!two && !none(a[12])) || (two && none(a[11]) != none(a[12]))) refuse("out must hold one tensor for each input");
+    at::Tensor outs[2];
+    cca_norm_tensor_t t[2];
+    for (int i = 0; i < (two ? 2 : 1); ++i) {
+        const at::Tensor &x = THPVariable_Unpack(a[i]);
+        outs[i] = none(a[11 + i]) ? at::empty(x.sizes(), q.options()) : same(a[11 + i], "out", q.scalar_type(), x.sizes(), at.dev);
+        t[i] = norm_tensor(x, outs[i], norm.w[i], i == 0 ? "Q" : "K");
+        to_write(a[11 + i], "out");
+    }
+    const cca_norm_params_t p = norm.params(q, dtype);
+    check(lib.norm_rope(t, two ? 2 : 1, &p, at.stream), "cca_norm_rope");
+    wrote(a[11]), wrote(a[12]);
+    PyObject *first = THPVariable_Wrap(outs[0]);
+    if (two) return Py_BuildValue("(NN)", first, THPVariable_Wrap(outs[1]));
+    return Py_BuildValue("(NO)", first, Py_None);
+}
+
+// Autograd of the same.  The backward pass reads the inputs again (rows' statistics are not kept) and
+// makes the gradients that are asked for; it cannot be differentiated again.
+struct NormFunction : torch::autograd::Function<NormFunction> {
+    using List = torch::autograd::variable_list;
+    using Optional = c10::optional<at::Tensor>;
+
+    static at::Tensor get(const Optional &t) { return t.has_value() ? *t : at::Tensor(); }
+
+    static Norm from(const List &saved, torch::autograd::AutogradContext *ctx) {
+        Norm norm;
+        norm.w[0] = saved[2];
+        norm.w[1] = saved[3];
+        norm.turn.inv_freq = saved[4];
+        norm.turn.positions = saved[5];
+        norm.turn.start = ctx->saved_data["start"].toInt();
+        norm.turn.layout = static_cast<int>(ctx->saved_data["layout"].toInt());
+        norm.turn.factor = static_cast<float>(ctx->saved_data["factor"].toDouble());
+        norm.eps = static_cast<float>(ctx->saved_data["eps"].toDouble());
+        norm.offset = static_cast<float>(ctx->saved_data["offset"].toDouble());
+        return norm;
+    }
+
+    static int type_of(const at::Tensor &t) { return t.scalar_type() == at::kBFloat16 ? CCA_BF16 : CCA_F32; }
+
+    static List forward(torch::autograd::AutogradContext *ctx, const at::Tensor &q, const Optional &k, const Optional &qw,
+                        const Optional &kw, const Optional &inv_freq, const Optional &positions, int64_t start, int64_t layout,
+                        double factor, double eps, double offset) {
+        const c10::cuda::CUDAGuard guard(q.device());
+        List x{RopeFunction::ready(q)};
+        if (k.has_value()) x.push_back(RopeFunction::ready(*k));
+        ctx->save_for_backward({x[0], k.has_value() ? x[1] : at::Tensor(), get(qw), get(kw), get(inv_freq), get(positions)});
+        ctx->saved_data["start"] = start;
+        ctx->saved_data["layout"] = layout;
+        ctx->saved_data["factor"] = factor;
+        ctx->saved_data["eps"] = eps;
+        ctx->saved_data["offset"] = offset;
+        const Norm norm = from({x[0], at::Tensor(), get(qw), get(kw), get(inv_freq), get(positions)}, ctx);
+        List out;
+        cca_norm_tensor_t t[2];
+        for (size_t i = 0; i < x.size(); ++i) {
+            out.push_back(at::empty(x[i].sizes(), x[i].options()));
+            t[i] = norm_tensor(x[i], out[i], norm.w[i], i == 0 ? "Q" : "K");
+        }
+        const cca_norm_params_t p = norm.params(q, type_of(q));
+        check_anywhere(lib.norm_rope(t, static_cast<int>(x.size()), &p, c10::cuda::getCurrentCUDAStream(q.get_device()).stream()),
+                       "cca_norm_rope");
+        return out;
+    }
+
+    static List backward(torch::autograd::AutogradContext *ctx, const List &grads) {
+        TORCH_CHECK(!c10::GradMode::is_enabled(), "norm_rope: its gradient cannot be differentiated again");
+        refuse_uncapturable_leaves();
+        const List saved = ctx->get_saved_variables();
+        const Norm norm = from(saved, ctx);
+        const bool two = saved[1].defined();
+        const c10::cuda::CUDAGuard guard(saved[0].device());
+        const auto here = torch::autograd::get_current_node();
+        auto asked = [&](size_t edge) { return here == nullptr || here->task_should_compute_output(edge); };
+        const size_t weight_edge[2] = {two ? 2u : 1u, (two ? 2u : 1u) + (norm.w[0].defined() ? 1u : 0u)};
+        List out(11), held;
+        cca_norm_tensor_t t[2];
+        int n = 0;
+        for (int i = 0; i < (two ? 2 : 1); ++i) {
+            const bool dx = asked(i), dw = norm.w[i].defined() && asked(weight_edge[i]);
+            if (!dx && !dw) continue;
+            const at::Tensor dy = RopeFunction::ready(grads[i]), y = at::empty(saved[i].sizes(), saved[i].options());
+            held.push_back(dy), held.push_back(y);
+            t[n] = norm_tensor(saved[i], y, norm.w[i], i == 0 ? "Q" : "K");
+            t[n].dy = dy.data_ptr();
+            for (int k = 0; k < 3; ++k) t[n].dy_stride[k] = dy.stride(k);
+            if (dx) out[i] = y;
+            if (dw) {
+                out[2 + i] = at::empty(norm.w[i].sizes(), norm.w[i].options());
+                t[n].dweight = out[2 + i].data_ptr();
+            }
+            ++n;
+        }
+        if (n == 0) return out;
+        const cca_norm_params_t p = norm.params(saved[0], type_of(saved[0]));
+        const int64_t bytes = static_cast<int64_t>(lib.norm_rope_bwd_workspace_size(t, n, &p));
+        at::Tensor space;
+        if (bytes > 0) space = at::empty({bytes}, saved[0].options().dtype(at::kByte));
+        check_anywhere(lib.norm_rope_bwd(t, n, &p, bytes > 0 ? space.data_ptr() : nullptr, bytes,
+                                         c10::cuda::getCurrentCUDAStream(saved[0].get_device()).stream()),
+                       "cca_norm_rope_bwd");
+        return out;
+    }
+};
+
+// Q, K, inv_freq, positions, start, layout, factor, q_weight, k_weight, eps, offset
+PyObject *norm_rope_grad(PyObject *const *a) {
+    const at::Tensor &q = leader(a[0], "Q");
+    const Place at(q);
+    check_pair(a, q, at.dev);
+    const bool two = !none(a[1]);
+    Norm norm;
+    norm.turn = Turn(a, q, at.dev);
+    norm.read(a + 7, &q, two ? &THPVariable_Unpack(a[1]) : nullptr, at.dev);
+    auto given = [](const at::Tensor &t) { return t.defined() ? c10::optional<at::Tensor>(t) : c10::nullopt; };
+    const auto out = NormFunction::apply(q, two ? c10::optional<at::Tensor>(THPVariable_Unpack(a[1])) : c10::nullopt, given(norm.w[0]),
+                                         given(norm.w[1]), given(norm.turn.inv_freq), given(norm.turn.positions), norm.turn.start,
+                                         static_cast<int64_t>(norm.turn.layout), static_cast<double>(norm.turn.factor),
+                                         static_cast<double>(norm.eps), static_cast<double>(norm.offset));
+    PyObject *first = THPVariable_Wrap(out[0]);
+    if (two) return Py_BuildValue("(NN)", first, THPVariable_Wrap(out[1]));
+    return Py_BuildValue("(NO)", first, Py_None);
+}
+
+// Q, K, V, Kp, Vp, table, lens, inv_freq, parents, counts, layout, factor, out, dev_status, q_weight, k_weight, eps, offset
+PyObject *norm_rope_append(PyObject *const *a) {
+    const at::Tensor &k = leader(a[1], "K");
+    const Place at(k);
+    const int64_t B = k.size(0), H = k.size(1), T = k.size(2), d = k.size(3);
+    cca_norm_params_t p = {};
+    p.rope.B = size32(B, "batch");
+    p.rope.N = size32(T, "tokens");
+    p.rope.d = size32(d, "head dimension");
+    p.rope.dtype = dtype_of(k, "K");
+    frequencies(a[7], d, at.dev, p.rope);
+    p.rope.layout = layout(a[10]);
+    p.rope.factor = real(a[11], "factor");
+    const at::Tensor &v = same(a[2], "V", k.scalar_type(), k.sizes(), at.dev);
+    const cca_rope_tensor_t vt = rows(v, nullptr, "V");
+    const cca_pages_t raw = pool(a[3], a[4], a[5], B, H, d, k.scalar_type(), at.dev, "raw pool", false);
+    int32_t *lens = words(a[6], "lens", {B}, at.dev), *parents = words(a[8], "parents", {B, T}, at.dev),
+            *counts = words(a[9], "counts", {B}, at.dev), *status = words(a[13], "dev_status", {1}, at.dev);
+    const bool has_q = !none(a[0]);
+    Norm norm;
+    if (has_q) same(a[0], "Q", k.scalar_type(), {B, leader(a[0], "Q").size(1), T, d}, at.dev);
+    norm.read(a + 14, has_q ? &THPVariable_Unpack(a[0]) : nullptr, &k, at.dev);
+    p.eps = norm.eps;
+    p.offset = norm.offset;
+    p.weight_dtype = norm.weight_type();
+    at::Tensor out;
+    cca_norm_tensor_t qt = {};
+    if (has_q) {
+        const at::Tensor &q = THPVariable_Unpack(a[0]);
+        out = none(a[12]) ? at::empty(q.sizes(), k.options()) : same(a[12], "out", k.scalar_type(), q.sizes(), at.dev);
+        qt = norm_tensor(q, out, norm.w[0], "Q");
+    } else if (!none(a[12])) {
+        refuse("out without Q");
+    }
+    const cca_norm_tensor_t kt = norm_tensor(k, at::Tensor(), norm.w[1], "K");
+    to_write(a[3], "raw pool"), to_write(a[4], "raw pool"), to_write(a[12], "out");
+    check(lib.norm_rope_append(has_q ? &qt : nullptr, &kt, &vt, &raw, lens, parents, counts, status, &p, at.stream),
+          "cca_norm_rope_append");
+    wrote(a[3]), wrote(a[4]), wrote(a[12]);
+    if (has_q) return THPVariable_Wrap(out);
+    Py_RETURN_NONE;
+}
+
+// ---------------------------------------------------------------- packed sequences
+
+// plan, S, T, g, w, window_mode
+cca_packed_t packed(PyObject *const *a, int dev) {
+    cca_packed_t p = {};
+    p.S = int32(a[1], "sequences");
+    p.T = int32(a[2], "tokens");
+    p.g = int32(a[3], "g");
+    p.w = int32(a[4], "w");
+    p.window_mode = int32(a[5], "window_mode");
+    const at::Tensor &plan = same(a[0], "plan", at::kByte, {static_cast<int64_t>(lib.pack_size(p.S, p.T, p.g))}, dev);
+    if (!plan.is_contiguous()) refuse("plan must be contiguous");
+    p.plan = plan.data_ptr();
+    p.plan_bytes = plan.nbytes();
+    return p;
+}
+
+// cu_seqlens, tokens, g, w, window_mode, plan, dev_status
+PyObject *pack(PyObject *const *a) {
+    const at::Tensor &cu = leader(a[0], "cu_seqlens", 1);
+    const Place at(cu);
+    cca_packed_t p = {};
+    p.S = size32(cu.size(0) - 1, "sequences");
+    p.T = int32(a[1], "tokens");
+    p.g = int32(a[2], "g");
+    p.w = int32(a[3], "w");
+    p.window_mode = int32(a[4], "window_mode");
+    const int64_t bytes = static_cast<int64_t>(lib.pack_size(p.S, p.T, p.g));
+    if (bytes == 0) refuse("%d sequences, %d tokens, g = %d", p.S, p.T, p.g);
+    const at::Tensor plan = none(a[5]) ? at::empty({bytes}, cu.options().dtype(at::kByte)) : same(a[5], "plan", at::kByte, {bytes}, at.dev);
+    if (!plan.is_contiguous()) refuse("plan must be contiguous");
+    p.plan = plan.data_ptr();
+    p.plan_bytes = plan.nbytes();
+    check(lib.pack(words(a[0], "cu_seqlens", cu.sizes(), at.dev), &p, words(a[6], "dev_status", {1}, at.dev), at.stream), "cca_pack");
+    wrote(a[5]);
+    const int64_t first = static_cast<int64_t>(lib.pack_positions_offset(p.S, p.T, p.g));
+    return Py_BuildValue("(NN)", THPVariable_Wrap(plan), THPVariable_Wrap(plan.narrow(0, first, 4 * static_cast<int64_t>(p.T)).view(at::kInt)));
+}
+
+cca_packed_rows_t packed_rows(const at::Tensor &x, const char *name) {
+    if (x.stride(2) != 1) refuse("%s must be contiguous in its last dimension", name);
+    return {x.data_ptr(), x.stride(0), x.stride(1)};
+}
+
+// Q, K, V of a call and what they say about it.
+struct PackedCall {
+    const at::Tensor &q, &k, &v;
+    const Place at;
+    cca_packed_t pk;
+    cca_params_t p;
+    cca_packed_rows_t Q, K, V;
+    int64_t G;
+    // Q, K, V and the plan's six
+    PackedCall(PyObject *const *a, PyObject *const *plan, PyObject *scale, PyObject *pool_mode, PyObject *status)
+        : q(leader(a[0], "Q", 3)), k(leader(a[1], "K", 3)), v(tensor(a[2], "V")), at(q) {
+        pk = packed(plan, at.dev);
+        same(a[1], "K", q.scalar_type(), {k.size(0), q.size(1), q.size(2)}, at.dev);
+        same(a[2], "V", q.scalar_type(), k.sizes(), at.dev);
+        if (q.size(1) != pk.T) refuse("Q has %lld tokens, the plan %d", static_cast<long long>(q.size(1)), pk.T);
+        p = params(1, q.size(0), k.size(0), q.size(2), dtype_of(q, "Q"), words(status, "dev_status", {1}, at.dev));
+        p.scale = real(scale, "scale");
+        p.pool_mode = pool_mode != nullptr ? int32(pool_mode, "pool_mode") : 0;
+        Q = packed_rows(q, "Q");
+        K = packed_rows(k, "K");
+        V = packed_rows(v, "V");
+        G = pk.T / pk.g;
+    }
+    // a core tensor, or null for None
+    void *cores(PyObject *o, const char *name) const { return ptr(o, name, q.scalar_type(), {k.size(0), G, q.size(2)}, at.dev); }
+    at::Tensor like(PyObject *o, const char *name, const at::Tensor &x) const {
+        return none(o) ? at::empty(x.sizes(), q.options()) : same(o, name, q.scalar_type(), x.sizes(), at.dev);
+    }
+};
+
+// Q, K, V, plan, S, T, g, w, window_mode, Kc, Vc, scale, pool_mode, dev_status
+PyObject *pool_packed(PyObject *const *a) {
+    const PackedCall c(a, a + 3, a[11], a[12], a[13]);
+    at::Tensor out[2];
+    for (int i = 0; i < 2; ++i) {
+        const char *name = i == 0 ? "Kc" : "Vc";
+        if (none(a[9 + i])) out[i] = at::empty({c.k.size(0), c.G, c.q.size(2)}, c.q.options());
+        else c.cores(a[9 + i], name), out[i] = THPVariable_Unpack(a[9 + i]);
+        to_write(a[9 + i], name);
+    }
+    check(lib.pool_packed(&c.Q, &c.K, &c.V, out[0].data_ptr(), out[1].data_ptr(), &c.pk, &c.p, c.at.stream), "cca_pool_packed");
+    wrote(a[9]), wrote(a[10]);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]));
+}
+
+// Q, K, V, Kc, Vc, plan, S, T, g, w, window_mode, O, LSE, scale, dev_status
+PyObject *attn_packed(PyObject *const *a) {
+    const PackedCall c(a, a + 5, a[13], nullptr, a[14]);
+    const at::Tensor O = c.like(a[11], "O", c.q);
+    const at::Tensor L = none(a[12]) ? at::empty({c.q.size(0), c.q.size(1)}, c.q.options().dtype(at::kFloat))
+                                     : same(a[12], "LSE", at::kFloat, {c.q.size(0), c.q.size(1)}, c.at.dev);
+    if (!L.is_contiguous()) refuse("LSE must be contiguous");
+    const cca_packed_rows_t o = packed_rows(O, "O");
+    to_write(a[11], "O"), to_write(a[12], "LSE");
+    check(lib.attn_packed(&c.Q, &c.K, &c.V, c.cores(a[3], "Kc"), c.cores(a[4], "Vc"), &o, static_cast<float *>(L.data_ptr()), &c.pk,
+                          &c.p, c.at.stream),
+          "cca_attn_packed");
+    wrote(a[11]), wrote(a[12]);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(O), THPVariable_Wrap(L));
+}
+
+// Q, K, V, Kc, Vc, O, LSE, dO, plan, S, T, g, w, window_mode, dQ, dK, dV, workspace, scale, pool_mode, dev_status
+PyObject *packed_bwd(PyObject *const *a) {
+    const PackedCall c(a, a + 8, a[18], a[19], a[20]);
+    const at::Tensor &O = same(a[5], "O", c.q.scalar_type(), c.q.sizes(), c.at.dev), &dO = same(a[7], "dO", c.q.scalar_type(), c.q.sizes(), c.at.dev);
+    const float *L = ptr<float>(a[6], "LSE", at::kFloat, {c.q.size(0), c.q.size(1)}, c.at.dev);
+    const cca_packed_rows_t o = packed_rows(O, "O"), g = packed_rows(dO, "dO");
+    const at::Tensor dQ = c.like(a[14], "dQ", c.q), dK = c.like(a[15], "dK", c.k), dV = c.like(a[16], "dV", c.k);
+    const cca_packed_rows_t dq = packed_rows(dQ, "dQ"), dk = packed_rows(dK, "dK"), dv = packed_rows(dV, "dV");
+    const Workspace ws(a[17], lib.packed_bwd_workspace_size(&c.pk, &c.p), c.q);
+    to_write(a[14], "dQ"), to_write(a[15], "dK"), to_write(a[16], "dV");
+    check(lib.packed_bwd(&c.Q, &c.K, &c.V, c.cores(a[3], "Kc"), c.cores(a[4], "Vc"), &o, L, &g, &dq, &dk, &dv, &c.pk, &c.p, ws.p,
+                         ws.bytes, c.at.stream),
+          "cca_packed_bwd");
+    wrote(a[14]), wrote(a[15]), wrote(a[16]);
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(dQ), THPVariable_Wrap(dK), THPVariable_Wrap(dV));
+}
+
+// plan, S, T, g, w, window_mode, four tensors
+PyObject *packed_clear(PyObject *const *a) {
+    const at::Tensor &first = leader(a[6], "tensor", 3);
+    const Place at(first);
+    const cca_packed_t pk = packed(a, at.dev);
+    const cca_params_t p = params(1, 1, 1, first.size(2), dtype_of(first, "tensor"), nullptr);
+    cca_packed_rows_t r[4];
+    int32_t heads[4];
+    int n = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (none(a[6 + i])) continue;
+        const at::Tensor &x = leader(a[6 + i], "tensor", 3);
+        same(a[6 + i], "tensor", first.scalar_type(), {x.size(0), pk.T, first.size(2)}, at.dev);
+        r[n] = packed_rows(x, "tensor");
+        heads[n++] = size32(x.size(0), "heads");
+        to_write(a[6 + i], "tensor");
+    }
+    check(lib.packed_clear(r, heads, n, &pk, &p, at.stream), "cca_packed_clear");
+    for (int i = 0; i < 4; ++i) wrote(a[6 + i]);
+    Py_RETURN_NONE;
+}
+
 // ---------------------------------------------------------------- paged attention and pooling
 
 // Q, Kp, Vp, table, Kcp, Vcp, core_table, lens, g, w, parents, O, LSE, workspace, scale, dev_status, window_mode
@@ -688,7 +1077,13 @@ PyObject *bind(PyObject *, PyObject *args) {
                {"cca_tree_workspace_size", &l.tree_workspace_size}, {"cca_pool_pages", &l.pool_pages},
                {"cca_pages_reserve", &l.pages_reserve}, {"cca_pages_reserve_workspace_size", &l.pages_reserve_workspace_size},
                {"cca_pages_fork", &l.pages_fork}, {"cca_pages_free", &l.pages_free}, {"cca_pages_copy", &l.pages_copy},
-               {"cca_pages_compact", &l.pages_compact}};
+               {"cca_pages_compact", &l.pages_compact},
+               {"cca_norm_rope", &l.norm_rope}, {"cca_norm_rope_bwd", &l.norm_rope_bwd},
+               {"cca_norm_rope_bwd_workspace_size", &l.norm_rope_bwd_workspace_size},
+               {"cca_norm_rope_append", &l.norm_rope_append}, {"cca_pack", &l.pack}, {"cca_pack_size", &l.pack_size},
+               {"cca_pack_positions_offset", &l.pack_positions_offset}, {"cca_pool_packed", &l.pool_packed},
+               {"cca_attn_packed", &l.attn_packed}, {"cca_packed_bwd", &l.packed_bwd}, {"cca_packed_clear", &l.packed_clear},
+               {"cca_packed_bwd_workspace_size", &l.packed_bwd_workspace_size}};
     for (const auto &f : all) {
         PyObject *address = PyDict_GetItemString(table, f.name);
         void *p = address == nullptr ? nullptr : PyLong_AsVoidPtr(address);
@@ -709,6 +1104,14 @@ PyMethodDef methods[] = {CCA_ENTRY(rope, 10),
                          CCA_ENTRY(rope_grad, 7),
                          CCA_ENTRY(check_leaves, 0),
                          CCA_ENTRY(rope_append, 14),
+                         CCA_ENTRY(norm_rope, 13),
+                         CCA_ENTRY(norm_rope_grad, 11),
+                         CCA_ENTRY(norm_rope_append, 18),
+                         CCA_ENTRY(pack, 7),
+                         CCA_ENTRY(pool_packed, 14),
+                         CCA_ENTRY(attn_packed, 15),
+                         CCA_ENTRY(packed_bwd, 21),
+                         CCA_ENTRY(packed_clear, 10),
                          CCA_ENTRY(tree_fwd, 17),
                          CCA_ENTRY(pool_pages, 14),
                          CCA_ENTRY(pages_reserve, 8),
