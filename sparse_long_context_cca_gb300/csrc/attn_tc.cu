@@ -36,14 +36,25 @@
 // coordinates are taken relative to q_off and kv_off.
 // Every mbarrier wait is bounded in time; on a time-out the CTA stops, drains
 // what it has in flight, frees its tensor memory and reports CCA_ERR_TIMEOUT.
+//
+// PACKED: the same kernel over packed sequences (packed.cuh).  An item's rows, its sequence's first row
+// and its cores come from the batch's plan, rows keep their indices in their sequence, and tensors are
+// read and written by strides.  What is masked must not reach an output, not even as 0 * NaN, so on a tile
+// that it masks a softmax group takes the values through its hands, a key to a thread: keys behind the
+// sequence's end (a tile there holds rows of the next one) are set to zero, the others are looked through
+// (one multiply-add per two values), and where one is not finite the half's rows of this item are computed
+// again, key by key on the CUDA cores, as the epilogue (direct_rows).  d = 64 is built for packed sequences
+// alone.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "internal.h"
+#include "packed.cuh"
 #include "sm100_ptx.cuh"
 #include "tma_host.h"
 #include "visibility.cuh"
@@ -53,10 +64,8 @@ namespace {
 
 constexpr int BM = 128;                       // query rows per half
 constexpr int BN = 128;                       // keys per tile
-constexpr int HD = 128;                       // head dimension
 constexpr int NS = 5;                         // ring slots
-constexpr uint32_t TILE_BYTES = BN * HD * 2;  // one bf16 128x128 tile
-constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;
+constexpr uint32_t HALF_BYTES = BN * 64 * 2;  // 64 columns of a tile, as one swizzled box
 constexpr int NUM_THREADS = 320;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;    // S_h at h * 128
@@ -64,12 +73,7 @@ constexpr uint32_t TM_O = 256;  // O_h at 256 + h * 128
 constexpr float LAZY_RESCALE_LOG2 = 16.0f;  // keep a stale max while it is within 2^16
 
 constexpr uint32_t IDESC_QK = ptx::idesc_bf16_f32(BM, BN, 0, 0);  // Q, K both K-major
-constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(BM, HD, 0, 1);  // P (TMEM), V MN-major
 
-// shared-memory layout (offsets from a 1024-byte aligned base)
-constexpr uint32_t OFF_Q = 0;  // Q_A, Q_B
-constexpr uint32_t OFF_RING = 2 * TILE_BYTES;
-constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE_BYTES;
 constexpr int B_QFULL = 0;
 constexpr int B_QFREE = 1;
 constexpr int B_FULL = 2;               // NS
@@ -80,11 +84,21 @@ constexpr int B_PVDONE = B_PFULL + 2;   // 2
 constexpr int B_OFREE = B_PVDONE + 2;   // 2
 constexpr int B_DRAIN = B_OFREE + 2;
 constexpr int NUM_BARS = B_DRAIN + 1;
-constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
-constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-constexpr uint32_t SMEM_USED = OFF_ABORT + 4;
-constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;  // slack for manual alignment
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+
+// shared-memory layout for head dimension HD (offsets from a 1024-byte aligned base)
+template <int HD>
+struct Layout {
+    static constexpr uint32_t TILE_BYTES = BN * HD * 2;  // one bf16 tile
+    static constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(BM, HD, 0, 1);  // P (TMEM), V MN-major
+    static constexpr uint32_t OFF_Q = 0;  // Q_A, Q_B
+    static constexpr uint32_t OFF_RING = 2 * TILE_BYTES;
+    static constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE_BYTES;
+    static constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
+    static constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
+    static constexpr uint32_t OFF_MARK = OFF_ABORT + 4;  // PACKED: items with a value that is not finite, [half][item parity]
+    static constexpr uint32_t SMEM_BYTES = OFF_MARK + 16 + 1024;  // slack for manual alignment
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
 
 struct Params {
     int B, Hq, Hkv, N, g, w, n_pairs, n_items;
@@ -100,6 +114,14 @@ struct Params {
     int skip_q_load;  // test hook: never load Q, so the pipeline waits run out
     int o_align32;    // O is 32-byte aligned: the epilogue may use 32-byte stores
 };
+struct PackedParams : Params {
+    Plan plan;
+    Rows<const __nv_bfloat16> rQ, rK, rV;
+    Rows<__nv_bfloat16> rO;
+    const __nv_bfloat16 *Kc, *Vc;
+};
+template <bool PACKED>
+using ParamsOf = typename std::conditional<PACKED, PackedParams, Params>::type;
 
 __device__ __forceinline__ int lo_of(int i, int w) { return window_lo(i, w); }
 // first raw token of row i's window (cores stay j < lo(i)/g in both modes)
@@ -121,6 +143,8 @@ struct Item {
     int Tc;   // core tiles loaded (max of the halves' tc)
     int lo0;  // first key of local tile 0
     int T;    // tiles loaded
+    // PACKED: the sequence's first row in the tensors, its first core row, its length, the head
+    int row0, core0, n, h;
 
     __device__ __forceinline__ const Half &half(int h) const { return h ? hB : hA; }
 };
@@ -145,11 +169,11 @@ __device__ __forceinline__ int half_max_step(const Half &x, int Tc) {
     return (x.valid && x.tc > 0) ? Tc + x.kl - (x.tc - 1) : 1;
 }
 
-__device__ __forceinline__ Half make_half(const Params &p, int a, int lo0) {
+__device__ __forceinline__ Half make_half(const Params &p, int a, int lo0, int q_off, int n_q) {
     Half x;
     x.a = a;
-    x.valid = a - p.q_off < p.n_q;
-    x.b = min(a + BM - 1, p.q_off + p.n_q - 1);
+    x.valid = a - q_off < n_q;
+    x.b = min(a + BM - 1, q_off + n_q - 1);
     if (!x.valid) {
         x.tc = x.kl = x.kh = 0;
         return x;
@@ -161,17 +185,31 @@ __device__ __forceinline__ Half make_half(const Params &p, int a, int lo0) {
     return x;
 }
 
-__device__ __forceinline__ Item make_item(const Params &p, int k) {
+template <bool PACKED>
+__device__ __forceinline__ Item make_item(const ParamsOf<PACKED> &p, int k) {
     Item it;
-    const int BH = p.B * p.Hq;
-    const int pair = p.n_pairs - 1 - k / BH;  // heaviest pairs first
-    it.bh = k % BH;
-    const int b = it.bh / p.Hq, h = it.bh % p.Hq;
-    it.kvz = b * p.Hkv + h / (p.Hq / p.Hkv);
-    const int i0 = p.q_off + pair * 2 * BM;  // first row (indices are the sequence's)
-    it.lo0 = win_of(p, i0);
-    it.hA = make_half(p, i0, it.lo0);
-    it.hB = make_half(p, i0 + BM, it.lo0);
+    if constexpr (PACKED) {
+        const int4 e = p.plan.pairs[k / p.Hq];  // heaviest first, all heads of a pair side by side
+        it.h = it.bh = k % p.Hq;
+        it.kvz = it.h / (p.Hq / p.Hkv);
+        it.row0 = e.x;
+        it.core0 = e.w;
+        it.n = e.y;
+        const int i0 = e.z * 2 * BM;
+        it.lo0 = win_of(p, i0);
+        it.hA = make_half(p, i0, it.lo0, 0, e.y);
+        it.hB = make_half(p, i0 + BM, it.lo0, 0, e.y);
+    } else {
+        const int BH = p.B * p.Hq;
+        const int pair = p.n_pairs - 1 - k / BH;  // heaviest pairs first
+        it.bh = k % BH;
+        const int b = it.bh / p.Hq, h = it.bh % p.Hq;
+        it.kvz = b * p.Hkv + h / (p.Hq / p.Hkv);
+        const int i0 = p.q_off + pair * 2 * BM;  // first row (indices are the sequence's)
+        it.lo0 = win_of(p, i0);
+        it.hA = make_half(p, i0, it.lo0, p.q_off, p.n_q);
+        it.hB = make_half(p, i0 + BM, it.lo0, p.q_off, p.n_q);
+    }
     const int last = it.hB.valid ? it.hB.b : it.hA.b;
     it.Tc = max(it.hA.tc, it.hB.tc);
     it.T = it.Tc + (last - it.lo0) / BN + 1;
@@ -187,17 +225,108 @@ __device__ __forceinline__ void report_timeout(const Params &p) {
     if (p.status != nullptr) atomicCAS(p.status, 0, static_cast<int32_t>(-4));
 }
 
+// A warp's 32 rows (lane l of quarter q: row x.a + 32 q + l) by the definition, in fp32 and key by key, only
+// visible keys read: for items in which a masked tile holds a value that is not finite.
+template <int HD>
+__device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, int first) {
+    constexpr int E = HD / 32;  // columns of a lane
+    const int lane = threadIdx.x & 31;
+    auto load = [&](const __nv_bfloat16 *row, float (&f)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = __bfloat162float(row[lane * E + e]);
+    };
+    const int end = it.hB.valid ? it.hB.b : it.hA.b;
+    const int64_t cores = (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD;
+    for (int i = first; i < first + 32 && i <= end; ++i) {
+        float q[E], o[E], m = -INFINITY, l = 0.f;
+        load(p.rQ.at(it.h, it.row0 + i), q);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        // visible keys, cores first, eight at a time (a key alone is a chain of shuffles)
+        const int nc = lo_of(i, p.w) / p.g, win = win_of(p, i), n = nc + i - win + 1;
+        constexpr int KEYS = 8;
+        for (int x0 = 0; x0 < n; x0 += KEYS) {
+            float s[KEYS], v[KEYS][E], top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < KEYS; ++x) {
+                const int key = min(x0 + x, n - 1);
+                float k[E];
+                load(key < nc ? p.Kc + cores + static_cast<int64_t>(key) * HD : p.rK.at(it.kvz, it.row0 + win + key - nc), k);
+                load(key < nc ? p.Vc + cores + static_cast<int64_t>(key) * HD : p.rV.at(it.kvz, it.row0 + win + key - nc), v[x]);
+                s[x] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[x] = fmaf(q[e], k[e], s[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < KEYS; ++x) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s[x] += __shfl_xor_sync(0xffffffffu, s[x], o);
+                s[x] *= p.scale_log2;
+                if (x0 + x < n) top = fmaxf(top, s[x]);
+            }
+            const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m - ref);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+            for (int x = 0; x < KEYS; ++x) {
+                if (x0 + x >= n) continue;
+                const float w = exp2f(s[x] - ref);
+                l += w;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[x][e], o[e]);
+            }
+        }
+        const float inv = 1.f / l;
+        __nv_bfloat16 *out = p.rO.at(it.h, it.row0 + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(o[e] * inv);
+        if (lane == 0) p.LSE[static_cast<int64_t>(it.h) * p.plan.T + it.row0 + i] = (m + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+// One key's values in a tile in shared memory: set to zero, or looked through; true where one of them is an
+// infinity or NaN (x * 0 is 0 for all else, so one packed multiply-add per two values collects them).  The
+// chunks are taken in the order of the swizzle, so that eight neighbouring keys read different banks.
+template <int HD>
+__device__ __forceinline__ bool clean_key(uint32_t tile, int key, bool clear) {
+    const uint32_t row = tile + key * 128, turn = key & 7;
+    uint32_t acc = 0;
+#pragma unroll
+    for (int x = 0; x < HD / 8; ++x) {
+        const uint32_t at = row + (x / 8) * HALF_BYTES + (((x & 7) ^ turn) << 4);
+        if (clear) {
+            ptx::st_shared_v4(at, 0.f, 0.f, 0.f, 0.f);
+        } else {
+            const uint4 v = ptx::ld_shared_v4(at);
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.x), "r"(0u));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.y), "r"(0u));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.z), "r"(0u));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.w), "r"(0u));
+        }
+    }
+    return (acc & 0x7fff7fffu) != 0;
+}
+
+template <bool PACKED, int HD>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_bf16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKc,
-                        const __grid_constant__ CUtensorMap tmVc, const Params p) {
+                        const __grid_constant__ CUtensorMap tmVc,
+                        const __grid_constant__ ParamsOf<PACKED> p) {
+    using L = Layout<HD>;
+    constexpr uint32_t TILE_BYTES = L::TILE_BYTES, OFF_Q = L::OFF_Q, OFF_RING = L::OFF_RING, OFF_BAR = L::OFF_BAR,
+                       IDESC_PV = L::IDESC_PV;
+    constexpr int HALVES = HD / 64;  // boxes of a tile
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *const gbase = smem_raw + (base - raw);
     auto bar = [&](int idx) -> uint32_t { return base + OFF_BAR + 8u * idx; };
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + OFF_ABORT);
-    uint32_t *tmem_ptr_smem = reinterpret_cast<uint32_t *>(gbase + OFF_TMEMPTR);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_ABORT);
+    uint32_t *tmem_ptr_smem = reinterpret_cast<uint32_t *>(gbase + L::OFF_TMEMPTR);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -217,10 +346,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         ptx::mbar_init(bar(B_DRAIN), 1);
         *abort_flag = 0;
+        if constexpr (PACKED) {
+            for (int k = 0; k < 4; ++k) reinterpret_cast<volatile int *>(gbase + L::OFF_MARK)[k] = 0;
+        }
         ptx::fence_mbar_init();
     }
     if (warp == 0) {
-        ptx::tmem_alloc(base + OFF_TMEMPTR, TMEM_COLS);
+        ptx::tmem_alloc(base + L::OFF_TMEMPTR, TMEM_COLS);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -228,6 +360,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_ptr_smem;
     const uint64_t lim = p.wait_limit_ns;
+    int n_items = 0;
+    if constexpr (PACKED) n_items = plan_counts(p.plan).x * p.Hq;
+    else n_items = p.n_items;
 
     if (warp < 2) {
         if (warp == 0 && lane == 0) {
@@ -240,21 +375,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t u = 0;  // ring loads issued so far
             int n_iter = 0;
             bool ok = true;
-            for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n_iter) {
-                const Item it = make_item(p, k);
+            for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x, ++n_iter) {
+                const Item it = make_item<PACKED>(p, k);
                 if (!ptx::wait_bounded(bar(B_QFREE), (n_iter & 1) ^ 1, abort_flag, lim)) break;
                 if (!p.skip_q_load) {
                     ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * TILE_BYTES);
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t dst = base + OFF_Q + h * TILE_BYTES;
-                        const int row0 = (h ? it.hB.a : it.hA.a) - p.q_off;
-                        ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst, 0, row0, it.bh);
-                        ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst + HALF_BYTES, 64, row0, it.bh);
+                        int row0 = h ? it.hB.a : it.hA.a;
+                        if constexpr (PACKED) row0 += it.row0;
+                        else row0 -= p.q_off;
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x)
+                            ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
                     }
                 }
                 for (int t = 0; ok && t < it.T; ++t, u += 2) {
                     const bool core = t < it.Tc;
-                    const int y = core ? t * BN : it.lo0 + (t - it.Tc) * BN - p.kv_off;
+                    int y;
+                    if constexpr (PACKED) y = core ? it.core0 + t * BN : it.row0 + it.lo0 + (t - it.Tc) * BN;
+                    else y = core ? t * BN : it.lo0 + (t - it.Tc) * BN - p.kv_off;
                     // K(t) goes to ring slot u % NS, V(t) to the next one; both copies
                     // complete the K slot's FULL barrier (u is even, see k_full_parity)
                     const int ks = u % NS, vs = (u + 1) % NS;
@@ -269,10 +409,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const void *mk = core ? (const void *)&tmKc : (const void *)&tmK;
                     const void *mv = core ? (const void *)&tmVc : (const void *)&tmV;
                     ptx::mbar_arrive_expect_tx(full, 2 * TILE_BYTES);
-                    ptx::tma_load_3d(mk, full, kdst, 0, y, it.kvz);
-                    ptx::tma_load_3d(mk, full, kdst + HALF_BYTES, 64, y, it.kvz);
-                    ptx::tma_load_3d(mv, full, vdst, 0, y, it.kvz);
-                    ptx::tma_load_3d(mv, full, vdst + HALF_BYTES, 64, y, it.kvz);
+#pragma unroll
+                    for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mk, full, kdst + x * HALF_BYTES, 64 * x, y, it.kvz);
+#pragma unroll
+                    for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mv, full, vdst + x * HALF_BYTES, 64 * x, y, it.kvz);
                 }
             }
             if (*abort_flag) {
@@ -301,8 +441,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t dk0 = ptx::smem_desc_sw128(base + OFF_RING, 16, 1024);
             const uint64_t dv0 = ptx::smem_desc_sw128(base + OFF_RING, HALF_BYTES, 1024);
             bool ok = true;
-            for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n_iter) {
-                const Item it = make_item(p, k);
+            for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x, ++n_iter) {
+                const Item it = make_item<PACKED>(p, k);
                 if (!wwait(bar(B_QFULL), n_iter & 1)) break;
                 int s_left = half_count(it.hA) + half_count(it.hB);
                 // S_h = Q_h K(t)^T into S_h.  The first user of a ring slot waits for the copy.
@@ -316,8 +456,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         pend = (half_uses(it.hA, it.Tc, t) ? 1u : 0u) + (half_uses(it.hB, it.Tc, t) ? 1u : 0u);
                     }
                     ptx::tc_fence_after();
-                    ptx::mma_ss_k128_warp(tmem + TM_S + h * BN, h ? dq1 : dq0, dk0 + static_cast<uint64_t>(slot) * (TILE_BYTES >> 4),
-                                     IDESC_QK, 0u);
+                    if constexpr (HD == 128)
+                        ptx::mma_ss_k128_warp(tmem + TM_S + h * BN, h ? dq1 : dq0, dk0 + static_cast<uint64_t>(slot) * (TILE_BYTES >> 4),
+                                         IDESC_QK, 0u);
+                    else
+                        ptx::mma_ss_k64_warp(tmem + TM_S + h * BN, h ? dq1 : dq0, dk0 + static_cast<uint64_t>(slot) * (TILE_BYTES >> 4),
+                                        IDESC_QK, 0u);
                     ptx::tc_commit_warp(bar(B_SFULL + h));
                     --pend;
                     kpend = (kpend & ~(3u << (2 * slot))) | (pend << (2 * slot));
@@ -459,9 +603,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t sf_cnt = 0;
         int n_done = 0;  // items of this half finished
         bool ok = true;
-        for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x) {
-            const Item it = make_item(p, k);
+        [[maybe_unused]] uint32_t ubase = 0;  // ring loads before this item (PACKED)
+        [[maybe_unused]] volatile int *const mark = reinterpret_cast<volatile int *>(gbase + L::OFF_MARK) + 2 * h;
+        for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x) {
+            const Item it = make_item<PACKED>(p, k);
             const Half x = h ? it.hB : it.hA;
+            [[maybe_unused]] const uint32_t u0 = ubase;
+            ubase += 2 * it.T;
             if (!x.valid) continue;
             const int i = x.a + row;
             const int lo_i = win_of(p, i);           // first raw token of this row's window
@@ -500,6 +648,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 // row max: 3-input max over eight independent partial maxima
                 float mp[8];
+                if constexpr (PACKED) {
+                    // Items of one half follow one another by at most one between its warps (a tile needs the
+                    // arrivals of all four), so two marks by parity are enough; a warp sees its neighbours'
+                    // marks once the item's last product, which waits for their arrivals, is done.
+                    if (masked) {
+                        const bool core = t < it.Tc;
+                        const int key = core ? t * BN + row : it.lo0 + (t - it.Tc) * BN + row;
+                        const bool past = key >= (core ? it.n / p.g : it.n);
+                        if (clean_key<HD>(base + OFF_RING + ((u0 + 2 * t + 1) % NS) * TILE_BYTES, row, past))
+                            mark[n_done & 1] = n_done + 1;
+                        // the other half, where it uses the tile, masks it too and writes the same zeros
+                        if (past) ptx::fence_proxy_async_smem();
+                    }
+                }
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -535,7 +697,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     // S_h complete => every earlier PV of this half is complete: O_h is stable.
                     const float f = rescale ? ptx::ex2(m - m_new) : 1.f;
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < HD / 16; ++c) {
                         uint32_t o[16];
                         ptx::tmem_ld16(tO + c * 16, o);
                         ptx::tmem_wait_ld16(o);
@@ -589,24 +751,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             ptx::tc_fence_after();
             const int li = i - p.q_off;  // row of O and LSE
-            const bool valid = li < p.n_q;
+            bool valid;
+            __nv_bfloat16 *orow;
+            float *lse;
+            if constexpr (PACKED) {
+                valid = i <= x.b;
+                orow = p.rO.at(it.h, it.row0 + i);
+                lse = p.LSE + static_cast<int64_t>(it.h) * p.plan.T + it.row0 + i;
+            } else {
+                valid = li < p.n_q;
+                orow = p.O + (static_cast<int64_t>(it.bh) * p.n_q + li) * HD;
+                lse = p.LSE + static_cast<int64_t>(it.bh) * p.n_q + li;
+            }
             const float inv = 1.f / l;
-            __nv_bfloat16 *orow = p.O + (static_cast<int64_t>(it.bh) * p.n_q + li) * HD;
-            uint32_t o[4][32];
+            uint32_t o[HD / 32][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tO + c * 32, o[c]);
+            for (int c = 0; c < HD / 32; ++c) ptx::tmem_ld32(tO + c * 32, o[c]);
             ptx::tmem_wait_ld(o[0]);
-            ptx::reg_touch(o[1]);
-            ptx::reg_touch(o[2]);
-            ptx::reg_touch(o[3]);
+#pragma unroll
+            for (int c = 1; c < HD / 32; ++c) ptx::reg_touch(o[c]);
             // O_h is in registers: the issuer may start this half's next item
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_OFREE + h));
+            if constexpr (PACKED) {
+                if (mark[n_done & 1] == n_done + 1) {  // the same for the whole warp: every arrival was waited for
+                    direct_rows<HD>(p, it, x.a + quarter * 32);
+                    ++n_done;
+                    continue;
+                }
+            }
             // O / l as bf16, one 32-byte sector per store (two 16-byte stores if O is
             // only 16-byte aligned)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < HD / 32; ++c) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t v[8];
@@ -625,7 +803,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                 }
             }
-            if (valid) p.LSE[static_cast<int64_t>(it.bh) * p.n_q + li] = (m + __log2f(l)) * 0.6931471805599453f;
+            if (valid) *lse = (m + __log2f(l)) * 0.6931471805599453f;
             ++n_done;
         }
     }
@@ -643,7 +821,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 struct DeviceInfo {
     bool ready = false;
     int sms = 0;
-    cudaError_t attr_err = cudaSuccess;
+    cudaError_t attr_err = cudaSuccess, packed_err = cudaSuccess;
 };
 
 DeviceInfo &device_info(int dev) {
@@ -653,8 +831,13 @@ DeviceInfo &device_info(int dev) {
     DeviceInfo &d = info[dev & 63];
     if (!d.ready) {
         cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-        d.attr_err = cudaFuncSetAttribute(attn_bf16_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          static_cast<int>(SMEM_BYTES));
+        d.attr_err = cudaFuncSetAttribute(attn_bf16_tc_kernel<false, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(Layout<128>::SMEM_BYTES));
+        d.packed_err = cudaFuncSetAttribute(attn_bf16_tc_kernel<true, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            static_cast<int>(Layout<128>::SMEM_BYTES));
+        if (d.packed_err == cudaSuccess)
+            d.packed_err = cudaFuncSetAttribute(attn_bf16_tc_kernel<true, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                static_cast<int>(Layout<64>::SMEM_BYTES));
         d.ready = true;
     }
     return d;
@@ -706,7 +889,58 @@ cudaError_t launch_attn_bf16_tc(const void *Q, const void *K, const void *V, con
     p.skip_q_load = g_skip_q_load;
     p.o_align32 = (reinterpret_cast<uintptr_t>(O) & 31u) == 0 ? 1 : 0;
     const unsigned grid = static_cast<unsigned>(p.n_items < di.sms ? p.n_items : di.sms);
-    attn_bf16_tc_kernel<<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
+    attn_bf16_tc_kernel<false, 128><<<grid, NUM_THREADS, Layout<128>::SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream) {
+    EncodeTiledFn enc = get_encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const DeviceInfo &di = device_info(dev);
+    if (di.packed_err != cudaSuccess) return di.packed_err;
+    CUtensorMap mQ, mK, mV, mKc, mVc;
+    if (!encode_packed_bf16(enc, &mQ, a.Q, a.d, a.plan.T, a.Hq) || !encode_packed_bf16(enc, &mK, a.K, a.d, a.plan.T, a.Hkv) ||
+        !encode_packed_bf16(enc, &mV, a.V, a.d, a.plan.T, a.Hkv))
+        return cudaErrorInvalidValue;
+    if (a.Kc != nullptr) {
+        const int64_t head = static_cast<int64_t>(a.plan.G) * a.d;
+        const cca_packed_rows_t kc = {const_cast<void *>(a.Kc), head, a.d}, vc = {const_cast<void *>(a.Vc), head, a.d};
+        if (!encode_packed_bf16(enc, &mKc, kc, a.d, a.plan.G, a.Hkv) || !encode_packed_bf16(enc, &mVc, vc, a.d, a.plan.G, a.Hkv))
+            return cudaErrorInvalidValue;
+    } else {
+        mKc = mK;  // no tile of cores is loaded
+        mVc = mV;
+    }
+    PackedParams p = {};
+    p.B = 1;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.g = a.plan.g;
+    p.w = a.plan.w;
+    p.window_mode = a.plan.window_mode;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.LSE = a.LSE;
+    p.status = a.plan.status;
+    p.wait_limit_ns = g_wait_limit_ns;
+    p.skip_q_load = g_skip_q_load;
+    p.plan = a.plan;
+    p.rQ = rows_of<const __nv_bfloat16>(a.Q);
+    p.rK = rows_of<const __nv_bfloat16>(a.K);
+    p.rV = rows_of<const __nv_bfloat16>(a.V);
+    p.rO = rows_of<__nv_bfloat16>(a.O);
+    p.Kc = static_cast<const __nv_bfloat16 *>(a.Kc);
+    p.Vc = static_cast<const __nv_bfloat16 *>(a.Vc);
+    p.o_align32 = ((reinterpret_cast<uintptr_t>(a.O.p) | (a.O.head_stride | a.O.row_stride) * 2) & 31u) == 0 ? 1 : 0;
+    const int64_t most = static_cast<int64_t>(a.plan.max_pairs) * a.Hq;
+    if (most > 0x7fffffff) return cudaErrorNotSupported;
+    const unsigned grid = static_cast<unsigned>(most < di.sms ? most : di.sms);
+    if (a.d == 128)
+        attn_bf16_tc_kernel<true, 128><<<grid, NUM_THREADS, Layout<128>::SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
+    else
+        attn_bf16_tc_kernel<true, 64><<<grid, NUM_THREADS, Layout<64>::SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
     return cudaGetLastError();
 }
 

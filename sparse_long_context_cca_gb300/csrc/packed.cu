@@ -656,6 +656,7 @@ int cca_attn_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, cons
     a.Vc = cores ? Vc : nullptr;
     a.LSE = LSE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.dtype == CCA_BF16) return from_cuda(launch_attn_packed_tc(a, s));
     return from_cuda(launch_attn_packed_simt(p.dtype, a, s));
 }
 
