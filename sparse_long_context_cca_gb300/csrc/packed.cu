@@ -657,7 +657,7 @@ int cca_attn_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, cons
     a.LSE = LSE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.dtype == CCA_BF16) return from_cuda(launch_attn_packed_tc(a, s));
-    return from_cuda(launch_attn_packed_simt(p.dtype, a, s));
+    return from_cuda(launch_attn_packed_f32(a, s));
 }
 
 int cca_packed_clear(const cca_packed_rows_t *tensors, const int32_t *heads, int n, const cca_packed_t *packed,
@@ -737,7 +737,7 @@ int cca_packed_bwd(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const
     a.Vc = cores ? Vc : nullptr;
     a.LSE = const_cast<float *>(LSE);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto part = [&](int k) { return launch_packed_bwd_simt(p.dtype, a, w, k, s); };
+    auto part = [&](int k) { return p.dtype == CCA_BF16 ? launch_packed_bwd_tc(a, w, k, s) : launch_packed_bwd_f32(a, w, k, s); };
     auto by_type = [&](auto f) {
         if (p.dtype == CCA_BF16) return p.d == 128 ? f(__nv_bfloat16(), std::integral_constant<int, 128>()) : f(__nv_bfloat16(), std::integral_constant<int, 64>());
         return p.d == 128 ? f(float(), std::integral_constant<int, 128>()) : f(float(), std::integral_constant<int, 64>());

@@ -116,9 +116,9 @@ struct PackedBwdSpace {
 };
 
 cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream);
-cudaError_t launch_attn_packed_simt(int dtype, const PackedArgs &a, cudaStream_t stream);
+cudaError_t launch_attn_packed_f32(const PackedArgs &a, cudaStream_t stream);
 // part 0: dKc, dVc; 1: dQ; 2: dK, dV
 cudaError_t launch_packed_bwd_tc(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaStream_t stream);
-cudaError_t launch_packed_bwd_simt(int dtype, const PackedArgs &a, const PackedBwdSpace &w, int part, cudaStream_t stream);
+cudaError_t launch_packed_bwd_f32(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaStream_t stream);
 
 }  // namespace cca

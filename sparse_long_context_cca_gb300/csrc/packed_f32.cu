@@ -1,17 +1,15 @@
-// Attention over packed sequences and its gradient on CUDA cores, for what the tensor-core kernels do
-// not take: fp32 (whose tolerance tf32 products would miss) and bf16 with d = 64.
+// Attention over packed sequences and its gradient in fp32 on CUDA cores (tf32 products would miss its
+// tolerance).
 //
-// Tiles of 64 query rows by 64 keys, 256 threads, everything in fp32.  A thread owns 4 x 4 scores, 16
+// Tiles of 64 query rows by 64 keys, 256 threads.  A thread owns 4 x 4 scores, 16
 // threads a row of them; operands lie in shared memory as fp32 rows padded by one 16-byte chunk, so
 // that a product's four-column reads of eight different rows fall into different banks.  Per 16-byte
 // read a thread does eight multiply-adds in the score products and 10.7 in the others.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "packed.cuh"
-#include "rope.cuh"
 
 namespace cca {
 namespace {
@@ -27,20 +25,16 @@ constexpr int SP = BS + 4;  // pitch of the score tile
 template <int D>
 constexpr int TILE_FLOATS = BS * PITCH<D>;
 
-// rows [y0, y0 + 64) of src (those below `end`, zeros behind) as fp32
-template <typename T, int D>
-__device__ __forceinline__ void load_rows(float *dst, const T *src, int64_t row_stride, int y0, int end) {
-    constexpr int E = 16 / sizeof(T), LPR = D / E, STEP = SIMT_THREADS / LPR;
+// rows [y0, y0 + 64) of src, those below `end`; zeros behind
+template <int D>
+__device__ __forceinline__ void load_rows(float *dst, const float *src, int64_t row_stride, int y0, int end) {
+    constexpr int LPR = D / 4, STEP = SIMT_THREADS / LPR;
 #pragma unroll
     for (int r = 0; r < BS; r += STEP) {
-        const int row = r + threadIdx.x / LPR, c = threadIdx.x % LPR * E;
-        Chunk<T, E> v;
-        v.raw = make_uint4(0u, 0u, 0u, 0u);
-        if (y0 + row < end) v.raw = *reinterpret_cast<const uint4 *>(src + (y0 + row) * row_stride + c);
-#pragma unroll
-        for (int e = 0; e < E; e += 4)
-            *reinterpret_cast<float4 *>(dst + row * PITCH<D> + c + e) =
-                make_float4(to_f(v.e[e]), to_f(v.e[e + 1]), to_f(v.e[e + 2]), to_f(v.e[e + 3]));
+        const int row = r + threadIdx.x / LPR, c = threadIdx.x % LPR * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (y0 + row < end) v = *reinterpret_cast<const float4 *>(src + (y0 + row) * row_stride + c);
+        *reinterpret_cast<float4 *>(dst + row * PITCH<D> + c) = v;
     }
 }
 
@@ -120,17 +114,10 @@ __device__ __forceinline__ void add_columns(const float *p, const float *b, floa
 __device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
     *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d) {
-    Chunk<__nv_bfloat16, 4> v;
-    from_f(a, v.e[0]), from_f(b, v.e[1]), from_f(c, v.e[2]), from_f(d, v.e[3]);
-    *reinterpret_cast<uint2 *>(p) = v.raw;
-}
-
-template <typename T>
 struct SimtArgs {
-    Rows<const T> Q, K, V, O, dO;
-    Rows<T> out, dK, dV;  // out: O, or dQ
-    const T *Kc, *Vc;
+    Rows<const float> Q, K, V, O, dO;
+    Rows<float> out, dK, dV;  // out: O, or dQ
+    const float *Kc, *Vc;
     float *LSE;
     PackedBwdSpace w;
     Plan plan;
@@ -143,8 +130,7 @@ struct Block {
     int a, n, i0, c0;  // first row of the sequence, its length, the block's first row in it, its first core row
     int h, kv;
 };
-template <typename T>
-__device__ __forceinline__ bool query_block(const SimtArgs<T> &p, Block &b) {
+__device__ __forceinline__ bool query_block(const SimtArgs &p, Block &b) {
     const int64_t item = blockIdx.x / p.Hq;
     if (item >= 2ll * plan_counts(p.plan).y) return false;
     const int4 e = p.plan.tiles[item / 2];
@@ -178,8 +164,8 @@ __device__ __forceinline__ bool sees(const Plan &p, int i, bool core, int key) {
     return core ? key < visible_cores(i, p.w, p.g) : key >= window_start(i, p.w, p.g, p.window_mode) && key <= i;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArgs<T> p) {
+template <int D>
+__global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArgs p) {
     extern __shared__ float4 smem4[];
     float *const sQ = reinterpret_cast<float *>(smem4), *const sK = sQ + TILE_FLOATS<D>, *const sP = sK + TILE_FLOATS<D>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -188,8 +174,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArg
     if (!query_block(p, b)) return;
     const Keys keys(p.plan, b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    load_rows<T, D>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n);
-    const T *kc = p.Kc + (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D, *vc = p.Vc + (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D;
+    load_rows<D>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n);
+    const float *kc = p.Kc + (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D, *vc = p.Vc + (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D;
     float m[4], l[4], o[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -202,8 +188,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArg
         int y0, stop;
         const bool core = keys.at(t, y0, stop);
         __syncthreads();
-        if (core) load_rows<T, D>(sK, kc, D, y0, stop);
-        else load_rows<T, D>(sK, p.K.at(b.kv, b.a), p.K.row, y0, stop);
+        if (core) load_rows<D>(sK, kc, D, y0, stop);
+        else load_rows<D>(sK, p.K.at(b.kv, b.a), p.K.row, y0, stop);
         __syncthreads();
         float s[4][4];
         scores<D>(sQ, sK, s);
@@ -237,8 +223,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArg
             for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
         }
         __syncthreads();
-        if (core) load_rows<T, D>(sK, vc, D, y0, stop);
-        else load_rows<T, D>(sK, p.V.at(b.kv, b.a), p.V.row, y0, stop);
+        if (core) load_rows<D>(sK, vc, D, y0, stop);
+        else load_rows<D>(sK, p.V.at(b.kv, b.a), p.V.row, y0, stop);
         __syncthreads();
         if (whole) add_rows<D, false>(sP, sK, o);
         else add_rows<D, true>(sP, sK, o);
@@ -250,7 +236,7 @@ __global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArg
         for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(kFull, l[i], x);
         if (row >= b.n) continue;
         const float inv = 1.f / l[i];
-        T *out = p.out.at(b.h, b.a + row);
+        float *out = p.out.at(b.h, b.a + row);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
             store4(out + tx * 4 + 64 * c, o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
@@ -259,8 +245,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArg
 }
 
 // dQ of 64 query rows: dQ = tau sum dS k (+ the pooling's share of a group-last row).
-template <typename T, int D>
-__global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs<T> p) {
+template <int D>
+__global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs p) {
     extern __shared__ float4 smem4[];
     float *const sQ = reinterpret_cast<float *>(smem4), *const sO = sQ + TILE_FLOATS<D>, *const sK = sO + TILE_FLOATS<D>,
                 *const sV = sK + TILE_FLOATS<D>, *const sP = sV + TILE_FLOATS<D>;
@@ -270,8 +256,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs<
     if (!query_block(p, b)) return;
     const Keys keys(p.plan, b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    load_rows<T, D>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n);
-    load_rows<T, D>(sO, p.dO.at(b.h, b.a), p.dO.row, b.i0, b.n);
+    load_rows<D>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n);
+    load_rows<D>(sO, p.dO.at(b.h, b.a), p.dO.row, b.i0, b.n);
     const int64_t core0 = (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D;
     float lse[4], d[4], dq[4][D / 16];
 #pragma unroll
@@ -289,11 +275,11 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs<
         const bool core = keys.at(t, y0, stop);
         __syncthreads();
         if (core) {
-            load_rows<T, D>(sK, p.Kc + core0, D, y0, stop);
-            load_rows<T, D>(sV, p.Vc + core0, D, y0, stop);
+            load_rows<D>(sK, p.Kc + core0, D, y0, stop);
+            load_rows<D>(sV, p.Vc + core0, D, y0, stop);
         } else {
-            load_rows<T, D>(sK, p.K.at(b.kv, b.a), p.K.row, y0, stop);
-            load_rows<T, D>(sV, p.V.at(b.kv, b.a), p.V.row, y0, stop);
+            load_rows<D>(sK, p.K.at(b.kv, b.a), p.K.row, y0, stop);
+            load_rows<D>(sV, p.V.at(b.kv, b.a), p.V.row, y0, stop);
         }
         __syncthreads();
         float s[4][4], g[4][4];
@@ -317,7 +303,7 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs<
     for (int i = 0; i < 4; ++i) {
         const int row = b.i0 + ty * 4 + i;
         if (row >= b.n) continue;
-        T *out = p.out.at(b.h, b.a + row);
+        float *out = p.out.at(b.h, b.a + row);
         const int j = row / p.plan.g;
         const bool last = j < seen && row - j * p.plan.g == p.plan.g - 1;
 #pragma unroll
@@ -332,8 +318,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs<
 }
 
 // dK and dV of 64 keys of one KV head, raw tokens or cores, over the rows of its query heads that see any.
-template <typename T, int D, bool CORE>
-__global__ void __launch_bounds__(SIMT_THREADS) packed_dkv_kernel(const SimtArgs<T> p) {
+template <int D, bool CORE>
+__global__ void __launch_bounds__(SIMT_THREADS) packed_dkv_kernel(const SimtArgs p) {
     extern __shared__ float4 smem4[];
     float *const sK = reinterpret_cast<float *>(smem4), *const sV = sK + TILE_FLOATS<D>, *const sQ = sV + TILE_FLOATS<D>,
                 *const sO = sQ + TILE_FLOATS<D>, *const sP = sO + TILE_FLOATS<D>;
@@ -369,11 +355,11 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dkv_kernel(const SimtArgs
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int64_t core0 = (static_cast<int64_t>(kv) * pl.G + e.w) * D;
     if (CORE) {
-        load_rows<T, D>(sK, p.Kc + core0, D, y0, nk);
-        load_rows<T, D>(sV, p.Vc + core0, D, y0, nk);
+        load_rows<D>(sK, p.Kc + core0, D, y0, nk);
+        load_rows<D>(sV, p.Vc + core0, D, y0, nk);
     } else {
-        load_rows<T, D>(sK, p.K.at(kv, a), p.K.row, y0, nk);
-        load_rows<T, D>(sV, p.V.at(kv, a), p.V.row, y0, nk);
+        load_rows<D>(sK, p.K.at(kv, a), p.K.row, y0, nk);
+        load_rows<D>(sV, p.V.at(kv, a), p.V.row, y0, nk);
     }
     float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
@@ -385,8 +371,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dkv_kernel(const SimtArgs
         for (int q = q0; q < q1; ++q) {
             const int i0 = q * BS;
             __syncthreads();
-            load_rows<T, D>(sQ, p.Q.at(h, a), p.Q.row, i0, n);
-            load_rows<T, D>(sO, p.dO.at(h, a), p.dO.row, i0, n);
+            load_rows<D>(sQ, p.Q.at(h, a), p.Q.row, i0, n);
+            load_rows<D>(sO, p.dO.at(h, a), p.dO.row, i0, n);
             __syncthreads();
             float s[4][4], g[4][4];
             scores<D>(sQ, sK, s);
@@ -453,8 +439,8 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dkv_kernel(const SimtArgs
     }
 }
 
-template <typename K, typename T>
-cudaError_t start(K kernel, int64_t blocks, int splits, int floats, cudaStream_t stream, const SimtArgs<T> &a) {
+template <typename K>
+cudaError_t start(K kernel, int64_t blocks, int splits, int floats, cudaStream_t stream, const SimtArgs &a) {
     if (blocks > 0x7fffffff) return cudaErrorNotSupported;
     const int smem = floats * 4;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -462,14 +448,14 @@ cudaError_t start(K kernel, int64_t blocks, int splits, int floats, cudaStream_t
     return start_dependent(kernel, dim3(static_cast<unsigned>(blocks), splits), SIMT_THREADS, smem, stream, a);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch(const PackedArgs &p, const PackedBwdSpace *w, int part, cudaStream_t stream) {
-    SimtArgs<T> a = {};
-    a.Q = rows_of<const T>(p.Q);
-    a.K = rows_of<const T>(p.K);
-    a.V = rows_of<const T>(p.V);
-    a.Kc = static_cast<const T *>(p.Kc);
-    a.Vc = static_cast<const T *>(p.Vc);
+    SimtArgs a = {};
+    a.Q = rows_of<const float>(p.Q);
+    a.K = rows_of<const float>(p.K);
+    a.V = rows_of<const float>(p.V);
+    a.Kc = static_cast<const float *>(p.Kc);
+    a.Vc = static_cast<const float *>(p.Vc);
     a.LSE = p.LSE;
     a.plan = p.plan;
     a.Hq = p.Hq;
@@ -479,29 +465,26 @@ cudaError_t launch(const PackedArgs &p, const PackedBwdSpace *w, int part, cudaS
     constexpr int F = TILE_FLOATS<D>, S = BS * SP;
     const int64_t rows = 2ll * p.plan.max_tiles;
     if (w == nullptr) {
-        a.out = rows_of<T>(p.O);
-        return start(attn_packed_kernel<T, D>, rows * p.Hq, 1, 2 * F + S, stream, a);
+        a.out = rows_of<float>(p.O);
+        return start(attn_packed_kernel<D>, rows * p.Hq, 1, 2 * F + S, stream, a);
     }
     a.w = *w;
-    a.dO = rows_of<const T>(p.dO);
-    a.out = rows_of<T>(p.dQ);
-    a.dK = rows_of<T>(p.dK);
-    a.dV = rows_of<T>(p.dV);
-    if (part == 0) return start(packed_dkv_kernel<T, D, true>, 2ll * p.plan.max_cores * p.Hkv, w->splits, 4 * F + S, stream, a);
-    if (part == 1) return start(packed_dq_kernel<T, D>, rows * p.Hq, 1, 4 * F + S, stream, a);
-    return start(packed_dkv_kernel<T, D, false>, rows * p.Hkv, 1, 4 * F + S, stream, a);
-}
-
-cudaError_t launch_any(int dtype, const PackedArgs &a, const PackedBwdSpace *w, int part, cudaStream_t stream) {
-    if (dtype == CCA_BF16) return a.d == 128 ? launch<__nv_bfloat16, 128>(a, w, part, stream) : launch<__nv_bfloat16, 64>(a, w, part, stream);
-    return a.d == 128 ? launch<float, 128>(a, w, part, stream) : launch<float, 64>(a, w, part, stream);
+    a.dO = rows_of<const float>(p.dO);
+    a.out = rows_of<float>(p.dQ);
+    a.dK = rows_of<float>(p.dK);
+    a.dV = rows_of<float>(p.dV);
+    if (part == 0) return start(packed_dkv_kernel<D, true>, 2ll * p.plan.max_cores * p.Hkv, w->splits, 4 * F + S, stream, a);
+    if (part == 1) return start(packed_dq_kernel<D>, rows * p.Hq, 1, 4 * F + S, stream, a);
+    return start(packed_dkv_kernel<D, false>, rows * p.Hkv, 1, 4 * F + S, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_packed_simt(int dtype, const PackedArgs &a, cudaStream_t stream) { return launch_any(dtype, a, nullptr, 0, stream); }
-cudaError_t launch_packed_bwd_simt(int dtype, const PackedArgs &a, const PackedBwdSpace &w, int part, cudaStream_t stream) {
-    return launch_any(dtype, a, &w, part, stream);
+cudaError_t launch_attn_packed_f32(const PackedArgs &a, cudaStream_t stream) {
+    return a.d == 128 ? launch<128>(a, nullptr, 0, stream) : launch<64>(a, nullptr, 0, stream);
+}
+cudaError_t launch_packed_bwd_f32(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaStream_t stream) {
+    return a.d == 128 ? launch<128>(a, &w, part, stream) : launch<64>(a, &w, part, stream);
 }
 
 }  // namespace cca
