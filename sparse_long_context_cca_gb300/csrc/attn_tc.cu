@@ -43,8 +43,9 @@
 // that it masks a softmax group takes the values through its hands, a key to a thread: keys behind the
 // sequence's end (a tile there holds rows of the next one) are set to zero, the others are looked through
 // (one multiply-add per two values), and where one is not finite the half's rows of this item are computed
-// again, key by key on the CUDA cores, as the epilogue (direct_rows).  d = 64 is built for packed sequences
-// alone.
+// again, key by key on the CUDA cores, as the epilogue (direct_rows).  A short sequence (n <= 256 / 2^k)
+// fills an item with 2^k query heads of a KV head side by side, 128 / 2^k rows of each in a half, as far as
+// 2^k divides the heads: an item costs 4 us whatever it holds.  d = 64 is built for packed sequences alone.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -96,7 +97,8 @@ struct Layout {
     static constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
     static constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
     static constexpr uint32_t OFF_MARK = OFF_ABORT + 4;  // PACKED: items with a value that is not finite, [half][item parity]
-    static constexpr uint32_t SMEM_BYTES = OFF_MARK + 16 + 1024;  // slack for manual alignment
+    static constexpr uint32_t OFF_BEGIN = OFF_MARK + 16;  // PACKED: begin[3] of make_item, and the number of items
+    static constexpr uint32_t SMEM_BYTES = OFF_BEGIN + 16 + 1024;  // slack for manual alignment
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
@@ -119,6 +121,8 @@ struct PackedParams : Params {
     Rows<const __nv_bfloat16> rQ, rK, rV;
     Rows<__nv_bfloat16> rO;
     const __nv_bfloat16 *Kc, *Vc;
+    CUtensorMap mQ[3];  // Q in boxes of 2, 4, 8 heads of 64, 32, 16 rows
+    int most;           // log2 of the heads that may share a half
 };
 template <bool PACKED>
 using ParamsOf = typename std::conditional<PACKED, PackedParams, Params>::type;
@@ -145,6 +149,7 @@ struct Item {
     int T;    // tiles loaded
     // PACKED: the sequence's first row in the tensors, its first core row, its length, the head
     int row0, core0, n, h;
+    int lr;  // log2 of the rows of one head in a half (7, less where heads share it)
 
     __device__ __forceinline__ const Half &half(int h) const { return h ? hB : hA; }
 };
@@ -169,11 +174,11 @@ __device__ __forceinline__ int half_max_step(const Half &x, int Tc) {
     return (x.valid && x.tc > 0) ? Tc + x.kl - (x.tc - 1) : 1;
 }
 
-__device__ __forceinline__ Half make_half(const Params &p, int a, int lo0, int q_off, int n_q) {
+__device__ __forceinline__ Half make_half(const Params &p, int a, int lo0, int q_off, int n_q, int rows = BM) {
     Half x;
     x.a = a;
     x.valid = a - q_off < n_q;
-    x.b = min(a + BM - 1, q_off + n_q - 1);
+    x.b = min(a + rows - 1, q_off + n_q - 1);
     if (!x.valid) {
         x.tc = x.kl = x.kh = 0;
         return x;
@@ -185,20 +190,35 @@ __device__ __forceinline__ Half make_half(const Params &p, int a, int lo0, int q
     return x;
 }
 
+// PACKED: begin[c - 1] is the first entry of pairs[] whose halves hold 2^c heads.
 template <bool PACKED>
-__device__ __forceinline__ Item make_item(const ParamsOf<PACKED> &p, int k) {
+__device__ __forceinline__ Item make_item(const ParamsOf<PACKED> &p, int k, [[maybe_unused]] const int *begin) {
     Item it;
     if constexpr (PACKED) {
-        const int4 e = p.plan.pairs[k / p.Hq];  // heaviest first, all heads of a pair side by side
-        it.h = it.bh = k % p.Hq;
+        // heaviest first, all heads of a pair side by side; short sequences, the last ones, by groups of 2^c heads
+        int idx = k / p.Hq, c = 0, at = k - idx * p.Hq;
+        if (idx >= begin[0]) {
+            at = k - begin[0] * p.Hq;
+            for (c = 1; c < 3; ++c) {
+                const int some = (begin[c] - begin[c - 1]) * (p.Hq >> c);
+                if (at < some) break;
+                at -= some;
+            }
+            idx = at / (p.Hq >> c);
+            at -= idx * (p.Hq >> c);
+            idx += begin[c - 1];
+        }
+        const int4 e = p.plan.pairs[idx];
+        it.lr = 7 - c;
+        it.h = it.bh = at << c;
         it.kvz = it.h / (p.Hq / p.Hkv);
         it.row0 = e.x;
         it.core0 = e.w;
         it.n = e.y;
         const int i0 = e.z * 2 * BM;
         it.lo0 = win_of(p, i0);
-        it.hA = make_half(p, i0, it.lo0, 0, e.y);
-        it.hB = make_half(p, i0 + BM, it.lo0, 0, e.y);
+        it.hA = make_half(p, i0, it.lo0, 0, e.y, 1 << it.lr);
+        it.hB = make_half(p, i0 + (1 << it.lr), it.lo0, 0, e.y, 1 << it.lr);
     } else {
         const int BH = p.B * p.Hq;
         const int pair = p.n_pairs - 1 - k / BH;  // heaviest pairs first
@@ -225,21 +245,22 @@ __device__ __forceinline__ void report_timeout(const Params &p) {
     if (p.status != nullptr) atomicCAS(p.status, 0, static_cast<int32_t>(-4));
 }
 
-// A warp's 32 rows (lane l of quarter q: row x.a + 32 q + l) by the definition, in fp32 and key by key, only
-// visible keys read: for items in which a masked tile holds a value that is not finite.
+// 32 rows of a half, from its row `first` on, by the definition, in fp32 and key by key, only visible keys
+// read: for items in which a masked tile holds a value that is not finite.
 template <int HD>
-__device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, int first) {
+__device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, const Half &x, int first) {
     constexpr int E = HD / 32;  // columns of a lane
     const int lane = threadIdx.x & 31;
     auto load = [&](const __nv_bfloat16 *row, float (&f)[E]) {
 #pragma unroll
         for (int e = 0; e < E; ++e) f[e] = __bfloat162float(row[lane * E + e]);
     };
-    const int end = it.hB.valid ? it.hB.b : it.hA.b;
     const int64_t cores = (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD;
-    for (int i = first; i < first + 32 && i <= end; ++i) {
+    for (int row = first; row < first + 32; ++row) {
+        const int i = x.a + (row & ((1 << it.lr) - 1)), h = it.h + (row >> it.lr);
+        if (i > x.b) continue;
         float q[E], o[E], m = -INFINITY, l = 0.f;
-        load(p.rQ.at(it.h, it.row0 + i), q);
+        load(p.rQ.at(h, it.row0 + i), q);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
         // visible keys, cores first, eight at a time (a key alone is a chain of shuffles)
@@ -280,10 +301,10 @@ __device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, 
             }
         }
         const float inv = 1.f / l;
-        __nv_bfloat16 *out = p.rO.at(it.h, it.row0 + i);
+        __nv_bfloat16 *out = p.rO.at(h, it.row0 + i);
 #pragma unroll
         for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-        if (lane == 0) p.LSE[static_cast<int64_t>(it.h) * p.plan.T + it.row0 + i] = (m + log2f(l)) * 0.6931471805599453f;
+        if (lane == 0) p.LSE[static_cast<int64_t>(h) * p.plan.T + it.row0 + i] = (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -348,6 +369,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         *abort_flag = 0;
         if constexpr (PACKED) {
             for (int k = 0; k < 4; ++k) reinterpret_cast<volatile int *>(gbase + L::OFF_MARK)[k] = 0;
+            const int pairs = max(plan_counts(p.plan).x, 0);
+            const int3 s = pairs > 0 ? plan_short(p.plan) : make_int3(0, 0, 0);
+            const int first[5] = {0, p.most >= 1 ? s.x : pairs, p.most >= 2 ? s.y : pairs, p.most >= 3 ? s.z : pairs, pairs};
+            int *out = reinterpret_cast<int *>(gbase + L::OFF_BEGIN), items = 0;
+            for (int c = 0; c < 4; ++c) items += (first[c + 1] - first[c]) * (p.Hq >> c);
+            for (int c = 0; c < 3; ++c) out[c] = first[c + 1];
+            out[3] = items;
         }
         ptx::fence_mbar_init();
     }
@@ -360,8 +388,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_ptr_smem;
     const uint64_t lim = p.wait_limit_ns;
-    int n_items = 0;
-    if constexpr (PACKED) n_items = plan_counts(p.plan).x * p.Hq;
+    const int *const begin = reinterpret_cast<const int *>(gbase + L::OFF_BEGIN);
+    int n_items;
+    if constexpr (PACKED) n_items = begin[3];
     else n_items = p.n_items;
 
     if (warp < 2) {
@@ -376,18 +405,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             int n_iter = 0;
             bool ok = true;
             for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x, ++n_iter) {
-                const Item it = make_item<PACKED>(p, k);
+                const Item it = make_item<PACKED>(p, k, begin);
                 if (!ptx::wait_bounded(bar(B_QFREE), (n_iter & 1) ^ 1, abort_flag, lim)) break;
                 if (!p.skip_q_load) {
                     ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * TILE_BYTES);
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t dst = base + OFF_Q + h * TILE_BYTES;
                         int row0 = h ? it.hB.a : it.hA.a;
-                        if constexpr (PACKED) row0 += it.row0;
-                        else row0 -= p.q_off;
+                        const CUtensorMap *map = &tmQ;
+                        if constexpr (PACKED) {
+                            row0 += it.row0;
+                            if (it.lr < 7) map = &p.mQ[6 - it.lr];
+                        } else {
+                            row0 -= p.q_off;
+                        }
 #pragma unroll
                         for (int x = 0; x < HALVES; ++x)
-                            ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
+                            ptx::tma_load_3d(map, bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
                     }
                 }
                 for (int t = 0; ok && t < it.T; ++t, u += 2) {
@@ -442,7 +476,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t dv0 = ptx::smem_desc_sw128(base + OFF_RING, HALF_BYTES, 1024);
             bool ok = true;
             for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x, ++n_iter) {
-                const Item it = make_item<PACKED>(p, k);
+                const Item it = make_item<PACKED>(p, k, begin);
                 if (!wwait(bar(B_QFULL), n_iter & 1)) break;
                 int s_left = half_count(it.hA) + half_count(it.hB);
                 // S_h = Q_h K(t)^T into S_h.  The first user of a ring slot waits for the copy.
@@ -606,12 +640,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         [[maybe_unused]] uint32_t ubase = 0;  // ring loads before this item (PACKED)
         [[maybe_unused]] volatile int *const mark = reinterpret_cast<volatile int *>(gbase + L::OFF_MARK) + 2 * h;
         for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x) {
-            const Item it = make_item<PACKED>(p, k);
+            const Item it = make_item<PACKED>(p, k, begin);
             const Half x = h ? it.hB : it.hA;
             [[maybe_unused]] const uint32_t u0 = ubase;
             ubase += 2 * it.T;
             if (!x.valid) continue;
-            const int i = x.a + row;
+            int i = x.a + row;
+            if constexpr (PACKED) i = x.a + (row & ((1 << it.lr) - 1));
             const int lo_i = win_of(p, i);           // first raw token of this row's window
             const int nc_i = lo_of(i, p.w) / p.g;    // cores visible to this row
             const int nc_first = lo_of(x.a, p.w) / p.g;
@@ -756,8 +791,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             float *lse;
             if constexpr (PACKED) {
                 valid = i <= x.b;
-                orow = p.rO.at(it.h, it.row0 + i);
-                lse = p.LSE + static_cast<int64_t>(it.h) * p.plan.T + it.row0 + i;
+                const int hh = it.h + (row >> it.lr);
+                orow = p.rO.at(hh, it.row0 + i);
+                lse = p.LSE + static_cast<int64_t>(hh) * p.plan.T + it.row0 + i;
             } else {
                 valid = li < p.n_q;
                 orow = p.O + (static_cast<int64_t>(it.bh) * p.n_q + li) * HD;
@@ -776,7 +812,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (lane == 0) ptx::mbar_arrive(bar(B_OFREE + h));
             if constexpr (PACKED) {
                 if (mark[n_done & 1] == n_done + 1) {  // the same for the whole warp: every arrival was waited for
-                    direct_rows<HD>(p, it, x.a + quarter * 32);
+                    direct_rows<HD>(p, it, x, quarter * 32);
                     ++n_done;
                     continue;
                 }
@@ -902,6 +938,10 @@ cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream) {
     const DeviceInfo &di = device_info(dev);
     if (di.packed_err != cudaSuccess) return di.packed_err;
     CUtensorMap mQ, mK, mV, mKc, mVc;
+    PackedParams p = {};
+    while (p.most < 3 && (a.Hq / a.Hkv) % (2 << p.most) == 0) ++p.most;
+    for (int c = 0; c < p.most; ++c)
+        if (!encode_packed_bf16(enc, &p.mQ[c], a.Q, a.d, a.plan.T, a.Hq, 2 << c)) return cudaErrorInvalidValue;
     if (!encode_packed_bf16(enc, &mQ, a.Q, a.d, a.plan.T, a.Hq) || !encode_packed_bf16(enc, &mK, a.K, a.d, a.plan.T, a.Hkv) ||
         !encode_packed_bf16(enc, &mV, a.V, a.d, a.plan.T, a.Hkv))
         return cudaErrorInvalidValue;
@@ -914,7 +954,6 @@ cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream) {
         mKc = mK;  // no tile of cores is loaded
         mVc = mV;
     }
-    PackedParams p = {};
     p.B = 1;
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;

@@ -28,8 +28,10 @@ namespace {
 constexpr int NORM_THREADS = 256;
 constexpr int NORM_WARPS = NORM_THREADS / 32;
 constexpr int NORM_BATCH = 4;      // heads whose loads are in flight together
-constexpr int NORM_BWD_BATCH = 2;  // the same backward, where a head is two loads
-constexpr int DW_THREADS = 512;
+constexpr int NORM_BWD_BATCH = 4;  // the same backward
+constexpr int NORM_BWD_BLOCKS = 2; // resident
+constexpr int HEAD_SUMS = 2;       // heads of a block whose dw it keeps apart
+constexpr int DW_THREADS = 1024;
 
 enum Turn { TURN_HALF, TURN_PAIRS, TURN_ANY };  // where a column's partner lies (above)
 
@@ -143,21 +145,13 @@ struct Lane {
                                                       : to_f(reinterpret_cast<const __nv_bfloat16 *>(w)[c]));
         }
     }
-    // factor * cos and factor * sin of the columns' angles (1 and 0 behind the rotated part)
-    __device__ __forceinline__ void angles(const NormArgs &a, const uint64_t *freq, int64_t pos, float (&c)[E], float (&s)[E]) const {
-        if constexpr (TURN == TURN_PAIRS) {
+    // factor * cos and factor * sin of the columns' angles (1 and 0 behind the rotated part), from the row's
+    // line of the block's table
+    __device__ __forceinline__ void angles(const float2 *line, float (&c)[E], float (&s)[E]) const {
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                c[e] = 1.f, s[e] = 0.f;
-                if (col + e < rot) turn_cos_sin(static_cast<uint64_t>(pos) * freq[pair(e)], a.factor, c[e], s[e]);
-                c[e + 1] = c[e], s[e + 1] = s[e];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                c[e] = 1.f, s[e] = 0.f;
-                if (col + e < rot) turn_cos_sin(static_cast<uint64_t>(pos) * freq[pair(e)], a.factor, c[e], s[e]);
-            }
+        for (int e = 0; e < E; ++e) {
+            const float2 v = col + e < rot ? line[pair(e)] : make_float2(1.f, 0.f);
+            c[e] = v.x, s[e] = v.y;
         }
     }
 };
@@ -170,20 +164,37 @@ __device__ __forceinline__ void load_freq(const NormArgs &a, uint64_t *freq) {
     }
 }
 
+// The angles of `rows` rows at positions pos[..], made by the whole block: table[row][pair].
+template <int D>
+__device__ __forceinline__ void make_angles(const NormArgs &a, const uint64_t *freq, const int64_t *pos, int rows, float2 *table) {
+    const int half = a.rot / 2;
+    for (int i = threadIdx.x; i < rows * (D / 2); i += NORM_THREADS) {
+        const int row = i / (D / 2), pair = i % (D / 2);
+        if (pair >= half) continue;
+        float2 v;
+        turn_cos_sin(static_cast<uint64_t>(pos[row]) * freq[pair], a.factor, v.x, v.y);
+        table[i] = v;
+    }
+}
+
 // PER_HEAD: a tensor has weights for each head, so they are no part of the coefficients.
 // PAGED: the serving form, one block row per sequence.
 template <typename T, int D, int TURN, bool PER_HEAD, bool PAGED>
 __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormArgs a) {
     using L = Lane<T, D, TURN>;
     constexpr int E = L::E;
+    constexpr int SLOTS = NORM_THREADS / L::LPR;
+    constexpr int BATCH = PER_HEAD ? NORM_BATCH / 2 : NORM_BATCH;
     __shared__ uint64_t sm_freq[D / 2];
+    __shared__ int64_t sm_pos[SLOTS];
+    __shared__ float2 sm_angle[SLOTS * (D / 2)];
     __shared__ int16_t sm_parent[PAGED ? TREE_MAX_NODES : 1];
     __shared__ uint4 sm_rows[TURN == TURN_ANY ? NORM_THREADS : 1];
     const L ln(a.rot, sm_rows);
     const int slot_of_block = threadIdx.x / L::LPR;
     const int64_t total = PAGED ? a.N : static_cast<int64_t>(a.B) * a.N;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * a.rows_per_block + (slot_of_block & (a.rows_per_block - 1));
-    const int sub = slot_of_block / a.rows_per_block, subs = NORM_THREADS / L::LPR / a.rows_per_block;
+    const int sub = slot_of_block / a.rows_per_block, subs = SLOTS / a.rows_per_block;
     const int h0 = (blockIdx.y * subs + sub) * a.heads_per_block, h1 = min(h0 + a.heads_per_block, a.heads);
     const bool work = row < total && h0 < h1;
     const int b = PAGED ? static_cast<int>(blockIdx.z) : static_cast<int>(row / a.N);
@@ -193,15 +204,15 @@ __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormAr
 
     int which = 0, first = 0;  // the tensor of the head walk, heads before it
     while (work && h0 - first >= a.t[which].H) first += a.t[which++].H;
-    Vec<T> x[NORM_BATCH];
+    Vec<T> x[BATCH];
     auto load = [&](int h, int count) {
         const NormSrc &t = a.t[which];
         const char *p = t.x + b * t.xs[0] + (h - first) * t.xs[1] + n * t.xs[2] + ln.col * static_cast<int64_t>(sizeof(T));
 #pragma unroll
-        for (int k = 0; k < NORM_BATCH; ++k)
+        for (int k = 0; k < BATCH; ++k)
             if (k < count) x[k].raw = *reinterpret_cast<const uint4 *>(p + k * t.xs[1]);
     };
-    auto batch_heads = [&](int h) { return min(min(NORM_BATCH, h1 - h), first + a.t[which].H - h); };
+    auto batch_heads = [&](int h) { return min(min(BATCH, h1 - h), first + a.t[which].H - h); };
     if (work) load(h0, batch_heads(h0));
     int len = 0, count_b = 0;
     if constexpr (PAGED) {
@@ -214,11 +225,10 @@ __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormAr
             }
     }
     load_freq(a, sm_freq);
-    __syncthreads();
-    if (!work) return;  // whole row groups leave together
+    if (PAGED && a.parents != nullptr) __syncthreads();
     int64_t pos = 0, page = -1;
     int page_off = 0;
-    bool real = true;
+    bool real = row < total;
     if constexpr (PAGED) {
         if (len < 0) {
             report(a.status, CCA_ERR_INVALID_ARG);
@@ -234,7 +244,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormAr
             page_off = static_cast<int>(slot - c * a.rows);
         }
         if (a.parents != nullptr) {
-            int depth = 0, k = sm_parent[n];
+            int depth = 0, k = row < total ? sm_parent[n] : -1;
             while (k >= 0) {  // parents are below their children, so this ends
                 ++depth;
                 k = sm_parent[k];
@@ -244,9 +254,15 @@ __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormAr
         }
         if (real && (page < 0 || page >= a.n_pages)) report(a.status, CCA_ERR_INVALID_ARG);
         if (!real || page >= a.n_pages) page = -1;
-    } else {
+    } else if (row < total) {
         pos = a.positions != nullptr ? a.positions[b * a.pos_stride + n] : a.start + n;
     }
+    if (sub == 0 && ln.col == 0) sm_pos[slot_of_block] = pos;
+    __syncthreads();
+    make_angles<D>(a, sm_freq, sm_pos, a.rows_per_block, sm_angle);
+    __syncthreads();
+    if (!work) return;  // whole row groups leave together
+    const float2 *const line = sm_angle + (slot_of_block & (a.rows_per_block - 1)) * (D / 2);
 
     for (int h = h0; h < h1;) {
         // one tensor's heads
@@ -254,7 +270,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormAr
         const int end = min(h1, first + t.H);
         float A[E], B[E];
         if (!t.plain) {
-            ln.angles(a, sm_freq, pos, A, B);
+            ln.angles(line, A, B);
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (ln.first(e)) B[e] = -B[e];
@@ -284,7 +300,7 @@ __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormAr
             }
             y += ln.col * static_cast<int64_t>(sizeof(T));
 #pragma unroll
-            for (int k = 0; k < NORM_BATCH; ++k) {
+            for (int k = 0; k < BATCH; ++k) {
                 if (k >= count) continue;  // the same for all lanes of a row
                 if (!t.plain) {
                     float f[E], p[E];
@@ -322,12 +338,14 @@ __global__ void __launch_bounds__(NORM_THREADS, 4) norm_rope_kernel(const NormAr
 // the block's sums go to `part` ([blocks, D] for shared weights, [gridDim.x, H, D] for those of each
 // head), and norm_dw_kernel adds them up in order.
 template <typename T, int D, int TURN, bool PER_HEAD>
-__global__ void __launch_bounds__(NORM_THREADS, 3) norm_rope_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(NORM_THREADS, NORM_BWD_BLOCKS) norm_rope_bwd_kernel(const NormArgs a) {
     using L = Lane<T, D, TURN>;
     constexpr int E = L::E;
     constexpr int SLOTS = NORM_THREADS / L::LPR;
-    constexpr int NB = NORM_BWD_BATCH;
+    constexpr int NB = PER_HEAD ? HEAD_SUMS : NORM_BWD_BATCH;
     __shared__ uint64_t sm_freq[D / 2];
+    __shared__ int64_t sm_pos[SLOTS];
+    __shared__ float2 sm_angle[SLOTS * (D / 2)];
     __shared__ uint4 sm_rows[TURN == TURN_ANY ? NORM_THREADS : 1];
     __shared__ float sm_dw[NORM_WARPS][D];
     const L ln(a.rot, sm_rows);
@@ -337,7 +355,6 @@ __global__ void __launch_bounds__(NORM_THREADS, 3) norm_rope_bwd_kernel(const No
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     load_freq(a, sm_freq);
-    __syncthreads();
     int first = 0;
     for (int which = 0; which < a.n_t; first += a.t[which++].H) {
         const NormSrc &t = a.t[which];
@@ -351,11 +368,15 @@ __global__ void __launch_bounds__(NORM_THREADS, 3) norm_rope_bwd_kernel(const No
         if (!PER_HEAD) ln.weights(a, t.w, true, w);
         for (int64_t tile = blockIdx.x; hs < he && tile < tiles; tile += gridDim.x) {
             const int64_t row = tile * SLOTS + threadIdx.x / L::LPR;
-            if (row >= total) continue;  // whole row groups
             const int64_t b = row / a.N, n = row - b * a.N;
-            const int64_t pos = a.positions != nullptr ? a.positions[b * a.pos_stride + n] : a.start + n;
+            if (ln.col == 0)
+                sm_pos[threadIdx.x / L::LPR] = row >= total ? 0 : a.positions != nullptr ? a.positions[b * a.pos_stride + n] : a.start + n;
+            __syncthreads();  // also: the tile before is done with its angles
+            make_angles<D>(a, sm_freq, sm_pos, SLOTS, sm_angle);
+            __syncthreads();
+            if (row >= total) continue;  // whole row groups
             float C[E], S[E];
-            ln.angles(a, sm_freq, pos, C, S);
+            ln.angles(sm_angle + threadIdx.x / L::LPR * (D / 2), C, S);
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (!ln.first(e)) S[e] = -S[e];  // the rotation back
@@ -432,28 +453,31 @@ struct DwArgs {
     int w_f32;
 };
 
-// dw of one head (or of all that share it): a block adds its partial sums, in a fixed order.
+// 32 columns of dw of one head (or of all that share it): a block adds their partial sums, in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(DW_THREADS) norm_dw_kernel(const DwArgs a) {
-    __shared__ float sm[DW_THREADS / D][D];
+    constexpr int SLICES = DW_THREADS / 32;
+    __shared__ float sm[SLICES][32];
     const int which = static_cast<int>(blockIdx.x) < a.heads[0] ? 0 : 1;
     const int head = blockIdx.x - (which ? a.heads[0] : 0);
-    const int col = threadIdx.x % D, slice = threadIdx.x / D;
+    const float *part = which ? a.part[1] : a.part[0];
+    const int heads = which ? a.heads[1] : a.heads[0], parts = which ? a.parts[1] : a.parts[0];
+    const int lane = threadIdx.x % 32, slice = threadIdx.x / 32, col = blockIdx.y * 32 + lane;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     float v = 0.f;
-#pragma unroll 8
-    for (int i = slice; i < a.parts[which]; i += DW_THREADS / D)
-        v += a.part[which][(static_cast<int64_t>(i) * a.heads[which] + head) * D + col];
-    sm[slice][col] = v;
+#pragma unroll 16
+    for (int i = slice; i < parts; i += SLICES) v += part[(static_cast<int64_t>(i) * heads + head) * D + col];
+    sm[slice][lane] = v;
     __syncthreads();
     if (slice != 0) return;
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < DW_THREADS / D; ++i) v += sm[i][col];
+    for (int i = 0; i < SLICES; ++i) v += sm[i][lane];
     const int64_t at = static_cast<int64_t>(head) * D + col;
-    if (a.w_f32) static_cast<float *>(a.dw[which])[at] = v;
-    else static_cast<__nv_bfloat16 *>(a.dw[which])[at] = __float2bfloat16_rn(v);
+    void *dw = which ? a.dw[1] : a.dw[0];
+    if (a.w_f32) static_cast<float *>(dw)[at] = v;
+    else static_cast<__nv_bfloat16 *>(dw)[at] = __float2bfloat16_rn(v);
 }
 
 // ---------------------------------------------------------------- launches
@@ -513,11 +537,11 @@ struct BwdGrid {
 BwdGrid bwd_grid(const cca_rope_params_t &p, int heads, bool per_head, int sms) {
     const int e = p.dtype == CCA_BF16 ? 8 : 4, slots = NORM_THREADS / (p.d / e);
     const int64_t tiles = (static_cast<int64_t>(p.B) * p.N + slots - 1) / slots;
-    const int want = 3 * sms;  // resident blocks
+    const int want = NORM_BWD_BLOCKS * sms;
     BwdGrid g;
     if (per_head) {
         // one batch of heads to a block, whose sums it keeps apart
-        g.heads_per_block = NORM_BWD_BATCH;
+        g.heads_per_block = HEAD_SUMS;
     } else {
         const int most = (heads + NORM_BWD_BATCH - 1) / NORM_BWD_BATCH;
         int64_t groups = (want + tiles - 1) / tiles;
@@ -759,8 +783,8 @@ int cca_norm_rope_bwd(const cca_norm_tensor_t *tensors, int n_tensors, const cca
         e = params->rope.d == 128 ? launch_bwd<float, 128>(a, turn, per_head, grid, strm)
                                   : launch_bwd<float, 64>(a, turn, per_head, grid, strm);
     if (e != cudaSuccess || rows == 0) return from_cuda(e);
-    return from_cuda(params->rope.d == 128 ? start_dependent(norm_dw_kernel<128>, dim3(rows), DW_THREADS, 0, strm, d)
-                                           : start_dependent(norm_dw_kernel<64>, dim3(rows), DW_THREADS, 0, strm, d));
+    return from_cuda(params->rope.d == 128 ? start_dependent(norm_dw_kernel<128>, dim3(rows, 4), DW_THREADS, 0, strm, d)
+                                           : start_dependent(norm_dw_kernel<64>, dim3(rows, 2), DW_THREADS, 0, strm, d));
 }
 
 int cca_norm_rope_append(const cca_norm_tensor_t *q, const cca_norm_tensor_t *k, const cca_rope_tensor_t *v,

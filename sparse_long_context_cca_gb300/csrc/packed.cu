@@ -76,13 +76,20 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const int32_t *cu, c
         for (int i = end + tid; i < T; i += step) positions[i] = 0;
         for (int c = end / g + tid; c < T / g; c += step) first[c] = -1;
         if (blockIdx.y == 0 && threadIdx.x < 32) {
-            int count[3] = {0, 0, 0};
-            for (int i = threadIdx.x; i < S; i += 32)
-                for (int list = 0; list < 3; ++list) count[list] += tiles_of(list, cu[i + 1] - cu[i]);
-            for (int list = 0; list < 3; ++list)
-                for (int o = 16; o > 0; o >>= 1) count[list] += __shfl_xor_sync(kFull, count[list], o);
+            int count[6] = {0, 0, 0, 0, 0, 0};  // tiles of each list; sequences of 1 to 128, 64, 32 tokens
+            for (int i = threadIdx.x; i < S; i += 32) {
+                const int m = cu[i + 1] - cu[i];
+#pragma unroll
+                for (int list = 0; list < 3; ++list) count[list] += tiles_of(list, m);
+#pragma unroll
+                for (int c = 0; c < 3; ++c) count[3 + c] += m > 0 && m <= 128 >> c ? 1 : 0;
+            }
+#pragma unroll
+            for (int c = 0; c < 6; ++c)
+                for (int o = 16; o > 0; o >>= 1) count[c] += __shfl_xor_sync(kFull, count[c], o);
             if (threadIdx.x == 0) {
-                const int32_t h[PACK_HEADER] = {PACK_MAGIC, T, g, w, window_mode, S, cu[0], end, count[0], count[1], count[2], 0, 0, 0, 0, 0};
+                const int32_t h[PACK_HEADER] = {PACK_MAGIC, T, g, w, window_mode, S, cu[0], end, count[0], count[1], count[2], 0,
+                                                count[0] - count[3], count[0] - count[4], count[0] - count[5], 0};
                 for (int i = 0; i < PACK_HEADER; ++i) header[i] = h[i];
             }
         }
@@ -132,13 +139,15 @@ struct PoolPackedArgs {
 };
 
 constexpr int POOL_WARPS = 4;
-constexpr int POOL_PASSES = 8;  // steps of a chunk: all its rows are asked for before any is used
+constexpr int POOL_BLOCKS = 4;  // resident
+constexpr int POOL_PASSES = 4;  // steps of a chunk: all its rows are asked for before any is used
 
 // One warp per core row and KV head.  D * sizeof(T) / 16 lanes hold a row, so a step takes 32 over that
-// many rows; a chunk of POOL_PASSES steps (16 rows of 128 bf16 columns) goes through one running
-// (maximum, sum).
+// many rows; a chunk of POOL_PASSES steps (8 rows of 128 bf16 columns) goes through one running
+// (maximum, sum).  12 prompts of 32 K tokens in all, 8 heads, g = 16: chunks of 8 steps 44 us at 12 warps an
+// SM (51 at 16, with spills), of 4 steps 38 us at 16 warps (47 at 24).
 template <typename T, int D>
-__global__ void __launch_bounds__(POOL_WARPS * 32) pool_packed_kernel(const PoolPackedArgs a) {
+__global__ void __launch_bounds__(POOL_WARPS * 32, POOL_BLOCKS) pool_packed_kernel(const PoolPackedArgs a) {
     using RT = Row16<T>;
     constexpr int E = RT::E, LPR = D / E, RPP = 32 / LPR;
     const int lane = threadIdx.x & 31, sub = lane / LPR, cl = lane % LPR;
@@ -159,31 +168,43 @@ __global__ void __launch_bounds__(POOL_WARPS * 32) pool_packed_kernel(const Pool
         return;
     }
     const int g = a.plan.g, r = a.Hq / a.Hkv;
+    // a chunk's keys and values; those of the first are asked for before the queries
+    uint4 k[POOL_PASSES], v[POOL_PASSES];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < POOL_PASSES; ++i) {
+            const int t = base + i * RPP + sub;
+            k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (t < g) {
+                k[i] = *reinterpret_cast<const uint4 *>(a.K.at(kv, t0 + t) + cl * 16);
+                v[i] = *reinterpret_cast<const uint4 *>(a.V.at(kv, t0 + t) + cl * 16);
+            }
+        }
+    };
+    load(0);
     float q[E], ak[E], av[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) q[e] = ak[e] = av[e] = 0.f;
     const float scale = a.scale_log2 / r;
     if (a.mode == 0) {
-        for (int h = 0; h < r; ++h) {
-            float f[E];
-            RT::unpack(*reinterpret_cast<const uint4 *>(a.Q.at(kv * r + h, t0 + g - 1) + cl * 16), f);
+        for (int h = 0; h < r; h += 4) {
+            uint4 x[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[e] += f[e];
+            for (int i = 0; i < 4; ++i)
+                if (h + i < r) x[i] = *reinterpret_cast<const uint4 *>(a.Q.at(kv * r + h + i, t0 + g - 1) + cl * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (h + i >= r) continue;
+                float f[E];
+                RT::unpack(x[i], f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) q[e] += f[e];
+            }
         }
     }
     float m = -INFINITY, l = 0.f;
     for (int base = 0; base < g; base += POOL_PASSES * RPP) {
-        uint4 k[POOL_PASSES], v[POOL_PASSES];
-#pragma unroll
-        for (int i = 0; i < POOL_PASSES; ++i) {
-            const int t = base + i * RPP + sub;
-            if (t < g) {
-                k[i] = *reinterpret_cast<const uint4 *>(a.K.at(kv, t0 + t) + cl * 16);
-                v[i] = *reinterpret_cast<const uint4 *>(a.V.at(kv, t0 + t) + cl * 16);
-            } else {
-                k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
+        if (base > 0) load(base);
         float s[POOL_PASSES], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < POOL_PASSES; ++i) {
@@ -335,7 +356,7 @@ __global__ void __launch_bounds__(POOL_WARPS * 32) pool_packed_bwd_kernel(const 
 #pragma unroll
         for (int e = 0; e < E; ++e) q[e] += f[e];
     }
-    constexpr int P = POOL_PASSES / 2;
+    constexpr int P = POOL_PASSES;
     uint4 k[P], v[P];
     float s[P], da[P];
     auto chunk = [&](int base) {

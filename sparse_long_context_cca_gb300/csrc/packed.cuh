@@ -81,6 +81,13 @@ __device__ __forceinline__ int3 plan_counts(const Plan &p) {
     return make_int3(min(c.x, p.max_pairs), min(c.y, p.max_tiles), min(c.z, p.max_cores));
 }
 
+// Where the entries of pairs[] of sequences of at most 128, 64 and 32 tokens begin (there are one each, and
+// they come last).
+__device__ __forceinline__ int3 plan_short(const Plan &p) {
+    const int4 d = *reinterpret_cast<const int4 *>(p.header + 12);
+    return make_int3(d.x, d.y, d.z);
+}
+
 // Cores that any row of a sequence of n tokens sees: (j + 1) * g <= n - w.
 __host__ __device__ __forceinline__ int seen_cores(int n, int w, int g) { return n > w ? (n - w) / g : 0; }
 

@@ -44,12 +44,13 @@ inline bool encode_3d_bf16_d128(EncodeTiledFn enc, CUtensorMap *map, const void 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A packed bf16 tensor [heads, rows, d] by strides, viewed as 3-D (d, rows, heads); box = 64 columns x 128
-// rows x 1 head with 128-byte swizzle.  Rows past `rows` read as zeros.
-inline bool encode_packed_bf16(EncodeTiledFn enc, CUtensorMap *map, const cca_packed_rows_t &t, int d, uint64_t rows, uint64_t heads) {
+// A packed bf16 tensor [heads, rows, d] by strides, viewed as 3-D (d, rows, heads); box = 64 columns x 128 / n
+// rows x n heads with 128-byte swizzle.  Rows past `rows` read as zeros.
+inline bool encode_packed_bf16(EncodeTiledFn enc, CUtensorMap *map, const cca_packed_rows_t &t, int d, uint64_t rows, uint64_t heads,
+                               uint32_t n = 1) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), rows, heads};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(t.row_stride) * 2, static_cast<cuuint64_t>(t.head_stride) * 2};
-    const cuuint32_t box[3] = {64, 128, 1};
+    const cuuint32_t box[3] = {64, 128 / n, n};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
