@@ -12,9 +12,9 @@
 //
 //  dq kernel, one 128-row query tile of one (b, h) per CTA, over the same key
 //  tiles as the forward (cores, then the band):
-//     S = Q K^T, dP = dO V^T (both SS, fp32 in TMEM)  ->  dS (bf16, over S)
+//     S = Q K^T, dP = dO V^T (both SS, fp32 in TMEM)  ->  dS (bf16, over dP)
 //     dQ += dS K  (A = dS in TMEM, B = K tile read MN-major)
-//  TMEM: S | dP | dQ.  K/V tiles are double-buffered: the next tile's copy is
+//  TMEM: S | dP | dP | dQ.  K/V tiles are double-buffered: the next tile's copy is
 //  in flight while this one is processed.
 //
 //  dkv kernel, one 128-key tile (raw tokens or cores) of one (b, kv) per CTA,
@@ -285,21 +285,21 @@ __device__ __forceinline__ void store_tile_f32(const CUtensorMap *map, uint32_t 
 // then the band).  Warp-specialised, 320 threads:
 //   warp 0      producer: Q and dO once, then K(t) into one of three stages and V(t)
 //               into one of two (TMA; K lives longer: S(t) and dQ(t) read it);
-//   warp 1      MMA issuer, per tile t:  S(t+1) = Q K(t+1)^T into the other S buffer,
-//               then (once the element-wise warps have written dS(t)) dQ += dS(t) K(t),
-//               then dP(t+1) = dO V(t+1)^T;
-//   warps 2..9  element-wise: P = 2^(S tau log2e - LSE) as soon as S(t) is there (while
-//               dP(t) is still being computed), then dS = P (dP - D) as bf16 over S.
+//   warp 1      MMA issuer, per tile t:  S(t+1) = Q K(t+1)^T (once the element-wise warps have S(t) in
+//               registers), dP(t+1) = dO V(t+1)^T into the other dP buffer, then (once they have
+//               written dS(t)) dQ += dS(t) K(t);
+//   warps 2..9  element-wise: P = 2^(S tau log2e - LSE) as soon as S(t) is there, then
+//               dS = P (dP - D) as bf16 over dP.
 //               Warps w and w + 4 share TMEM lanes 32*(w%4)..+31 (the query rows) and
 //               split the 128 key columns, 64 each.  Each also computes D = dO . O of its
 //               row (the first of the pair stores it for the dK/dV kernel).
-// TMEM: S0 | S1 | dP | dQ, 128 columns each.  S is double-buffered so that the tensor
-// pipe computes the next tile's S while this tile's dS is formed.
+// TMEM: S | dP0 | dP1 | dQ, 128 columns each.  S needs one buffer, as its warps hold P in registers; with
+// two of dP both products of the next tile run while this tile's dS is formed, and only dQ waits for it.
 constexpr int DQ_THREADS = 320;
 constexpr int DQ_KST = 3, DQ_VST = 2;
-constexpr int QB_QD = 0, QB_FULLK = 1, QB_EMPTYK = 4, QB_FULLV = 7, QB_EMPTYV = 9, QB_SFULL = 11, QB_DPFULL = 13,
-              QB_PFULL = 14, QB_DONE = 15, QB_DRAIN = 16, QB_CUT = 17;
-constexpr int DQ_NBARS = 18;
+constexpr int QB_QD = 0, QB_FULLK = 1, QB_EMPTYK = 4, QB_FULLV = 7, QB_EMPTYV = 9, QB_SFULL = 11, QB_SREAD = 12,
+              QB_DPFULL = 13, QB_PFULL = 15, QB_DONE = 16, QB_DRAIN = 17, QB_CUT = 18;
+constexpr int DQ_NBARS = 19;
 template <int HD>
 struct DqLayout {
     static constexpr uint32_t TILE_BYTES = BT * HD * 2;
@@ -379,8 +379,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             ptx::mbar_init(bar(QB_EMPTYV + st), 1);
         }
         ptx::mbar_init(bar(QB_SFULL), 1);
-        ptx::mbar_init(bar(QB_SFULL + 1), 1);
+        ptx::mbar_init(bar(QB_SREAD), 8);  // one arrive per element-wise warp
         ptx::mbar_init(bar(QB_DPFULL), 1);
+        ptx::mbar_init(bar(QB_DPFULL + 1), 1);
         ptx::mbar_init(bar(QB_PFULL), 8);  // one arrive per element-wise warp
         ptx::mbar_init(bar(QB_DONE), 1);
         ptx::mbar_init(bar(QB_DRAIN), 1);
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(gb + DQ_OFF_TMEM);
-    constexpr uint32_t T_DP = 256, T_DQ = 384;  // TMEM columns; S(t) at 128 * (t & 1)
+    constexpr uint32_t T_DP = 128, T_DQ = 384;  // TMEM columns; S at 0, dP(t) at T_DP + 128 * (t & 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -481,13 +482,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         const uint64_t dQd = ptx::smem_desc_sw128(sQ, 16, 1024), ddOd = ptx::smem_desc_sw128(sdO, 16, 1024);
         auto issue_s = [&](int x) {  // S(x) = Q K(x)^T
             ptx::tc_fence_after();
-            mma_ss<HD>(tmem + 128u * (x & 1), dQd, ptx::smem_desc_sw128(stage_k(x), 16, 1024));
-            ptx::tc_commit_warp(bar(QB_SFULL + (x & 1)));
+            mma_ss<HD>(tmem, dQd, ptx::smem_desc_sw128(stage_k(x), 16, 1024));
+            ptx::tc_commit_warp(bar(QB_SFULL));
         };
         auto issue_dp = [&](int x) {  // dP(x) = dO V(x)^T
             ptx::tc_fence_after();
-            mma_ss<HD>(tmem + T_DP, ddOd, ptx::smem_desc_sw128(stage_v(x), 16, 1024));
-            ptx::tc_commit_warp(bar(QB_DPFULL));
+            mma_ss<HD>(tmem + T_DP + 128u * (x & 1), ddOd, ptx::smem_desc_sw128(stage_v(x), 16, 1024));
+            ptx::tc_commit_warp(bar(QB_DPFULL + (x & 1)));
             ptx::tc_commit_warp(bar(QB_EMPTYV + x % DQ_VST));
         };
         bool ok = wwait(bar(QB_QD), 0) && wwait(bar(QB_FULLK), 0);
@@ -497,18 +498,18 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             const int x = tt + 1;
             if (x < T) {
                 if (!(ok = wwait(bar(QB_FULLK + x % DQ_KST), (x / DQ_KST) & 1))) break;
+                if (!(ok = wwait(bar(QB_SREAD), tt & 1))) break;
                 issue_s(x);
-            }
-            if (!(ok = wwait(bar(QB_PFULL), tt & 1))) break;
-            ptx::tc_fence_after();
-            ptx::mma_ts_k128_split_warp(tmem + T_DQ, tmem + 128u * (tt & 1),
-                                        ptx::smem_desc_sw128(stage_k(tt), HALF_BYTES, 1024), IDESC_TS,
-                                        tt > 0 ? 1u : 0u);  // dQ += dS K
-            ptx::tc_commit_warp(bar(QB_EMPTYK + tt % DQ_KST));  // K(tt)'s stage is free once this has read it
-            if (x < T) {
+                // dP(x) takes the buffer of dS(x - 2), which dQ(x - 2), issued before, has read by then
                 if (!(ok = wwait(bar(QB_FULLV + x % DQ_VST), (x / DQ_VST) & 1))) break;
                 issue_dp(x);
             }
+            if (!(ok = wwait(bar(QB_PFULL), tt & 1))) break;
+            ptx::tc_fence_after();
+            ptx::mma_ts_k128_split_warp(tmem + T_DQ, tmem + T_DP + 128u * (tt & 1),
+                                        ptx::smem_desc_sw128(stage_k(tt), HALF_BYTES, 1024), IDESC_TS,
+                                        tt > 0 ? 1u : 0u);  // dQ += dS K
+            ptx::tc_commit_warp(bar(QB_EMPTYK + tt % DQ_KST));  // K(tt)'s stage is free once this has read it
         }
         ptx::tc_commit_warp(ok ? bar(QB_DONE) : bar(QB_DRAIN));
         if (!ok) {
@@ -566,12 +567,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         const float c1 = p.tau * LOG2E;
         bool ok = true;
         for (int tt = 0; tt < T; ++tt) {
-            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_SFULL + (tt & 1)), (tt >> 1) & 1, abort_flag, lim))) {
+            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_SFULL), tt & 1, abort_flag, lim))) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            const uint32_t sS = tmem + lane_addr + 128u * (tt & 1) + h0;
+            const uint32_t sS = tmem + lane_addr + h0, sD = tmem + lane_addr + T_DP + 128u * (tt & 1) + h0;
             uint32_t pa[32], pb[32];
             ptx::tmem_ld32(sS, pa);
             ptx::tmem_ld32(sS + 32, pb);
@@ -587,6 +588,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             if (!valid) c_hi = -1;
             ptx::tmem_wait_ld(pa);
             ptx::reg_touch(pb);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(QB_SREAD));  // the next S may come
             // P = 2^(S tau log2e - LSE), zero off the visible columns
             const bool whole = __all_sync(0xffffffffu, c_lo <= h0 && c_hi >= h0 + 63);
             if (whole) {
@@ -605,15 +609,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                                 ? __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pb[k]), c1, -lse2))) : 0u;
                 }
             }
-            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_DPFULL), tt & 1, abort_flag, lim))) {
+            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_DPFULL + (tt & 1)), (tt >> 1) & 1, abort_flag, lim))) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            // dS = P (dP - D), bf16 pairs written over the S columns [h0, h0 + 32), which
+            // dS = P (dP - D), bf16 pairs written over the dP columns [h0, h0 + 32), which
             // this warp has already read
             uint32_t dp[32], pk[16];
-            ptx::tmem_ld32(tmem + lane_addr + T_DP + h0, dp);
+            ptx::tmem_ld32(sD, dp);
             ptx::tmem_wait_ld(dp);
             if (PACKED && !whole) {  // nothing of a masked value gets on, not as 0 * NaN either
 #pragma unroll
@@ -624,8 +628,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             for (int k = 0; k < 16; ++k)
                 pk[k] = ptx::pack_bf16x2(__uint_as_float(pa[2 * k]) * (__uint_as_float(dp[2 * k]) - Di),
                                          __uint_as_float(pa[2 * k + 1]) * (__uint_as_float(dp[2 * k + 1]) - Di));
-            ptx::tmem_st16(sS, pk);
-            ptx::tmem_ld32(tmem + lane_addr + T_DP + h0 + 32, dp);
+            ptx::tmem_st16(sD, pk);
+            ptx::tmem_ld32(sD + 32, dp);
             ptx::tmem_wait_ld(dp);
             if (PACKED && !whole) {
 #pragma unroll
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             for (int k = 0; k < 16; ++k)
                 pk[k] = ptx::pack_bf16x2(__uint_as_float(pb[2 * k]) * (__uint_as_float(dp[2 * k]) - Di),
                                          __uint_as_float(pb[2 * k + 1]) * (__uint_as_float(dp[2 * k + 1]) - Di));
-            ptx::tmem_st16(sS + 16, pk);
+            ptx::tmem_st16(sD + 16, pk);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();

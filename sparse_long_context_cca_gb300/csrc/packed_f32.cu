@@ -4,19 +4,24 @@
 // Tiles of 64 query rows by 64 keys, 256 threads.  A thread owns 4 x 4 scores, 16
 // threads a row of them; operands lie in shared memory as fp32 rows padded by one 16-byte chunk, so
 // that a product's four-column reads of eight different rows fall into different banks.  Per 16-byte
-// read a thread does eight multiply-adds in the score products and 10.7 in the others.
+// read a thread does eight multiply-adds in the score products and 10.7 in the others.  A tile's copies
+// (cp.async) run while the products that do not need them are formed: keys while weights meet values,
+// values while scores are formed.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "packed.cuh"
+#include "sm100_ptx.cuh"
 
 namespace cca {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int BS = 64;  // rows and keys of a tile
-constexpr int SIMT_THREADS = 256;
+constexpr int SIMT_THREADS = 256;  // four threads to a row
+constexpr int SMALL_BLOCKS = 4;    // blocks of 64 rows an SM below which a call is small
+constexpr int SMALL_GROUPS = 2;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 template <int D>
@@ -25,23 +30,28 @@ constexpr int SP = BS + 4;  // pitch of the score tile
 template <int D>
 constexpr int TILE_FLOATS = BS * PITCH<D>;
 
-// rows [y0, y0 + 64) of src, those below `end`; zeros behind
-template <int D>
-__device__ __forceinline__ void load_rows(float *dst, const float *src, int64_t row_stride, int y0, int end) {
-    constexpr int LPR = D / 4, STEP = SIMT_THREADS / LPR;
-#pragma unroll
-    for (int r = 0; r < BS; r += STEP) {
-        const int row = r + threadIdx.x / LPR, c = threadIdx.x % LPR * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (y0 + row < end) v = *reinterpret_cast<const float4 *>(src + (y0 + row) * row_stride + c);
-        *reinterpret_cast<float4 *>(dst + row * PITCH<D> + c) = v;
+// Starts copying `rows` rows from y0 on of src (those below `end`; zeros behind) to dst, as one group.
+template <int D, int THREADS>
+__device__ __forceinline__ void copy_rows(float *dst, const float *src, int64_t row_stride, int y0, int end, int rows) {
+    constexpr int LPR = D / 4, STEP = THREADS / LPR;
+    const int tid = threadIdx.x % THREADS, c = tid % LPR * 4;
+    const uint32_t to = ptx::smem_addr(dst);
+#pragma unroll 4
+    for (int row = tid / LPR; row < rows; row += STEP) {
+        const bool in = y0 + row < end;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (row * PITCH<D> + c) * 4),
+                     "l"(src + (in ? (y0 + row) * row_stride : 0) + c), "r"(in ? 16 : 0)
+                     : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // s[i][j] = a_(4 ty + i) . b_(tx + 16 j)
 template <int D>
-__device__ __forceinline__ void scores(const float *a, const float *b, float (&s)[4][4]) {
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+__device__ __forceinline__ void scores(const float *a, const float *b, int ty, float (&s)[4][4]) {
+    const int tx = threadIdx.x % 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -64,8 +74,8 @@ __device__ __forceinline__ void scores(const float *a, const float *b, float (&s
 
 // acc[i][..] += sum_k p[4 ty + i][k] b_k over the columns 4 tx + 64 c.  GUARD: keys of weight zero take no part.
 template <int D, bool GUARD>
-__device__ __forceinline__ void add_rows(const float *p, const float *b, float (&acc)[4][D / 16]) {
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+__device__ __forceinline__ void add_rows(const float *p, const float *b, int ty, float (&acc)[4][D / 16]) {
+    const int tx = threadIdx.x % 16;
 #pragma unroll 2
     for (int k = 0; k < BS; k += 4) {
         float4 w[4];
@@ -125,27 +135,29 @@ struct SimtArgs {
     float tau;
 };
 
-// 64 query rows of one head.
+// ROWS query rows of one head.
 struct Block {
     int a, n, i0, c0;  // first row of the sequence, its length, the block's first row in it, its first core row
     int h, kv;
 };
+template <int ROWS>
 __device__ __forceinline__ bool query_block(const SimtArgs &p, Block &b) {
+    constexpr int PER = PACK_TILE / ROWS;
     const int64_t item = blockIdx.x / p.Hq;
-    if (item >= 2ll * plan_counts(p.plan).y) return false;
-    const int4 e = p.plan.tiles[item / 2];
+    if (item >= static_cast<int64_t>(PER) * plan_counts(p.plan).y) return false;
+    const int4 e = p.plan.tiles[item / PER];
     b.a = e.x, b.n = e.y, b.c0 = e.w;
-    b.i0 = e.z * PACK_TILE + (1 - static_cast<int>(item % 2)) * BS;
+    b.i0 = e.z * PACK_TILE + (PER - 1 - static_cast<int>(item % PER)) * ROWS;
     b.h = blockIdx.x % p.Hq;
     b.kv = b.h / (p.Hq / p.Hkv);
     return b.i0 < b.n;
 }
 
-// The key tiles that 64 query rows see: cores, then the band from the first row's window on.
+// The key tiles that `rows` query rows see: cores, then the band from the first row's window on.
 struct Keys {
     int cores, lo, tiles, end;
-    __device__ __forceinline__ Keys(const Plan &p, const Block &b) {
-        const int last = min(b.i0 + BS, b.n) - 1;
+    __device__ __forceinline__ Keys(const Plan &p, const Block &b, int rows) {
+        const int last = min(b.i0 + rows, b.n) - 1;
         cores = visible_cores(last, p.w, p.g);
         lo = window_start(b.i0, p.w, p.g, p.window_mode);
         end = last + 1;
@@ -160,50 +172,82 @@ struct Keys {
     }
 };
 
-__device__ __forceinline__ bool sees(const Plan &p, int i, bool core, int key) {
-    return core ? key < visible_cores(i, p.w, p.g) : key >= window_start(i, p.w, p.g, p.window_mode) && key <= i;
-}
+// What row i sees: the cores below `cores`, and the tokens from `start` to i.
+struct Sight {
+    int i, cores, start;
+    __device__ __forceinline__ Sight() {}
+    __device__ __forceinline__ Sight(const Plan &p, int row)
+        : i(row), cores(visible_cores(row, p.w, p.g)), start(window_start(row, p.w, p.g, p.window_mode)) {}
+    __device__ __forceinline__ bool sees(bool core, int key) const { return core ? key < cores : key >= start && key <= i; }
+};
 
-template <int D>
-__global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArgs p) {
+// GROUPS: groups of threads that take the key tiles in turn, each with its own running maximum, sum and output,
+// which are joined at the end (few blocks: the chain of tiles is what takes the time).
+template <int D, int ROWS, int GROUPS>
+__global__ void __launch_bounds__(ROWS * 4 * GROUPS) attn_packed_kernel(const SimtArgs p) {
+    constexpr int THREADS = ROWS * 4;
+    const int group = threadIdx.x / THREADS;
     extern __shared__ float4 smem4[];
-    float *const sQ = reinterpret_cast<float *>(smem4), *const sK = sQ + TILE_FLOATS<D>, *const sP = sK + TILE_FLOATS<D>;
+    float *const sQ = reinterpret_cast<float *>(smem4), *const sK = sQ + ROWS * PITCH<D> + group * (2 * TILE_FLOATS<D> + ROWS * SP),
+                *const sV = sK + TILE_FLOATS<D>, *const sP = sV + TILE_FLOATS<D>;
+    auto sync = [&]() {
+        if constexpr (GROUPS == 1) __syncthreads();
+        else ptx::named_bar_sync(1 + group, THREADS);
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     Block b;
-    if (!query_block(p, b)) return;
-    const Keys keys(p.plan, b);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    load_rows<D>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n);
+    if (!query_block<ROWS>(p, b)) return;
+    const Keys keys(p.plan, b, ROWS);
+    const int ty = threadIdx.x % THREADS / 16, tx = threadIdx.x % 16;
     const float *kc = p.Kc + (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D, *vc = p.Vc + (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D;
+    auto copy_k = [&](int t) {
+        int y0, stop;
+        const bool core = t < keys.tiles && keys.at(t, y0, stop);
+        if (t >= keys.tiles) y0 = 0, stop = 0;
+        if (core) copy_rows<D, THREADS>(sK, kc, D, y0, stop, t < keys.tiles ? BS : 0);
+        else copy_rows<D, THREADS>(sK, p.K.at(b.kv, b.a), p.K.row, y0, stop, t < keys.tiles ? BS : 0);
+    };
+    auto copy_v = [&](int t) {
+        int y0, stop;
+        const bool core = t < keys.tiles && keys.at(t, y0, stop);
+        if (t >= keys.tiles) y0 = 0, stop = 0;
+        if (core) copy_rows<D, THREADS>(sV, vc, D, y0, stop, t < keys.tiles ? BS : 0);
+        else copy_rows<D, THREADS>(sV, p.V.at(b.kv, b.a), p.V.row, y0, stop, t < keys.tiles ? BS : 0);
+    };
+    // every group copies the queries (the same values to the same place), so that it waits for its own copies alone
+    copy_rows<D, THREADS>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n, ROWS);
+    copy_k(group);
+    copy_v(group);
     float m[4], l[4], o[4][D / 16];
+    Sight sight[4];
+    const Sight top_row(p.plan, b.i0), last_row(p.plan, min(b.i0 + ROWS, b.n) - 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        sight[i] = Sight(p.plan, b.i0 + ty * 4 + i);
         m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
     }
     const float scale = p.tau * LOG2E;
-    for (int t = 0; t < keys.tiles; ++t) {
+    for (int t = group; t < keys.tiles; t += GROUPS) {
         int y0, stop;
         const bool core = keys.at(t, y0, stop);
-        __syncthreads();
-        if (core) load_rows<D>(sK, kc, D, y0, stop);
-        else load_rows<D>(sK, p.K.at(b.kv, b.a), p.K.row, y0, stop);
-        __syncthreads();
+        copies_wait<1>();  // all but the values
+        sync();
         float s[4][4];
-        scores<D>(sQ, sK, s);
+        scores<D>(sQ, sK, ty, s);
+        sync();
+        copy_k(t + GROUPS);
         // whether every row sees every key of the tile
-        const bool whole = y0 + BS <= stop && sees(p.plan, b.i0, core, y0) && sees(p.plan, b.i0, core, y0 + BS - 1) &&
-                           sees(p.plan, min(b.i0 + BS, b.n) - 1, core, y0);
+        const bool whole = y0 + BS <= stop && top_row.sees(core, y0) && top_row.sees(core, y0 + BS - 1) && last_row.sees(core, y0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = b.i0 + ty * 4 + i;
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = y0 + tx + 16 * j;
-                s[i][j] = whole || (key < stop && sees(p.plan, row, core, key)) ? s[i][j] * scale : -INFINITY;
+                s[i][j] = whole || (key < stop && sight[i].sees(core, key)) ? s[i][j] * scale : -INFINITY;
                 top = fmaxf(top, s[i][j]);
             }
 #pragma unroll
@@ -222,12 +266,39 @@ __global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArg
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) o[i][c] *= f;
         }
+        copies_wait<1>();  // all but the next keys
+        sync();
+        if (whole) add_rows<D, false>(sP, sV, ty, o);
+        else add_rows<D, true>(sP, sV, ty, o);
+        sync();
+        copy_v(t + GROUPS);
+    }
+    if constexpr (GROUPS > 1) {
+        // group 0 joins: the others leave (m, l, o) where their keys were, a thread's values together
+        copies_wait<0>();
+        float *const mine = sK + (threadIdx.x % THREADS) * (8 + D / 4 + 1);
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mine[i] = m[i], mine[4 + i] = l[i];
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) mine[8 + i * (D / 16) + c] = o[i][c];
+            }
+        }
         __syncthreads();
-        if (core) load_rows<D>(sK, vc, D, y0, stop);
-        else load_rows<D>(sK, p.V.at(b.kv, b.a), p.V.row, y0, stop);
-        __syncthreads();
-        if (whole) add_rows<D, false>(sP, sK, o);
-        else add_rows<D, true>(sP, sK, o);
+        if (group > 0) return;
+        for (int k = 1; k < GROUPS; ++k) {
+            const float *const other = mine + k * (2 * TILE_FLOATS<D> + ROWS * SP);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float mn = fmaxf(m[i], other[i]), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[i] - ref), g = exp2f(other[i] - ref);
+                m[i] = mn;
+                l[i] = l[i] * f + other[4 + i] * g;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) o[i][c] = o[i][c] * f + other[8 + i * (D / 16) + c] * g;
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -244,25 +315,42 @@ __global__ void __launch_bounds__(SIMT_THREADS) attn_packed_kernel(const SimtArg
     }
 }
 
-// dQ of 64 query rows: dQ = tau sum dS k (+ the pooling's share of a group-last row).
-template <int D>
-__global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs p) {
+// dQ of ROWS query rows: dQ = tau sum dS k (+ the pooling's share of a group-last row).
+template <int D, int ROWS, int GROUPS>
+__global__ void __launch_bounds__(ROWS * 4 * GROUPS) packed_dq_kernel(const SimtArgs p) {
+    constexpr int THREADS = ROWS * 4;
+    const int group = threadIdx.x / THREADS;
+    auto sync = [&]() {
+        if constexpr (GROUPS == 1) __syncthreads();
+        else ptx::named_bar_sync(1 + group, THREADS);
+    };
     extern __shared__ float4 smem4[];
-    float *const sQ = reinterpret_cast<float *>(smem4), *const sO = sQ + TILE_FLOATS<D>, *const sK = sO + TILE_FLOATS<D>,
+    float *const sQ = reinterpret_cast<float *>(smem4), *const sO = sQ + ROWS * PITCH<D>,
+                *const sK = sO + ROWS * PITCH<D> + group * (2 * TILE_FLOATS<D> + ROWS * SP),
                 *const sV = sK + TILE_FLOATS<D>, *const sP = sV + TILE_FLOATS<D>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     Block b;
-    if (!query_block(p, b)) return;
-    const Keys keys(p.plan, b);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    load_rows<D>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n);
-    load_rows<D>(sO, p.dO.at(b.h, b.a), p.dO.row, b.i0, b.n);
+    if (!query_block<ROWS>(p, b)) return;
+    const Keys keys(p.plan, b, ROWS);
+    const int ty = threadIdx.x % THREADS / 16, tx = threadIdx.x % 16;
     const int64_t core0 = (static_cast<int64_t>(b.kv) * p.plan.G + b.c0) * D;
+    auto copy_keys = [&](float *dst, const float *cores, const Rows<const float> &raw, int t) {
+        int y0 = 0, stop = 0;
+        const bool core = t < keys.tiles && keys.at(t, y0, stop);
+        if (core) copy_rows<D, THREADS>(dst, cores + core0, D, y0, stop, BS);
+        else copy_rows<D, THREADS>(dst, raw.at(b.kv, b.a), raw.row, y0, stop, t < keys.tiles ? BS : 0);
+    };
+    copy_rows<D, THREADS>(sQ, p.Q.at(b.h, b.a), p.Q.row, b.i0, b.n, ROWS);
+    copy_rows<D, THREADS>(sO, p.dO.at(b.h, b.a), p.dO.row, b.i0, b.n, ROWS);
+    copy_keys(sV, p.Vc, p.V, group);
+    copy_keys(sK, p.Kc, p.K, group);
     float lse[4], d[4], dq[4][D / 16];
+    Sight sight[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = b.i0 + ty * 4 + i;
+        sight[i] = Sight(p.plan, row);
         const int64_t at = static_cast<int64_t>(b.h) * p.plan.T + b.a + row;
         lse[i] = row < b.n ? p.LSE[at] * LOG2E : 0.f;
         d[i] = row < b.n ? p.w.D[at] : 0.f;
@@ -270,33 +358,49 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dq_kernel(const SimtArgs 
         for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
     }
     const float scale = p.tau * LOG2E;
-    for (int t = 0; t < keys.tiles; ++t) {
+    for (int t = group; t < keys.tiles; t += GROUPS) {
         int y0, stop;
         const bool core = keys.at(t, y0, stop);
-        __syncthreads();
-        if (core) {
-            load_rows<D>(sK, p.Kc + core0, D, y0, stop);
-            load_rows<D>(sV, p.Vc + core0, D, y0, stop);
-        } else {
-            load_rows<D>(sK, p.K.at(b.kv, b.a), p.K.row, y0, stop);
-            load_rows<D>(sV, p.V.at(b.kv, b.a), p.V.row, y0, stop);
-        }
-        __syncthreads();
+        copies_wait<1>();  // all but the keys
+        sync();
         float s[4][4], g[4][4];
-        scores<D>(sQ, sK, s);
-        scores<D>(sO, sV, g);
+        scores<D>(sO, sV, ty, g);
+        sync();
+        copy_keys(sV, p.Vc, p.V, t + GROUPS);
+        copies_wait<1>();  // all but the next values
+        sync();
+        scores<D>(sQ, sK, ty, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = b.i0 + ty * 4 + i;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = y0 + tx + 16 * j;
-                const bool seen = row < b.n && key < stop && sees(p.plan, row, core, key);
+                const bool seen = row < b.n && key < stop && sight[i].sees(core, key);
                 sP[(ty * 4 + i) * SP + tx + 16 * j] = seen ? exp2f(fmaf(s[i][j], scale, -lse[i])) * (g[i][j] - d[i]) : 0.f;
             }
         }
+        sync();
+        add_rows<D, false>(sP, sK, ty, dq);
+        sync();
+        copy_keys(sK, p.Kc, p.K, t + GROUPS);
+    }
+    if constexpr (GROUPS > 1) {
+        copies_wait<0>();
+        float *const mine = sK + (threadIdx.x % THREADS) * (D / 4 + 1);
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) mine[i * (D / 16) + c] = dq[i][c];
+        }
         __syncthreads();
-        add_rows<D, false>(sP, sK, dq);
+        if (group > 0) return;
+        for (int k = 1; k < GROUPS; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) dq[i][c] += mine[k * (2 * TILE_FLOATS<D> + ROWS * SP) + i * (D / 16) + c];
     }
     const int seen = p.cores ? seen_cores(b.n, p.plan.w, p.plan.g) : 0;
 #pragma unroll
@@ -354,54 +458,67 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dkv_kernel(const SimtArgs
     }
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int64_t core0 = (static_cast<int64_t>(kv) * pl.G + e.w) * D;
-    if (CORE) {
-        load_rows<D>(sK, p.Kc + core0, D, y0, nk);
-        load_rows<D>(sV, p.Vc + core0, D, y0, nk);
-    } else {
-        load_rows<D>(sK, p.K.at(kv, a), p.K.row, y0, nk);
-        load_rows<D>(sV, p.V.at(kv, a), p.V.row, y0, nk);
-    }
+    copy_rows<D, SIMT_THREADS>(sK, CORE ? p.Kc + core0 : p.K.at(kv, a), CORE ? D : p.K.row, y0, nk, BS);
+    copy_rows<D, SIMT_THREADS>(sV, CORE ? p.Vc + core0 : p.V.at(kv, a), CORE ? D : p.V.row, y0, nk, BS);
+    // the query tiles of all heads, one after the other
+    const int per_head = max(q1 - q0, 0), steps = per_head * r;
+    auto copy_q = [&](float *dst, const Rows<const float> &src, int x) {
+        const bool in = x < steps;
+        const int h = kv * r + (in ? x / per_head : 0), i0 = in ? (q0 + x % per_head) * BS : 0;
+        copy_rows<D, SIMT_THREADS>(dst, src.at(h, a), src.row, i0, n, in ? BS : 0);
+    };
+    copy_q(sO, p.dO, 0);
+    copy_q(sQ, p.Q, 0);
     float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
     const float scale = p.tau * LOG2E;
-    for (int h = kv * r; h < (kv + 1) * r; ++h) {
-        for (int q = q0; q < q1; ++q) {
-            const int i0 = q * BS;
-            __syncthreads();
-            load_rows<D>(sQ, p.Q.at(h, a), p.Q.row, i0, n);
-            load_rows<D>(sO, p.dO.at(h, a), p.dO.row, i0, n);
-            __syncthreads();
-            float s[4][4], g[4][4];
-            scores<D>(sQ, sK, s);
-            scores<D>(sO, sV, g);
+    for (int x = 0; x < steps; ++x) {
+        const int h = kv * r + x / per_head, i0 = (q0 + x % per_head) * BS;
+        float lse[4], d[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = i0 + ty * 4 + i;
-                const int64_t at = static_cast<int64_t>(h) * pl.T + a + row;
-                const float lse = row < n ? p.LSE[at] * LOG2E : 0.f, d = row < n ? p.w.D[at] : 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = y0 + tx + 16 * j;
-                    const bool seen = row < n && key < nk && sees(pl, row, CORE, key);
-                    s[i][j] = seen ? exp2f(fmaf(s[i][j], scale, -lse)) : 0.f;
-                    g[i][j] = seen ? s[i][j] * (g[i][j] - d) : 0.f;
-                    sP[(ty * 4 + i) * SP + tx + 16 * j] = s[i][j];
-                }
-            }
-            __syncthreads();
-            add_columns<D>(sP, sO, dv);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sP[(ty * 4 + i) * SP + tx + 16 * j] = g[i][j];
-            __syncthreads();
-            add_columns<D>(sP, sQ, dk);
+        for (int i = 0; i < 4; ++i) {
+            const int row = i0 + ty * 4 + i;
+            const int64_t at = static_cast<int64_t>(h) * pl.T + a + row;
+            lse[i] = row < n ? p.LSE[at] * LOG2E : 0.f;
+            d[i] = row < n ? p.w.D[at] : 0.f;
         }
+        copies_wait<1>();  // all but the queries
+        __syncthreads();
+        float s[4][4], g[4][4];
+        scores<D>(sO, sV, ty, g);
+        copies_wait<0>();
+        __syncthreads();
+        scores<D>(sQ, sK, ty, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = i0 + ty * 4 + i;
+            const Sight sight(pl, row);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = y0 + tx + 16 * j;
+                const bool seen = row < n && key < nk && sight.sees(CORE, key);
+                s[i][j] = seen ? exp2f(fmaf(s[i][j], scale, -lse[i])) : 0.f;
+                g[i][j] = seen ? s[i][j] * (g[i][j] - d[i]) : 0.f;
+                sP[(ty * 4 + i) * SP + tx + 16 * j] = s[i][j];
+            }
+        }
+        __syncthreads();
+        add_columns<D>(sP, sO, dv);
+        __syncthreads();
+        copy_q(sO, p.dO, x + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sP[(ty * 4 + i) * SP + tx + 16 * j] = g[i][j];
+        __syncthreads();
+        add_columns<D>(sP, sQ, dk);
+        __syncthreads();
+        copy_q(sQ, p.Q, x + 1);
     }
+    copies_wait<0>();  // without query rows, keys and values are still under way
     const int seen = !CORE && p.cores ? seen_cores(n, pl.w, pl.g) : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -440,12 +557,12 @@ __global__ void __launch_bounds__(SIMT_THREADS) packed_dkv_kernel(const SimtArgs
 }
 
 template <typename K>
-cudaError_t start(K kernel, int64_t blocks, int splits, int floats, cudaStream_t stream, const SimtArgs &a) {
+cudaError_t start(K kernel, int64_t blocks, int splits, int threads, int floats, cudaStream_t stream, const SimtArgs &a) {
     if (blocks > 0x7fffffff) return cudaErrorNotSupported;
     const int smem = floats * 4;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return start_dependent(kernel, dim3(static_cast<unsigned>(blocks), splits), SIMT_THREADS, smem, stream, a);
+    return start_dependent(kernel, dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream, a);
 }
 
 template <int D>
@@ -463,19 +580,26 @@ cudaError_t launch(const PackedArgs &p, const PackedBwdSpace *w, int part, cudaS
     a.cores = p.Kc != nullptr;
     a.tau = p.scale;
     constexpr int F = TILE_FLOATS<D>, S = BS * SP;
-    const int64_t rows = 2ll * p.plan.max_tiles;
+    // Few blocks: of 32 query rows, in two groups.  fp32, us, 64 rows against 32 in two groups: 1500 tokens of 4 heads
+    // 32 and 25, 1024 of 8 heads 58 and 43, a training step of 2048 of 8 heads 846 and 702.
+    const int64_t heads64 = static_cast<int64_t>(PACK_TILE / 64) * p.plan.max_tiles * p.Hq;
+    const bool small = heads64 < SMALL_BLOCKS * device_sms();
     if (w == nullptr) {
         a.out = rows_of<float>(p.O);
-        return start(attn_packed_kernel<D>, rows * p.Hq, 1, 2 * F + S, stream, a);
+        if (small) return start(attn_packed_kernel<D, 32, SMALL_GROUPS>, 2 * heads64, 1, 128 * SMALL_GROUPS, F / 2 + SMALL_GROUPS * (2 * F + S / 2), stream, a);
+        return start(attn_packed_kernel<D, 64, 1>, heads64, 1, 256, 3 * F + S, stream, a);
     }
     a.w = *w;
     a.dO = rows_of<const float>(p.dO);
     a.out = rows_of<float>(p.dQ);
     a.dK = rows_of<float>(p.dK);
     a.dV = rows_of<float>(p.dV);
-    if (part == 0) return start(packed_dkv_kernel<D, true>, 2ll * p.plan.max_cores * p.Hkv, w->splits, 4 * F + S, stream, a);
-    if (part == 1) return start(packed_dq_kernel<D>, rows * p.Hq, 1, 4 * F + S, stream, a);
-    return start(packed_dkv_kernel<D, false>, rows * p.Hkv, 1, 4 * F + S, stream, a);
+    if (part == 0) return start(packed_dkv_kernel<D, true>, 2ll * p.plan.max_cores * p.Hkv, w->splits, SIMT_THREADS, 4 * F + S, stream, a);
+    if (part == 1) {
+        if (small) return start(packed_dq_kernel<D, 32, SMALL_GROUPS>, 2 * heads64, 1, 128 * SMALL_GROUPS, F + SMALL_GROUPS * (2 * F + S / 2), stream, a);
+        return start(packed_dq_kernel<D, 64, 1>, heads64, 1, 256, 4 * F + S, stream, a);
+    }
+    return start(packed_dkv_kernel<D, false>, 2ll * p.plan.max_tiles * p.Hkv, 1, SIMT_THREADS, 4 * F + S, stream, a);
 }
 
 }  // namespace
