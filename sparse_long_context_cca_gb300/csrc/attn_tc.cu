@@ -236,6 +236,11 @@ __device__ __forceinline__ Item make_item(const ParamsOf<PACKED> &p, int k, [[ma
     return it;
 }
 
+template <bool PACKED>
+__device__ __forceinline__ int item_at(int round) {
+    return PACKED ? item_of_round(round) : static_cast<int>(blockIdx.x + round * gridDim.x);
+}
+
 // Parity of the FULL barrier of the ring slot holding K for ring index u (u even).
 // Only K slots complete a FULL barrier (the tile's V copy completes the same one),
 // and with NS odd an even u reaches each slot once every 2*NS indices.
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t u = 0;  // ring loads issued so far
             int n_iter = 0;
             bool ok = true;
-            for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x, ++n_iter) {
+            for (int k; ok && (k = item_at<PACKED>(n_iter)) < n_items; ++n_iter) {
                 const Item it = make_item<PACKED>(p, k, begin);
                 if (!ptx::wait_bounded(bar(B_QFREE), (n_iter & 1) ^ 1, abort_flag, lim)) break;
                 if (!p.skip_q_load) {
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t dk0 = ptx::smem_desc_sw128(base + OFF_RING, 16, 1024);
             const uint64_t dv0 = ptx::smem_desc_sw128(base + OFF_RING, HALF_BYTES, 1024);
             bool ok = true;
-            for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x, ++n_iter) {
+            for (int k; ok && (k = item_at<PACKED>(n_iter)) < n_items; ++n_iter) {
                 const Item it = make_item<PACKED>(p, k, begin);
                 if (!wwait(bar(B_QFULL), n_iter & 1)) break;
                 int s_left = half_count(it.hA) + half_count(it.hB);
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         bool ok = true;
         [[maybe_unused]] uint32_t ubase = 0;  // ring loads before this item (PACKED)
         [[maybe_unused]] volatile int *const mark = reinterpret_cast<volatile int *>(gbase + L::OFF_MARK) + 2 * h;
-        for (int k = blockIdx.x; ok && k < n_items; k += gridDim.x) {
+        for (int round = 0, k; ok && (k = item_at<PACKED>(round)) < n_items; ++round) {
             const Item it = make_item<PACKED>(p, k, begin);
             const Half x = h ? it.hB : it.hA;
             [[maybe_unused]] const uint32_t u0 = ubase;

@@ -12,9 +12,9 @@
 //
 //  dq kernel, one 128-row query tile of one (b, h) per CTA, over the same key
 //  tiles as the forward (cores, then the band):
-//     S = Q K^T, dP = dO V^T (both SS, fp32 in TMEM)  ->  dS (bf16, over dP)
+//     S = Q K^T, dP = dO V^T (both SS, fp32 in TMEM)  ->  dS (bf16, over S)
 //     dQ += dS K  (A = dS in TMEM, B = K tile read MN-major)
-//  TMEM: S | dP | dP | dQ.  K/V tiles are double-buffered: the next tile's copy is
+//  TMEM: S | dP | dQ.  K/V tiles are double-buffered: the next tile's copy is
 //  in flight while this one is processed.
 //
 //  dkv kernel, one 128-key tile (raw tokens or cores) of one (b, kv) per CTA,
@@ -24,15 +24,6 @@
 //  TMEM: S^T | dP^T | dK | dV.  Q/dO tiles are double-buffered.
 //
 // The pooling backward (bwd.cu) then adds the paths through the core tokens.
-// PACKED: the same kernels over packed sequences (packed.cuh).  A CTA's rows come from the batch's plan,
-// tensors are read and written by strides, D is there already, and gradients leave once, in bf16, from the
-// thread that holds the row (rows of other sequences in a tile must stay as they are, so tiles are not stored
-// whole): dQ with the pooling's share of a group-last row, dK and dV of raw tokens with theirs.  Rows of a tile
-// behind the sequence's end belong to the next one and would reach sums over rows as 0 * NaN: the producer
-// waits for such a tile (one at the end of a sequence) and sets them to zero before it hands it over.  The
-// query rows of a core tile are split over CTAs, whose sums are added up in order later.  d = 64 is built
-// for packed sequences alone.
-//
 // Every wait is bounded and a time-out sets the CTA's abort flag, which ends every
 // other wait at once: the issuer then waits (bounded) for the MMAs it has issued,
 // the producer for its copies in flight, TMEM is freed and CCA_ERR_TIMEOUT is
@@ -43,10 +34,8 @@
 #include <stdint.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "internal.h"
-#include "packed.cuh"
 #include "sm100_ptx.cuh"
 #include "tma_host.h"
 #include "visibility.cuh"
@@ -59,8 +48,11 @@ extern int g_skip_q_load;
 namespace {
 
 constexpr int BT = 128;  // rows per tile (queries or keys)
-constexpr uint32_t HALF_BYTES = BT * 64 * 2;  // 64 columns of a tile, as one swizzled box
+constexpr int HD = 128;
+constexpr uint32_t TILE_BYTES = BT * HD * 2;
+constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;
 constexpr uint32_t IDESC_SS = ptx::idesc_bf16_f32(128, 128, 0, 0);  // K-major A and B
+constexpr uint32_t IDESC_TS = ptx::idesc_bf16_f32(128, 128, 0, 1);  // A in TMEM, B MN-major
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int32_t STATUS_TIMEOUT = -4;
 
@@ -79,15 +71,6 @@ struct BwdTcParams {
     unsigned long long wait_limit_ns;
     int skip_loads;  // test hook: issue no copies, so the first wait runs out
 };
-struct PackedBwdParams : BwdTcParams {
-    Plan plan;
-    Rows<__nv_bfloat16> rdQ, rdK, rdV;
-    PackedBwdSpace space;
-    int core;  // dkv: core tiles (else raw ones)
-    int cores;  // whether any core is seen
-};
-template <bool PACKED>
-using ParamsOf = typename std::conditional<PACKED, PackedBwdParams, BwdTcParams>::type;
 
 __device__ __forceinline__ int lo_of(int i, int w) { return window_lo(i, w); }
 __device__ __forceinline__ int win_of(const BwdTcParams &p, int i) { return window_start(i, p.w, p.g, p.window_mode); }
@@ -96,114 +79,9 @@ __device__ __forceinline__ float bf(uint32_t w, int hi) {
     return __uint_as_float(hi ? (w & 0xffff0000u) : (w << 16));
 }
 
-template <int HD>
 __device__ __forceinline__ void load_tile(const void *map, uint32_t bar, uint32_t dst, int y, int z) {
-#pragma unroll
-    for (int x = 0; x < HD / 64; ++x) ptx::tma_load_3d(map, bar, dst + x * HALF_BYTES, 64 * x, y, z);
-}
-
-// load_tile by a whole warp, with the tile's rows from `rows` on set to zero before it is handed over on
-// `full` (an arrival like that of a plain tile, whose copies complete the phase).  `own` is a barrier for
-// these copies alone, `phase` its phase.  false: the wait ran out.
-template <int HD>
-__device__ __forceinline__ bool load_cut_tile(const void *map, uint32_t full, uint32_t own, uint32_t &phase, uint32_t dst, int y, int z,
-                                              int rows, volatile int *abort_flag, uint64_t lim) {
-    const int lane = threadIdx.x & 31;
-    if (rows >= BT) {
-        if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(full, BT * HD * 2);
-            load_tile<HD>(map, full, dst, y, z);
-        }
-        __syncwarp();
-        return true;
-    }
-    if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(own, BT * HD * 2);
-        load_tile<HD>(map, own, dst, y, z);
-    }
-    __syncwarp();
-    // the copies land in any case: the wait that may give up is followed by one that only time ends
-    const bool ok = __all_sync(0xffffffffu, ptx::wait_bounded(own, phase & 1, abort_flag, lim));
-    if (!ok) {
-        volatile int never = 0;
-        ptx::wait_bounded(own, phase & 1, &never, lim);
-        return false;
-    }
-    ++phase;
-    for (int i = rows * 8 + lane; i < BT * 8; i += 32)
-#pragma unroll
-        for (int x = 0; x < HD / 64; ++x) ptx::st_shared_v4(dst + x * HALF_BYTES + i * 16, 0.f, 0.f, 0.f, 0.f);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(full);
-    return true;
-}
-
-// This thread's COLS fp32 sums at TMEM address `taddr` times `scale`, plus xs * x + ys * y (rows of fp32, either
-// may be nullptr), to a row of bf16.
-template <int COLS>
-__device__ __forceinline__ void store_row_bf16(uint32_t taddr, float scale, bool zero, const float *x, float xs, const float *y,
-                                               float ys, __nv_bfloat16 *out, bool valid) {
-#pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
-        uint32_t v[32];
-        if (!zero) {
-            ptx::tmem_ld32(taddr + c, v);
-            ptx::tmem_wait_ld(v);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0u;
-        }
-        if (!valid) continue;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[8 * q + k]) * scale;
-#pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-                if (x != nullptr) {
-                    const float4 a = *reinterpret_cast<const float4 *>(x + c + 8 * q + k);
-                    f[k] = fmaf(xs, a.x, f[k]), f[k + 1] = fmaf(xs, a.y, f[k + 1]);
-                    f[k + 2] = fmaf(xs, a.z, f[k + 2]), f[k + 3] = fmaf(xs, a.w, f[k + 3]);
-                }
-                if (y != nullptr) {
-                    const float4 a = *reinterpret_cast<const float4 *>(y + c + 8 * q + k);
-                    f[k] = fmaf(ys, a.x, f[k]), f[k + 1] = fmaf(ys, a.y, f[k + 1]);
-                    f[k + 2] = fmaf(ys, a.z, f[k + 2]), f[k + 3] = fmaf(ys, a.w, f[k + 3]);
-                }
-            }
-            *reinterpret_cast<uint4 *>(out + c + 8 * q) = make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]),
-                                                                     ptx::pack_bf16x2(f[4], f[5]), ptx::pack_bf16x2(f[6], f[7]));
-        }
-    }
-}
-// The same times `scale` to a row of fp32.
-template <int COLS>
-__device__ __forceinline__ void store_row_f32(uint32_t taddr, float scale, bool zero, float *out, bool valid) {
-#pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
-        uint32_t v[32];
-        if (!zero) {
-            ptx::tmem_ld32(taddr + c, v);
-            ptx::tmem_wait_ld(v);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0u;
-        }
-        if (!valid) continue;
-#pragma unroll
-        for (int q = 0; q < 32; q += 4)
-            *reinterpret_cast<float4 *>(out + c + q) = make_float4(__uint_as_float(v[q]) * scale, __uint_as_float(v[q + 1]) * scale,
-                                                                   __uint_as_float(v[q + 2]) * scale, __uint_as_float(v[q + 3]) * scale);
-    }
-}
-
-// D = A B^T over the HD columns of two K-major tiles.
-template <int HD>
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc) {
-    if constexpr (HD == 128) ptx::mma_ss_k128_warp(d_tmem, a_desc, b_desc, IDESC_SS, 0u);
-    else ptx::mma_ss_k64_warp(d_tmem, a_desc, b_desc, IDESC_SS, 0u);
+    ptx::tma_load_3d(map, bar, dst, 0, y, z);
+    ptx::tma_load_3d(map, bar, dst + HALF_BYTES, 64, y, z);
 }
 
 // Writes this thread's 64 fp32 values (columns [64*ch, 64*ch + 64) of TMEM row `row`,
@@ -285,46 +163,37 @@ __device__ __forceinline__ void store_tile_f32(const CUtensorMap *map, uint32_t 
 // then the band).  Warp-specialised, 320 threads:
 //   warp 0      producer: Q and dO once, then K(t) into one of three stages and V(t)
 //               into one of two (TMA; K lives longer: S(t) and dQ(t) read it);
-//   warp 1      MMA issuer, per tile t:  S(t+1) = Q K(t+1)^T (once the element-wise warps have S(t) in
-//               registers), dP(t+1) = dO V(t+1)^T into the other dP buffer, then (once they have
-//               written dS(t)) dQ += dS(t) K(t);
-//   warps 2..9  element-wise: P = 2^(S tau log2e - LSE) as soon as S(t) is there, then
-//               dS = P (dP - D) as bf16 over dP.
+//   warp 1      MMA issuer, per tile t:  S(t+1) = Q K(t+1)^T into the other S buffer,
+//               then (once the element-wise warps have written dS(t)) dQ += dS(t) K(t),
+//               then dP(t+1) = dO V(t+1)^T;
+//   warps 2..9  element-wise: P = 2^(S tau log2e - LSE) as soon as S(t) is there (while
+//               dP(t) is still being computed), then dS = P (dP - D) as bf16 over S.
 //               Warps w and w + 4 share TMEM lanes 32*(w%4)..+31 (the query rows) and
 //               split the 128 key columns, 64 each.  Each also computes D = dO . O of its
 //               row (the first of the pair stores it for the dK/dV kernel).
-// TMEM: S | dP0 | dP1 | dQ, 128 columns each.  S needs one buffer, as its warps hold P in registers; with
-// two of dP both products of the next tile run while this tile's dS is formed, and only dQ waits for it.
+// TMEM: S0 | S1 | dP | dQ, 128 columns each.  S is double-buffered so that the tensor
+// pipe computes the next tile's S while this tile's dS is formed.
 constexpr int DQ_THREADS = 320;
 constexpr int DQ_KST = 3, DQ_VST = 2;
-constexpr int QB_QD = 0, QB_FULLK = 1, QB_EMPTYK = 4, QB_FULLV = 7, QB_EMPTYV = 9, QB_SFULL = 11, QB_SREAD = 12,
-              QB_DPFULL = 13, QB_PFULL = 15, QB_DONE = 16, QB_DRAIN = 17, QB_CUT = 18;
-constexpr int DQ_NBARS = 19;
-template <int HD>
-struct DqLayout {
-    static constexpr uint32_t TILE_BYTES = BT * HD * 2;
-    static constexpr uint32_t OFF_K = 2 * TILE_BYTES;  // after Q, dO
-    static constexpr uint32_t OFF_V = OFF_K + DQ_KST * TILE_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_V + DQ_VST * TILE_BYTES;
-    static constexpr uint32_t OFF_TMEM = OFF_BAR + DQ_NBARS * 8;
-    static constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
-    static constexpr uint32_t OFF_DPART = OFF_BAR + 256;           // 2 x 128 partial sums of D
-    static constexpr uint32_t SMEM = OFF_DPART + 2 * BT * 4 + 1024;  // + slack for the 1024-byte alignment
-    static_assert(OFF_ABORT + 4 <= OFF_DPART, "control words overlap the D staging");
-    static_assert(SMEM <= 232448, "shared memory budget");
-};
+constexpr uint32_t DQ_OFF_K = 2 * TILE_BYTES;  // after Q, dO
+constexpr uint32_t DQ_OFF_V = DQ_OFF_K + DQ_KST * TILE_BYTES;
+constexpr uint32_t DQ_OFF_BAR = DQ_OFF_V + DQ_VST * TILE_BYTES;
+constexpr int QB_QD = 0, QB_FULLK = 1, QB_EMPTYK = 4, QB_FULLV = 7, QB_EMPTYV = 9, QB_SFULL = 11, QB_DPFULL = 13,
+              QB_PFULL = 14, QB_DONE = 15, QB_DRAIN = 16;
+constexpr int DQ_NBARS = 17;
+constexpr uint32_t DQ_OFF_TMEM = DQ_OFF_BAR + DQ_NBARS * 8;
+constexpr uint32_t DQ_OFF_ABORT = DQ_OFF_TMEM + 4;
+constexpr uint32_t DQ_OFF_DPART = DQ_OFF_BAR + 256;                // 2 x 128 partial sums of D
+constexpr uint32_t DQ_SMEM = DQ_OFF_DPART + 2 * BT * 4 + 1024;  // + slack for the 1024-byte alignment
+static_assert(DQ_OFF_ABORT + 4 <= DQ_OFF_DPART, "control words overlap the D staging");
+static_assert(DQ_SMEM <= 232448, "shared memory budget");
 static_assert(DQ_KST >= 2, "the fp32 dQ tile is staged over the first two K stages");
 
-template <bool PACKED, int HD>
 __global__ void __launch_bounds__(DQ_THREADS, 1)
     bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmKc, const __grid_constant__ CUtensorMap tmVc,
-                     const __grid_constant__ CUtensorMap tmdQ, const __grid_constant__ ParamsOf<PACKED> p) {
-    using L = DqLayout<HD>;
-    constexpr uint32_t TILE_BYTES = L::TILE_BYTES, DQ_OFF_K = L::OFF_K, DQ_OFF_V = L::OFF_V, DQ_OFF_BAR = L::OFF_BAR,
-                       DQ_OFF_TMEM = L::OFF_TMEM, DQ_OFF_ABORT = L::OFF_ABORT, DQ_OFF_DPART = L::OFF_DPART;
-    constexpr uint32_t IDESC_TS = ptx::idesc_bf16_f32(128, HD, 0, 1);  // A in TMEM, B MN-major
+                     const __grid_constant__ CUtensorMap tmdQ, const BwdTcParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t r0 = ptx::smem_addr(smem_raw);
     const uint32_t base = (r0 + 1023u) & ~1023u;
@@ -337,23 +206,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     const uint64_t lim = p.wait_limit_ns;
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    // the tile's rows [i0, i1] of a sequence of n, which starts at row0 of the tensors (its cores at core0)
-    int qt, bh, kvz, n, row0 = 0, core0 = 0;
-    if constexpr (PACKED) {
-        const int item = static_cast<int>(blockIdx.x / p.Hq);
-        if (item >= plan_counts(p.plan).y) return;
-        const int4 e = p.plan.tiles[item];  // heaviest tiles first
-        bh = static_cast<int>(blockIdx.x % p.Hq);
-        kvz = bh / (p.Hq / p.Hkv);
-        row0 = e.x, n = e.y, qt = e.z, core0 = e.w;
-    } else {
-        const int BH = p.B * p.Hq, n_qt = (p.N + BT - 1) / BT;
-        qt = n_qt - 1 - static_cast<int>(blockIdx.x / BH);  // heaviest tiles first
-        bh = static_cast<int>(blockIdx.x % BH);
-        kvz = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / (p.Hq / p.Hkv);
-        n = p.N;
-    }
-    const int i0 = qt * BT, i1 = min(i0 + BT - 1, n - 1);
+    const int BH = p.B * p.Hq, n_qt = (p.N + BT - 1) / BT;
+    const int qt = n_qt - 1 - static_cast<int>(blockIdx.x / BH);  // heaviest tiles first
+    const int bh = static_cast<int>(blockIdx.x % BH);
+    const int kvz = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / (p.Hq / p.Hkv);
+    const int i0 = qt * BT, i1 = min(i0 + BT - 1, p.N - 1);
     const int lo0 = win_of(p, i0);
     const int Tc = (lo_of(i1, p.w) / p.g + BT - 1) / BT;  // core tiles
     const int T = Tc + (i1 - lo0) / BT + 1;               // + band tiles
@@ -367,8 +224,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         ptx::prefetch_tmap(&tmVc);
         ptx::prefetch_tmap(&tmK);
         ptx::prefetch_tmap(&tmV);
-        if constexpr (!PACKED) ptx::prefetch_tmap(&tmdQ);
-        if constexpr (PACKED) ptx::mbar_init(bar(QB_CUT), 1);
+        ptx::prefetch_tmap(&tmdQ);
         ptx::mbar_init(bar(QB_QD), 1);
         for (int st = 0; st < DQ_KST; ++st) {
             ptx::mbar_init(bar(QB_FULLK + st), 1);
@@ -379,9 +235,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             ptx::mbar_init(bar(QB_EMPTYV + st), 1);
         }
         ptx::mbar_init(bar(QB_SFULL), 1);
-        ptx::mbar_init(bar(QB_SREAD), 8);  // one arrive per element-wise warp
+        ptx::mbar_init(bar(QB_SFULL + 1), 1);
         ptx::mbar_init(bar(QB_DPFULL), 1);
-        ptx::mbar_init(bar(QB_DPFULL + 1), 1);
         ptx::mbar_init(bar(QB_PFULL), 8);  // one arrive per element-wise warp
         ptx::mbar_init(bar(QB_DONE), 1);
         ptx::mbar_init(bar(QB_DRAIN), 1);
@@ -396,53 +251,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<uint32_t *>(gb + DQ_OFF_TMEM);
-    constexpr uint32_t T_DP = 128, T_DQ = 384;  // TMEM columns; S at 0, dP(t) at T_DP + 128 * (t & 1)
+    constexpr uint32_t T_DP = 256, T_DQ = 384;  // TMEM columns; S(t) at 128 * (t & 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
-        if (PACKED && !p.skip_loads) {
-            // the whole warp, for the tiles that end behind the sequence (cores, or its last tokens)
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(QB_QD), 2 * TILE_BYTES);
-                load_tile<HD>(&tmQ, bar(QB_QD), sQ, row0 + i0, bh);
-                load_tile<HD>(&tmdO, bar(QB_QD), sdO, row0 + i0, bh);
-            }
-            uint32_t cut = 0;
-            int nk = 0, nv = 0;  // tiles whose K / V copies have been issued
-            auto wwait = [&](uint32_t bb, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, ptx::wait_bounded(bb, parity, abort_flag, lim));
-            };
-            for (int x = 0; x < T; ++x) {
-                const bool core = x < Tc;
-                const int y = core ? core0 + tile_y(x) : row0 + tile_y(x);
-                const int left = core ? n / p.g - tile_y(x) : n - tile_y(x);
-                if (x >= DQ_KST && !wwait(bar(QB_EMPTYK + x % DQ_KST), (x / DQ_KST - 1) & 1)) break;
-                // only K takes part in a sum over keys; V's products stay in their column
-                if (!load_cut_tile<HD>(core ? (const void *)&tmKc : (const void *)&tmK, bar(QB_FULLK + x % DQ_KST), bar(QB_CUT), cut,
-                                       stage_k(x), y, kvz, left, abort_flag, lim))
-                    break;
-                nk = x + 1;
-                if (x >= DQ_VST && !wwait(bar(QB_EMPTYV + x % DQ_VST), (x / DQ_VST - 1) & 1)) break;
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(bar(QB_FULLV + x % DQ_VST), TILE_BYTES);
-                    load_tile<HD>(core ? (const void *)&tmVc : (const void *)&tmV, bar(QB_FULLV + x % DQ_VST), stage_v(x), y, kvz);
-                }
-                nv = x + 1;
-            }
-            __syncwarp();
-            if (*abort_flag) {
-                // let the copies already issued land before the CTA exits
-                volatile int never = 0;
-                ptx::wait_bounded(bar(QB_QD), 0, &never, lim);
-                for (int x = nk > DQ_KST ? nk - DQ_KST : 0; x < nk; ++x)
-                    ptx::wait_bounded(bar(QB_FULLK + x % DQ_KST), (x / DQ_KST) & 1, &never, lim);
-                for (int x = nv > DQ_VST ? nv - DQ_VST : 0; x < nv; ++x)
-                    ptx::wait_bounded(bar(QB_FULLV + x % DQ_VST), (x / DQ_VST) & 1, &never, lim);
-            }
-        } else if (!PACKED && lane == 0 && !p.skip_loads) {
+        if (lane == 0 && !p.skip_loads) {
             ptx::mbar_arrive_expect_tx(bar(QB_QD), 2 * TILE_BYTES);
-            load_tile<HD>(&tmQ, bar(QB_QD), sQ, i0, bh);
-            load_tile<HD>(&tmdO, bar(QB_QD), sdO, i0, bh);
+            load_tile(&tmQ, bar(QB_QD), sQ, i0, bh);
+            load_tile(&tmdO, bar(QB_QD), sdO, i0, bh);
             int nk = 0, nv = 0;  // tiles whose K / V copies have been issued
             for (int x = 0; x < T; ++x) {
                 const bool core = x < Tc;
@@ -451,7 +267,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     !ptx::wait_bounded(bar(QB_EMPTYK + x % DQ_KST), (x / DQ_KST - 1) & 1, abort_flag, lim))
                     break;
                 ptx::mbar_arrive_expect_tx(bar(QB_FULLK + x % DQ_KST), TILE_BYTES);
-                load_tile<HD>(core ? (const void *)&tmKc : (const void *)&tmK, bar(QB_FULLK + x % DQ_KST), stage_k(x),
+                load_tile(core ? (const void *)&tmKc : (const void *)&tmK, bar(QB_FULLK + x % DQ_KST), stage_k(x),
                           tile_y(x), kvz);
                 nk = x + 1;
                 // V(x) reuses the stage of V(x - 2) once dP(x - 2) has read it
@@ -459,7 +275,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     !ptx::wait_bounded(bar(QB_EMPTYV + x % DQ_VST), (x / DQ_VST - 1) & 1, abort_flag, lim))
                     break;
                 ptx::mbar_arrive_expect_tx(bar(QB_FULLV + x % DQ_VST), TILE_BYTES);
-                load_tile<HD>(core ? (const void *)&tmVc : (const void *)&tmV, bar(QB_FULLV + x % DQ_VST), stage_v(x),
+                load_tile(core ? (const void *)&tmVc : (const void *)&tmV, bar(QB_FULLV + x % DQ_VST), stage_v(x),
                           tile_y(x), kvz);
                 nv = x + 1;
             }
@@ -482,13 +298,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         const uint64_t dQd = ptx::smem_desc_sw128(sQ, 16, 1024), ddOd = ptx::smem_desc_sw128(sdO, 16, 1024);
         auto issue_s = [&](int x) {  // S(x) = Q K(x)^T
             ptx::tc_fence_after();
-            mma_ss<HD>(tmem, dQd, ptx::smem_desc_sw128(stage_k(x), 16, 1024));
-            ptx::tc_commit_warp(bar(QB_SFULL));
+            ptx::mma_ss_k128_warp(tmem + 128u * (x & 1), dQd, ptx::smem_desc_sw128(stage_k(x), 16, 1024), IDESC_SS,
+                                  0u);
+            ptx::tc_commit_warp(bar(QB_SFULL + (x & 1)));
         };
         auto issue_dp = [&](int x) {  // dP(x) = dO V(x)^T
             ptx::tc_fence_after();
-            mma_ss<HD>(tmem + T_DP + 128u * (x & 1), ddOd, ptx::smem_desc_sw128(stage_v(x), 16, 1024));
-            ptx::tc_commit_warp(bar(QB_DPFULL + (x & 1)));
+            ptx::mma_ss_k128_warp(tmem + T_DP, ddOd, ptx::smem_desc_sw128(stage_v(x), 16, 1024), IDESC_SS, 0u);
+            ptx::tc_commit_warp(bar(QB_DPFULL));
             ptx::tc_commit_warp(bar(QB_EMPTYV + x % DQ_VST));
         };
         bool ok = wwait(bar(QB_QD), 0) && wwait(bar(QB_FULLK), 0);
@@ -498,18 +315,18 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             const int x = tt + 1;
             if (x < T) {
                 if (!(ok = wwait(bar(QB_FULLK + x % DQ_KST), (x / DQ_KST) & 1))) break;
-                if (!(ok = wwait(bar(QB_SREAD), tt & 1))) break;
                 issue_s(x);
-                // dP(x) takes the buffer of dS(x - 2), which dQ(x - 2), issued before, has read by then
-                if (!(ok = wwait(bar(QB_FULLV + x % DQ_VST), (x / DQ_VST) & 1))) break;
-                issue_dp(x);
             }
             if (!(ok = wwait(bar(QB_PFULL), tt & 1))) break;
             ptx::tc_fence_after();
-            ptx::mma_ts_k128_split_warp(tmem + T_DQ, tmem + T_DP + 128u * (tt & 1),
+            ptx::mma_ts_k128_split_warp(tmem + T_DQ, tmem + 128u * (tt & 1),
                                         ptx::smem_desc_sw128(stage_k(tt), HALF_BYTES, 1024), IDESC_TS,
                                         tt > 0 ? 1u : 0u);  // dQ += dS K
             ptx::tc_commit_warp(bar(QB_EMPTYK + tt % DQ_KST));  // K(tt)'s stage is free once this has read it
+            if (x < T) {
+                if (!(ok = wwait(bar(QB_FULLV + x % DQ_VST), (x / DQ_VST) & 1))) break;
+                issue_dp(x);
+            }
         }
         ptx::tc_commit_warp(ok ? bar(QB_DONE) : bar(QB_DRAIN));
         if (!ok) {
@@ -529,17 +346,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         // the LSE in log2 units.  O comes from global memory (all eight 16-byte loads in
         // flight at once), dO from the swizzled tile already copied for the MMAs.
         const int i = i0 + row;
-        const bool valid = i < n;
-        float lse2 = 0.f, Di = 0.f;
-        if constexpr (PACKED) {
-            if (valid) {
-                const int64_t u = static_cast<int64_t>(bh) * p.plan.T + row0 + i;
-                lse2 = p.LSE[u] * LOG2E;
-                Di = p.Dbuf[u];
-            }
-        } else {
+        const bool valid = i < p.N;
         const int64_t u = static_cast<int64_t>(bh) * p.N + i;
         uint4 o4[8];
+        float lse2 = 0.f;
         if (valid) {
             const uint4 *src = reinterpret_cast<const uint4 *>(p.O + u * HD) + ch * 8;
 #pragma unroll
@@ -560,19 +370,18 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         float *const dpart = reinterpret_cast<float *>(gb + DQ_OFF_DPART);
         dpart[ch * BT + row] = Dpart;
         ptx::named_bar_sync(1, 256);  // the eight element-wise warps, every one of them, always
-        Di = dpart[row] + dpart[BT + row];
+        const float Di = dpart[row] + dpart[BT + row];
         if (valid && ch == 0) p.Dbuf[u] = Di;
-        }
         const int lo_i = win_of(p, i), nc_i = lo_of(i, p.w) / p.g;
         const float c1 = p.tau * LOG2E;
         bool ok = true;
         for (int tt = 0; tt < T; ++tt) {
-            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_SFULL), tt & 1, abort_flag, lim))) {
+            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_SFULL + (tt & 1)), (tt >> 1) & 1, abort_flag, lim))) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            const uint32_t sS = tmem + lane_addr + h0, sD = tmem + lane_addr + T_DP + 128u * (tt & 1) + h0;
+            const uint32_t sS = tmem + lane_addr + 128u * (tt & 1) + h0;
             uint32_t pa[32], pb[32];
             ptx::tmem_ld32(sS, pa);
             ptx::tmem_ld32(sS + 32, pb);
@@ -588,12 +397,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             if (!valid) c_hi = -1;
             ptx::tmem_wait_ld(pa);
             ptx::reg_touch(pb);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(QB_SREAD));  // the next S may come
             // P = 2^(S tau log2e - LSE), zero off the visible columns
-            const bool whole = __all_sync(0xffffffffu, c_lo <= h0 && c_hi >= h0 + 63);
-            if (whole) {
+            if (__all_sync(0xffffffffu, c_lo <= h0 && c_hi >= h0 + 63)) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     pa[k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pa[k]), c1, -lse2)));
@@ -609,38 +414,28 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                                 ? __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pb[k]), c1, -lse2))) : 0u;
                 }
             }
-            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_DPFULL + (tt & 1)), (tt >> 1) & 1, abort_flag, lim))) {
+            if (!__all_sync(0xffffffffu, ptx::wait_bounded(bar(QB_DPFULL), tt & 1, abort_flag, lim))) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            // dS = P (dP - D), bf16 pairs written over the dP columns [h0, h0 + 32), which
+            // dS = P (dP - D), bf16 pairs written over the S columns [h0, h0 + 32), which
             // this warp has already read
             uint32_t dp[32], pk[16];
-            ptx::tmem_ld32(sD, dp);
+            ptx::tmem_ld32(tmem + lane_addr + T_DP + h0, dp);
             ptx::tmem_wait_ld(dp);
-            if (PACKED && !whole) {  // nothing of a masked value gets on, not as 0 * NaN either
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (h0 + k < c_lo || h0 + k > c_hi) dp[k] = 0u;
-            }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 pk[k] = ptx::pack_bf16x2(__uint_as_float(pa[2 * k]) * (__uint_as_float(dp[2 * k]) - Di),
                                          __uint_as_float(pa[2 * k + 1]) * (__uint_as_float(dp[2 * k + 1]) - Di));
-            ptx::tmem_st16(sD, pk);
-            ptx::tmem_ld32(sD + 32, dp);
+            ptx::tmem_st16(sS, pk);
+            ptx::tmem_ld32(tmem + lane_addr + T_DP + h0 + 32, dp);
             ptx::tmem_wait_ld(dp);
-            if (PACKED && !whole) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (h0 + 32 + k < c_lo || h0 + 32 + k > c_hi) dp[k] = 0u;
-            }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 pk[k] = ptx::pack_bf16x2(__uint_as_float(pb[2 * k]) * (__uint_as_float(dp[2 * k]) - Di),
                                          __uint_as_float(pb[2 * k + 1]) * (__uint_as_float(dp[2 * k + 1]) - Di));
-            ptx::tmem_st16(sD + 16, pk);
+            ptx::tmem_st16(sS + 16, pk);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
@@ -650,25 +445,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         if (ok) {
             // dQ * tau through shared memory (the first two K stages, idle now) to a tiled store
             ptx::tc_fence_after();
-            if constexpr (PACKED) {
-                // a group-last row that is pooled into a core some row sees has the pooling's share too
-                const int j = i / p.g;
-                const bool last = valid && p.cores != 0 && i - j * p.g == p.g - 1 && j < seen_cores(n, p.w, p.g);
-                const int c0 = ch * (HD / 2);
-                const float *add = last ? p.space.dqs + (static_cast<int64_t>(kvz) * p.plan.G + core0 + j) * HD + c0 : nullptr;
-                store_row_bf16<HD / 2>(tmem + lane_addr + T_DQ + c0, p.tau, false, add, 1.f, nullptr, 0.f, p.rdQ.at(bh, row0 + i) + c0,
-                                       valid);
-            } else {
-                stage_f32_rows(tmem + lane_addr, T_DQ, ch, row, p.tau, false, base + DQ_OFF_K);
-                ptx::fence_proxy_async_smem();
-            }
+            stage_f32_rows(tmem + lane_addr, T_DQ, ch, row, p.tau, false, base + DQ_OFF_K);
+            ptx::fence_proxy_async_smem();
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
     if (*abort_flag) {
         if (t == 0 && p.status != nullptr) atomicCAS(p.status, 0, STATUS_TIMEOUT);
-    } else if (!PACKED && t == 0) {
+    } else if (t == 0) {
         store_tile_f32(&tmdQ, base + DQ_OFF_K, i0, bh);
         ptx::bulk_wait_read();
     }
@@ -700,35 +485,26 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 constexpr int DKV_THREADS = 320;
 constexpr int BWD_CORE_CHUNK = 64;  // query tiles per core-tile item
 constexpr int DKV_QST = 3, DKV_OST = 2;
+constexpr uint32_t DKV_OFF_Q = 2 * TILE_BYTES;  // after K, V
+constexpr uint32_t DKV_OFF_O = DKV_OFF_Q + DKV_QST * TILE_BYTES;
+constexpr uint32_t DKV_OFF_SLOT = DKV_OFF_O + DKV_OST * TILE_BYTES;  // LSE (log2 units) 128 | D 128
+constexpr uint32_t DKV_OFF_BAR = DKV_OFF_SLOT + 2 * BT * 4;
 constexpr int DB_KV = 0, DB_FULLQ = 1, DB_EMPTYQ = 4, DB_FULLO = 7, DB_EMPTYO = 9, DB_SFULL = 11, DB_DPFULL = 12,
-              DB_PFULL = 13, DB_DSFULL = 14, DB_DONE = 15, DB_DRAIN = 16, DB_CUT = 17;
-constexpr int DKV_NBARS = 18;
-template <int HD>
-struct DkvLayout {
-    static constexpr uint32_t TILE_BYTES = BT * HD * 2;
-    static constexpr uint32_t OFF_Q = 2 * TILE_BYTES;  // after K, V
-    static constexpr uint32_t OFF_O = OFF_Q + DKV_QST * TILE_BYTES;
-    static constexpr uint32_t OFF_SLOT = OFF_O + DKV_OST * TILE_BYTES;  // LSE (log2 units) 128 | D 128
-    static constexpr uint32_t OFF_BAR = OFF_SLOT + 2 * BT * 4;
-    static constexpr uint32_t OFF_TMEM = OFF_BAR + DKV_NBARS * 8;
-    static constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
-    static constexpr uint32_t SMEM = OFF_ABORT + 4 + 1024;  // + slack for the 1024-byte alignment
-    static_assert(SMEM <= 232448, "shared memory budget");
-};
+              DB_PFULL = 13, DB_DSFULL = 14, DB_DONE = 15, DB_DRAIN = 16;
+constexpr int DKV_NBARS = 17;
+constexpr uint32_t DKV_OFF_TMEM = DKV_OFF_BAR + DKV_NBARS * 8;
+constexpr uint32_t DKV_OFF_ABORT = DKV_OFF_TMEM + 4;
+constexpr uint32_t DKV_SMEM = DKV_OFF_ABORT + 4 + 1024;  // + slack for the 1024-byte alignment
+static_assert(DKV_SMEM <= 232448, "shared memory budget");
 static_assert(DKV_QST + DKV_OST >= 4, "the fp32 dK and dV tiles are staged over the Q and dO stages");
 
-template <bool PACKED, int HD>
 __global__ void __launch_bounds__(DKV_THREADS, 1)
     bwd_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmKc, const __grid_constant__ CUtensorMap tmVc,
                       const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
                       const __grid_constant__ CUtensorMap tmdKc, const __grid_constant__ CUtensorMap tmdVc,
-                      const __grid_constant__ ParamsOf<PACKED> p) {
-    using L = DkvLayout<HD>;
-    constexpr uint32_t TILE_BYTES = L::TILE_BYTES, DKV_OFF_Q = L::OFF_Q, DKV_OFF_O = L::OFF_O, DKV_OFF_SLOT = L::OFF_SLOT,
-                       DKV_OFF_BAR = L::OFF_BAR, DKV_OFF_TMEM = L::OFF_TMEM, DKV_OFF_ABORT = L::OFF_ABORT;
-    constexpr uint32_t IDESC_TS = ptx::idesc_bf16_f32(128, HD, 0, 1);  // A in TMEM, B MN-major
+                      const BwdTcParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t r0 = ptx::smem_addr(smem_raw);
     const uint32_t base = (r0 + 1023u) & ~1023u;
@@ -741,59 +517,42 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
     const uint64_t lim = p.wait_limit_ns;
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    // the tile's keys: of the cores or of the raw tokens, from y0 of the n_keys that the sequence has of them; the
-    // sequence has n rows from row0 of the tensors on, its cores start at core0
-    int idx, bk, chunk = -1, n, y0, n_keys, row0 = 0, core0 = 0;
-    bool core;
+    const int BK = p.B * p.Hkv;
     const int n_core_t = (p.G + BT - 1) / BT;
-    if constexpr (PACKED) {
-        const int item = static_cast<int>(blockIdx.x / p.Hkv);
-        const int3 counts = plan_counts(p.plan);
-        core = p.core != 0;
-        if (item >= (core ? counts.z : counts.y)) return;
-        const int4 e = (core ? p.plan.cores : p.plan.tiles)[item];
-        bk = static_cast<int>(blockIdx.x % p.Hkv);
-        row0 = e.x, n = e.y, core0 = e.w;
-        n_keys = core ? seen_cores(n, p.w, p.g) : n;
-        idx = (n_keys + BT - 1) / BT - 1 - e.z;  // the list's order is by the rows behind a key
-        y0 = idx * BT;
+    const int n_qt = (p.N + BT - 1) / BT;
+    // core tiles first (they are seen by the most query rows), then raw-token tiles.  With
+    // core_chunk > 0 (core tiles only) an item is one core tile over one chunk of query
+    // tiles, [c * core_chunk, (c + 1) * core_chunk); items run top chunk first, each chunk
+    // head by head, a head's core tiles side by side, so the CTAs that run together stream
+    // the same Q/dO tiles.
+    int idx, bk, chunk = -1;
+    if (p.core_chunk > 0) {
+        const int per_chunk = BK * n_core_t;
+        const int n_chunks = (n_qt + p.core_chunk - 1) / p.core_chunk;
+        chunk = n_chunks - 1 - static_cast<int>(blockIdx.x / per_chunk);
+        const int rem = static_cast<int>(blockIdx.x % per_chunk);
+        bk = rem / n_core_t;
+        idx = rem % n_core_t;
     } else {
-        const int BK = p.B * p.Hkv;
-        const int n_qt = (p.N + BT - 1) / BT;
-        // core tiles first (they are seen by the most query rows), then raw-token tiles.  With
-        // core_chunk > 0 (core tiles only) an item is one core tile over one chunk of query
-        // tiles, [c * core_chunk, (c + 1) * core_chunk); items run top chunk first, each chunk
-        // head by head, a head's core tiles side by side, so the CTAs that run together stream
-        // the same Q/dO tiles.
-        if (p.core_chunk > 0) {
-            const int per_chunk = BK * n_core_t;
-            const int n_chunks = (n_qt + p.core_chunk - 1) / p.core_chunk;
-            chunk = n_chunks - 1 - static_cast<int>(blockIdx.x / per_chunk);
-            const int rem = static_cast<int>(blockIdx.x % per_chunk);
-            bk = rem / n_core_t;
-            idx = rem % n_core_t;
-        } else {
-            idx = p.tile0 + static_cast<int>(blockIdx.x / BK);
-            bk = static_cast<int>(blockIdx.x % BK);
-        }
-        core = idx < n_core_t;
-        y0 = core ? idx * BT : (idx - n_core_t) * BT;
-        n = p.N;
-        n_keys = core ? p.G : p.N;
+        idx = p.tile0 + static_cast<int>(blockIdx.x / BK);
+        bk = static_cast<int>(blockIdx.x % BK);
     }
+    const bool core = idx < n_core_t;
+    const int y0 = core ? idx * BT : (idx - n_core_t) * BT;
+    const int n_keys = core ? p.G : p.N;
     const int r = p.Hq / p.Hkv;
     const int b = bk / p.Hkv, kv = bk % p.Hkv;
     // the query rows that see at least one key of the tile
     int r_lo, r_hi;
     if (core) {
         r_lo = (y0 + 1) * p.g + p.w - 1;  // core j is seen from row (j+1)g + w - 1 on
-        r_hi = n - 1;
+        r_hi = p.N - 1;
     } else {
-        const int m_last = min(y0 + BT - 1, n - 1);
+        const int m_last = min(y0 + BT - 1, p.N - 1);
         const int64_t last = p.window_mode ? static_cast<int64_t>(m_last / p.g + 1) * p.g + p.w - 2
                                            : static_cast<int64_t>(m_last) + p.w - 1;
         r_lo = y0;
-        r_hi = static_cast<int>(last < n - 1 ? last : n - 1);
+        r_hi = static_cast<int>(last < p.N - 1 ? last : p.N - 1);
     }
     int qt_hi = r_hi / BT, qt_lo = r_lo / BT;
     if (chunk >= 0) {
@@ -801,14 +560,6 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
         qt_hi = min(qt_hi, (chunk + 1) * p.core_chunk - 1);
         qt_lo = max(qt_lo, chunk * p.core_chunk);
         if (r_lo > r_hi || qt_lo > qt_hi) return;
-    }
-    if constexpr (PACKED) {
-        if (core && gridDim.y > 1) {  // this CTA's part of the rows (it may be none: its sums are zero)
-            const int per = (qt_hi - qt_lo + gridDim.y) / gridDim.y;
-            qt_hi -= per * blockIdx.y;
-            qt_lo = max(qt_lo, qt_hi - per + 1);
-            if (qt_lo > qt_hi) r_lo = r_hi + 1;
-        }
     }
     const int nq = r_lo <= r_hi ? qt_hi - qt_lo + 1 : 0;
     // (query tile, head) pairs from the last query tile down, heads fastest: every CTA of a
@@ -824,11 +575,8 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
         ptx::prefetch_tmap(core ? (const void *)&tmVc : (const void *)&tmV);
         ptx::prefetch_tmap(&tmQ);
         ptx::prefetch_tmap(&tmdO);
-        if constexpr (!PACKED) {
-            ptx::prefetch_tmap(core ? (const void *)&tmdKc : (const void *)&tmdK);
-            ptx::prefetch_tmap(core ? (const void *)&tmdVc : (const void *)&tmdV);
-        }
-        if constexpr (PACKED) ptx::mbar_init(bar(DB_CUT), 1);
+        ptx::prefetch_tmap(core ? (const void *)&tmdKc : (const void *)&tmdK);
+        ptx::prefetch_tmap(core ? (const void *)&tmdVc : (const void *)&tmdV);
         ptx::mbar_init(bar(DB_KV), 1);
         for (int st = 0; st < DKV_QST; ++st) {
             ptx::mbar_init(bar(DB_FULLQ + st), 1);
@@ -859,44 +607,10 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
-        if (PACKED && !p.skip_loads && n_it > 0) {
-            // the whole warp, for the tile of rows at the sequence's end
-            auto wwait = [&](uint32_t bb, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, ptx::wait_bounded(bb, parity, abort_flag, lim));
-            };
-            if (lane == 0) {
-                const int y = (core ? core0 : row0) + y0;
-                ptx::mbar_arrive_expect_tx(bar(DB_KV), 2 * TILE_BYTES);
-                load_tile<HD>(core ? (const void *)&tmKc : (const void *)&tmK, bar(DB_KV), sK, y, bk);
-                load_tile<HD>(core ? (const void *)&tmVc : (const void *)&tmV, bar(DB_KV), sV, y, bk);
-            }
-            uint32_t cut = 0;
-            int nqd = 0, nod = 0;  // tiles whose Q / dO copies have been issued
-            for (int x = 0; x < n_it; ++x) {
-                const int bh = bh_of(x), i0 = i0_of(x), left = n - i0;
-                if (x >= DKV_QST && !wwait(bar(DB_EMPTYQ + x % DKV_QST), (x / DKV_QST - 1) & 1)) break;
-                if (!load_cut_tile<HD>(&tmQ, bar(DB_FULLQ + x % DKV_QST), bar(DB_CUT), cut, stage_q(x), row0 + i0, bh, left, abort_flag, lim))
-                    break;
-                nqd = x + 1;
-                if (x >= DKV_OST && !wwait(bar(DB_EMPTYO + x % DKV_OST), (x / DKV_OST - 1) & 1)) break;
-                if (!load_cut_tile<HD>(&tmdO, bar(DB_FULLO + x % DKV_OST), bar(DB_CUT), cut, stage_o(x), row0 + i0, bh, left, abort_flag, lim))
-                    break;
-                nod = x + 1;
-            }
-            __syncwarp();
-            if (*abort_flag) {
-                // let the copies already issued land before the CTA exits
-                volatile int never = 0;
-                ptx::wait_bounded(bar(DB_KV), 0, &never, lim);
-                for (int x = nqd > DKV_QST ? nqd - DKV_QST : 0; x < nqd; ++x)
-                    ptx::wait_bounded(bar(DB_FULLQ + x % DKV_QST), (x / DKV_QST) & 1, &never, lim);
-                for (int x = nod > DKV_OST ? nod - DKV_OST : 0; x < nod; ++x)
-                    ptx::wait_bounded(bar(DB_FULLO + x % DKV_OST), (x / DKV_OST) & 1, &never, lim);
-            }
-        } else if (!PACKED && lane == 0 && !p.skip_loads && n_it > 0) {
+        if (lane == 0 && !p.skip_loads && n_it > 0) {
             ptx::mbar_arrive_expect_tx(bar(DB_KV), 2 * TILE_BYTES);
-            load_tile<HD>(core ? (const void *)&tmKc : (const void *)&tmK, bar(DB_KV), sK, y0, bk);
-            load_tile<HD>(core ? (const void *)&tmVc : (const void *)&tmV, bar(DB_KV), sV, y0, bk);
+            load_tile(core ? (const void *)&tmKc : (const void *)&tmK, bar(DB_KV), sK, y0, bk);
+            load_tile(core ? (const void *)&tmVc : (const void *)&tmV, bar(DB_KV), sV, y0, bk);
             int nqd = 0, nod = 0;  // tiles whose Q / dO copies have been issued
             for (int x = 0; x < n_it; ++x) {
                 const int bh = bh_of(x), i0 = i0_of(x);
@@ -905,14 +619,14 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
                     !ptx::wait_bounded(bar(DB_EMPTYQ + x % DKV_QST), (x / DKV_QST - 1) & 1, abort_flag, lim))
                     break;
                 ptx::mbar_arrive_expect_tx(bar(DB_FULLQ + x % DKV_QST), TILE_BYTES);
-                load_tile<HD>(&tmQ, bar(DB_FULLQ + x % DKV_QST), stage_q(x), i0, bh);
+                load_tile(&tmQ, bar(DB_FULLQ + x % DKV_QST), stage_q(x), i0, bh);
                 nqd = x + 1;
                 // dO(x) reuses the stage of dO(x - 2) once dV(x - 2) has read it
                 if (x >= DKV_OST &&
                     !ptx::wait_bounded(bar(DB_EMPTYO + x % DKV_OST), (x / DKV_OST - 1) & 1, abort_flag, lim))
                     break;
                 ptx::mbar_arrive_expect_tx(bar(DB_FULLO + x % DKV_OST), TILE_BYTES);
-                load_tile<HD>(&tmdO, bar(DB_FULLO + x % DKV_OST), stage_o(x), i0, bh);
+                load_tile(&tmdO, bar(DB_FULLO + x % DKV_OST), stage_o(x), i0, bh);
                 nod = x + 1;
             }
             if (*abort_flag) {
@@ -934,12 +648,12 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
         const uint64_t dKk = ptx::smem_desc_sw128(sK, 16, 1024), dVk = ptx::smem_desc_sw128(sV, 16, 1024);
         auto issue_s = [&](int x) {  // S^T(x) = K Q(x)^T
             ptx::tc_fence_after();
-            mma_ss<HD>(tmem + 0, dKk, ptx::smem_desc_sw128(stage_q(x), 16, 1024));
+            ptx::mma_ss_k128_warp(tmem + 0, dKk, ptx::smem_desc_sw128(stage_q(x), 16, 1024), IDESC_SS, 0u);
             ptx::tc_commit_warp(bar(DB_SFULL));
         };
         auto issue_dp = [&](int x) {  // dP^T(x) = V dO(x)^T
             ptx::tc_fence_after();
-            mma_ss<HD>(tmem + T_DP, dVk, ptx::smem_desc_sw128(stage_o(x), 16, 1024));
+            ptx::mma_ss_k128_warp(tmem + T_DP, dVk, ptx::smem_desc_sw128(stage_o(x), 16, 1024), IDESC_SS, 0u);
             ptx::tc_commit_warp(bar(DB_DPFULL));
         };
         bool ok = n_it == 0 || (wwait(bar(DB_KV), 0) && wwait(bar(DB_FULLQ), 0));
@@ -985,14 +699,12 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
         const float c1 = p.tau * LOG2E;
         int64_t key_last = 0;
         if (!core) key_last = p.window_mode ? static_cast<int64_t>(m / p.g + 1) * p.g + p.w - 2 : static_cast<int64_t>(m) + p.w - 1;
-        int64_t tokens = p.N;  // rows of a head in LSE and D
-        if constexpr (PACKED) tokens = p.plan.T;
         // this thread's value of the LSE/D slot: LSE (log2 units) of query e, or D of query e - 128
         const int e = (warp - 2) * 32 + lane;
         auto slot_value = [&](int x) -> float {
             const int iq = i0_of(x) + (e & (BT - 1));
-            if (iq >= n) return 0.f;
-            const int64_t off = bh_of(x) * tokens + row0 + iq;
+            if (iq >= p.N) return 0.f;
+            const int64_t off = static_cast<int64_t>(bh_of(x)) * p.N + iq;
             return e < BT ? p.LSE[off] * LOG2E : p.Dbuf[off];
         };
         float *const slot_f = reinterpret_cast<float *>(gb + DKV_OFF_SLOT);
@@ -1001,39 +713,26 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
         ptx::named_bar_sync(1, 256);
         bool ok = true;
         // the pooling backward's terms for this key's row (raw tiles, folded pooling backward)
-        bool fuse = !core && p.pool_fuse != 0;
-        const int mm = m < n ? m : n - 1;  // rows past N only take part in collective loads
-        int64_t uj;
+        const bool fuse = !core && p.pool_fuse != 0;
+        const int mm = m < p.N ? m : p.N - 1;  // rows past N only take part in collective loads
+        const int64_t uj = static_cast<int64_t>(bk) * p.G + mm / p.g;
         float am = 0.f, cm = 0.f;
-        if constexpr (PACKED) {
-            fuse = fuse && m < n && mm / p.g < seen_cores(n, p.w, p.g);
-            uj = static_cast<int64_t>(bk) * p.plan.G + core0 + mm / p.g;
-            if (fuse) {
-                const int64_t um = static_cast<int64_t>(bk) * p.plan.T + row0 + mm;
-                am = p.space.a[um];
-                cm = p.space.cds[um];
-            }
-        } else {
-            uj = static_cast<int64_t>(bk) * p.G + mm / p.g;
-            if (fuse) {
-                const int64_t um = static_cast<int64_t>(bk) * p.N + mm;
-                am = p.pool_fuse == 1 ? 1.f / p.g : p.pool_a[um];
-                cm = p.pool_fuse == 1 ? 0.f : p.pool_cds[um];
-            }
+        if (fuse) {
+            const int64_t um = static_cast<int64_t>(bk) * p.N + mm;
+            am = p.pool_fuse == 1 ? 1.f / p.g : p.pool_a[um];
+            cm = p.pool_fuse == 1 ? 0.f : p.pool_cds[um];
         }
         // Every element-wise thread runs every iteration and both named barriers of it, so
         // that a time-out (which skips the work) cannot leave a barrier short of threads.
         for (int it = 0; it < n_it; ++it) {
-            [[maybe_unused]] bool whole = true;
-            [[maybe_unused]] int lo_q = 0, hi_q = BT - 1;
             const float v_next = it + 1 < n_it ? slot_value(it + 1) : 0.f;
             if (fuse && it == n_it - 1) {
                 // bring this row's half of dKc_j, dVc_j (and qsum_j) into L1 for the epilogue
 #pragma unroll
-                for (int l = 0; l < HD / 64; ++l) {
-                    ptx::prefetch_l1(p.pool_dkc + uj * HD + ch * (HD / 2) + 32 * l);
-                    ptx::prefetch_l1(p.pool_dvc + uj * HD + ch * (HD / 2) + 32 * l);
-                    if (p.pool_fuse == 2) ptx::prefetch_l1(p.pool_qs + uj * HD + ch * (HD / 2) + 32 * l);
+                for (int l = 0; l < 2; ++l) {
+                    ptx::prefetch_l1(p.pool_dkc + uj * HD + h0 + 32 * l);
+                    ptx::prefetch_l1(p.pool_dvc + uj * HD + h0 + 32 * l);
+                    if (p.pool_fuse == 2) ptx::prefetch_l1(p.pool_qs + uj * HD + h0 + 32 * l);
                 }
             }
             if (ok) ok = __all_sync(0xffffffffu, ptx::wait_bounded(bar(DB_SFULL), it & 1, abort_flag, lim));
@@ -1051,9 +750,9 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
                     q_hi = -1;
                 } else if (core) {
                     q_lo = max((m + 1) * p.g + p.w - 1 - i0, 0);
-                    q_hi = min(n - 1 - i0, BT - 1);
+                    q_hi = min(p.N - 1 - i0, BT - 1);
                 } else {
-                    const int last_i = static_cast<int>(key_last < n - 1 ? key_last : n - 1);
+                    const int last_i = static_cast<int>(key_last < p.N - 1 ? key_last : p.N - 1);
                     q_lo = max(m - i0, 0);
                     q_hi = min(last_i - i0, BT - 1);
                 }
@@ -1061,9 +760,7 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
                 ptx::reg_touch(pb);
                 // P^T = 2^(S^T tau log2e - LSE), zero off the visible columns (the LSE of four
                 // columns per shared-memory load, the same address across the warp)
-                whole = __all_sync(0xffffffffu, q_lo <= h0 && q_hi >= h0 + 63);
-                lo_q = q_lo, hi_q = q_hi;
-                if (whole) {
+                if (__all_sync(0xffffffffu, q_lo <= h0 && q_hi >= h0 + 63)) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const float4 la = slot4[h0 / 4 + q], lb = slot4[h0 / 4 + 8 + q];
@@ -1112,11 +809,6 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
                 for (int j = 0; j < 2; ++j) {
                     ptx::tmem_ld32(sD + 32 * j, dp);
                     ptx::tmem_wait_ld(dp);
-                    if (PACKED && !whole) {  // nothing of a masked value gets on, not as 0 * NaN either
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (h0 + 32 * j + k < lo_q || h0 + 32 * j + k > hi_q) dp[k] = 0u;
-                    }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const float4 dv = slot4[(BT + h0) / 4 + 8 * j + q];
@@ -1147,21 +839,7 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
             // dK * tau and dV through shared memory (the Q and dO stages, idle now) to tiled
             // stores; a tile no query row sees stores zeros
             ptx::tc_fence_after();
-            if constexpr (PACKED) {
-                const int c0 = ch * (HD / 2);
-                const bool valid = m < n_keys, none = n_it == 0;
-                const uint32_t tk = tmem + lane_addr + T_DK + c0, tv = tmem + lane_addr + T_DV + c0;
-                if (core) {
-                    const int64_t at = ((static_cast<int64_t>(blockIdx.y) * p.Hkv + bk) * p.plan.G + core0 + m) * HD + c0;
-                    store_row_f32<HD / 2>(tk, p.tau, none, p.space.dKc + at, valid);
-                    store_row_f32<HD / 2>(tv, 1.f, none, p.space.dVc + at, valid);
-                } else {
-                    const float *xk = fuse ? p.space.dKc + uj * HD + c0 : nullptr, *xv = fuse ? p.space.dVc + uj * HD + c0 : nullptr,
-                                *qs = fuse ? p.space.qsum + uj * HD + c0 : nullptr;
-                    store_row_bf16<HD / 2>(tk, p.tau, none, xk, am, qs, cm, p.rdK.at(bk, row0 + m) + c0, valid);
-                    store_row_bf16<HD / 2>(tv, 1.f, none, xv, am, nullptr, 0.f, p.rdV.at(bk, row0 + m) + c0, valid);
-                }
-            } else if (fuse) {
+            if (fuse) {
                 // + the pooling backward: a_m dKc_j + (tau/r) ds_m qsum_j and a_m dVc_j, j = m / g
                 // (the store drops rows past N)
                 const float *qs = p.pool_fuse == 1 ? nullptr : p.pool_qs + uj * HD;
@@ -1173,14 +851,14 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
                 stage_f32_rows(tmem + lane_addr, T_DK, ch, row, p.tau, n_it == 0, base + DKV_OFF_Q);
                 stage_f32_rows(tmem + lane_addr, T_DV, ch, row, 1.f, n_it == 0, base + DKV_OFF_Q + 2 * TILE_BYTES);
             }
-            if constexpr (!PACKED) ptx::fence_proxy_async_smem();
+            ptx::fence_proxy_async_smem();
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
     if (*abort_flag) {
         if (t == 0 && p.status != nullptr) atomicCAS(p.status, 0, STATUS_TIMEOUT);
-    } else if (!PACKED && t == 0) {
+    } else if (t == 0) {
         // a chunked core item adds its share to dKc/dVc (zeroed before the launch)
         store_tile_f32(core ? &tmdKc : &tmdK, base + DKV_OFF_Q, y0, bk, chunk >= 0);
         store_tile_f32(core ? &tmdVc : &tmdV, base + DKV_OFF_Q + 2 * TILE_BYTES, y0, bk, chunk >= 0);
@@ -1214,10 +892,10 @@ cudaError_t launch_attn_bwd_tc(const void *Q, const void *K, const void *V, cons
         std::lock_guard<std::mutex> lock(mu);
         Attr &a = attr[dev & 63];
         if (!a.done) {
-            a.err = cudaFuncSetAttribute(bwd_dq_tc_kernel<false, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLayout<128>::SMEM);
+            a.err = cudaFuncSetAttribute(bwd_dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM);
             if (a.err == cudaSuccess)
-                a.err = cudaFuncSetAttribute(bwd_dkv_tc_kernel<false, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             DkvLayout<128>::SMEM);
+                a.err = cudaFuncSetAttribute(bwd_dkv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             DKV_SMEM);
             a.done = true;
         }
         if (a.err != cudaSuccess) return a.err;
@@ -1257,8 +935,8 @@ cudaError_t launch_attn_bwd_tc(const void *Q, const void *K, const void *V, cons
     p.skip_loads = g_skip_q_load;
     if (part != 2) {
         const unsigned n_qt = static_cast<unsigned>((s.N + BT - 1) / BT);
-        bwd_dq_tc_kernel<false, 128><<<n_qt * static_cast<unsigned>(qh), DQ_THREADS, DqLayout<128>::SMEM, stream>>>(
-            mQ, mdO, mK, mV, mKc, mVc, mdQ, p);
+        bwd_dq_tc_kernel<<<n_qt * static_cast<unsigned>(qh), DQ_THREADS, DQ_SMEM, stream>>>(mQ, mdO, mK, mV, mKc,
+                                                                                            mVc, mdQ, p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -1287,87 +965,9 @@ cudaError_t launch_attn_bwd_tc(const void *Q, const void *K, const void *V, cons
     }
     if (n_kt == 0) return cudaSuccess;
     if (grid == 0) grid = n_kt * static_cast<unsigned>(kh);
-    bwd_dkv_tc_kernel<false, 128><<<grid, DKV_THREADS, DkvLayout<128>::SMEM, stream>>>(
+    bwd_dkv_tc_kernel<<<grid, DKV_THREADS, DKV_SMEM, stream>>>(
         mQ, mdO, mK, mV, mKc, mVc, mdK, mdV, mdKc, mdVc, p);
     return cudaGetLastError();
-}
-
-namespace {
-
-template <int HD>
-cudaError_t launch_packed(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaStream_t stream) {
-    EncodeTiledFn enc = get_encoder();
-    if (enc == nullptr) return cudaErrorNotSupported;
-    static std::mutex mu;
-    static Attr attr[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        Attr &at = attr[dev & 63];
-        if (!at.done) {
-            at.err = cudaFuncSetAttribute(bwd_dq_tc_kernel<true, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLayout<HD>::SMEM);
-            if (at.err == cudaSuccess)
-                at.err = cudaFuncSetAttribute(bwd_dkv_tc_kernel<true, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              DkvLayout<HD>::SMEM);
-            at.done = true;
-        }
-        if (at.err != cudaSuccess) return at.err;
-    }
-    CUtensorMap mQ, mdO, mK, mV, mKc, mVc;
-    if (!encode_packed_bf16(enc, &mQ, a.Q, HD, a.plan.T, a.Hq) || !encode_packed_bf16(enc, &mdO, a.dO, HD, a.plan.T, a.Hq) ||
-        !encode_packed_bf16(enc, &mK, a.K, HD, a.plan.T, a.Hkv) || !encode_packed_bf16(enc, &mV, a.V, HD, a.plan.T, a.Hkv))
-        return cudaErrorInvalidValue;
-    mKc = mK;
-    mVc = mV;
-    if (a.Kc != nullptr) {
-        const int64_t head = static_cast<int64_t>(a.plan.G) * HD;
-        const cca_packed_rows_t kc = {const_cast<void *>(a.Kc), head, HD}, vc = {const_cast<void *>(a.Vc), head, HD};
-        if (!encode_packed_bf16(enc, &mKc, kc, HD, a.plan.G, a.Hkv) || !encode_packed_bf16(enc, &mVc, vc, HD, a.plan.G, a.Hkv))
-            return cudaErrorInvalidValue;
-    }
-    PackedBwdParams p = {};
-    p.B = 1;
-    p.Hq = a.Hq;
-    p.Hkv = a.Hkv;
-    p.g = a.plan.g;
-    p.w = a.plan.w;
-    p.window_mode = a.plan.window_mode;
-    p.G = a.plan.G;
-    p.tau = a.scale;
-    p.LSE = a.LSE;
-    p.Dbuf = w.D;
-    p.pool_fuse = a.Kc != nullptr ? 2 : 0;
-    p.pool_dkc = w.dKc;
-    p.pool_dvc = w.dVc;
-    p.pool_qs = w.qsum;
-    p.status = a.plan.status;
-    p.wait_limit_ns = g_wait_limit_ns;
-    p.skip_loads = g_skip_q_load;
-    p.plan = a.plan;
-    p.rdQ = rows_of<__nv_bfloat16>(a.dQ);
-    p.rdK = rows_of<__nv_bfloat16>(a.dK);
-    p.rdV = rows_of<__nv_bfloat16>(a.dV);
-    p.space = w;
-    p.core = part == 0;
-    p.cores = a.Kc != nullptr;
-    const int64_t blocks = part == 1 ? static_cast<int64_t>(a.plan.max_tiles) * a.Hq
-                                     : static_cast<int64_t>(part == 0 ? a.plan.max_cores : a.plan.max_tiles) * a.Hkv;
-    if (blocks > 0x7fffffff) return cudaErrorNotSupported;
-    if (part == 1) {
-        bwd_dq_tc_kernel<true, HD><<<static_cast<unsigned>(blocks), DQ_THREADS, DqLayout<HD>::SMEM, stream>>>(mQ, mdO, mK, mV, mKc, mVc, mQ, p);
-    } else {
-        const dim3 grid(static_cast<unsigned>(blocks), part == 0 ? w.splits : 1);
-        bwd_dkv_tc_kernel<true, HD><<<grid, DKV_THREADS, DkvLayout<HD>::SMEM, stream>>>(mQ, mdO, mK, mV, mKc, mVc, mQ, mQ, mQ, mQ, p);
-    }
-    return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_packed_bwd_tc(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaStream_t stream) {
-    return a.d == 128 ? launch_packed<128>(a, w, part, stream) : launch_packed<64>(a, w, part, stream);
 }
 
 }  // namespace cca

@@ -88,6 +88,12 @@ __device__ __forceinline__ int3 plan_short(const Plan &p) {
     return make_int3(d.x, d.y, d.z);
 }
 
+// The item of a persistent CTA in its round-th turn (n or more: none).  Lists run from heavy to light, so the CTAs
+// go through them to and fro: straight rounds would give the first CTA the heaviest item of each.
+__device__ __forceinline__ int item_of_round(int round) {
+    return round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 // Cores that any row of a sequence of n tokens sees: (j + 1) * g <= n - w.
 __host__ __device__ __forceinline__ int seen_cores(int n, int w, int g) { return n > w ? (n - w) / g : 0; }
 
