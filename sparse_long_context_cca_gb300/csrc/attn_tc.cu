@@ -123,11 +123,16 @@ struct PackedParams : Params {
     const __nv_bfloat16 *Kc, *Vc;
     CUtensorMap mQ[3];  // Q in boxes of 2, 4, 8 heads of 64, 32, 16 rows
     int most;           // log2 of the heads that may share a half
+    FastDiv by_r, by_heads[4];  // by Hq / Hkv, and by Hq >> c
 };
 template <bool PACKED>
 using ParamsOf = typename std::conditional<PACKED, PackedParams, Params>::type;
 
 __device__ __forceinline__ int lo_of(int i, int w) { return window_lo(i, w); }
+// PACKED: the same without a division
+__device__ __forceinline__ int win_of(const PackedParams &p, int i) { return p.plan.start_of(i); }
+__device__ __forceinline__ int cores_of(const Params &p, int i) { return lo_of(i, p.w) / p.g; }
+__device__ __forceinline__ int cores_of(const PackedParams &p, int i) { return p.plan.cores_of(i); }
 // first raw token of row i's window (cores stay j < lo(i)/g in both modes)
 __device__ __forceinline__ int win_of(const Params &p, int i) { return window_start(i, p.w, p.g, p.window_mode); }
 
@@ -174,7 +179,8 @@ __device__ __forceinline__ int half_max_step(const Half &x, int Tc) {
     return (x.valid && x.tc > 0) ? Tc + x.kl - (x.tc - 1) : 1;
 }
 
-__device__ __forceinline__ Half make_half(const Params &p, int a, int lo0, int q_off, int n_q, int rows = BM) {
+template <typename P>
+__device__ __forceinline__ Half make_half(const P &p, int a, int lo0, int q_off, int n_q, int rows = BM) {
     Half x;
     x.a = a;
     x.valid = a - q_off < n_q;
@@ -183,7 +189,7 @@ __device__ __forceinline__ Half make_half(const Params &p, int a, int lo0, int q
         x.tc = x.kl = x.kh = 0;
         return x;
     }
-    const int nc = lo_of(x.b, p.w) / p.g;
+    const int nc = cores_of(p, x.b);
     x.tc = (nc + BN - 1) / BN;
     x.kl = (win_of(p, a) - lo0) / BN;
     x.kh = (x.b - lo0) / BN + 1;
@@ -196,22 +202,19 @@ __device__ __forceinline__ Item make_item(const ParamsOf<PACKED> &p, int k, [[ma
     Item it;
     if constexpr (PACKED) {
         // heaviest first, all heads of a pair side by side; short sequences, the last ones, by groups of 2^c heads
-        int idx = k / p.Hq, c = 0, at = k - idx * p.Hq;
-        if (idx >= begin[0]) {
-            at = k - begin[0] * p.Hq;
-            for (c = 1; c < 3; ++c) {
-                const int some = (begin[c] - begin[c - 1]) * (p.Hq >> c);
-                if (at < some) break;
-                at -= some;
-            }
-            idx = at / (p.Hq >> c);
-            at -= idx * (p.Hq >> c);
-            idx += begin[c - 1];
+        int c = 0, at = k;
+        for (; c < 3; ++c) {
+            const int some = (begin[c] - (c > 0 ? begin[c - 1] : 0)) * (p.Hq >> c);
+            if (at < some) break;
+            at -= some;
         }
+        int idx = p.by_heads[c].div(at);
+        at -= idx * (p.Hq >> c);
+        idx += c > 0 ? begin[c - 1] : 0;
         const int4 e = p.plan.pairs[idx];
         it.lr = 7 - c;
         it.h = it.bh = at << c;
-        it.kvz = it.h / (p.Hq / p.Hkv);
+        it.kvz = p.by_r.div(it.h);
         it.row0 = e.x;
         it.core0 = e.w;
         it.n = e.y;
@@ -269,7 +272,7 @@ __device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, 
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
         // visible keys, cores first, eight at a time (a key alone is a chain of shuffles)
-        const int nc = lo_of(i, p.w) / p.g, win = win_of(p, i), n = nc + i - win + 1;
+        const int nc = cores_of(p, i), win = win_of(p, i), n = nc + i - win + 1;
         constexpr int KEYS = 8;
         for (int x0 = 0; x0 < n; x0 += KEYS) {
             float s[KEYS], v[KEYS][E], top = -INFINITY;
@@ -653,8 +656,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             int i = x.a + row;
             if constexpr (PACKED) i = x.a + (row & ((1 << it.lr) - 1));
             const int lo_i = win_of(p, i);           // first raw token of this row's window
-            const int nc_i = lo_of(i, p.w) / p.g;    // cores visible to this row
-            const int nc_first = lo_of(x.a, p.w) / p.g;
+            const int nc_i = cores_of(p, i);         // cores visible to this row
+            const int nc_first = cores_of(p, x.a);
             const int lo_last = win_of(p, x.b);
             float m = -INFINITY;  // running max of the log2-scaled logits
             float l = 0.f;
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (masked) {
                         const bool core = t < it.Tc;
                         const int key = core ? t * BN + row : it.lo0 + (t - it.Tc) * BN + row;
-                        const bool past = key >= (core ? it.n / p.g : it.n);
+                        const bool past = key >= (core ? p.plan.by_g.div(it.n) : it.n);
                         if (clean_key<HD>(base + OFF_RING + ((u0 + 2 * t + 1) % NS) * TILE_BYTES, row, past))
                             mark[n_done & 1] = n_done + 1;
                         // the other half, where it uses the tile, masks it too and writes the same zeros
@@ -971,6 +974,8 @@ cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream) {
     p.wait_limit_ns = g_wait_limit_ns;
     p.skip_q_load = g_skip_q_load;
     p.plan = a.plan;
+    p.by_r = fast_div(a.Hq / a.Hkv);
+    for (int c = 0; c <= p.most; ++c) p.by_heads[c] = fast_div(a.Hq >> c);
     p.rQ = rows_of<const __nv_bfloat16>(a.Q);
     p.rK = rows_of<const __nv_bfloat16>(a.K);
     p.rV = rows_of<const __nv_bfloat16>(a.V);

@@ -48,6 +48,14 @@ struct Plan {
     int T, G, g, w, window_mode;
     int max_pairs, max_tiles, max_cores;
     int32_t *status;
+    FastDiv by_g;
+    // visibility.cuh's, with a division that the host has prepared
+    __device__ __forceinline__ int cores_of(int i) const { return by_g.div(window_lo(i, w)); }
+    __device__ __forceinline__ int start_of(int i) const {
+        const int lo = window_lo(i, w);
+        return window_mode ? by_g.div(lo) * g : lo;
+    }
+    __device__ __forceinline__ int seen_of(int n) const { return n > w ? by_g.div(n - w) : 0; }
 };
 inline Plan plan_of(const cca_packed_t &p, int32_t *status) {
     const PlanLayout l = plan_layout(p.S, p.T, p.g);
@@ -67,6 +75,7 @@ inline Plan plan_of(const cca_packed_t &p, int32_t *status) {
     r.max_tiles = l.max_tiles;
     r.max_cores = l.max_cores;
     r.status = status;
+    r.by_g = fast_div(p.g);
     return r;
 }
 

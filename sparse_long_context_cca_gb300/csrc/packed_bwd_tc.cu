@@ -57,7 +57,9 @@ struct Args {
     Rows<__nv_bfloat16> dQ, dK, dV;
     PackedBwdSpace space;
     const float *LSE;
-    int Hq, Hkv;
+    int Hq, Hkv, r;  // r: query heads of a KV head
+    FastDiv by_Hq, by_Hkv, by_r, by_per;  // per: items of a dkv tile
+    int per;
     float tau;
     int core;   // dkv: core tiles (else raw ones)
     int cores;  // whether any core is seen
@@ -242,14 +244,15 @@ __device__ __forceinline__ void drain_copies(const Cta<HD> &c, uint32_t nl, uint
 struct DqItem {
     int h, kv, n, row0, core0, i0, lo0, Tc, T;
     __device__ __forceinline__ DqItem(const Args &p, int item) {
-        const int4 e = p.plan.tiles[item / p.Hq];
-        h = item % p.Hq;
-        kv = h / (p.Hq / p.Hkv);
+        const int tile = p.by_Hq.div(item);
+        const int4 e = p.plan.tiles[tile];
+        h = item - tile * p.Hq;
+        kv = p.by_r.div(h);
         row0 = e.x, n = e.y, core0 = e.w;
         i0 = e.z * BT;
         const int i1 = min(i0 + BT, n) - 1;
-        lo0 = window_start(i0, p.plan.w, p.plan.g, p.plan.window_mode);
-        Tc = (visible_cores(i1, p.plan.w, p.plan.g) + BT - 1) / BT;  // core tiles
+        lo0 = p.plan.start_of(i0);
+        Tc = (p.plan.cores_of(i1) + BT - 1) / BT;                    // core tiles
         T = Tc + (i1 - lo0) / BT + 1;                                // + band tiles
     }
     __device__ __forceinline__ int tile_y(int x) const { return x < Tc ? x * BT : lo0 + (x - Tc) * BT; }
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = !p.skip_loads;
         for (int round = 0, item; ok && (item = item_of_round(round)) < n_items; ++round) {
             const DqItem d(p, item);
+            const int groups = p.plan.by_g.div(d.n);
             if (!c.wait(c.bar(B_RESFREE), (it & 1) ^ 1)) break;
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(c.bar(B_RES), 2 * Layout<HD>::TILE);
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int x = 0; x < d.T; ++x, ++g) {
                 const bool core = x < d.Tc;
                 const int y = (core ? d.core0 : d.row0) + d.tile_y(x);
-                const int left = (core ? d.n / p.plan.g : d.n) - d.tile_y(x);
+                const int left = (core ? groups : d.n) - d.tile_y(x);
                 // only K takes part in a sum over keys; V's products stay in their column
                 if (!(ok = c.wait(c.bar(B_LEMPTY + g % LONG_ST), ((g / LONG_ST) & 1) ^ 1))) break;
                 if (!(ok = load_cut_tile<HD>(core ? (const void *)&tmKc : (const void *)&tmK, c.bar(B_LFULL + g % LONG_ST), c.bar(B_CUT), cut,
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 lse2 = p.LSE[u] * LOG2E;
                 Di = p.space.D[u];
             }
-            const int lo_i = window_start(i, p.plan.w, p.plan.g, p.plan.window_mode), nc_i = visible_cores(i, p.plan.w, p.plan.g);
+            const int lo_i = p.plan.start_of(i), nc_i = p.plan.cores_of(i);
             for (int x = 0; x < d.T; ++x, ++g) {
                 if (!(ok = c.wait(c.bar(B_S), g & 1))) break;
                 ptx::tc_fence_after();
@@ -449,8 +453,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) ptx::mbar_arrive(c.bar(B_ACCFREE));
             if (valid) {
                 // a group-last row that is pooled into a core some row sees has the pooling's share too
-                const int j = i / p.plan.g;
-                const bool last = p.cores != 0 && i - j * p.plan.g == p.plan.g - 1 && j < seen_cores(d.n, p.plan.w, p.plan.g);
+                const int j = p.plan.by_g.div(i);
+                const bool last = p.cores != 0 && i - j * p.plan.g == p.plan.g - 1 && j < p.plan.seen_of(d.n);
                 const float *add = last ? p.space.dqs + (static_cast<int64_t>(d.kv) * p.plan.G + d.core0 + j) * HD + c0 : nullptr;
                 __nv_bfloat16 *out = p.dQ.at(d.h, d.row0 + i) + c0;
 #pragma unroll
@@ -467,12 +471,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 struct DkvItem {
     int kv, n, row0, core0, y0, n_keys, qt_hi, n_it, split;
     __device__ __forceinline__ DkvItem(const Args &p, int item) {
-        const int splits = p.core ? p.space.splits : 1, per = p.Hkv * splits;
-        const int4 e = (p.core ? p.plan.cores : p.plan.tiles)[item / per];
-        split = item % per / p.Hkv;
-        kv = item % p.Hkv;
+        const int splits = p.core ? p.space.splits : 1, tile = p.by_per.div(item);
+        const int4 e = (p.core ? p.plan.cores : p.plan.tiles)[tile];
+        kv = item - tile * p.per;
+        split = p.by_Hkv.div(kv);
+        kv -= split * p.Hkv;
         row0 = e.x, n = e.y, core0 = e.w;
-        n_keys = p.core ? seen_cores(n, p.plan.w, p.plan.g) : n;
+        n_keys = p.core ? p.plan.seen_of(n) : n;
         y0 = ((n_keys + BT - 1) / BT - 1 - e.z) * BT;  // the list's order is by the rows behind a key
         // the query rows [lo, hi] that see at least one key of the tile
         int lo = y0, hi = n - 1;
@@ -491,17 +496,23 @@ struct DkvItem {
         }
         // (query tile, head) pairs from the last tile down, heads fastest: the CTAs of a KV head then read
         // the same Q and dO tiles at about the same time, so they come from L2
-        n_it = max(qt_hi - qt_lo + 1, 0) * (p.Hq / p.Hkv);
+        n_it = max(qt_hi - qt_lo + 1, 0) * p.r;
     }
     // the last row whose window holds token m (it may lie behind the sequence)
     __device__ static __forceinline__ int64_t last_row(const Args &p, int m) {
-        return p.plan.window_mode ? static_cast<int64_t>(m / p.plan.g + 1) * p.plan.g + p.plan.w - 2 : static_cast<int64_t>(m) + p.plan.w - 1;
+        return p.plan.window_mode ? static_cast<int64_t>(p.plan.by_g.div(m) + 1) * p.plan.g + p.plan.w - 2 : static_cast<int64_t>(m) + p.plan.w - 1;
     }
-    __device__ __forceinline__ int head(const Args &p, int x) const {
-        const int r = p.Hq / p.Hkv;
-        return kv * r + x % r;
+};
+// The (query tile, head) pairs of an item in order.
+struct Walk {
+    int h, i0, first, r;
+    __device__ __forceinline__ Walk(const Args &p, const DkvItem &d) : h(d.kv * p.r), i0(d.qt_hi * BT), first(d.kv * p.r), r(p.r) {}
+    __device__ __forceinline__ void next() {
+        if (++h == first + r) {
+            h = first;
+            i0 -= BT;
+        }
     }
-    __device__ __forceinline__ int first_row(const Args &p, int x) const { return (qt_hi - x / (p.Hq / p.Hkv)) * BT; }
 };
 
 template <int HD>
@@ -538,8 +549,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 load_tile<HD>(&tmV, c.bar(B_RES), c.res(1), y, d.kv);
             }
             ++nr;
-            for (int x = 0; x < d.n_it; ++x, ++g) {
-                const int i0 = d.first_row(p, x), h = d.head(p, x);
+            Walk at(p, d);
+            for (int x = 0; x < d.n_it; ++x, ++g, at.next()) {
+                const int i0 = at.i0, h = at.h;
                 if (!(ok = c.wait(c.bar(B_LEMPTY + g % LONG_ST), ((g / LONG_ST) & 1) ^ 1))) break;
                 if (!(ok = load_cut_tile<HD>(&tmQ, c.bar(B_LFULL + g % LONG_ST), c.bar(B_CUT), cut, c.stage_l(g), d.row0 + i0, h, d.n - i0,
                                              c.abort_flag, c.lim)))
@@ -630,17 +642,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int m = d.y0 + row;  // this thread's key (core or token of the sequence)
             const bool valid = m < d.n_keys;
             const int64_t key_last = p.core ? 0 : DkvItem::last_row(p, m);
-            auto slot_value = [&](int x) -> float {
-                const int iq = d.first_row(p, x) + (e & (BT - 1));
+            Walk at(p, d);  // the tile whose LSE and D come next
+            auto slot_value = [&]() -> float {
+                const int iq = at.i0 + (e & (BT - 1));
                 if (iq >= d.n) return 0.f;
-                const int64_t off = static_cast<int64_t>(d.head(p, x)) * p.plan.T + d.row0 + iq;
+                const int64_t off = static_cast<int64_t>(at.h) * p.plan.T + d.row0 + iq;
                 return e < BT ? p.LSE[off] * LOG2E : p.space.D[off];
             };
-            if (d.n_it > 0) slot_f[e] = slot_value(0);  // nobody reads the slot behind the last item's last barrier
+            if (d.n_it > 0) slot_f[e] = slot_value();  // nobody reads the slot behind the last item's last barrier
             ptx::named_bar_sync(1, 256);
             // the pooling's share of a raw token: a_m dKc_j + (tau/r) ds_m qsum_j and a_m dVc_j, j its group
-            const int c0 = ch * (HD / 2), j = valid ? m / p.plan.g : 0;
-            const bool fuse = !p.core && p.cores != 0 && valid && j < seen_cores(d.n, p.plan.w, p.plan.g);
+            const int c0 = ch * (HD / 2), j = valid ? p.plan.by_g.div(m) : 0;
+            const bool fuse = !p.core && p.cores != 0 && valid && j < p.plan.seen_of(d.n);
             const int64_t uj = (static_cast<int64_t>(d.kv) * p.plan.G + d.core0 + j) * HD + c0;
             float am = 0.f, cm = 0.f;
             if (fuse) {
@@ -649,7 +662,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 cm = p.space.cds[um];
             }
             for (int x = 0; x < d.n_it; ++x, ++g) {
-                const float v_next = x + 1 < d.n_it ? slot_value(x + 1) : 0.f;
+                const int i0 = at.i0;
+                at.next();
+                const float v_next = x + 1 < d.n_it ? slot_value() : 0.f;
                 if (fuse && x == d.n_it - 1) {
                     // bring this row's half of dKc_j, dVc_j and qsum_j into L1 for the end
 #pragma unroll
@@ -662,7 +677,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (ok) ok = c.wait(c.bar(B_S), g & 1);
                 uint32_t pa[32], pb[32];
                 // this key's visible query columns [q_lo, q_hi] of the tile
-                const int i0 = d.first_row(p, x);
                 int q_lo = 0, q_hi = -1;
                 if (valid && p.core) {
                     q_lo = max((m + 1) * p.plan.g + p.plan.w - 1 - i0, 0);
@@ -828,8 +842,14 @@ cudaError_t launch(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaS
     p.LSE = a.LSE;
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
+    p.r = a.Hq / a.Hkv;
     p.tau = a.scale;
     p.core = part == 0;
+    p.per = a.Hkv * (p.core ? w.splits : 1);
+    p.by_Hq = fast_div(a.Hq);
+    p.by_Hkv = fast_div(a.Hkv);
+    p.by_r = fast_div(p.r);
+    p.by_per = fast_div(p.per);
     p.cores = a.Kc != nullptr;
     p.wait_limit_ns = g_wait_limit_ns;
     p.skip_loads = g_skip_q_load;
