@@ -87,10 +87,11 @@ constexpr int B_S = 12;                     // S is there
 constexpr int B_SREAD = 13;                 // dq: S is in registers
 constexpr int B_DP = 14;                    // 2: dP is there (dkv uses the first)
 constexpr int B_P = 16;                     // P (dkv) is there
-constexpr int B_DS = 17;                    // dS is there
-constexpr int B_DONE = 18;                  // the item's sums are there
-constexpr int B_ACCFREE = 19;               // ... have been read
-constexpr int B_DRAIN = 20, B_CUT = 21, N_BARS = 22;
+constexpr int B_DS = 17;                    // 2: dS is there (dkv uses the first).  dq: a warp that is ahead may finish the next
+                                            // tile, whose products are done, before the others finish this one
+constexpr int B_DONE = 19;                  // the item's sums are there
+constexpr int B_ACCFREE = 20;               // ... have been read
+constexpr int B_DRAIN = 21, B_CUT = 22, N_BARS = 23;
 
 template <int HD>
 __device__ __forceinline__ void load_tile(const void *map, uint32_t bar, uint32_t dst, int y, int z) {
@@ -202,7 +203,7 @@ __device__ __forceinline__ Cta<HD> setup(uint8_t *smem_raw, const Args &p) {
     c.lim = p.wait_limit_ns;
     if (threadIdx.x == 0) {
         for (int k = 0; k < N_BARS; ++k)  // one arrival, but for those of the eight element-wise warps
-            ptx::mbar_init(c.bar(k), k == B_SREAD || k == B_P || k == B_DS || k == B_ACCFREE ? 8 : 1);
+            ptx::mbar_init(c.bar(k), k == B_SREAD || k == B_P || k == B_DS || k == B_DS + 1 || k == B_ACCFREE ? 8 : 1);
         *c.abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 } else {
                     ptx::tc_commit_warp(c.bar(B_RESFREE));
                 }
-                if (!(ok = c.wait(c.bar(B_DS), g & 1))) break;
+                if (!(ok = c.wait(c.bar(B_DS + (g & 1)), (g >> 1) & 1))) break;
                 if (x == 0 && !(ok = c.wait(c.bar(B_ACCFREE), (it & 1) ^ 1))) break;
                 ptx::tc_fence_after();
                 ptx::mma_ts_k128_split_warp(c.tmem + T_DQ, c.tmem + T_DP + 128u * (g & 1),
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(c.bar(B_DS));
+                if (lane == 0) ptx::mbar_arrive(c.bar(B_DS + (g & 1)));
             }
             if (!ok || !(ok = c.wait(c.bar(B_DONE), it & 1))) break;
             ptx::tc_fence_after();
