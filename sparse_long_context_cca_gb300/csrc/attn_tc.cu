@@ -39,11 +39,10 @@
 //
 // PACKED: the same kernel over packed sequences (packed.cuh).  An item's rows, its sequence's first row
 // and its cores come from the batch's plan, rows keep their indices in their sequence, and tensors are
-// read and written by strides.  What is masked must not reach an output, not even as 0 * NaN, so on a tile
-// that it masks a softmax group takes the values through its hands, a key to a thread: keys behind the
-// sequence's end (a tile there holds rows of the next one) are set to zero, the others are looked through
-// (one multiply-add per two values), and where one is not finite the half's rows of this item are computed
-// again, key by key on the CUDA cores, as the epilogue (direct_rows).  A short sequence (n <= 256 / 2^k)
+// read and written by strides.  What is masked must not reach an output, not even as 0 * NaN: the producer
+// sets values behind a sequence's end (the next sequence's) to zero before it hands over the tile that holds
+// them, and where a row's sums are not finite at its end it is computed again, key by key on the CUDA cores
+// (direct_rows), since a later token's value may have done it.  A short sequence (n <= 256 / 2^k)
 // fills an item with 2^k query heads of a KV head side by side, 128 / 2^k rows of each in a half, as far as
 // 2^k divides the heads: an item costs 4 us whatever it holds.  d = 64 is built for packed sequences alone.
 #include <cuda.h>
@@ -84,7 +83,8 @@ constexpr int B_PFULL = B_SFULL + 2;    // 2
 constexpr int B_PVDONE = B_PFULL + 2;   // 2
 constexpr int B_OFREE = B_PVDONE + 2;   // 2
 constexpr int B_DRAIN = B_OFREE + 2;
-constexpr int NUM_BARS = B_DRAIN + 1;
+constexpr int B_CUT = B_DRAIN + 1;      // PACKED: copies of a tile that ends behind its sequence
+constexpr int NUM_BARS = B_CUT + 1;
 
 // shared-memory layout for head dimension HD (offsets from a 1024-byte aligned base)
 template <int HD>
@@ -96,8 +96,7 @@ struct Layout {
     static constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE_BYTES;
     static constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
     static constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-    static constexpr uint32_t OFF_MARK = OFF_ABORT + 4;  // PACKED: items with a value that is not finite, [half][item parity]
-    static constexpr uint32_t OFF_BEGIN = OFF_MARK + 16;  // PACKED: begin[3] of make_item, and the number of items
+    static constexpr uint32_t OFF_BEGIN = OFF_ABORT + 4;  // PACKED: begin[3] of make_item, and the number of items
     static constexpr uint32_t SMEM_BYTES = OFF_BEGIN + 16 + 1024;  // slack for manual alignment
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -244,6 +243,15 @@ __device__ __forceinline__ int item_at(int round) {
     return PACKED ? item_of_round(round) : static_cast<int>(blockIdx.x + round * gridDim.x);
 }
 
+// PACKED producer: an item's whole groups, the tensor row of a row of its sequence, and the map of its queries.
+__device__ __forceinline__ int groups_of(const PackedParams &p, const Item &it) { return p.plan.by_g.div(it.n); }
+__device__ __forceinline__ int groups_of(const Params &, const Item &) { return 0; }
+__device__ __forceinline__ int tensor_row(const Params &, const Item &it, int row) { return it.row0 + row; }
+__device__ __forceinline__ const CUtensorMap *q_map(const PackedParams &p, const CUtensorMap *one, const Item &it) {
+    return it.lr < 7 ? &p.mQ[6 - it.lr] : one;
+}
+__device__ __forceinline__ const CUtensorMap *q_map(const Params &, const CUtensorMap *one, const Item &) { return one; }
+
 // Parity of the FULL barrier of the ring slot holding K for ring index u (u even).
 // Only K slots complete a FULL barrier (the tile's V copy completes the same one),
 // and with NS odd an even u reaches each slot once every 2*NS indices.
@@ -253,10 +261,10 @@ __device__ __forceinline__ void report_timeout(const Params &p) {
     if (p.status != nullptr) atomicCAS(p.status, 0, static_cast<int32_t>(-4));
 }
 
-// 32 rows of a half, from its row `first` on, by the definition, in fp32 and key by key, only visible keys
-// read: for items in which a masked tile holds a value that is not finite.
+// Rows of a half, `which` of the 32 from its row `first` on, by the definition, in fp32 and key by key, only
+// visible keys read: for rows whose sums are not finite.
 template <int HD>
-__device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, const Half &x, int first) {
+__device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, const Half &x, int first, unsigned which) {
     constexpr int E = HD / 32;  // columns of a lane
     const int lane = threadIdx.x & 31;
     auto load = [&](const __nv_bfloat16 *row, float (&f)[E]) {
@@ -264,9 +272,9 @@ __device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, 
         for (int e = 0; e < E; ++e) f[e] = __bfloat162float(row[lane * E + e]);
     };
     const int64_t cores = (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD;
-    for (int row = first; row < first + 32; ++row) {
+    for (; which != 0; which &= which - 1) {
+        const int row = first + __ffs(which) - 1;
         const int i = x.a + (row & ((1 << it.lr) - 1)), h = it.h + (row >> it.lr);
-        if (i > x.b) continue;
         float q[E], o[E], m = -INFINITY, l = 0.f;
         load(p.rQ.at(h, it.row0 + i), q);
 #pragma unroll
@@ -316,29 +324,6 @@ __device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, 
     }
 }
 
-// One key's values in a tile in shared memory: set to zero, or looked through; true where one of them is an
-// infinity or NaN (x * 0 is 0 for all else, so one packed multiply-add per two values collects them).  The
-// chunks are taken in the order of the swizzle, so that eight neighbouring keys read different banks.
-template <int HD>
-__device__ __forceinline__ bool clean_key(uint32_t tile, int key, bool clear) {
-    const uint32_t row = tile + key * 128, turn = key & 7;
-    uint32_t acc = 0;
-#pragma unroll
-    for (int x = 0; x < HD / 8; ++x) {
-        const uint32_t at = row + (x / 8) * HALF_BYTES + (((x & 7) ^ turn) << 4);
-        if (clear) {
-            ptx::st_shared_v4(at, 0.f, 0.f, 0.f, 0.f);
-        } else {
-            const uint4 v = ptx::ld_shared_v4(at);
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.x), "r"(0u));
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.y), "r"(0u));
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.z), "r"(0u));
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.w), "r"(0u));
-        }
-    }
-    return (acc & 0x7fff7fffu) != 0;
-}
-
 template <bool PACKED, int HD>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_bf16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -374,9 +359,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::mbar_init(bar(B_OFREE + h), 4);
         }
         ptx::mbar_init(bar(B_DRAIN), 1);
+        ptx::mbar_init(bar(B_CUT), 1);
         *abort_flag = 0;
         if constexpr (PACKED) {
-            for (int k = 0; k < 4; ++k) reinterpret_cast<volatile int *>(gbase + L::OFF_MARK)[k] = 0;
             const int pairs = max(plan_counts(p.plan).x, 0);
             const int3 s = pairs > 0 ? plan_short(p.plan) : make_int3(0, 0, 0);
             const int first[5] = {0, p.most >= 1 ? s.x : pairs, p.most >= 2 ? s.y : pairs, p.most >= 3 ? s.z : pairs, pairs};
@@ -402,7 +387,79 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     else n_items = p.n_items;
 
     if (warp < 2) {
-        if (warp == 0 && lane == 0) {
+        if (PACKED && warp == 0) {
+            // ------------------------------------------------------------ producer over packed sequences: the
+            // whole warp, for the tiles that end behind their sequence
+            if (lane == 0) {
+                ptx::prefetch_tmap(&tmQ);
+                ptx::prefetch_tmap(&tmK);
+                ptx::prefetch_tmap(&tmV);
+                ptx::prefetch_tmap(&tmKc);
+                ptx::prefetch_tmap(&tmVc);
+            }
+            auto wwait = [&](uint32_t b, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, ptx::wait_bounded(b, parity, abort_flag, lim));
+            };
+            uint32_t u = 0, cut = 0;  // ring loads issued so far, tiles cut
+            int n_iter = 0;
+            bool ok = true;
+            for (int k; ok && (k = item_at<PACKED>(n_iter)) < n_items; ++n_iter) {
+                const Item it = make_item<PACKED>(p, k, begin);
+                const int groups = groups_of(p, it);
+                if (!wwait(bar(B_QFREE), (n_iter & 1) ^ 1)) break;
+                if (!p.skip_q_load && lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * TILE_BYTES);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t dst = base + OFF_Q + h * TILE_BYTES;
+                        const int row0 = tensor_row(p, it, h ? it.hB.a : it.hA.a);
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x)
+                            ptx::tma_load_3d(q_map(p, &tmQ, it), bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
+                    }
+                }
+                for (int t = 0; t < it.T; ++t, u += 2) {
+                    const bool core = t < it.Tc;
+                    const int first = core ? t * BN : it.lo0 + (t - it.Tc) * BN;  // the tile's first key in the sequence
+                    const int left = (core ? groups : it.n) - first;
+                    const int y = (core ? it.core0 : it.row0) + first;
+                    const int ks = u % NS, vs = (u + 1) % NS;
+                    if (!(ok = wwait(bar(B_EMPTY + ks), ((u / NS) & 1) ^ 1) && wwait(bar(B_EMPTY + vs), (((u + 1) / NS) & 1) ^ 1))) break;
+                    const uint32_t full = bar(B_FULL + ks), here = left < BN ? bar(B_CUT) : full;
+                    const uint32_t kdst = base + OFF_RING + ks * TILE_BYTES, vdst = base + OFF_RING + vs * TILE_BYTES;
+                    if (lane == 0) {
+                        const void *mk = core ? (const void *)&tmKc : (const void *)&tmK;
+                        const void *mv = core ? (const void *)&tmVc : (const void *)&tmV;
+                        ptx::mbar_arrive_expect_tx(here, 2 * TILE_BYTES);
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mk, here, kdst + x * HALF_BYTES, 64 * x, y, it.kvz);
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mv, here, vdst + x * HALF_BYTES, 64 * x, y, it.kvz);
+                    }
+                    __syncwarp();
+                    if (left >= BN) continue;
+                    if (!(ok = wwait(bar(B_CUT), cut & 1))) {
+                        volatile int never = 0;  // these copies land before the CTA exits
+                        ptx::wait_bounded(bar(B_CUT), cut & 1, &never, lim);
+                        break;
+                    }
+                    ++cut;
+                    for (int i = left * 8 + lane; i < BN * 8; i += 32)
+#pragma unroll
+                        for (int x = 0; x < HALVES; ++x) ptx::st_shared_v4(vdst + x * HALF_BYTES + i * 16, 0.f, 0.f, 0.f, 0.f);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(full);
+                }
+            }
+            __syncwarp();
+            if (*abort_flag) {
+                // Let the copies already issued land before the CTA exits.
+                volatile int never = 0;
+                for (uint32_t v = u > 2 * NS ? u - 2 * NS : 0; v < u; v += 2)
+                    ptx::wait_bounded(bar(B_FULL + v % NS), k_full_parity(v), &never, lim);
+                if (!p.skip_q_load && n_iter > 0) ptx::wait_bounded(bar(B_QFULL), (n_iter - 1) & 1, &never, lim);
+            }
+        } else if (!PACKED && warp == 0 && lane == 0) {
             // ------------------------------------------------------------ producer
             ptx::prefetch_tmap(&tmQ);
             ptx::prefetch_tmap(&tmK);
@@ -419,24 +476,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * TILE_BYTES);
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t dst = base + OFF_Q + h * TILE_BYTES;
-                        int row0 = h ? it.hB.a : it.hA.a;
-                        const CUtensorMap *map = &tmQ;
-                        if constexpr (PACKED) {
-                            row0 += it.row0;
-                            if (it.lr < 7) map = &p.mQ[6 - it.lr];
-                        } else {
-                            row0 -= p.q_off;
-                        }
+                        const int row0 = (h ? it.hB.a : it.hA.a) - p.q_off;
 #pragma unroll
                         for (int x = 0; x < HALVES; ++x)
-                            ptx::tma_load_3d(map, bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
+                            ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
                     }
                 }
                 for (int t = 0; ok && t < it.T; ++t, u += 2) {
                     const bool core = t < it.Tc;
-                    int y;
-                    if constexpr (PACKED) y = core ? it.core0 + t * BN : it.row0 + it.lo0 + (t - it.Tc) * BN;
-                    else y = core ? t * BN : it.lo0 + (t - it.Tc) * BN - p.kv_off;
+                    const int y = core ? t * BN : it.lo0 + (t - it.Tc) * BN - p.kv_off;
                     // K(t) goes to ring slot u % NS, V(t) to the next one; both copies
                     // complete the K slot's FULL barrier (u is even, see k_full_parity)
                     const int ks = u % NS, vs = (u + 1) % NS;
@@ -645,13 +693,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t sf_cnt = 0;
         int n_done = 0;  // items of this half finished
         bool ok = true;
-        [[maybe_unused]] uint32_t ubase = 0;  // ring loads before this item (PACKED)
-        [[maybe_unused]] volatile int *const mark = reinterpret_cast<volatile int *>(gbase + L::OFF_MARK) + 2 * h;
         for (int round = 0, k; ok && (k = item_at<PACKED>(round)) < n_items; ++round) {
             const Item it = make_item<PACKED>(p, k, begin);
             const Half x = h ? it.hB : it.hA;
-            [[maybe_unused]] const uint32_t u0 = ubase;
-            ubase += 2 * it.T;
             if (!x.valid) continue;
             int i = x.a + row;
             if constexpr (PACKED) i = x.a + (row & ((1 << it.lr) - 1));
@@ -691,28 +735,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 // row max: 3-input max over eight independent partial maxima
                 float mp[8];
-                if constexpr (PACKED) {
-                    // Items of one half follow one another by at most one between its warps (a tile needs the
-                    // arrivals of all four), so two marks by parity are enough; a warp sees its neighbours'
-                    // marks once the item's last product, which waits for their arrivals, is done.
-                    if (masked) {
-                        const bool core = t < it.Tc;
-                        const int key = core ? t * BN + row : it.lo0 + (t - it.Tc) * BN + row;
-                        const bool past = key >= (core ? p.plan.by_g.div(it.n) : it.n);
-                        if (clean_key<HD>(base + OFF_RING + ((u0 + 2 * t + 1) % NS) * TILE_BYTES, row, past))
-                            mark[n_done & 1] = n_done + 1;
-                        // the other half, where it uses the tile, masks it too and writes the same zeros
-                        if (past) ptx::fence_proxy_async_smem();
-                    }
-                }
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
+                        if constexpr (PACKED) {
+                            // most 32-column pieces of a masked tile lie wholly inside every row's part; in the others
+                            // a column is a bit (with comparisons a masked tile took 1.8 us, three times a plain one)
+                            if (__all_sync(0xffffffffu, c_lo <= c * 32 && c_hi >= c * 32 + 31)) continue;
+                            const uint32_t seen = ptx::bits(c_lo - c * 32, c_hi - c * 32);
 #pragma unroll
-                        for (int kk = 0; kk < 32; ++kk) {
-                            const int col = c * 32 + kk;
-                            const float x = __uint_as_float(s[c][kk]);
-                            s[c][kk] = __float_as_uint((col < c_lo || col > c_hi) ? -INFINITY : x);
+                            for (int kk = 0; kk < 32; ++kk)
+                                if (!(seen & (1u << kk))) s[c][kk] = __float_as_uint(-INFINITY);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < 32; ++kk) {
+                                const int col = c * 32 + kk;
+                                const float x = __uint_as_float(s[c][kk]);
+                                s[c][kk] = __float_as_uint((col < c_lo || col > c_hi) ? -INFINITY : x);
+                            }
                         }
                     }
                 }
@@ -818,12 +858,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_OFREE + h));
+            [[maybe_unused]] unsigned bad = 0;  // rows of this warp with a sum that is not finite
             if constexpr (PACKED) {
-                if (mark[n_done & 1] == n_done + 1) {  // the same for the whole warp: every arrival was waited for
-                    direct_rows<HD>(p, it, x, quarter * 32);
-                    ++n_done;
-                    continue;
-                }
+                uint64_t odd = 0;  // stays zero as long as every sum is finite
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        odd = ptx::fma2(ptx::f2(__uint_as_float(o[c][k]), __uint_as_float(o[c][k + 1])), 0, odd);
+                float a, b;
+                ptx::f2_split(odd, a, b);
+                bad = __ballot_sync(0xffffffffu, valid && !(a + b == 0.f));
+                if ((bad >> lane) & 1) valid = false;
             }
             // O / l as bf16, one 32-byte sector per store (two 16-byte stores if O is
             // only 16-byte aligned)
@@ -848,6 +894,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (valid) *lse = (m + __log2f(l)) * 0.6931471805599453f;
+            if constexpr (PACKED) {
+                if (bad != 0) direct_rows<HD>(p, it, x, quarter * 32, bad);
+            }
             ++n_done;
         }
     }

@@ -174,6 +174,14 @@ __device__ __forceinline__ void store32_f32(const uint32_t (&v)[32], float scale
                                                            __uint_as_float(v[q + 2]) * scale, __uint_as_float(v[q + 3]) * scale);
 }
 
+// Zero where a column's bit is not set; `whole`: all bits of all lanes are.
+__device__ __forceinline__ void clear_unseen(uint32_t (&v)[32], uint32_t seen, bool whole) {
+    if (whole) return;
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        if (!(seen & (1u << k))) v[k] = 0u;
+}
+
 // What every role has.
 template <int HD>
 struct Cta {
@@ -400,21 +408,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(c.bar(B_SREAD));  // the next S may come
                 // P = 2^(S tau log2e - LSE), zero off the visible columns
-                const bool whole = __all_sync(0xffffffffu, c_lo <= h0 && c_hi >= h0 + 63);
-                if (whole) {
+                const uint32_t seen[2] = {ptx::bits(c_lo - h0, c_hi - h0), ptx::bits(c_lo - h0 - 32, c_hi - h0 - 32)};
+                const bool whole[2] = {__all_sync(0xffffffffu, seen[0] == 0xffffffffu) != 0, __all_sync(0xffffffffu, seen[1] == 0xffffffffu) != 0};
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        pa[k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pa[k]), c1, -lse2)));
-                        pb[k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pb[k]), c1, -lse2)));
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int ca = h0 + k, cb = h0 + 32 + k;
-                        pa[k] = (ca >= c_lo && ca <= c_hi) ? __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pa[k]), c1, -lse2))) : 0u;
-                        pb[k] = (cb >= c_lo && cb <= c_hi) ? __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pb[k]), c1, -lse2))) : 0u;
-                    }
+                for (int k = 0; k < 32; ++k) {
+                    pa[k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pa[k]), c1, -lse2)));
+                    pb[k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pb[k]), c1, -lse2)));
                 }
+                clear_unseen(pa, seen[0], whole[0]);
+                clear_unseen(pb, seen[1], whole[1]);
                 if (!(ok = c.wait(c.bar(B_DP + (g & 1)), (g >> 1) & 1))) break;
                 ptx::tc_fence_after();
                 // dS = P (dP - D), bf16 pairs written over the dP columns [h0, h0 + 32), which this warp has
@@ -424,11 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t dp[32], pk[16];
                     ptx::tmem_ld32(sD + 32 * j, dp);
                     ptx::tmem_wait_ld(dp);
-                    if (!whole) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (h0 + 32 * j + k < c_lo || h0 + 32 * j + k > c_hi) dp[k] = 0u;
-                    }
+                    clear_unseen(dp, seen[j], whole[j]);
                     const uint32_t *pp = j ? pb : pa;
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
@@ -687,7 +685,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     q_lo = max(m - i0, 0);
                     q_hi = min(last_i - i0, BT - 1);
                 }
-                const bool whole = __all_sync(0xffffffffu, q_lo <= h0 && q_hi >= h0 + 63);
+                const uint32_t seen[2] = {ptx::bits(q_lo - h0, q_hi - h0), ptx::bits(q_lo - h0 - 32, q_hi - h0 - 32)};
+                const bool whole[2] = {__all_sync(0xffffffffu, seen[0] == 0xffffffffu) != 0, __all_sync(0xffffffffu, seen[1] == 0xffffffffu) != 0};
                 if (ok) {
                     ptx::tc_fence_after();
                     const uint32_t sS = lane_addr + h0;
@@ -707,13 +706,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             pb[4 * q + k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pb[4 * q + k]), c1, -lsb[k])));
                         }
                     }
-                    if (!whole) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            if (h0 + k < q_lo || h0 + k > q_hi) pa[k] = 0u;
-                            if (h0 + 32 + k < q_lo || h0 + 32 + k > q_hi) pb[k] = 0u;
-                        }
-                    }
+                    clear_unseen(pa, seen[0], whole[0]);
+                    clear_unseen(pb, seen[1], whole[1]);
                     uint32_t pk[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) pk[k] = ptx::pack_bf16x2(__uint_as_float(pa[2 * k]), __uint_as_float(pa[2 * k + 1]));
@@ -737,11 +731,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int j = 0; j < 2; ++j) {
                         ptx::tmem_ld32(sD + 32 * j, dp);
                         ptx::tmem_wait_ld(dp);
-                        if (!whole) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (h0 + 32 * j + k < q_lo || h0 + 32 * j + k > q_hi) dp[k] = 0u;
-                        }
+                        clear_unseen(dp, seen[j], whole[j]);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             const float4 dv = slot4[(BT + h0) / 4 + 8 * j + q];

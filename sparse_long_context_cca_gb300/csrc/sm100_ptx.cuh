@@ -349,6 +349,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn_maj
 
 
 
+// The bits [from, to] of a word; either end may lie outside it.
+__device__ __forceinline__ uint32_t bits(int from, int to) {
+    const int a = from > 0 ? from : 0, z = to < 31 ? to : 31;
+    return a > z ? 0u : (0xffffffffu << a) & (0xffffffffu >> (31 - z));
+}
+
 // max(a, b, c) in one instruction.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
