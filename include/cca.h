@@ -561,7 +561,7 @@ int cca_pages_compact(const cca_pages_t *pages, const int32_t *lens, const int32
  * and lays out their work in `plan`: the tiles of all sequences by falling cost, every token's position,
  * every group's first token.  The lengths stay on the device: the host never waits, and a captured call
  * serves later lengths.  The calls below read the plan alone; a plan that cca_pack did not finish, or
- * made for another T, g, w or window_mode than the call's, is reported in *dev_status
+ * made for another S, T, g, w or window_mode than the call's, is reported in *dev_status
  * (CCA_ERR_INVALID_ARG) and nothing is written.
  * cu_seqlens that fall, start below 0 or end above T are reported and make such a plan.
  */
@@ -583,7 +583,8 @@ uint64_t cca_pack_positions_offset(int S, int T, int g);
 int cca_pack(const int32_t *cu_seqlens, const cca_packed_t *packed, int32_t *dev_status, void *stream);
 
 /* A packed tensor [H, T, d]: columns contiguous, every row 16-byte aligned, strides (elements) of head
- * and row.  Those of a result may not make two rows share memory. */
+ * and row, each at least d (where there is more than one).  A result's rows may share no memory with one
+ * another nor with another tensor of the call; tensors may be slices of the columns of one wider tensor. */
 typedef struct cca_packed_rows {
     void *p;
     int64_t head_stride, row_stride;
@@ -602,7 +603,7 @@ int cca_pool_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, cons
  * cca_attn_packed - the fusion equation for every row of every sequence.  O by strides, LSE [Hq, T] fp32.
  * Kc, Vc may be NULL where w >= T.  What a row does not see (later tokens, other sequences, other
  * cores) never reaches its output, whatever it holds.
- * Supported: bf16 or f32, d in {64, 128}; bf16 with d = 128 on the tensor cores.
+ * Supported: bf16 (on the tensor cores) or f32, d in {64, 128}.
  */
 int cca_attn_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const cca_packed_rows_t *V, const void *Kc,
                     const void *Vc, const cca_packed_rows_t *O, float *LSE, const cca_packed_t *packed,

@@ -787,7 +787,7 @@ def cca_packed_clear(packed: Packed, *tensors, stream=None):
 def _packed_rows(t):
     """t itself where its rows can be read in place, a contiguous copy otherwise."""
     es = t.element_size()
-    ok = t.stride(2) == 1 and all(s >= 0 and s * es % 16 == 0 for s in t.stride()[:2]) and t.data_ptr() % 16 == 0
+    ok = t.stride(2) == 1 and all(s >= t.shape[2] and s * es % 16 == 0 for s in t.stride()[:2]) and t.data_ptr() % 16 == 0
     return t if ok else t.contiguous()
 
 
@@ -800,7 +800,7 @@ class CcaPackedAttentionFunction(torch.autograd.Function):
         Q, K, V = (_packed_rows(t) for t in (Q, K, V))
         O, LSE, Kc, Vc = cca_prefill_packed(Q, K, V, packed, scale, pool_mode)
         cca_packed_clear(packed, O)
-        ctx.save_for_backward(Q, K, V, Kc, Vc, O, LSE)
+        ctx.save_for_backward(Q, K, V, Kc, Vc, O, LSE, packed.plan)   # a plan made anew before the backward pass is refused
         ctx.cfg = (packed, scale, pool_mode)
         return O
 
@@ -809,7 +809,7 @@ class CcaPackedAttentionFunction(torch.autograd.Function):
     def backward(ctx, dO):
         if torch.cuda.is_current_stream_capturing():
             (_fast or _bound()).check_leaves()
-        Q, K, V, Kc, Vc, O, LSE = ctx.saved_tensors
+        Q, K, V, Kc, Vc, O, LSE, _ = ctx.saved_tensors
         packed, scale, pool_mode = ctx.cfg
         grads = cca_packed_bwd(Q, K, V, Kc, Vc, O, LSE, _packed_rows(dO.to(Q.dtype)), packed, scale, pool_mode)
         cca_packed_clear(packed, *grads)

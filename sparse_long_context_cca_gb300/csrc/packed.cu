@@ -24,7 +24,7 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // One block column per sequence.  Entry (s, p) of a list stands behind every entry of a higher tile number
 // and behind those of the same number of longer sequences (of equal ones, the earlier first): its place is
 // the sum over all sequences s' of max(0, tiles(s') - p - 1), and the rank of s by length.  So a block needs no
-// other block's result, and nothing is sorted; a thread's entry costs a walk over the lengths.
+// other block's result, and nothing is sorted; an entry costs a walk over the lengths, which a warp shares.
 __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const int32_t *cu, char *plan, const PlanLayout l, int S, int T, int g,
                                                             int w, int window_mode, int32_t *status) {
     const int s = blockIdx.x;
@@ -59,10 +59,11 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const int32_t *cu, c
     for (int list = 0; list < 3; ++list) {
         const int mine = tiles_of(list, n);
         int4 *out = reinterpret_cast<int4 *>(plan + at[list]);
-        for (int p = tid; p < mine; p += step) {
-            int place = rank;
-            for (int i = 0; i < S; ++i) place += max(0, tiles_of(list, cu[i + 1] - cu[i]) - p - 1);
-            out[place] = make_int4(a, n, p, a / g);
+        for (int p = tid / 32; p < mine; p += step / 32) {
+            int place = 0;
+            for (int i = tid % 32; i < S; i += 32) place += max(0, tiles_of(list, cu[i + 1] - cu[i]) - p - 1);
+            place = __reduce_add_sync(kFull, place) + rank;
+            if (tid % 32 == 0) out[place] = make_int4(a, n, p, a / g);
         }
     }
     int32_t *positions = reinterpret_cast<int32_t *>(plan + l.positions), *first = reinterpret_cast<int32_t *>(plan + l.first);
@@ -484,29 +485,47 @@ int params_packed(const cca_params_t *p) {
     return CCA_OK;
 }
 
-bool rows_ok(const cca_packed_rows_t *r, int H, int T, const cca_params_t &p, bool written, Span &out) {
+// Where a tensor lies: from its first byte to its last, and, where all heads of a token stand within one
+// row of `row` bytes, how much of that row they take.
+struct Place {
+    Span span;
+    uint64_t row, inner;  // row 0: not of that kind
+};
+
+bool rows_ok(const cca_packed_rows_t *r, int H, int T, const cca_params_t &p, bool written, Place &out) {
     if (r == nullptr) return false;
     const int es = p.dtype == CCA_BF16 ? 2 : 4;
     const int64_t size[3] = {1, H, T}, stride[3] = {0, r->head_stride, r->row_stride};
-    if (!span_of(r->p, stride, size, p.d, es, out)) return false;
-    // the copy engine takes strides of at least a row's bytes, below 2^40
-    if (H > 1 && (r->head_stride < 0 || r->head_stride * es >= (int64_t{1} << 40))) return false;
-    if (T > 1 && (r->row_stride < 0 || r->row_stride * es >= (int64_t{1} << 40))) return false;
+    if (!span_of(r->p, stride, size, p.d, es, out.span)) return false;
+    // the copy engine's strides lie between a row's bytes and 2^40
+    if (H > 1 && (r->head_stride < p.d || r->head_stride * es >= (int64_t{1} << 40))) return false;
+    if (T > 1 && (r->row_stride < p.d || r->row_stride * es >= (int64_t{1} << 40))) return false;
+    out.inner = (static_cast<uint64_t>(H - 1) * (H > 1 ? r->head_stride : 0) + p.d) * es;
+    out.row = T > 1 && out.inner <= static_cast<uint64_t>(r->row_stride) * es ? r->row_stride * es : 0;
     return !written || rows_apart(stride, size, p.d);
 }
 
-Span bytes_at(const void *p, uint64_t n) {
+Place bytes_at(const void *p, uint64_t n) {
     const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    return {b, b + (p == nullptr ? 0 : n)};
+    return {{b, b + (p == nullptr ? 0 : n)}, 0, 0};
+}
+
+// Slices of one wider row, as queries, keys and values of a single projection are, lie between one another
+// without sharing memory.
+bool meet(const Place &a, const Place &b) {
+    if (!spans_meet(a.span, b.span)) return false;
+    if (a.row == 0 || a.row != b.row) return true;
+    const uint64_t to_b = ((b.span.lo % a.row) + a.row - a.span.lo % a.row) % a.row;  // b's place in the row that begins with a
+    return !(a.inner <= to_b && to_b + b.inner <= a.row);
 }
 
 // Whether any of what is written meets what is read or something else that is written.
-bool apart(const Span *out, int n_out, const Span *in, int n_in) {
+bool apart(const Place *out, int n_out, const Place *in, int n_in) {
     for (int i = 0; i < n_out; ++i) {
         for (int k = 0; k < n_in; ++k)
-            if (spans_meet(out[i], in[k])) return false;
+            if (meet(out[i], in[k])) return false;
         for (int k = i + 1; k < n_out; ++k)
-            if (spans_meet(out[i], out[k])) return false;
+            if (meet(out[i], out[k])) return false;
     }
     return true;
 }
@@ -611,7 +630,7 @@ int cca_pool_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, cons
     if (!packed_ok(packed)) return CCA_ERR_INVALID_ARG;
     const cca_params_t &p = *params;
     const int G = packed->T / packed->g;
-    Span in[4], out[2];
+    Place in[4], out[2];
     if (!rows_ok(Q, p.Hq, packed->T, p, false, in[0]) || !rows_ok(K, p.Hkv, packed->T, p, false, in[1]) ||
         !rows_ok(V, p.Hkv, packed->T, p, false, in[2]))
         return CCA_ERR_INVALID_ARG;
@@ -654,7 +673,7 @@ int cca_attn_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, cons
     if (!packed_ok(packed) || !word_ptr(LSE, true)) return CCA_ERR_INVALID_ARG;
     const cca_params_t &p = *params;
     const int T = packed->T, G = T / packed->g;
-    Span in[6], out[2];
+    Place in[6], out[2];
     if (!rows_ok(Q, p.Hq, T, p, false, in[0]) || !rows_ok(K, p.Hkv, T, p, false, in[1]) || !rows_ok(V, p.Hkv, T, p, false, in[2]) ||
         !rows_ok(O, p.Hq, T, p, true, out[0]))
         return CCA_ERR_INVALID_ARG;
@@ -689,13 +708,13 @@ int cca_packed_clear(const cca_packed_rows_t *tensors, const int32_t *heads, int
     if (params->d != 64 && params->d != 128) return CCA_ERR_UNSUPPORTED;
     ClearArgs a = {};
     const int es = params->dtype == CCA_BF16 ? 2 : 4;
-    Span out[4];
+    Place out[4];
     for (int i = 0; i < n; ++i) {
         if (heads[i] < 1 || heads[i] > 65535 || !rows_ok(&tensors[i], heads[i], packed->T, *params, true, out[i])) return CCA_ERR_INVALID_ARG;
         a.t[i] = {static_cast<char *>(tensors[i].p), tensors[i].head_stride * es, tensors[i].row_stride * es};
         a.heads[i] = heads[i];
     }
-    const Span plan = bytes_at(packed->plan, packed->plan_bytes);
+    const Place plan = bytes_at(packed->plan, packed->plan_bytes);
     if (!apart(out, n, &plan, 1)) return CCA_ERR_INVALID_ARG;
     const int st = check_device();
     if (st != CCA_OK) return st;
@@ -724,7 +743,7 @@ int cca_packed_bwd(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const
         return CCA_ERR_INVALID_ARG;
     const cca_params_t &p = *params;
     const int T = packed->T, G = T / packed->g;
-    Span in[9], out[4];
+    Place in[9], out[4];
     if (!rows_ok(Q, p.Hq, T, p, false, in[0]) || !rows_ok(K, p.Hkv, T, p, false, in[1]) || !rows_ok(V, p.Hkv, T, p, false, in[2]) ||
         !rows_ok(O, p.Hq, T, p, false, in[3]) || !rows_ok(dO, p.Hq, T, p, false, in[4]) || !rows_ok(dQ, p.Hq, T, p, true, out[0]) ||
         !rows_ok(dK, p.Hkv, T, p, true, out[1]) || !rows_ok(dV, p.Hkv, T, p, true, out[2]))

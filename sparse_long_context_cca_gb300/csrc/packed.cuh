@@ -45,7 +45,7 @@ inline PlanLayout plan_layout(int S, int T, int g) {
 struct Plan {
     const int4 *pairs, *tiles, *cores;
     const int32_t *header, *first;
-    int T, G, g, w, window_mode;
+    int S, T, G, g, w, window_mode;
     int max_pairs, max_tiles, max_cores;
     int32_t *status;
     FastDiv by_g;
@@ -66,6 +66,7 @@ inline Plan plan_of(const cca_packed_t &p, int32_t *status) {
     r.tiles = reinterpret_cast<const int4 *>(base + l.tiles);
     r.cores = reinterpret_cast<const int4 *>(base + l.cores);
     r.first = reinterpret_cast<const int32_t *>(base + l.first);
+    r.S = p.S;
     r.T = p.T;
     r.G = p.T / p.g;
     r.g = p.g;
@@ -83,7 +84,7 @@ inline Plan plan_of(const cca_packed_t &p, int32_t *status) {
 __device__ __forceinline__ int3 plan_counts(const Plan &p) {
     const int4 a = *reinterpret_cast<const int4 *>(p.header), b = *reinterpret_cast<const int4 *>(p.header + 4),
                c = *reinterpret_cast<const int4 *>(p.header + 8);
-    if (a.x != PACK_MAGIC || a.y != p.T || a.z != p.g || a.w != p.w || b.x != p.window_mode) {
+    if (a.x != PACK_MAGIC || a.y != p.T || a.z != p.g || a.w != p.w || b.x != p.window_mode || b.y != p.S) {
         if (threadIdx.x == 0) report(p.status, CCA_ERR_INVALID_ARG);
         return make_int3(-1, -1, -1);
     }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import packed_ref as ref
-from paged_ref import close, t64
+from paged_ref import HALF, close, t64
 from sparse_long_context_cca_gb300 import api
 
 pytestmark = pytest.mark.gpu
@@ -413,3 +413,220 @@ def test_gradients_take_nothing_from_the_workspace(dtype, d):
         g = api.cca_packed_bwd(c.Q, c.K, c.V, Kc, Vc, O, L, c.dO, c.packed, workspace=ws)
         first = g if first is None else first
         assert all(torch.equal(a, b) and not torch.isnan(a).any() for a, b in zip(g, first))
+
+
+def test_a_plan_of_another_number_of_sequences_is_reported():
+    # where the lists lie depends on the number: a plan is read only by calls of the same
+    T, d = 64, 64
+    cu = device([0, 10, 20, 30, 64])
+    Q, K, V = (rand(h, T, d, seed=i) for i, h in enumerate((2, 1, 1)))
+    p = api.cca_pack(cu, T, 4, T)
+    other = api.load_library().cca_pack_size(3, T, 4)
+    q = api.Packed(p.plan[:other], p.positions, 3, T, 4, T, 0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    O, L = torch.full_like(Q, 3.0), torch.full((2, T), 3.0, device="cuda")
+    api.cca_attn_packed(Q, K, V, None, None, q, O, L, dev_status=status)
+    assert int(status) == api.CCA_ERR_INVALID_ARG and (O == 3).all() and (L == 3).all()
+
+
+@pytest.mark.parametrize("dtype,d", KINDS, ids=IDS)
+def test_broadcast_tensors(dtype, d):
+    # heads or tokens that share memory: refused by the calls, copied by the function with gradients
+    T = 50
+    packed = api.cca_pack(device([0, 20, 50]), T, 4, 8)
+    Q = rand(4, T, d, dtype=dtype, seed=1)
+    one = rand(1, T, d, dtype=dtype, seed=2)
+    wide = one.expand(2, T, d)
+    with pytest.raises(api.CcaError):
+        api.cca_pool_packed(Q, wide, wide, packed)
+    with pytest.raises(api.CcaError):
+        api.cca_attn_packed(Q, rand(2, 1, d, dtype=dtype).expand(2, T, d), wide.contiguous(), None, None, api.cca_pack(device([0, T]), T))
+    x = [Q.clone().requires_grad_(), one.clone().requires_grad_(), one.clone().requires_grad_()]
+    y = [t.detach().clone().requires_grad_() for t in (Q, wide, wide)]
+    dO = rand(1, T, d, dtype=dtype, seed=5).expand(4, T, d)
+    a = torch.autograd.grad(api.cca_attention_packed(x[0], x[1].expand(2, T, d), x[2].expand(2, T, d), packed), x, dO)
+    b = torch.autograd.grad(api.cca_attention_packed(*y, packed), y, dO.contiguous())
+    assert torch.equal(a[0], b[0])
+    for i in (1, 2):
+        close(a[i], t64(b[i]).sum(0, keepdims=True), 2 * HALF[dtype] * np.abs(t64(b[i])).sum(0, keepdims=True), "sum over heads")
+    z = y[0].detach().requires_grad_()
+    api.cca_attention_packed(z, *(t.detach() for t in y[1:]), packed).sum().backward()      # a gradient of one element
+    assert torch.isfinite(z.grad).all()
+
+
+def test_a_plan_made_anew_before_the_backward_pass_is_refused():
+    T, d = 60, 64
+    X = [rand(h, T, d, seed=i).requires_grad_() for i, h in enumerate((2, 1, 1))]
+    f = (10000.0 ** (-torch.arange(d // 2, dtype=torch.float64) / (d // 2))).cuda()
+    for freq in (None, f):
+        p = api.cca_pack(device([0, 20, 60]), T, 4, 8)
+        O = api.cca_attention_packed(*X, p, inv_freq=freq)
+        api.cca_pack(device([0, 30, 60]), T, 4, 8, plan=p.plan)
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            torch.autograd.grad(O.sum(), X)
+
+
+@pytest.mark.parametrize("r", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("d", [128, 64])
+def test_short_sequences_that_share_a_tile(r, d):
+    # the query heads of a short sequence stand below one another in a tile: lengths around 32, 64, 128, 256
+    lens = [31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1, 2]
+    for g, w in ((16, None), (4, 24)):
+        Case(lens, Hq=2 * r, Hkv=2, d=d, g=g, w=w, first=3, tail=2, seed=r).check(what=f"r={r} w={w}")
+
+
+def test_offsets_beyond_32_bits():
+    # tokens of one wide buffer each: the last rows lie more than 2^31 elements behind the first
+    T, W, d = 66000, 34000, 128
+    lens = [300, 65400, 290]
+    assert (T - 1) * W > 2 ** 31
+    cu = offsets(lens, 5)
+    buffers = [torch.zeros(T, W, dtype=BF, device="cuda") for _ in range(3)]
+    packed = api.cca_pack(device(cu), T, 16, 200)
+    near = [rand(T, h, d, dtype=BF, seed=i).transpose(0, 1) for i, h in enumerate((2, 1, 1, 2))]
+
+    def far(k, h, src=None):
+        x = buffers[k // 2][:, W - (k % 2 + 1) * 1024:][:, :h * d].unflatten(1, (h, d)).transpose(0, 1)
+        if src is not None:
+            x.copy_(src)
+        return x
+    Q, K, V, dO = (far(i, near[i].shape[0], near[i]) for i in range(4))
+    a = api.cca_prefill_packed(*near[:3], packed)
+    O = far(4, 2)
+    b = api.cca_prefill_packed(Q, K, V, packed, out=(O, None, None, None))
+    m = slice(int(cu[0]), int(cu[-1]))
+    assert all(torch.equal(x[:, m], y[:, m]) for x, y in zip(a[:2], b[:2])) and torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
+    ga = api.cca_packed_bwd(*near[:3], a[2], a[3], a[0], a[1], near[3], packed)
+    gb = api.cca_packed_bwd(Q, K, V, b[2], b[3], O, b[1], dO, packed, dQ=far(5, 2))
+    assert all(torch.equal(x[:, m], y[:, m]) for x, y in zip(ga, gb))
+    api.cca_packed_clear(packed, O)
+    assert (O[:, :5] == 0).all() and (O[:, int(cu[-1]):] == 0).all() and torch.equal(O[:, m], a[0][:, m])
+    # the last sequence and the first are small enough for the formulas
+    for s in (0, 2):
+        rows = slice(int(cu[s]), int(cu[s + 1]))
+        c = slice(int(cu[s]) // 16, int(cu[s]) // 16 + lens[s] // 16)
+        o, l, eo, el = ref.attention(*(x[:, rows] for x in near[:3]), a[2][:, c], a[3][:, c], [0, lens[s]], 16, 200)
+        close(O[:, rows], o, eo, "O")
+        close(b[1][:, rows], l, el, "LSE")
+
+
+def test_a_captured_training_step():
+    # forward and backward in one graph, replayed for other inputs and lengths
+    T, Hq, Hkv, d, g, w = 300, 4, 2, 128, 16, 48
+    X = [rand(T, h, d, dtype=BF, seed=i).transpose(0, 1) for i, h in enumerate((Hq, Hkv, Hkv))]
+    cu, dO = device([0, 100, 300]), rand(Hq, T, d, dtype=BF, seed=8)
+    leaves = [x.detach().requires_grad_() for x in X]
+
+    def step():
+        O = api.cca_attention_packed(*leaves, api.cca_pack(cu, T, g, w))
+        return (O, *torch.autograd.grad(O, leaves, dO))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    leaves = [x.detach().requires_grad_() for x in leaves]      # no eager graph holds these
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = step()
+    for k, lens in enumerate(([0, 100, 300], [3, 290, 296], [0, 0, 17])):
+        cu.copy_(device(lens))
+        with torch.no_grad():
+            for i, x in enumerate(leaves):
+                x.copy_(rand(T, x.shape[0], d, dtype=BF, seed=20 * k + i).transpose(0, 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = [x.detach().clone().requires_grad_() for x in leaves]
+        O = api.cca_attention_packed(*eager, api.cca_pack(device(lens), T, g, w))
+        assert all(torch.equal(a, b) for a, b in zip(out, (O, *torch.autograd.grad(O, eager, dO))))
+
+
+def test_a_backward_pass_is_not_captured_while_an_eager_graph_holds_its_leaves():
+    T, d = 60, 64
+    X = [rand(h, T, d, seed=i).requires_grad_() for i, h in enumerate((2, 1, 1))]
+    dO = rand(2, T, d, seed=7)
+
+    def step():
+        O = api.cca_attention_packed(*X, api.cca_pack(cu, T, 4, 8))
+        return O, torch.autograd.grad(O, X, dO)
+    cu = device([0, 25, T])
+    held, want = step()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="being captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            step()
+    del held
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()[1]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_waits_that_run_out_are_reported(d):
+    # with no queries copied the first wait of every kernel ends; the next calls are right
+    lib = api.load_library()
+    c = Case([500, 300, 40], Hq=4, Hkv=2, d=d, g=16, w=100)
+    O, L, Kc, Vc = api.cca_prefill_packed(c.Q, c.K, c.V, c.packed)
+    for call in (lambda: api.cca_attn_packed(c.Q, c.K, c.V, Kc, Vc, c.packed, dev_status=c.status),
+                 lambda: api.cca_packed_bwd(c.Q, c.K, c.V, Kc, Vc, O, L, c.dO, c.packed, dev_status=c.status)):
+        torch.cuda.synchronize()
+        lib.cca_test_set_wait_limit_ns(20_000_000)
+        lib.cca_test_skip_q_load(1)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            lib.cca_test_skip_q_load(0)
+            lib.cca_test_set_wait_limit_ns(1_000_000_000)
+        assert int(c.status) == api.CCA_ERR_TIMEOUT
+        c.status.zero_()
+        c.check(what="after a time-out")
+
+
+def test_thousands_of_sequences():
+    # the plan of many sequences, against one built on the host
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 40, 9000)
+    lens[4000] = 70001
+    cu, g, w = offsets(lens, 7), 8, 16
+    T = int(cu[-1]) + 9
+    p = api.cca_pack(device(cu), T, g, w)
+    h = p.plan.view(torch.int32).cpu().numpy()
+    assert h[1] == T and h[5] == 9000 and h[6] == 7 and h[7] == cu[-1]
+    seen = np.maximum(lens - w, 0) // g
+    at = 16
+    for list_, size in enumerate((-(-lens // 256), -(-lens // 128), -(-seen // 128))):
+        order = sorted(((int(k), -int(n), s) for s, (n, t) in enumerate(zip(lens, size)) for k in range(t)), key=lambda x: (-x[0], x[1], x[2]))
+        want = np.array([[cu[s], -n, k, cu[s] // g] for k, n, s in order])
+        assert h[8 + list_] == len(want)
+        assert np.array_equal(h[at:at + 4 * len(want)].reshape(-1, 4), want)
+        at += 4 * ((T // 256, T // 128, T // g // 128)[list_] + 9000)
+    pos = np.zeros(T)
+    for a, n in zip(cu, lens):
+        pos[a:a + n] = np.arange(n)
+    assert np.array_equal(p.positions.cpu().numpy(), pos)
+
+
+def test_slices_of_one_projection():
+    # inputs from one tensor, gradients into another: the same as apart; slices that do share columns are refused
+    lens, Hq, Hkv, d, g, w = [90, 33, 200], 4, 2, 128, 16, 48
+    T, H = sum(lens), Hq + 2 * Hkv
+    for dtype in (BF, F32):
+        x = rand(T, H, d, dtype=dtype)
+        Q, K, V = (x[:, a:b].transpose(0, 1) for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, H)))
+        packed = api.cca_pack(device(offsets(lens)), T, g, w)
+        O, L, Kc, Vc = api.cca_prefill_packed(Q, K, V, packed)
+        dO = rand(Hq, T, d, dtype=dtype, seed=3)
+        want = api.cca_packed_bwd(Q, K, V, Kc, Vc, O, L, dO, packed)
+        dx = torch.zeros(T, H, d, dtype=dtype, device="cuda")
+        grads = [dx[:, a:b].transpose(0, 1) for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, H))]
+        got = api.cca_packed_bwd(Q, K, V, Kc, Vc, O, L, dO, packed, dQ=grads[0], dK=grads[1], dV=grads[2])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(torch.cat(want).transpose(0, 1), dx)
+        for a in (Hq - 1, Hq + 1):
+            with pytest.raises(api.CcaError):
+                api.cca_packed_bwd(Q, K, V, Kc, Vc, O, L, dO, packed, dQ=grads[0] if a < Hq else None, dK=dx[:, a:a + Hkv].transpose(0, 1), dV=grads[2])
+        with pytest.raises(api.CcaError):
+            api.cca_attn_packed(Q, K, V, Kc, Vc, packed, O=x[:, 1:1 + Hq].transpose(0, 1))
