@@ -361,7 +361,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ptx::mbar_init(bar(B_DRAIN), 1);
         ptx::mbar_init(bar(B_CUT), 1);
         *abort_flag = 0;
-        if constexpr (PACKED) {
+        if constexpr (!PACKED) ptx::fence_mbar_init();
+    }
+    if (warp == 0) {
+        ptx::tmem_alloc(base + L::OFF_TMEMPTR, TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    if constexpr (PACKED) {
+        // Everything above runs while the kernel before ends.  This one does not let the next begin early: CTAs that
+        // take SMs one by one lie anywhere, and 12 prompts then take 473 us instead of 462, a training step with cores
+        // 1233 instead of 1209 (neighbours read the same keys).
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (threadIdx.x == 0) {
             const int pairs = max(plan_counts(p.plan).x, 0);
             const int3 s = pairs > 0 ? plan_short(p.plan) : make_int3(0, 0, 0);
             const int first[5] = {0, p.most >= 1 ? s.x : pairs, p.most >= 2 ? s.y : pairs, p.most >= 3 ? s.z : pairs, pairs};
@@ -369,12 +380,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int c = 0; c < 4; ++c) items += (first[c + 1] - first[c]) * (p.Hq >> c);
             for (int c = 0; c < 3; ++c) out[c] = first[c + 1];
             out[3] = items;
+            ptx::fence_mbar_init();
         }
-        ptx::fence_mbar_init();
-    }
-    if (warp == 0) {
-        ptx::tmem_alloc(base + L::OFF_TMEMPTR, TMEM_COLS);
-        ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -1036,10 +1043,8 @@ cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream) {
     if (most > 0x7fffffff) return cudaErrorNotSupported;
     const unsigned grid = static_cast<unsigned>(most < di.sms ? most : di.sms);
     if (a.d == 128)
-        attn_bf16_tc_kernel<true, 128><<<grid, NUM_THREADS, Layout<128>::SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
-    else
-        attn_bf16_tc_kernel<true, 64><<<grid, NUM_THREADS, Layout<64>::SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
-    return cudaGetLastError();
+        return start_dependent(attn_bf16_tc_kernel<true, 128>, dim3(grid), NUM_THREADS, Layout<128>::SMEM_BYTES, stream, mQ, mK, mV, mKc, mVc, p);
+    return start_dependent(attn_bf16_tc_kernel<true, 64>, dim3(grid), NUM_THREADS, Layout<64>::SMEM_BYTES, stream, mQ, mK, mV, mKc, mVc, p);
 }
 
 }  // namespace cca

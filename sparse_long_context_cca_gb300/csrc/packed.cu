@@ -260,27 +260,39 @@ __global__ void __launch_bounds__(POOL_WARPS * 32, POOL_BLOCKS) pool_packed_kern
 // ---------------------------------------------------------------- backward: D, and the pooling's gradient
 
 // D_i = dO_i . O_i, a row per LPR lanes.
+constexpr int D_ROWS = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) packed_d_kernel(Rows<const char> O, Rows<const char> dO, float *out, Plan plan, int Hq, int heads_first) {
     using RT = Row16<T>;
     constexpr int E = RT::E, LPR = D / E;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
-    const bool in = item < static_cast<int64_t>(plan.T) * Hq;
-    const int64_t row = heads_first ? item / Hq : item % plan.T;
-    const int h = static_cast<int>(heads_first ? item % Hq : item / plan.T);
-    float x = 0.f;
-    if (in) {
-        float f[E], g[E];
-        RT::unpack(*reinterpret_cast<const uint4 *>(O.at(h, row) + threadIdx.x % LPR * 16), f);
-        RT::unpack(*reinterpret_cast<const uint4 *>(dO.at(h, row) + threadIdx.x % LPR * 16), g);
+    const int64_t n = static_cast<int64_t>(plan.T) * Hq;
+    uint4 a[D_ROWS], b[D_ROWS];
+    int64_t at[D_ROWS];  // the row's place in `out`; -1: none
 #pragma unroll
-        for (int e = 0; e < E; ++e) x = fmaf(f[e], g[e], x);
+    for (int k = 0; k < D_ROWS; ++k) {
+        const int64_t item = (static_cast<int64_t>(blockIdx.x) * D_ROWS + k) * (256 / LPR) + threadIdx.x / LPR;
+        const int64_t row = heads_first ? item / Hq : item % plan.T;
+        const int h = static_cast<int>(heads_first ? item % Hq : item / plan.T);
+        at[k] = item < n ? static_cast<int64_t>(h) * plan.T + row : -1;
+        a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (item < n) {
+            a[k] = *reinterpret_cast<const uint4 *>(O.at(h, row) + threadIdx.x % LPR * 16);
+            b[k] = *reinterpret_cast<const uint4 *>(dO.at(h, row) + threadIdx.x % LPR * 16);
+        }
     }
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-    if (in && threadIdx.x % LPR == 0) out[static_cast<int64_t>(h) * plan.T + row] = x;
+    for (int k = 0; k < D_ROWS; ++k) {
+        float f[E], g[E], x = 0.f;
+        RT::unpack(a[k], f);
+        RT::unpack(b[k], g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x = fmaf(f[e], g[e], x);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        if (at[k] >= 0 && threadIdx.x % LPR == 0) out[at[k]] = x;
+    }
 }
 
 struct ClearArgs {
@@ -785,7 +797,7 @@ int cca_packed_bwd(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const
     cudaError_t e = by_type([&](auto t, auto d) {
         using X = decltype(t);
         constexpr int D = decltype(d)::value;
-        const int64_t per = 256 / (D * sizeof(X) / 16), blocks = (static_cast<int64_t>(T) * p.Hq + per - 1) / per;
+        const int64_t per = D_ROWS * 256 / (D * sizeof(X) / 16), blocks = (static_cast<int64_t>(T) * p.Hq + per - 1) / per;
         if (blocks > 0x7fffffff) return cudaErrorNotSupported;
         return start_dependent(packed_d_kernel<X, D>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, in_bytes(*O, p.dtype),
                                in_bytes(*dO, p.dtype), w.D, a.plan, p.Hq, heads_inside(*O));
