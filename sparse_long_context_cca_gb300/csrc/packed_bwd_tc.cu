@@ -83,15 +83,16 @@ constexpr int B_RES = 0;                    // resident tiles are there
 constexpr int B_RESFREE = 1;                // ... have been read
 constexpr int B_LFULL = 2, B_LEMPTY = 5;    // LONG_ST each
 constexpr int B_SFULL_RING = 8, B_SEMPTY = 10;  // SHORT_ST each
-constexpr int B_S = 12;                     // S is there
-constexpr int B_SREAD = 13;                 // dq: S is in registers
-constexpr int B_DP = 14;                    // 2: dP is there (dkv uses the first)
-constexpr int B_P = 16;                     // P (dkv) is there
-constexpr int B_DS = 17;                    // 2: dS is there (dkv uses the first).  dq: a warp that is ahead may finish the next
-                                            // tile, whose products are done, before the others finish this one
-constexpr int B_DONE = 19;                  // the item's sums are there
-constexpr int B_ACCFREE = 20;               // ... have been read
-constexpr int B_DRAIN = 21, B_CUT = 22, N_BARS = 23;
+constexpr int B_S = 12;                     // dkv: S is there
+constexpr int B_READ = 13;                  // dq: S and dP are in registers
+constexpr int B_DP = 14;                    // dP is there (dq: S too)
+constexpr int B_P = 15;                     // dkv: P is there
+constexpr int B_DS = 16;                    // dS is there
+constexpr int B_DSFREE = 17;                // dq: dS has been read
+constexpr int B_DONE = 18;                  // the item's sums are there
+constexpr int B_ACCFREE = 19;               // ... have been read
+constexpr int B_Q = 20, B_QT = 21;          // dq: the queries are in shared memory; in tensor memory
+constexpr int B_DRAIN = 22, B_CUT = 23, N_BARS = 24;
 
 template <int HD>
 __device__ __forceinline__ void load_tile(const void *map, uint32_t bar, uint32_t dst, int y, int z) {
@@ -211,7 +212,7 @@ __device__ __forceinline__ Cta<HD> setup(uint8_t *smem_raw, const Args &p) {
     c.lim = p.wait_limit_ns;
     if (threadIdx.x == 0) {
         for (int k = 0; k < N_BARS; ++k)  // one arrival, but for those of the eight element-wise warps
-            ptx::mbar_init(c.bar(k), k == B_SREAD || k == B_P || k == B_DS || k == B_DS + 1 || k == B_ACCFREE ? 8 : 1);
+            ptx::mbar_init(c.bar(k), k == B_READ || k == B_P || k == B_DS || k == B_ACCFREE || k == B_QT ? 8 : 1);
         *c.abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Cta<HD> c = setup<HD>(smem_raw, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_items = plan_counts(p.plan).y * p.Hq;
-    constexpr uint32_t T_DP = 128, T_DQ = 384;  // TMEM columns; S at 0, dP(g) at T_DP + 128 * (g & 1)
+    constexpr uint32_t T_DP = 128, T_DS = 256, T_Q = 320, T_DQ = 384;  // TMEM columns; S at 0
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -293,15 +294,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             ptx::prefetch_tmap(&tmKc);
             ptx::prefetch_tmap(&tmVc);
         }
-        uint32_t g = 0, nl = 0, ns = 0, it = 0, cut = 0;
+        uint32_t g = 0, nl = 0, ns = 0, nq = 0, it = 0, cut = 0;
         bool ok = !p.skip_loads;
         for (int round = 0, item; ok && (item = item_of_round(round)) < n_items; ++round) {
             const DqItem d(p, item);
             const int groups = p.plan.by_g.div(d.n);
+            if (!c.wait(c.bar(B_QT), (it & 1) ^ 1)) break;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(c.bar(B_Q), Layout<HD>::TILE);
+                load_tile<HD>(&tmQ, c.bar(B_Q), c.res(0), d.row0 + d.i0, d.h);
+            }
+            nq = it + 1;
             if (!c.wait(c.bar(B_RESFREE), (it & 1) ^ 1)) break;
             if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(c.bar(B_RES), 2 * Layout<HD>::TILE);
-                load_tile<HD>(&tmQ, c.bar(B_RES), c.res(0), d.row0 + d.i0, d.h);
+                ptx::mbar_arrive_expect_tx(c.bar(B_RES), Layout<HD>::TILE);
                 load_tile<HD>(&tmdO, c.bar(B_RES), c.res(1), d.row0 + d.i0, d.h);
             }
             ++it;
@@ -324,24 +330,30 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         __syncwarp();
-        if (*c.abort_flag && !p.skip_loads) drain_copies(c, nl, ns, it);
+        if (*c.abort_flag && !p.skip_loads) {
+            drain_copies(c, nl, ns, it);
+            volatile int never = 0;
+            if (nq > 0) ptx::wait_bounded(c.bar(B_Q), (nq - 1) & 1, &never, c.lim);
+        }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         constexpr uint32_t IDESC_TS = ptx::idesc_bf16_f32(128, HD, 0, 1);  // A in TMEM, B MN-major
-        const uint64_t dQd = ptx::smem_desc_sw128(c.res(0), 16, 1024), ddOd = ptx::smem_desc_sw128(c.res(1), 16, 1024);
-        // S(g) = Q K(g)^T and dP(g) = dO V(g)^T; dP(g) takes the buffer of dS(g - 2), which dQ(g - 2), issued
-        // before, has read by then
-        auto products = [&](uint32_t g) -> bool {
+        const uint64_t ddOd = ptx::smem_desc_sw128(c.res(1), 16, 1024);
+        // S(g) = Q K(g)^T and dP(g) = dO V(g)^T of the first or a later tile of item `it`
+        auto products = [&](uint32_t g, uint32_t it, bool first) -> bool {
             if (!c.wait(c.bar(B_LFULL + g % LONG_ST), (g / LONG_ST) & 1)) return false;
-            if (g > 0 && !c.wait(c.bar(B_SREAD), (g - 1) & 1)) return false;
+            if (first && !c.wait(c.bar(B_QT), it & 1)) return false;
+            if (g > 0 && !c.wait(c.bar(B_READ), (g - 1) & 1)) return false;
             ptx::tc_fence_after();
-            mma_ss<HD>(c.tmem, dQd, ptx::smem_desc_sw128(c.stage_l(g), 16, 1024));
-            ptx::tc_commit_warp(c.bar(B_S));
+            const uint64_t k = ptx::smem_desc_sw128(c.stage_l(g), 16, 1024);
+            if constexpr (HD == 128) ptx::mma_ts_nt_k128_warp(c.tmem, c.tmem + T_Q, k, IDESC_SS);
+            else ptx::mma_ts_nt_k64_warp(c.tmem, c.tmem + T_Q, k, IDESC_SS);
             if (!c.wait(c.bar(B_SFULL_RING + g % SHORT_ST), (g / SHORT_ST) & 1)) return false;
+            if (first && !c.wait(c.bar(B_RES), it & 1)) return false;
             ptx::tc_fence_after();
-            mma_ss<HD>(c.tmem + T_DP + 128u * (g & 1), ddOd, ptx::smem_desc_sw128(c.stage_s(g), 16, 1024));
-            ptx::tc_commit_warp(c.bar(B_DP + (g & 1)));
+            mma_ss<HD>(c.tmem + T_DP, ddOd, ptx::smem_desc_sw128(c.stage_s(g), 16, 1024));
+            ptx::tc_commit_warp(c.bar(B_DP));
             ptx::tc_commit_warp(c.bar(B_SEMPTY + g % SHORT_ST));
             return true;
         };
@@ -349,18 +361,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
         for (int item; ok && (item = item_of_round(it)) < n_items; ++it) {
             const DqItem d(p, item);
-            if (!(ok = c.wait(c.bar(B_RES), it & 1) && products(g))) break;
+            if (!(ok = products(g, it, true))) break;
             for (int x = 0; x < d.T; ++x, ++g) {
                 if (x + 1 < d.T) {
-                    if (!(ok = products(g + 1))) break;
+                    if (!(ok = products(g + 1, it, false))) break;
                 } else {
                     ptx::tc_commit_warp(c.bar(B_RESFREE));
                 }
-                if (!(ok = c.wait(c.bar(B_DS + (g & 1)), (g >> 1) & 1))) break;
+                if (!(ok = c.wait(c.bar(B_DS), g & 1))) break;
                 if (x == 0 && !(ok = c.wait(c.bar(B_ACCFREE), (it & 1) ^ 1))) break;
                 ptx::tc_fence_after();
-                ptx::mma_ts_k128_split_warp(c.tmem + T_DQ, c.tmem + T_DP + 128u * (g & 1),
-                                            ptx::smem_desc_sw128(c.stage_l(g), HALF_BYTES, 1024), IDESC_TS, x > 0 ? 1u : 0u);
+                ptx::mma_ts_k128_warp(c.tmem + T_DQ, c.tmem + T_DS, ptx::smem_desc_sw128(c.stage_l(g), HALF_BYTES, 1024), IDESC_TS,
+                                      x > 0 ? 1u : 0u);
+                ptx::tc_commit_warp(c.bar(B_DSFREE));
                 ptx::tc_commit_warp(c.bar(B_LEMPTY + g % LONG_ST));
             }
             if (ok) ptx::tc_commit_warp(c.bar(B_DONE));
@@ -375,9 +388,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int ch = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const int h0 = ch * 64;  // this warp's 64 key columns of the tile
         const uint32_t lane_addr = c.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const float c1 = p.tau * LOG2E;
+        const uint64_t c2 = ptx::f2(p.tau * LOG2E, p.tau * LOG2E);
+        // this warp's half of its rows' queries of item `it`, from the swizzled tile to tensor memory
+        auto copy_q = [&](uint32_t it) -> bool {
+            if (!c.wait(c.bar(B_Q), it & 1)) return false;
+            const uint32_t src = c.res(0) + (HD == 128 ? ch * HALF_BYTES : 0) + row * 128;
+#pragma unroll
+            for (int k = 0; k < HD / 64; ++k) {
+                uint32_t q[16];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int piece = (HD == 128 ? 4 * k : 4 * ch) + x;
+                    const uint4 v = ptx::ld_shared_v4(src + ((piece ^ (row & 7)) << 4));
+                    q[4 * x] = v.x, q[4 * x + 1] = v.y, q[4 * x + 2] = v.z, q[4 * x + 3] = v.w;
+                }
+                ptx::tmem_st16(lane_addr + T_Q + ch * (HD / 4) + 16 * k, q);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(c.bar(B_QT));
+            return true;
+        };
         uint32_t g = 0, it = 0;
-        bool ok = true;
+        bool ok = item_of_round(0) >= n_items || copy_q(0);
         for (int item; ok && (item = item_of_round(it)) < n_items; ++it) {
             const DqItem d(p, item);
             const int i = d.i0 + row;
@@ -388,14 +422,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 lse2 = p.LSE[u] * LOG2E;
                 Di = p.space.D[u];
             }
+            const uint64_t nl2 = ptx::f2(-lse2, -lse2), nd2 = ptx::f2(-Di, -Di);
             const int lo_i = p.plan.start_of(i), nc_i = p.plan.cores_of(i);
             for (int x = 0; x < d.T; ++x, ++g) {
-                if (!(ok = c.wait(c.bar(B_S), g & 1))) break;
-                ptx::tc_fence_after();
-                const uint32_t sS = lane_addr + h0, sD = lane_addr + T_DP + 128u * (g & 1) + h0;
-                uint32_t pa[32], pb[32];
-                ptx::tmem_ld32(sS, pa);
-                ptx::tmem_ld32(sS + 32, pb);
                 // the row's visible key columns of this tile
                 const int y0 = d.tile_y(x);
                 int c_lo = 0, c_hi = BT - 1;
@@ -406,43 +435,56 @@ __global__ void __launch_bounds__(THREADS, 1)
                     c_hi = min(i - y0, BT - 1);
                 }
                 if (!valid) c_hi = -1;
-                ptx::tmem_wait_ld(pa);
-                ptx::reg_touch(pb);
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(c.bar(B_SREAD));  // the next S may come
-                // P = 2^(S tau log2e - LSE), zero off the visible columns
                 const uint32_t seen[2] = {ptx::bits(c_lo - h0, c_hi - h0), ptx::bits(c_lo - h0 - 32, c_hi - h0 - 32)};
                 const bool whole[2] = {__all_sync(0xffffffffu, seen[0] == 0xffffffffu) != 0, __all_sync(0xffffffffu, seen[1] == 0xffffffffu) != 0};
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    pa[k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pa[k]), c1, -lse2)));
-                    pb[k] = __float_as_uint(ptx::ex2(fmaf(__uint_as_float(pb[k]), c1, -lse2)));
-                }
-                clear_unseen(pa, seen[0], whole[0]);
-                clear_unseen(pb, seen[1], whole[1]);
-                if (!(ok = c.wait(c.bar(B_DP + (g & 1)), (g >> 1) & 1))) break;
+                if (!(ok = c.wait(c.bar(B_DP), g & 1))) break;  // S was issued before dP
                 ptx::tc_fence_after();
-                // dS = P (dP - D), bf16 pairs written over the dP columns [h0, h0 + 32), which this warp has
-                // already read; nothing of a masked value gets on, not as 0 * NaN either
+                uint32_t s[2][32], dp[2][32];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    uint32_t dp[32], pk[16];
-                    ptx::tmem_ld32(sD + 32 * j, dp);
-                    ptx::tmem_wait_ld(dp);
-                    clear_unseen(dp, seen[j], whole[j]);
-                    const uint32_t *pp = j ? pb : pa;
+                    ptx::tmem_ld32(lane_addr + h0 + 32 * j, s[j]);
+                    ptx::tmem_ld32(lane_addr + T_DP + h0 + 32 * j, dp[j]);
+                }
+                ptx::tmem_wait_ld(s[0]);
+                ptx::reg_touch(dp[0]);
+                ptx::reg_touch(s[1]);
+                ptx::reg_touch(dp[1]);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(c.bar(B_READ));  // the next S and dP may come
+                // the product that reads the dS of the tile before is done
+                if (g > 0 && !(ok = c.wait(c.bar(B_DSFREE), (g - 1) & 1))) break;
+                ptx::tc_fence_after();
+                // P = 2^(S tau log2e - LSE), dS = P (dP - D) as bf16 pairs; nothing of a masked value gets on, not as
+                // 0 * NaN either
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        pk[k] = ptx::pack_bf16x2(__uint_as_float(pp[2 * k]) * (__uint_as_float(dp[2 * k]) - Di),
-                                                 __uint_as_float(pp[2 * k + 1]) * (__uint_as_float(dp[2 * k + 1]) - Di));
-                    ptx::tmem_st16(sD + 16 * j, pk);
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float a, b;
+                        ptx::f2_split(ptx::fma2(ptx::f2(__uint_as_float(s[j][k]), __uint_as_float(s[j][k + 1])), c2, nl2), a, b);
+                        s[j][k] = __float_as_uint(ptx::ex2(a));
+                        s[j][k + 1] = __float_as_uint(ptx::ex2(b));
+                    }
+                    clear_unseen(s[j], seen[j], whole[j]);
+                    clear_unseen(dp[j], seen[j], whole[j]);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const uint64_t x2 = ptx::add2(ptx::f2(__uint_as_float(dp[j][2 * k]), __uint_as_float(dp[j][2 * k + 1])), nd2);
+                        float a, b;
+                        ptx::f2_split(ptx::mul2(ptx::f2(__uint_as_float(s[j][2 * k]), __uint_as_float(s[j][2 * k + 1])), x2), a, b);
+                        pk[k] = ptx::pack_bf16x2(a, b);
+                    }
+                    ptx::tmem_st16(lane_addr + T_DS + ch * 32 + 16 * j, pk);
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(c.bar(B_DS + (g & 1)));
+                if (lane == 0) ptx::mbar_arrive(c.bar(B_DS));
             }
+            // the last S of this item is done: its queries give way to the next one's
+            if (ok && item_of_round(it + 1) < n_items) ok = copy_q(it + 1);
             if (!ok || !(ok = c.wait(c.bar(B_DONE), it & 1))) break;
             ptx::tc_fence_after();
             const int c0 = ch * (HD / 2);
