@@ -619,7 +619,9 @@ int cca_packed_clear(const cca_packed_rows_t *tensors, const int32_t *heads, int
 /*
  * cca_packed_bwd - gradients of the loss sum(dO * O) through cca_attn_packed and, where w < T,
  * cca_pool_packed, in the inputs' type (rounded once).  Kc, Vc, O, LSE are the forward's.  Sums have a
- * fixed order: results repeat to the bit.  The gradients of a sequence that holds infinities or NaN
+ * fixed order: results repeat to the bit.  bf16: weights and score gradients are rounded to bf16 before the
+ * products; dO . O of rows whose keys fit one tile of 128 is formed from the weights, so that the rounding
+ * of O does not reach them.  The gradients of a sequence that holds infinities or NaN
  * (in any tensor) are not defined; those of the others are not touched by it.
  *   workspace: 16-byte aligned, at least cca_packed_bwd_workspace_size() bytes, rewritten by every call;
  *   calls that may run at the same time need one each.

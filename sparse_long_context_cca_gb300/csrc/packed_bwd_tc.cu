@@ -10,14 +10,24 @@
 // first copies and last stores: 5 or 6 tiles of work.)
 //
 //  dq: an item is 128 query rows of one head, over its key tiles (cores, then the band):
-//     S = Q K^T, dP = dO V^T  ->  dS (bf16, over dP);   dQ += dS K
-//  TMEM: S | dP0 | dP1 | dQ.  The element-wise warps hold P in registers, so S needs one buffer; with two of dP
-//  both products of the next tile run while this tile's dS is formed.
+//     S = Q K^T, dP = dO V^T  ->  dS (bf16);   dQ += dS K
+//  TMEM: S | dP | dS | Q | dQ.  The element-wise warps take S and dP of a tile into registers at once, and both
+//  products of the next tile run while they form dS; Q, the left side of every S, is copied to tensor memory,
+//  where it takes no shared-memory bandwidth.
 //
 //  dkv: an item is 128 keys (raw tokens or cores) of one KV head, over the rows of its query heads that see any:
 //     S^T = K Q^T, dP^T = V dO^T  ->  P^T over S^T, dS^T over dP^T (bf16);   dV += P^T dO,  dK += dS^T Q
 //  TMEM: S^T | dP^T | dK | dV.  The rows of a core tile are split over items, whose sums are added up in order
 //  later.
+//
+// What bounds them (32 heads over 8, 16 K tokens in five sequences, window 1024): dq 370 us, dkv of the tokens 388
+// and of the cores 92, the tensor pipe active 52 and 59% of the time.  With its parts taken out in turn, dq took
+// 372 us without copies, 370 without exponentials, 343 without dQ's product, 310 without any product, and 229 with
+// nothing but waits, tensor-memory reads and writes, and dS: the chain of a tile through the eight element-wise
+// warps.  Sixteen of them gained nothing.  dkv of few long sequences (six of up to 2543 tokens, 132 us) is as long as
+// its longest item, 80 (query tile, head) pairs; two items for it cost more than they gain (135-140 us).
+//
+// P and dS are rounded to bf16 for the tensor cores (half a step, 2^-9 relative, each); everything between is fp32.
 //
 // Results leave once, in bf16 (a core's in fp32), from the thread that holds the row, with the pooling's share:
 // rows of a tile behind the sequence's end belong to the next one and must stay as they are.  Read, they
@@ -388,7 +398,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int ch = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const int h0 = ch * 64;  // this warp's 64 key columns of the tile
         const uint32_t lane_addr = c.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint64_t c2 = ptx::f2(p.tau * LOG2E, p.tau * LOG2E);
+        const float c1 = p.tau * LOG2E;
+        const uint64_t c2 = ptx::f2(c1, c1);
         // this warp's half of its rows' queries of item `it`, from the swizzled tile to tensor memory
         auto copy_q = [&](uint32_t it) -> bool {
             if (!c.wait(c.bar(B_Q), it & 1)) return false;
@@ -422,7 +433,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 lse2 = p.LSE[u] * LOG2E;
                 Di = p.space.D[u];
             }
-            const uint64_t nl2 = ptx::f2(-lse2, -lse2), nd2 = ptx::f2(-Di, -Di);
+            const uint64_t nl2 = ptx::f2(-lse2, -lse2);
+            uint64_t nd2 = ptx::f2(-Di, -Di);
             const int lo_i = p.plan.start_of(i), nc_i = p.plan.cores_of(i);
             for (int x = 0; x < d.T; ++x, ++g) {
                 // the row's visible key columns of this tile
@@ -439,6 +451,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool whole[2] = {__all_sync(0xffffffffu, seen[0] == 0xffffffffu) != 0, __all_sync(0xffffffffu, seen[1] == 0xffffffffu) != 0};
                 if (!(ok = c.wait(c.bar(B_DP), g & 1))) break;  // S was issued before dP
                 ptx::tc_fence_after();
+                if (d.T == 1) {
+                    // Few keys: D is formed from them, sum_j P_ij dP_ij.  dO . O carries the roundings of P and O to bf16,
+                    // which for a few large weights are as much as dS itself is rounded (three tokens: dQ 0.0037 off
+                    // instead of 0.0024, 2-norms, with 0.0017 the rounding of dQ).  Each warp goes over all 128 columns.
+                    float sum = 0.f;
+#pragma unroll 1
+                    for (int j = 0; j < BT; j += 16) {
+                        uint32_t s[16], dp[16];
+                        ptx::tmem_ld16(lane_addr + j, s);
+                        ptx::tmem_ld16(lane_addr + T_DP + j, dp);
+                        ptx::tmem_wait_ld16(s);
+                        ptx::tmem_wait_ld16(dp);
+                        const uint32_t m = ptx::bits(c_lo - j, c_hi - j);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float w = ptx::ex2(fmaf(__uint_as_float(s[k]), c1, -lse2));
+                            if (m & (1u << k)) sum = fmaf(w, __uint_as_float(dp[k]), sum);
+                        }
+                    }
+                    nd2 = ptx::f2(-sum, -sum);
+                    if (valid && ch == 0) p.space.D[static_cast<int64_t>(d.h) * p.plan.T + d.row0 + i] = sum;  // for dK and dV
+                }
                 uint32_t s[2][32], dp[2][32];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {

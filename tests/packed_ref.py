@@ -95,6 +95,17 @@ def keys(k, v, Kc, Vc, kv, a, n, g):
     return np.concatenate([t64(Kc)[kv, c], k[kv, a:a + n]]), np.concatenate([t64(Vc)[kv, c], v[kv, a:a + n]])
 
 
+def few_keys(see, G):
+    """The rows whose tile of 128 sees no core and at most 128 tokens from the first one that its first row sees:
+    for these the bf16 kernels form D from P and dP, and not from the rounded O."""
+    n = len(see)
+    few = np.zeros(n, bool)
+    for i0 in range(0, n, 128):
+        i1 = min(i0 + 128, n) - 1
+        few[i0:i1 + 1] = not see[i1, :G].any() and i1 - see[i0, G:].argmax() < 128
+    return few
+
+
 def backward(Q, K, V, Kc, Vc, O, LSE, dO, cu, g, w, mode=0, pool_mode=0, scale=None):
     """((dQ, dK, dV), (their bounds)) of the formulas at the given Kc, Vc, O and LSE; NaN for rows of no sequence."""
     Hq, T, d = Q.shape
@@ -108,6 +119,7 @@ def backward(Q, K, V, Kc, Vc, O, LSE, dO, cu, g, w, mode=0, pool_mode=0, scale=N
     for a, b in sequences(cu):
         n, G = b - a, (b - a) // g
         see = visible(n, g, w, mode)
+        few = few_keys(see, G)
         dk, dv, ek, ev = (np.zeros((Hkv, G + n, d)) for _ in range(4))
         dq, eq = np.zeros((Hq, n, d)), np.zeros((Hq, n, d))
         for h in range(Hq):
@@ -117,6 +129,8 @@ def backward(Q, K, V, Kc, Vc, O, LSE, dO, cu, g, w, mode=0, pool_mode=0, scale=N
             p = np.where(see, np.exp(np.where(see, s, 0) - lse[h, a:b, None]), 0)
             D = (gs * o[h, a:b]).sum(1, keepdims=True)
             dp = gs @ vv.T
+            if bf:
+                D = np.where(few[:, None], np.where(see, p * dp, 0).sum(1, keepdims=True), D)
             ds = p * (dp - D)
             ds_abs = (d + 4) * U * tau * (np.abs(qs) @ np.abs(kk).T) + 2 * U * np.abs(lse[h, a:b, None]) + U * np.abs(s) * 4
             relp = ds_abs + EX * np.maximum(1.0, np.abs(s - lse[h, a:b, None]))
