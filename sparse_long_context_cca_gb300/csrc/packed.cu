@@ -768,6 +768,7 @@ int cca_packed_bwd(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const
     in[6] = bytes_at(cores ? Vc : nullptr, bytes);
     in[7] = bytes_at(packed->plan, packed->plan_bytes);
     in[8] = bytes_at(LSE, 4ull * p.Hq * T);
+    if (!apart(out, 3, in, 9)) return CCA_ERR_INVALID_ARG;
     if ((st = check_device()) != CCA_OK) return st;
     const int sms = device_sms();
     if (sms < 1) return CCA_ERR_CUDA;

@@ -21,13 +21,13 @@
 //  later.
 //
 // What bounds them (32 heads over 8, 16 K tokens in five sequences, window 1024): dq 370 us, dkv of the tokens 388
-// and of the cores 92, the tensor pipe active 52 and 59% of the time.  With its parts taken out in turn, dq took
+// and of the cores 92, the tensor pipe active 52 and 59% of the time.  With its parts taken out in turn, dq (376 us then) took
 // 372 us without copies, 370 without exponentials, 343 without dQ's product, 310 without any product, and 229 with
 // nothing but waits, tensor-memory reads and writes, and dS: the chain of a tile through the eight element-wise
 // warps.  Sixteen of them gained nothing.  dkv of few long sequences (six of up to 2543 tokens, 132 us) is as long as
 // its longest item, 80 (query tile, head) pairs; two items for it cost more than they gain (135-140 us).
 //
-// P and dS are rounded to bf16 for the tensor cores (half a step, 2^-9 relative, each); everything between is fp32.
+// P and dS are rounded to bf16 for the tensor cores (off by at most half a step, 2^-8 relative, each); everything between is fp32.
 //
 // Results leave once, in bf16 (a core's in fp32), from the thread that holds the row, with the pooling's share:
 // rows of a tile behind the sequence's end belong to the next one and must stay as they are.  Read, they
