@@ -359,3 +359,74 @@ def test_refusals():
         api.cca_norm_rope(x, None, w, None, f, eps=-1.0)
     with pytest.raises(ValueError):
         api.cca_norm_rope(x.requires_grad_(), None, w, None, f, out=(x, None))
+
+
+def test_offsets_beyond_32_bits():
+    # rows of one wide buffer each: the last ones lie more than 2^31 elements behind the first
+    N, W, H, d = 66000, 34000, 2, 128
+    assert (N - 1) * W > 2 ** 31
+    x, dy = rand(1, N, H, d, dtype=torch.bfloat16).transpose(1, 2), rand(1, N, H, d, dtype=torch.bfloat16, seed=2).transpose(1, 2)
+    f, w = freqs(d), weights(H, d, False, torch.float32)
+    want, _ = api.cca_norm_rope(x, None, w, None, f, start=100)
+
+    def far(src):
+        y = torch.zeros(N, W, dtype=torch.bfloat16, device="cuda")[:, W - 1024:][:, :H * d].unflatten(1, (H, d)).transpose(0, 1)[None]
+        y.copy_(src)
+        return y
+    a = far(x)
+    got, _ = api.cca_norm_rope(a, None, w, None, f, start=100)
+    assert torch.equal(got, want)
+    leaves, back = [x.detach().requires_grad_(), w.clone().requires_grad_()], []
+    for t, g in ((leaves[0], dy), (a.requires_grad_(), far(dy))):
+        y, _ = api.norm_rope(t, None, leaves[1], None, f, start=100)
+        back.append(torch.autograd.grad(y, [t, leaves[1]], g))
+    assert all(torch.equal(p, q) for p, q in zip(*back))
+    with torch.no_grad():
+        api.cca_norm_rope(a, None, w, None, f, start=100, out=(a, None))      # in place
+    assert torch.equal(a, want)
+
+
+def test_a_backward_pass_is_not_captured_while_an_eager_graph_holds_its_leaves():
+    x, w, f = rand(1, 2, 40, 64).requires_grad_(), weights(2, 64, True, torch.float32).requires_grad_(), freqs(64)
+    dy = rand(1, 2, 40, 64, seed=4)
+
+    def step():
+        y, _ = api.norm_rope(x, None, w, None, f)
+        return y, torch.autograd.grad(y, [x, w], dy)
+    held, want = step()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="being captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            step()
+    del held
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()[1]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_graphs_replayed_together():
+    # each captured pass has a workspace of its own
+    f, w = freqs(128), weights(1, 128, False, torch.float32).requires_grad_()
+    graphs, streams, outs, wants = [], [], [], []
+    for k in range(2):
+        x, dy = rand(1, 8, 3000, 128, dtype=torch.bfloat16, seed=k).requires_grad_(), rand(1, 8, 3000, 128, dtype=torch.bfloat16, seed=9 + k)
+        y, _ = api.norm_rope(x, None, w, None, f)
+        wants.append(torch.autograd.grad(y, [x, w], dy))
+        del y
+        torch.cuda.synchronize()
+        s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        leaf, lw = x.detach().requires_grad_(), w.detach().requires_grad_()
+        with torch.cuda.graph(graph, stream=s):
+            y, _ = api.norm_rope(leaf, None, lw, None, f)
+            outs.append(torch.autograd.grad(y, [leaf, lw], dy))
+        graphs.append((graph, leaf, lw, dy, y)), streams.append(s)
+    for _ in range(20):
+        for (graph, *_), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for got, want in zip(outs, wants):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -630,3 +630,33 @@ def test_slices_of_one_projection():
                 api.cca_packed_bwd(Q, K, V, Kc, Vc, O, L, dO, packed, dQ=grads[0] if a < Hq else None, dK=dx[:, a:a + Hkv].transpose(0, 1), dV=grads[2])
         with pytest.raises(api.CcaError):
             api.cca_attn_packed(Q, K, V, Kc, Vc, packed, O=x[:, 1:1 + Hq].transpose(0, 1))
+
+
+@pytest.mark.parametrize("g,w,mode", [(2 ** 31 - 1, 2 ** 31 - 1, 0), (2 ** 31 - 1, 5, 1), (16, 2 ** 31 - 1, 1), (300, 7, 0), (90, 1, 1)])
+def test_groups_and_windows_of_any_size(g, w, mode):
+    # groups that no sequence fills, windows past every length
+    for dtype, d in ((BF, 128), (F32, 64)):
+        c = Case([130, 7, 95], Hq=4, Hkv=2, d=d, dtype=dtype, g=g, w=w, mode=mode)
+        if c.packed.cores and g > c.T:
+            raise AssertionError("no group fits")
+        c.check(what=f"g={g} w={w}")
+        Kc, Vc = api.cca_pool_packed(c.Q, c.K, c.V, c.packed)
+        assert Kc.shape == Vc.shape == (2, c.T // g, d)
+
+
+def test_inputs_of_which_some_need_gradients():
+    T, d = 90, 128
+    packed = api.cca_pack(device([0, 40, T]), T, 8, 16)
+    X = [rand(T, h, d, dtype=BF, seed=i).transpose(0, 1) for i, h in enumerate((4, 2, 2))]
+    dO = rand(4, T, d, dtype=BF, seed=5)
+    whole = [x.detach().clone().requires_grad_() for x in X]
+    want = torch.autograd.grad(api.cca_attention_packed(*whole, packed), whole, dO)
+    for k in range(3):
+        some = [x.detach().clone().requires_grad_(i == k) for i, x in enumerate(X)]
+        got, = torch.autograd.grad(api.cca_attention_packed(*some, packed), some[k], dO)
+        assert torch.equal(got, want[k])
+    with torch.no_grad():
+        assert not api.cca_attention_packed(*whole, packed).requires_grad
+    again = torch.autograd.grad(api.cca_attention_packed(*whole, packed), whole[0], dO, create_graph=True)[0]
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(again.float().square().sum(), whole[0])
