@@ -244,8 +244,8 @@ __device__ __forceinline__ Item make_item(const ParamsOf<PACKED> &p, int k, [[ma
 }
 
 template <bool PACKED>
-__device__ __forceinline__ int item_at(int round) {
-    return PACKED ? item_of_round(round) : static_cast<int>(blockIdx.x + round * gridDim.x);
+__device__ __forceinline__ int item_at(int round, [[maybe_unused]] int n) {
+    return PACKED ? item_of_round(round, n) : static_cast<int>(blockIdx.x + round * gridDim.x);
 }
 
 // PACKED producer: an item's whole groups, the tensor row of a row of its sequence, and the map of its queries.
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t u = 0, cut = 0;  // ring loads issued so far, tiles cut
             int n_iter = 0;
             bool ok = true;
-            for (int k; ok && (k = item_at<PACKED>(n_iter)) < n_items; ++n_iter) {
+            for (int k; ok && (k = item_at<PACKED>(n_iter, n_items)) < n_items; ++n_iter) {
                 const Item it = make_item<PACKED>(p, k, begin);
                 const int groups = groups_of(p, it);
                 if (!wwait(bar(B_QFREE), (n_iter & 1) ^ 1)) break;
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t u = 0;  // ring loads issued so far
             int n_iter = 0;
             bool ok = true;
-            for (int k; ok && (k = item_at<PACKED>(n_iter)) < n_items; ++n_iter) {
+            for (int k; ok && (k = item_at<PACKED>(n_iter, n_items)) < n_items; ++n_iter) {
                 const Item it = make_item<PACKED>(p, k, begin);
                 if (!ptx::wait_bounded(bar(B_QFREE), (n_iter & 1) ^ 1, abort_flag, lim)) break;
                 if (!p.skip_q_load) {
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t dk0 = ptx::smem_desc_sw128(base + OFF_RING, 16, 1024);
             const uint64_t dv0 = ptx::smem_desc_sw128(base + OFF_RING, HALF_BYTES, 1024);
             bool ok = true;
-            for (int k; ok && (k = item_at<PACKED>(n_iter)) < n_items; ++n_iter) {
+            for (int k; ok && (k = item_at<PACKED>(n_iter, n_items)) < n_items; ++n_iter) {
                 const Item it = make_item<PACKED>(p, k, begin);
                 if (!wwait(bar(B_QFULL), n_iter & 1)) break;
                 int s_left = half_count(it.hA) + half_count(it.hB);
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t sf_cnt = 0;
         int n_done = 0;  // items of this half finished
         bool ok = true;
-        for (int round = 0, k; ok && (k = item_at<PACKED>(round)) < n_items; ++round) {
+        for (int round = 0, k; ok && (k = item_at<PACKED>(round, n_items)) < n_items; ++round) {
             const Item it = make_item<PACKED>(p, k, begin);
             const Half x = h ? it.hB : it.hA;
             if (!x.valid) continue;
