@@ -784,49 +784,17 @@ def cca_packed_clear(packed: Packed, *tensors, stream=None):
     (_fast or _bound()).packed_clear(*packed._args(), *(tensors + (None,) * (4 - len(tensors))))
 
 
-def _packed_rows(t):
-    """t itself where its rows can be read in place, a contiguous copy otherwise."""
-    es = t.element_size()
-    ok = t.stride(2) == 1 and all(s >= t.shape[2] and s * es % 16 == 0 for s in t.stride()[:2]) and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
-
-
-class CcaPackedAttentionFunction(torch.autograd.Function):
-    """Autograd wrapper of cca_prefill_packed: backward = cca_packed_bwd.  Tokens of no sequence have output
-    and gradients zero."""
-
-    @staticmethod
-    def forward(ctx, Q, K, V, packed, scale, pool_mode):
-        Q, K, V = (_packed_rows(t) for t in (Q, K, V))
-        O, LSE, Kc, Vc = cca_prefill_packed(Q, K, V, packed, scale, pool_mode)
-        cca_packed_clear(packed, O)
-        ctx.save_for_backward(Q, K, V, Kc, Vc, O, LSE, packed.plan)   # a plan made anew before the backward pass is refused
-        ctx.cfg = (packed, scale, pool_mode)
-        return O
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dO):
-        if torch.cuda.is_current_stream_capturing():
-            (_fast or _bound()).check_leaves()
-        Q, K, V, Kc, Vc, O, LSE, _ = ctx.saved_tensors
-        packed, scale, pool_mode = ctx.cfg
-        grads = cca_packed_bwd(Q, K, V, Kc, Vc, O, LSE, _packed_rows(dO.to(Q.dtype)), packed, scale, pool_mode)
-        cca_packed_clear(packed, *grads)
-        return (*grads, None, None, None)
-
-
 def cca_attention_packed(Q, K, V, packed: Packed, scale: float = 0.0, pool_mode: int = 0, inv_freq=None, q_weight=None,
                          k_weight=None, norm: bool = False, **rotary):
-    """CCA attention output O [Hq, tokens, d] of packed sequences with gradients for Q, K and V.  With inv_freq
-    and weights of the norms (see cca_attention), Q and K are first normed and given their positions
-    within their sequences."""
+    """CCA attention output O [Hq, tokens, d] of packed sequences with gradients for Q, K and V; tokens of no
+    sequence have output and gradients zero.  With inv_freq and weights of the norms (see cca_attention), Q and
+    K are first normed and given their positions within their sequences."""
     if inv_freq is not None or norm or q_weight is not None or k_weight is not None:
         Q, K = _positioned(Q[None], K[None], q_weight, k_weight, norm, inv_freq, {"positions": packed.positions, **rotary})
         Q, K = Q[0], K[0]
     elif rotary:
         raise ValueError(f"{sorted(rotary)} without inv_freq")
-    return CcaPackedAttentionFunction.apply(Q, K, V, packed, scale, pool_mode)
+    return (_fast or _bound()).attention_packed(Q, K, V, *packed._args(), scale, pool_mode)
 
 
 # ---------------------------------------------------------------- paged caches

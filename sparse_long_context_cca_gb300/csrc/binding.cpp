@@ -882,6 +882,108 @@ PyObject *packed_bwd(PyObject *const *a) {
     return Py_BuildValue("(NNN)", THPVariable_Wrap(dQ), THPVariable_Wrap(dK), THPVariable_Wrap(dV));
 }
 
+// Autograd of pooling and attention over a packed batch; tokens of no sequence have outputs and gradients zero.
+struct PackedFunction : torch::autograd::Function<PackedFunction> {
+    using List = torch::autograd::variable_list;
+    using Context = torch::autograd::AutogradContext;
+
+    // x itself where its rows can be read in place, a contiguous copy otherwise
+    static at::Tensor ready(const at::Tensor &x) {
+        const int64_t es = x.element_size();
+        const bool in_place = x.stride(2) == 1 && x.stride(0) >= x.size(2) && x.stride(1) >= x.size(2) &&
+                              (x.stride(0) | x.stride(1)) * es % 16 == 0 && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
+        return in_place ? x : x.contiguous();
+    }
+    static void *data(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+    static void clear(const List &tensors, const cca_packed_t &pk, const cca_params_t &p, void *stream) {
+        cca_packed_rows_t r[4];
+        int32_t heads[4];
+        int n = 0;
+        for (const at::Tensor &t : tensors) r[n] = packed_rows(t, "tensor"), heads[n++] = static_cast<int32_t>(t.size(0));
+        check_anywhere(lib.packed_clear(r, heads, n, &pk, &p, stream), "cca_packed_clear");
+    }
+
+    struct Batch {
+        cca_packed_t pk = {};
+        cca_params_t p;
+        int64_t cores;  // rows of Kc and Vc; 0: none is seen
+        Batch(Context *ctx, const at::Tensor &q, const at::Tensor &k, const at::Tensor &plan) {
+            auto number = [&](const char *name) { return static_cast<int32_t>(ctx->saved_data[name].toInt()); };
+            pk.plan = plan.data_ptr();
+            pk.plan_bytes = plan.nbytes();
+            pk.S = number("S"), pk.T = static_cast<int32_t>(q.size(1)), pk.g = number("g"), pk.w = number("w"), pk.window_mode = number("window_mode");
+            p = params(1, q.size(0), k.size(0), q.size(2), NormFunction::type_of(q), nullptr);
+            p.scale = static_cast<float>(ctx->saved_data["scale"].toDouble());
+            p.pool_mode = number("pool_mode");
+            cores = pk.w < pk.T ? pk.T / pk.g : 0;
+        }
+    };
+
+    static at::Tensor forward(Context *ctx, const at::Tensor &q, const at::Tensor &k, const at::Tensor &v, const at::Tensor &plan, int64_t S,
+                              int64_t g, int64_t w, int64_t window_mode, double scale, int64_t pool_mode) {
+        const c10::cuda::CUDAGuard guard(q.device());
+        void *const stream = c10::cuda::getCurrentCUDAStream(q.get_device()).stream();
+        ctx->saved_data["S"] = S, ctx->saved_data["g"] = g, ctx->saved_data["w"] = w, ctx->saved_data["window_mode"] = window_mode;
+        ctx->saved_data["scale"] = scale, ctx->saved_data["pool_mode"] = pool_mode;
+        const at::Tensor x[3] = {ready(q), ready(k), ready(v)};
+        const cca_packed_rows_t Q = packed_rows(x[0], "Q"), K = packed_rows(x[1], "K"), V = packed_rows(x[2], "V");
+        const Batch b(ctx, x[0], x[1], plan);
+        at::Tensor c[2];
+        if (b.cores > 0) {
+            for (at::Tensor &t : c) t = at::empty({k.size(0), b.cores, k.size(2)}, q.options());
+            check_anywhere(lib.pool_packed(&Q, &K, &V, c[0].data_ptr(), c[1].data_ptr(), &b.pk, &b.p, stream), "cca_pool_packed");
+        }
+        const at::Tensor O = at::empty(q.sizes(), q.options()), L = at::empty({q.size(0), q.size(1)}, q.options().dtype(at::kFloat));
+        const cca_packed_rows_t o = packed_rows(O, "O");
+        check_anywhere(lib.attn_packed(&Q, &K, &V, data(c[0]), data(c[1]), &o, static_cast<float *>(L.data_ptr()), &b.pk, &b.p, stream),
+                       "cca_attn_packed");
+        clear({O}, b.pk, b.p, stream);
+        ctx->save_for_backward({x[0], x[1], x[2], c[0], c[1], O, L, plan});  // a plan made anew before the backward pass is refused
+        return O;
+    }
+
+    static List backward(Context *ctx, const List &grads) {
+        TORCH_CHECK(!c10::GradMode::is_enabled() || !grads[0].requires_grad(), "cca_attention_packed: its gradient cannot be differentiated again");
+        refuse_uncapturable_leaves();
+        const List s = ctx->get_saved_variables();
+        const c10::cuda::CUDAGuard guard(s[0].device());
+        void *const stream = c10::cuda::getCurrentCUDAStream(s[0].get_device()).stream();
+        const Batch b(ctx, s[0], s[1], s[7]);
+        const at::Tensor dO = ready(grads[0].to(s[0].scalar_type()));
+        List out;
+        cca_packed_rows_t in[5], d[3];
+        const at::Tensor *const read[5] = {&s[0], &s[1], &s[2], &s[5], &dO};
+        for (int i = 0; i < 5; ++i) in[i] = packed_rows(*read[i], "a saved tensor");
+        for (int i = 0; i < 3; ++i) {
+            out.push_back(at::empty(s[i].sizes(), s[i].options()));
+            d[i] = packed_rows(out[i], "a gradient");
+        }
+        const int64_t bytes = static_cast<int64_t>(lib.packed_bwd_workspace_size(&b.pk, &b.p));
+        const at::Tensor space = at::empty({bytes < 16 ? 16 : bytes}, s[0].options().dtype(at::kByte));
+        check_anywhere(lib.packed_bwd(&in[0], &in[1], &in[2], data(s[3]), data(s[4]), &in[3], static_cast<const float *>(s[6].data_ptr()), &in[4],
+                                      &d[0], &d[1], &d[2], &b.pk, &b.p, space.data_ptr(), space.nbytes(), stream),
+                       "cca_packed_bwd");
+        clear(out, b.pk, b.p, stream);
+        out.resize(10);
+        return out;
+    }
+};
+
+// Q, K, V, plan, S, T, g, w, window_mode, scale, pool_mode
+PyObject *attention_packed(PyObject *const *a) {
+    const at::Tensor &q = leader(a[0], "Q", 3), &k = leader(a[1], "K", 3), &v = tensor(a[2], "V");
+    const Place at(q);
+    const cca_packed_t pk = packed(a + 3, at.dev);
+    dtype_of(q, "Q");
+    same(a[1], "K", q.scalar_type(), {k.size(0), q.size(1), q.size(2)}, at.dev);
+    same(a[2], "V", q.scalar_type(), k.sizes(), at.dev);
+    if (q.size(1) != pk.T) refuse("Q has %lld tokens, the plan %d", static_cast<long long>(q.size(1)), pk.T);
+    const at::Tensor &plan = THPVariable_Unpack(a[3]);
+    return THPVariable_Wrap(PackedFunction::apply(q, k, v, plan, static_cast<int64_t>(pk.S), static_cast<int64_t>(pk.g), static_cast<int64_t>(pk.w),
+                                                  static_cast<int64_t>(pk.window_mode), static_cast<double>(real(a[9], "scale")),
+                                                  static_cast<int64_t>(int32(a[10], "pool_mode"))));
+}
+
 // plan, S, T, g, w, window_mode, four tensors
 PyObject *packed_clear(PyObject *const *a) {
     const at::Tensor &first = leader(a[6], "tensor", 3);
@@ -1112,6 +1214,7 @@ PyMethodDef methods[] = {CCA_ENTRY(rope, 10),
                          CCA_ENTRY(attn_packed, 15),
                          CCA_ENTRY(packed_bwd, 21),
                          CCA_ENTRY(packed_clear, 10),
+                         CCA_ENTRY(attention_packed, 11),
                          CCA_ENTRY(tree_fwd, 17),
                          CCA_ENTRY(pool_pages, 14),
                          CCA_ENTRY(pages_reserve, 8),
