@@ -12,7 +12,8 @@
 
 namespace cca {
 
-// Launches a kernel as a programmatic dependent of what the stream ran before it.
+// Launches a kernel as a programmatic dependent of what the stream ran before it.  A kernel that allocates
+// tensor memory does so before it lets dependents start: one of them could take it first, and wait for it.
 template <typename... P, typename... A>
 cudaError_t start_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
