@@ -260,14 +260,16 @@ __global__ void __launch_bounds__(POOL_WARPS * 32, POOL_BLOCKS) pool_packed_kern
 
 // ---------------------------------------------------------------- backward: D, and the pooling's gradient
 
-// D_i = dO_i . O_i, a row per LPR lanes: bound by memory (16 K rows of 32 heads of 128, 268 MB, 45 us, 6.0 TB/s).
+// D_i = dO_i . O_i, a row per LPR lanes (and zeros for the counters of the kernels behind it): bound by memory (16 K rows of 32 heads of 128, 268 MB, 45 us, 6.0 TB/s).
 constexpr int D_ROWS = 4;
 template <typename T, int D>
-__global__ void __launch_bounds__(256) packed_d_kernel(Rows<const char> O, Rows<const char> dO, float *out, Plan plan, int Hq, int heads_first) {
+__global__ void __launch_bounds__(256) packed_d_kernel(Rows<const char> O, Rows<const char> dO, float *out, Plan plan, int Hq, int heads_first,
+                                                       int32_t *zero, int n_zero) {
     using RT = Row16<T>;
     constexpr int E = RT::E, LPR = D / E;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n_zero; i += gridDim.x * 256ll) zero[i] = 0;
     const int64_t n = static_cast<int64_t>(plan.T) * Hq;
     uint4 a[D_ROWS], b[D_ROWS];
     int64_t at[D_ROWS];  // the row's place in `out`; -1: none
@@ -571,6 +573,12 @@ PackedArgs packed_args(const cca_packed_t &pk, const cca_params_t &p) {
     return a;
 }
 
+// Tiles of tokens (of all KV heads) an SM up to which long ones are dealt out in halves: the longest item is longer
+// than a CTA's mean then.  One sequence of 4 K tokens, 16 heads over 4 (0.9 an SM) 193 -> 132 us, three of 4 K over one
+// (0.2) 147 -> 86, six of 8 K over 4 (1.8) 128 -> 115; with 3.5 an SM six of 16 K gain 4% and six of 8 K with 8 heads
+// over 8 lose 7%.
+constexpr int HALVED_TILES = 2;
+
 inline uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
 uint64_t bwd_space(const cca_packed_t &pk, const cca_params_t &p, int sms, char *base, PackedBwdSpace *w) {
@@ -582,16 +590,27 @@ uint64_t bwd_space(const cca_packed_t &pk, const cca_params_t &p, int sms, char 
         at += round256(n);
         return r;
     };
-    // The query rows of a core tile are split so that the tiles fill the SMs several times over (a tile's
-    // rows are a serial chain); 8 parts at most.
+    // The query rows of a core tile are split so that there is an item for every SM (a tile's rows are a serial
+    // chain, and its items go to whoever comes); 8 parts at most.  Four items an SM were no faster, and the
+    // pooling's gradient adds more parts up (29 us instead of 24 for 16 K tokens).
     int splits = 1;
     if (cores) {
         const int64_t tiles = (static_cast<int64_t>(G) / PACK_TILE + 1) * p.Hkv;
-        while (splits < 8 && tiles * splits < 4ll * sms) splits *= 2;
+        while (splits < 8 && tiles * splits < sms) splits *= 2;
     }
     PackedBwdSpace s = {};
     s.splits = splits;
     s.D = take(4ull * p.Hq * pk.T);
+    s.token_splits = 1;
+    if (p.dtype == CCA_BF16) {
+        const PlanLayout l = plan_layout(pk.S, pk.T, pk.g);
+        const int64_t tiles = static_cast<int64_t>(l.max_tiles) * p.Hkv;
+        if (tiles <= HALVED_TILES * sms) s.token_splits = 2;
+        s.n_zero = 2 + (s.token_splits == 2 ? static_cast<int>(tiles) * 8 : 0);
+        s.taken = reinterpret_cast<int32_t *>(take(4ull * s.n_zero));
+        s.there = s.taken + 2;
+        if (s.token_splits == 2) s.parts = take(tiles * 2 * 2ull * PACK_TILE * p.d * 4);
+    }
     if (cores) {
         s.dKc = take(core * splits);
         s.dVc = take(core * splits);
@@ -803,7 +822,7 @@ int cca_packed_bwd(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const
         const int64_t per = D_ROWS * 256 / (D * sizeof(X) / 16), blocks = (static_cast<int64_t>(T) * p.Hq + per - 1) / per;
         if (blocks > 0x7fffffff) return cudaErrorNotSupported;
         return start_dependent(packed_d_kernel<X, D>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, in_bytes(*O, p.dtype),
-                               in_bytes(*dO, p.dtype), w.D, a.plan, p.Hq, heads_inside(*O));
+                               in_bytes(*dO, p.dtype), w.D, a.plan, p.Hq, heads_inside(*O), w.taken, w.n_zero);
     });
     if (e == cudaSuccess && cores) {
         e = part(0);

@@ -140,6 +140,13 @@ struct PackedBwdSpace {
     float *a, *cds;        // [Hkv, T]: a_t and (tau / r) ds_t
     float *qsum, *dqs;     // [Hkv, G, d]: sum of the group-last queries, and their gradient through the pooling
     int splits;            // parts of a core tile's query rows
+    // bf16: counters of the items that CTAs have taken (cores, tokens); a token tile's rows in one or two parts, with the
+    // sums of both, [tile, Hkv, 8 warps, 2], and how many of them are there
+    int32_t *taken;
+    int token_splits;
+    float *parts;
+    int32_t *there;
+    int n_zero;            // words from `taken` on that start at zero
 };
 
 cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream);

@@ -18,14 +18,15 @@
 //  dkv: an item is 128 keys (raw tokens or cores) of one KV head, over the rows of its query heads that see any:
 //     S^T = K Q^T, dP^T = V dO^T  ->  P^T over S^T, dS^T over dP^T (bf16);   dV += P^T dO,  dK += dS^T Q
 //  TMEM: S^T | dP^T | dK | dV.  The rows of a core tile are split over items, whose sums are added up in order
-//  later.
+//  later; those of few tokens' tiles over two, the second of which to end adds the other's sums.
 //
-// What bounds them (32 heads over 8, 16 K tokens in five sequences, window 1024): dq 370 us, dkv of the tokens 388
-// and of the cores 92, the tensor pipe active 52 and 59% of the time.  With its parts taken out in turn, dq (376 us then) took
+// What bounds them (32 heads over 8, 16 K tokens in five sequences, window 1024): dq 370 us, dkv of the tokens 382
+// and of the cores 79, the tensor pipe active 50 and 56% of the time.  With its parts taken out in turn, dq (376 us then) took
 // 372 us without copies, 370 without exponentials, 343 without dQ's product, 310 without any product, and 229 with
 // nothing but waits, tensor-memory reads and writes, and dS: the chain of a tile through the eight element-wise
-// warps.  Sixteen of them gained nothing.  dkv of few long sequences (six of up to 2543 tokens, 132 us) is as long as
-// its longest item, 80 (query tile, head) pairs; two items for it cost more than they gain (135-140 us).
+// warps.  Sixteen of them gained nothing.  dkv without any product took 315 us of 388, and with nothing but waits,
+// tensor-memory traffic and dS 271; paired arithmetic (391), dP read at once (408) and slots handed over by the
+// barriers of P and dS (417) gained nothing either.
 //
 // P and dS are rounded to bf16 for the tensor cores (off by at most half a step, 2^-8 relative, each); everything between is fp32.
 //
@@ -71,7 +72,6 @@ struct Args {
     FastDiv by_Hq, by_Hkv, by_r, by_per;  // per: items of a dkv tile
     int per;
     float tau;
-    int core;   // dkv: core tiles (else raw ones)
     int cores;  // whether any core is seen
     unsigned long long wait_limit_ns;
     int skip_loads;  // test hook: issue no copies, so the first wait runs out
@@ -84,8 +84,8 @@ struct Layout {
     static constexpr uint32_t LONG = 2 * TILE, SHORT = LONG + LONG_ST * TILE;
     static constexpr uint32_t SLOT = SHORT + SHORT_ST * TILE;
     static constexpr uint32_t BAR = SLOT + 2 * BT * 4;
-    static constexpr uint32_t TMEM = BAR + 32 * 8, ABORT = TMEM + 4;
-    static constexpr uint32_t SMEM = ABORT + 4 + 1024;  // + slack for the 1024-byte alignment
+    static constexpr uint32_t TMEM = BAR + 32 * 8, ABORT = TMEM + 4, ITEMS = ABORT + 4;
+    static constexpr uint32_t SMEM = ITEMS + 3 * 4 + 1024;  // + slack for the 1024-byte alignment
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 // Barriers of both kernels.
@@ -102,7 +102,9 @@ constexpr int B_DSFREE = 17;                // dq: dS has been read
 constexpr int B_DONE = 18;                  // the item's sums are there
 constexpr int B_ACCFREE = 19;               // ... have been read
 constexpr int B_Q = 20, B_QT = 21;          // dq: the queries are in shared memory; in tensor memory
-constexpr int B_DRAIN = 22, B_CUT = 23, N_BARS = 24;
+constexpr int B_DRAIN = 22, B_CUT = 23;
+constexpr int B_ITEM = 24, B_ITEMFREE = 26;  // dkv: 2 each, the next item's number is there; has been read
+constexpr int N_BARS = 28;
 
 template <int HD>
 __device__ __forceinline__ void load_tile(const void *map, uint32_t bar, uint32_t dst, int y, int z) {
@@ -222,7 +224,9 @@ __device__ __forceinline__ Cta<HD> setup(uint8_t *smem_raw, const Args &p) {
     c.lim = p.wait_limit_ns;
     if (threadIdx.x == 0) {
         for (int k = 0; k < N_BARS; ++k)  // one arrival, but for those of the eight element-wise warps
-            ptx::mbar_init(c.bar(k), k == B_READ || k == B_P || k == B_DS || k == B_ACCFREE || k == B_QT ? 8 : 1);
+            ptx::mbar_init(c.bar(k), k == B_READ || k == B_P || k == B_DS || k == B_ACCFREE || k == B_QT ? 8
+                                        : k == B_ITEMFREE || k == B_ITEMFREE + 1                                        ? 2
+                                                                                                                        : 1);
         *c.abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -547,20 +551,33 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ---------------------------------------------------------------- dK, dV
 
+// Whose keys an item's are, and how items are dealt.
+//  CORES: each CTA's first item is its own, later ones go to whoever comes (92 -> 79 us).
+//  TOKENS: dealt to and fro, as dq's: items differ little where there are many, and handing numbers on costs 2%.
+//  FEW_TOKENS (up to two tiles an SM): as cores; items of more than HALVED_PAIRS (query tile, head) pairs are two,
+//  which share the rows: the longest one would be as long as the launch.  Six sequences of up to 2543 tokens, 16
+//  heads over 4: 128 us whole, 115 so (from 64 pairs on 113, 32 119, 16 125); one of 4 K tokens 193 and 132 (125, 121, 115).
+enum Kind { CORES, TOKENS, FEW_TOKENS };
+constexpr int HALVED_PAIRS = 48;
+template <Kind KIND>
 struct DkvItem {
-    int kv, n, row0, core0, y0, n_keys, qt_hi, n_it, split;
+    int kv, n, row0, core0, y0, n_keys, qt_hi, n_it, split, tile;
+    bool halved;   // another item has the rest of the rows of these tokens
+    bool nothing;  // the second item of tokens that are not halved
     __device__ __forceinline__ DkvItem(const Args &p, int item) {
-        const int splits = p.core ? p.space.splits : 1, tile = p.by_per.div(item);
-        const int4 e = (p.core ? p.plan.cores : p.plan.tiles)[tile];
+        constexpr bool CORE = KIND == CORES;
+        const int splits = CORE ? p.space.splits : KIND == FEW_TOKENS ? 2 : 1;
+        tile = p.by_per.div(item);
+        const int4 e = (CORE ? p.plan.cores : p.plan.tiles)[tile];
         kv = item - tile * p.per;
         split = p.by_Hkv.div(kv);
         kv -= split * p.Hkv;
         row0 = e.x, n = e.y, core0 = e.w;
-        n_keys = p.core ? p.plan.seen_of(n) : n;
+        n_keys = CORE ? p.plan.seen_of(n) : n;
         y0 = ((n_keys + BT - 1) / BT - 1 - e.z) * BT;  // the list's order is by the rows behind a key
         // the query rows [lo, hi] that see at least one key of the tile
         int lo = y0, hi = n - 1;
-        if (p.core) {
+        if (CORE) {
             lo = static_cast<int>(static_cast<int64_t>(y0 + 1) * p.plan.g + p.plan.w - 1);  // core j is seen from row (j+1)g + w - 1 on
         } else {
             const int64_t last = last_row(p, min(y0 + BT, n) - 1);
@@ -568,7 +585,9 @@ struct DkvItem {
         }
         int qt_lo = lo / BT;
         qt_hi = hi / BT;
-        if (splits > 1) {  // this item's part of the tiles (it may be none: its sums are zero)
+        halved = KIND == FEW_TOKENS && (qt_hi - qt_lo + 1) * p.r > HALVED_PAIRS && qt_hi > qt_lo;
+        nothing = KIND == FEW_TOKENS && !halved && split > 0;
+        if (CORE ? splits > 1 : halved) {  // this item's part of the tiles (it may be none: its sums are zero)
             const int part = (qt_hi - qt_lo + splits) / splits;
             qt_hi -= part * split;
             qt_lo = max(qt_lo, qt_hi - part + 1);
@@ -585,7 +604,8 @@ struct DkvItem {
 // The (query tile, head) pairs of an item in order.
 struct Walk {
     int h, i0, first, r;
-    __device__ __forceinline__ Walk(const Args &p, const DkvItem &d) : h(d.kv * p.r), i0(d.qt_hi * BT), first(d.kv * p.r), r(p.r) {}
+    template <typename I>
+    __device__ __forceinline__ Walk(const Args &p, const I &d) : h(d.kv * p.r), i0(d.qt_hi * BT), first(d.kv * p.r), r(p.r) {}
     __device__ __forceinline__ void next() {
         if (++h == first + r) {
             h = first;
@@ -594,17 +614,20 @@ struct Walk {
     }
 };
 
-template <int HD>
+template <int HD, Kind KIND>
 __global__ void __launch_bounds__(THREADS, 1)
     packed_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ Args p) {
     using L = Layout<HD>;
+    using Dkv = DkvItem<KIND>;
+    constexpr bool CORE = KIND == CORES, BY_NEED = KIND != TOKENS;
     extern __shared__ uint8_t smem_raw[];
     const Cta<HD> c = setup<HD>(smem_raw, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int3 counts = plan_counts(p.plan);
-    const int n_items = p.core ? counts.z * p.Hkv * p.space.splits : counts.y * p.Hkv;
+    const int n_items = (CORE ? counts.z : counts.y) * p.per;
+    volatile int *const slot_item = reinterpret_cast<volatile int *>(c.gb + L::ITEMS);  // two of the producer's, and the element-wise warps'
     constexpr uint32_t T_DP = 128, T_DK = 256, T_DV = 384;  // TMEM columns; S^T at 0
 
     if (warp == 0) {
@@ -617,12 +640,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         uint32_t g = 0, nl = 0, ns = 0, nr = 0, cut = 0;
         bool ok = !p.skip_loads;
-        for (int round = 0, item; ok && (item = item_of_round(round)) < n_items; ++round) {
-            const DkvItem d(p, item);
-            if (d.n_it == 0) continue;
+        for (int round = 0; ok; ++round) {
+            // the next item (n_items or more: none)
+            int item = item_of_round(round);
+            if constexpr (BY_NEED) {
+                if (lane == 0 && round > 0) item = gridDim.x + atomicAdd(p.space.taken + (CORE ? 0 : 1), 1);
+                item = __shfl_sync(0xffffffffu, item, 0);
+                if (!(ok = c.wait(c.bar(B_ITEMFREE + (round & 1)), ((round >> 1) & 1) ^ 1))) break;
+                if (lane == 0) {
+                    slot_item[round & 1] = item;
+                    ptx::mbar_arrive(c.bar(B_ITEM + (round & 1)));
+                }
+                __syncwarp();
+            }
+            if (item >= n_items) break;
+            const Dkv d(p, item);
+            if (d.n_it == 0 || d.nothing) continue;
             if (!c.wait(c.bar(B_RESFREE), (nr & 1) ^ 1)) break;
             if (lane == 0) {
-                const int y = (p.core ? d.core0 : d.row0) + d.y0;
+                const int y = (CORE ? d.core0 : d.row0) + d.y0;
                 ptx::mbar_arrive_expect_tx(c.bar(B_RES), 2 * L::TILE);
                 load_tile<HD>(&tmK, c.bar(B_RES), c.res(0), y, d.kv);
                 load_tile<HD>(&tmV, c.bar(B_RES), c.res(1), y, d.kv);
@@ -668,8 +704,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         };
         uint32_t g = 0, it = 0, nr = 0;
         bool ok = true;
-        for (int item; ok && (item = item_of_round(it)) < n_items; ++it) {
-            const DkvItem d(p, item);
+        for (int round = 0; ok; ++round) {
+            int item = item_of_round(round);
+            if constexpr (BY_NEED) {
+                if (!(ok = c.wait(c.bar(B_ITEM + (round & 1)), (round >> 1) & 1))) break;
+                item = slot_item[round & 1];
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(c.bar(B_ITEMFREE + (round & 1)));
+            }
+            if (item >= n_items) break;
+            const Dkv d(p, item);
+            if (d.nothing) continue;
             if (d.n_it > 0) {
                 if (!(ok = c.wait(c.bar(B_RES), nr & 1) && issue_s(g) && issue_dp(g))) break;
                 ++nr;
@@ -697,6 +742,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (ok) ptx::tc_commit_warp(c.bar(B_DONE));
+            ++it;
         }
         // whatever was issued must complete before tensor memory is freed
         ptx::tc_commit_warp(c.bar(B_DRAIN));
@@ -714,13 +760,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float4 *const slot4 = reinterpret_cast<const float4 *>(slot_f);
         uint32_t g = 0, it = 0;
         bool ok = true;
-        // Every element-wise thread runs every item, every iteration and all their named barriers, so that a time-out
-        // (which skips the work) cannot leave a barrier short of threads.
-        for (int item; (item = item_of_round(it)) < n_items; ++it) {
-            const DkvItem d(p, item);
+        // Every element-wise thread runs every iteration of an item and all their named barriers, so that a time-out (which
+        // skips the work) cannot leave a barrier short of threads.
+        for (int round = 0;; ++round) {
+            int item = item_of_round(round);
+            if constexpr (BY_NEED) {
+                // one warp waits for the item and passes it on, so that all leave together after a time-out
+                if (warp == 2) {
+                    const bool got = c.wait(c.bar(B_ITEM + (round & 1)), (round >> 1) & 1);
+                    if (lane == 0) {
+                        slot_item[2] = got ? slot_item[round & 1] : 0x7fffffff;
+                        ptx::mbar_arrive(c.bar(B_ITEMFREE + (round & 1)));
+                    }
+                    __syncwarp();
+                }
+                ptx::named_bar_sync(1, 256);
+                item = slot_item[2];
+                ptx::named_bar_sync(1, 256);
+            }
+            if (item >= n_items) break;
+            const Dkv d(p, item);
+            if (d.nothing) continue;
             const int m = d.y0 + row;  // this thread's key (core or token of the sequence)
             const bool valid = m < d.n_keys;
-            const int64_t key_last = p.core ? 0 : DkvItem::last_row(p, m);
+            const int64_t key_last = CORE ? 0 : Dkv::last_row(p, m);
             Walk at(p, d);  // the tile whose LSE and D come next
             auto slot_value = [&]() -> float {
                 const int iq = at.i0 + (e & (BT - 1));
@@ -732,7 +795,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ptx::named_bar_sync(1, 256);
             // the pooling's share of a raw token: a_m dKc_j + (tau/r) ds_m qsum_j and a_m dVc_j, j its group
             const int c0 = ch * (HD / 2), j = valid ? p.plan.by_g.div(m) : 0;
-            const bool fuse = !p.core && p.cores != 0 && valid && j < p.plan.seen_of(d.n);
+            const bool fuse = !CORE && p.cores != 0 && valid && j < p.plan.seen_of(d.n);
             const int64_t uj = (static_cast<int64_t>(d.kv) * p.plan.G + d.core0 + j) * HD + c0;
             float am = 0.f, cm = 0.f;
             if (fuse) {
@@ -757,7 +820,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t pa[32], pb[32];
                 // this key's visible query columns [q_lo, q_hi] of the tile
                 int q_lo = 0, q_hi = -1;
-                if (valid && p.core) {
+                if (valid && CORE) {
                     q_lo = max((m + 1) * p.plan.g + p.plan.w - 1 - i0, 0);
                     q_hi = min(d.n - 1 - i0, BT - 1);
                 } else if (valid) {
@@ -837,11 +900,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ptx::named_bar_sync(1, 256);
             }
             if (ok) ok = c.wait(c.bar(B_DONE), it & 1);
+            ++it;
             if (!ok) continue;
-            // dK * tau and dV; a tile that no query row sees gets zeros (and the pooling's share)
+            // dK * tau and dV, in pieces of 32 columns: of dK, then of dV
+            auto store = [&](const uint32_t (&v)[32], int k) {
+                const bool of_v = k >= HD / 64;
+                const int x0 = c0 + 32 * (k % (HD / 64));
+                const float scale = of_v ? 1.f : p.tau;
+                if (CORE) {
+                    const int64_t at = ((static_cast<int64_t>(d.split) * p.Hkv + d.kv) * p.plan.G + d.core0 + m) * HD + x0;
+                    store32_f32(v, scale, (of_v ? p.space.dVc : p.space.dKc) + at);
+                } else {
+                    const float *add = fuse ? (of_v ? p.space.dVc : p.space.dKc) + uj + 32 * (k % (HD / 64)) : nullptr;
+                    const float *qs = fuse && !of_v ? p.space.qsum + uj + 32 * (k % (HD / 64)) : nullptr;
+                    store32_bf16(v, scale, add, am, qs, cm, (of_v ? p.dV : p.dK).at(d.kv, d.row0 + m) + x0);
+                }
+            };
+            // Of two items that share these tokens, the warp that comes second adds the other's sums to its own and
+            // stores; nobody waits, and a sum of two does not depend on their order.
+            int32_t *const there = p.space.there + (static_cast<int64_t>(d.tile) * p.Hkv + d.kv) * 8 + (warp - 2);
+            float4 *const parts = reinterpret_cast<float4 *>(p.space.parts) +
+                                  ((static_cast<int64_t>(d.tile) * p.Hkv + d.kv) * 8 + (warp - 2)) * 2 * (HD * 8) + lane;
+            float4 *const mine = parts + d.split * (HD * 8), *const other = parts + (1 - d.split) * (HD * 8);
+            bool second = false;
+            if (d.halved) {
+                int count = 0;
+                if (lane == 0) count = *static_cast<volatile int32_t *>(there);
+                second = __shfl_sync(0xffffffffu, count, 0) == 1;
+                __threadfence();
+            }
             ptx::tc_fence_after();
+            // a core tile that no query row sees gets zeros
 #pragma unroll
-            for (int k = 0; k < HD / 32; ++k) {  // pieces of 32 columns: of dK, then of dV
+            for (int k = 0; k < HD / 32; ++k) {
                 const bool of_v = k >= HD / 64;
                 const int x0 = c0 + 32 * (k % (HD / 64));
                 uint32_t v[32];
@@ -857,15 +948,41 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(c.bar(B_ACCFREE));
                 }
-                if (!valid) continue;
-                const float scale = of_v ? 1.f : p.tau;
-                if (p.core) {
-                    const int64_t at = ((static_cast<int64_t>(d.split) * p.Hkv + d.kv) * p.plan.G + d.core0 + m) * HD + x0;
-                    store32_f32(v, scale, (of_v ? p.space.dVc : p.space.dKc) + at);
-                } else {
-                    const float *add = fuse ? (of_v ? p.space.dVc : p.space.dKc) + uj + 32 * (k % (HD / 64)) : nullptr;
-                    const float *qs = fuse && !of_v ? p.space.qsum + uj + 32 * (k % (HD / 64)) : nullptr;
-                    store32_bf16(v, scale, add, am, qs, cm, (of_v ? p.dV : p.dK).at(d.kv, d.row0 + m) + x0);
+                if (d.halved) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        if (second) {
+                            const float4 o = __ldcg(other + (k * 8 + q) * 32);
+                            v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + o.x);
+                            v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + o.y);
+                            v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + o.z);
+                            v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + o.w);
+                        } else {
+                            __stcg(mine + (k * 8 + q) * 32, make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                                                        __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])));
+                        }
+                    }
+                }
+                if (valid && (!d.halved || second)) store(v, k);
+            }
+            if (d.halved && !second) {
+                __threadfence();
+                __syncwarp();
+                int count = 0;
+                if (lane == 0) count = atomicAdd(there, 1);
+                if (__shfl_sync(0xffffffffu, count, 0) == 1) {  // both came at the same time: this one is the later
+                    __threadfence();
+#pragma unroll 1
+                    for (int k = 0; k < HD / 32; ++k) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float4 a = __ldcg(mine + (k * 8 + q) * 32), b = __ldcg(other + (k * 8 + q) * 32);
+                            v[4 * q] = __float_as_uint(a.x + b.x), v[4 * q + 1] = __float_as_uint(a.y + b.y);
+                            v[4 * q + 2] = __float_as_uint(a.z + b.z), v[4 * q + 3] = __float_as_uint(a.w + b.w);
+                        }
+                        if (valid) store(v, k);
+                    }
                 }
             }
         }
@@ -886,8 +1003,10 @@ cudaError_t launch(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaS
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev & 63]) {
             e = cudaFuncSetAttribute(packed_dq_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::SMEM);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(packed_dkv_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::SMEM);
+            auto room = [](auto kernel) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::SMEM); };
+            if (e == cudaSuccess) e = room(packed_dkv_tc_kernel<HD, CORES>);
+            if (e == cudaSuccess) e = room(packed_dkv_tc_kernel<HD, TOKENS>);
+            if (e == cudaSuccess) e = room(packed_dkv_tc_kernel<HD, FEW_TOKENS>);
             if (e != cudaSuccess) return e;
             done[dev & 63] = true;
         }
@@ -915,8 +1034,7 @@ cudaError_t launch(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaS
     p.Hkv = a.Hkv;
     p.r = a.Hq / a.Hkv;
     p.tau = a.scale;
-    p.core = part == 0;
-    p.per = a.Hkv * (p.core ? w.splits : 1);
+    p.per = a.Hkv * (part == 0 ? w.splits : w.token_splits);
     p.by_Hq = fast_div(a.Hq);
     p.by_Hkv = fast_div(a.Hkv);
     p.by_r = fast_div(p.r);
@@ -925,15 +1043,18 @@ cudaError_t launch(const PackedArgs &a, const PackedBwdSpace &w, int part, cudaS
     p.wait_limit_ns = g_wait_limit_ns;
     p.skip_loads = g_skip_q_load;
     const int64_t most = part == 1 ? static_cast<int64_t>(a.plan.max_tiles) * a.Hq
-                                   : static_cast<int64_t>(part == 0 ? a.plan.max_cores * w.splits : a.plan.max_tiles) * a.Hkv;
+                                   : static_cast<int64_t>(part == 0 ? a.plan.max_cores : a.plan.max_tiles) * p.per;
     if (most > 0x7fffffff) return cudaErrorNotSupported;
     const int sms = device_sms();
     if (sms < 1) return cudaErrorNoDevice;
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     if (part == 1)
         return start_dependent(packed_dq_tc_kernel<HD>, dim3(grid), THREADS, Layout<HD>::SMEM, stream, mQ, mdO, mK, mV, mKc, mVc, p);
-    return start_dependent(packed_dkv_tc_kernel<HD>, dim3(grid), THREADS, Layout<HD>::SMEM, stream, mQ, mdO, part == 0 ? mKc : mK,
-                           part == 0 ? mVc : mV, p);
+    auto dkv = [&](auto kernel) {
+        return start_dependent(kernel, dim3(grid), THREADS, Layout<HD>::SMEM, stream, mQ, mdO, part == 0 ? mKc : mK, part == 0 ? mVc : mV, p);
+    };
+    if (part == 0) return dkv(packed_dkv_tc_kernel<HD, CORES>);
+    return w.token_splits == 2 ? dkv(packed_dkv_tc_kernel<HD, FEW_TOKENS>) : dkv(packed_dkv_tc_kernel<HD, TOKENS>);
 }
 
 }  // namespace

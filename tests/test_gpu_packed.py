@@ -660,3 +660,17 @@ def test_inputs_of_which_some_need_gradients():
     again = torch.autograd.grad(api.cca_attention_packed(*whole, packed), whole[0], dO, create_graph=True)[0]
     with pytest.raises(RuntimeError):
         torch.autograd.grad(again.float().square().sum(), whole[0])
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("w,g", [(None, 16), (900, 4)])
+def test_keys_whose_rows_are_shared_by_two_items(w, g, d):
+    # eight query heads over one: long tiles of keys are dealt out in halves, whoever ends second adds them up
+    c = Case([1300, 40, 900], Hq=8, Hkv=1, d=d, g=g, w=w, first=2, tail=3)
+    O, L, Kc, Vc = c.check(what="halves")
+    want = api.cca_packed_bwd(c.Q, c.K, c.V, Kc, Vc, O, L, c.dO, c.packed, dQ=torch.zeros_like(c.Q), dK=torch.zeros_like(c.K), dV=torch.zeros_like(c.V))
+    for _ in range(30):
+        ws = torch.full((48 << 20,), 255, dtype=torch.uint8, device="cuda")
+        got = api.cca_packed_bwd(c.Q, c.K, c.V, Kc, Vc, O, L, c.dO, c.packed, workspace=ws, dQ=torch.zeros_like(c.Q), dK=torch.zeros_like(c.K),
+                                 dV=torch.zeros_like(c.V))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

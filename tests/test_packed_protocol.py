@@ -196,8 +196,13 @@ def run_dq(tiles, seed):
     return stuck
 
 
-def run_dkv(tiles, seed):
-    """tiles[i]: (query tile, head) pairs of item i; there may be none."""
+def run_dkv(tiles, seed, by_need=False):
+    """tiles[i]: (query tile, head) pairs of item i; there may be none.  by_need: the producer hands the items' numbers on, and
+    None is an item that all pass over."""
+    END = len(tiles)
+    item, itemfree = [Bar("item0"), Bar("item1")], [Bar("itemfree0", 2), Bar("itemfree1", 2)]
+    number, cur = [None, None], [None]
+
     B = {n: Bar(n, WARPS if n in ("p", "ds", "accfree", "named") else 1)
          for n in ("res", "resfree", "s", "p", "dp", "ds", "done", "accfree", "named")}
     lfull, lempty = [Bar(f"lfull{s}") for s in range(LONG)], [Bar(f"lempty{s}") for s in range(LONG)]
@@ -208,8 +213,13 @@ def run_dkv(tiles, seed):
 
     def producer():
         g = nr = 0
-        for it, n in enumerate(tiles):
-            if n == 0:
+        for it in range(END + 1):
+            if by_need:
+                yield itemfree[it & 1], it // 2
+                number[it & 1] = it
+                item[it & 1].arrive()
+            n = tiles[it] if it < END else None
+            if not n:
                 continue
             yield B["resfree"], nr
             smem["kv"] = it
@@ -245,7 +255,15 @@ def run_dkv(tiles, seed):
             pipe.issue(dp)
             pipe.commit(B["dp"])
 
-        for it, n in enumerate(tiles):
+        done = 0
+        for it in range(END + 1):
+            if by_need:
+                yield item[it & 1], it // 2 + 1
+                assert number[it & 1] == it
+                itemfree[it & 1].arrive()
+            n = tiles[it] if it < END else None
+            if n is None:
+                continue
             if n > 0:
                 yield B["res"], nr + 1
                 yield from issue_s(g, it)
@@ -254,11 +272,11 @@ def run_dkv(tiles, seed):
                 if n == 1:
                     pipe.commit(B["resfree"])
             else:
-                yield B["accfree"], it
+                yield B["accfree"], done
             for x in range(n):
                 yield B["p"], g + 1
                 if x == 0:
-                    yield B["accfree"], it
+                    yield B["accfree"], done
 
                 def dv(g=g, it=it, x=x):
                     assert tmem["s"] == [("p", g)] * WARPS and smem["do"][g % SHORT] == g
@@ -282,10 +300,24 @@ def run_dkv(tiles, seed):
                         pipe.commit(B["resfree"])
                 g += 1
             pipe.commit(B["done"])
+            done += 1
 
     def warp(w):
-        g = named = 0
-        for it, n in enumerate(tiles):
+        g = named = done = 0
+        for it in range(END + 1):
+            if by_need:
+                if w == 0:
+                    yield item[it & 1], it // 2 + 1
+                    cur[0] = number[it & 1]
+                    itemfree[it & 1].arrive()
+                for read in (True, False):      # the second barrier: every warp has read it
+                    B["named"].arrive()
+                    named += 1
+                    yield B["named"], named
+                    assert not read or cur[0] == it
+            n = tiles[it] if it < END else None
+            if n is None:
+                continue
             if n > 0:
                 smem["slot"][w] = g
             B["named"].arrive()
@@ -307,7 +339,8 @@ def run_dkv(tiles, seed):
                     if move:
                         smem["slot"][w] = g + 1 if x + 1 < n else None
                 g += 1
-            yield B["done"], it + 1
+            yield B["done"], done + 1
+            done += 1
             assert n == 0 or tmem["dk"] == tmem["dv"] == (it, n)
             out.append((it, w))
             B["accfree"].arrive()
@@ -315,7 +348,7 @@ def run_dkv(tiles, seed):
     procs = {"producer": producer(), "issuer": issuer(), "pipe": pipe.run(), **{f"warp{w}": warp(w) for w in range(WARPS)}}
     stuck = simulate(procs, seed)
     if stuck is None:
-        assert sorted(out) == [(it, w) for it in range(len(tiles)) for w in range(WARPS)]
+        assert sorted(out) == [(it, w) for it in range(len(tiles)) if tiles[it] is not None for w in range(WARPS)]
     return stuck
 
 
@@ -332,3 +365,10 @@ def test_dq(tiles):
 def test_dkv(tiles):
     for seed in range(60):
         assert run_dkv(tiles, seed) is None
+        assert run_dkv(tiles, seed, True) is None
+
+
+@pytest.mark.parametrize("tiles", [[], [None], [3, None, 1, None, None, 0, 2], [None, None, 4, 0, None]], ids=str)
+def test_dkv_items_handed_on(tiles):
+    for seed in range(60):
+        assert run_dkv(tiles, seed, True) is None
