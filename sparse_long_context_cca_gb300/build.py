@@ -16,7 +16,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcca.so")
 BINDING = os.path.join(PKG, "_binding.so")
 BINDING_FOR = os.path.join(BUILD, "binding_for")  # what it was built for
-SOURCES = ["cca_api.cu", "pool.cu", "attn_f32.cu", "attn_tc.cu", "decode.cu", "bwd.cu", "bwd_tc.cu", "host_pipeline.cu",
+SOURCES = ["cca_api.cu", "pool.cu", "attn_f32.cu", "attn_tc.cu", "attn_packed_tc.cu", "decode.cu", "bwd.cu", "bwd_tc.cu", "host_pipeline.cu",
            "rope.cu", "norm_rope.cu", "packed.cu", "packed_f32.cu", "packed_bwd_tc.cu", "pages.cu", "pool_pages.cu", "tree.cu", "tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]

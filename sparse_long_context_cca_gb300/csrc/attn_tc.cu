@@ -36,30 +36,14 @@
 // coordinates are taken relative to q_off and kv_off.
 // Every mbarrier wait is bounded in time; on a time-out the CTA stops, drains
 // what it has in flight, frees its tensor memory and reports CCA_ERR_TIMEOUT.
-//
-// PACKED: the same kernel over packed sequences (packed.cuh).  An item's rows, its sequence's first row
-// and its cores come from the batch's plan, rows keep their indices in their sequence, and tensors are
-// read and written by strides.  What is masked must not reach an output, not even as 0 * NaN: the producer
-// sets values behind a sequence's end (the next sequence's) to zero before it hands over the tile that holds
-// them, and where a row's sums are not finite at its end it is computed again, key by key on the CUDA cores
-// (direct_rows), since a later token's value may have done it.  A short sequence (n <= 256 / 2^k)
-// fills an item with 2^k query heads of a KV head side by side, 128 / 2^k rows of each in a half, as far as
-// 2^k divides the heads: an item costs 4 us at least (its plan entry, first copies, scores, softmax, output one
-// after the other), 32 short prompts with 32 heads 31 us without and 22 with it.  d = 64 is built for packed
-// sequences alone.  12 prompts of 32 K tokens in all (32 heads over 8, window 1024) take 460 us, 1.04 PF/s of visible
-// pairs, the tensor pipe active 51% of the time: 8 tiles an item leave a quarter to an item's start and end, and
-// a tile waits for its chain as in the contiguous kernel.  Three of 64 K (15 tiles an item): 1.39 ms, 1.30 PF/s.
-// Letting a half go on with the next item by itself was slower (517 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "internal.h"
-#include "packed.cuh"
 #include "sm100_ptx.cuh"
 #include "tma_host.h"
 #include "visibility.cuh"
@@ -69,8 +53,10 @@ namespace {
 
 constexpr int BM = 128;                       // query rows per half
 constexpr int BN = 128;                       // keys per tile
+constexpr int HD = 128;                       // head dimension
 constexpr int NS = 5;                         // ring slots
-constexpr uint32_t HALF_BYTES = BN * 64 * 2;  // 64 columns of a tile, as one swizzled box
+constexpr uint32_t TILE_BYTES = BN * HD * 2;  // one bf16 128x128 tile
+constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;
 constexpr int NUM_THREADS = 320;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;    // S_h at h * 128
@@ -78,7 +64,12 @@ constexpr uint32_t TM_O = 256;  // O_h at 256 + h * 128
 constexpr float LAZY_RESCALE_LOG2 = 16.0f;  // keep a stale max while it is within 2^16
 
 constexpr uint32_t IDESC_QK = ptx::idesc_bf16_f32(BM, BN, 0, 0);  // Q, K both K-major
+constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(BM, HD, 0, 1);  // P (TMEM), V MN-major
 
+// shared-memory layout (offsets from a 1024-byte aligned base)
+constexpr uint32_t OFF_Q = 0;  // Q_A, Q_B
+constexpr uint32_t OFF_RING = 2 * TILE_BYTES;
+constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE_BYTES;
 constexpr int B_QFULL = 0;
 constexpr int B_QFREE = 1;
 constexpr int B_FULL = 2;               // NS
@@ -88,23 +79,12 @@ constexpr int B_PFULL = B_SFULL + 2;    // 2
 constexpr int B_PVDONE = B_PFULL + 2;   // 2
 constexpr int B_OFREE = B_PVDONE + 2;   // 2
 constexpr int B_DRAIN = B_OFREE + 2;
-constexpr int B_CUT = B_DRAIN + 1;      // PACKED: copies of a tile that ends behind its sequence
-constexpr int NUM_BARS = B_CUT + 1;
-
-// shared-memory layout for head dimension HD (offsets from a 1024-byte aligned base)
-template <int HD>
-struct Layout {
-    static constexpr uint32_t TILE_BYTES = BN * HD * 2;  // one bf16 tile
-    static constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(BM, HD, 0, 1);  // P (TMEM), V MN-major
-    static constexpr uint32_t OFF_Q = 0;  // Q_A, Q_B
-    static constexpr uint32_t OFF_RING = 2 * TILE_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE_BYTES;
-    static constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
-    static constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-    static constexpr uint32_t OFF_BEGIN = OFF_ABORT + 4;  // PACKED: begin[3] of make_item, and the number of items
-    static constexpr uint32_t SMEM_BYTES = OFF_BEGIN + 16 + 1024;  // slack for manual alignment
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-};
+constexpr int NUM_BARS = B_DRAIN + 1;
+constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
+constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
+constexpr uint32_t SMEM_USED = OFF_ABORT + 4;
+constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;  // slack for manual alignment
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 struct Params {
     int B, Hq, Hkv, N, g, w, n_pairs, n_items;
@@ -120,23 +100,8 @@ struct Params {
     int skip_q_load;  // test hook: never load Q, so the pipeline waits run out
     int o_align32;    // O is 32-byte aligned: the epilogue may use 32-byte stores
 };
-struct PackedParams : Params {
-    Plan plan;
-    Rows<const __nv_bfloat16> rQ, rK, rV;
-    Rows<__nv_bfloat16> rO;
-    const __nv_bfloat16 *Kc, *Vc;
-    CUtensorMap mQ[3];  // Q in boxes of 2, 4, 8 heads of 64, 32, 16 rows
-    int most;           // log2 of the heads that may share a half
-    FastDiv by_r, by_heads[4];  // by Hq / Hkv, and by Hq >> c
-};
-template <bool PACKED>
-using ParamsOf = typename std::conditional<PACKED, PackedParams, Params>::type;
 
 __device__ __forceinline__ int lo_of(int i, int w) { return window_lo(i, w); }
-// PACKED: the same without a division
-__device__ __forceinline__ int win_of(const PackedParams &p, int i) { return p.plan.start_of(i); }
-__device__ __forceinline__ int cores_of(const Params &p, int i) { return lo_of(i, p.w) / p.g; }
-__device__ __forceinline__ int cores_of(const PackedParams &p, int i) { return p.plan.cores_of(i); }
 // first raw token of row i's window (cores stay j < lo(i)/g in both modes)
 __device__ __forceinline__ int win_of(const Params &p, int i) { return window_start(i, p.w, p.g, p.window_mode); }
 
@@ -156,9 +121,6 @@ struct Item {
     int Tc;   // core tiles loaded (max of the halves' tc)
     int lo0;  // first key of local tile 0
     int T;    // tiles loaded
-    // PACKED: the sequence's first row in the tensors, its first core row, its length, the head
-    int row0, core0, n, h;
-    int lr;  // log2 of the rows of one head in a half (7, less where heads share it)
 
     __device__ __forceinline__ const Half &half(int h) const { return h ? hB : hA; }
 };
@@ -183,79 +145,38 @@ __device__ __forceinline__ int half_max_step(const Half &x, int Tc) {
     return (x.valid && x.tc > 0) ? Tc + x.kl - (x.tc - 1) : 1;
 }
 
-template <typename P>
-__device__ __forceinline__ Half make_half(const P &p, int a, int lo0, int q_off, int n_q, int rows = BM) {
+__device__ __forceinline__ Half make_half(const Params &p, int a, int lo0) {
     Half x;
     x.a = a;
-    x.valid = a - q_off < n_q;
-    x.b = min(a + rows - 1, q_off + n_q - 1);
+    x.valid = a - p.q_off < p.n_q;
+    x.b = min(a + BM - 1, p.q_off + p.n_q - 1);
     if (!x.valid) {
         x.tc = x.kl = x.kh = 0;
         return x;
     }
-    const int nc = cores_of(p, x.b);
+    const int nc = lo_of(x.b, p.w) / p.g;
     x.tc = (nc + BN - 1) / BN;
     x.kl = (win_of(p, a) - lo0) / BN;
     x.kh = (x.b - lo0) / BN + 1;
     return x;
 }
 
-// PACKED: begin[c - 1] is the first entry of pairs[] whose halves hold 2^c heads.
-template <bool PACKED>
-__device__ __forceinline__ Item make_item(const ParamsOf<PACKED> &p, int k, [[maybe_unused]] const int *begin) {
+__device__ __forceinline__ Item make_item(const Params &p, int k) {
     Item it;
-    if constexpr (PACKED) {
-        // heaviest first, all heads of a pair side by side; short sequences, the last ones, by groups of 2^c heads
-        int c = 0, at = k;
-        for (; c < 3; ++c) {
-            const int some = (begin[c] - (c > 0 ? begin[c - 1] : 0)) * (p.Hq >> c);
-            if (at < some) break;
-            at -= some;
-        }
-        int idx = p.by_heads[c].div(at);
-        at -= idx * (p.Hq >> c);
-        idx += c > 0 ? begin[c - 1] : 0;
-        const int4 e = p.plan.pairs[idx];
-        it.lr = 7 - c;
-        it.h = it.bh = at << c;
-        it.kvz = p.by_r.div(it.h);
-        it.row0 = e.x;
-        it.core0 = e.w;
-        it.n = e.y;
-        const int i0 = e.z * 2 * BM;
-        it.lo0 = win_of(p, i0);
-        it.hA = make_half(p, i0, it.lo0, 0, e.y, 1 << it.lr);
-        it.hB = make_half(p, i0 + (1 << it.lr), it.lo0, 0, e.y, 1 << it.lr);
-    } else {
-        const int BH = p.B * p.Hq;
-        const int pair = p.n_pairs - 1 - k / BH;  // heaviest pairs first
-        it.bh = k % BH;
-        const int b = it.bh / p.Hq, h = it.bh % p.Hq;
-        it.kvz = b * p.Hkv + h / (p.Hq / p.Hkv);
-        const int i0 = p.q_off + pair * 2 * BM;  // first row (indices are the sequence's)
-        it.lo0 = win_of(p, i0);
-        it.hA = make_half(p, i0, it.lo0, p.q_off, p.n_q);
-        it.hB = make_half(p, i0 + BM, it.lo0, p.q_off, p.n_q);
-    }
+    const int BH = p.B * p.Hq;
+    const int pair = p.n_pairs - 1 - k / BH;  // heaviest pairs first
+    it.bh = k % BH;
+    const int b = it.bh / p.Hq, h = it.bh % p.Hq;
+    it.kvz = b * p.Hkv + h / (p.Hq / p.Hkv);
+    const int i0 = p.q_off + pair * 2 * BM;  // first row (indices are the sequence's)
+    it.lo0 = win_of(p, i0);
+    it.hA = make_half(p, i0, it.lo0);
+    it.hB = make_half(p, i0 + BM, it.lo0);
     const int last = it.hB.valid ? it.hB.b : it.hA.b;
     it.Tc = max(it.hA.tc, it.hB.tc);
     it.T = it.Tc + (last - it.lo0) / BN + 1;
     return it;
 }
-
-template <bool PACKED>
-__device__ __forceinline__ int item_at(int round, [[maybe_unused]] int n) {
-    return PACKED ? item_of_round(round, n) : static_cast<int>(blockIdx.x + round * gridDim.x);
-}
-
-// PACKED producer: an item's whole groups, the tensor row of a row of its sequence, and the map of its queries.
-__device__ __forceinline__ int groups_of(const PackedParams &p, const Item &it) { return p.plan.by_g.div(it.n); }
-__device__ __forceinline__ int groups_of(const Params &, const Item &) { return 0; }
-__device__ __forceinline__ int tensor_row(const Params &, const Item &it, int row) { return it.row0 + row; }
-__device__ __forceinline__ const CUtensorMap *q_map(const PackedParams &p, const CUtensorMap *one, const Item &it) {
-    return it.lr < 7 ? &p.mQ[6 - it.lr] : one;
-}
-__device__ __forceinline__ const CUtensorMap *q_map(const Params &, const CUtensorMap *one, const Item &) { return one; }
 
 // Parity of the FULL barrier of the ring slot holding K for ring index u (u even).
 // Only K slots complete a FULL barrier (the tile's V copy completes the same one),
@@ -266,86 +187,17 @@ __device__ __forceinline__ void report_timeout(const Params &p) {
     if (p.status != nullptr) atomicCAS(p.status, 0, static_cast<int32_t>(-4));
 }
 
-// Rows of a half, `which` of the 32 from its row `first` on, by the definition, in fp32 and key by key, only
-// visible keys read: for rows whose sums are not finite.
-template <int HD>
-__device__ __noinline__ void direct_rows(const PackedParams &p, const Item &it, const Half &x, int first, unsigned which) {
-    constexpr int E = HD / 32;  // columns of a lane
-    const int lane = threadIdx.x & 31;
-    auto load = [&](const __nv_bfloat16 *row, float (&f)[E]) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = __bfloat162float(row[lane * E + e]);
-    };
-    const int64_t cores = (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD;
-    for (; which != 0; which &= which - 1) {
-        const int row = first + __ffs(which) - 1;
-        const int i = x.a + (row & ((1 << it.lr) - 1)), h = it.h + (row >> it.lr);
-        float q[E], o[E], m = -INFINITY, l = 0.f;
-        load(p.rQ.at(h, it.row0 + i), q);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        // visible keys, cores first, eight at a time (a key alone is a chain of shuffles)
-        const int nc = cores_of(p, i), win = win_of(p, i), n = nc + i - win + 1;
-        constexpr int KEYS = 8;
-        for (int x0 = 0; x0 < n; x0 += KEYS) {
-            float s[KEYS], v[KEYS][E], top = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < KEYS; ++x) {
-                const int key = min(x0 + x, n - 1);
-                float k[E];
-                load(key < nc ? p.Kc + cores + static_cast<int64_t>(key) * HD : p.rK.at(it.kvz, it.row0 + win + key - nc), k);
-                load(key < nc ? p.Vc + cores + static_cast<int64_t>(key) * HD : p.rV.at(it.kvz, it.row0 + win + key - nc), v[x]);
-                s[x] = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) s[x] = fmaf(q[e], k[e], s[x]);
-            }
-#pragma unroll
-            for (int x = 0; x < KEYS; ++x) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s[x] += __shfl_xor_sync(0xffffffffu, s[x], o);
-                s[x] *= p.scale_log2;
-                if (x0 + x < n) top = fmaxf(top, s[x]);
-            }
-            const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m - ref);
-            m = mn;
-            l *= f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-            for (int x = 0; x < KEYS; ++x) {
-                if (x0 + x >= n) continue;
-                const float w = exp2f(s[x] - ref);
-                l += w;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[x][e], o[e]);
-            }
-        }
-        const float inv = 1.f / l;
-        __nv_bfloat16 *out = p.rO.at(h, it.row0 + i);
-#pragma unroll
-        for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-        if (lane == 0) p.LSE[static_cast<int64_t>(h) * p.plan.T + it.row0 + i] = (m + log2f(l)) * 0.6931471805599453f;
-    }
-}
-
-template <bool PACKED, int HD>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_bf16_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKc,
-                        const __grid_constant__ CUtensorMap tmVc,
-                        const __grid_constant__ ParamsOf<PACKED> p) {
-    using L = Layout<HD>;
-    constexpr uint32_t TILE_BYTES = L::TILE_BYTES, OFF_Q = L::OFF_Q, OFF_RING = L::OFF_RING, OFF_BAR = L::OFF_BAR,
-                       IDESC_PV = L::IDESC_PV;
-    constexpr int HALVES = HD / 64;  // boxes of a tile
+                        const __grid_constant__ CUtensorMap tmVc, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *const gbase = smem_raw + (base - raw);
     auto bar = [&](int idx) -> uint32_t { return base + OFF_BAR + 8u * idx; };
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_ABORT);
-    uint32_t *tmem_ptr_smem = reinterpret_cast<uint32_t *>(gbase + L::OFF_TMEMPTR);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + OFF_ABORT);
+    uint32_t *tmem_ptr_smem = reinterpret_cast<uint32_t *>(gbase + OFF_TMEMPTR);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -364,114 +216,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::mbar_init(bar(B_OFREE + h), 4);
         }
         ptx::mbar_init(bar(B_DRAIN), 1);
-        ptx::mbar_init(bar(B_CUT), 1);
         *abort_flag = 0;
-        if constexpr (!PACKED) ptx::fence_mbar_init();
+        ptx::fence_mbar_init();
     }
     if (warp == 0) {
-        ptx::tmem_alloc(base + L::OFF_TMEMPTR, TMEM_COLS);
+        ptx::tmem_alloc(base + OFF_TMEMPTR, TMEM_COLS);
         ptx::tmem_relinquish();
-    }
-    if constexpr (PACKED) {
-        // Everything above runs while the kernel before ends.  This one does not let the next begin early: CTAs that
-        // take SMs one by one lie anywhere, and 12 prompts then take 473 us instead of 462, a training step with cores
-        // 1233 instead of 1209 (neighbours read the same keys).
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-            if (threadIdx.x == 0) {
-            const int pairs = max(plan_counts(p.plan).x, 0);
-            const int3 s = pairs > 0 ? plan_short(p.plan) : make_int3(0, 0, 0);
-            const int first[5] = {0, p.most >= 1 ? s.x : pairs, p.most >= 2 ? s.y : pairs, p.most >= 3 ? s.z : pairs, pairs};
-            int *out = reinterpret_cast<int *>(gbase + L::OFF_BEGIN), items = 0;
-            for (int c = 0; c < 4; ++c) items += (first[c + 1] - first[c]) * (p.Hq >> c);
-            for (int c = 0; c < 3; ++c) out[c] = first[c + 1];
-            out[3] = items;
-            ptx::fence_mbar_init();
-        }
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_ptr_smem;
     const uint64_t lim = p.wait_limit_ns;
-    const int *const begin = reinterpret_cast<const int *>(gbase + L::OFF_BEGIN);
-    int n_items;
-    if constexpr (PACKED) n_items = begin[3];
-    else n_items = p.n_items;
 
     if (warp < 2) {
-        if (PACKED && warp == 0) {
-            // ------------------------------------------------------------ producer over packed sequences: the
-            // whole warp, for the tiles that end behind their sequence
-            if (lane == 0) {
-                ptx::prefetch_tmap(&tmQ);
-                ptx::prefetch_tmap(&tmK);
-                ptx::prefetch_tmap(&tmV);
-                ptx::prefetch_tmap(&tmKc);
-                ptx::prefetch_tmap(&tmVc);
-            }
-            auto wwait = [&](uint32_t b, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, ptx::wait_bounded(b, parity, abort_flag, lim));
-            };
-            uint32_t u = 0, cut = 0;  // ring loads issued so far, tiles cut
-            int n_iter = 0;
-            bool ok = true;
-            for (int k; ok && (k = item_at<PACKED>(n_iter, n_items)) < n_items; ++n_iter) {
-                const Item it = make_item<PACKED>(p, k, begin);
-                const int groups = groups_of(p, it);
-                if (!wwait(bar(B_QFREE), (n_iter & 1) ^ 1)) break;
-                if (!p.skip_q_load && lane == 0) {
-                    ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * TILE_BYTES);
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t dst = base + OFF_Q + h * TILE_BYTES;
-                        const int row0 = tensor_row(p, it, h ? it.hB.a : it.hA.a);
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x)
-                            ptx::tma_load_3d(q_map(p, &tmQ, it), bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
-                    }
-                }
-                for (int t = 0; t < it.T; ++t, u += 2) {
-                    const bool core = t < it.Tc;
-                    const int first = core ? t * BN : it.lo0 + (t - it.Tc) * BN;  // the tile's first key in the sequence
-                    const int left = (core ? groups : it.n) - first;
-                    const int y = (core ? it.core0 : it.row0) + first;
-                    const int ks = u % NS, vs = (u + 1) % NS;
-                    if (!(ok = wwait(bar(B_EMPTY + ks), ((u / NS) & 1) ^ 1) && wwait(bar(B_EMPTY + vs), (((u + 1) / NS) & 1) ^ 1))) break;
-                    const uint32_t full = bar(B_FULL + ks), here = left < BN ? bar(B_CUT) : full;
-                    const uint32_t kdst = base + OFF_RING + ks * TILE_BYTES, vdst = base + OFF_RING + vs * TILE_BYTES;
-                    if (lane == 0) {
-                        const void *mk = core ? (const void *)&tmKc : (const void *)&tmK;
-                        const void *mv = core ? (const void *)&tmVc : (const void *)&tmV;
-                        ptx::mbar_arrive_expect_tx(here, 2 * TILE_BYTES);
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mk, here, kdst + x * HALF_BYTES, 64 * x, y, it.kvz);
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mv, here, vdst + x * HALF_BYTES, 64 * x, y, it.kvz);
-                    }
-                    __syncwarp();
-                    if (left >= BN) continue;
-                    if (!(ok = wwait(bar(B_CUT), cut & 1))) {
-                        volatile int never = 0;  // these copies land before the CTA exits
-                        ptx::wait_bounded(bar(B_CUT), cut & 1, &never, lim);
-                        break;
-                    }
-                    ++cut;
-                    for (int i = left * 8 + lane; i < BN * 8; i += 32)
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x) ptx::st_shared_v4(vdst + x * HALF_BYTES + i * 16, 0.f, 0.f, 0.f, 0.f);
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(full);
-                }
-            }
-            __syncwarp();
-            if (*abort_flag) {
-                // Let the copies already issued land before the CTA exits.
-                volatile int never = 0;
-                for (uint32_t v = u > 2 * NS ? u - 2 * NS : 0; v < u; v += 2)
-                    ptx::wait_bounded(bar(B_FULL + v % NS), k_full_parity(v), &never, lim);
-                if (!p.skip_q_load && n_iter > 0) ptx::wait_bounded(bar(B_QFULL), (n_iter - 1) & 1, &never, lim);
-            }
-        } else if (!PACKED && warp == 0 && lane == 0) {
+        if (warp == 0 && lane == 0) {
             // ------------------------------------------------------------ producer
             ptx::prefetch_tmap(&tmQ);
             ptx::prefetch_tmap(&tmK);
@@ -481,17 +240,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t u = 0;  // ring loads issued so far
             int n_iter = 0;
             bool ok = true;
-            for (int k; ok && (k = item_at<PACKED>(n_iter, n_items)) < n_items; ++n_iter) {
-                const Item it = make_item<PACKED>(p, k, begin);
+            for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n_iter) {
+                const Item it = make_item(p, k);
                 if (!ptx::wait_bounded(bar(B_QFREE), (n_iter & 1) ^ 1, abort_flag, lim)) break;
                 if (!p.skip_q_load) {
                     ptx::mbar_arrive_expect_tx(bar(B_QFULL), 2 * TILE_BYTES);
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t dst = base + OFF_Q + h * TILE_BYTES;
                         const int row0 = (h ? it.hB.a : it.hA.a) - p.q_off;
-#pragma unroll
-                        for (int x = 0; x < HALVES; ++x)
-                            ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst + x * HALF_BYTES, 64 * x, row0, it.bh);
+                        ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst, 0, row0, it.bh);
+                        ptx::tma_load_3d(&tmQ, bar(B_QFULL), dst + HALF_BYTES, 64, row0, it.bh);
                     }
                 }
                 for (int t = 0; ok && t < it.T; ++t, u += 2) {
@@ -511,10 +269,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const void *mk = core ? (const void *)&tmKc : (const void *)&tmK;
                     const void *mv = core ? (const void *)&tmVc : (const void *)&tmV;
                     ptx::mbar_arrive_expect_tx(full, 2 * TILE_BYTES);
-#pragma unroll
-                    for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mk, full, kdst + x * HALF_BYTES, 64 * x, y, it.kvz);
-#pragma unroll
-                    for (int x = 0; x < HALVES; ++x) ptx::tma_load_3d(mv, full, vdst + x * HALF_BYTES, 64 * x, y, it.kvz);
+                    ptx::tma_load_3d(mk, full, kdst, 0, y, it.kvz);
+                    ptx::tma_load_3d(mk, full, kdst + HALF_BYTES, 64, y, it.kvz);
+                    ptx::tma_load_3d(mv, full, vdst, 0, y, it.kvz);
+                    ptx::tma_load_3d(mv, full, vdst + HALF_BYTES, 64, y, it.kvz);
                 }
             }
             if (*abort_flag) {
@@ -543,8 +301,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t dk0 = ptx::smem_desc_sw128(base + OFF_RING, 16, 1024);
             const uint64_t dv0 = ptx::smem_desc_sw128(base + OFF_RING, HALF_BYTES, 1024);
             bool ok = true;
-            for (int k; ok && (k = item_at<PACKED>(n_iter, n_items)) < n_items; ++n_iter) {
-                const Item it = make_item<PACKED>(p, k, begin);
+            for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n_iter) {
+                const Item it = make_item(p, k);
                 if (!wwait(bar(B_QFULL), n_iter & 1)) break;
                 int s_left = half_count(it.hA) + half_count(it.hB);
                 // S_h = Q_h K(t)^T into S_h.  The first user of a ring slot waits for the copy.
@@ -558,12 +316,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         pend = (half_uses(it.hA, it.Tc, t) ? 1u : 0u) + (half_uses(it.hB, it.Tc, t) ? 1u : 0u);
                     }
                     ptx::tc_fence_after();
-                    if constexpr (HD == 128)
-                        ptx::mma_ss_k128_warp(tmem + TM_S + h * BN, h ? dq1 : dq0, dk0 + static_cast<uint64_t>(slot) * (TILE_BYTES >> 4),
-                                         IDESC_QK, 0u);
-                    else
-                        ptx::mma_ss_k64_warp(tmem + TM_S + h * BN, h ? dq1 : dq0, dk0 + static_cast<uint64_t>(slot) * (TILE_BYTES >> 4),
-                                        IDESC_QK, 0u);
+                    ptx::mma_ss_k128_warp(tmem + TM_S + h * BN, h ? dq1 : dq0, dk0 + static_cast<uint64_t>(slot) * (TILE_BYTES >> 4),
+                                     IDESC_QK, 0u);
                     ptx::tc_commit_warp(bar(B_SFULL + h));
                     --pend;
                     kpend = (kpend & ~(3u << (2 * slot))) | (pend << (2 * slot));
@@ -705,15 +459,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t sf_cnt = 0;
         int n_done = 0;  // items of this half finished
         bool ok = true;
-        for (int round = 0, k; ok && (k = item_at<PACKED>(round, n_items)) < n_items; ++round) {
-            const Item it = make_item<PACKED>(p, k, begin);
+        for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x) {
+            const Item it = make_item(p, k);
             const Half x = h ? it.hB : it.hA;
             if (!x.valid) continue;
-            int i = x.a + row;
-            if constexpr (PACKED) i = x.a + (row & ((1 << it.lr) - 1));
+            const int i = x.a + row;
             const int lo_i = win_of(p, i);           // first raw token of this row's window
-            const int nc_i = cores_of(p, i);         // cores visible to this row
-            const int nc_first = cores_of(p, x.a);
+            const int nc_i = lo_of(i, p.w) / p.g;    // cores visible to this row
+            const int nc_first = lo_of(x.a, p.w) / p.g;
             const int lo_last = win_of(p, x.b);
             float m = -INFINITY;  // running max of the log2-scaled logits
             float l = 0.f;
@@ -750,21 +503,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        if constexpr (PACKED) {
-                            // most 32-column pieces of a masked tile lie wholly inside every row's part; in the others
-                            // a column is a bit (with comparisons a masked tile took 1.8 us, three times a plain one)
-                            if (__all_sync(0xffffffffu, c_lo <= c * 32 && c_hi >= c * 32 + 31)) continue;
-                            const uint32_t seen = ptx::bits(c_lo - c * 32, c_hi - c * 32);
 #pragma unroll
-                            for (int kk = 0; kk < 32; ++kk)
-                                if (!(seen & (1u << kk))) s[c][kk] = __float_as_uint(-INFINITY);
-                        } else {
-#pragma unroll
-                            for (int kk = 0; kk < 32; ++kk) {
-                                const int col = c * 32 + kk;
-                                const float x = __uint_as_float(s[c][kk]);
-                                s[c][kk] = __float_as_uint((col < c_lo || col > c_hi) ? -INFINITY : x);
-                            }
+                        for (int kk = 0; kk < 32; ++kk) {
+                            const int col = c * 32 + kk;
+                            const float x = __uint_as_float(s[c][kk]);
+                            s[c][kk] = __float_as_uint((col < c_lo || col > c_hi) ? -INFINITY : x);
                         }
                     }
                 }
@@ -792,7 +535,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     // S_h complete => every earlier PV of this half is complete: O_h is stable.
                     const float f = rescale ? ptx::ex2(m - m_new) : 1.f;
 #pragma unroll 1
-                    for (int c = 0; c < HD / 16; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         uint32_t o[16];
                         ptx::tmem_ld16(tO + c * 16, o);
                         ptx::tmem_wait_ld16(o);
@@ -846,47 +589,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             ptx::tc_fence_after();
             const int li = i - p.q_off;  // row of O and LSE
-            bool valid;
-            __nv_bfloat16 *orow;
-            float *lse;
-            if constexpr (PACKED) {
-                valid = i <= x.b;
-                const int hh = it.h + (row >> it.lr);
-                orow = p.rO.at(hh, it.row0 + i);
-                lse = p.LSE + static_cast<int64_t>(hh) * p.plan.T + it.row0 + i;
-            } else {
-                valid = li < p.n_q;
-                orow = p.O + (static_cast<int64_t>(it.bh) * p.n_q + li) * HD;
-                lse = p.LSE + static_cast<int64_t>(it.bh) * p.n_q + li;
-            }
+            const bool valid = li < p.n_q;
             const float inv = 1.f / l;
-            uint32_t o[HD / 32][32];
+            __nv_bfloat16 *orow = p.O + (static_cast<int64_t>(it.bh) * p.n_q + li) * HD;
+            uint32_t o[4][32];
 #pragma unroll
-            for (int c = 0; c < HD / 32; ++c) ptx::tmem_ld32(tO + c * 32, o[c]);
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tO + c * 32, o[c]);
             ptx::tmem_wait_ld(o[0]);
-#pragma unroll
-            for (int c = 1; c < HD / 32; ++c) ptx::reg_touch(o[c]);
+            ptx::reg_touch(o[1]);
+            ptx::reg_touch(o[2]);
+            ptx::reg_touch(o[3]);
             // O_h is in registers: the issuer may start this half's next item
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(B_OFREE + h));
-            [[maybe_unused]] unsigned bad = 0;  // rows of this warp with a sum that is not finite
-            if constexpr (PACKED) {
-                uint64_t odd = 0;  // stays zero as long as every sum is finite
-#pragma unroll
-                for (int c = 0; c < HD / 32; ++c)
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-                        odd = ptx::fma2(ptx::f2(__uint_as_float(o[c][k]), __uint_as_float(o[c][k + 1])), 0, odd);
-                float a, b;
-                ptx::f2_split(odd, a, b);
-                bad = __ballot_sync(0xffffffffu, valid && !(a + b == 0.f));
-                if ((bad >> lane) & 1) valid = false;
-            }
             // O / l as bf16, one 32-byte sector per store (two 16-byte stores if O is
             // only 16-byte aligned)
 #pragma unroll
-            for (int c = 0; c < HD / 32; ++c) {
+            for (int c = 0; c < 4; ++c) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t v[8];
@@ -905,10 +625,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                 }
             }
-            if (valid) *lse = (m + __log2f(l)) * 0.6931471805599453f;
-            if constexpr (PACKED) {
-                if (bad != 0) direct_rows<HD>(p, it, x, quarter * 32, bad);
-            }
+            if (valid) p.LSE[static_cast<int64_t>(it.bh) * p.n_q + li] = (m + __log2f(l)) * 0.6931471805599453f;
             ++n_done;
         }
     }
@@ -926,7 +643,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 struct DeviceInfo {
     bool ready = false;
     int sms = 0;
-    cudaError_t attr_err = cudaSuccess, packed_err = cudaSuccess;
+    cudaError_t attr_err = cudaSuccess;
 };
 
 DeviceInfo &device_info(int dev) {
@@ -936,13 +653,8 @@ DeviceInfo &device_info(int dev) {
     DeviceInfo &d = info[dev & 63];
     if (!d.ready) {
         cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-        d.attr_err = cudaFuncSetAttribute(attn_bf16_tc_kernel<false, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          static_cast<int>(Layout<128>::SMEM_BYTES));
-        d.packed_err = cudaFuncSetAttribute(attn_bf16_tc_kernel<true, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            static_cast<int>(Layout<128>::SMEM_BYTES));
-        if (d.packed_err == cudaSuccess)
-            d.packed_err = cudaFuncSetAttribute(attn_bf16_tc_kernel<true, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                static_cast<int>(Layout<64>::SMEM_BYTES));
+        d.attr_err = cudaFuncSetAttribute(attn_bf16_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(SMEM_BYTES));
         d.ready = true;
     }
     return d;
@@ -994,62 +706,8 @@ cudaError_t launch_attn_bf16_tc(const void *Q, const void *K, const void *V, con
     p.skip_q_load = g_skip_q_load;
     p.o_align32 = (reinterpret_cast<uintptr_t>(O) & 31u) == 0 ? 1 : 0;
     const unsigned grid = static_cast<unsigned>(p.n_items < di.sms ? p.n_items : di.sms);
-    attn_bf16_tc_kernel<false, 128><<<grid, NUM_THREADS, Layout<128>::SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
+    attn_bf16_tc_kernel<<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(mQ, mK, mV, mKc, mVc, p);
     return cudaGetLastError();
-}
-
-cudaError_t launch_attn_packed_tc(const PackedArgs &a, cudaStream_t stream) {
-    EncodeTiledFn enc = get_encoder();
-    if (enc == nullptr) return cudaErrorNotSupported;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const DeviceInfo &di = device_info(dev);
-    if (di.packed_err != cudaSuccess) return di.packed_err;
-    CUtensorMap mQ, mK, mV, mKc, mVc;
-    PackedParams p = {};
-    while (p.most < 3 && (a.Hq / a.Hkv) % (2 << p.most) == 0) ++p.most;
-    for (int c = 0; c < p.most; ++c)
-        if (!encode_packed_bf16(enc, &p.mQ[c], a.Q, a.d, a.plan.T, a.Hq, 2 << c)) return cudaErrorInvalidValue;
-    if (!encode_packed_bf16(enc, &mQ, a.Q, a.d, a.plan.T, a.Hq) || !encode_packed_bf16(enc, &mK, a.K, a.d, a.plan.T, a.Hkv) ||
-        !encode_packed_bf16(enc, &mV, a.V, a.d, a.plan.T, a.Hkv))
-        return cudaErrorInvalidValue;
-    if (a.Kc != nullptr) {
-        const int64_t head = static_cast<int64_t>(a.plan.G) * a.d;
-        const cca_packed_rows_t kc = {const_cast<void *>(a.Kc), head, a.d}, vc = {const_cast<void *>(a.Vc), head, a.d};
-        if (!encode_packed_bf16(enc, &mKc, kc, a.d, a.plan.G, a.Hkv) || !encode_packed_bf16(enc, &mVc, vc, a.d, a.plan.G, a.Hkv))
-            return cudaErrorInvalidValue;
-    } else {
-        mKc = mK;  // no tile of cores is loaded
-        mVc = mV;
-    }
-    p.B = 1;
-    p.Hq = a.Hq;
-    p.Hkv = a.Hkv;
-    p.g = a.plan.g;
-    p.w = a.plan.w;
-    p.window_mode = a.plan.window_mode;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.LSE = a.LSE;
-    p.status = a.plan.status;
-    p.wait_limit_ns = g_wait_limit_ns;
-    p.skip_q_load = g_skip_q_load;
-    p.plan = a.plan;
-    p.by_r = fast_div(a.Hq / a.Hkv);
-    for (int c = 0; c <= p.most; ++c) p.by_heads[c] = fast_div(a.Hq >> c);
-    p.rQ = rows_of<const __nv_bfloat16>(a.Q);
-    p.rK = rows_of<const __nv_bfloat16>(a.K);
-    p.rV = rows_of<const __nv_bfloat16>(a.V);
-    p.rO = rows_of<__nv_bfloat16>(a.O);
-    p.Kc = static_cast<const __nv_bfloat16 *>(a.Kc);
-    p.Vc = static_cast<const __nv_bfloat16 *>(a.Vc);
-    p.o_align32 = ((reinterpret_cast<uintptr_t>(a.O.p) | (a.O.head_stride | a.O.row_stride) * 2) & 31u) == 0 ? 1 : 0;
-    const int64_t most = static_cast<int64_t>(a.plan.max_pairs) * a.Hq;
-    if (most > 0x7fffffff) return cudaErrorNotSupported;
-    const unsigned grid = static_cast<unsigned>(most < di.sms ? most : di.sms);
-    if (a.d == 128)
-        return start_dependent(attn_bf16_tc_kernel<true, 128>, dim3(grid), NUM_THREADS, Layout<128>::SMEM_BYTES, stream, mQ, mK, mV, mKc, mVc, p);
-    return start_dependent(attn_bf16_tc_kernel<true, 64>, dim3(grid), NUM_THREADS, Layout<64>::SMEM_BYTES, stream, mQ, mK, mV, mKc, mVc, p);
 }
 
 }  // namespace cca
