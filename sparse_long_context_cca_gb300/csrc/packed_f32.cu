@@ -9,8 +9,9 @@
 // values while scores are formed.
 //
 // 1500 tokens of four heads of 64 (few tiles): 25 us against 45 without the groups of small calls, which give
-// each SM two blocks of 32 rows whose thread groups take every second key tile; with many tiles the multiply-adds
-// bound it: eight sequences of 4 K tokens in all, 8 heads of 128, causal, take 318 us, 30 TF/s of the units' 74.
+// each SM two blocks of 32 rows whose thread groups take every second key tile, and 21 since products leave out
+// the keys that a list's last tile does not have; with many tiles the multiply-adds bound it: eight sequences of
+// 4 K tokens in all, 8 heads of 128, causal, take 297 us, 32 TF/s of the units' 74.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -52,8 +53,8 @@ __device__ __forceinline__ void copy_rows(float *dst, const float *src, int64_t 
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// s[i][j] = a_(4 ty + i) . b_(tx + 16 j)
-template <int D>
+// s[i][j] = a_(4 ty + i) . b_(tx + 16 j), j < NJ
+template <int D, int NJ = 4>
 __device__ __forceinline__ void scores(const float *a, const float *b, int ty, float (&s)[4][4]) {
     const int tx = threadIdx.x % 16;
 #pragma unroll
@@ -62,26 +63,32 @@ __device__ __forceinline__ void scores(const float *a, const float *b, int ty, f
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
-        float4 x[4], y[4];
+        float4 x[4], y[NJ];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = *reinterpret_cast<const float4 *>(a + (ty * 4 + i) * PITCH<D> + k);
-            y[i] = *reinterpret_cast<const float4 *>(b + (tx + 16 * i) * PITCH<D> + k);
-        }
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(a + (ty * 4 + i) * PITCH<D> + k);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) y[j] = *reinterpret_cast<const float4 *>(b + (tx + 16 * j) * PITCH<D> + k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < NJ; ++j)
                 s[i][j] = fmaf(x[i].w, y[j].w, fmaf(x[i].z, y[j].z, fmaf(x[i].y, y[j].y, fmaf(x[i].x, y[j].x, s[i][j]))));
     }
 }
+// The same of the first `keys` rows of b: the last tile of a list of keys often holds few.
+template <int D>
+__device__ __forceinline__ void scores_of(const float *a, const float *b, int ty, int keys, float (&s)[4][4]) {
+    if (keys > 32) scores<D, 4>(a, b, ty, s);
+    else if (keys > 16) scores<D, 2>(a, b, ty, s);
+    else scores<D, 1>(a, b, ty, s);
+}
 
-// acc[i][..] += sum_k p[4 ty + i][k] b_k over the columns 4 tx + 64 c.  GUARD: keys of weight zero take no part.
+// acc[i][..] += sum_k p[4 ty + i][k] b_k, k < keys, over the columns 4 tx + 64 c.  GUARD: keys of weight zero take no part.
 template <int D, bool GUARD>
-__device__ __forceinline__ void add_rows(const float *p, const float *b, int ty, float (&acc)[4][D / 16]) {
+__device__ __forceinline__ void add_rows(const float *p, const float *b, int ty, int keys, float (&acc)[4][D / 16]) {
     const int tx = threadIdx.x % 16;
 #pragma unroll 2
-    for (int k = 0; k < BS; k += 4) {
+    for (int k = 0; k < keys; k += 4) {
         float4 w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(p + (ty * 4 + i) * SP + k);
@@ -237,10 +244,11 @@ __global__ void __launch_bounds__(ROWS * 4 * GROUPS) attn_packed_kernel(const Si
     for (int t = group; t < keys.tiles; t += GROUPS) {
         int y0, stop;
         const bool core = keys.at(t, y0, stop);
+        const int here = min(stop - y0, BS);
         copies_wait<1>();  // all but the values
         sync();
         float s[4][4];
-        scores<D>(sQ, sK, ty, s);
+        scores_of<D>(sQ, sK, ty, here, s);
         sync();
         copy_k(t + GROUPS);
         // whether every row sees every key of the tile
@@ -272,8 +280,8 @@ __global__ void __launch_bounds__(ROWS * 4 * GROUPS) attn_packed_kernel(const Si
         }
         copies_wait<1>();  // all but the next keys
         sync();
-        if (whole) add_rows<D, false>(sP, sV, ty, o);
-        else add_rows<D, true>(sP, sV, ty, o);
+        if (whole) add_rows<D, false>(sP, sV, ty, BS, o);
+        else add_rows<D, true>(sP, sV, ty, here, o);
         sync();
         copy_v(t + GROUPS);
     }
@@ -365,15 +373,16 @@ __global__ void __launch_bounds__(ROWS * 4 * GROUPS) packed_dq_kernel(const Simt
     for (int t = group; t < keys.tiles; t += GROUPS) {
         int y0, stop;
         const bool core = keys.at(t, y0, stop);
+        const int here = min(stop - y0, BS);
         copies_wait<1>();  // all but the keys
         sync();
         float s[4][4], g[4][4];
-        scores<D>(sO, sV, ty, g);
+        scores_of<D>(sO, sV, ty, here, g);
         sync();
         copy_keys(sV, p.Vc, p.V, t + GROUPS);
         copies_wait<1>();  // all but the next values
         sync();
-        scores<D>(sQ, sK, ty, s);
+        scores_of<D>(sQ, sK, ty, here, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = b.i0 + ty * 4 + i;
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(ROWS * 4 * GROUPS) packed_dq_kernel(const Simt
             }
         }
         sync();
-        add_rows<D, false>(sP, sK, ty, dq);
+        add_rows<D, false>(sP, sK, ty, here, dq);
         sync();
         copy_keys(sK, p.Kc, p.K, t + GROUPS);
     }
