@@ -169,8 +169,8 @@ struct Keys {
     int cores, lo, tiles, end;
     __device__ __forceinline__ Keys(const Plan &p, const Block &b, int rows) {
         const int last = min(b.i0 + rows, b.n) - 1;
-        cores = visible_cores(last, p.w, p.g);
-        lo = window_start(b.i0, p.w, p.g, p.window_mode);
+        cores = p.cores_of(last);
+        lo = p.start_of(b.i0);
         end = last + 1;
         tiles = (cores + BS - 1) / BS + (end - lo + BS - 1) / BS;
     }
@@ -188,7 +188,7 @@ struct Sight {
     int i, cores, start;
     __device__ __forceinline__ Sight() {}
     __device__ __forceinline__ Sight(const Plan &p, int row)
-        : i(row), cores(visible_cores(row, p.w, p.g)), start(window_start(row, p.w, p.g, p.window_mode)) {}
+        : i(row), cores(p.cores_of(row)), start(p.start_of(row)) {}
     __device__ __forceinline__ bool sees(bool core, int key) const { return core ? key < cores : key >= start && key <= i; }
 };
 
