@@ -618,8 +618,8 @@ int cca_packed_clear(const cca_packed_rows_t *tensors, const int32_t *heads, int
 
 /*
  * cca_packed_bwd - gradients of the loss sum(dO * O) through cca_attn_packed and, where w < T,
- * cca_pool_packed, in the inputs' type (rounded once).  Kc, Vc, O, LSE are the forward's.  Sums have a
- * fixed order: results repeat to the bit.  bf16: weights and score gradients are rounded to bf16 before the
+ * cca_pool_packed, in the inputs' type (rounded once).  Kc, Vc, O, LSE are the forward's.  No sum depends
+ * on what ends first: results repeat to the bit (another batch may add up a sequence's in other parts).  bf16: weights and score gradients are rounded to bf16 before the
  * products; dO . O of rows whose keys fit one tile of 128 is formed from the weights, so that the rounding
  * of O does not reach them.  The gradients of a sequence that holds infinities or NaN
  * (in any tensor) are not defined; those of the others are not touched by it.
