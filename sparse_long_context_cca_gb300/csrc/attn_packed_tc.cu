@@ -9,8 +9,10 @@
 //
 // What is masked must not reach an output, not even as 0 * NaN: the producer sets values behind a sequence's end
 // (the next sequence's) to zero before it hands over the tile that holds them, and where a row's sums are not finite
-// at its end it is computed again, key by key on the CUDA cores (direct_rows), since a later token's value may have
-// done it.  A short sequence (n <= 256 / 2^k) fills an item with 2^k query heads of a KV head side by side, 128 / 2^k
+// although its scores are, a later token's value may have done it: the warp looks at such rows again once its last item is
+// done (mend_rows), when no bounded wait depends on it.  One sequence of 32 K tokens, causal, 8 heads over one: 1.3 ms; with a
+// NaN among its first values 1.7, an infinite one 8.2 (every later row's values are looked through), either in its last
+// row 10.7 (the other rows of its tiles are formed again); row by row inside the pipeline it was 801 ms.  A short sequence (n <= 256 / 2^k) fills an item with 2^k query heads of a KV head side by side, 128 / 2^k
 // rows of each in a half, as far as 2^k divides the heads: an item costs 4 us at least (its plan entry, first copies,
 // scores, softmax, output one after the other), 32 short prompts with 32 heads 31 us without and 22 with it (19 since).
 //
@@ -27,6 +29,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "packed.cuh"
@@ -189,66 +192,247 @@ __device__ __forceinline__ Item make_item(const Params &p, int k, const int *beg
 // and with NS odd an even u reaches each slot once every 2*NS indices.
 __device__ __forceinline__ uint32_t k_full_parity(uint32_t u) { return (u / (2 * NS)) & 1; }
 
-// Rows of a half, `which` of the 32 from its row `first` on, by the definition, in fp32 and key by key, only
-// visible keys read: for rows whose sums are not finite.
+// What a lane of a warp that holds whole rows has of one: E columns from E * lane on.
 template <int HD>
-__device__ __noinline__ void direct_rows(const Params &p, const Item &it, const Half &x, int first, unsigned which) {
-    constexpr int E = HD / 32;  // columns of a lane
-    const int lane = threadIdx.x & 31;
-    auto load = [&](const __nv_bfloat16 *row, float (&f)[E]) {
+struct Piece {
+    static constexpr int E = HD / 32;
+    using Raw = typename std::conditional<E == 4, uint2, uint32_t>::type;
+    Raw raw;
+    static __device__ __forceinline__ Piece at(const __nv_bfloat16 *row) {
+        Piece x;
+        x.raw = reinterpret_cast<const Raw *>(row)[threadIdx.x & 31];
+        return x;
+    }
+    __device__ __forceinline__ void floats(float (&f)[E]) const {
+        uint32_t w[E / 2];
+        if constexpr (E == 4) w[0] = raw.x, w[1] = raw.y;
+        else w[0] = raw;
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = __bfloat162float(row[lane * E + e]);
-    };
-    const int64_t cores = (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD;
-    for (; which != 0; which &= which - 1) {
-        const int row = first + __ffs(which) - 1;
-        const int i = x.a + (row & ((1 << it.lr) - 1)), h = it.h + (row >> it.lr);
-        float q[E], o[E], m = -INFINITY, l = 0.f;
-        load(p.Q.at(h, it.row0 + i), q);
+        for (int i = 0; i < E / 2; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+__device__ __forceinline__ bool not_finite(float x) { return !(x - x == 0.f); }
+
+// Values of a row's keys: rows [0, cores) of Vc and [from, to] of V, of one sequence and KV head.
+template <int HD>
+struct RowValues {
+    const __nv_bfloat16 *core, *token;  // rows 0
+    int64_t step;                       // from a token to the next one
+    int cores, from, to;
+    __device__ __forceinline__ int count() const { return cores + max(to - from + 1, 0); }
+    __device__ __forceinline__ Piece<HD> at(int k) const {
+        return Piece<HD>::at(k < cores ? core + static_cast<int64_t>(k) * HD : token + (from + k - cores) * step);
+    }
+    // Adds up what is not finite of the values [k0, k1), column by column: zero where nothing is, and otherwise what a
+    // sum with positive weights becomes (an infinity, or NaN of both or of a NaN).  Ends early where every lane's
+    // columns in `asked` are NaN.
+    __device__ __forceinline__ void add_odd(int k0, int k1, unsigned asked, float (&odd)[HD / 32]) const {
+        constexpr int E = HD / 32, AHEAD = 16;
+        for (int k = k0; k < k1; k += AHEAD) {
+            Piece<HD> x[AHEAD];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        // visible keys, cores first, eight at a time (a key alone is a chain of shuffles)
-        const int nc = p.plan.cores_of(i), win = p.plan.start_of(i), n = nc + i - win + 1;
-        constexpr int KEYS = 8;
-        for (int x0 = 0; x0 < n; x0 += KEYS) {
-            float s[KEYS], v[KEYS][E], top = -INFINITY;
+            for (int i = 0; i < AHEAD; ++i) x[i] = at(min(k + i, k1 - 1));
 #pragma unroll
-            for (int x = 0; x < KEYS; ++x) {
-                const int key = min(x0 + x, n - 1);
-                float k[E];
-                load(key < nc ? p.Kc + cores + static_cast<int64_t>(key) * HD : p.K.at(it.kvz, it.row0 + win + key - nc), k);
-                load(key < nc ? p.Vc + cores + static_cast<int64_t>(key) * HD : p.V.at(it.kvz, it.row0 + win + key - nc), v[x]);
-                s[x] = 0.f;
+            for (int i = 0; i < AHEAD; ++i) {
+                float f[E];
+                x[i].floats(f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) s[x] = fmaf(q[e], k[e], s[x]);
+                for (int e = 0; e < E; ++e) odd[e] += not_finite(f[e]) ? f[e] : 0.f;
+            }
+            bool all = true;
+#pragma unroll
+            for (int e = 0; e < E; ++e) all = all && (!(asked & (1u << e)) || odd[e] != odd[e]);
+            if (__all_sync(0xffffffffu, all)) return;
+        }
+    }
+};
+
+// A place of O that is to be formed again; no conversion to bf16 makes this NaN.
+constexpr uint32_t FORM_AGAIN = 0x7fa5;
+
+// Two bf16 of a word, zero where one is not finite.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    return w & ~((((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15)) * 0xffffu);
+}
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The places FORM_AGAIN of those of a half's 16 rows from `base` on that `rows` names, by one warp: values that are not finite
+// count as zero (no such place has one among its visible keys), and weights are 2^(s - LSE), about 1 at most, so that no sum
+// passes the largest number that the result does not.  16 keys a step: S = Q K^T, P in registers, O += P V.  Which columns of the
+// head a fragment's depth (S) or width (O) stands for is free as long as both sides agree, so a lane reads 16-byte pieces:
+// of keys lane / 4 at columns 32 c + 8 (lane % 4), of values (lane % 4) * 2, + 1, + 8, + 9 at lane / 4 * HD / 8.
+template <int HD>
+__device__ __forceinline__ void form_again(const Params &p, const Item &it, const Half &x, int base, unsigned rows) {
+    constexpr int C = HD / 32, NT = HD / 8;  // 16-byte pieces of a lane's share of a row; width tiles of O
+    const unsigned full = 0xffffffffu;
+    const int lane = threadIdx.x & 31, quad = lane >> 2, t = lane & 3, h = it.h + (base >> it.lr);
+    bool in[2];
+    int i[2], cores[2], from[2];
+    float lse2[2], l[2] = {0.f, 0.f};
+    uint4 q[2][C];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = quad + 8 * k;
+        in[k] = (rows >> r) & 1;
+        i[k] = min(x.a + ((base + r) & ((1 << it.lr) - 1)), x.b);
+        cores[k] = in[k] ? p.plan.cores_of(i[k]) : 0;
+        from[k] = in[k] ? p.plan.start_of(i[k]) : 0x7fffffff;
+        lse2[k] = in[k] ? p.LSE[static_cast<int64_t>(h) * p.plan.T + it.row0 + i[k]] * 1.4426950408889634f : 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) q[k][c] = *reinterpret_cast<const uint4 *>(p.Q.at(h, it.row0 + i[k]) + 32 * c + 8 * t);
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    const int64_t head = (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {  // cores, then tokens
+        const bool core = part == 0;
+        const int k0 = core ? 0 : __reduce_min_sync(full, min(from[0], from[1]));
+        const int k1 = core ? __reduce_max_sync(full, max(cores[0], cores[1])) : __reduce_max_sync(full, max(in[0] ? i[0] : 0, in[1] ? i[1] : 0)) + 1;
+        const __nv_bfloat16 *const K = core ? p.Kc + head : p.K.at(it.kvz, it.row0), *const V = core ? p.Vc + head : p.V.at(it.kvz, it.row0);
+        const int64_t ks = core ? HD : p.K.row, vs = core ? HD : p.V.row;
+#pragma unroll 1
+        for (int k = k0; k < k1; k += 16) {
+            uint4 kk[2][C], vv[4][C / 2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    kk[j][c] = *reinterpret_cast<const uint4 *>(K + min(k + 8 * j + quad, k1 - 1) * ks + 32 * c + 8 * t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int c = 0; c < C / 2; ++c)
+                    vv[j][c] = *reinterpret_cast<const uint4 *>(V + min(k + 2 * t + (j & 1) + 8 * (j >> 1), k1 - 1) * vs + quad * NT + 8 * c);
+            uint32_t w[4];  // weights, as the left side of the second product
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t lo[4] = {q[0][c].x, q[1][c].x, q[0][c].y, q[1][c].y}, hi[4] = {q[0][c].z, q[1][c].z, q[0][c].w, q[1][c].w};
+                    mma_16x8x16(s, lo, kk[j][c].x, kk[j][c].y);
+                    mma_16x8x16(s, hi, kk[j][c].z, kk[j][c].w);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = e >> 1, key = k + 8 * j + 2 * t + (e & 1);
+                    const bool seen = core ? key < cores[r] : key >= from[r] && key <= i[r];
+                    s[e] = seen ? exp2f(fmaf(s[e], p.scale_log2, -lse2[r])) : 0.f;
+                    l[r] += s[e];
+                }
+                w[2 * j] = ptx::pack_bf16x2(s[0], s[1]);
+                w[2 * j + 1] = ptx::pack_bf16x2(s[2], s[3]);
             }
 #pragma unroll
-            for (int x = 0; x < KEYS; ++x) {
+            for (int c = 0; c < C / 2; ++c) {
+                uint32_t f[4][4];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s[x] += __shfl_xor_sync(0xffffffffu, s[x], o);
-                s[x] *= p.scale_log2;
-                if (x0 + x < n) top = fmaxf(top, s[x]);
-            }
-            const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m - ref);
-            m = mn;
-            l *= f;
+                for (int j = 0; j < 4; ++j) {
+                    f[j][0] = finite_only(vv[j][c].x), f[j][1] = finite_only(vv[j][c].y);
+                    f[j][2] = finite_only(vv[j][c].z), f[j][3] = finite_only(vv[j][c].w);
+                }
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-            for (int x = 0; x < KEYS; ++x) {
-                if (x0 + x >= n) continue;
-                const float w = exp2f(s[x] - ref);
-                l += w;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[x][e], o[e]);
+                for (int n = 0; n < 8; ++n) {
+                    const unsigned half = n & 1 ? 0x7632 : 0x5410;
+                    mma_16x8x16(o[8 * c + n], w, __byte_perm(f[0][n / 2], f[1][n / 2], half), __byte_perm(f[2][n / 2], f[3][n / 2], half));
+                }
             }
         }
-        const float inv = 1.f / l;
-        __nv_bfloat16 *out = p.O.at(h, it.row0 + i);
+    }
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-        if (lane == 0) p.LSE[static_cast<int64_t>(h) * p.plan.T + it.row0 + i] = (m + log2f(l)) * 0.6931471805599453f;
+    for (int k = 0; k < 2; ++k) {
+        l[k] += __shfl_xor_sync(full, l[k], 1);
+        l[k] += __shfl_xor_sync(full, l[k], 2);
+        if (!in[k]) continue;
+        // width tile j of column n is column n * NT + j, so a lane has 2 NT columns side by side
+        __nv_bfloat16 *const out = p.O.at(h, it.row0 + i[k]) + 2 * NT * t;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (__bfloat16_as_ushort(out[n * NT + j]) == FORM_AGAIN) out[n * NT + j] = __float2bfloat16_rn(o[j][2 * k + n] / l[k]);
+    }
+}
+
+// Once more through the CTA's items, for the rows of this warp whose sums were not finite although their scores are
+// (LSE is finite).  Such a column is what the row's visible values say if one of them is not finite; if none is, a masked
+// key's value or a sum that passed the largest number has come in, and it is formed again.  The other columns stand.
+template <int HD>
+__device__ __noinline__ void mend_rows(const Params &p, int n_items, const int *begin, int h, int quarter) {
+    constexpr int E = HD / 32;
+    const unsigned full = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    __syncwarp();  // the rows that the other lanes have stored
+    for (int round = 0, k; (k = item_of_round(round, n_items)) < n_items; ++round) {
+        const Item it = make_item(p, k, begin);
+        const Half x = h ? it.hB : it.hA;
+        if (!x.valid) continue;
+        auto row_of = [&](int r) { return x.a + ((quarter * 32 + r) & ((1 << it.lr) - 1)); };   // its place in the sequence
+        auto head_of = [&](int r) { return it.h + ((quarter * 32 + r) >> it.lr); };
+        auto odd_columns = [&](const Piece<HD> &v) {
+            float f[E];
+            v.floats(f);
+            unsigned bits = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) bits |= not_finite(f[e]) ? 1u << e : 0u;
+            return bits;
+        };
+        const int mine = row_of(lane);
+        const float lse = mine <= x.b ? p.LSE[static_cast<int64_t>(head_of(lane)) * p.plan.T + it.row0 + mine] : INFINITY;
+        unsigned rows = __ballot_sync(full, !not_finite(lse)), todo = 0, asked = 0, again = 0;
+        for (; rows != 0; rows &= rows - 1) {
+            const int r = __ffs(rows) - 1;
+            const unsigned c = odd_columns(Piece<HD>::at(p.O.at(head_of(r), it.row0 + row_of(r))));
+            if (__any_sync(full, c != 0)) todo |= 1u << r;
+            asked |= c;
+        }
+        if (todo == 0) continue;
+        // what all of them see: cores [0, shared.cores), tokens [shared.from, shared.to]
+        const bool in = (todo >> lane) & 1;
+        const int i0 = __reduce_min_sync(full, in ? mine : 0x7fffffff), i1 = __reduce_max_sync(full, in ? mine : 0);
+        const RowValues<HD> shared = {p.Vc + (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD, p.V.at(it.kvz, it.row0), p.V.row,
+                                      p.plan.cores_of(i0), p.plan.start_of(i1), i0};
+        float seen[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) seen[e] = 0.f;
+        shared.add_odd(0, shared.count(), asked, seen);
+        for (; todo != 0; todo &= todo - 1) {
+            const int r = __ffs(todo) - 1, i = row_of(r);
+            __nv_bfloat16 *const out = p.O.at(head_of(r), it.row0 + i);
+            const unsigned c = odd_columns(Piece<HD>::at(out));
+            // ... and what this one sees besides: later cores, earlier tokens, later tokens
+            RowValues<HD> v = shared;
+            v.cores = p.plan.cores_of(i), v.from = p.plan.start_of(i), v.to = i;
+            float odd[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) odd[e] = seen[e];
+            const int t0 = v.cores - v.from;  // place of token 0 among the row's keys
+            v.add_odd(shared.cores, v.cores, c, odd);
+            v.add_odd(t0 + v.from, t0 + min(shared.from, i + 1), c, odd);
+            v.add_odd(t0 + max(shared.from, i0 + 1), t0 + i + 1, c, odd);
+            bool left = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (!((c >> e) & 1)) continue;
+                left = left || !not_finite(odd[e]);
+                out[lane * E + e] = not_finite(odd[e]) ? __float2bfloat16_rn(odd[e]) : __ushort_as_bfloat16(FORM_AGAIN);
+            }
+            if (__any_sync(full, left)) again |= 1u << r;
+        }
+        __syncwarp();
+        for (int k = 0; k < 32; k += 16)  // 16 rows are of one head: a half has 16 of each at least
+            if ((again >> k) & 0xffff) form_again<HD>(p, it, x, quarter * 32 + k, (again >> k) & 0xffff);
     }
 }
 
@@ -568,7 +752,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t tO = tmem + lane_addr + TM_O + h * HD;
         uint32_t sf_cnt = 0;
         int n_done = 0;  // items of this half finished
-        bool ok = true;
+        bool ok = true, mend = false;  // mend: some row of this thread has sums that are not finite
         for (int round = 0, k; ok && (k = item_of_round(round, n_items)) < n_items; ++round) {
             const Item it = make_item(p, k, begin);
             const Half x = h ? it.hB : it.hA;
@@ -699,7 +883,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 break;
             }
             ptx::tc_fence_after();
-            bool valid = i <= x.b;
+            const bool valid = i <= x.b;
             const int hh = it.h + (row >> it.lr);
             __nv_bfloat16 *const orow = p.O.at(hh, it.row0 + i);
             float *const lse = p.LSE + static_cast<int64_t>(hh) * p.plan.T + it.row0 + i;
@@ -722,8 +906,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     odd = ptx::fma2(ptx::f2(__uint_as_float(o[c][k]), __uint_as_float(o[c][k + 1])), 0, odd);
             float odd0, odd1;
             ptx::f2_split(odd, odd0, odd1);
-            const unsigned bad = __ballot_sync(0xffffffffu, valid && !(odd0 + odd1 == 0.f));  // rows of this warp
-            if ((bad >> lane) & 1) valid = false;
+            mend = mend || (valid && !(odd0 + odd1 == 0.f) && l - l == 0.f);  // l is NaN: so is the row, by its scores
             // O / l as bf16, one 32-byte sector per store (two 16-byte stores if O is
             // only 16-byte aligned)
 #pragma unroll
@@ -747,9 +930,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (valid) *lse = (m + __log2f(l)) * 0.6931471805599453f;
-            if (bad != 0) direct_rows<HD>(p, it, x, quarter * 32, bad);
             ++n_done;
         }
+        // nobody waits for this warp any more
+        if (ok && __any_sync(0xffffffffu, mend)) mend_rows<HD>(p, n_items, begin, h, quarter);
     }
 
     ptx::tc_fence_before();
