@@ -788,7 +788,8 @@ def cca_attention_packed(Q, K, V, packed: Packed, scale: float = 0.0, pool_mode:
                          k_weight=None, norm: bool = False, **rotary):
     """CCA attention output O [Hq, tokens, d] of packed sequences with gradients for Q, K and V; tokens of no
     sequence have output and gradients zero.  With inv_freq and weights of the norms (see cca_attention), Q and
-    K are first normed and given their positions within their sequences."""
+    K are first normed and given their positions within their sequences.  The gradients cannot be differentiated
+    again: under create_graph they carry an error (RuntimeError) for whoever tries."""
     if inv_freq is not None or norm or q_weight is not None or k_weight is not None:
         Q, K = _positioned(Q[None], K[None], q_weight, k_weight, norm, inv_freq, {"positions": packed.positions, **rotary})
         Q, K = Q[0], K[0]

@@ -925,9 +925,8 @@ struct PackedFunction : torch::autograd::Function<PackedFunction> {
         void *const stream = c10::cuda::getCurrentCUDAStream(q.get_device()).stream();
         ctx->saved_data["S"] = S, ctx->saved_data["g"] = g, ctx->saved_data["w"] = w, ctx->saved_data["window_mode"] = window_mode;
         ctx->saved_data["scale"] = scale, ctx->saved_data["pool_mode"] = pool_mode;
-        const at::Tensor x[3] = {ready(q), ready(k), ready(v)};
-        const cca_packed_rows_t Q = packed_rows(x[0], "Q"), K = packed_rows(x[1], "K"), V = packed_rows(x[2], "V");
-        const Batch b(ctx, x[0], x[1], plan);
+        const cca_packed_rows_t Q = packed_rows(q, "Q"), K = packed_rows(k, "K"), V = packed_rows(v, "V");
+        const Batch b(ctx, q, k, plan);
         at::Tensor c[2];
         if (b.cores > 0) {
             for (at::Tensor &t : c) t = at::empty({k.size(0), b.cores, k.size(2)}, q.options());
@@ -938,18 +937,15 @@ struct PackedFunction : torch::autograd::Function<PackedFunction> {
         check_anywhere(lib.attn_packed(&Q, &K, &V, data(c[0]), data(c[1]), &o, static_cast<float *>(L.data_ptr()), &b.pk, &b.p, stream),
                        "cca_attn_packed");
         clear({O}, b.pk, b.p, stream);
-        ctx->save_for_backward({x[0], x[1], x[2], c[0], c[1], O, L, plan});  // a plan made anew before the backward pass is refused
+        ctx->save_for_backward({q, k, v, c[0], c[1], O, L, plan});  // a plan made anew before the backward pass is refused
         return O;
     }
 
-    static List backward(Context *ctx, const List &grads) {
-        TORCH_CHECK(!c10::GradMode::is_enabled() || !grads[0].requires_grad(), "cca_attention_packed: its gradient cannot be differentiated again");
-        refuse_uncapturable_leaves();
-        const List s = ctx->get_saved_variables();
+    // dQ, dK, dV of what the forward pass saved
+    static List gradients(const Batch &b, const List &s, const at::Tensor &grad) {
         const c10::cuda::CUDAGuard guard(s[0].device());
         void *const stream = c10::cuda::getCurrentCUDAStream(s[0].get_device()).stream();
-        const Batch b(ctx, s[0], s[1], s[7]);
-        const at::Tensor dO = ready(grads[0].to(s[0].scalar_type()));
+        const at::Tensor dO = ready(grad.to(s[0].scalar_type()));
         List out;
         cca_packed_rows_t in[5], d[3];
         const at::Tensor *const read[5] = {&s[0], &s[1], &s[2], &s[5], &dO};
@@ -964,6 +960,26 @@ struct PackedFunction : torch::autograd::Function<PackedFunction> {
                                       &d[0], &d[1], &d[2], &b.pk, &b.p, space.data_ptr(), space.nbytes(), stream),
                        "cca_packed_bwd");
         clear(out, b.pk, b.p, stream);
+        return out;
+    }
+
+    // The gradients as a function of what they depend on, where someone might differentiate them again: that is an error
+    // then, and not a term that is left out.
+    struct Once : torch::autograd::Function<Once> {
+        static List forward(Context *, const at::Tensor &, const at::Tensor &, const at::Tensor &, const at::Tensor &grad, const Batch *b,
+                            const List *saved) {
+            return gradients(*b, *saved, grad);
+        }
+        static List backward(Context *, const List &) {
+            TORCH_CHECK(false, "cca_attention_packed: its gradient cannot be differentiated again");
+        }
+    };
+
+    static List backward(Context *ctx, const List &grads) {
+        refuse_uncapturable_leaves();
+        const List s = ctx->get_saved_variables();
+        const Batch b(ctx, s[0], s[1], s[7]);
+        List out = c10::GradMode::is_enabled() ? Once::apply(s[0], s[1], s[2], grads[0], &b, &s) : gradients(b, s, grads[0]);
         out.resize(10);
         return out;
     }
@@ -979,7 +995,9 @@ PyObject *attention_packed(PyObject *const *a) {
     same(a[2], "V", q.scalar_type(), k.sizes(), at.dev);
     if (q.size(1) != pk.T) refuse("Q has %lld tokens, the plan %d", static_cast<long long>(q.size(1)), pk.T);
     const at::Tensor &plan = THPVariable_Unpack(a[3]);
-    return THPVariable_Wrap(PackedFunction::apply(q, k, v, plan, static_cast<int64_t>(pk.S), static_cast<int64_t>(pk.g), static_cast<int64_t>(pk.w),
+    // copies are made outside, so that what the function saves is what its gradients depend on
+    auto in = [](const at::Tensor &x) { return PackedFunction::ready(x); };
+    return THPVariable_Wrap(PackedFunction::apply(in(q), in(k), in(v), plan, static_cast<int64_t>(pk.S), static_cast<int64_t>(pk.g), static_cast<int64_t>(pk.w),
                                                   static_cast<int64_t>(pk.window_mode), static_cast<double>(real(a[9], "scale")),
                                                   static_cast<int64_t>(int32(a[10], "pool_mode"))));
 }
