@@ -785,17 +785,19 @@ def cca_packed_clear(packed: Packed, *tensors, stream=None):
 
 
 def cca_attention_packed(Q, K, V, packed: Packed, scale: float = 0.0, pool_mode: int = 0, inv_freq=None, q_weight=None,
-                         k_weight=None, norm: bool = False, **rotary):
+                         k_weight=None, norm: bool = False, dev_status=None, **rotary):
     """CCA attention output O [Hq, tokens, d] of packed sequences with gradients for Q, K and V; tokens of no
     sequence have output and gradients zero.  With inv_freq and weights of the norms (see cca_attention), Q and
     K are first normed and given their positions within their sequences.  The gradients cannot be differentiated
-    again: under create_graph they carry an error (RuntimeError) for whoever tries."""
+    again: under create_graph they carry an error (RuntimeError) for whoever tries.
+    dev_status (int32 [1]) takes what the kernels report, of this call and of its backward pass: lengths that cca_pack
+    has refused (output and gradients are zero then), and waits that ran out (rows may be unwritten then)."""
     if inv_freq is not None or norm or q_weight is not None or k_weight is not None:
         Q, K = _positioned(Q[None], K[None], q_weight, k_weight, norm, inv_freq, {"positions": packed.positions, **rotary})
         Q, K = Q[0], K[0]
     elif rotary:
         raise ValueError(f"{sorted(rotary)} without inv_freq")
-    return (_fast or _bound()).attention_packed(Q, K, V, *packed._args(), scale, pool_mode)
+    return (_fast or _bound()).attention_packed(Q, K, V, *packed._args(), scale, pool_mode, dev_status)
 
 
 # ---------------------------------------------------------------- paged caches

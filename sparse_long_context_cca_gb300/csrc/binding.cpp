@@ -912,7 +912,8 @@ struct PackedFunction : torch::autograd::Function<PackedFunction> {
             pk.plan = plan.data_ptr();
             pk.plan_bytes = plan.nbytes();
             pk.S = number("S"), pk.T = static_cast<int32_t>(q.size(1)), pk.g = number("g"), pk.w = number("w"), pk.window_mode = number("window_mode");
-            p = params(1, q.size(0), k.size(0), q.size(2), NormFunction::type_of(q), nullptr);
+            const at::Tensor status = ctx->saved_data["status"].toTensor();
+            p = params(1, q.size(0), k.size(0), q.size(2), NormFunction::type_of(q), static_cast<int32_t *>(data(status)));
             p.scale = static_cast<float>(ctx->saved_data["scale"].toDouble());
             p.pool_mode = number("pool_mode");
             cores = pk.w < pk.T ? pk.T / pk.g : 0;
@@ -920,11 +921,13 @@ struct PackedFunction : torch::autograd::Function<PackedFunction> {
     };
 
     static at::Tensor forward(Context *ctx, const at::Tensor &q, const at::Tensor &k, const at::Tensor &v, const at::Tensor &plan, int64_t S,
-                              int64_t g, int64_t w, int64_t window_mode, double scale, int64_t pool_mode) {
+                              int64_t g, int64_t w, int64_t window_mode, double scale, int64_t pool_mode, const c10::optional<at::Tensor> &status) {
         const c10::cuda::CUDAGuard guard(q.device());
         void *const stream = c10::cuda::getCurrentCUDAStream(q.get_device()).stream();
         ctx->saved_data["S"] = S, ctx->saved_data["g"] = g, ctx->saved_data["w"] = w, ctx->saved_data["window_mode"] = window_mode;
         ctx->saved_data["scale"] = scale, ctx->saved_data["pool_mode"] = pool_mode;
+        // not among the saved tensors: it is there to be read and reset between the passes
+        ctx->saved_data["status"] = status.has_value() ? *status : at::Tensor();
         const cca_packed_rows_t Q = packed_rows(q, "Q"), K = packed_rows(k, "K"), V = packed_rows(v, "V");
         const Batch b(ctx, q, k, plan);
         at::Tensor c[2];
@@ -980,12 +983,12 @@ struct PackedFunction : torch::autograd::Function<PackedFunction> {
         const List s = ctx->get_saved_variables();
         const Batch b(ctx, s[0], s[1], s[7]);
         List out = c10::GradMode::is_enabled() ? Once::apply(s[0], s[1], s[2], grads[0], &b, &s) : gradients(b, s, grads[0]);
-        out.resize(10);
+        out.resize(11);
         return out;
     }
 };
 
-// Q, K, V, plan, S, T, g, w, window_mode, scale, pool_mode
+// Q, K, V, plan, S, T, g, w, window_mode, scale, pool_mode, dev_status
 PyObject *attention_packed(PyObject *const *a) {
     const at::Tensor &q = leader(a[0], "Q", 3), &k = leader(a[1], "K", 3), &v = tensor(a[2], "V");
     const Place at(q);
@@ -995,11 +998,13 @@ PyObject *attention_packed(PyObject *const *a) {
     same(a[2], "V", q.scalar_type(), k.sizes(), at.dev);
     if (q.size(1) != pk.T) refuse("Q has %lld tokens, the plan %d", static_cast<long long>(q.size(1)), pk.T);
     const at::Tensor &plan = THPVariable_Unpack(a[3]);
+    words(a[11], "dev_status", {1}, at.dev);
     // copies are made outside, so that what the function saves is what its gradients depend on
     auto in = [](const at::Tensor &x) { return PackedFunction::ready(x); };
     return THPVariable_Wrap(PackedFunction::apply(in(q), in(k), in(v), plan, static_cast<int64_t>(pk.S), static_cast<int64_t>(pk.g), static_cast<int64_t>(pk.w),
                                                   static_cast<int64_t>(pk.window_mode), static_cast<double>(real(a[9], "scale")),
-                                                  static_cast<int64_t>(int32(a[10], "pool_mode"))));
+                                                  static_cast<int64_t>(int32(a[10], "pool_mode")),
+                                                  none(a[11]) ? c10::nullopt : c10::optional<at::Tensor>(THPVariable_Unpack(a[11]))));
 }
 
 // plan, S, T, g, w, window_mode, four tensors
@@ -1232,7 +1237,7 @@ PyMethodDef methods[] = {CCA_ENTRY(rope, 10),
                          CCA_ENTRY(attn_packed, 15),
                          CCA_ENTRY(packed_bwd, 21),
                          CCA_ENTRY(packed_clear, 10),
-                         CCA_ENTRY(attention_packed, 11),
+                         CCA_ENTRY(attention_packed, 12),
                          CCA_ENTRY(tree_fwd, 17),
                          CCA_ENTRY(pool_pages, 14),
                          CCA_ENTRY(pages_reserve, 8),

@@ -36,3 +36,55 @@ def test_a_penalty_on_gradients_is_refused_and_not_left_out(needs, wide):
         loss = sum(x.square().sum() for x in asked) + sum(a.square().sum() for a in got)
         with pytest.raises(RuntimeError, match="differentiated again"):
             torch.autograd.grad(loss, asked)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_lengths_that_the_device_refuses_reach_the_caller(dtype):
+    X, dO, _, T = step([40], dtype=dtype)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    packed = api.cca_pack(device([0, 30, 20]), T, 16, 8)
+    O = api.cca_attention_packed(*X, packed, dev_status=status)
+    assert int(status) == api.CCA_ERR_INVALID_ARG and (O == 0).all()
+    status.zero_()                                  # the backward pass reports by itself, into a word that was reset
+    assert all((x == 0).all() for x in torch.autograd.grad(O, X, dO))
+    assert int(status) == api.CCA_ERR_INVALID_ARG
+    status.zero_()
+    f = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).cuda()
+    good = api.cca_pack(device([0, T]), T, 16, 8)
+    O = api.cca_attention_packed(*X, good, inv_freq=f, norm=True, dev_status=status)
+    torch.autograd.grad(O, X, dO)
+    assert int(status) == 0
+    for bad in (torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="dev_status"):
+            api.cca_attention_packed(*X, good, dev_status=bad)
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_waits_that_run_out_reach_the_caller(d):
+    # the kernels' test hook copies no queries: the first wait of each ends, forward and backward
+    lib = api.load_library()
+    X, dO, cu, T = step([500, 300, 40], d=d, w=100)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    packed = api.cca_pack(cu, T, 16, 100)
+
+    def run(on, call):
+        torch.cuda.synchronize()
+        lib.cca_test_set_wait_limit_ns(20_000_000 if on else 1_000_000_000)
+        lib.cca_test_skip_q_load(on)
+        try:
+            out = call()
+            torch.cuda.synchronize()
+        finally:
+            lib.cca_test_skip_q_load(0)
+            lib.cca_test_set_wait_limit_ns(1_000_000_000)
+        code = int(status)
+        status.zero_()
+        return out, code
+    want, code = run(0, lambda: api.cca_attention_packed(*X, packed, dev_status=status))
+    assert code == 0
+    assert run(1, lambda: api.cca_attention_packed(*X, packed, dev_status=status))[1] == api.CCA_ERR_TIMEOUT
+    grads, code = run(0, lambda: torch.autograd.grad(want, X, dO, retain_graph=True))
+    assert code == 0
+    assert run(1, lambda: torch.autograd.grad(want, X, dO, retain_graph=True))[1] == api.CCA_ERR_TIMEOUT
+    again, code = run(0, lambda: torch.autograd.grad(want, X, dO))
+    assert code == 0 and all(torch.equal(a, b) for a, b in zip(again, grads))
