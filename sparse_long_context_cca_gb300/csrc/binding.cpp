@@ -381,18 +381,22 @@ void refuse_uncapturable_leaves() {
     }
 }
 
+// x itself where its rows can be read in place, a copy otherwise (also where x is contiguous, but begins between 16-byte
+// boundaries).  apart: no two rows may share memory.
+at::Tensor readable(const at::Tensor &x, bool apart) {
+    const int64_t last = x.dim() - 1;
+    bool in_place = x.stride(last) == 1 && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
+    for (int64_t i = 0; i < last; ++i)
+        if (x.size(i) > 1) in_place = in_place && x.stride(i) * x.element_size() % 16 == 0 && (!apart || x.stride(i) >= x.size(last));
+    return in_place ? x : x.clone(at::MemoryFormat::Contiguous);
+}
+
 // Autograd of the rotation.  It is linear: the gradient is the rotation back, by the same kernel,
 // and can be differentiated again.  The backward pass runs on the engine's thread, without Python.
 struct RopeFunction : torch::autograd::Function<RopeFunction> {
     using List = torch::autograd::variable_list;
 
-    // x itself where its rows can be read in place, a contiguous copy otherwise
-    static at::Tensor ready(const at::Tensor &x) {
-        const int64_t es = x.element_size();
-        const bool in_place = x.stride(3) == 1 && (x.stride(0) | x.stride(1) | x.stride(2)) * es % 16 == 0 &&
-                              reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
-        return in_place ? x : x.contiguous();
-    }
+    static at::Tensor ready(const at::Tensor &x) { return readable(x, false); }
 
     static List turned(const Turn &turn, const List &in) {
         const c10::cuda::CUDAGuard guard(in[0].device());
@@ -887,13 +891,7 @@ struct PackedFunction : torch::autograd::Function<PackedFunction> {
     using List = torch::autograd::variable_list;
     using Context = torch::autograd::AutogradContext;
 
-    // x itself where its rows can be read in place, a contiguous copy otherwise
-    static at::Tensor ready(const at::Tensor &x) {
-        const int64_t es = x.element_size();
-        const bool in_place = x.stride(2) == 1 && x.stride(0) >= x.size(2) && x.stride(1) >= x.size(2) &&
-                              (x.stride(0) | x.stride(1)) * es % 16 == 0 && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
-        return in_place ? x : x.contiguous();
-    }
+    static at::Tensor ready(const at::Tensor &x) { return readable(x, true); }
     static void *data(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
     static void clear(const List &tensors, const cca_packed_t &pk, const cca_params_t &p, void *stream) {
         cca_packed_rows_t r[4];

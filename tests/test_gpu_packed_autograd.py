@@ -88,3 +88,41 @@ def test_waits_that_run_out_reach_the_caller(d):
     assert run(1, lambda: torch.autograd.grad(want, X, dO, retain_graph=True))[1] == api.CCA_ERR_TIMEOUT
     again, code = run(0, lambda: torch.autograd.grad(want, X, dO))
     assert code == 0 and all(torch.equal(a, b) for a, b in zip(again, grads))
+
+
+def shifted(x):
+    """The same values, contiguous, one element behind a 16-byte boundary."""
+    y = torch.empty(x.numel() + 1, dtype=x.dtype, device=x.device)[1:].view(x.shape)
+    y.copy_(x.detach())
+    assert y.is_contiguous() and y.data_ptr() % 16 != 0
+    return y
+
+
+@pytest.mark.parametrize("dtype,d", KINDS, ids=IDS)
+def test_tensors_off_the_copies_boundary(dtype, d):
+    # inputs and gradients that lie between 16-byte boundaries are copied, as broadcast ones are
+    X, dO, cu, T = step([40, 33], d=d, dtype=dtype, g=8, w=16)
+    packed = api.cca_pack(cu, T, 8, 16)
+    want = torch.autograd.grad(api.cca_attention_packed(*X, packed), X, dO)
+    Y = [shifted(x).requires_grad_() for x in X]
+    got = torch.autograd.grad(api.cca_attention_packed(*Y, packed), Y, shifted(dO))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # such a gradient as autograd makes it: of the output behind an odd number of other values
+    odd = torch.zeros(3, dtype=dtype, device="cuda", requires_grad=True)
+    O = api.cca_attention_packed(*X, packed)
+    row = torch.cat([odd, O.reshape(-1)])
+    got = torch.autograd.grad(row, X, torch.cat([odd.detach(), dO.reshape(-1)]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype,d", KINDS, ids=IDS)
+def test_norms_and_rotations_off_the_copies_boundary(dtype, d):
+    f = (10000.0 ** (-torch.arange(d // 2, dtype=torch.float64) / (d // 2))).cuda()
+    X = [rand(2, h, 21, d, dtype=dtype, seed=h).requires_grad_() for h in (4, 2)]
+    dY = [rand(2, h, 21, d, dtype=dtype, seed=10 + h) for h in (4, 2)]
+    w = rand(d, dtype=dtype, seed=3).requires_grad_()
+    for call, more in ((lambda q, k: api.norm_rope(q, k, w, w, f), [w]), (lambda q, k: api.rope(q, k, f), [])):
+        want = [x.detach() for x in call(*X)], torch.autograd.grad(call(*X), X + more, dY)
+        Y = [shifted(x).requires_grad_() for x in X]
+        got = [x.detach() for x in call(*Y)], torch.autograd.grad(call(*Y), Y + more, [shifted(g) for g in dY])
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
