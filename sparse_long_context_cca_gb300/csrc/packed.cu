@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(POOL_WARPS * 32, POOL_BLOCKS) pool_packed_kern
             for (int e = 0; e < E; ++e) x = fmaf(q[e], f[e], x);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+            if (a.mode == 1) x = 0.f;  // a mean has no scores, whatever the keys hold
             s[i] = base + i * RPP + sub < g ? x * scale : -INFINITY;
             top = fmaxf(top, s[i]);
         }

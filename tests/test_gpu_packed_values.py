@@ -130,3 +130,16 @@ def test_keys_that_are_not_finite():
             if bad != bad:
                 assert torch.isnan(O[:, 77:200]).all() and torch.isnan(L[:, 77:200]).all()
         assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("dtype,d", KINDS, ids=IDS)
+def test_mean_pooling_takes_no_weights_from_keys(dtype, d):
+    # the mean of a group's values does not depend on its keys
+    c = Case([64, 33], Hq=4, Hkv=2, d=d, dtype=dtype, g=8, w=16)
+    _, want = api.cca_pool_packed(c.Q, c.K, c.V, c.packed, pool_mode=1)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        Q, K = c.Q.clone(), c.K.clone()
+        K[:, 5], Q[:, 15] = bad, bad
+        Kc, Vc = api.cca_pool_packed(Q, K, c.V, c.packed, pool_mode=1)
+        assert torch.equal(Vc, want)
+        assert not torch.isfinite(Kc[:, 0]).any() and torch.isfinite(Kc[:, 1:]).all()
