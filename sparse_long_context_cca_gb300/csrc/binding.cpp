@@ -774,7 +774,9 @@ cca_packed_t packed(PyObject *const *a, int dev) {
     p.g = int32(a[3], "g");
     p.w = int32(a[4], "w");
     p.window_mode = int32(a[5], "window_mode");
-    const at::Tensor &plan = same(a[0], "plan", at::kByte, {static_cast<int64_t>(lib.pack_size(p.S, p.T, p.g))}, dev);
+    const int64_t bytes = static_cast<int64_t>(lib.pack_size(p.S, p.T, p.g));
+    if (bytes == 0) refuse("%d sequences, %d tokens, g = %d", p.S, p.T, p.g);  // g divides the tokens below
+    const at::Tensor &plan = same(a[0], "plan", at::kByte, {bytes}, dev);
     if (!plan.is_contiguous()) refuse("plan must be contiguous");
     p.plan = plan.data_ptr();
     p.plan_bytes = plan.nbytes();

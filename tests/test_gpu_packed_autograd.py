@@ -126,3 +126,14 @@ def test_norms_and_rotations_off_the_copies_boundary(dtype, d):
         Y = [shifted(x).requires_grad_() for x in X]
         got = [x.detach() for x in call(*Y)], torch.autograd.grad(call(*Y), Y + more, [shifted(g) for g in dY])
         assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+
+
+def test_a_batch_of_impossible_sizes_is_refused():
+    # an empty plan for g = 0: no number of groups can be formed from it
+    X, _, _, T = step([40])
+    for p in (api.Packed(torch.empty(0, dtype=torch.uint8, device="cuda"), None, 1, T, 0, 8, 0),
+              api.Packed(torch.empty(0, dtype=torch.uint8, device="cuda"), None, 0, T, 4, 8, 0)):
+        for call in (lambda: api.cca_pool_packed(*X, p), lambda: api.cca_attn_packed(*X, None, None, p), lambda: api.cca_attention_packed(*X, p),
+                     lambda: api.cca_packed_clear(p, X[0].detach())):
+            with pytest.raises(ValueError, match="sequences"):
+                call()
