@@ -19,7 +19,8 @@ constexpr int PACK_THREADS = 256;
 
 // ---------------------------------------------------------------- the plan
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// (a + b may pass 2^31: so may a loop's index plus its step, which is why those are unsigned)
+__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0 ? 1 : 0); }
 
 // One block column per sequence.  Entry (s, p) of a list stands behind every entry of a higher tile number
 // and behind those of the same number of longer sequences (of equal ones, the earlier first): its place is
@@ -67,15 +68,20 @@ __global__ void __launch_bounds__(PACK_THREADS) pack_kernel(const int32_t *cu, c
         }
     }
     int32_t *positions = reinterpret_cast<int32_t *>(plan + l.positions), *first = reinterpret_cast<int32_t *>(plan + l.first);
-    for (int i = tid; i < n; i += step) positions[a + i] = i;
+    auto each = [&](int from, int to, auto f) {
+        for (unsigned i = static_cast<unsigned>(from) + tid; i < static_cast<unsigned>(to); i += step) f(static_cast<int>(i));
+    };
+    each(0, n, [&](int i) { positions[a + i] = i; });
     const int c0 = a / g, c1 = (a + n) / g, groups = n / g;
-    for (int c = c0 + tid; c < c1; c += step) first[c] = c - c0 < groups ? a + (c - c0) * g : -1;
+    each(c0, c1, [&](int c) { first[c] = c - c0 < groups ? a + (c - c0) * g : -1; });
     if (s == 0) {  // tokens and core rows of no sequence
-        for (int i = tid; i < a; i += step) positions[i] = 0;
-        for (int c = tid; c < c0; c += step) first[c] = -1;
+        auto clear = [&](int i) { positions[i] = 0; };
+        auto none = [&](int c) { first[c] = -1; };
+        each(0, a, clear);
+        each(0, c0, none);
         const int end = cu[S];
-        for (int i = end + tid; i < T; i += step) positions[i] = 0;
-        for (int c = end / g + tid; c < T / g; c += step) first[c] = -1;
+        each(end, T, clear);
+        each(end / g, T / g, none);
         if (blockIdx.y == 0 && threadIdx.x < 32) {
             int count[6] = {0, 0, 0, 0, 0, 0};  // tiles of each list; sequences of 1 to 128, 64, 32 tokens
             for (int i = threadIdx.x; i < S; i += 32) {
