@@ -556,11 +556,28 @@ class CcaAttentionFunction(torch.autograd.Function):
     def backward(ctx, dO):
         if torch.cuda.is_current_stream_capturing() and _build.binding_is_for_this_torch():
             (_fast or _bound()).check_leaves()
-        Q, K, V, Kc, Vc, O, LSE = ctx.saved_tensors
-        g, w, scale, pool_mode, window_mode = ctx.cfg
-        dQ, dK, dV = cca_prefill_bwd(Q, K, V, Kc, Vc, O, LSE, dO.contiguous().to(Q.dtype), g, w, scale,
-                                     pool_mode=pool_mode, window_mode=window_mode)
-        return dQ.to(Q.dtype), dK.to(K.dtype), dV.to(V.dtype), None, None, None, None, None
+        of = _CcaGradients.apply if torch.is_grad_enabled() else _cca_gradients
+        return (*of(*ctx.saved_tensors, dO, ctx.cfg), None, None, None, None, None)
+
+
+def _cca_gradients(Q, K, V, Kc, Vc, O, LSE, dO, cfg):
+    g, w, scale, pool_mode, window_mode = cfg
+    dQ, dK, dV = cca_prefill_bwd(Q, K, V, Kc, Vc, O, LSE, dO.contiguous().to(Q.dtype), g, w, scale,
+                                 pool_mode=pool_mode, window_mode=window_mode)
+    return dQ.to(Q.dtype), dK.to(K.dtype), dV.to(V.dtype)
+
+
+class _CcaGradients(torch.autograd.Function):
+    """The gradients as a function of what they depend on, where someone might differentiate them again:
+    that is an error then, and not a term that is left out."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return _cca_gradients(*args)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("cca_attention: its gradient cannot be differentiated again")
 
 
 def _positioned(Q, K, q_weight, k_weight, norm, inv_freq, rotary):
@@ -578,8 +595,11 @@ def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 
                   inv_freq=None, q_weight=None, k_weight=None, norm: bool = False, **rotary):
     """CCA attention output O [B, Hq, N, d] with gradients for Q, K and V (prefill step).
     With inv_freq, Q and K are first given their positions by rope(Q, K, inv_freq, **rotary); with
-    weights of their norms (or norm=True), by norm_rope(Q, K, q_weight, k_weight, inv_freq, **rotary)."""
+    weights of their norms (or norm=True), by norm_rope(Q, K, q_weight, k_weight, inv_freq, **rotary).
+    The gradients cannot be differentiated again: under create_graph they carry an error (RuntimeError)."""
     Q, K = _positioned(Q, K, q_weight, k_weight, norm, inv_freq, rotary)
+    # copies are made outside the function, so that what it saves is what its gradients depend on
+    Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
     return CcaAttentionFunction.apply(Q, K, V, g, w, scale, pool_mode, window_mode)
 
 
