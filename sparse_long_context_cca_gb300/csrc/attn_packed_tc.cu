@@ -566,13 +566,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             __syncwarp();
-            if (*abort_flag) {
-                // Let the copies already issued land before the CTA exits.
-                volatile int never = 0;
-                for (uint32_t v = u > 2 * NS ? u - 2 * NS : 0; v < u; v += 2)
-                    ptx::wait_bounded(bar(B_FULL + v % NS), k_full_parity(v), &never, lim);
-                if (!p.skip_q_load && n_iter > 0) ptx::wait_bounded(bar(B_QFULL), (n_iter - 1) & 1, &never, lim);
-            }
+            // The copies land before the CTA exits.  Whoever gives up later than this may leave some that nobody else
+            // waits for; otherwise they have been waited for and this takes no time.
+            volatile int never = 0;
+            for (uint32_t v = u > 2 * NS ? u - 2 * NS : 0; v < u; v += 2)
+                ptx::wait_bounded(bar(B_FULL + v % NS), k_full_parity(v), &never, lim);
+            if (!p.skip_q_load && n_iter > 0) ptx::wait_bounded(bar(B_QFULL), (n_iter - 1) & 1, &never, lim);
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
             // The whole warp runs the issuer with identical values in every lane; the

@@ -256,7 +256,8 @@ __device__ __forceinline__ void finish(const Cta<HD> &c, const Args &p) {
     }
 }
 
-// The producer's wait for its last copies after a time-out: `nl`, `ns` tiles were asked for, `nr` times the resident ones.
+// The producer's wait for its last copies: `nl`, `ns` tiles were asked for, `nr` times the resident ones.  Not only where the
+// abort flag is set: whoever gives up later than this may leave copies that nobody else waits for.
 template <int HD>
 __device__ __forceinline__ void drain_copies(const Cta<HD> &c, uint32_t nl, uint32_t ns, uint32_t nr) {
     volatile int never = 0;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         __syncwarp();
-        if (*c.abort_flag && !p.skip_loads) {
+        if (!p.skip_loads) {
             drain_copies(c, nl, ns, it);
             volatile int never = 0;
             if (nq > 0) ptx::wait_bounded(c.bar(B_Q), (nq - 1) & 1, &never, c.lim);
@@ -680,7 +681,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         __syncwarp();
-        if (*c.abort_flag && !p.skip_loads) drain_copies(c, nl, ns, nr);
+        if (!p.skip_loads) drain_copies(c, nl, ns, nr);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
