@@ -78,7 +78,8 @@ struct Layout {
     static constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE_BYTES;
     static constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
     static constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-    static constexpr uint32_t OFF_BEGIN = OFF_ABORT + 4;  // begin[3] of make_item, and the number of items
+    static constexpr uint32_t OFF_MEND = OFF_ABORT + 4;   // some row's sums are not finite
+    static constexpr uint32_t OFF_BEGIN = OFF_MEND + 4;  // begin[3] of make_item, and the number of items
     static constexpr uint32_t SMEM_BYTES = OFF_BEGIN + 16 + 1024;  // slack for manual alignment
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t *const gbase = smem_raw + (base - raw);
     auto bar = [&](int idx) -> uint32_t { return base + OFF_BAR + 8u * idx; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_ABORT);
+    volatile int *mend_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_MEND);
     uint32_t *tmem_ptr_smem = reinterpret_cast<uint32_t *>(gbase + L::OFF_TMEMPTR);
 
     const int warp = threadIdx.x >> 5;
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         ptx::mbar_init(bar(B_DRAIN), 1);
         ptx::mbar_init(bar(B_CUT), 1);
-        *abort_flag = 0;
+        *abort_flag = *mend_flag = 0;
     }
     if (warp == 0) {
         ptx::tmem_alloc(base + L::OFF_TMEMPTR, TMEM_COLS);
@@ -751,7 +753,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t tO = tmem + lane_addr + TM_O + h * HD;
         uint32_t sf_cnt = 0;
         int n_done = 0;  // items of this half finished
-        bool ok = true, mend = false;  // mend: some row of this thread has sums that are not finite
+        bool ok = true;
         for (int round = 0, k; ok && (k = item_of_round(round, n_items)) < n_items; ++round) {
             const Item it = make_item(p, k, begin);
             const Half x = h ? it.hB : it.hA;
@@ -905,7 +907,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     odd = ptx::fma2(ptx::f2(__uint_as_float(o[c][k]), __uint_as_float(o[c][k + 1])), 0, odd);
             float odd0, odd1;
             ptx::f2_split(odd, odd0, odd1);
-            mend = mend || (valid && !(odd0 + odd1 == 0.f) && l - l == 0.f);  // l is NaN: so is the row, by its scores
+            if (valid && !(odd0 + odd1 == 0.f) && l - l == 0.f) *mend_flag = 1;  // l is NaN: so is the row, by its scores
             // O / l as bf16, one 32-byte sector per store (two 16-byte stores if O is
             // only 16-byte aligned)
 #pragma unroll
@@ -932,7 +934,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ++n_done;
         }
         // nobody waits for this warp any more
-        if (ok && __any_sync(0xffffffffu, mend)) mend_rows<HD>(p, n_items, begin, h, quarter);
+        __syncwarp();
+        if (ok && __any_sync(0xffffffffu, *mend_flag)) mend_rows<HD>(p, n_items, begin, h, quarter);
     }
 
     ptx::tc_fence_before();
