@@ -82,7 +82,8 @@ constexpr int B_DRAIN = B_OFREE + 2;
 constexpr int NUM_BARS = B_DRAIN + 1;
 constexpr uint32_t OFF_TMEMPTR = OFF_BAR + NUM_BARS * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-constexpr uint32_t SMEM_USED = OFF_ABORT + 4;
+constexpr uint32_t OFF_SENT = OFF_ABORT + 4;  // ring loads and query loads that the producer has issued
+constexpr uint32_t SMEM_USED = OFF_SENT + 8;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;  // slack for manual alignment
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     auto bar = [&](int idx) -> uint32_t { return base + OFF_BAR + 8u * idx; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + OFF_ABORT);
     uint32_t *tmem_ptr_smem = reinterpret_cast<uint32_t *>(gbase + OFF_TMEMPTR);
+    volatile uint32_t *sent = reinterpret_cast<volatile uint32_t *>(gbase + OFF_SENT);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -275,14 +277,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ptx::tma_load_3d(mv, full, vdst + HALF_BYTES, 64, y, it.kvz);
                 }
             }
-            if (*abort_flag) {
-                // Let the copies already issued land before the CTA exits.
-                volatile int never = 0;
-                for (uint32_t v = u > 2 * NS ? u - 2 * NS : 0; v < u; v += 2)
-                    ptx::wait_bounded(bar(B_FULL + v % NS), k_full_parity(v), &never, lim);
-                if (!p.skip_q_load && n_iter > 0)
-                    ptx::wait_bounded(bar(B_QFULL), (n_iter - 1) & 1, &never, lim);
-            }
+            sent[0] = u;
+            sent[1] = p.skip_q_load ? 0 : n_iter;
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
             // The whole warp runs the issuer with identical values in every lane; the
@@ -632,7 +628,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     ptx::tc_fence_before();
     __syncthreads();
-    if (*abort_flag && threadIdx.x == 0) report_timeout(p);
+    if (*abort_flag && threadIdx.x == 0) {
+        // The copies already issued land before the CTA exits; now, since another warp may have given up after the
+        // producer's end.
+        volatile int never = 0;
+        const uint32_t u = sent[0], nq = sent[1];
+        for (uint32_t v = u > 2 * NS ? u - 2 * NS : 0; v < u; v += 2)
+            ptx::wait_bounded(bar(B_FULL + v % NS), k_full_parity(v), &never, lim);
+        if (nq > 0) ptx::wait_bounded(bar(B_QFULL), (nq - 1) & 1, &never, lim);
+        report_timeout(p);
+    }
     if (warp == 0) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, TMEM_COLS);

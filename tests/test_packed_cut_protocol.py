@@ -31,6 +31,13 @@ def test_the_models_are_of_these_kernels():
             assert "report(" in line, line
 
 
+def test_the_contiguous_kernel_waits_for_its_copies_at_its_end():
+    # behind the barrier that all warps come to, so that the flag is what it will be
+    text = source("attn_tc.cu")
+    at = text.index("The copies already issued land before the CTA exits")
+    assert "__syncthreads();\n    if (*abort_flag && threadIdx.x == 0) {" in text[at - 200:at] and text.count("if (*abort_flag") == 1
+
+
 class Bar:
     def __init__(self, name, count=1):
         self.name, self.count, self.left, self.bytes, self.phases = name, count, count, 0, 0
