@@ -560,9 +560,15 @@ class CcaAttentionFunction(torch.autograd.Function):
         return (*of(*ctx.saved_tensors, dO, ctx.cfg), None, None, None, None, None)
 
 
+def _dense(x):
+    """x, contiguous from a 16-byte boundary on."""
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 def _cca_gradients(Q, K, V, Kc, Vc, O, LSE, dO, cfg):
     g, w, scale, pool_mode, window_mode = cfg
-    dQ, dK, dV = cca_prefill_bwd(Q, K, V, Kc, Vc, O, LSE, dO.contiguous().to(Q.dtype), g, w, scale,
+    dQ, dK, dV = cca_prefill_bwd(Q, K, V, Kc, Vc, O, LSE, _dense(dO.to(Q.dtype)), g, w, scale,
                                  pool_mode=pool_mode, window_mode=window_mode)
     return dQ.to(Q.dtype), dK.to(K.dtype), dV.to(V.dtype)
 
@@ -599,7 +605,7 @@ def cca_attention(Q, K, V, g: int, w: int, scale: float = 0.0, pool_mode: int = 
     The gradients cannot be differentiated again: under create_graph they carry an error (RuntimeError)."""
     Q, K = _positioned(Q, K, q_weight, k_weight, norm, inv_freq, rotary)
     # copies are made outside the function, so that what it saves is what its gradients depend on
-    Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
+    Q, K, V = _dense(Q), _dense(K), _dense(V)
     return CcaAttentionFunction.apply(Q, K, V, g, w, scale, pool_mode, window_mode)
 
 
