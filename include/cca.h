@@ -594,7 +594,8 @@ typedef struct cca_packed_rows {
 
 /*
  * cca_pool_packed - the pooling equation for every whole group of every sequence.  Core rows that
- * belong to no group are set to zero.  Supported: bf16 or f32, d in {64, 128}, pool_mode 0 or 1.
+ * belong to no group are set to zero.  Supported: bf16 or f32, d in {64, 128}, pool_mode 0 or 1 (the mean: queries and the
+ * other tensor's values do not reach it).
  */
 int cca_pool_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const cca_packed_rows_t *V, void *Kc, void *Vc,
                     const cca_packed_t *packed, const cca_params_t *params, void *stream);
@@ -602,7 +603,8 @@ int cca_pool_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, cons
 /*
  * cca_attn_packed - the fusion equation for every row of every sequence.  O by strides, LSE [Hq, T] fp32.
  * Kc, Vc may be NULL where w >= T.  What a row does not see (later tokens, other sequences, other
- * cores) never reaches its output, whatever it holds.
+ * cores) never reaches its output, whatever it holds; what it sees and is not finite shows in its output column by
+ * column (infinities of both signs, and any NaN, as NaN).
  * Supported: bf16 (on the tensor cores) or f32, d in {64, 128}.
  */
 int cca_attn_packed(const cca_packed_rows_t *Q, const cca_packed_rows_t *K, const cca_packed_rows_t *V, const void *Kc,

@@ -9,17 +9,21 @@
 //
 // What is masked must not reach an output, not even as 0 * NaN: the producer sets values behind a sequence's end
 // (the next sequence's) to zero before it hands over the tile that holds them, and where a row's sums are not finite
-// although its scores are, a later token's value may have done it: the warp looks at such rows again once its last item is
-// done (mend_rows), when no bounded wait depends on it.  One sequence of 32 K tokens, causal, 8 heads over one: 1.3 ms; with a
-// NaN among its first values 1.7, an infinite one 8.2 (every later row's values are looked through), either in its last
-// row 10.7 (the other rows of its tiles are formed again); row by row inside the pipeline it was 801 ms.  A short sequence (n <= 256 / 2^k) fills an item with 2^k query heads of a KV head side by side, 128 / 2^k
-// rows of each in a half, as far as 2^k divides the heads: an item costs 4 us at least (its plan entry, first copies,
-// scores, softmax, output one after the other), 32 short prompts with 32 heads 31 us without and 22 with it (19 since).
+// although its scores are, a later token's value may have done it: the warp looks at such rows again once its last
+// item is done (mend_rows), when no bounded wait depends on it.  One sequence of 32 K tokens, causal, 8 heads over
+// one: 1.3 ms; with a NaN among its first values 1.7, an infinite one 8.2 (every later row's values are looked
+// through), either in its last row 10.7 (the other rows of its tiles are formed again); row by row inside the pipeline
+// it was 801 ms.
 //
-// 12 prompts of 32 K tokens in all (32 heads over 8, window 1024) take 460 us, 1.04 PF/s of visible pairs, the tensor
-// pipe active 51% of the time: 8 tiles an item leave a quarter to an item's start and end, and a tile waits for its
-// chain as in the contiguous kernel.  Three of 64 K (15 tiles an item): 1.39 ms, 1.30 PF/s.  Letting a half go on
-// with the next item by itself was slower (517 us).
+// A short sequence (n <= 256 / 2^k) fills an item with 2^k query heads of a KV head side by side, 128 / 2^k rows of
+// each in a half, as far as 2^k divides the heads: an item costs 4 us at least (its plan entry, first copies, scores,
+// softmax, output one after the other), 32 short prompts with 32 heads 31 us without and 22 with it (18.3-18.9 since).
+//
+// 12 prompts of 32 K tokens in all (32 heads over 8, window 1024) take 456-473 us on different boxes, 1.01-1.05 PF/s of
+// visible pairs, the tensor pipe active 53% of the time: their tiles hold 20% more pairs than are visible (a last core
+// tile is multiplied whole), 8 tiles an item leave a quarter to an item's start and end, and a tile waits for its chain as in
+// the contiguous kernel.  Three of 64 K (15 tiles an item, 11% more pairs): 1.43-1.46 ms, 1.24-1.27 PF/s; d = 64, 12 prompts
+// of 16 K: 192-195 us, 0.51-0.52 PF/s.  Letting a half go on with the next item by itself was slower (517 us).
 //
 // Every mbarrier wait is bounded in time; on a time-out the CTA stops, drains what it has in flight, frees its tensor
 // memory and reports CCA_ERR_TIMEOUT.

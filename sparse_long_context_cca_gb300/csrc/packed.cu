@@ -152,8 +152,9 @@ constexpr int POOL_PASSES = 4;  // steps of a chunk: all its rows are asked for 
 // One warp per core row and KV head.  D * sizeof(T) / 16 lanes hold a row, so a step takes 32 over that
 // many rows; a chunk of POOL_PASSES steps (8 rows of 128 bf16 columns) goes through one running
 // (maximum, sum).  12 prompts of 32 K tokens in all, 8 heads, g = 16: chunks of 8 steps 44 us at 12 warps an
-// SM (51 at 16, with spills), of 4 steps 38 us at 16 warps (47 at 24): 159 MB at 4.2 TB/s, bound by the loads
-// in flight (a group is 16 rows of K, V and r query rows, then a chain of shuffles and exponentials).
+// SM (51 at 16, with spills), of 4 steps 38 us at 16 warps (47 at 24): 159 MB at 4.2 TB/s.  Rows under way are held in
+// registers, eight a warp, so 16 warps an SM are all that fit; a ring of copies in shared memory, with which the pooling of
+// contiguous tensors reads 5.8 TB/s, was not built for packed ones.
 template <typename T, int D>
 __global__ void __launch_bounds__(POOL_WARPS * 32, POOL_BLOCKS) pool_packed_kernel(const PoolPackedArgs a) {
     using RT = Row16<T>;

@@ -102,7 +102,8 @@ __device__ __forceinline__ int3 plan_short(const Plan &p) {
 // go through them to and fro: straight rounds would give the first CTA the heaviest item of each.  Where the third
 // round is the last and does not reach every CTA, it begins at the last one: with few items their costs fall
 // steeply, and the first CTA's first item outweighs the light one that it has had since (32 prompts with one of
-// 648 tokens: 19.2 us instead of 22.9; with many rounds it is a loss, 466 against 461 us for 12 long prompts).
+// 648 tokens: 19.2 us instead of 22.9; with many rounds it is a loss, 466 against 461 us for 12 long prompts; a last
+// fifth round, to which the same would apply, was not measured).
 __device__ __forceinline__ int item_of_round(int round, int n = 0x7fffffff) {
     const bool back = (round & 1) != 0 || (round == 2 && n < 3 * static_cast<int>(gridDim.x));
     return round * gridDim.x + (back ? gridDim.x - 1 - blockIdx.x : blockIdx.x);

@@ -20,8 +20,10 @@
 //  TMEM: S^T | dP^T | dK | dV.  The rows of a core tile are split over items, whose sums are added up in order
 //  later; those of few tokens' tiles over two, the second of which to end adds the other's sums.
 //
-// What bounds them (32 heads over 8, 16 K tokens in five sequences, window 1024): dq 370 us, dkv of the tokens 382
-// and of the cores 79, the tensor pipe active 50 and 56% of the time.  With its parts taken out in turn, dq (376 us then) took
+// What bounds them (32 heads over 8, 16 K tokens in five sequences, window 1024): dq 370-373 us, dkv of the tokens 382-385
+// and of the cores 79, the tensor pipe active 50 and 57% of the time.  S and dP, and the exponentials, are formed in both
+// kernels: with the forward nine products for a tile where seven would do, and tiles hold 19% more pairs than are
+// visible.  One kernel for all three sums was not built: at d = 128 tensor memory has no room for dQ beside dK and dV.  With its parts taken out in turn, dq (376 us then) took
 // 372 us without copies, 370 without exponentials, 343 without dQ's product, 310 without any product, and 229 with
 // nothing but waits, tensor-memory reads and writes, and dS: the chain of a tile through the eight element-wise
 // warps.  Sixteen of them gained nothing.  dkv without any product took 315 us of 388, and with nothing but waits,
@@ -234,9 +236,8 @@ __device__ __forceinline__ Cta<HD> setup(uint8_t *smem_raw, const Args &p) {
         ptx::tmem_alloc(c.base + L::TMEM, 512);
         ptx::tmem_relinquish();
     }
-    // Everything above runs while the kernel before ends.  This one does not let the next begin early: CTAs that
-    // take SMs one by one lie anywhere, and 12 prompts then take 473 us instead of 462, a training step with cores
-    // 1233 instead of 1209 (neighbours read the same keys).
+    // Everything above runs while the kernel before ends.  This one does not let the next begin early, for the same
+    // reason as the forward: with it the training step with cores took 1233 us instead of 1209.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     ptx::tc_fence_before();
     __syncthreads();
