@@ -29,6 +29,8 @@ constexpr int SIMT_THREADS = 256;  // four threads to a row
 constexpr int SMALL_BLOCKS = 4;    // blocks of 64 rows an SM below which a call is small
 constexpr int SMALL_GROUPS = 2;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+// The weight of a key that is not seen.  One that is seen may have a weight of +0, and that times an infinite value is NaN.
+constexpr float MASKED = -0.f;
 
 template <int D>
 constexpr int PITCH = D + 4;
@@ -84,7 +86,7 @@ __device__ __forceinline__ void scores_of(const float *a, const float *b, int ty
     else scores<D, 1>(a, b, ty, s);
 }
 
-// acc[i][..] += sum_k p[4 ty + i][k] b_k, k < keys, over the columns 4 tx + 64 c.  GUARD: keys of weight zero take no part.
+// acc[i][..] += sum_k p[4 ty + i][k] b_k, k < keys, over the columns 4 tx + 64 c.  GUARD: keys of weight MASKED take no part.
 template <int D, bool GUARD>
 __device__ __forceinline__ void add_rows(const float *p, const float *b, int ty, int keys, float (&acc)[4][D / 16]) {
     const int tx = threadIdx.x % 16;
@@ -101,7 +103,7 @@ __device__ __forceinline__ void add_rows(const float *p, const float *b, int ty,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-                    if (GUARD && x == 0.f) continue;
+                    if (GUARD && __float_as_uint(x) == 0x80000000u) continue;
                     acc[i][4 * c] = fmaf(x, v.x, acc[i][4 * c]);
                     acc[i][4 * c + 1] = fmaf(x, v.y, acc[i][4 * c + 1]);
                     acc[i][4 * c + 2] = fmaf(x, v.z, acc[i][4 * c + 2]);
@@ -254,13 +256,16 @@ __global__ void __launch_bounds__(ROWS * 4 * GROUPS) attn_packed_kernel(const Si
         copy_k(t + GROUPS);
         // whether every row sees every key of the tile
         const bool whole = y0 + BS <= stop && top_row.sees(core, y0) && top_row.sees(core, y0 + BS - 1) && last_row.sees(core, y0);
+        unsigned seen = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = y0 + tx + 16 * j;
-                s[i][j] = whole || (key < stop && sight[i].sees(core, key)) ? s[i][j] * scale : -INFINITY;
+                const bool in = whole || (key < stop && sight[i].sees(core, key));
+                seen |= in ? 1u << (4 * i + j) : 0u;
+                s[i][j] = in ? s[i][j] * scale : -INFINITY;
                 top = fmaxf(top, s[i][j]);
             }
 #pragma unroll
@@ -272,6 +277,7 @@ __global__ void __launch_bounds__(ROWS * 4 * GROUPS) attn_packed_kernel(const Si
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s[i][j] = exp2f(s[i][j] - ref);
+                if (!whole && !(seen & (1u << (4 * i + j)))) s[i][j] = MASKED;
                 sum += s[i][j];
                 sP[(ty * 4 + i) * SP + tx + 16 * j] = s[i][j];
             }

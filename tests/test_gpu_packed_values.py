@@ -143,3 +143,37 @@ def test_mean_pooling_takes_no_weights_from_keys(dtype, d):
         Kc, Vc = api.cca_pool_packed(Q, K, c.V, c.packed, pool_mode=1)
         assert torch.equal(Vc, want)
         assert not torch.isfinite(Kc[:, 0]).any() and torch.isfinite(Kc[:, 1:]).all()
+
+
+@pytest.mark.parametrize("dtype,d", KINDS[2:], ids=IDS[2:])
+@pytest.mark.parametrize("g,w", [(16, None), (8, 40)])
+def test_tokens_whose_keys_and_values_are_not_finite(g, w, dtype, d):
+    # a token of which keys and values have overflowed: for the rows whose score of it is minus infinity its weight is zero, and zero
+    # times an infinite value is NaN; the other columns, and cores that hold it, are weighed as ever
+    N, bad = 300, (5, 131, 290)
+    Q, K, V = (rand(h, N, d, dtype=dtype, seed=i) for i, h in enumerate((4, 2, 2)))
+    for t in bad:
+        K[:, t, 3], V[:, t, 7], V[:, t, 9] = float("inf"), float("inf"), -float("inf")
+    V[:, 60, 7] = float("inf")
+    w = N if w is None else w
+    packed = api.cca_pack(device([0, N]), N, g, w)
+    Kc = Vc = None
+    if packed.cores:
+        Kc, Vc = (rand(2, N // g, d, dtype=dtype, seed=i) for i in (7, 8))
+        Kc[:, 2, 5], Vc[:, 2, 11] = -float("inf"), float("inf")
+        Kc[:, 9, 5], Vc[:, 9, 11] = float("inf"), float("inf")
+    O, L = api.cca_attn_packed(Q, K, V, Kc, Vc, packed)
+    q, k, v, got, lse = (t64(x) for x in (Q, K, V, O, L))
+    see = ref.visible(N, g, w, 0)
+    tol = 2.0 ** -7 if dtype == BF else 2.0 ** -16       # a weight's and the result's rounding, of values of a few units at most
+    with np.errstate(all="ignore"):
+        for h in range(4):
+            kk, vv = ref.keys(k, v, Kc, Vc, h // 2, 0, N, g)
+            for i in range(N):
+                s = kk[see[i]] @ q[h, i] * d ** -0.5
+                p = np.exp(s - s.max())
+                o, x = (p[:, None] * vv[see[i]]).sum(0) / p.sum(), got[h, i]
+                assert np.array_equal(np.isnan(x), np.isnan(o)) and np.array_equal(x[np.isinf(o)], o[np.isinf(o)]), (h, i)
+                fine = np.isfinite(o)
+                assert (np.abs(x - o)[fine] <= tol * np.abs(vv[see[i]][:, fine]).max(initial=1.0)).all(), (h, i)
+                assert np.isnan(lse[h, i]) == np.isnan(p.sum())
