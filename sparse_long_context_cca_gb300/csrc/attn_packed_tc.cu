@@ -11,15 +11,15 @@
 // (the next sequence's) to zero before it hands over the tile that holds them, and where a row's sums are not finite
 // although its scores are, a later token's value may have done it: the warp looks at such rows again once its last
 // item is done (mend_rows), when no bounded wait depends on it.  One sequence of 32 K tokens, causal, 8 heads over
-// one: 1.3 ms; with a NaN among its first values 1.7, an infinite one 8.2 (every later row's values are looked
-// through), either in its last row 10.7 (the other rows of its tiles are formed again); row by row inside the pipeline
-// it was 801 ms.
+// one: 1.3 ms; with a NaN among its first values 1.8, an infinite one 7.0 (every later row's values are looked
+// through), a column of them 15, either in its last row 10.6 (the other rows of its tiles are formed again); row by row
+// inside the pipeline it was 801 ms.
 //
 // A short sequence (n <= 256 / 2^k) fills an item with 2^k query heads of a KV head side by side, 128 / 2^k rows of
 // each in a half, as far as 2^k divides the heads: an item costs 4 us at least (its plan entry, first copies, scores,
 // softmax, output one after the other), 32 short prompts with 32 heads 31 us without and 22 with it (18.3-18.9 since).
 //
-// 12 prompts of 32 K tokens in all (32 heads over 8, window 1024) take 456-473 us on different boxes, 1.01-1.05 PF/s of
+// 12 prompts of 32 K tokens in all (32 heads over 8, window 1024) take 452-473 us on different boxes, 1.01-1.06 PF/s of
 // visible pairs, the tensor pipe active 53% of the time: their tiles hold 20% more pairs than are visible (a last core
 // tile is multiplied whole), 8 tiles an item leave a quarter to an item's start and end, and a tile waits for its chain as in
 // the contiguous kernel.  Three of 64 K (15 tiles an item, 11% more pairs): 1.43-1.46 ms, 1.24-1.27 PF/s; d = 64, 12 prompts
@@ -197,6 +197,9 @@ __device__ __forceinline__ Item make_item(const Params &p, int k, const int *beg
 // and with NS odd an even u reaches each slot once every 2*NS indices.
 __device__ __forceinline__ uint32_t k_full_parity(uint32_t u) { return (u / (2 * NS)) & 1; }
 
+// The top bits of a word's bf16 that are not finite: their exponents are all ones, and one more carries over.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
 // What a lane of a warp that holds whole rows has of one: E columns from E * lane on.
 template <int HD>
 struct Piece {
@@ -207,6 +210,11 @@ struct Piece {
         Piece x;
         x.raw = reinterpret_cast<const Raw *>(row)[threadIdx.x & 31];
         return x;
+    }
+    // not zero where an element is not finite
+    __device__ __forceinline__ uint32_t odd_halves() const {
+        if constexpr (E == 4) return cca::odd_halves(raw.x) | cca::odd_halves(raw.y);
+        else return cca::odd_halves(raw);
     }
     __device__ __forceinline__ void floats(float (&f)[E]) const {
         uint32_t w[E / 2];
@@ -221,31 +229,46 @@ struct Piece {
 };
 __device__ __forceinline__ bool not_finite(float x) { return !(x - x == 0.f); }
 
-// Values of a row's keys: rows [0, cores) of Vc and [from, to] of V, of one sequence and KV head.
+// A row's keys and values: rows [0, cores) of Kc, Vc and [from, to] of K, V, of one sequence and KV head.
 template <int HD>
-struct RowValues {
-    const __nv_bfloat16 *core, *token;  // rows 0
-    int64_t step;                       // from a token to the next one
+struct RowKeys {
+    const __nv_bfloat16 *kc, *vc, *k, *v;  // rows 0
+    int64_t k_step, v_step;                // from a token to the next one
     int cores, from, to;
     __device__ __forceinline__ int count() const { return cores + max(to - from + 1, 0); }
-    __device__ __forceinline__ Piece<HD> at(int k) const {
-        return Piece<HD>::at(k < cores ? core + static_cast<int64_t>(k) * HD : token + (from + k - cores) * step);
+    __device__ __forceinline__ Piece<HD> key(int j) const {
+        return Piece<HD>::at(j < cores ? kc + static_cast<int64_t>(j) * HD : k + (from + j - cores) * k_step);
     }
-    // Adds up what is not finite of the values [k0, k1), column by column: zero where nothing is, and otherwise what a
-    // sum with positive weights becomes (an infinity, or NaN of both or of a NaN).  Ends early where every lane's
-    // columns in `asked` are NaN.
-    __device__ __forceinline__ void add_odd(int k0, int k1, unsigned asked, float (&odd)[HD / 32]) const {
+    __device__ __forceinline__ Piece<HD> value(int j) const {
+        return Piece<HD>::at(j < cores ? vc + static_cast<int64_t>(j) * HD : v + (from + j - cores) * v_step);
+    }
+    // Adds up what is not finite of the values [j0, j1), column by column: zero where nothing is, and otherwise what a
+    // weighted sum becomes: an infinity, or NaN of both, of a NaN, or of one whose weight is zero.  (The row's LSE is finite, so a key that
+    // is not has a score of minus infinity; a weight that is small, however small, is not zero.)  Ends early where every
+    // lane's columns in `asked` are NaN.
+    __device__ __forceinline__ void add_odd(int j0, int j1, unsigned asked, float (&odd)[HD / 32]) const {
         constexpr int E = HD / 32, AHEAD = 16;
-        for (int k = k0; k < k1; k += AHEAD) {
+        for (int j = j0; j < j1; j += AHEAD) {
             Piece<HD> x[AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) x[i] = at(min(k + i, k1 - 1));
+            for (int i = 0; i < AHEAD; ++i) x[i] = value(min(j + i, j1 - 1));
+            uint32_t some = 0;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) some |= x[i].odd_halves();
+            if (!__any_sync(0xffffffffu, some != 0)) continue;
+            Piece<HD> y[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) y[i] = key(min(j + i, j1 - 1));
+            unsigned none = 0;  // keys of weight zero
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) none |= y[i].odd_halves() != 0 ? 1u << i : 0u;
+            none = __reduce_or_sync(0xffffffffu, none);
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 float f[E];
                 x[i].floats(f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) odd[e] += not_finite(f[e]) ? f[e] : 0.f;
+                for (int e = 0; e < E; ++e) odd[e] += !not_finite(f[e]) ? 0.f : none & (1u << i) ? NAN : f[e];
             }
             bool all = true;
 #pragma unroll
@@ -259,9 +282,7 @@ struct RowValues {
 constexpr uint32_t FORM_AGAIN = 0x7fa5;
 
 // Two bf16 of a word, zero where one is not finite.
-__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-    return w & ~((((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15)) * 0xffffu);
-}
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) { return w & ~((odd_halves(w) >> 15) * 0xffffu); }
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -406,8 +427,9 @@ __device__ __noinline__ void mend_rows(const Params &p, int n_items, const int *
         // what all of them see: cores [0, shared.cores), tokens [shared.from, shared.to]
         const bool in = (todo >> lane) & 1;
         const int i0 = __reduce_min_sync(full, in ? mine : 0x7fffffff), i1 = __reduce_max_sync(full, in ? mine : 0);
-        const RowValues<HD> shared = {p.Vc + (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD, p.V.at(it.kvz, it.row0), p.V.row,
-                                      p.plan.cores_of(i0), p.plan.start_of(i1), i0};
+        const int64_t head = (static_cast<int64_t>(it.kvz) * p.plan.G + it.core0) * HD;
+        const RowKeys<HD> shared = {p.Kc + head, p.Vc + head, p.K.at(it.kvz, it.row0), p.V.at(it.kvz, it.row0), p.K.row, p.V.row,
+                                    p.plan.cores_of(i0), p.plan.start_of(i1), i0};
         float seen[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) seen[e] = 0.f;
@@ -417,15 +439,15 @@ __device__ __noinline__ void mend_rows(const Params &p, int n_items, const int *
             __nv_bfloat16 *const out = p.O.at(head_of(r), it.row0 + i);
             const unsigned c = odd_columns(Piece<HD>::at(out));
             // ... and what this one sees besides: later cores, earlier tokens, later tokens
-            RowValues<HD> v = shared;
-            v.cores = p.plan.cores_of(i), v.from = p.plan.start_of(i), v.to = i;
+            RowKeys<HD> own = shared;
+            own.cores = p.plan.cores_of(i), own.from = p.plan.start_of(i), own.to = i;
             float odd[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) odd[e] = seen[e];
-            const int t0 = v.cores - v.from;  // place of token 0 among the row's keys
-            v.add_odd(shared.cores, v.cores, c, odd);
-            v.add_odd(t0 + v.from, t0 + min(shared.from, i + 1), c, odd);
-            v.add_odd(t0 + max(shared.from, i0 + 1), t0 + i + 1, c, odd);
+            const int t0 = own.cores - own.from;  // place of token 0 among the row's keys
+            own.add_odd(shared.cores, own.cores, c, odd);
+            own.add_odd(t0 + own.from, t0 + min(shared.from, i + 1), c, odd);
+            own.add_odd(t0 + max(shared.from, i0 + 1), t0 + i + 1, c, odd);
             bool left = false;
 #pragma unroll
             for (int e = 0; e < E; ++e) {

@@ -11,7 +11,7 @@
 // 1500 tokens of four heads of 64 (few tiles): 25 us against 45 without the groups of small calls, which give
 // each SM two blocks of 32 rows whose thread groups take every second key tile, and 21 since products leave out
 // the keys that a list's last tile does not have; with many tiles the multiply-adds bound it: eight sequences of
-// 4 K tokens in all, 8 heads of 128, causal, take 297-301 us, 32 TF/s of the units' 74, a training step of four sequences
+// 4 K tokens in all, 8 heads of 128, causal, take 297-304 us, 31-32 TF/s of the units' 74, a training step of four sequences
 // of 2 K in all (8 heads over 4) 631-659 us at d = 64, causal, and 452 at d = 128 with a window of 256 and cores.
 #include <cuda_runtime.h>
 #include <math.h>

@@ -145,7 +145,7 @@ def test_mean_pooling_takes_no_weights_from_keys(dtype, d):
         assert not torch.isfinite(Kc[:, 0]).any() and torch.isfinite(Kc[:, 1:]).all()
 
 
-@pytest.mark.parametrize("dtype,d", KINDS[2:], ids=IDS[2:])
+@pytest.mark.parametrize("dtype,d", KINDS, ids=IDS)
 @pytest.mark.parametrize("g,w", [(16, None), (8, 40)])
 def test_tokens_whose_keys_and_values_are_not_finite(g, w, dtype, d):
     # a token of which keys and values have overflowed: for the rows whose score of it is minus infinity its weight is zero, and zero
