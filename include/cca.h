@@ -590,7 +590,9 @@ typedef struct cca_packed_rows {
     int64_t head_stride, row_stride;
 } cca_packed_rows_t;
 
-/* params of the calls below: Hq, Hkv, d, dtype, scale, dev_status, pool_mode; the others are not used. */
+/* params of the calls below: Hq, Hkv, d, dtype, scale, dev_status, pool_mode; the others are not used.
+ * Weighted sums are formed in fp32 before they are divided by their weights' sum: values above the largest number divided by
+ * the number of a row's keys (of a group's) may overflow in pooling and in fp32 attention; bf16 attention forms such rows again. */
 
 /*
  * cca_pool_packed - the pooling equation for every whole group of every sequence.  Core rows that
