@@ -19,7 +19,7 @@
 // each in a half, as far as 2^k divides the heads: an item costs 4 us at least (its plan entry, first copies, scores,
 // softmax, output one after the other), 32 short prompts with 32 heads 31 us without and 22 with it (18.3-18.9 since).
 //
-// 12 prompts of 32 K tokens in all (32 heads over 8, window 1024) take 452-473 us on different boxes, 1.01-1.06 PF/s of
+// 12 prompts of 32 K tokens in all (32 heads over 8, window 1024) take 452-474 us on different boxes, 1.01-1.06 PF/s of
 // visible pairs, the tensor pipe active 53% of the time: their tiles hold 20% more pairs than are visible (a last core
 // tile is multiplied whole), 8 tiles an item leave a quarter to an item's start and end, and a tile waits for its chain as in
 // the contiguous kernel.  Three of 64 K (15 tiles an item, 11% more pairs): 1.43-1.46 ms, 1.24-1.27 PF/s; d = 64, 12 prompts
